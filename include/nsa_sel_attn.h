@@ -461,6 +461,91 @@ int nsa_swa_fwd(const void* Q, const void* K, const void* V, void* O, float* LSE
                 void* stream);
 
 /*
+ * nsa_qk_norm_rope -- RMS norm of every query and key head and the position
+ * rotation in one pass: what a layer does between its Q/K projections and
+ * the attention entry points of this library.
+ *
+ *   Q, K           device, fp16 or bf16 (dtype), [B, M, H, D] and [B, M, G, D]
+ *   Qo, Ko         device, same type and shapes (output); each may be its
+ *                  input (same address and strides), else no overlap
+ *   wq, wk         device, [D] norm weights, weight_dtype NSA_F32 or dtype;
+ *                  NULL: no weight (ones)
+ *   cos_table,     device, fp32, [table_rows, R/2]: cosine and sine of the
+ *   sin_table      angle of pair i at a position (row); unused when R = 0
+ *   positions      device, int32: token (b, m) is at
+ *                  positions[b * positions_stride + m] (stride 0: one row for
+ *                  the whole batch); NULL: token m is at position m
+ *   H, G           > 0 (no relation between them is needed); D 64 or 128
+ *   R              rotated entries per head, the first R: 0 (norm alone) to D,
+ *                  a multiple of 16
+ *   eps            >= 0, finite
+ *   interleaved    0: pair i is entries (i, i + R/2); else (2i, 2i + 1)
+ *   strides        host array of 12 element strides, (b, m, head) of Q, K, Qo
+ *                  and Ko, or NULL for contiguous; each a multiple of 8 (else
+ *                  NSA_ERR_ALIGN) in [0, 2^40], and not 0 for a written
+ *                  tensor's dimension of more than one (else NSA_ERR_SHAPE).
+ *                  D is contiguous. Q and K can so be slices of one projection.
+ *
+ * Per row x: n = x rsqrt(mean(x^2) + eps) w, then every pair (a, b) of n
+ * becomes (a cos - b sin, b cos + a sin); all in fp32, rounded once (nearest
+ * even) to dtype. A token whose position is negative, or >= table_rows when
+ * R > 0, is padding: its inputs are not read and its output rows are zero.
+ * A non-finite entry reaches its own row only. With positions NULL and R > 0
+ * the table must hold M rows (else NSA_ERR_SHAPE).
+ *
+ * One kernel on `stream`; allocates nothing and keeps no state. Errors before
+ * launch: NSA_ERR_SHAPE (sizes, R, eps, B*M >= 2^31), NSA_ERR_HEAD_DIM,
+ * NSA_ERR_DTYPE, NSA_ERR_NULL, NSA_ERR_ALIGN (Q, K, Qo, Ko, weights, tables
+ * 16-byte; positions 4-byte). An empty problem returns NSA_OK at once.
+ */
+int nsa_qk_norm_rope(const void* Q, const void* K, void* Qo, void* Ko, const void* wq,
+                     const void* wk, const float* cos_table, const float* sin_table,
+                     const int32_t* positions, int64_t B, int64_t M, int64_t H, int64_t G,
+                     int64_t D, int64_t R, int64_t table_rows, int64_t positions_stride,
+                     float eps, int interleaved, int dtype, int weight_dtype,
+                     const int64_t* strides, void* stream);
+
+/*
+ * nsa_qk_norm_rope_bwd_workspace_bytes -- device workspace of
+ * nsa_qk_norm_rope_bwd: one partial sum of the two weight gradients per CTA
+ * (at most 304). Negative nsa_status for invalid sizes. Pure host arithmetic.
+ */
+int64_t nsa_qk_norm_rope_bwd_workspace_bytes(int64_t B, int64_t M, int64_t D);
+
+/*
+ * nsa_qk_norm_rope_bwd -- gradients of nsa_qk_norm_rope.
+ *
+ *   Q, K           the forward's inputs (the norms are formed again)
+ *   dQo, dKo       gradients of its outputs, grad_dtype NSA_F32 (what
+ *                  nsa_sel_attn_bwd writes) or dtype
+ *   dQ, dK         device, dtype (output); each may be the input of its shape
+ *                  (dQo, dKo of type dtype, or Q, K) with the same strides
+ *   dwq, dwk       device, fp32 [D] (output), or NULL: not wanted
+ *   strides        host array of 18 element strides, (b, m, head) of Q, K,
+ *                  dQo, dKo, dQ, dK, or NULL; rules as for the forward
+ *   workspace      device memory of at least
+ *                  nsa_qk_norm_rope_bwd_workspace_bytes() bytes, 16-byte
+ *                  aligned (else NSA_ERR_WORKSPACE, NSA_ERR_ALIGN); unused
+ *                  when both dwq and dwk are NULL
+ *
+ * With g the pairs of a row of dQo (dKo) turned back and xhat = x
+ * rsqrt(mean(x^2) + eps): dw = sum over rows of g xhat, dx = rsqrt(...) (g w -
+ * xhat mean(g w xhat)); fp32, dx rounded once. Padding tokens (as in the
+ * forward; their rows are not read) get a zero gradient and add nothing to
+ * dw. The sums of dw have a fixed order: equal calls give equal bits. Two
+ * kernels on `stream` (one when no dw is wanted); allocates nothing. With no
+ * token, dwq and dwk are zeroed. Everything else is nsa_qk_norm_rope.
+ */
+int nsa_qk_norm_rope_bwd(const void* Q, const void* K, const void* dQo, const void* dKo, void* dQ,
+                         void* dK, float* dwq, float* dwk, const void* wq, const void* wk,
+                         const float* cos_table, const float* sin_table, const int32_t* positions,
+                         int64_t B, int64_t M, int64_t H, int64_t G, int64_t D, int64_t R,
+                         int64_t table_rows, int64_t positions_stride, float eps,
+                         int interleaved, int dtype, int weight_dtype, int grad_dtype,
+                         const int64_t* strides, void* workspace, int64_t workspace_bytes,
+                         void* stream);
+
+/*
  * nsa_sync_status -- wait for `stream`, then read and clear the device status
  * word of the current device.
  *

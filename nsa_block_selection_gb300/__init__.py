@@ -11,14 +11,20 @@ Public API (GPU only; the CUDA library must be built):
   common to a tile of 16 consecutive queries are gathered once per tile;
 * :func:`sel_attn_fwd_host` -- the forward with host buffers in and out;
 * :func:`swa_fwd` -- GQA sliding-window (or dense) attention forward on the
-  tcgen05 tensor cores.
+  tcgen05 tensor cores;
+* :func:`qk_norm_rope` and :func:`qk_norm_rope_bwd` -- RMS norm of every
+  query and key head and the position rotation in one pass, before any of
+  the attention calls, and its gradients (:func:`rope_tables` builds the
+  angle tables).
 
 The C ABI is declared in ``include/nsa_sel_attn.h``; ``inputs`` draws the
 seeded synthetic workloads.
 """
 
-from ._lib import (NsaError, load, sel_attn_bwd, sel_attn_fwd, sel_attn_fwd_host,  # noqa: F401
-                   sel_attn_fwd_shared, status_string, swa_fwd, topk_blocks)
+from ._lib import (NsaError, load, qk_norm_rope, qk_norm_rope_bwd, rope_tables,  # noqa: F401
+                   sel_attn_bwd, sel_attn_fwd, sel_attn_fwd_host, sel_attn_fwd_shared,
+                   status_string, swa_fwd, topk_blocks)
 
 __all__ = ["sel_attn_fwd", "sel_attn_fwd_shared", "sel_attn_bwd", "sel_attn_fwd_host",
-           "topk_blocks", "swa_fwd", "load", "status_string", "NsaError"]
+           "topk_blocks", "swa_fwd", "qk_norm_rope", "qk_norm_rope_bwd", "rope_tables",
+           "load", "status_string", "NsaError"]

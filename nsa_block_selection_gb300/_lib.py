@@ -25,7 +25,8 @@ EXPORTS = ("nsa_status_string", "nsa_version", "nsa_sel_attn_fwd", "nsa_sel_attn
            "nsa_sel_attn_bwd_noalloc", "nsa_topk_blocks", "nsa_swa_fwd",
            "nsa_sel_attn_fwd_shared_workspace_bytes", "nsa_sel_attn_fwd_shared",
            "nsa_probe_l2_gather", "nsa_probe_l2_gather_bytes", "nsa_probe_gather_rows",
-           "nsa_probe_reduce_rows", "nsa_sel_attn_fwd_host_ex", "nsa_sel_attn_bwd_ex")
+           "nsa_probe_reduce_rows", "nsa_sel_attn_fwd_host_ex", "nsa_sel_attn_bwd_ex",
+           "nsa_qk_norm_rope", "nsa_qk_norm_rope_bwd", "nsa_qk_norm_rope_bwd_workspace_bytes")
 
 _lib = None
 
@@ -108,6 +109,14 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.nsa_probe_gather_rows.restype = c_int
     lib.nsa_probe_gather_rows.argtypes = [vp, vp, vp, i64, i64, i64, i64, i64, i64, c_int, i64,
                                           c_int, c_int, i64, vp]
+    f32 = ctypes.c_float
+    lib.nsa_qk_norm_rope.restype = c_int
+    lib.nsa_qk_norm_rope.argtypes = [vp] * 9 + [i64] * 8 + [f32, c_int, c_int, c_int, vp, vp]
+    lib.nsa_qk_norm_rope_bwd_workspace_bytes.restype = i64
+    lib.nsa_qk_norm_rope_bwd_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.nsa_qk_norm_rope_bwd.restype = c_int
+    lib.nsa_qk_norm_rope_bwd.argtypes = [vp] * 13 + [i64] * 8 + [f32, c_int, c_int, c_int, c_int,
+                                                                 vp, vp, i64, vp]
     if path is None:
         _lib = lib
     return lib
@@ -460,6 +469,182 @@ def swa_fwd(q, k, v, window=(-1, -1), scale: Optional[float] = None, out=None, l
     if st != NSA_OK:
         raise NsaError(st, "nsa_swa_fwd")
     return out, lse
+
+
+def rope_tables(rows: int, rot_dim: int, base: float = 10000.0, device="cuda"):
+    """Cosine and sine tables for :func:`qk_norm_rope`: fp32 [rows, rot_dim/2]
+    each, the angle of pair i at position p being p * base^(-2i / rot_dim),
+    formed in fp64 (an fp32 angle of a far position is off by whole turns'
+    fractions). A program builds them once; any other tables of that shape
+    (scaled or interpolated positions) serve as well."""
+    import torch
+
+    if rows < 0 or rot_dim <= 0 or rot_dim % 2:
+        raise ValueError("rows must be >= 0 and rot_dim a positive even number")
+    half = rot_dim // 2
+    freq = float(base) ** (-torch.arange(half, dtype=torch.float64, device=device) / half)
+    ang = torch.arange(rows, dtype=torch.float64, device=device)[:, None] * freq
+    return ang.cos().float(), ang.sin().float()
+
+
+def _check_rope(named, weights, cos, sin, positions):
+    """Checks shared by the norm-and-rotation calls; returns the sizes and
+    pointers they pass on."""
+    import torch
+
+    q, k = named[0][1], named[1][1]
+    if q.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"q must be fp16 or bf16, got {q.dtype}")
+    if q.dim() != 4 or k.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]:
+        raise ValueError("shape mismatch: q [B,M,H,D], k [B,M,G,D]")
+    B, M, H, D = q.shape
+    for i, (name, t, dtypes) in enumerate(named):
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name} must be one of {dtypes}, got {t.dtype}")
+        if tuple(t.shape) != tuple((q, k)[i % 2].shape):
+            raise ValueError(f"{name} must have the shape of {'qk'[i % 2]}")
+    for name, t, _ in named:
+        if not t.is_cuda or t.device != q.device:
+            raise ValueError(f"{name} must be on q's CUDA device")
+        if t.numel() > 0 and t.stride(-1) != 1:
+            raise ValueError(f"{name} must have a contiguous last dimension")
+    wdt = None
+    for name, w in weights:
+        if w is None:
+            continue
+        if w.dtype not in (torch.float32, q.dtype) or (wdt is not None and w.dtype != wdt):
+            raise TypeError(f"{name} must be fp32 or {q.dtype}, and both weights alike")
+        wdt = w.dtype
+        if tuple(w.shape) != (D,) or not w.is_contiguous() or w.device != q.device:
+            raise ValueError(f"{name} must be a contiguous [D] tensor on q's device")
+    if (cos is None) != (sin is None):
+        raise ValueError("pass both tables or neither")
+    R = rows = 0
+    if cos is not None:
+        if cos.dtype != torch.float32 or sin.dtype != torch.float32:
+            raise TypeError("cos and sin must be fp32")
+        if cos.dim() != 2 or cos.shape != sin.shape or not cos.is_contiguous() or \
+                not sin.is_contiguous() or cos.device != q.device or sin.device != q.device:
+            raise ValueError("cos and sin must be contiguous [rows, R/2] tensors on q's device")
+        rows, R = cos.shape[0], 2 * cos.shape[1]
+    pstride = 0
+    if positions is not None:
+        if positions.dtype != torch.int32:
+            raise TypeError(f"positions must be int32, got {positions.dtype}")
+        if tuple(positions.shape) not in ((M,), (B, M)) or not positions.is_contiguous() or \
+                positions.device != q.device:
+            raise ValueError("positions must be a contiguous [M] or [B, M] tensor on q's device")
+        pstride = M if positions.dim() == 2 else 0
+    return B, M, H, k.shape[2], D, R, rows, pstride, _dtype_code(q.dtype if wdt is None else wdt)
+
+
+def _strides(tensors):
+    """(b, m, head) element strides of [B, M, heads, D] tensors; None if all
+    are contiguous. The stride of a dimension of one is never used."""
+    if all(t.is_contiguous() or t.numel() == 0 for t in tensors):
+        return None
+    s = [st if n > 1 else 0 for t in tensors for st, n in zip(t.stride()[:3], t.shape[:3])]
+    return (ctypes.c_int64 * len(s))(*s)
+
+
+def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
+                 eps: float = 1e-6, interleaved: bool = False, q_out=None, k_out=None,
+                 stream=None):
+    """RMS norm of every query and key head and the position rotation, in one
+    pass (nsa_qk_norm_rope).
+
+    q: fp16 or bf16 [B, M, H, D], k: [B, M, G, D] of q's dtype, D 64 or 128;
+    both (and preallocated outputs) may be strided views, such as slices of
+    one projection, with a contiguous last dimension and strides that are
+    multiples of 8. ``q_weight``, ``k_weight``: [D], fp32 or q's dtype, or None (ones).
+    ``cos``, ``sin``: fp32 [rows, R/2] (:func:`rope_tables`); R/2 pairs per
+    head are rotated, entries (i, i + R/2), or (2i, 2i + 1) with
+    ``interleaved``; None: no rotation. ``positions``: int32 [B, M] or [M]
+    table rows of the tokens (None: 0 .. M - 1); a position outside the table
+    marks padding, whose output rows are zero. The outputs may be the inputs.
+    Returns (q_out, k_out).
+    """
+    import torch
+
+    lib = load()
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
+    named = [("q", q, (q.dtype,)), ("k", k, (q.dtype,)), ("q_out", q_out, (q.dtype,)),
+             ("k_out", k_out, (q.dtype,))]
+    B, M, H, G, D, R, rows, ps, wdt = _check_rope(
+        named, (("q_weight", q_weight), ("k_weight", k_weight)), cos, sin, positions)
+    if stream is None:
+        stream = torch.cuda.current_stream(q.device)
+    with torch.cuda.device(q.device):
+        st = lib.nsa_qk_norm_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(q_weight),
+                                  _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(positions), B, M, H,
+                                  G, D, R, rows, ps, float(eps), int(bool(interleaved)),
+                                  _dtype_code(q.dtype), wdt, _strides((q, k, q_out, k_out)),
+                                  ctypes.c_void_p(stream.cuda_stream))
+    if st != NSA_OK:
+        raise NsaError(st, "nsa_qk_norm_rope")
+    return q_out, k_out
+
+
+def norm_rope_bwd_workspace_bytes(B, M, D) -> int:
+    n = load().nsa_qk_norm_rope_bwd_workspace_bytes(B, M, D)
+    if n < 0:
+        raise NsaError(int(n), "nsa_qk_norm_rope_bwd_workspace_bytes")
+    return int(n)
+
+
+def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, cos=None, sin=None,
+                     positions=None, eps: float = 1e-6, interleaved: bool = False, dq=None,
+                     dk=None, dq_weight=None, dk_weight=None, weight_grads: bool = True,
+                     workspace=None, stream=None):
+    """Gradients of :func:`qk_norm_rope` (nsa_qk_norm_rope_bwd).
+
+    q, k and the arguments after them are the forward's; ``dq_out``,
+    ``dk_out`` the gradients of its outputs, fp32 (as :func:`sel_attn_bwd`
+    returns them) or q's dtype, both alike; strided views are taken as in
+    the forward. Returns (dq, dk, dq_weight, dk_weight): dq, dk of q's dtype,
+    the weights' gradients fp32 [D] (None with ``weight_grads=False``).
+    ``workspace`` (CUDA uint8, norm_rope_bwd_workspace_bytes) is allocated
+    when omitted.
+    """
+    import torch
+
+    lib = load()
+    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
+    dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
+    gts = (torch.float32, q.dtype)
+    named = [("q", q, (q.dtype,)), ("k", k, (q.dtype,)), ("dq_out", dq_out, gts),
+             ("dk_out", dk_out, (dq_out.dtype,)), ("dq", dq, (q.dtype,)), ("dk", dk, (q.dtype,))]
+    B, M, H, G, D, R, rows, ps, wdt = _check_rope(
+        named, (("q_weight", q_weight), ("k_weight", k_weight)), cos, sin, positions)
+    need = norm_rope_bwd_workspace_bytes(B, M, D) if weight_grads else 0
+    if weight_grads:
+        dws = []
+        for name, w in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
+            w = torch.empty((D,), dtype=torch.float32, device=q.device) if w is None else w
+            if w.dtype != torch.float32 or tuple(w.shape) != (D,) or not w.is_contiguous() or \
+                    w.device != q.device:
+                raise ValueError(f"{name} must be a contiguous fp32 [D] tensor on q's device")
+            dws.append(w)
+        if workspace is None:
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        if not workspace.is_cuda or workspace.device != q.device:
+            raise ValueError("workspace must be on q's CUDA device")
+    else:
+        dws, workspace = [None, None], None
+    if stream is None:
+        stream = torch.cuda.current_stream(q.device)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with torch.cuda.device(q.device):
+        st = lib.nsa_qk_norm_rope_bwd(
+            _ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dws[0]),
+            _ptr(dws[1]), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(positions), B,
+            M, H, G, D, R, rows, ps, float(eps), int(bool(interleaved)), _dtype_code(q.dtype), wdt,
+            _dtype_code(dq_out.dtype), _strides((q, k, dq_out, dk_out, dq, dk)), _ptr(workspace),
+            nbytes, ctypes.c_void_p(stream.cuda_stream))
+    if st != NSA_OK:
+        raise NsaError(st, "nsa_qk_norm_rope_bwd")
+    return dq, dk, dws[0], dws[1]
 
 
 def probe_l2_gather(k, v, g: int, block_size: int, ctas: int, warps_per_cta: int,

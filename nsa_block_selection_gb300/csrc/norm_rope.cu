@@ -1,0 +1,643 @@
+// RMS norm of every query and key head and the position rotation in one pass
+// over the projections' outputs, and its backward, for sm_103a.
+//
+// Per row x of D entries (one head of one token), with the head norm's weight
+// w and the token's angles c_i, s_i (cos and sin tables, row = position):
+//   r = rsqrt(mean(x^2) + eps),  n = x r w,
+//   (a, b) -> (a c_i - b s_i, b c_i + a s_i)  for the R / 2 pairs (a, b) of
+//   the first R entries (entries i and i + R/2, or 2i and 2i + 1),
+// entries past R pass through. Backward, with g = the pairs of dy turned by
+// the opposite angle and xhat = x r:
+//   dw += g xhat,   dx = r (g w - xhat mean(g w xhat)).
+// All of it is fp32, rounded once when a result is stored.
+//
+// The bytes bound both: each row is read once and written once. A row is held
+// by D / 16 lanes, 16 entries each, as two 16-byte chunks that hold both
+// entries of every pair: lane t takes chunks t and t + R/16 while t < R/16,
+// and two consecutive chunks of the tail after that, so the rotation needs no
+// exchange between lanes in either pairing and the only shuffles are the
+// row sums (3 steps at D = 128, 2 at 64). A warp covers 32 / (D/16) rows at a time.
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "common.cuh"
+#include "nsa_sel_attn.h"
+#include "ptx.cuh"
+
+namespace nsa {
+namespace {
+
+constexpr int kRopeThreads = 128;      // forward CTAs: 4 warps, each a unit of its own
+constexpr int kRopeBwdThreads = 256;   // backward CTAs: 8 warps that share one dw partial
+constexpr int kRopeSms = 152;
+
+struct RopeRows {
+  const uint8_t* x;  // one of Q, K: element strides over (b, m, h)
+  uint8_t* y;
+  const void* w;
+  int64_t xb, xm, xh, yb, ym, yh;
+  int heads;
+};
+
+struct RopeProblem {
+  RopeRows q, k;
+  const float* cos_t;
+  const float* sin_t;
+  const int32_t* pos;
+  int64_t pos_b, table_rows;
+  int B, M, half;  // half = R / 2
+  bool interleaved, w32;
+  float eps;
+};
+
+// The two chunks of 8 entries that lane t of a row holds.
+__device__ __forceinline__ void row_chunks(int t, int half, int& c0, int& c1) {
+  const int pc = half >> 3;  // chunks of a half
+  if (t < pc) {
+    c0 = t;
+    c1 = t + pc;
+  } else {
+    c0 = 2 * t;  // 2 pc + 2 (t - pc)
+    c1 = 2 * t + 1;
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+  if constexpr (BF16) {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+  } else {
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void unpack8(const uint4& v, float* f) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = unpack2<BF16>(u[i]);
+    f[2 * i] = p.x;
+    f[2 * i + 1] = p.y;
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint4 pack8(const float* f) {
+  return make_uint4(pack2_t<BF16>(f[0], f[1]), pack2_t<BF16>(f[2], f[3]),
+                    pack2_t<BF16>(f[4], f[5]), pack2_t<BF16>(f[6], f[7]));
+}
+
+__device__ __forceinline__ void load8(const float* p, float* f) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  const float4 b = *reinterpret_cast<const float4*>(p + 4);
+  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+  f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
+
+// The 16 weights of this lane's chunks (1 without a weight).
+template <bool BF16>
+__device__ __forceinline__ void load_weights(const void* w, bool w32, int c0, int c1, float* f) {
+  if (w == nullptr) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[i] = 1.f;
+  } else if (w32) {
+    load8(static_cast<const float*>(w) + 8 * c0, f);
+    load8(static_cast<const float*>(w) + 8 * c1, f + 8);
+  } else {
+    const uint4* p = static_cast<const uint4*>(w);
+    unpack8<BF16>(p[c0], f);
+    unpack8<BF16>(p[c1], f + 8);
+  }
+}
+
+// The 8 angles of the lane's 8 pairs. Halves: pair j is entries j of the two
+// chunks. Interleaved: pairs 0..3 are the entries (2j, 2j + 1) of the first
+// chunk, 4..7 those of the second.
+__device__ __forceinline__ void load_angles(const RopeProblem& p, int64_t at, int c0, int c1,
+                                            float* c, float* s) {
+  const float* ct = p.cos_t + at * p.half;
+  const float* st = p.sin_t + at * p.half;
+  if (p.interleaved) {
+    const float4 a = *reinterpret_cast<const float4*>(ct + 4 * c0);
+    const float4 b = *reinterpret_cast<const float4*>(ct + 4 * c1);
+    const float4 d = *reinterpret_cast<const float4*>(st + 4 * c0);
+    const float4 e = *reinterpret_cast<const float4*>(st + 4 * c1);
+    c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w, c[4] = b.x, c[5] = b.y, c[6] = b.z, c[7] = b.w;
+    s[0] = d.x, s[1] = d.y, s[2] = d.z, s[3] = d.w, s[4] = e.x, s[5] = e.y, s[6] = e.z, s[7] = e.w;
+  } else {
+    load8(ct + 8 * c0, c);
+    load8(st + 8 * c0, s);
+  }
+}
+
+// (a, b) -> (a c - b s, b c + a s) on the lane's 8 pairs.
+__device__ __forceinline__ void turn(float* f, const float* c, const float* s, bool interleaved) {
+  if (interleaved) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float a = f[2 * j], b = f[2 * j + 1];
+      f[2 * j] = a * c[j] - b * s[j];
+      f[2 * j + 1] = b * c[j] + a * s[j];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float a = f[j], b = f[j + 8];
+      f[j] = a * c[j] - b * s[j];
+      f[j + 8] = b * c[j] + a * s[j];
+    }
+  }
+}
+
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+// A token's position, or -1 for padding (outside the table).
+__device__ __forceinline__ int64_t token_position(const RopeProblem& p, int b, int m) {
+  int64_t at = m;
+  if (p.pos != nullptr) at = p.pos[b * p.pos_b + m];
+  if (at < 0 || (p.half > 0 && at >= p.table_rows)) return -1;
+  return at;
+}
+
+// Rows [r0, r1) of one token's heads, UN groups of rows in flight per warp.
+template <int D, bool BF16, int UN>
+__device__ __forceinline__ void norm_rope_rows(const RopeProblem& p, const RopeRows& t, int b, int m,
+                                               int r0, int r1, bool live, bool rot, int c0, int c1,
+                                               const float* c, const float* s) {
+  constexpr int LPR = D / 16, RPW = 32 / LPR;
+  const int sub = (threadIdx.x & 31) / LPR;
+  const uint8_t* x = t.x + 2 * (b * t.xb + m * t.xm);
+  uint8_t* y = t.y + 2 * (b * t.yb + m * t.ym);
+  float w[16];
+  if (live) load_weights<BF16>(t.w, p.w32, c0, c1, w);
+  for (int r = r0; r < r1; r += RPW * UN) {
+    uint4 v[UN][2];
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const int row = r + u * RPW + sub;
+      v[u][0] = v[u][1] = make_uint4(0, 0, 0, 0);
+      if (live && row < r1) {
+        const uint4* src = reinterpret_cast<const uint4*>(x + 2 * row * t.xh);
+        v[u][0] = src[c0];
+        v[u][1] = src[c1];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const int row = r + u * RPW + sub;
+      float f[16];
+      unpack8<BF16>(v[u][0], f);
+      unpack8<BF16>(v[u][1], f + 8);
+      float sq = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sq = fmaf(f[i], f[i], sq);
+      sq = row_sum<LPR>(sq);
+      if (live) {  // a padding token's rows are zero
+        const float rs = rsqrtf(sq * (1.f / D) + p.eps);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] *= rs * w[i];
+        if (rot) turn(f, c, s, p.interleaved);
+      }
+      if (row < r1) {
+        uint4* dst = reinterpret_cast<uint4*>(y + 2 * row * t.yh);
+        dst[c0] = pack8<BF16>(f);
+        dst[c1] = pack8<BF16>(f + 8);
+      }
+    }
+  }
+}
+
+// One warp per unit: `per` rows of the H + G head rows of one token.
+template <int D, bool BF16, int UN>
+__global__ void __launch_bounds__(kRopeThreads)
+    norm_rope_kernel(const RopeProblem p, int segs, int per, int64_t units) {
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5);
+  if (unit >= units) return;
+  const uint32_t tok = static_cast<uint32_t>(unit) / static_cast<uint32_t>(segs);
+  const int seg = static_cast<int>(static_cast<uint32_t>(unit) - tok * segs);
+  const int b = static_cast<int>(tok / static_cast<uint32_t>(p.M));
+  const int m = static_cast<int>(tok - static_cast<uint32_t>(b) * p.M);
+  const int64_t at = token_position(p, b, m);
+  const bool live = at >= 0;
+  int c0, c1;
+  const int t = (threadIdx.x & 31) % (D / 16);
+  row_chunks(t, p.half, c0, c1);
+  const bool rot = t < (p.half >> 3);
+  float c[8], s[8];
+  if (live && rot) load_angles(p, at, c0, c1, c, s);
+  const int r0 = seg * per, r1 = min(r0 + per, p.q.heads + p.k.heads);
+  if (r0 < p.q.heads)
+    norm_rope_rows<D, BF16, UN>(p, p.q, b, m, r0, min(r1, p.q.heads), live, rot, c0, c1, c, s);
+  if (r1 > p.q.heads)
+    norm_rope_rows<D, BF16, UN>(p, p.k, b, m, max(r0 - p.q.heads, 0), r1 - p.q.heads, live, rot, c0,
+                                c1, c, s);
+}
+
+struct RopeBwdRows {
+  const uint8_t* x;   // Q or K as the forward read it
+  const uint8_t* dy;  // gradient of the forward's result, in the grad type
+  uint8_t* dx;
+  const void* w;
+  int64_t xb, xm, xh, gb, gm, gh, db, dm, dh;
+  int heads;
+};
+
+struct RopeBwdProblem {
+  RopeProblem a;  // tables, positions, flags (its q and k are unused)
+  RopeBwdRows q, k;
+  float* part;    // [CTAs, 2, D] partial dw, or NULL
+};
+
+template <int D, bool BF16, bool G32, int UN>
+__device__ __forceinline__ void norm_rope_bwd_rows(const RopeProblem& p, const RopeBwdRows& t, int b,
+                                                   int m, bool live, bool rot, int c0, int c1,
+                                                   const float* c, const float* s, float* dw) {
+  constexpr int LPR = D / 16, RPW = 32 / LPR;
+  const int sub = (threadIdx.x & 31) / LPR;
+  const uint8_t* x = t.x + 2 * (b * t.xb + m * t.xm);
+  const uint8_t* dy = t.dy + (G32 ? 4 : 2) * (b * t.gb + m * t.gm);
+  uint8_t* dx = t.dx + 2 * (b * t.db + m * t.dm);
+  if (!live) {  // padding: a zero gradient
+    for (int row = sub; row < t.heads; row += RPW) {
+      uint4* dst = reinterpret_cast<uint4*>(dx + 2 * row * t.dh);
+      dst[c0] = dst[c1] = make_uint4(0, 0, 0, 0);
+    }
+    return;
+  }
+  float w[16];
+  load_weights<BF16>(t.w, p.w32, c0, c1, w);
+  for (int r = 0; r < t.heads; r += RPW * UN) {
+    uint4 v[UN][2], g[UN][G32 ? 4 : 2];
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const int row = r + u * RPW + sub;
+      v[u][0] = v[u][1] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < (G32 ? 4 : 2); ++i) g[u][i] = make_uint4(0, 0, 0, 0);
+      if (row < t.heads) {
+        const uint4* src = reinterpret_cast<const uint4*>(x + 2 * row * t.xh);
+        v[u][0] = src[c0];
+        v[u][1] = src[c1];
+        if constexpr (G32) {
+          const uint4* gr = reinterpret_cast<const uint4*>(dy + 4 * row * t.gh);
+          g[u][0] = gr[2 * c0];
+          g[u][1] = gr[2 * c0 + 1];
+          g[u][2] = gr[2 * c1];
+          g[u][3] = gr[2 * c1 + 1];
+        } else {
+          const uint4* gr = reinterpret_cast<const uint4*>(dy + 2 * row * t.gh);
+          g[u][0] = gr[c0];
+          g[u][1] = gr[c1];
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const int row = r + u * RPW + sub;
+      float f[16], y[16];
+      unpack8<BF16>(v[u][0], f);
+      unpack8<BF16>(v[u][1], f + 8);
+      if constexpr (G32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          y[4 * i] = __uint_as_float(g[u][i].x);
+          y[4 * i + 1] = __uint_as_float(g[u][i].y);
+          y[4 * i + 2] = __uint_as_float(g[u][i].z);
+          y[4 * i + 3] = __uint_as_float(g[u][i].w);
+        }
+      } else {
+        unpack8<BF16>(g[u][0], y);
+        unpack8<BF16>(g[u][1], y + 8);
+      }
+      if (rot) {
+        float ns[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ns[i] = -s[i];
+        turn(y, c, ns, p.interleaved);
+      }
+      float sq = 0.f, gx = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        sq = fmaf(f[i], f[i], sq);
+        gx = fmaf(y[i] * w[i], f[i], gx);
+      }
+      sq = row_sum<LPR>(sq);
+      gx = row_sum<LPR>(gx);
+      const float rs = rsqrtf(sq * (1.f / D) + p.eps);
+      // rows past the heads hold zeros; with eps = 0 their rs is infinite
+      if (row < t.heads) {
+        const float k = gx * rs * rs * (1.f / D);  // mean(g w xhat) rs
+        float d[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          dw[i] = fmaf(y[i], f[i] * rs, dw[i]);
+          d[i] = rs * fmaf(-f[i], k, y[i] * w[i]);
+        }
+        uint4* dst = reinterpret_cast<uint4*>(dx + 2 * row * t.dh);
+        dst[c0] = pack8<BF16>(d);
+        dst[c1] = pack8<BF16>(d + 8);
+      }
+    }
+  }
+}
+
+// Sum of the 16 lane values over a warp's row groups, added by the lanes of
+// the first group into shared [D], warp after warp (a fixed order).
+template <int D>
+__device__ __forceinline__ void block_dw(const float* dw, int c0, int c1, float* sh) {
+  constexpr int LPR = D / 16;
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    v[i] = dw[i];
+#pragma unroll
+    for (int o = LPR; o < 32; o <<= 1) v[i] += __shfl_xor_sync(kFull, v[i], o);
+  }
+  for (int wi = 0; wi < kRopeBwdThreads / 32; ++wi) {
+    if ((threadIdx.x >> 5) == wi && (threadIdx.x & 31) < LPR) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sh[8 * c0 + i] = wi == 0 ? v[i] : sh[8 * c0 + i] + v[i];
+        sh[8 * c1 + i] = wi == 0 ? v[8 + i] : sh[8 * c1 + i] + v[8 + i];
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Warps walk the tokens; a CTA leaves one dw partial per norm.
+template <int D, bool BF16, bool G32, int UN>
+__global__ void __launch_bounds__(kRopeBwdThreads, 2)
+    norm_rope_bwd_kernel(const RopeBwdProblem pr) {
+  const RopeProblem& p = pr.a;
+  constexpr int kWarps = kRopeBwdThreads / 32;
+  __shared__ float sh[2][D];
+  int c0, c1;
+  const int t = (threadIdx.x & 31) % (D / 16);
+  row_chunks(t, p.half, c0, c1);
+  const bool rot = t < (p.half >> 3);
+  float dwq[16], dwk[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) dwq[i] = dwk[i] = 0.f;
+  const int64_t tokens = static_cast<int64_t>(p.B) * p.M;
+  for (int64_t tok = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); tok < tokens;
+       tok += static_cast<int64_t>(gridDim.x) * kWarps) {
+    const int b = static_cast<int>(static_cast<uint32_t>(tok) / static_cast<uint32_t>(p.M));
+    const int m = static_cast<int>(static_cast<uint32_t>(tok) - static_cast<uint32_t>(b) * p.M);
+    const int64_t at = token_position(p, b, m);
+    const bool live = at >= 0;
+    float c[8], s[8];
+    if (live && rot) load_angles(p, at, c0, c1, c, s);
+    norm_rope_bwd_rows<D, BF16, G32, UN>(p, pr.q, b, m, live, rot, c0, c1, c, s, dwq);
+    norm_rope_bwd_rows<D, BF16, G32, UN>(p, pr.k, b, m, live, rot, c0, c1, c, s, dwk);
+  }
+  if (pr.part == nullptr) return;
+  block_dw<D>(dwq, c0, c1, sh[0]);
+  block_dw<D>(dwk, c0, c1, sh[1]);
+  for (int i = threadIdx.x; i < 2 * D; i += kRopeBwdThreads)
+    pr.part[static_cast<int64_t>(blockIdx.x) * (2 * D) + i] = sh[i / D][i % D];
+}
+
+// dw from the CTAs' partials: a CTA sums 32 columns, 32 rows of partials side
+// by side, in a fixed order.
+template <int D>
+__global__ void __launch_bounds__(1024)
+    norm_rope_dw_kernel(const float* part, int parts, float* dwq, float* dwk) {
+  __shared__ float sh[32][33];
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + x;
+  float v = 0.f;
+  for (int r = y; r < parts; r += 32) v += part[static_cast<int64_t>(r) * (2 * D) + col];
+  sh[y][x] = v;
+  __syncthreads();
+  v = sh[x][y];  // the 32 sums of column y of this CTA
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  if (x == 0) {
+    const int out = blockIdx.x * 32 + y;
+    float* dst = out < D ? dwq : dwk;
+    if (dst != nullptr) dst[out < D ? out : out - D] = v;
+  }
+}
+
+// ---- host ---------------------------------------------------------------
+
+bool aligned(const void* p, uintptr_t a) {
+  return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
+int check_rope(int64_t B, int64_t M, int64_t H, int64_t G, int64_t D, int64_t R, int64_t table_rows,
+               int64_t positions_stride, float eps, int dtype, int weight_dtype) {
+  if (B < 0 || M < 0 || H <= 0 || G <= 0) return NSA_ERR_SHAPE;
+  if (D != 64 && D != 128) return NSA_ERR_HEAD_DIM;
+  if (R < 0 || R > D || R % 16 != 0) return NSA_ERR_SHAPE;
+  if (table_rows < 0 || table_rows > (int64_t(1) << 31) || positions_stride < 0)
+    return NSA_ERR_SHAPE;
+  if (!(eps >= 0.f) || std::isinf(eps)) return NSA_ERR_SHAPE;
+  const int64_t lim = int64_t(1) << 30;
+  if (B > lim || M > lim || H > 65536 || G > 65536) return NSA_ERR_SHAPE;
+  if (B * M >= (int64_t(1) << 31)) return NSA_ERR_SHAPE;
+  if (dtype != NSA_F16 && dtype != NSA_BF16) return NSA_ERR_DTYPE;
+  if (weight_dtype != NSA_F32 && weight_dtype != dtype) return NSA_ERR_DTYPE;
+  return NSA_OK;
+}
+
+// n groups of 3 element strides; NULL: contiguous rows of D. The last two
+// groups are written: a stride of 0 would put several rows in one place.
+int take_strides(const int64_t* strides, int n, const int64_t* heads, int64_t B, int64_t M,
+                 int64_t D, int64_t* out) {
+  for (int i = 0; i < n; ++i) {
+    if (strides == nullptr) {
+      out[3 * i] = M * heads[i] * D;
+      out[3 * i + 1] = heads[i] * D;
+      out[3 * i + 2] = D;
+    } else {
+      for (int j = 0; j < 3; ++j) {
+        const int64_t s = strides[3 * i + j];
+        if (s < 0 || s > (int64_t(1) << 40)) return NSA_ERR_SHAPE;
+        if (s % 8 != 0) return NSA_ERR_ALIGN;
+        const int64_t extent = j == 0 ? B : j == 1 ? M : heads[i];
+        if (i >= n - 2 && s == 0 && extent > 1) return NSA_ERR_SHAPE;
+        out[3 * i + j] = s;
+      }
+    }
+  }
+  return NSA_OK;
+}
+
+int check_tables(const float* cos_t, const float* sin_t, const int32_t* positions, int64_t M,
+                 int64_t R, int64_t table_rows) {
+  if (R > 0) {
+    if (table_rows > 0 && (!cos_t || !sin_t)) return NSA_ERR_NULL;
+    if (!aligned(cos_t, 16) || !aligned(sin_t, 16)) return NSA_ERR_ALIGN;
+    if (positions == nullptr && M > table_rows) return NSA_ERR_SHAPE;
+  }
+  return aligned(positions, 4) ? NSA_OK : NSA_ERR_ALIGN;
+}
+
+// CTAs of the backward, each with one dw partial: enough warps for the
+// loads of every SM (2 CTAs of 8 warps an SM at its registers), one warp a
+// token below that.
+int rope_bwd_ctas(int64_t tokens) {
+  const int64_t c = (tokens + kRopeBwdThreads / 32 - 1) / (kRopeBwdThreads / 32);
+  return static_cast<int>(c < 2 * kRopeSms ? c : 2 * kRopeSms);
+}
+
+template <int D, bool BF16>
+int launch_norm_rope(const RopeProblem& p, cudaStream_t st) {
+  constexpr int RPW = 32 / (D / 16), UN = 4;
+  const int rows = p.q.heads + p.k.heads;
+  const int64_t tokens = static_cast<int64_t>(p.B) * p.M;
+  // rows per warp: a whole token when the tokens alone give every SM 16
+  // warps, else as few rows as it takes to get there
+  const int64_t want = 16 * kRopeSms;
+  int64_t segs = (want + tokens - 1) / tokens;
+  const int64_t most = (rows + RPW - 1) / RPW;
+  if (segs > most) segs = most;
+  int64_t per = (rows + segs - 1) / segs;
+  per = (per + RPW - 1) / RPW * RPW;
+  segs = (rows + per - 1) / per;
+  const int64_t units = tokens * segs;
+  const int64_t blocks = (units + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+  if (units >= (int64_t(1) << 32)) return NSA_ERR_SHAPE;
+  norm_rope_kernel<D, BF16, UN><<<static_cast<unsigned>(blocks), kRopeThreads, 0, st>>>(
+      p, static_cast<int>(segs), static_cast<int>(per), units);
+  return cudaGetLastError() == cudaSuccess ? NSA_OK : NSA_ERR_LAUNCH;
+}
+
+template <int D, bool BF16, bool G32>
+int launch_norm_rope_bwd(const RopeBwdProblem& p, float* dwq, float* dwk, cudaStream_t st) {
+  const int ctas = rope_bwd_ctas(static_cast<int64_t>(p.a.B) * p.a.M);
+  norm_rope_bwd_kernel<D, BF16, G32, 1><<<ctas, kRopeBwdThreads, 0, st>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return NSA_ERR_LAUNCH;
+  if (p.part != nullptr) {
+    norm_rope_dw_kernel<D><<<2 * D / 32, 1024, 0, st>>>(p.part, ctas, dwq, dwk);
+    if (cudaGetLastError() != cudaSuccess) return NSA_ERR_LAUNCH;
+  }
+  return NSA_OK;
+}
+
+}  // namespace
+}  // namespace nsa
+
+extern "C" int nsa_qk_norm_rope(const void* Q, const void* K, void* Qo, void* Ko, const void* wq,
+                                const void* wk, const float* cos_table, const float* sin_table,
+                                const int32_t* positions, int64_t B, int64_t M, int64_t H,
+                                int64_t G, int64_t D, int64_t R, int64_t table_rows,
+                                int64_t positions_stride, float eps, int interleaved, int dtype,
+                                int weight_dtype, const int64_t* strides, void* stream) {
+  using namespace nsa;
+  int rc = check_rope(B, M, H, G, D, R, table_rows, positions_stride, eps, dtype, weight_dtype);
+  if (rc != NSA_OK) return rc;
+  const int64_t heads[4] = {H, G, H, G};
+  int64_t s[12];
+  if ((rc = take_strides(strides, 4, heads, B, M, D, s)) != NSA_OK) return rc;
+  if (B == 0 || M == 0) return NSA_OK;
+  if (!Q || !K || !Qo || !Ko) return NSA_ERR_NULL;
+  if (!aligned(Q, 16) || !aligned(K, 16) || !aligned(Qo, 16) || !aligned(Ko, 16) ||
+      !aligned(wq, 16) || !aligned(wk, 16))
+    return NSA_ERR_ALIGN;
+  if ((rc = check_tables(cos_table, sin_table, positions, M, R, table_rows)) != NSA_OK) return rc;
+  RopeProblem p{};
+  p.q = {static_cast<const uint8_t*>(Q), static_cast<uint8_t*>(Qo), wq, s[0], s[1], s[2], s[6], s[7],
+         s[8], static_cast<int>(H)};
+  p.k = {static_cast<const uint8_t*>(K), static_cast<uint8_t*>(Ko), wk, s[3], s[4], s[5], s[9],
+         s[10], s[11], static_cast<int>(G)};
+  p.cos_t = cos_table;
+  p.sin_t = sin_table;
+  p.pos = positions;
+  p.pos_b = positions_stride;
+  p.table_rows = table_rows;
+  p.B = static_cast<int>(B);
+  p.M = static_cast<int>(M);
+  p.half = static_cast<int>(R / 2);
+  p.interleaved = interleaved != 0;
+  p.w32 = weight_dtype == NSA_F32;
+  p.eps = eps;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool bf = dtype == NSA_BF16;
+  if (D == 64) return bf ? launch_norm_rope<64, true>(p, st) : launch_norm_rope<64, false>(p, st);
+  return bf ? launch_norm_rope<128, true>(p, st) : launch_norm_rope<128, false>(p, st);
+}
+
+extern "C" int64_t nsa_qk_norm_rope_bwd_workspace_bytes(int64_t B, int64_t M, int64_t D) {
+  using namespace nsa;
+  const int rc = check_rope(B, M, 1, 1, D, 0, 0, 0, 0.f, NSA_F16, NSA_F32);
+  if (rc != NSA_OK) return rc;
+  return (static_cast<int64_t>(rope_bwd_ctas(B * M)) * 2 * D * 4 + 255) / 256 * 256;
+}
+
+extern "C" int nsa_qk_norm_rope_bwd(
+    const void* Q, const void* K, const void* dQo, const void* dKo, void* dQ, void* dK, float* dwq,
+    float* dwk, const void* wq, const void* wk, const float* cos_table, const float* sin_table,
+    const int32_t* positions, int64_t B, int64_t M, int64_t H, int64_t G, int64_t D, int64_t R,
+    int64_t table_rows, int64_t positions_stride, float eps, int interleaved, int dtype,
+    int weight_dtype, int grad_dtype, const int64_t* strides, void* workspace,
+    int64_t workspace_bytes, void* stream) {
+  using namespace nsa;
+  int rc = check_rope(B, M, H, G, D, R, table_rows, positions_stride, eps, dtype, weight_dtype);
+  if (rc != NSA_OK) return rc;
+  if (grad_dtype != NSA_F32 && grad_dtype != dtype) return NSA_ERR_DTYPE;
+  const int64_t heads[6] = {H, G, H, G, H, G};
+  int64_t s[18];
+  if ((rc = take_strides(strides, 6, heads, B, M, D, s)) != NSA_OK) return rc;
+  if (!aligned(dwq, 4) || !aligned(dwk, 4)) return NSA_ERR_ALIGN;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (B == 0 || M == 0) {  // no token: the weights' gradients are zero
+    if (dwq && cudaMemsetAsync(dwq, 0, D * 4, st) != cudaSuccess) return NSA_ERR_LAUNCH;
+    if (dwk && cudaMemsetAsync(dwk, 0, D * 4, st) != cudaSuccess) return NSA_ERR_LAUNCH;
+    return NSA_OK;
+  }
+  if (!Q || !K || !dQo || !dKo || !dQ || !dK) return NSA_ERR_NULL;
+  if (!aligned(Q, 16) || !aligned(K, 16) || !aligned(dQo, 16) || !aligned(dKo, 16) ||
+      !aligned(dQ, 16) || !aligned(dK, 16) || !aligned(wq, 16) || !aligned(wk, 16))
+    return NSA_ERR_ALIGN;
+  if ((rc = check_tables(cos_table, sin_table, positions, M, R, table_rows)) != NSA_OK) return rc;
+  const bool want_dw = dwq != nullptr || dwk != nullptr;
+  if (want_dw) {
+    if (!workspace || workspace_bytes < nsa_qk_norm_rope_bwd_workspace_bytes(B, M, D))
+      return NSA_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return NSA_ERR_ALIGN;
+  }
+  RopeBwdProblem p{};
+  p.a.cos_t = cos_table;
+  p.a.sin_t = sin_table;
+  p.a.pos = positions;
+  p.a.pos_b = positions_stride;
+  p.a.table_rows = table_rows;
+  p.a.B = static_cast<int>(B);
+  p.a.M = static_cast<int>(M);
+  p.a.half = static_cast<int>(R / 2);
+  p.a.interleaved = interleaved != 0;
+  p.a.w32 = weight_dtype == NSA_F32;
+  p.a.eps = eps;
+  p.q = {static_cast<const uint8_t*>(Q), static_cast<const uint8_t*>(dQo), static_cast<uint8_t*>(dQ),
+         wq, s[0], s[1], s[2], s[6], s[7], s[8], s[12], s[13], s[14], static_cast<int>(H)};
+  p.k = {static_cast<const uint8_t*>(K), static_cast<const uint8_t*>(dKo), static_cast<uint8_t*>(dK),
+         wk, s[3], s[4], s[5], s[9], s[10], s[11], s[15], s[16], s[17], static_cast<int>(G)};
+  p.part = want_dw ? static_cast<float*>(workspace) : nullptr;
+  const bool bf = dtype == NSA_BF16, g32 = grad_dtype == NSA_F32;
+  if (D == 64) {
+    if (bf)
+      return g32 ? launch_norm_rope_bwd<64, true, true>(p, dwq, dwk, st)
+                 : launch_norm_rope_bwd<64, true, false>(p, dwq, dwk, st);
+    return g32 ? launch_norm_rope_bwd<64, false, true>(p, dwq, dwk, st)
+               : launch_norm_rope_bwd<64, false, false>(p, dwq, dwk, st);
+  }
+  if (bf)
+    return g32 ? launch_norm_rope_bwd<128, true, true>(p, dwq, dwk, st)
+               : launch_norm_rope_bwd<128, true, false>(p, dwq, dwk, st);
+  return g32 ? launch_norm_rope_bwd<128, false, true>(p, dwq, dwk, st)
+             : launch_norm_rope_bwd<128, false, false>(p, dwq, dwk, st);
+}
