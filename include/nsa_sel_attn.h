@@ -461,6 +461,57 @@ int nsa_swa_fwd(const void* Q, const void* K, const void* V, void* O, float* LSE
                 void* stream);
 
 /*
+ * nsa_swa_bwd_workspace_bytes -- device workspace of nsa_swa_bwd: LSE and
+ * delta of every (batch, head, query), and, where the key tiles are fewer than
+ * the SMs, fp32 parts of dK and dV. Negative nsa_status for invalid sizes.
+ * Pure host arithmetic.
+ */
+int64_t nsa_swa_bwd_workspace_bytes(int64_t B, int64_t M, int64_t N, int64_t H, int64_t H_kv,
+                                    int64_t D, int64_t window_left, int64_t window_right);
+
+/*
+ * nsa_swa_bwd -- gradients of nsa_swa_fwd.
+ *
+ *   Q, K, V, window_left, window_right, scale, dtype   as for the forward
+ *   O, LSE         the forward's outputs: O of type dtype, LSE fp32 [B, H, M]
+ *   dO             upstream gradient of O, dtype, [B, M, H, D]
+ *   dQ             [B, M, H, D]     (output, grad_dtype)
+ *   dK, dV         [B, N, H_kv, D]  (output, grad_dtype)
+ *   grad_dtype     NSA_F32, or dtype: the fp32 sums rounded once (nearest even)
+ *   workspace      device memory of at least nsa_swa_bwd_workspace_bytes()
+ *                  bytes for these arguments, 16-byte aligned (else
+ *                  NSA_ERR_WORKSPACE, NSA_ERR_ALIGN)
+ *
+ * With p = exp(scale q.k - LSE), dP = dO.v and delta = dO.O per row and head:
+ * dS = p (dP - delta), dQ = scale sum dS k, dK = scale sum dS q, dV = sum p dO
+ * over the visible pairs (dK and dV over the query heads of the KV head too).
+ * The products run on the 5th-generation tensor cores with fp32 sums in tensor
+ * memory; p and dS are rounded to dtype before the products they enter. Every
+ * sum has a fixed order: equal calls give equal bits. With fp16 inputs p and dS
+ * are carried times 2^12 and 2^6, so small ones keep their precision; dS is
+ * then finite while |dP - delta| < 1023.
+ *
+ * A query without keys (LSE = -inf) gets dQ = 0 and adds nothing to dK, dV; a
+ * key that no query sees gets dK = dV = 0. p and dS of hidden pairs are exactly
+ * 0 whatever Q, K, V and dO hold there, but they are multiplied by rows that
+ * share a tile with visible ones: K must be finite in the 64-key tiles that
+ * hold a key some query of a 128-query tile sees, Q and dO in the 64-query
+ * tiles that hold a query which sees some key of a 128-key tile (as V must for
+ * the forward, in 128-key tiles). M and N are at most 2^29.
+ *
+ * Asynchronous: two kernels on `stream` (three where dK, dV are joined from
+ * parts), no allocation; calls that may overlap need workspaces of their own.
+ * Errors before launch as nsa_swa_fwd, plus NSA_ERR_WORKSPACE. With no query,
+ * or no key, the gradients are zeroed and no workspace is needed. A timed-out
+ * device wait is reported by nsa_sync_status.
+ */
+int nsa_swa_bwd(const void* Q, const void* K, const void* V, const void* O, const float* LSE,
+                const void* dO, void* dQ, void* dK, void* dV, int64_t B, int64_t M, int64_t N,
+                int64_t H, int64_t H_kv, int64_t D, int64_t window_left, int64_t window_right,
+                float scale, int dtype, int grad_dtype, void* workspace, int64_t workspace_bytes,
+                void* stream);
+
+/*
  * nsa_qk_norm_rope -- RMS norm of every query and key head and the position
  * rotation in one pass: what a layer does between its Q/K projections and
  * the attention entry points of this library.

@@ -12,6 +12,7 @@ Public API (GPU only; the CUDA library must be built):
 * :func:`sel_attn_fwd_host` -- the forward with host buffers in and out;
 * :func:`swa_fwd` -- GQA sliding-window (or dense) attention forward on the
   tcgen05 tensor cores;
+* :func:`swa_bwd` -- dQ, dK, dV from dO and that forward's O and LSE;
 * :func:`qk_norm_rope` and :func:`qk_norm_rope_bwd` -- RMS norm of every
   query and key head and the position rotation in one pass, before any of
   the attention calls, and its gradients (:func:`rope_tables` builds the
@@ -23,8 +24,8 @@ seeded synthetic workloads.
 
 from ._lib import (NsaError, load, qk_norm_rope, qk_norm_rope_bwd, rope_tables,  # noqa: F401
                    sel_attn_bwd, sel_attn_fwd, sel_attn_fwd_host, sel_attn_fwd_shared,
-                   status_string, swa_fwd, topk_blocks)
+                   status_string, swa_bwd, swa_fwd, topk_blocks)
 
 __all__ = ["sel_attn_fwd", "sel_attn_fwd_shared", "sel_attn_bwd", "sel_attn_fwd_host",
-           "topk_blocks", "swa_fwd", "qk_norm_rope", "qk_norm_rope_bwd", "rope_tables",
+           "topk_blocks", "swa_fwd", "swa_bwd", "qk_norm_rope", "qk_norm_rope_bwd", "rope_tables",
            "load", "status_string", "NsaError"]

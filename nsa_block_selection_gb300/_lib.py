@@ -26,7 +26,8 @@ EXPORTS = ("nsa_status_string", "nsa_version", "nsa_sel_attn_fwd", "nsa_sel_attn
            "nsa_sel_attn_fwd_shared_workspace_bytes", "nsa_sel_attn_fwd_shared",
            "nsa_probe_l2_gather", "nsa_probe_l2_gather_bytes", "nsa_probe_gather_rows",
            "nsa_probe_reduce_rows", "nsa_sel_attn_fwd_host_ex", "nsa_sel_attn_bwd_ex",
-           "nsa_qk_norm_rope", "nsa_qk_norm_rope_bwd", "nsa_qk_norm_rope_bwd_workspace_bytes")
+           "nsa_qk_norm_rope", "nsa_qk_norm_rope_bwd", "nsa_qk_norm_rope_bwd_workspace_bytes",
+           "nsa_swa_bwd", "nsa_swa_bwd_workspace_bytes")
 
 _lib = None
 
@@ -110,6 +111,10 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.nsa_probe_gather_rows.argtypes = [vp, vp, vp, i64, i64, i64, i64, i64, i64, c_int, i64,
                                           c_int, c_int, i64, vp]
     f32 = ctypes.c_float
+    lib.nsa_swa_bwd_workspace_bytes.restype = i64
+    lib.nsa_swa_bwd_workspace_bytes.argtypes = [i64] * 8
+    lib.nsa_swa_bwd.restype = c_int
+    lib.nsa_swa_bwd.argtypes = [vp] * 9 + [i64] * 8 + [f32, c_int, c_int, vp, i64, vp]
     lib.nsa_qk_norm_rope.restype = c_int
     lib.nsa_qk_norm_rope.argtypes = [vp] * 9 + [i64] * 8 + [f32, c_int, c_int, c_int, vp, vp]
     lib.nsa_qk_norm_rope_bwd_workspace_bytes.restype = i64
@@ -469,6 +474,76 @@ def swa_fwd(q, k, v, window=(-1, -1), scale: Optional[float] = None, out=None, l
     if st != NSA_OK:
         raise NsaError(st, "nsa_swa_fwd")
     return out, lse
+
+
+def swa_bwd_workspace_bytes(B, M, N, H, H_kv, D, window=(-1, -1)) -> int:
+    n = load().nsa_swa_bwd_workspace_bytes(B, M, N, H, H_kv, D, int(window[0]), int(window[1]))
+    if n < 0:
+        raise NsaError(int(n), "nsa_swa_bwd_workspace_bytes")
+    return int(n)
+
+
+def swa_bwd(q, k, v, o, lse, do, window=(-1, -1), scale: Optional[float] = None, dq=None, dk=None,
+            dv=None, grad_dtype=None, workspace=None, stream=None):
+    """Gradients of :func:`swa_fwd` (nsa_swa_bwd): returns (dQ, dK, dV).
+
+    q, k, v, ``window`` and ``scale`` as passed to the forward, ``o`` and
+    ``lse`` what it returned, ``do`` the upstream gradient of o (q's dtype,
+    [B, M, H, D]); all contiguous on one CUDA device. The gradients are of
+    q's dtype, or fp32 with ``grad_dtype=torch.float32`` (or preallocated
+    ones). ``workspace`` (CUDA uint8, swa_bwd_workspace_bytes) is allocated
+    when omitted; calls that may overlap need one each.
+    """
+    import torch
+
+    lib = load()
+    if q.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"q must be fp16 or bf16, got {q.dtype}")
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("shape mismatch: q [B,M,H,D], k/v [B,N,H_kv,D]")
+    B, M, H, D = q.shape
+    Bk, N, Hkv, Dk = k.shape
+    if (Bk, Dk) != (B, D):
+        raise ValueError("shape mismatch: q [B,M,H,D], k/v [B,N,H_kv,D]")
+    if grad_dtype is None:
+        given = [t for t in (dq, dk, dv) if t is not None]
+        grad_dtype = given[0].dtype if given else q.dtype
+    if grad_dtype not in (torch.float32, q.dtype):
+        raise TypeError(f"gradients must be fp32 or {q.dtype}, got {grad_dtype}")
+    dev = q.device
+    dq = torch.empty(q.shape, dtype=grad_dtype, device=dev) if dq is None else dq
+    dk = torch.empty(k.shape, dtype=grad_dtype, device=dev) if dk is None else dk
+    dv = torch.empty(k.shape, dtype=grad_dtype, device=dev) if dv is None else dv
+    named = (("q", q, q.dtype, q.shape), ("k", k, q.dtype, k.shape), ("v", v, q.dtype, k.shape),
+             ("o", o, q.dtype, q.shape), ("lse", lse, torch.float32, (B, H, M)),
+             ("do", do, q.dtype, q.shape), ("dq", dq, grad_dtype, q.shape),
+             ("dk", dk, grad_dtype, k.shape), ("dv", dv, grad_dtype, k.shape))
+    for name, t, dt, shape in named:
+        if t.dtype != dt:
+            raise TypeError(f"{name} must be {dt}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have the shape {tuple(shape)}")
+    for name, t, _, _ in named:
+        if not t.is_cuda or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous tensor on q's CUDA device")
+    left, right = (int(window[0]), int(window[1])) if window is not None else (-1, -1)
+    if workspace is None:
+        need = swa_bwd_workspace_bytes(B, M, N, H, Hkv, D, (left, right))
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    if workspace.device != dev:
+        raise ValueError("workspace must be on q's CUDA device")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    sc = float(scale) if scale is not None else 0.0  # the ABI: <= 0 selects 1/sqrt(D)
+    with torch.cuda.device(dev):
+        st = lib.nsa_swa_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(do), _ptr(dq),
+                             _ptr(dk), _ptr(dv), B, M, N, H, Hkv, D, left, right, sc,
+                             _dtype_code(q.dtype), _dtype_code(grad_dtype), _ptr(workspace),
+                             workspace.numel() * workspace.element_size(),
+                             ctypes.c_void_p(stream.cuda_stream))
+    if st != NSA_OK:
+        raise NsaError(st, "nsa_swa_bwd")
+    return dq, dk, dv
 
 
 def rope_tables(rows: int, rot_dim: int, base: float = 10000.0, device="cuda"):

@@ -1,0 +1,894 @@
+// Gradients of the GQA sliding-window (or dense) attention forward for
+// sm_103a, on the 5th-generation tensor cores.
+//
+// Per visible (query i, key j) of a head, with the forward's LSE and O:
+//   p = exp(scale q.k - LSE_i),  delta_i = dO_i . O_i,  dP = dO_i . v_j,
+//   dS = p (dP - delta_i),
+//   dQ_i = scale sum_j dS k_j,  dK_j = scale sum_i dS q_i,  dV_j = sum_i p dO_i
+// (dK, dV over the query heads of the KV head too). Scores, p, dP, dS and all
+// sums are fp32; p and dS are rounded to the inputs' type for the products
+// they enter, gradients once when they are stored.
+//
+// Two kernels form p and dP each for itself: 7 products of 2 D operations a
+// pair instead of the 5 that one pass needs, but no dQ row has to be added up
+// in memory. A pass over key tiles adds 4 D bytes of fp32 a (query, key tile)
+// to dQ, 64 KB for the 5 x 512 tensor-pipe clocks of a 128 x 128 tile at
+// D = 128: 7 TB/s over 152 SMs, twice the 3.6 TB/s that fp32 reductions
+// reach here, in an order that changes from run to run. Here every sum is
+// made in tensor memory in a fixed order: equal calls give equal bits.
+//
+//  1. swa_bwd_dq_kernel: one CTA per 128 queries of a head, walking the key
+//     tiles of 64 that their windows touch. Q and dO stay in tensor memory as
+//     the A operands of S = Q K^T and dP = dO V^T; dS overwrites S there and
+//     is the A operand of dQ += dS K. Taking every A from tensor memory
+//     leaves 64 B a clock of shared-memory reads for B: with A in shared
+//     memory the 64-column products would need 192 of the 128 there are.
+//     S and dP have two buffers each, so the tensor pipe runs S and dP of the
+//     next tile and dQ of the previous one while eight warps form dS. It also
+//     leaves LSE log2 e and delta of every query for the second kernel.
+//  2. swa_bwd_dkv_kernel: one CTA per 128 keys of a KV head (or per part of
+//     its query heads and queries, where there are too few keys for the SMs),
+//     walking its (query head, 64 queries) steps: S^T = K Q^T, dP^T = V dO^T,
+//     dV += P^T dO, dK += dS^T Q. K (and V at D = 64) is kept in tensor memory.
+//     What the two accumulators leave of it holds three 64-column slots that
+//     S, dP of successive steps take in turn: S of the next step is formed
+//     while dP of this one is in use, and dP of the next where P was.
+//  3. swa_bwd_join_kernel: where step 2 was split, the sum of its fp32 parts.
+//
+// Every mbarrier wait is bounded (1 s); a role that gives up sets the status
+// word, waits for its own copies, and every role reaches the teardown, which
+// frees the tensor memory.
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "common.cuh"
+#include "nsa_sel_attn.h"
+#include "ptx.cuh"
+#include "status.cuh"
+#include "tc.cuh"
+
+namespace nsa {
+namespace {
+
+constexpr int kBlk = 128;       // queries (dQ) or keys (dK, dV) of a CTA: the M of its products
+constexpr int kStep = 64;       // keys (dQ) or queries (dK, dV) of a step
+constexpr int kThreads = 320;   // 8 elementwise warps, the TMA warp, the MMA warp
+constexpr int kAtomStep = kStep * 128;  // bytes of 64 rows x 64 entries
+constexpr int kAtomBlk = kBlk * 128;
+constexpr uint32_t kTmemAll = 512;
+
+// fp16 has no exponents below 2^-14 at full precision, and over thousands of
+// keys p is smaller than that: with fp16 inputs p is carried as 2^12 p (at
+// most 4096) and dS as 2^6 dS (finite while |dP - delta| < 1023), both
+// exact factors that the epilogues divide out. bf16 needs neither.
+template <bool BF16>
+struct Shift {
+  static constexpr float kP = BF16 ? 0.f : 12.f;
+  static constexpr float kS = BF16 ? 0.f : 6.f;
+  static constexpr float kPInv = BF16 ? 1.f : 1.f / 4096.f;
+  static constexpr float kSInv = BF16 ? 1.f : 1.f / 64.f;   // also 2^(kS - kP)
+};
+
+struct SwaBwdProblem {
+  const uint16_t *Q, *K, *V, *O, *dO;
+  const float* LSE;
+  void *dQ, *dK, *dV;
+  float* lse2;   // [B, H, Mp]: LSE log2 e less Shift::kP; +inf for rows without keys
+  float* delta;  // [B, H, Mp]: delta 2^(kS - kP)
+  float* part;   // [splits, 2, B, N, Hkv, D], or NULL
+  int B, M, N, H, Hkv, hpg, Mp, qtiles, ktiles, splits;
+  int left, right;  // clamped to [0, M] and [0, N]: unbounded in effect
+  float sl2, scale;
+  bool g32;  // gradients fp32 instead of the inputs' type
+};
+
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+}
+
+template <bool BF16>
+__device__ __forceinline__ float lo16(uint32_t v) {
+  if constexpr (BF16) return __uint_as_float(v << 16);
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(v & 0xffffu)));
+}
+template <bool BF16>
+__device__ __forceinline__ float hi16(uint32_t v) {
+  if constexpr (BF16) return __uint_as_float(v & 0xffff0000u);
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(v >> 16)));
+}
+
+// Row of D 16-bit entries -> this thread's lane of tensor memory (two entries
+// a column: an A operand). NULL: a row of zeros.
+template <int D>
+__device__ __forceinline__ void row_to_tmem(uint32_t taddr, const uint16_t* row) {
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) {
+    uint32_t r[32];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (row != nullptr) v = reinterpret_cast<const uint4*>(row)[8 * c + q];
+      r[4 * q] = v.x, r[4 * q + 1] = v.y, r[4 * q + 2] = v.z, r[4 * q + 3] = v.w;
+    }
+    tc_st32(taddr + 32 * c, r);
+  }
+}
+
+// 32 fp32 columns times `f`, stored from column `col` of a row of gradients.
+template <bool BF16>
+__device__ __forceinline__ void store_row32(void* base, int64_t row_off, int col, bool g32,
+                                            const uint32_t* r, float f) {
+  if (g32) {
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(base) + row_off + col);
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      dst[q] = make_float4(__uint_as_float(r[4 * q]) * f, __uint_as_float(r[4 * q + 1]) * f,
+                           __uint_as_float(r[4 * q + 2]) * f, __uint_as_float(r[4 * q + 3]) * f);
+  } else {
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + row_off + col);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = pack2_t<BF16>(__uint_as_float(r[8 * q + 2 * e]) * f,
+                             __uint_as_float(r[8 * q + 2 * e + 1]) * f);
+      dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- dQ
+
+template <int D>
+struct DqCfg {
+  static constexpr int kAtoms = D / 64;
+  static constexpr int kTile = kStep * D * 2;      // one K or V tile
+  static constexpr int kStages = D == 128 ? 6 : 8;
+  static constexpr int kOffStat = kStages * 2 * kTile;  // lse2 and delta of the CTA's rows
+  static constexpr int kOffBar = kOffStat + 2 * kBlk * 4;
+  static constexpr int kFull = 0, kEmpty = kStages, kReady = 2 * kStages, kSFull = kReady + 1,
+                       kDsFull = kSFull + 2, kDone = kDsFull + 2, kNumBars = kDone + 1;
+  static constexpr int kOffTmem = kOffBar + kNumBars * 8;
+  static constexpr int kSmem = kOffTmem + 16 + 1024;
+  static_assert(kSmem <= 232448 && kSmem > 118784, "one CTA per SM");
+  // tensor-memory columns
+  static constexpr uint32_t kColQ = 0, kColDo = D / 2, kColDq = D, kColS = 2 * D,
+                            kColP = 2 * D + 2 * kStep;
+  static_assert(2 * D + 4 * kStep <= 512, "tensor memory");
+};
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    swa_bwd_dq_kernel(const SwaBwdProblem p, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV) {
+  using C = DqCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const gbase = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto bar = [&](int i) { return base + C::kOffBar + 8u * static_cast<uint32_t>(i); };
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(bar(C::kFull + s), 1);
+      mbar_init(bar(C::kEmpty + s), 1);
+    }
+    mbar_init(bar(C::kReady), 256);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(C::kSFull + s), 1);
+      mbar_init(bar(C::kDsFull + s), 256);
+    }
+    mbar_init(bar(C::kDone), 1);
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tc_alloc(base + C::kOffTmem, kTmemAll);
+    tc_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + C::kOffTmem);
+
+  // the CTA's item: (b, KV head, query tile, head), heads fastest so that
+  // the CTAs of a moment share K and V in L2; later tiles, which see more
+  // keys under a causal window, first
+  uint32_t x = blockIdx.x;
+  const int hh = static_cast<int>(x % static_cast<uint32_t>(p.hpg));
+  x /= static_cast<uint32_t>(p.hpg);
+  const int qt = p.qtiles - 1 - static_cast<int>(x % static_cast<uint32_t>(p.qtiles));
+  x /= static_cast<uint32_t>(p.qtiles);
+  const int g = static_cast<int>(x % static_cast<uint32_t>(p.Hkv));
+  const int b = static_cast<int>(x / static_cast<uint32_t>(p.Hkv));
+  const int h = g * p.hpg + hh;
+  const int q0 = qt * kBlk, q_last = min(q0 + kBlk, p.M) - 1;
+  const int jlo = max(0, q0 - p.left), jhi = min(p.N - 1, q_last + p.right);
+  const int t0 = jlo / kStep, nt = jhi >= jlo ? jhi / kStep - t0 + 1 : 0;
+  bool failed = false;
+
+  if (warp == 8) {
+    if (lane == 0 && nt > 0) {
+      // ---- TMA producer: K and V tiles of 64 keys ----
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+      const uint64_t keep = l2_policy_evict_last();
+      int i = 0;
+      for (; i < nt; ++i) {
+        const int s = i % C::kStages;
+        if (i >= C::kStages &&
+            !wait_phase(bar(C::kEmpty + s), (i / C::kStages - 1) & 1, kWaitLimitNs)) {
+          failed = true;
+          break;
+        }
+        mbar_arrive_expect_tx(bar(C::kFull + s), 2 * C::kTile);
+        const uint32_t dst = base + s * 2 * C::kTile;
+        for (int a = 0; a < C::kAtoms; ++a) {
+          tma_load_4d(dst + a * kAtomStep, &tmK, bar(C::kFull + s), a * 64, g, (t0 + i) * kStep, b,
+                      keep);
+          tma_load_4d(dst + C::kTile + a * kAtomStep, &tmV, bar(C::kFull + s), a * 64, g,
+                      (t0 + i) * kStep, b, keep);
+        }
+      }
+      if (failed)  // leave nothing in flight
+        for (int k = max(0, i - C::kStages); k < i; ++k)
+          wait_phase(bar(C::kFull + k % C::kStages), (k / C::kStages) & 1, kWaitLimitNs);
+    }
+  } else if (warp == 9) {
+    if (lane == 0 && nt > 0) {
+      // ---- MMA issuer: S_i, dP_i, dQ_{i-1} ----
+      constexpr uint32_t id_s = umma_idesc_f16(kBlk, kStep, BF16, false);
+      constexpr uint32_t id_q = umma_idesc_f16(kBlk, D, BF16, true);
+      auto issue_dq = [&](int i) -> bool {
+        if (!wait_phase(bar(C::kDsFull + (i & 1)), (i >> 1) & 1, kWaitLimitNs)) return false;
+        tc_fence_after();
+        const uint32_t ds = tmem + C::kColS + (i & 1) * kStep;
+        const uint32_t kb = base + (i % C::kStages) * 2 * C::kTile;
+#pragma unroll
+        for (int kk = 0; kk < kStep / 16; ++kk)  // dS of keys 0..31 at column 0, 32..63 at 32
+          tc_mma_ts(tmem + C::kColDq, ds + (kk >> 1) * 32 + (kk & 1) * 8,
+                    umma_desc_sw128(kb + kk * 2048, kAtomStep), id_q, (i > 0 || kk > 0) ? 1u : 0u);
+        tc_commit(bar(C::kEmpty + i % C::kStages));
+        return true;
+      };
+      bool ok = wait_phase(bar(C::kReady), 0, kWaitLimitNs);
+      for (int i = 0; i < nt && ok; ++i) {
+        const int s = i % C::kStages;
+        ok = wait_phase(bar(C::kFull + s), (i / C::kStages) & 1, kWaitLimitNs);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t kb = base + s * 2 * C::kTile, vb = kb + C::kTile;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc_mma_ts(tmem + C::kColS + (i & 1) * kStep, tmem + C::kColQ + 8 * kk,
+                    umma_desc_sw128(kb + (kk >> 2) * kAtomStep + (kk & 3) * 32, 16), id_s,
+                    kk > 0 ? 1u : 0u);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc_mma_ts(tmem + C::kColP + (i & 1) * kStep, tmem + C::kColDo + 8 * kk,
+                    umma_desc_sw128(vb + (kk >> 2) * kAtomStep + (kk & 3) * 32, 16), id_s,
+                    kk > 0 ? 1u : 0u);
+        tc_commit(bar(C::kSFull + (i & 1)));
+        if (i > 0) ok = issue_dq(i - 1);
+      }
+      if (ok) ok = issue_dq(nt - 1);
+      // also after a failed wait: nothing is left in flight at the teardown
+      tc_commit(bar(C::kDone));
+      failed = !wait_phase(bar(C::kDone), 0, kWaitLimitNs) || !ok;
+    }
+  } else {
+    // ---- elementwise: thread <-> (query row, half of a step's columns) ----
+    const int wg = warp >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane, iq = q0 + row;
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    float* const stat = reinterpret_cast<float*>(gbase + C::kOffStat);
+    auto wait_all = [&](int i, uint32_t parity) {
+      return __all_sync(kFull, wait_phase(bar(i), parity, kWaitLimitNs));
+    };
+    const bool in = iq < p.M;
+    const int64_t off = ((static_cast<int64_t>(b) * p.M + (in ? iq : 0)) * p.H + h) * D;
+    if (wg == 0) {
+      row_to_tmem<D>(lane_addr + C::kColQ, in ? p.Q + off : nullptr);
+    } else {
+      // dO to tensor memory; delta, LSE in base 2
+      float dl = 0.f, l2 = INFINITY;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t r[32];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          uint4 v = make_uint4(0, 0, 0, 0), o = v;
+          if (in) {
+            v = reinterpret_cast<const uint4*>(p.dO + off)[8 * c + q];
+            o = reinterpret_cast<const uint4*>(p.O + off)[8 * c + q];
+          }
+          const uint32_t vv[4] = {v.x, v.y, v.z, v.w}, oo[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            dl = fmaf(lo16<BF16>(vv[e]), lo16<BF16>(oo[e]), dl);
+            dl = fmaf(hi16<BF16>(vv[e]), hi16<BF16>(oo[e]), dl);
+            r[4 * q + e] = vv[e];
+          }
+        }
+        tc_st32(lane_addr + C::kColDo + 32 * c, r);
+      }
+      if (in) {
+        const float l = p.LSE[(static_cast<int64_t>(b) * p.H + h) * p.M + iq];
+        if (l != -INFINITY) l2 = l * 1.4426950408889634f;
+        else dl = 0.f;
+      }
+      stat[row] = l2;
+      stat[kBlk + row] = dl;
+      if (iq < p.Mp) {
+        const int64_t at = (static_cast<int64_t>(b) * p.H + h) * p.Mp + iq;
+        p.lse2[at] = l2 - Shift<BF16>::kP;
+        p.delta[at] = dl * Shift<BF16>::kSInv;
+      }
+    }
+    tc_wait_st();
+    tc_fence_before();
+    mbar_arrive(bar(C::kReady));
+    bar_sync(1, 256);
+    const float neg = -(stat[row] - Shift<BF16>::kS), dl = stat[kBlk + row];
+    const int lo_i = max(0, iq - p.left), hi_i = min(p.N - 1, iq + p.right);
+    const int in_lo = max(0, q_last - p.left), in_hi = min(p.N - 1, q0 + p.right);
+    for (int i = 0; i < nt; ++i) {
+      if (!wait_all(C::kSFull + (i & 1), (i >> 1) & 1)) {
+        failed = true;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t sa = lane_addr + C::kColS + (i & 1) * kStep + 32 * wg;
+      uint32_t s[32], d[32];
+      tc_ld32(sa, s);
+      tc_ld32(lane_addr + C::kColP + (i & 1) * kStep + 32 * wg, d);
+      tc_wait_ld();
+      const int j0 = (t0 + i) * kStep;
+      float v[32];
+#pragma unroll
+      for (int c = 0; c < 32; ++c)
+        v[c] = ex2(fmaf(__uint_as_float(s[c]), p.sl2, neg)) * (__uint_as_float(d[c]) - dl);
+      if (j0 < in_lo || j0 + kStep - 1 > in_hi) {  // the same for the whole CTA
+        const int jc = j0 + 32 * wg;
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (jc + c < lo_i || jc + c > hi_i) v[c] = 0.f;
+      }
+      uint32_t w[16];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) w[c] = pack2_t<BF16>(v[2 * c], v[2 * c + 1]);
+      tc_st16(sa, w);
+      tc_wait_st();
+      tc_fence_before();
+      mbar_arrive(bar(C::kDsFull + (i & 1)));
+    }
+    if (!failed) {
+      if (nt > 0 && !wait_all(C::kDone, 0)) failed = true;
+    }
+    if (!failed) {
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        const int col = wg * (D / 2) + 32 * c;
+        uint32_t r[32];
+        if (nt > 0) {
+          tc_ld32(lane_addr + C::kColDq + col, r);
+          tc_wait_ld();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) r[e] = 0u;
+        }
+        if (in) store_row32<BF16>(p.dQ, off, col, p.g32, r, p.scale * Shift<BF16>::kSInv);
+      }
+    }
+  }
+
+  if (failed) report_timeout();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    __syncwarp();
+    tc_fence_after();
+    tc_dealloc(tmem, kTmemAll);
+  }
+}
+
+// ---------------------------------------------------------------- dK, dV
+
+template <int D>
+struct DkvCfg {
+  static constexpr int kAtoms = D / 64;
+  static constexpr bool kVTmem = D == 64;          // V an A operand in tensor memory too
+  static constexpr int kTile = kStep * D * 2;      // one Q or dO tile
+  static constexpr int kStage = 2 * kTile + 2 * kStep * 4;  // and the lse2, delta of its queries
+  static constexpr int kStagePitch = (kStage + 1023) / 1024 * 1024;
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kOffV = kStages * kStagePitch;
+  static constexpr int kOffBar = kOffV + (kVTmem ? 0 : kBlk * D * 2);
+  static constexpr int kFull = 0, kEmpty = kStages, kReady = 2 * kStages, kVFull = kReady + 1,
+                       kSFull = kVFull + 1, kPFull = kSFull + 2, kDpFull = kPFull + 2,
+                       kDsFull = kDpFull + 2, kDone = kDsFull + 2, kNumBars = kDone + 1;
+  static constexpr int kOffTmem = kOffBar + kNumBars * 8;
+  static constexpr int kSmem = kOffTmem + 16 + 1024;
+  static_assert(kSmem <= 232448 && kSmem > 118784, "one CTA per SM");
+  static constexpr uint32_t kColK = 0, kColV = D / 2, kColDv = 64, kColDk = 64 + D,
+                            kColSlot = 64 + 2 * D;
+  static_assert(64 + 2 * D + 3 * kStep <= 512, "tensor memory");
+};
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    swa_bwd_dkv_kernel(const SwaBwdProblem p, const __grid_constant__ CUtensorMap tmQ,
+                       const __grid_constant__ CUtensorMap tmDo,
+                       const __grid_constant__ CUtensorMap tmV) {
+  using C = DkvCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const gbase = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto bar = [&](int i) { return base + C::kOffBar + 8u * static_cast<uint32_t>(i); };
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(bar(C::kFull + s), 1);
+      mbar_init(bar(C::kEmpty + s), 1);
+    }
+    mbar_init(bar(C::kReady), 256);
+    mbar_init(bar(C::kVFull), 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(C::kSFull + s), 1);
+      mbar_init(bar(C::kPFull + s), 256);
+      mbar_init(bar(C::kDpFull + s), 1);
+      mbar_init(bar(C::kDsFull + s), 256);
+    }
+    mbar_init(bar(C::kDone), 1);
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tc_alloc(base + C::kOffTmem, kTmemAll);
+    tc_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + C::kOffTmem);
+
+  // the CTA's item: (b, KV head, key tile, part), and its steps, numbered
+  // head after head over the query steps that see the tile
+  uint32_t x = blockIdx.x;
+  const int sp = static_cast<int>(x % static_cast<uint32_t>(p.splits));
+  x /= static_cast<uint32_t>(p.splits);
+  const int kt = static_cast<int>(x % static_cast<uint32_t>(p.ktiles));
+  x /= static_cast<uint32_t>(p.ktiles);
+  const int g = static_cast<int>(x % static_cast<uint32_t>(p.Hkv));
+  const int b = static_cast<int>(x / static_cast<uint32_t>(p.Hkv));
+  const int j0 = kt * kBlk, j_last = min(j0 + kBlk, p.N) - 1;
+  const int ilo = max(0, j0 - p.right), ihi = min(p.M - 1, j_last + p.left);
+  const int u0 = ilo / kStep, nq = ihi >= ilo ? ihi / kStep - u0 + 1 : 0;
+  const int64_t all = static_cast<int64_t>(nq) * p.hpg;
+  const int64_t first = all * sp / p.splits;
+  const int nt = static_cast<int>(all * (sp + 1) / p.splits - first);
+  const int h_first = nq > 0 ? g * p.hpg + static_cast<int>(first / nq) : 0;
+  const int u_first = nq > 0 ? static_cast<int>(first % nq) : 0;
+  bool failed = false;
+
+  if (warp == 8) {
+    if (lane == 0 && nt > 0) {
+      // ---- TMA producer ----
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmDo);
+      const uint64_t keep = l2_policy_evict_last();
+      if (!C::kVTmem) {
+        mbar_arrive_expect_tx(bar(C::kVFull), kBlk * D * 2);
+        for (int a = 0; a < C::kAtoms; ++a)
+          for (int r = 0; r < 2; ++r)  // rows past N arrive as zeros
+            tma_load_4d(base + C::kOffV + a * kAtomBlk + r * kAtomStep, &tmV, bar(C::kVFull),
+                        a * 64, g, j0 + r * kStep, b, keep);
+      }
+      int h = h_first, u = u_first, n = 0;
+      for (; n < nt; ++n) {
+        const int s = n % C::kStages;
+        if (n >= C::kStages &&
+            !wait_phase(bar(C::kEmpty + s), (n / C::kStages - 1) & 1, kWaitLimitNs)) {
+          failed = true;
+          break;
+        }
+        const uint32_t full = bar(C::kFull + s), dst = base + s * C::kStagePitch;
+        const int i0 = (u0 + u) * kStep;
+        mbar_arrive_expect_tx(full, C::kStage);
+        for (int a = 0; a < C::kAtoms; ++a) {
+          tma_load_4d(dst + a * kAtomStep, &tmQ, full, a * 64, h, i0, b, keep);
+          tma_load_4d(dst + C::kTile + a * kAtomStep, &tmDo, full, a * 64, h, i0, b, keep);
+        }
+        const int64_t at = (static_cast<int64_t>(b) * p.H + h) * p.Mp + i0;
+        bulk_load(dst + 2 * C::kTile, p.lse2 + at, kStep * 4, full);
+        bulk_load(dst + 2 * C::kTile + kStep * 4, p.delta + at, kStep * 4, full);
+        if (++u == nq) {
+          u = 0;
+          ++h;
+        }
+      }
+      if (failed) {  // leave nothing in flight
+        for (int k = max(0, n - C::kStages); k < n; ++k)
+          wait_phase(bar(C::kFull + k % C::kStages), (k / C::kStages) & 1, kWaitLimitNs);
+        if (!C::kVTmem) wait_phase(bar(C::kVFull), 0, kWaitLimitNs);
+      }
+    }
+  } else if (warp == 9) {
+    if (lane == 0 && nt > 0) {
+      // ---- MMA issuer: S_0, dP_0, then S_{n+1}, dV_n, dP_{n+1}, dK_n ----
+      constexpr uint32_t id_s = umma_idesc_f16(kBlk, kStep, BF16, false);
+      constexpr uint32_t id_d = umma_idesc_f16(kBlk, D, BF16, true);
+      auto slot = [&](int k) { return tmem + C::kColSlot + static_cast<uint32_t>(k % 3) * kStep; };
+      auto stage = [&](int n) { return base + (n % C::kStages) * C::kStagePitch; };
+      auto issue_s = [&](int n) -> bool {
+        if (!wait_phase(bar(C::kFull + n % C::kStages), (n / C::kStages) & 1, kWaitLimitNs))
+          return false;
+        tc_fence_after();
+        const uint32_t qb = stage(n);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc_mma_ts(slot(2 * n), tmem + C::kColK + 8 * kk,
+                    umma_desc_sw128(qb + (kk >> 2) * kAtomStep + (kk & 3) * 32, 16), id_s,
+                    kk > 0 ? 1u : 0u);
+        tc_commit(bar(C::kSFull + (n & 1)));
+        return true;
+      };
+      auto issue_dp = [&](int n) {
+        const uint32_t ob = stage(n) + C::kTile;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t bd = umma_desc_sw128(ob + (kk >> 2) * kAtomStep + (kk & 3) * 32, 16);
+          if (C::kVTmem)
+            tc_mma_ts(slot(2 * n + 1), tmem + C::kColV + 8 * kk, bd, id_s, kk > 0 ? 1u : 0u);
+          else
+            tc_mma(slot(2 * n + 1),
+                   umma_desc_sw128(base + C::kOffV + (kk >> 2) * kAtomBlk + (kk & 3) * 32, 16), bd,
+                   id_s, kk > 0 ? 1u : 0u);
+        }
+        tc_commit(bar(C::kDpFull + (n & 1)));
+      };
+      // dst += A B over a step's 64 queries; A (P or dS) in `a`: queries
+      // 0..31 from column 0, 32..63 from column 32
+      auto issue_d = [&](uint32_t dst, uint32_t a, uint32_t b0, bool start) {
+#pragma unroll
+        for (int kk = 0; kk < kStep / 16; ++kk)
+          tc_mma_ts(dst, a + (kk >> 1) * 32 + (kk & 1) * 8, umma_desc_sw128(b0 + kk * 2048, kAtomStep),
+                    id_d, (!start || kk > 0) ? 1u : 0u);
+      };
+      bool ok = wait_phase(bar(C::kReady), 0, kWaitLimitNs) &&
+                (C::kVTmem || wait_phase(bar(C::kVFull), 0, kWaitLimitNs));
+      if (ok) ok = issue_s(0);
+      if (ok) issue_dp(0);
+      for (int n = 0; n < nt && ok; ++n) {
+        if (n + 1 < nt) ok = issue_s(n + 1);
+        if (!ok || !wait_phase(bar(C::kPFull + (n & 1)), (n >> 1) & 1, kWaitLimitNs)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        issue_d(tmem + C::kColDv, slot(2 * n), stage(n) + C::kTile, n == 0);
+        if (n + 1 < nt) issue_dp(n + 1);
+        if (!wait_phase(bar(C::kDsFull + (n & 1)), (n >> 1) & 1, kWaitLimitNs)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        issue_d(tmem + C::kColDk, slot(2 * n + 1), stage(n), n == 0);
+        tc_commit(bar(C::kEmpty + n % C::kStages));
+      }
+      tc_commit(bar(C::kDone));
+      failed = !wait_phase(bar(C::kDone), 0, kWaitLimitNs) || !ok;
+    }
+  } else {
+    // ---- elementwise: thread <-> (key row, half of a step's queries) ----
+    const int wg = warp >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane, j = j0 + row;
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    auto wait_all = [&](int i, uint32_t parity) {
+      return __all_sync(kFull, wait_phase(bar(i), parity, kWaitLimitNs));
+    };
+    const bool in = j < p.N;
+    const int64_t off = ((static_cast<int64_t>(b) * p.N + (in ? j : 0)) * p.Hkv + g) * D;
+    if (wg == 0) row_to_tmem<D>(lane_addr + C::kColK, in ? p.K + off : nullptr);
+    if (wg == 1 && C::kVTmem) row_to_tmem<D>(lane_addr + C::kColV, in ? p.V + off : nullptr);
+    tc_wait_st();
+    tc_fence_before();
+    mbar_arrive(bar(C::kReady));
+    const int lo_j = j - p.right, hi_j = min(j + p.left, p.M - 1);  // the queries that see key j
+    int u = u_first;
+    for (int n = 0; n < nt; ++n) {
+      const int i0 = (u0 + u) * kStep, ic = i0 + 32 * wg;
+      if (++u == nq) u = 0;
+      // (the second wait, long over by then, is for the lse2 and delta of the
+      // stage, which this warp reads itself)
+      if (!wait_all(C::kSFull + (n & 1), (n >> 1) & 1) ||
+          !wait_all(C::kFull + n % C::kStages, (n / C::kStages) & 1)) {
+        failed = true;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t sa = lane_addr + C::kColSlot + (2 * n) % 3 * kStep + 32 * wg;
+      const uint32_t da = lane_addr + C::kColSlot + (2 * n + 1) % 3 * kStep + 32 * wg;
+      const float4* l2 = reinterpret_cast<const float4*>(
+          gbase + (n % C::kStages) * C::kStagePitch + 2 * C::kTile + 32 * wg * 4);
+      const float4* dl = l2 + kStep / 4;
+      const bool edge =
+          j0 < i0 + kStep - 1 - p.left || j0 + kBlk - 1 > i0 + p.right || i0 + kStep > p.M;
+      uint32_t s[32];
+      float pr[32];
+      tc_ld32(sa, s);
+      tc_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float4 l = l2[c];
+        const float lv[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          pr[4 * c + e] = ex2(fmaf(__uint_as_float(s[4 * c + e]), p.sl2, -lv[e]));
+      }
+      if (edge) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (ic + c < lo_j || ic + c > hi_j) pr[c] = 0.f;
+      }
+      uint32_t w[16];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) w[c] = pack2_t<BF16>(pr[2 * c], pr[2 * c + 1]);
+      tc_st16(sa, w);
+      tc_wait_st();
+      tc_fence_before();
+      mbar_arrive(bar(C::kPFull + (n & 1)));
+      if (!wait_all(C::kDpFull + (n & 1), (n >> 1) & 1)) {
+        failed = true;
+        break;
+      }
+      tc_fence_after();
+      tc_ld32(da, s);
+      tc_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float4 d = dl[c];
+        const float dv[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          pr[4 * c + e] *= fmaf(__uint_as_float(s[4 * c + e]), Shift<BF16>::kSInv, -dv[e]);
+      }
+      if (edge) {  // again: 0 times an infinite dP of a hidden pair is not 0
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (ic + c < lo_j || ic + c > hi_j) pr[c] = 0.f;
+      }
+#pragma unroll
+      for (int c = 0; c < 16; ++c) w[c] = pack2_t<BF16>(pr[2 * c], pr[2 * c + 1]);
+      tc_st16(da, w);
+      tc_wait_st();
+      tc_fence_before();
+      mbar_arrive(bar(C::kDsFull + (n & 1)));
+    }
+    if (!failed && nt > 0 && !wait_all(C::kDone, 0)) failed = true;
+    if (!failed) {
+      tc_fence_after();
+      // warpgroup 0 stores dV, 1 dK
+      const float f = wg == 0 ? Shift<BF16>::kPInv : p.scale * Shift<BF16>::kSInv;
+      void* dst = wg == 0 ? p.dV : p.dK;
+      bool f32 = p.g32;
+      if (p.part != nullptr) {
+        const int64_t n = static_cast<int64_t>(p.B) * p.N * p.Hkv * D;
+        dst = p.part + (2 * sp + (wg == 0 ? 1 : 0)) * n;
+        f32 = true;
+      }
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t r[32];
+        if (nt > 0) {
+          tc_ld32(lane_addr + (wg == 0 ? C::kColDv : C::kColDk) + 32 * c, r);
+          tc_wait_ld();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) r[e] = 0u;
+        }
+        if (in) store_row32<BF16>(dst, off, 32 * c, f32, r, f);
+      }
+    }
+  }
+
+  if (failed) report_timeout();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    __syncwarp();
+    tc_fence_after();
+    tc_dealloc(tmem, kTmemAll);
+  }
+}
+
+// dK and dV from the parts, added in order; 8 entries a thread.
+template <bool BF16>
+__global__ void __launch_bounds__(256)
+    swa_bwd_join_kernel(const float* part, int splits, int64_t n, void* dK, void* dV, bool g32) {
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
+  if (i >= n) return;
+  const int which = blockIdx.y;  // 0 dK, 1 dV
+  float f[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = 0.f;
+  for (int s = 0; s < splits; ++s) {
+    const float4* src = reinterpret_cast<const float4*>(part + (2 * s + which) * n + i);
+    const float4 a = src[0], c = src[1];
+    f[0] += a.x, f[1] += a.y, f[2] += a.z, f[3] += a.w;
+    f[4] += c.x, f[5] += c.y, f[6] += c.z, f[7] += c.w;
+  }
+  void* dst = which == 0 ? dK : dV;
+  if (g32) {
+    float4* o = reinterpret_cast<float4*>(static_cast<float*>(dst) + i);
+    o[0] = make_float4(f[0], f[1], f[2], f[3]);
+    o[1] = make_float4(f[4], f[5], f[6], f[7]);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + i) =
+        make_uint4(pack2_t<BF16>(f[0], f[1]), pack2_t<BF16>(f[2], f[3]), pack2_t<BF16>(f[4], f[5]),
+                   pack2_t<BF16>(f[6], f[7]));
+  }
+}
+
+// ---------------------------------------------------------------- host
+
+constexpr int kSms = 152;
+
+int check_swa_bwd(int64_t B, int64_t M, int64_t N, int64_t H, int64_t H_kv, int64_t D) {
+  if (B < 0 || M < 0 || N < 0 || H <= 0 || H_kv <= 0) return NSA_ERR_SHAPE;
+  if (H % H_kv != 0) return NSA_ERR_GROUPS;
+  if (D != 64 && D != 128) return NSA_ERR_HEAD_DIM;
+  const int64_t lim = int64_t(1) << 29;
+  if (M > lim || N > lim || H > 65536 || B > 65536) return NSA_ERR_SHAPE;
+  const int64_t top = (int64_t(1) << 31) - 1;
+  if (B * H * ((M + kBlk - 1) / kBlk) > top || B * H * ((N + kBlk - 1) / kBlk) > top)
+    return NSA_ERR_SHAPE;
+  return NSA_OK;
+}
+
+// Parts of the dK, dV steps of a key tile: as many as give every SM an item,
+// with at least 4 steps to each of them.
+int swa_bwd_splits(int64_t B, int64_t M, int64_t N, int64_t H, int64_t H_kv, int64_t left,
+                   int64_t right) {
+  const int64_t items = B * H_kv * ((N + kBlk - 1) / kBlk);
+  if (items == 0 || items >= kSms) return 1;
+  int64_t rows = left + right + kBlk;  // queries that see a key tile
+  if (rows > M) rows = M;
+  const int64_t steps = (rows + kStep - 1) / kStep * (H / H_kv);
+  int64_t s = (kSms + items - 1) / items;
+  if (s > steps / 4) s = steps / 4;
+  return static_cast<int>(s < 1 ? 1 : s);
+}
+
+struct WindowSides {
+  int64_t left, right;
+};
+
+WindowSides clamp_window(int64_t M, int64_t N, int64_t left, int64_t right) {
+  return {left < 0 || left > M ? M : left, right < 0 || right > N ? N : right};
+}
+
+template <int D, bool BF16>
+int launch_swa_bwd(const SwaBwdProblem& p, cudaStream_t st) {
+  constexpr CUtensorMapDataType dt =
+      BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  CUtensorMap tk, tv, tq, td;
+  if (!encode_kv_map(&tk, p.K, p.B, p.N, p.Hkv, D, kStep, dt) ||
+      !encode_kv_map(&tv, p.V, p.B, p.N, p.Hkv, D, kStep, dt) ||
+      !encode_kv_map(&tq, p.Q, p.B, p.M, p.H, D, kStep, dt) ||
+      !encode_kv_map(&td, p.dO, p.B, p.M, p.H, D, kStep, dt))
+    return NSA_ERR_LAUNCH;
+  auto dq = swa_bwd_dq_kernel<D, BF16>;
+  auto dkv = swa_bwd_dkv_kernel<D, BF16>;
+  if (cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, DqCfg<D>::kSmem) !=
+          cudaSuccess ||
+      cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, DkvCfg<D>::kSmem) !=
+          cudaSuccess)
+    return NSA_ERR_LAUNCH;
+  const int64_t qi = static_cast<int64_t>(p.B) * p.H * p.qtiles;
+  const int64_t ki = static_cast<int64_t>(p.B) * p.Hkv * p.ktiles * p.splits;
+  dq<<<static_cast<unsigned>(qi), kThreads, DqCfg<D>::kSmem, st>>>(p, tk, tv);
+  if (cudaGetLastError() != cudaSuccess) return NSA_ERR_LAUNCH;
+  dkv<<<static_cast<unsigned>(ki), kThreads, DkvCfg<D>::kSmem, st>>>(p, tq, td, tv);
+  if (cudaGetLastError() != cudaSuccess) return NSA_ERR_LAUNCH;
+  if (p.part != nullptr) {
+    const int64_t n = static_cast<int64_t>(p.B) * p.N * p.Hkv * D;
+    const dim3 grid(static_cast<unsigned>((n / 8 + 255) / 256), 2);
+    swa_bwd_join_kernel<BF16><<<grid, 256, 0, st>>>(p.part, p.splits, n, p.dK, p.dV, p.g32);
+    if (cudaGetLastError() != cudaSuccess) return NSA_ERR_LAUNCH;
+  }
+  return NSA_OK;
+}
+
+}  // namespace
+
+int swa_bwd_read_and_clear_status(unsigned int* value) { return read_and_clear_status(value); }
+
+}  // namespace nsa
+
+extern "C" int64_t nsa_swa_bwd_workspace_bytes(int64_t B, int64_t M, int64_t N, int64_t H,
+                                               int64_t H_kv, int64_t D, int64_t window_left,
+                                               int64_t window_right) {
+  using namespace nsa;
+  const int rc = check_swa_bwd(B, M, N, H, H_kv, D);
+  if (rc != NSA_OK) return rc;
+  if (B == 0 || M == 0 || N == 0) return 0;
+  const WindowSides w = clamp_window(M, N, window_left, window_right);
+  const int64_t Mp = (M + kStep - 1) / kStep * kStep;
+  const int splits = swa_bwd_splits(B, M, N, H, H_kv, w.left, w.right);
+  return 2 * B * H * Mp * 4 + (splits > 1 ? splits * 2 * B * N * H_kv * D * 4 : 0);
+}
+
+extern "C" int nsa_swa_bwd(const void* Q, const void* K, const void* V, const void* O,
+                           const float* LSE, const void* dO, void* dQ, void* dK, void* dV,
+                           int64_t B, int64_t M, int64_t N, int64_t H, int64_t H_kv, int64_t D,
+                           int64_t window_left, int64_t window_right, float scale, int dtype,
+                           int grad_dtype, void* workspace, int64_t workspace_bytes,
+                           void* stream) {
+  using namespace nsa;
+  const int rc = check_swa_bwd(B, M, N, H, H_kv, D);
+  if (rc != NSA_OK) return rc;
+  if (dtype != NSA_F16 && dtype != NSA_BF16) return NSA_ERR_DTYPE;
+  if (grad_dtype != NSA_F32 && grad_dtype != dtype) return NSA_ERR_DTYPE;
+  auto mis = [](const void* ptr, uintptr_t a) {
+    return ptr != nullptr && (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) != 0;
+  };
+  const bool queries = B > 0 && M > 0, keys = B > 0 && N > 0;
+  if (queries && (!Q || !O || !LSE || !dO || !dQ)) return NSA_ERR_NULL;
+  if (keys && (!K || !V || !dK || !dV)) return NSA_ERR_NULL;
+  if (mis(Q, 16) || mis(K, 16) || mis(V, 16) || mis(O, 16) || mis(dO, 16) || mis(dQ, 16) ||
+      mis(dK, 16) || mis(dV, 16) || mis(LSE, 4))
+    return NSA_ERR_ALIGN;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int64_t ge = grad_dtype == NSA_F32 ? 4 : 2;
+  if (!queries || !keys) {  // nothing is visible: zero gradients
+    if (queries && cudaMemsetAsync(dQ, 0, B * M * H * D * ge, st) != cudaSuccess)
+      return NSA_ERR_LAUNCH;
+    if (keys && (cudaMemsetAsync(dK, 0, B * N * H_kv * D * ge, st) != cudaSuccess ||
+                 cudaMemsetAsync(dV, 0, B * N * H_kv * D * ge, st) != cudaSuccess))
+      return NSA_ERR_LAUNCH;
+    return NSA_OK;
+  }
+  if (!workspace || workspace_bytes < nsa_swa_bwd_workspace_bytes(B, M, N, H, H_kv, D, window_left,
+                                                                  window_right))
+    return NSA_ERR_WORKSPACE;
+  if (mis(workspace, 16)) return NSA_ERR_ALIGN;
+  const WindowSides w = clamp_window(M, N, window_left, window_right);
+  SwaBwdProblem p{};
+  p.Q = static_cast<const uint16_t*>(Q);
+  p.K = static_cast<const uint16_t*>(K);
+  p.V = static_cast<const uint16_t*>(V);
+  p.O = static_cast<const uint16_t*>(O);
+  p.dO = static_cast<const uint16_t*>(dO);
+  p.LSE = LSE;
+  p.dQ = dQ;
+  p.dK = dK;
+  p.dV = dV;
+  p.B = static_cast<int>(B);
+  p.M = static_cast<int>(M);
+  p.N = static_cast<int>(N);
+  p.H = static_cast<int>(H);
+  p.Hkv = static_cast<int>(H_kv);
+  p.hpg = static_cast<int>(H / H_kv);
+  p.Mp = static_cast<int>((M + kStep - 1) / kStep * kStep);
+  p.qtiles = static_cast<int>((M + kBlk - 1) / kBlk);
+  p.ktiles = static_cast<int>((N + kBlk - 1) / kBlk);
+  p.splits = swa_bwd_splits(B, M, N, H, H_kv, w.left, w.right);
+  p.left = static_cast<int>(w.left);
+  p.right = static_cast<int>(w.right);
+  p.scale = scale > 0.f ? scale : 1.0f / sqrtf(static_cast<float>(D));
+  p.sl2 = p.scale * 1.4426950408889634f;
+  p.g32 = grad_dtype == NSA_F32;
+  const int64_t stat = B * H * p.Mp;
+  p.lse2 = static_cast<float*>(workspace);
+  p.delta = p.lse2 + stat;
+  p.part = p.splits > 1 ? p.delta + stat : nullptr;
+  const bool bf = dtype == NSA_BF16;
+  if (D == 64) return bf ? launch_swa_bwd<64, true>(p, st) : launch_swa_bwd<64, false>(p, st);
+  return bf ? launch_swa_bwd<128, true>(p, st) : launch_swa_bwd<128, false>(p, st);
+}

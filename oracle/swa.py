@@ -37,7 +37,7 @@ from typing import Iterable, Optional, Tuple
 
 import numpy as np
 
-__all__ = ["window_keys", "swa_row", "swa_rows", "swa_fwd"]
+__all__ = ["window_keys", "swa_row", "swa_rows", "swa_fwd", "swa_bwd"]
 
 
 def window_keys(i: int, N: int, left: int, right: int) -> np.ndarray:
@@ -98,3 +98,53 @@ def swa_fwd(Q, K, V, left: int, right: int, scale: Optional[float] = None):
                 O[b, i, g * hpg:(g + 1) * hpg] = o
                 L[b, g * hpg:(g + 1) * hpg, i] = lse
     return O, L
+
+
+def swa_bwd(Q, K, V, O, LSE, dO, left: int, right: int, scale: Optional[float] = None,
+            magnitudes: bool = False):
+    """Gradients (dQ, dK, dV), float64, from the forward's O and LSE as given.
+
+    p = exp(scale q.k - LSE), delta = dO.O, dS = p (dO.v - delta),
+    dQ = scale sum_j dS k_j, dK_j = scale sum_i dS q_i, dV_j = sum_i p dO_i,
+    over the visible pairs and the query heads of each KV head. A row with
+    LSE = -inf has no pair.
+
+    magnitudes: instead, for each gradient a tuple of sums of positive
+    terms that rounding errors are measured against: (sum |dS| |k|, sum
+    p (|dO|.|v| + |dO|.|O|) |k|, scaled) for dQ, the same with |q| for dK, and
+    (sum p |dO|,) for dV.
+    """
+    Q, K, V, O, dO = (np.asarray(x, np.float64) for x in (Q, K, V, O, dO))
+    B, M, H, D = Q.shape
+    N, Hkv = K.shape[1], K.shape[2]
+    hpg = H // Hkv
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    see = np.zeros((M, N), bool)
+    for i in range(M):
+        see[i, window_keys(i, N, left, right)] = True
+    n = 2 if magnitudes else 1
+    dQ = [np.zeros((B, M, H, D)) for _ in range(n)]
+    dK = [np.zeros((B, N, Hkv, D)) for _ in range(n)]
+    dV = np.zeros((B, N, Hkv, D))
+    for b in range(B):
+        for h in range(H):
+            g = h // hpg
+            q, k, v, o, do = Q[b, :, h], K[b, :, g], V[b, :, g], O[b, :, h], dO[b, :, h]
+            lse = np.asarray(LSE[b, h], np.float64)[:, None]
+            live = see & ~np.isneginf(lse)
+            p = np.where(live, np.exp(np.where(live, scale * (q @ k.T) - lse, 0.0)), 0.0)
+            ds = p * (do @ v.T - np.sum(do * o, 1)[:, None])
+            if magnitudes:
+                terms = [np.abs(ds), p * (np.abs(do) @ np.abs(v).T
+                                          + np.sum(np.abs(do * o), 1)[:, None])]
+                q, k, do = np.abs(q), np.abs(k), np.abs(do)
+            else:
+                terms = [ds]
+            for t, x, y in zip(terms, dQ, dK):
+                x[b, :, h] = scale * (t @ k)
+                y[b, :, g] += scale * (t.T @ q)
+            dV[b, :, g] += p.T @ do
+    if magnitudes:
+        return tuple(dQ), tuple(dK), (dV,)
+    return dQ[0], dK[0], dV
