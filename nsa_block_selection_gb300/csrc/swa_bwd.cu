@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(C::kReady), 256);
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(C::kSFull + s), 1);
-      mbar_init(bar(C::kDsFull + s), 256);
+      mbar_init(bar(C::kDsFull + s), 8);
     }
     mbar_init(bar(C::kDone), 1);
     fence_mbar_init();
@@ -239,46 +239,57 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait_phase(bar(C::kFull + k % C::kStages), (k / C::kStages) & 1, kWaitLimitNs);
     }
   } else if (warp == 9) {
-    if (lane == 0 && nt > 0) {
-      // ---- MMA issuer: S_i, dP_i, dQ_{i-1} ----
+    if (nt > 0) {
+      // ---- MMA issuer (the whole warp, one lane elected): S_i, dP_i, dQ_{i-1} ----
       constexpr uint32_t id_s = umma_idesc_f16(kBlk, kStep, BF16, false);
       constexpr uint32_t id_q = umma_idesc_f16(kBlk, D, BF16, true);
-      auto issue_dq = [&](int i) -> bool {
-        if (!wait_phase(bar(C::kDsFull + (i & 1)), (i >> 1) & 1, kWaitLimitNs)) return false;
+      const uint32_t on = elect_one();
+      auto wait_all = [&](int i, uint32_t parity) {
+        return __all_sync(kFull, wait_phase(bar(i), parity, kWaitLimitNs));
+      };
+      auto issue_dq = [&](int i, int s) -> bool {
+        if (!wait_all(C::kDsFull + (i & 1), (i >> 1) & 1)) return false;
         tc_fence_after();
         const uint32_t ds = tmem + C::kColS + (i & 1) * kStep;
-        const uint32_t kb = base + (i % C::kStages) * 2 * C::kTile;
+        const uint32_t kb = base + s * 2 * C::kTile;
 #pragma unroll
         for (int kk = 0; kk < kStep / 16; ++kk)  // dS of keys 0..31 at column 0, 32..63 at 32
-          tc_mma_ts(tmem + C::kColDq, ds + (kk >> 1) * 32 + (kk & 1) * 8,
-                    umma_desc_sw128(kb + kk * 2048, kAtomStep), id_q, (i > 0 || kk > 0) ? 1u : 0u);
-        tc_commit(bar(C::kEmpty + i % C::kStages));
+          tc_mma_ts_if(on, tmem + C::kColDq, ds + (kk >> 1) * 32 + (kk & 1) * 8,
+                       umma_desc_sw128(kb + kk * 2048, kAtomStep), id_q,
+                       (i > 0 || kk > 0) ? 1u : 0u);
+        tc_commit_if(on, bar(C::kEmpty + s));
         return true;
       };
-      bool ok = wait_phase(bar(C::kReady), 0, kWaitLimitNs);
+      bool ok = wait_all(C::kReady, 0);
+      int s = 0, s_prev = 0;
+      uint32_t ph = 0;
       for (int i = 0; i < nt && ok; ++i) {
-        const int s = i % C::kStages;
-        ok = wait_phase(bar(C::kFull + s), (i / C::kStages) & 1, kWaitLimitNs);
+        ok = wait_all(C::kFull + s, ph);
         if (!ok) break;
         tc_fence_after();
         const uint32_t kb = base + s * 2 * C::kTile, vb = kb + C::kTile;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          tc_mma_ts(tmem + C::kColS + (i & 1) * kStep, tmem + C::kColQ + 8 * kk,
-                    umma_desc_sw128(kb + (kk >> 2) * kAtomStep + (kk & 3) * 32, 16), id_s,
-                    kk > 0 ? 1u : 0u);
+          tc_mma_ts_if(on, tmem + C::kColS + (i & 1) * kStep, tmem + C::kColQ + 8 * kk,
+                       umma_desc_sw128(kb + (kk >> 2) * kAtomStep + (kk & 3) * 32, 16), id_s,
+                       kk > 0 ? 1u : 0u);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          tc_mma_ts(tmem + C::kColP + (i & 1) * kStep, tmem + C::kColDo + 8 * kk,
-                    umma_desc_sw128(vb + (kk >> 2) * kAtomStep + (kk & 3) * 32, 16), id_s,
-                    kk > 0 ? 1u : 0u);
-        tc_commit(bar(C::kSFull + (i & 1)));
-        if (i > 0) ok = issue_dq(i - 1);
+          tc_mma_ts_if(on, tmem + C::kColP + (i & 1) * kStep, tmem + C::kColDo + 8 * kk,
+                       umma_desc_sw128(vb + (kk >> 2) * kAtomStep + (kk & 3) * 32, 16), id_s,
+                       kk > 0 ? 1u : 0u);
+        tc_commit_if(on, bar(C::kSFull + (i & 1)));
+        if (i > 0) ok = issue_dq(i - 1, s_prev);
+        s_prev = s;
+        if (++s == C::kStages) {
+          s = 0;
+          ph ^= 1;
+        }
       }
-      if (ok) ok = issue_dq(nt - 1);
+      if (ok) ok = issue_dq(nt - 1, s_prev);
       // also after a failed wait: nothing is left in flight at the teardown
-      tc_commit(bar(C::kDone));
-      failed = !wait_phase(bar(C::kDone), 0, kWaitLimitNs) || !ok;
+      tc_commit_if(on, bar(C::kDone));
+      failed = !wait_all(C::kDone, 0) || !ok;
     }
   } else {
     // ---- elementwise: thread <-> (query row, half of a step's columns) ----
@@ -364,7 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_st16(sa, w);
       tc_wait_st();
       tc_fence_before();
-      mbar_arrive(bar(C::kDsFull + (i & 1)));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::kDsFull + (i & 1)));
     }
     if (!failed) {
       if (nt > 0 && !wait_all(C::kDone, 0)) failed = true;
@@ -441,9 +453,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(C::kVFull), 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(C::kSFull + s), 1);
-      mbar_init(bar(C::kPFull + s), 256);
+      mbar_init(bar(C::kPFull + s), 8);
       mbar_init(bar(C::kDpFull + s), 1);
-      mbar_init(bar(C::kDsFull + s), 256);
+      mbar_init(bar(C::kDsFull + s), 8);
     }
     mbar_init(bar(C::kDone), 1);
     fence_mbar_init();
@@ -519,70 +531,82 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 9) {
-    if (lane == 0 && nt > 0) {
-      // ---- MMA issuer: S_0, dP_0, then S_{n+1}, dV_n, dP_{n+1}, dK_n ----
+    if (nt > 0) {
+      // ---- MMA issuer (the whole warp, one lane elected): S_0, dP_0, then
+      // S_{n+1}, dV_n, dP_{n+1}, dK_n ----
       constexpr uint32_t id_s = umma_idesc_f16(kBlk, kStep, BF16, false);
       constexpr uint32_t id_d = umma_idesc_f16(kBlk, D, BF16, true);
-      auto slot = [&](int k) { return tmem + C::kColSlot + static_cast<uint32_t>(k % 3) * kStep; };
-      auto stage = [&](int n) { return base + (n % C::kStages) * C::kStagePitch; };
-      auto issue_s = [&](int n) -> bool {
-        if (!wait_phase(bar(C::kFull + n % C::kStages), (n / C::kStages) & 1, kWaitLimitNs))
-          return false;
+      const uint32_t on = elect_one();
+      auto wait_all = [&](int i, uint32_t parity) {
+        return __all_sync(kFull, wait_phase(bar(i), parity, kWaitLimitNs));
+      };
+      auto issue_s = [&](int n, uint32_t slot, int st, uint32_t ph) -> bool {
+        if (!wait_all(C::kFull + st, ph)) return false;
         tc_fence_after();
-        const uint32_t qb = stage(n);
+        const uint32_t qb = base + st * C::kStagePitch;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          tc_mma_ts(slot(2 * n), tmem + C::kColK + 8 * kk,
-                    umma_desc_sw128(qb + (kk >> 2) * kAtomStep + (kk & 3) * 32, 16), id_s,
-                    kk > 0 ? 1u : 0u);
-        tc_commit(bar(C::kSFull + (n & 1)));
+          tc_mma_ts_if(on, slot, tmem + C::kColK + 8 * kk,
+                       umma_desc_sw128(qb + (kk >> 2) * kAtomStep + (kk & 3) * 32, 16), id_s,
+                       kk > 0 ? 1u : 0u);
+        tc_commit_if(on, bar(C::kSFull + (n & 1)));
         return true;
       };
-      auto issue_dp = [&](int n) {
-        const uint32_t ob = stage(n) + C::kTile;
+      auto issue_dp = [&](int n, uint32_t slot, int st) {
+        const uint32_t ob = base + st * C::kStagePitch + C::kTile;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t bd = umma_desc_sw128(ob + (kk >> 2) * kAtomStep + (kk & 3) * 32, 16);
           if (C::kVTmem)
-            tc_mma_ts(slot(2 * n + 1), tmem + C::kColV + 8 * kk, bd, id_s, kk > 0 ? 1u : 0u);
+            tc_mma_ts_if(on, slot, tmem + C::kColV + 8 * kk, bd, id_s, kk > 0 ? 1u : 0u);
           else
-            tc_mma(slot(2 * n + 1),
-                   umma_desc_sw128(base + C::kOffV + (kk >> 2) * kAtomBlk + (kk & 3) * 32, 16), bd,
-                   id_s, kk > 0 ? 1u : 0u);
+            tc_mma_if(on, slot,
+                      umma_desc_sw128(base + C::kOffV + (kk >> 2) * kAtomBlk + (kk & 3) * 32, 16),
+                      bd, id_s, kk > 0 ? 1u : 0u);
         }
-        tc_commit(bar(C::kDpFull + (n & 1)));
+        tc_commit_if(on, bar(C::kDpFull + (n & 1)));
       };
       // dst += A B over a step's 64 queries; A (P or dS) in `a`: queries
       // 0..31 from column 0, 32..63 from column 32
       auto issue_d = [&](uint32_t dst, uint32_t a, uint32_t b0, bool start) {
 #pragma unroll
         for (int kk = 0; kk < kStep / 16; ++kk)
-          tc_mma_ts(dst, a + (kk >> 1) * 32 + (kk & 1) * 8, umma_desc_sw128(b0 + kk * 2048, kAtomStep),
-                    id_d, (!start || kk > 0) ? 1u : 0u);
+          tc_mma_ts_if(on, dst, a + (kk >> 1) * 32 + (kk & 1) * 8,
+                       umma_desc_sw128(b0 + kk * 2048, kAtomStep), id_d, (!start || kk > 0) ? 1u : 0u);
       };
-      bool ok = wait_phase(bar(C::kReady), 0, kWaitLimitNs) &&
-                (C::kVTmem || wait_phase(bar(C::kVFull), 0, kWaitLimitNs));
-      if (ok) ok = issue_s(0);
-      if (ok) issue_dp(0);
+      // slots of S_n (a), dP_n (c) and S_{n+1} (e); dP_{n+1} takes a
+      uint32_t a = tmem + C::kColSlot, c = a + kStep, e = c + kStep;
+      int st = 0;       // stage of step n
+      uint32_t ph = 0;  // phase of the stage of step n + 1
+      bool ok = wait_all(C::kReady, 0) && (C::kVTmem || wait_all(C::kVFull, 0));
+      if (ok) ok = issue_s(0, a, 0, 0);
+      if (ok) issue_dp(0, c, 0);
       for (int n = 0; n < nt && ok; ++n) {
-        if (n + 1 < nt) ok = issue_s(n + 1);
-        if (!ok || !wait_phase(bar(C::kPFull + (n & 1)), (n >> 1) & 1, kWaitLimitNs)) {
-          ok = false;
-          break;
+        int next = st + 1;
+        if (next == C::kStages) {
+          next = 0;
+          ph ^= 1;
         }
+        if (n + 1 < nt) ok = issue_s(n + 1, e, next, ph);
+        if (ok) ok = wait_all(C::kPFull + (n & 1), (n >> 1) & 1);
+        if (!ok) break;
         tc_fence_after();
-        issue_d(tmem + C::kColDv, slot(2 * n), stage(n) + C::kTile, n == 0);
-        if (n + 1 < nt) issue_dp(n + 1);
-        if (!wait_phase(bar(C::kDsFull + (n & 1)), (n >> 1) & 1, kWaitLimitNs)) {
-          ok = false;
-          break;
-        }
+        const uint32_t qb = base + st * C::kStagePitch;
+        issue_d(tmem + C::kColDv, a, qb + C::kTile, n == 0);
+        if (n + 1 < nt) issue_dp(n + 1, a, next);
+        ok = wait_all(C::kDsFull + (n & 1), (n >> 1) & 1);
+        if (!ok) break;
         tc_fence_after();
-        issue_d(tmem + C::kColDk, slot(2 * n + 1), stage(n), n == 0);
-        tc_commit(bar(C::kEmpty + n % C::kStages));
+        issue_d(tmem + C::kColDk, c, qb, n == 0);
+        tc_commit_if(on, bar(C::kEmpty + st));
+        st = next;
+        const uint32_t t = a;  // step n + 1: S in e, dP in a, and c is free
+        a = e;
+        e = c;
+        c = t;
       }
-      tc_commit(bar(C::kDone));
-      failed = !wait_phase(bar(C::kDone), 0, kWaitLimitNs) || !ok;
+      tc_commit_if(on, bar(C::kDone));
+      failed = !wait_all(C::kDone, 0) || !ok;
     }
   } else {
     // ---- elementwise: thread <-> (key row, half of a step's queries) ----
@@ -642,7 +666,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_st16(sa, w);
       tc_wait_st();
       tc_fence_before();
-      mbar_arrive(bar(C::kPFull + (n & 1)));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::kPFull + (n & 1)));
       if (!wait_all(C::kDpFull + (n & 1), (n >> 1) & 1)) {
         failed = true;
         break;
@@ -668,7 +693,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_st16(da, w);
       tc_wait_st();
       tc_fence_before();
-      mbar_arrive(bar(C::kDsFull + (n & 1)));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::kDsFull + (n & 1)));
     }
     if (!failed && nt > 0 && !wait_all(C::kDone, 0)) failed = true;
     if (!failed) {
