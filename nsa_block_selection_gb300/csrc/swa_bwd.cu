@@ -58,7 +58,6 @@ constexpr int kBlk = 128;       // queries (dQ) or keys (dK, dV) of a CTA: the M
 constexpr int kStep = 64;       // keys (dQ) or queries (dK, dV) of a step
 constexpr int kThreads = 320;   // 8 elementwise warps, the TMA warp, the MMA warp
 constexpr int kAtomStep = kStep * 128;  // bytes of 64 rows x 64 entries
-constexpr int kAtomBlk = kBlk * 128;
 constexpr uint32_t kTmemAll = 512;
 
 // fp16 has no exponents below 2^-14 at full precision, and over thousands of
@@ -77,8 +76,8 @@ struct SwaBwdProblem {
   const uint16_t *Q, *K, *V, *O, *dO;
   const float* LSE;
   void *dQ, *dK, *dV;
-  float* lse2;   // [B, H, Mp]: LSE log2 e less Shift::kP; +inf for rows without keys
-  float* delta;  // [B, H, Mp]: delta 2^(kS - kP)
+  float* nlse2;   // [B, H, Mp]: Shift::kP - LSE log2 e; -inf for rows without keys
+  float* ndelta;  // [B, H, Mp]: -delta 2^(kS - kP)
   float* part;   // [splits, 2, B, N, Hkv, D], or NULL
   int B, M, N, H, Hkv, hpg, Mp, qtiles, ktiles, splits;
   int left, right;  // clamped to [0, M] and [0, N]: unbounded in effect
@@ -88,6 +87,41 @@ struct SwaBwdProblem {
 
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Two fp32 operations an instruction.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  return pair(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  uint32_t lo, hi;
+  asm("mov.b64 {%0, %1}, %2;\n" : "=r"(lo), "=r"(hi) : "l"(v));
+  return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 2^x of both halves.
+__device__ __forceinline__ uint64_t ex2_2(uint64_t x) {
+  const float2 v = unpair(x);
+  return pair(ex2(v.x), ex2(v.y));
 }
 
 template <bool BF16>
@@ -336,8 +370,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       stat[kBlk + row] = dl;
       if (iq < p.Mp) {
         const int64_t at = (static_cast<int64_t>(b) * p.H + h) * p.Mp + iq;
-        p.lse2[at] = l2 - Shift<BF16>::kP;
-        p.delta[at] = dl * Shift<BF16>::kSInv;
+        p.nlse2[at] = Shift<BF16>::kP - l2;
+        p.ndelta[at] = -dl * Shift<BF16>::kSInv;
       }
     }
     tc_wait_st();
@@ -345,6 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_arrive(bar(C::kReady));
     bar_sync(1, 256);
     const float neg = -(stat[row] - Shift<BF16>::kS), dl = stat[kBlk + row];
+    const uint64_t sl2_2 = pair(p.sl2, p.sl2), neg_2 = pair(neg, neg), ndl_2 = pair(-dl, -dl);
     const int lo_i = max(0, iq - p.left), hi_i = min(p.N - 1, iq + p.right);
     const int in_lo = max(0, q_last - p.left), in_hi = min(p.N - 1, q0 + p.right);
     for (int i = 0; i < nt; ++i) {
@@ -359,19 +394,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_ld32(lane_addr + C::kColP + (i & 1) * kStep + 32 * wg, d);
       tc_wait_ld();
       const int j0 = (t0 + i) * kStep;
-      float v[32];
+      uint64_t v[16];
 #pragma unroll
-      for (int c = 0; c < 32; ++c)
-        v[c] = ex2(fmaf(__uint_as_float(s[c]), p.sl2, neg)) * (__uint_as_float(d[c]) - dl);
+      for (int c = 0; c < 16; ++c)
+        v[c] = mul2(ex2_2(fma2(pair(s[2 * c], s[2 * c + 1]), sl2_2, neg_2)),
+                    add2(pair(d[2 * c], d[2 * c + 1]), ndl_2));
       if (j0 < in_lo || j0 + kStep - 1 > in_hi) {  // the same for the whole CTA
         const int jc = j0 + 32 * wg;
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
-          if (jc + c < lo_i || jc + c > hi_i) v[c] = 0.f;
+        for (int c = 0; c < 16; ++c) {
+          float2 f = unpair(v[c]);
+          if (jc + 2 * c < lo_i || jc + 2 * c > hi_i) f.x = 0.f;
+          if (jc + 2 * c + 1 < lo_i || jc + 2 * c + 1 > hi_i) f.y = 0.f;
+          v[c] = pair(f.x, f.y);
+        }
       }
       uint32_t w[16];
 #pragma unroll
-      for (int c = 0; c < 16; ++c) w[c] = pack2_t<BF16>(v[2 * c], v[2 * c + 1]);
+      for (int c = 0; c < 16; ++c) {
+        const float2 f = unpair(v[c]);
+        w[c] = pack2_t<BF16>(f.x, f.y);
+      }
       tc_st16(sa, w);
       tc_wait_st();
       tc_fence_before();
@@ -414,29 +457,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D>
 struct DkvCfg {
   static constexpr int kAtoms = D / 64;
-  static constexpr bool kVTmem = D == 64;          // V an A operand in tensor memory too
   static constexpr int kTile = kStep * D * 2;      // one Q or dO tile
-  static constexpr int kStage = 2 * kTile + 2 * kStep * 4;  // and the lse2, delta of its queries
+  static constexpr int kStage = 2 * kTile + 2 * kStep * 4;  // and the nlse2, ndelta of its queries
   static constexpr int kStagePitch = (kStage + 1023) / 1024 * 1024;
-  static constexpr int kStages = D == 128 ? 5 : 8;
-  static constexpr int kOffV = kStages * kStagePitch;
-  static constexpr int kOffBar = kOffV + (kVTmem ? 0 : kBlk * D * 2);
-  static constexpr int kFull = 0, kEmpty = kStages, kReady = 2 * kStages, kVFull = kReady + 1,
-                       kSFull = kVFull + 1, kPFull = kSFull + 2, kDpFull = kPFull + 2,
-                       kDsFull = kDpFull + 2, kDone = kDsFull + 2, kNumBars = kDone + 1;
+  static constexpr int kStages = D == 128 ? 6 : 8;
+  static constexpr int kBuf = D == 128 ? 1 : 2;  // buffers of S and of dP
+  static constexpr int kOffBar = kStages * kStagePitch;
+  static constexpr int kFull = 0, kEmpty = kStages, kReady = 2 * kStages, kSFull = kReady + 1,
+                       kPFull = kSFull + 2, kDpFull = kPFull + 2, kDsFull = kDpFull + 2,
+                       kDone = kDsFull + 2, kNumBars = kDone + 1;
   static constexpr int kOffTmem = kOffBar + kNumBars * 8;
   static constexpr int kSmem = kOffTmem + 16 + 1024;
   static_assert(kSmem <= 232448 && kSmem > 118784, "one CTA per SM");
-  static constexpr uint32_t kColK = 0, kColV = D / 2, kColDv = 64, kColDk = 64 + D,
-                            kColSlot = 64 + 2 * D;
-  static_assert(64 + 2 * D + 3 * kStep <= 512, "tensor memory");
+  static constexpr uint32_t kColK = 0, kColV = D / 2, kColDv = D, kColDk = 2 * D, kColS = 3 * D,
+                            kColP = 3 * D + kBuf * kStep;
+  static_assert(3 * D + 2 * kBuf * kStep <= 512, "tensor memory");
 };
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1)
     swa_bwd_dkv_kernel(const SwaBwdProblem p, const __grid_constant__ CUtensorMap tmQ,
-                       const __grid_constant__ CUtensorMap tmDo,
-                       const __grid_constant__ CUtensorMap tmV) {
+                       const __grid_constant__ CUtensorMap tmDo) {
   using C = DkvCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -450,7 +491,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(C::kEmpty + s), 1);
     }
     mbar_init(bar(C::kReady), 256);
-    mbar_init(bar(C::kVFull), 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(C::kSFull + s), 1);
       mbar_init(bar(C::kPFull + s), 8);
@@ -494,13 +534,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tmQ);
       tma_prefetch_desc(&tmDo);
       const uint64_t keep = l2_policy_evict_last();
-      if (!C::kVTmem) {
-        mbar_arrive_expect_tx(bar(C::kVFull), kBlk * D * 2);
-        for (int a = 0; a < C::kAtoms; ++a)
-          for (int r = 0; r < 2; ++r)  // rows past N arrive as zeros
-            tma_load_4d(base + C::kOffV + a * kAtomBlk + r * kAtomStep, &tmV, bar(C::kVFull),
-                        a * 64, g, j0 + r * kStep, b, keep);
-      }
       int h = h_first, u = u_first, n = 0;
       for (; n < nt; ++n) {
         const int s = n % C::kStages;
@@ -517,8 +550,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_4d(dst + C::kTile + a * kAtomStep, &tmDo, full, a * 64, h, i0, b, keep);
         }
         const int64_t at = (static_cast<int64_t>(b) * p.H + h) * p.Mp + i0;
-        bulk_load(dst + 2 * C::kTile, p.lse2 + at, kStep * 4, full);
-        bulk_load(dst + 2 * C::kTile + kStep * 4, p.delta + at, kStep * 4, full);
+        bulk_load(dst + 2 * C::kTile, p.nlse2 + at, kStep * 4, full);
+        bulk_load(dst + 2 * C::kTile + kStep * 4, p.ndelta + at, kStep * 4, full);
         if (++u == nq) {
           u = 0;
           ++h;
@@ -527,83 +560,74 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (failed) {  // leave nothing in flight
         for (int k = max(0, n - C::kStages); k < n; ++k)
           wait_phase(bar(C::kFull + k % C::kStages), (k / C::kStages) & 1, kWaitLimitNs);
-        if (!C::kVTmem) wait_phase(bar(C::kVFull), 0, kWaitLimitNs);
       }
     }
   } else if (warp == 9) {
     if (nt > 0) {
-      // ---- MMA issuer (the whole warp, one lane elected): S_0, dP_0, then
-      // S_{n+1}, dV_n, dP_{n+1}, dK_n ----
+      // ---- MMA issuer (the whole warp, one lane elected): the first kBuf S
+      // and dP, then dV_n, S_{n+kBuf}, dK_n, dP_{n+kBuf} ----
       constexpr uint32_t id_s = umma_idesc_f16(kBlk, kStep, BF16, false);
       constexpr uint32_t id_d = umma_idesc_f16(kBlk, D, BF16, true);
       const uint32_t on = elect_one();
       auto wait_all = [&](int i, uint32_t parity) {
-        return __all_sync(kFull, wait_phase(bar(i), parity, kWaitLimitNs));
-      };
-      auto issue_s = [&](int n, uint32_t slot, int st, uint32_t ph) -> bool {
-        if (!wait_all(C::kFull + st, ph)) return false;
+        const bool r = __all_sync(kFull, wait_phase(bar(i), parity, kWaitLimitNs));
         tc_fence_after();
-        const uint32_t qb = base + st * C::kStagePitch;
+        return r;
+      };
+      // slot = A (of tensor memory column `a`) B^T, B the tile at b0
+      auto mma_s = [&](uint32_t slot, uint32_t a, uint32_t b0) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          tc_mma_ts_if(on, slot, tmem + C::kColK + 8 * kk,
-                       umma_desc_sw128(qb + (kk >> 2) * kAtomStep + (kk & 3) * 32, 16), id_s,
+          tc_mma_ts_if(on, slot, a + 8 * kk,
+                       umma_desc_sw128(b0 + (kk >> 2) * kAtomStep + (kk & 3) * 32, 16), id_s,
                        kk > 0 ? 1u : 0u);
-        tc_commit_if(on, bar(C::kSFull + (n & 1)));
-        return true;
-      };
-      auto issue_dp = [&](int n, uint32_t slot, int st) {
-        const uint32_t ob = base + st * C::kStagePitch + C::kTile;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t bd = umma_desc_sw128(ob + (kk >> 2) * kAtomStep + (kk & 3) * 32, 16);
-          if (C::kVTmem)
-            tc_mma_ts_if(on, slot, tmem + C::kColV + 8 * kk, bd, id_s, kk > 0 ? 1u : 0u);
-          else
-            tc_mma_if(on, slot,
-                      umma_desc_sw128(base + C::kOffV + (kk >> 2) * kAtomBlk + (kk & 3) * 32, 16),
-                      bd, id_s, kk > 0 ? 1u : 0u);
-        }
-        tc_commit_if(on, bar(C::kDpFull + (n & 1)));
       };
       // dst += A B over a step's 64 queries; A (P or dS) in `a`: queries
       // 0..31 from column 0, 32..63 from column 32
-      auto issue_d = [&](uint32_t dst, uint32_t a, uint32_t b0, bool start) {
+      auto mma_d = [&](uint32_t dst, uint32_t a, uint32_t b0, bool start) {
 #pragma unroll
         for (int kk = 0; kk < kStep / 16; ++kk)
           tc_mma_ts_if(on, dst, a + (kk >> 1) * 32 + (kk & 1) * 8,
                        umma_desc_sw128(b0 + kk * 2048, kAtomStep), id_d, (!start || kk > 0) ? 1u : 0u);
       };
-      // slots of S_n (a), dP_n (c) and S_{n+1} (e); dP_{n+1} takes a
-      uint32_t a = tmem + C::kColSlot, c = a + kStep, e = c + kStep;
-      int st = 0;       // stage of step n
-      uint32_t ph = 0;  // phase of the stage of step n + 1
-      bool ok = wait_all(C::kReady, 0) && (C::kVTmem || wait_all(C::kVFull, 0));
-      if (ok) ok = issue_s(0, a, 0, 0);
-      if (ok) issue_dp(0, c, 0);
-      for (int n = 0; n < nt && ok; ++n) {
-        int next = st + 1;
-        if (next == C::kStages) {
-          next = 0;
-          ph ^= 1;
-        }
-        if (n + 1 < nt) ok = issue_s(n + 1, e, next, ph);
-        if (ok) ok = wait_all(C::kPFull + (n & 1), (n >> 1) & 1);
+      int st = 0, sl = 0;  // stages of step n and of the next step to start
+      uint32_t ph = 0;
+      bool ok = wait_all(C::kReady, 0);
+      for (int n = 0; n < C::kBuf && n < nt && ok; ++n) {
+        ok = wait_all(C::kFull + sl, ph);
         if (!ok) break;
-        tc_fence_after();
-        const uint32_t qb = base + st * C::kStagePitch;
-        issue_d(tmem + C::kColDv, a, qb + C::kTile, n == 0);
-        if (n + 1 < nt) issue_dp(n + 1, a, next);
+        const uint32_t qb = base + sl * C::kStagePitch;
+        mma_s(tmem + C::kColS + n * kStep, tmem + C::kColK, qb);
+        tc_commit_if(on, bar(C::kSFull + n));
+        mma_s(tmem + C::kColP + n * kStep, tmem + C::kColV, qb + C::kTile);
+        tc_commit_if(on, bar(C::kDpFull + n));
+        ++sl;
+      }
+      for (int n = 0; n < nt && ok; ++n) {
+        const uint32_t qb = base + st * C::kStagePitch, nb = base + sl * C::kStagePitch;
+        const uint32_t buf = C::kBuf == 2 ? (n & 1) * kStep : 0;
+        const int m = n + C::kBuf;
+        if (m < nt) ok = wait_all(C::kFull + sl, ph);
+        ok = ok && wait_all(C::kPFull + (n & 1), (n >> 1) & 1);
+        if (!ok) break;
+        mma_d(tmem + C::kColDv, tmem + C::kColS + buf, qb + C::kTile, n == 0);
+        if (m < nt) {
+          mma_s(tmem + C::kColS + buf, tmem + C::kColK, nb);
+          tc_commit_if(on, bar(C::kSFull + (m & 1)));
+        }
         ok = wait_all(C::kDsFull + (n & 1), (n >> 1) & 1);
         if (!ok) break;
-        tc_fence_after();
-        issue_d(tmem + C::kColDk, c, qb, n == 0);
+        mma_d(tmem + C::kColDk, tmem + C::kColP + buf, qb, n == 0);
         tc_commit_if(on, bar(C::kEmpty + st));
-        st = next;
-        const uint32_t t = a;  // step n + 1: S in e, dP in a, and c is free
-        a = e;
-        e = c;
-        c = t;
+        if (m < nt) {
+          mma_s(tmem + C::kColP + buf, tmem + C::kColV, nb + C::kTile);
+          tc_commit_if(on, bar(C::kDpFull + (m & 1)));
+        }
+        if (++st == C::kStages) st = 0;
+        if (++sl == C::kStages) {
+          sl = 0;
+          ph ^= 1;
+        }
       }
       tc_commit_if(on, bar(C::kDone));
       failed = !wait_all(C::kDone, 0) || !ok;
@@ -618,12 +642,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     const bool in = j < p.N;
     const int64_t off = ((static_cast<int64_t>(b) * p.N + (in ? j : 0)) * p.Hkv + g) * D;
-    if (wg == 0) row_to_tmem<D>(lane_addr + C::kColK, in ? p.K + off : nullptr);
-    if (wg == 1 && C::kVTmem) row_to_tmem<D>(lane_addr + C::kColV, in ? p.V + off : nullptr);
+    const uint16_t* const kv = wg == 0 ? p.K : p.V;
+    row_to_tmem<D>(lane_addr + (wg == 0 ? C::kColK : C::kColV), in ? kv + off : nullptr);
     tc_wait_st();
     tc_fence_before();
     mbar_arrive(bar(C::kReady));
     const int lo_j = j - p.right, hi_j = min(j + p.left, p.M - 1);  // the queries that see key j
+    const uint64_t sl2_2 = pair(p.sl2, p.sl2);
+    const uint64_t shift_2 = pair(Shift<BF16>::kSInv, Shift<BF16>::kSInv);
     int u = u_first;
     for (int n = 0; n < nt; ++n) {
       const int i0 = (u0 + u) * kStep, ic = i0 + 32 * wg;
@@ -636,33 +662,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      const uint32_t sa = lane_addr + C::kColSlot + (2 * n) % 3 * kStep + 32 * wg;
-      const uint32_t da = lane_addr + C::kColSlot + (2 * n + 1) % 3 * kStep + 32 * wg;
-      const float4* l2 = reinterpret_cast<const float4*>(
+      const uint32_t sa = lane_addr + C::kColS + (C::kBuf == 2 ? (n & 1) * kStep : 0) + 32 * wg;
+      const uint32_t da = sa + C::kBuf * kStep;
+      const ulonglong2* nl2 = reinterpret_cast<const ulonglong2*>(
           gbase + (n % C::kStages) * C::kStagePitch + 2 * C::kTile + 32 * wg * 4);
-      const float4* dl = l2 + kStep / 4;
+      const ulonglong2* ndl = nl2 + kStep / 4;
       const bool edge =
           j0 < i0 + kStep - 1 - p.left || j0 + kBlk - 1 > i0 + p.right || i0 + kStep > p.M;
       uint32_t s[32];
-      float pr[32];
+      uint64_t pr[16];
       tc_ld32(sa, s);
       tc_wait_ld();
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const float4 l = l2[c];
-        const float lv[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          pr[4 * c + e] = ex2(fmaf(__uint_as_float(s[4 * c + e]), p.sl2, -lv[e]));
+        const ulonglong2 l = nl2[c];  // -lse2 of 4 queries
+        pr[2 * c] = ex2_2(fma2(pair(s[4 * c], s[4 * c + 1]), sl2_2, l.x));
+        pr[2 * c + 1] = ex2_2(fma2(pair(s[4 * c + 2], s[4 * c + 3]), sl2_2, l.y));
       }
-      if (edge) {
+      auto hide = [&]() {
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
-          if (ic + c < lo_j || ic + c > hi_j) pr[c] = 0.f;
-      }
+        for (int c = 0; c < 16; ++c) {
+          float2 f = unpair(pr[c]);
+          if (ic + 2 * c < lo_j || ic + 2 * c > hi_j) f.x = 0.f;
+          if (ic + 2 * c + 1 < lo_j || ic + 2 * c + 1 > hi_j) f.y = 0.f;
+          pr[c] = pair(f.x, f.y);
+        }
+      };
+      auto pack = [&](uint32_t (&w)[16]) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const float2 f = unpair(pr[c]);
+          w[c] = pack2_t<BF16>(f.x, f.y);
+        }
+      };
+      if (edge) hide();
       uint32_t w[16];
-#pragma unroll
-      for (int c = 0; c < 16; ++c) w[c] = pack2_t<BF16>(pr[2 * c], pr[2 * c + 1]);
+      pack(w);
       tc_st16(sa, w);
       tc_wait_st();
       tc_fence_before();
@@ -677,19 +712,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_wait_ld();
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const float4 d = dl[c];
-        const float dv[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          pr[4 * c + e] *= fmaf(__uint_as_float(s[4 * c + e]), Shift<BF16>::kSInv, -dv[e]);
+        const ulonglong2 d = ndl[c];  // -delta of 4 queries
+        const uint64_t x = pair(s[4 * c], s[4 * c + 1]), y = pair(s[4 * c + 2], s[4 * c + 3]);
+        pr[2 * c] = mul2(pr[2 * c], BF16 ? add2(x, d.x) : fma2(x, shift_2, d.x));
+        pr[2 * c + 1] = mul2(pr[2 * c + 1], BF16 ? add2(y, d.y) : fma2(y, shift_2, d.y));
       }
-      if (edge) {  // again: 0 times an infinite dP of a hidden pair is not 0
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-          if (ic + c < lo_j || ic + c > hi_j) pr[c] = 0.f;
-      }
-#pragma unroll
-      for (int c = 0; c < 16; ++c) w[c] = pack2_t<BF16>(pr[2 * c], pr[2 * c + 1]);
+      if (edge) hide();  // again: 0 times an infinite dP of a hidden pair is not 0
+      pack(w);
       tc_st16(da, w);
       tc_wait_st();
       tc_fence_before();
@@ -820,7 +849,7 @@ int launch_swa_bwd(const SwaBwdProblem& p, cudaStream_t st) {
   const int64_t ki = static_cast<int64_t>(p.B) * p.Hkv * p.ktiles * p.splits;
   dq<<<static_cast<unsigned>(qi), kThreads, DqCfg<D>::kSmem, st>>>(p, tk, tv);
   if (cudaGetLastError() != cudaSuccess) return NSA_ERR_LAUNCH;
-  dkv<<<static_cast<unsigned>(ki), kThreads, DkvCfg<D>::kSmem, st>>>(p, tq, td, tv);
+  dkv<<<static_cast<unsigned>(ki), kThreads, DkvCfg<D>::kSmem, st>>>(p, tq, td);
   if (cudaGetLastError() != cudaSuccess) return NSA_ERR_LAUNCH;
   if (p.part != nullptr) {
     const int64_t n = static_cast<int64_t>(p.B) * p.N * p.Hkv * D;
@@ -911,9 +940,9 @@ extern "C" int nsa_swa_bwd(const void* Q, const void* K, const void* V, const vo
   p.sl2 = p.scale * 1.4426950408889634f;
   p.g32 = grad_dtype == NSA_F32;
   const int64_t stat = B * H * p.Mp;
-  p.lse2 = static_cast<float*>(workspace);
-  p.delta = p.lse2 + stat;
-  p.part = p.splits > 1 ? p.delta + stat : nullptr;
+  p.nlse2 = static_cast<float*>(workspace);
+  p.ndelta = p.nlse2 + stat;
+  p.part = p.splits > 1 ? p.ndelta + stat : nullptr;
   const bool bf = dtype == NSA_BF16;
   if (D == 64) return bf ? launch_swa_bwd<64, true>(p, st) : launch_swa_bwd<64, false>(p, st);
   return bf ? launch_swa_bwd<128, true>(p, st) : launch_swa_bwd<128, false>(p, st);
