@@ -56,7 +56,8 @@ namespace {
 
 constexpr int kBlk = 128;       // queries (dQ) or keys (dK, dV) of a CTA: the M of its products
 constexpr int kStep = 64;       // keys (dQ) or queries (dK, dV) of a step
-constexpr int kThreads = 320;   // 8 elementwise warps, the TMA warp, the MMA warp
+constexpr int kHalf = kStep / 2;  // queries of a step that one warpgroup takes
+constexpr int kThreads = 352;   // 8 elementwise warps, the TMA warp, two MMA warps
 constexpr int kAtomStep = kStep * 128;  // bytes of 64 rows x 64 entries
 constexpr uint32_t kTmemAll = 512;
 
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_commit_if(on, bar(C::kDone));
       failed = !wait_all(C::kDone, 0) || !ok;
     }
-  } else {
+  } else if (warp < 8) {
     // ---- elementwise: thread <-> (query row, half of a step's columns) ----
     const int wg = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane, iq = q0 + row;
@@ -464,8 +465,8 @@ struct DkvCfg {
   static constexpr int kBuf = D == 128 ? 1 : 2;  // buffers of S and of dP
   static constexpr int kOffBar = kStages * kStagePitch;
   static constexpr int kFull = 0, kEmpty = kStages, kReady = 2 * kStages, kSFull = kReady + 1,
-                       kPFull = kSFull + 2, kDpFull = kPFull + 2, kDsFull = kDpFull + 2,
-                       kDone = kDsFull + 2, kNumBars = kDone + 1;
+                       kPFull = kSFull + 4, kDpFull = kPFull + 4, kDsFull = kDpFull + 4,
+                       kDone = kDsFull + 4, kNumBars = kDone + 1;
   static constexpr int kOffTmem = kOffBar + kNumBars * 8;
   static constexpr int kSmem = kOffTmem + 16 + 1024;
   static_assert(kSmem <= 232448 && kSmem > 118784, "one CTA per SM");
@@ -488,16 +489,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(bar(C::kFull + s), 1);
-      mbar_init(bar(C::kEmpty + s), 1);
+      mbar_init(bar(C::kEmpty + s), 2);
     }
     mbar_init(bar(C::kReady), 256);
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < 4; ++s) {
       mbar_init(bar(C::kSFull + s), 1);
-      mbar_init(bar(C::kPFull + s), 8);
+      mbar_init(bar(C::kPFull + s), 4);
       mbar_init(bar(C::kDpFull + s), 1);
-      mbar_init(bar(C::kDsFull + s), 8);
+      mbar_init(bar(C::kDsFull + s), 4);
     }
-    mbar_init(bar(C::kDone), 1);
+    mbar_init(bar(C::kDone), 2);
     fence_mbar_init();
   }
   if (warp == 9) {
@@ -562,11 +563,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait_phase(bar(C::kFull + k % C::kStages), (k / C::kStages) & 1, kWaitLimitNs);
       }
     }
-  } else if (warp == 9) {
+  } else if (warp >= 9) {
     if (nt > 0) {
-      // ---- MMA issuer (the whole warp, one lane elected): the first kBuf S
-      // and dP, then dV_n, S_{n+kBuf}, dK_n, dP_{n+kBuf} ----
-      constexpr uint32_t id_s = umma_idesc_f16(kBlk, kStep, BF16, false);
+      // ---- MMA issuers (a whole warp each, one lane elected). Warp 9 forms S
+      // and dV, warp 10 dP and dK: P overwrites its S and dS its dP, so the
+      // two share no tensor memory, each accumulator is added to in one
+      // order, and one warp's waits pass while the other's products run.
+      // Half w of a step (queries 32 w .. 32 w + 31) belongs to warpgroup w. ----
+      constexpr uint32_t id_s = umma_idesc_f16(kBlk, kHalf, BF16, false);
       constexpr uint32_t id_d = umma_idesc_f16(kBlk, D, BF16, true);
       const uint32_t on = elect_one();
       auto wait_all = [&](int i, uint32_t parity) {
@@ -574,60 +578,63 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         return r;
       };
-      // slot = A (of tensor memory column `a`) B^T, B the tile at b0
-      auto mma_s = [&](uint32_t slot, uint32_t a, uint32_t b0) {
+      const bool is_v = warp == 9;
+      const uint32_t a_col = tmem + (is_v ? C::kColK : C::kColV);
+      const uint32_t s_col = tmem + (is_v ? C::kColS : C::kColP);
+      const uint32_t d_col = tmem + (is_v ? C::kColDv : C::kColDk);
+      // in a stage: the tile that forms S (dP), and the one dV (dK) sums over
+      const uint32_t s_tile = is_v ? 0 : C::kTile, d_tile = is_v ? C::kTile : 0;
+      const int s_bar = is_v ? C::kSFull : C::kDpFull, p_bar = is_v ? C::kPFull : C::kDsFull;
+      auto slot = [&](int n, int w) {
+        return s_col + (C::kBuf == 2 ? (n & 1) * kStep : 0) + w * kHalf;
+      };
+      auto half = [&](int stage, int w) {
+        return base + stage * C::kStagePitch + w * (kHalf * 128);
+      };
+      auto form = [&](int n, int w, int stage) {
+        const uint32_t b0 = half(stage, w) + s_tile, d = slot(n, w);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          tc_mma_ts_if(on, slot, a + 8 * kk,
+          tc_mma_ts_if(on, d, a_col + 8 * kk,
                        umma_desc_sw128(b0 + (kk >> 2) * kAtomStep + (kk & 3) * 32, 16), id_s,
                        kk > 0 ? 1u : 0u);
+        tc_commit_if(on, bar(s_bar + 2 * w + (n & 1)));
       };
-      // dst += A B over a step's 64 queries; A (P or dS) in `a`: queries
-      // 0..31 from column 0, 32..63 from column 32
-      auto mma_d = [&](uint32_t dst, uint32_t a, uint32_t b0, bool start) {
+      auto add = [&](int n, int w, int stage) {
+        const uint32_t b0 = half(stage, w) + d_tile, a = slot(n, w);
 #pragma unroll
-        for (int kk = 0; kk < kStep / 16; ++kk)
-          tc_mma_ts_if(on, dst, a + (kk >> 1) * 32 + (kk & 1) * 8,
-                       umma_desc_sw128(b0 + kk * 2048, kAtomStep), id_d, (!start || kk > 0) ? 1u : 0u);
+        for (int kk = 0; kk < kHalf / 16; ++kk)
+          tc_mma_ts_if(on, d_col, a + 8 * kk, umma_desc_sw128(b0 + kk * 2048, kAtomStep), id_d,
+                       (n > 0 || w > 0 || kk > 0) ? 1u : 0u);
       };
-      int st = 0, sl = 0;  // stages of step n and of the next step to start
+      int st = 0, sl = 0;  // stages of the steps n and n + kBuf
       uint32_t ph = 0;
       bool ok = wait_all(C::kReady, 0);
       for (int n = 0; n < C::kBuf && n < nt && ok; ++n) {
         ok = wait_all(C::kFull + sl, ph);
         if (!ok) break;
-        const uint32_t qb = base + sl * C::kStagePitch;
-        mma_s(tmem + C::kColS + n * kStep, tmem + C::kColK, qb);
-        tc_commit_if(on, bar(C::kSFull + n));
-        mma_s(tmem + C::kColP + n * kStep, tmem + C::kColV, qb + C::kTile);
-        tc_commit_if(on, bar(C::kDpFull + n));
+        form(n, 0, sl);
+        form(n, 1, sl);
         ++sl;
       }
+      if (ok && nt > C::kBuf) ok = wait_all(C::kFull + sl, ph);
       for (int n = 0; n < nt && ok; ++n) {
-        const uint32_t qb = base + st * C::kStagePitch, nb = base + sl * C::kStagePitch;
-        const uint32_t buf = C::kBuf == 2 ? (n & 1) * kStep : 0;
         const int m = n + C::kBuf;
-        if (m < nt) ok = wait_all(C::kFull + sl, ph);
-        ok = ok && wait_all(C::kPFull + (n & 1), (n >> 1) & 1);
+        ok = wait_all(p_bar + (n & 1), (n >> 1) & 1);
         if (!ok) break;
-        mma_d(tmem + C::kColDv, tmem + C::kColS + buf, qb + C::kTile, n == 0);
-        if (m < nt) {
-          mma_s(tmem + C::kColS + buf, tmem + C::kColK, nb);
-          tc_commit_if(on, bar(C::kSFull + (m & 1)));
-        }
-        ok = wait_all(C::kDsFull + (n & 1), (n >> 1) & 1);
+        add(n, 0, st);
+        if (m < nt) form(m, 0, sl);
+        ok = wait_all(p_bar + 2 + (n & 1), (n >> 1) & 1);
         if (!ok) break;
-        mma_d(tmem + C::kColDk, tmem + C::kColP + buf, qb, n == 0);
+        add(n, 1, st);
         tc_commit_if(on, bar(C::kEmpty + st));
-        if (m < nt) {
-          mma_s(tmem + C::kColP + buf, tmem + C::kColV, nb + C::kTile);
-          tc_commit_if(on, bar(C::kDpFull + (m & 1)));
-        }
+        if (m < nt) form(m, 1, sl);
         if (++st == C::kStages) st = 0;
         if (++sl == C::kStages) {
           sl = 0;
           ph ^= 1;
         }
+        if (m + 1 < nt) ok = wait_all(C::kFull + sl, ph);  // ahead of the wait for P (dS)
       }
       tc_commit_if(on, bar(C::kDone));
       failed = !wait_all(C::kDone, 0) || !ok;
@@ -654,30 +661,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int n = 0; n < nt; ++n) {
       const int i0 = (u0 + u) * kStep, ic = i0 + 32 * wg;
       if (++u == nq) u = 0;
-      // (the second wait, long over by then, is for the lse2 and delta of the
-      // stage, which this warp reads itself)
-      if (!wait_all(C::kSFull + (n & 1), (n >> 1) & 1) ||
-          !wait_all(C::kFull + n % C::kStages, (n / C::kStages) & 1)) {
+      // The stage's nlse2 and ndelta first, while S is being formed: a wait
+      // costs some 100 clocks even when it is over, and S is on the chain.
+      if (!wait_all(C::kFull + n % C::kStages, (n / C::kStages) & 1)) {
         failed = true;
         break;
       }
-      tc_fence_after();
       const uint32_t sa = lane_addr + C::kColS + (C::kBuf == 2 ? (n & 1) * kStep : 0) + 32 * wg;
       const uint32_t da = sa + C::kBuf * kStep;
       const ulonglong2* nl2 = reinterpret_cast<const ulonglong2*>(
           gbase + (n % C::kStages) * C::kStagePitch + 2 * C::kTile + 32 * wg * 4);
       const ulonglong2* ndl = nl2 + kStep / 4;
+      ulonglong2 nl[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) nl[c] = nl2[c];
       const bool edge =
           j0 < i0 + kStep - 1 - p.left || j0 + kBlk - 1 > i0 + p.right || i0 + kStep > p.M;
       uint32_t s[32];
       uint64_t pr[16];
+      if (!wait_all(C::kSFull + 2 * wg + (n & 1), (n >> 1) & 1)) {
+        failed = true;
+        break;
+      }
+      tc_fence_after();
       tc_ld32(sa, s);
       tc_wait_ld();
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const ulonglong2 l = nl2[c];  // -lse2 of 4 queries
-        pr[2 * c] = ex2_2(fma2(pair(s[4 * c], s[4 * c + 1]), sl2_2, l.x));
-        pr[2 * c + 1] = ex2_2(fma2(pair(s[4 * c + 2], s[4 * c + 3]), sl2_2, l.y));
+        pr[2 * c] = ex2_2(fma2(pair(s[4 * c], s[4 * c + 1]), sl2_2, nl[c].x));
+        pr[2 * c + 1] = ex2_2(fma2(pair(s[4 * c + 2], s[4 * c + 3]), sl2_2, nl[c].y));
       }
       auto hide = [&]() {
 #pragma unroll
@@ -702,8 +714,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(C::kPFull + (n & 1)));
-      if (!wait_all(C::kDpFull + (n & 1), (n >> 1) & 1)) {
+      if (lane == 0) mbar_arrive(bar(C::kPFull + 2 * wg + (n & 1)));
+      if (!wait_all(C::kDpFull + 2 * wg + (n & 1), (n >> 1) & 1)) {
         failed = true;
         break;
       }
@@ -723,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(C::kDsFull + (n & 1)));
+      if (lane == 0) mbar_arrive(bar(C::kDsFull + 2 * wg + (n & 1)));
     }
     if (!failed && nt > 0 && !wait_all(C::kDone, 0)) failed = true;
     if (!failed) {
