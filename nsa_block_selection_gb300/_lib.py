@@ -123,6 +123,7 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.nsa_qk_norm_rope_bwd.argtypes = [vp] * 13 + [i64] * 8 + [f32, c_int, c_int, c_int, c_int,
                                                                  vp, vp, i64, vp]
     if path is None:
+        _fill_dtype_codes()
         _lib = lib
     return lib
 
@@ -496,51 +497,54 @@ def swa_bwd(q, k, v, o, lse, do, window=(-1, -1), scale: Optional[float] = None,
     """
     import torch
 
-    lib = load()
-    if q.dtype not in (torch.float16, torch.bfloat16):
-        raise TypeError(f"q must be fp16 or bf16, got {q.dtype}")
-    if q.dim() != 4 or k.dim() != 4:
+    lib = _lib or load()
+    dt, qs, ks = q.dtype, q.shape, k.shape
+    if dt is not torch.bfloat16 and dt is not torch.float16:
+        raise TypeError(f"q must be fp16 or bf16, got {dt}")
+    if len(qs) != 4 or len(ks) != 4 or qs[0] != ks[0] or qs[3] != ks[3]:
         raise ValueError("shape mismatch: q [B,M,H,D], k/v [B,N,H_kv,D]")
-    B, M, H, D = q.shape
-    Bk, N, Hkv, Dk = k.shape
-    if (Bk, Dk) != (B, D):
-        raise ValueError("shape mismatch: q [B,M,H,D], k/v [B,N,H_kv,D]")
+    B, M, H, D = qs
+    N, Hkv = ks[1], ks[2]
     if grad_dtype is None:
         given = [t for t in (dq, dk, dv) if t is not None]
-        grad_dtype = given[0].dtype if given else q.dtype
-    if grad_dtype not in (torch.float32, q.dtype):
-        raise TypeError(f"gradients must be fp32 or {q.dtype}, got {grad_dtype}")
-    dev = q.device
-    dq = torch.empty(q.shape, dtype=grad_dtype, device=dev) if dq is None else dq
-    dk = torch.empty(k.shape, dtype=grad_dtype, device=dev) if dk is None else dk
-    dv = torch.empty(k.shape, dtype=grad_dtype, device=dev) if dv is None else dv
-    named = (("q", q, q.dtype, q.shape), ("k", k, q.dtype, k.shape), ("v", v, q.dtype, k.shape),
-             ("o", o, q.dtype, q.shape), ("lse", lse, torch.float32, (B, H, M)),
-             ("do", do, q.dtype, q.shape), ("dq", dq, grad_dtype, q.shape),
-             ("dk", dk, grad_dtype, k.shape), ("dv", dv, grad_dtype, k.shape))
-    for name, t, dt, shape in named:
-        if t.dtype != dt:
-            raise TypeError(f"{name} must be {dt}, got {t.dtype}")
+        grad_dtype = given[0].dtype if given else dt
+    if grad_dtype is not torch.float32 and grad_dtype is not dt:
+        raise TypeError(f"gradients must be fp32 or {dt}, got {grad_dtype}")
+    if dq is None:
+        dq = torch.empty_like(q, dtype=grad_dtype)
+    if dk is None:
+        dk = torch.empty_like(k, dtype=grad_dtype)
+    if dv is None:
+        dv = torch.empty_like(k, dtype=grad_dtype)
+    named = (("q", q, dt, qs), ("k", k, dt, ks), ("v", v, dt, ks), ("o", o, dt, qs),
+             ("lse", lse, torch.float32, (B, H, M)), ("do", do, dt, qs),
+             ("dq", dq, grad_dtype, qs), ("dk", dk, grad_dtype, ks), ("dv", dv, grad_dtype, ks))
+    for name, t, want, shape in named:
+        if t.dtype is not want:
+            raise TypeError(f"{name} must be {want}, got {t.dtype}")
         if t.shape != shape:
             raise ValueError(f"{name} must have the shape {tuple(shape)}")
+    dev = q.get_device()
     for name, t, _, _ in named:
-        if not t.is_cuda or t.device != dev or not t.is_contiguous():
+        if t.get_device() != dev or dev < 0 or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous tensor on q's CUDA device")
     left, right = (int(window[0]), int(window[1])) if window is not None else (-1, -1)
     if workspace is None:
-        need = swa_bwd_workspace_bytes(B, M, N, H, Hkv, D, (left, right))
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    if workspace.device != dev:
+        need = lib.nsa_swa_bwd_workspace_bytes(B, M, N, H, Hkv, D, left, right)
+        if need < 0:
+            raise NsaError(need, "nsa_swa_bwd_workspace_bytes")
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if workspace.get_device() != dev:
         raise ValueError("workspace must be on q's CUDA device")
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    sc = float(scale) if scale is not None else 0.0  # the ABI: <= 0 selects 1/sqrt(D)
-    with torch.cuda.device(dev):
-        st = lib.nsa_swa_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(do), _ptr(dq),
-                             _ptr(dk), _ptr(dv), B, M, N, H, Hkv, D, left, right, sc,
-                             _dtype_code(q.dtype), _dtype_code(grad_dtype), _ptr(workspace),
+    with _on_device(dev):
+        # scale: the ABI takes <= 0 for 1/sqrt(D)
+        st = lib.nsa_swa_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                             lse.data_ptr(), do.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+                             dv.data_ptr(), B, M, N, H, Hkv, D, left, right,
+                             0.0 if scale is None else scale, _DTYPE_CODES[dt],
+                             _DTYPE_CODES[grad_dtype], workspace.data_ptr(),
                              workspace.numel() * workspace.element_size(),
-                             ctypes.c_void_p(stream.cuda_stream))
+                             _raw_stream(stream, dev))
     if st != NSA_OK:
         raise NsaError(st, "nsa_swa_bwd")
     return dq, dk, dv
@@ -562,64 +566,127 @@ def rope_tables(rows: int, rot_dim: int, base: float = 10000.0, device="cuda"):
     return ang.cos().float(), ang.sin().float()
 
 
+class _on_device:
+    """Makes a CUDA device current for a launch; does nothing where it is."""
+
+    def __init__(self, index):
+        self.index = index
+
+    def __enter__(self):
+        import torch
+
+        self.prev = torch._C._cuda_getDevice()
+        if self.prev != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        import torch
+
+        if self.prev != self.index:
+            torch.cuda.set_device(self.prev)
+
+
+def _raw_stream(stream, index):
+    """The cudaStream_t of ``stream``, or of the device's current stream."""
+    import torch
+
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
 def _check_rope(named, weights, cos, sin, positions):
-    """Checks shared by the norm-and-rotation calls; returns the sizes and
-    pointers they pass on."""
+    """Checks shared by the norm-and-rotation calls; ``named``: (name, tensor,
+    allowed dtypes), of q's and k's shapes in turn. Returns the sizes and codes
+    that the calls pass on. These calls may be a token's work: what is checked
+    here costs microseconds beside them, so each property is read once."""
     import torch
 
     q, k = named[0][1], named[1][1]
-    if q.dtype not in (torch.float16, torch.bfloat16):
-        raise TypeError(f"q must be fp16 or bf16, got {q.dtype}")
-    if q.dim() != 4 or k.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]:
+    dt, qs, ks = q.dtype, q.shape, k.shape
+    if dt is not torch.bfloat16 and dt is not torch.float16:
+        raise TypeError(f"q must be fp16 or bf16, got {dt}")
+    if len(qs) != 4 or len(ks) != 4 or qs[0] != ks[0] or qs[1] != ks[1] or qs[3] != ks[3]:
         raise ValueError("shape mismatch: q [B,M,H,D], k [B,M,G,D]")
-    B, M, H, D = q.shape
-    for i, (name, t, dtypes) in enumerate(named):
+    B, M, H, D = qs
+    dev = q.get_device()
+    shape = ks
+    for name, t, dtypes in named:
+        shape = qs if shape is ks else ks
         if t.dtype not in dtypes:
             raise TypeError(f"{name} must be one of {dtypes}, got {t.dtype}")
-        if tuple(t.shape) != tuple((q, k)[i % 2].shape):
-            raise ValueError(f"{name} must have the shape of {'qk'[i % 2]}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have the shape {tuple(shape)}")
     for name, t, _ in named:
-        if not t.is_cuda or t.device != q.device:
+        if t.get_device() != dev or dev < 0:
             raise ValueError(f"{name} must be on q's CUDA device")
-        if t.numel() > 0 and t.stride(-1) != 1:
+        if not t.is_contiguous() and t.stride(3) != 1:
             raise ValueError(f"{name} must have a contiguous last dimension")
     wdt = None
     for name, w in weights:
         if w is None:
             continue
-        if w.dtype not in (torch.float32, q.dtype) or (wdt is not None and w.dtype != wdt):
-            raise TypeError(f"{name} must be fp32 or {q.dtype}, and both weights alike")
+        if (w.dtype is not torch.float32 and w.dtype is not dt) or \
+                (wdt is not None and w.dtype is not wdt):
+            raise TypeError(f"{name} must be fp32 or {dt}, and both weights alike")
         wdt = w.dtype
-        if tuple(w.shape) != (D,) or not w.is_contiguous() or w.device != q.device:
+        if w.shape != (D,) or not w.is_contiguous() or w.get_device() != dev:
             raise ValueError(f"{name} must be a contiguous [D] tensor on q's device")
-    if (cos is None) != (sin is None):
-        raise ValueError("pass both tables or neither")
     R = rows = 0
-    if cos is not None:
-        if cos.dtype != torch.float32 or sin.dtype != torch.float32:
+    if cos is not None and sin is not None:
+        cs = cos.shape
+        if cos.dtype is not torch.float32 or sin.dtype is not torch.float32:
             raise TypeError("cos and sin must be fp32")
-        if cos.dim() != 2 or cos.shape != sin.shape or not cos.is_contiguous() or \
-                not sin.is_contiguous() or cos.device != q.device or sin.device != q.device:
+        if len(cs) != 2 or cs != sin.shape or not cos.is_contiguous() or \
+                not sin.is_contiguous() or cos.get_device() != dev or sin.get_device() != dev:
             raise ValueError("cos and sin must be contiguous [rows, R/2] tensors on q's device")
-        rows, R = cos.shape[0], 2 * cos.shape[1]
+        rows, R = cs[0], 2 * cs[1]
+    elif cos is not None or sin is not None:
+        raise ValueError("pass both tables or neither")
     pstride = 0
     if positions is not None:
-        if positions.dtype != torch.int32:
+        if positions.dtype is not torch.int32:
             raise TypeError(f"positions must be int32, got {positions.dtype}")
-        if tuple(positions.shape) not in ((M,), (B, M)) or not positions.is_contiguous() or \
-                positions.device != q.device:
-            raise ValueError("positions must be a contiguous [M] or [B, M] tensor on q's device")
-        pstride = M if positions.dim() == 2 else 0
-    return B, M, H, k.shape[2], D, R, rows, pstride, _dtype_code(q.dtype if wdt is None else wdt)
+        ps = positions.shape
+        if ps == (B, M):
+            pstride = M
+        elif ps != (M,):
+            raise ValueError("positions must be [M] or [B, M]")
+        if not positions.is_contiguous() or positions.get_device() != dev:
+            raise ValueError("positions must be a contiguous tensor on q's device")
+    return dev, B, M, H, ks[2], D, R, rows, pstride, _DTYPE_CODES[dt], \
+        NSA_F32 if wdt is None else _DTYPE_CODES[wdt]
 
 
-def _strides(tensors):
+_DTYPE_CODES = {}
+
+
+def _fill_dtype_codes():
+    import torch
+
+    _DTYPE_CODES.update({torch.float16: NSA_F16, torch.bfloat16: NSA_BF16,
+                         torch.float32: NSA_F32})
+
+
+_STRIDES12, _STRIDES18 = ctypes.c_int64 * 12, ctypes.c_int64 * 18
+
+
+def _strides(kind, *tensors):
     """(b, m, head) element strides of [B, M, heads, D] tensors; None if all
     are contiguous. The stride of a dimension of one is never used."""
-    if all(t.is_contiguous() or t.numel() == 0 for t in tensors):
+    for t in tensors:
+        if not t.is_contiguous():
+            break
+    else:
         return None
-    s = [st if n > 1 else 0 for t in tensors for st, n in zip(t.stride()[:3], t.shape[:3])]
-    return (ctypes.c_int64 * len(s))(*s)
+    s = []
+    for t in tensors:
+        sb, sm, sh, _ = t.stride()
+        B, M, H, _ = t.shape
+        s += (sb if B > 1 else 0, sm if M > 1 else 0, sh if H > 1 else 0)
+    return kind(*s)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
@@ -641,31 +708,32 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positio
     """
     import torch
 
-    lib = load()
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
-    named = [("q", q, (q.dtype,)), ("k", k, (q.dtype,)), ("q_out", q_out, (q.dtype,)),
-             ("k_out", k_out, (q.dtype,))]
-    B, M, H, G, D, R, rows, ps, wdt = _check_rope(
-        named, (("q_weight", q_weight), ("k_weight", k_weight)), cos, sin, positions)
-    if stream is None:
-        stream = torch.cuda.current_stream(q.device)
-    with torch.cuda.device(q.device):
-        st = lib.nsa_qk_norm_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(q_weight),
-                                  _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(positions), B, M, H,
-                                  G, D, R, rows, ps, float(eps), int(bool(interleaved)),
-                                  _dtype_code(q.dtype), wdt, _strides((q, k, q_out, k_out)),
-                                  ctypes.c_void_p(stream.cuda_stream))
+    lib = _lib or load()
+    if q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    if k_out is None:
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+    own = (q.dtype,)
+    dev, B, M, H, G, D, R, rows, ps, code, wcode = _check_rope(
+        (("q", q, own), ("k", k, own), ("q_out", q_out, own), ("k_out", k_out, own)),
+        (("q_weight", q_weight), ("k_weight", k_weight)), cos, sin, positions)
+    with _on_device(dev):
+        st = lib.nsa_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
+                                  _at(q_weight), _at(k_weight), _at(cos), _at(sin),
+                                  _at(positions), B, M, H, G, D, R, rows, ps, eps,
+                                  1 if interleaved else 0, code, wcode,
+                                  _strides(_STRIDES12, q, k, q_out, k_out),
+                                  _raw_stream(stream, dev))
     if st != NSA_OK:
         raise NsaError(st, "nsa_qk_norm_rope")
     return q_out, k_out
 
 
 def norm_rope_bwd_workspace_bytes(B, M, D) -> int:
-    n = load().nsa_qk_norm_rope_bwd_workspace_bytes(B, M, D)
+    n = (_lib or load()).nsa_qk_norm_rope_bwd_workspace_bytes(B, M, D)
     if n < 0:
         raise NsaError(int(n), "nsa_qk_norm_rope_bwd_workspace_bytes")
-    return int(n)
+    return n
 
 
 def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, cos=None, sin=None,
@@ -684,42 +752,45 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, cos=Non
     """
     import torch
 
-    lib = load()
-    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
-    dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
-    gts = (torch.float32, q.dtype)
-    named = [("q", q, (q.dtype,)), ("k", k, (q.dtype,)), ("dq_out", dq_out, gts),
-             ("dk_out", dk_out, (dq_out.dtype,)), ("dq", dq, (q.dtype,)), ("dk", dk, (q.dtype,))]
-    B, M, H, G, D, R, rows, ps, wdt = _check_rope(
-        named, (("q_weight", q_weight), ("k_weight", k_weight)), cos, sin, positions)
-    need = norm_rope_bwd_workspace_bytes(B, M, D) if weight_grads else 0
+    lib = _lib or load()
+    if dq is None:
+        dq = torch.empty_like(q, memory_format=torch.contiguous_format)
+    if dk is None:
+        dk = torch.empty_like(k, memory_format=torch.contiguous_format)
+    own = (q.dtype,)
+    dev, B, M, H, G, D, R, rows, ps, code, wcode = _check_rope(
+        (("q", q, own), ("k", k, own), ("dq_out", dq_out, (torch.float32, q.dtype)),
+         ("dk_out", dk_out, (dq_out.dtype,)), ("dq", dq, own), ("dk", dk, own)),
+        (("q_weight", q_weight), ("k_weight", k_weight)), cos, sin, positions)
+    nbytes = 0
     if weight_grads:
-        dws = []
+        if dq_weight is None:
+            dq_weight = torch.empty(D, dtype=torch.float32, device=q.device)
+        if dk_weight is None:
+            dk_weight = torch.empty(D, dtype=torch.float32, device=q.device)
         for name, w in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
-            w = torch.empty((D,), dtype=torch.float32, device=q.device) if w is None else w
-            if w.dtype != torch.float32 or tuple(w.shape) != (D,) or not w.is_contiguous() or \
-                    w.device != q.device:
+            if w.dtype is not torch.float32 or w.shape != (D,) or not w.is_contiguous() or \
+                    w.get_device() != dev:
                 raise ValueError(f"{name} must be a contiguous fp32 [D] tensor on q's device")
-            dws.append(w)
         if workspace is None:
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
-        if not workspace.is_cuda or workspace.device != q.device:
+            workspace = torch.empty(norm_rope_bwd_workspace_bytes(B, M, D), dtype=torch.uint8,
+                                    device=q.device)
+        if workspace.get_device() != dev:
             raise ValueError("workspace must be on q's CUDA device")
+        nbytes = workspace.numel() * workspace.element_size()
     else:
-        dws, workspace = [None, None], None
-    if stream is None:
-        stream = torch.cuda.current_stream(q.device)
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with torch.cuda.device(q.device):
+        dq_weight = dk_weight = workspace = None
+    with _on_device(dev):
         st = lib.nsa_qk_norm_rope_bwd(
-            _ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dws[0]),
-            _ptr(dws[1]), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(positions), B,
-            M, H, G, D, R, rows, ps, float(eps), int(bool(interleaved)), _dtype_code(q.dtype), wdt,
-            _dtype_code(dq_out.dtype), _strides((q, k, dq_out, dk_out, dq, dk)), _ptr(workspace),
-            nbytes, ctypes.c_void_p(stream.cuda_stream))
+            q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(),
+            dk.data_ptr(), _at(dq_weight), _at(dk_weight), _at(q_weight), _at(k_weight), _at(cos),
+            _at(sin), _at(positions), B, M, H, G, D, R, rows, ps, eps, 1 if interleaved else 0,
+            code, wcode, _DTYPE_CODES[dq_out.dtype],
+            _strides(_STRIDES18, q, k, dq_out, dk_out, dq, dk), _at(workspace), nbytes,
+            _raw_stream(stream, dev))
     if st != NSA_OK:
         raise NsaError(st, "nsa_qk_norm_rope_bwd")
-    return dq, dk, dws[0], dws[1]
+    return dq, dk, dq_weight, dk_weight
 
 
 def probe_l2_gather(k, v, g: int, block_size: int, ctas: int, warps_per_cta: int,
