@@ -58,7 +58,9 @@ constexpr int kBlk = 128;       // queries (dQ) or keys (dK, dV) of a CTA: the M
 constexpr int kStep = 64;       // keys (dQ) or queries (dK, dV) of a step
 constexpr int kHalf = kStep / 2;  // queries of a step that one warpgroup takes
 constexpr int kThreads = 352;   // 8 elementwise warps, the TMA warp, two MMA warps
+constexpr int kDqThreads = 448;  // 8 elementwise and 4 auxiliary warps, the TMA warp, the MMA warp
 constexpr int kAtomStep = kStep * 128;  // bytes of 64 rows x 64 entries
+constexpr int kAtomBlk = kBlk * 128;
 constexpr uint32_t kTmemAll = 512;
 
 // fp16 has no exponents below 2^-14 at full precision, and over thousands of
@@ -81,6 +83,7 @@ struct SwaBwdProblem {
   float* ndelta;  // [B, H, Mp]: -delta 2^(kS - kP)
   float* part;   // [splits, 2, B, N, Hkv, D], or NULL
   int B, M, N, H, Hkv, hpg, Mp, qtiles, ktiles, splits;
+  int dq_items;  // B H qtiles
   int left, right;  // clamped to [0, M] and [0, N]: unbounded in effect
   float sl2, scale;
   bool g32;  // gradients fp32 instead of the inputs' type
@@ -183,11 +186,14 @@ template <int D>
 struct DqCfg {
   static constexpr int kAtoms = D / 64;
   static constexpr int kTile = kStep * D * 2;      // one K or V tile
-  static constexpr int kStages = D == 128 ? 6 : 8;
-  static constexpr int kOffStat = kStages * 2 * kTile;  // lse2 and delta of the CTA's rows
-  static constexpr int kOffBar = kOffStat + 2 * kBlk * 4;
-  static constexpr int kFull = 0, kEmpty = kStages, kReady = 2 * kStages, kSFull = kReady + 1,
-                       kDsFull = kSFull + 2, kDone = kDsFull + 2, kNumBars = kDone + 1;
+  static constexpr int kStages = D == 128 ? 4 : 6;
+  static constexpr int kOffQ = kStages * 2 * kTile;      // the next item's Q and dO
+  static constexpr int kOffDo = kOffQ + kBlk * D * 2;
+  static constexpr int kOffStat = kOffDo + kBlk * D * 2;  // 2 x (LSE in base 2, delta) of the rows
+  static constexpr int kOffBar = kOffStat + 4 * kBlk * 4;
+  static constexpr int kFull = 0, kEmpty = kStages, kStaged = 2 * kStages, kReady = kStaged + 1,
+                       kSDone = kReady + 1, kSFull = kSDone + 1, kDsFull = kSFull + 2,
+                       kDqDone = kDsFull + 2, kDqFree = kDqDone + 1, kNumBars = kDqFree + 1;
   static constexpr int kOffTmem = kOffBar + kNumBars * 8;
   static constexpr int kSmem = kOffTmem + 16 + 1024;
   static_assert(kSmem <= 232448 && kSmem > 118784, "one CTA per SM");
@@ -197,10 +203,38 @@ struct DqCfg {
   static_assert(2 * D + 4 * kStep <= 512, "tensor memory");
 };
 
+// One item of the dQ kernel: 128 queries of a head, and the key tiles of 64
+// that their windows touch.
+struct DqItem {
+  int b, g, h, q0, q_last, t0, nt;
+};
+
+// Items in the order (b, KV head, query tile, head): heads fastest, so that
+// the CTAs of a moment share K and V in L2; later tiles, which see more keys
+// under a causal window, first.
+__device__ __forceinline__ DqItem dq_item(const SwaBwdProblem& p, uint32_t x) {
+  DqItem it;
+  const int hh = static_cast<int>(x % static_cast<uint32_t>(p.hpg));
+  x /= static_cast<uint32_t>(p.hpg);
+  const int qt = p.qtiles - 1 - static_cast<int>(x % static_cast<uint32_t>(p.qtiles));
+  x /= static_cast<uint32_t>(p.qtiles);
+  it.g = static_cast<int>(x % static_cast<uint32_t>(p.Hkv));
+  it.b = static_cast<int>(x / static_cast<uint32_t>(p.Hkv));
+  it.h = it.g * p.hpg + hh;
+  it.q0 = qt * kBlk;
+  it.q_last = min(it.q0 + kBlk, p.M) - 1;
+  const int jlo = max(0, it.q0 - p.left), jhi = min(p.N - 1, it.q_last + p.right);
+  it.t0 = jlo / kStep;
+  it.nt = jhi >= jlo ? jhi / kStep - it.t0 + 1 : 0;
+  return it;
+}
+
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kDqThreads, 1)
     swa_bwd_dq_kernel(const SwaBwdProblem p, const __grid_constant__ CUtensorMap tmK,
-                      const __grid_constant__ CUtensorMap tmV) {
+                      const __grid_constant__ CUtensorMap tmV,
+                      const __grid_constant__ CUtensorMap tmQ,
+                      const __grid_constant__ CUtensorMap tmDo) {
   using C = DqCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -213,15 +247,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(C::kFull + s), 1);
       mbar_init(bar(C::kEmpty + s), 1);
     }
-    mbar_init(bar(C::kReady), 256);
+    mbar_init(bar(C::kStaged), 1);
+    mbar_init(bar(C::kReady), 4);
+    mbar_init(bar(C::kSDone), 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(C::kSFull + s), 1);
       mbar_init(bar(C::kDsFull + s), 8);
     }
-    mbar_init(bar(C::kDone), 1);
+    mbar_init(bar(C::kDqDone), 1);
+    mbar_init(bar(C::kDqFree), 4);
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == 13) {
     tc_alloc(base + C::kOffTmem, kTmemAll);
     tc_relinquish();
   }
@@ -229,224 +266,339 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + C::kOffTmem);
-
-  // the CTA's item: (b, KV head, query tile, head), heads fastest so that
-  // the CTAs of a moment share K and V in L2; later tiles, which see more
-  // keys under a causal window, first
-  uint32_t x = blockIdx.x;
-  const int hh = static_cast<int>(x % static_cast<uint32_t>(p.hpg));
-  x /= static_cast<uint32_t>(p.hpg);
-  const int qt = p.qtiles - 1 - static_cast<int>(x % static_cast<uint32_t>(p.qtiles));
-  x /= static_cast<uint32_t>(p.qtiles);
-  const int g = static_cast<int>(x % static_cast<uint32_t>(p.Hkv));
-  const int b = static_cast<int>(x / static_cast<uint32_t>(p.Hkv));
-  const int h = g * p.hpg + hh;
-  const int q0 = qt * kBlk, q_last = min(q0 + kBlk, p.M) - 1;
-  const int jlo = max(0, q0 - p.left), jhi = min(p.N - 1, q_last + p.right);
-  const int t0 = jlo / kStep, nt = jhi >= jlo ? jhi / kStep - t0 + 1 : 0;
+  float* const stat = reinterpret_cast<float*>(gbase + C::kOffStat);
   bool failed = false;
+  auto wait_all = [&](int i, uint32_t parity) {
+    const bool r = __all_sync(kFull, wait_phase(bar(i), parity, kWaitLimitNs));
+    tc_fence_after();
+    return r;
+  };
+  // Items are dealt in rounds of gridDim.x, in snake order, as in the forward.
+  // Below, n counts the items with keys, g0 their steps.
+  const uint32_t items = static_cast<uint32_t>(p.dq_items);
+  const uint32_t rounds = (items + gridDim.x - 1) / gridDim.x;
+  auto item_of = [&](uint32_t k) {
+    return k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  };
 
-  if (warp == 8) {
-    if (lane == 0 && nt > 0) {
+  if (warp == 12) {
+    if (lane == 0) {
       // ---- TMA producer: K and V tiles of 64 keys ----
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
       const uint64_t keep = l2_policy_evict_last();
-      int i = 0;
-      for (; i < nt; ++i) {
-        const int s = i % C::kStages;
-        if (i >= C::kStages &&
-            !wait_phase(bar(C::kEmpty + s), (i / C::kStages - 1) & 1, kWaitLimitNs)) {
-          failed = true;
-          break;
-        }
-        mbar_arrive_expect_tx(bar(C::kFull + s), 2 * C::kTile);
-        const uint32_t dst = base + s * 2 * C::kTile;
-        for (int a = 0; a < C::kAtoms; ++a) {
-          tma_load_4d(dst + a * kAtomStep, &tmK, bar(C::kFull + s), a * 64, g, (t0 + i) * kStep, b,
-                      keep);
-          tma_load_4d(dst + C::kTile + a * kAtomStep, &tmV, bar(C::kFull + s), a * 64, g,
-                      (t0 + i) * kStep, b, keep);
+      int s = 0;
+      uint32_t ph = 1;  // of the wait for an empty stage: the first round passes
+      int in_flight = 0;
+      for (uint32_t k = 0; k < rounds && !failed; ++k) {
+        const uint32_t x = item_of(k);
+        if (x >= items) continue;
+        const DqItem it = dq_item(p, x);
+        for (int i = 0; i < it.nt; ++i) {
+          if (!wait_phase(bar(C::kEmpty + s), ph, kWaitLimitNs)) {
+            failed = true;
+            break;
+          }
+          mbar_arrive_expect_tx(bar(C::kFull + s), 2 * C::kTile);
+          const uint32_t dst = base + s * 2 * C::kTile;
+          const int j0 = (it.t0 + i) * kStep;
+          for (int a = 0; a < C::kAtoms; ++a) {
+            tma_load_4d(dst + a * kAtomStep, &tmK, bar(C::kFull + s), a * 64, it.g, j0, it.b, keep);
+            tma_load_4d(dst + C::kTile + a * kAtomStep, &tmV, bar(C::kFull + s), a * 64, it.g, j0,
+                        it.b, keep);
+          }
+          if (in_flight < C::kStages) ++in_flight;
+          if (++s == C::kStages) {
+            s = 0;
+            ph ^= 1;
+          }
         }
       }
-      if (failed)  // leave nothing in flight
-        for (int k = max(0, i - C::kStages); k < i; ++k)
-          wait_phase(bar(C::kFull + k % C::kStages), (k / C::kStages) & 1, kWaitLimitNs);
+      if (failed) {  // leave nothing in flight: the last loads of the stages before s
+        for (int k = 0; k < in_flight; ++k) {
+          s = s == 0 ? C::kStages - 1 : s - 1;
+          if (s == C::kStages - 1) ph ^= 1;
+          wait_phase(bar(C::kFull + s), ph ^ 1, kWaitLimitNs);
+        }
+      }
     }
-  } else if (warp == 9) {
-    if (nt > 0) {
-      // ---- MMA issuer (the whole warp, one lane elected): S_i, dP_i, dQ_{i-1} ----
-      constexpr uint32_t id_s = umma_idesc_f16(kBlk, kStep, BF16, false);
-      constexpr uint32_t id_q = umma_idesc_f16(kBlk, D, BF16, true);
-      const uint32_t on = elect_one();
-      auto wait_all = [&](int i, uint32_t parity) {
-        return __all_sync(kFull, wait_phase(bar(i), parity, kWaitLimitNs));
-      };
-      auto issue_dq = [&](int i, int s) -> bool {
-        if (!wait_all(C::kDsFull + (i & 1), (i >> 1) & 1)) return false;
-        tc_fence_after();
-        const uint32_t ds = tmem + C::kColS + (i & 1) * kStep;
-        const uint32_t kb = base + s * 2 * C::kTile;
+  } else if (warp == 13) {
+    // ---- MMA issuer (the whole warp, one lane elected): S_i, dP_i, dQ_{i-1} ----
+    constexpr uint32_t id_s = umma_idesc_f16(kBlk, kStep, BF16, false);
+    constexpr uint32_t id_q = umma_idesc_f16(kBlk, D, BF16, true);
+    const uint32_t on = elect_one();
+    int s = 0, s_prev = 0;
+    uint32_t ph = 0, g0 = 0, n = 0;
+    auto issue_dq = [&](uint32_t g, int stage, bool start) -> bool {
+      if (!wait_all(C::kDsFull + (g & 1), (g >> 1) & 1)) return false;
+      const uint32_t ds = tmem + C::kColS + (g & 1) * kStep;
+      const uint32_t kb = base + stage * 2 * C::kTile;
 #pragma unroll
-        for (int kk = 0; kk < kStep / 16; ++kk)  // dS of keys 0..31 at column 0, 32..63 at 32
-          tc_mma_ts_if(on, tmem + C::kColDq, ds + (kk >> 1) * 32 + (kk & 1) * 8,
-                       umma_desc_sw128(kb + kk * 2048, kAtomStep), id_q,
-                       (i > 0 || kk > 0) ? 1u : 0u);
-        tc_commit_if(on, bar(C::kEmpty + s));
-        return true;
-      };
-      bool ok = wait_all(C::kReady, 0);
-      int s = 0, s_prev = 0;
-      uint32_t ph = 0;
+      for (int kk = 0; kk < kStep / 16; ++kk)  // dS of keys 0..31 at column 0, 32..63 at 32
+        tc_mma_ts_if(on, tmem + C::kColDq, ds + (kk >> 1) * 32 + (kk & 1) * 8,
+                     umma_desc_sw128(kb + kk * 2048, kAtomStep), id_q, (!start || kk > 0) ? 1u : 0u);
+      tc_commit_if(on, bar(C::kEmpty + stage));
+      return true;
+    };
+    bool ok = true;
+    for (uint32_t k = 0; k < rounds && ok; ++k) {
+      const uint32_t x = item_of(k);
+      if (x >= items) continue;
+      const int nt = dq_item(p, x).nt;
+      if (nt == 0) continue;
+      ok = wait_all(C::kReady, n & 1);
       for (int i = 0; i < nt && ok; ++i) {
+        const uint32_t g = g0 + i;
         ok = wait_all(C::kFull + s, ph);
         if (!ok) break;
-        tc_fence_after();
         const uint32_t kb = base + s * 2 * C::kTile, vb = kb + C::kTile;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          tc_mma_ts_if(on, tmem + C::kColS + (i & 1) * kStep, tmem + C::kColQ + 8 * kk,
+          tc_mma_ts_if(on, tmem + C::kColS + (g & 1) * kStep, tmem + C::kColQ + 8 * kk,
                        umma_desc_sw128(kb + (kk >> 2) * kAtomStep + (kk & 3) * 32, 16), id_s,
                        kk > 0 ? 1u : 0u);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          tc_mma_ts_if(on, tmem + C::kColP + (i & 1) * kStep, tmem + C::kColDo + 8 * kk,
+          tc_mma_ts_if(on, tmem + C::kColP + (g & 1) * kStep, tmem + C::kColDo + 8 * kk,
                        umma_desc_sw128(vb + (kk >> 2) * kAtomStep + (kk & 3) * 32, 16), id_s,
                        kk > 0 ? 1u : 0u);
-        tc_commit_if(on, bar(C::kSFull + (i & 1)));
-        if (i > 0) ok = issue_dq(i - 1, s_prev);
+        tc_commit_if(on, bar(C::kSFull + (g & 1)));
+        if (i == nt - 1) tc_commit_if(on, bar(C::kSDone));  // Q and dO have been read
+        if (i > 0) {
+          // (the item's first dQ overwrites the last item's)
+          if (i == 1 && n > 0) ok = wait_all(C::kDqFree, (n - 1) & 1);
+          ok = ok && issue_dq(g - 1, s_prev, i == 1);
+        }
         s_prev = s;
         if (++s == C::kStages) {
           s = 0;
           ph ^= 1;
         }
       }
-      if (ok) ok = issue_dq(nt - 1, s_prev);
-      // also after a failed wait: nothing is left in flight at the teardown
-      tc_commit_if(on, bar(C::kDone));
-      failed = !wait_all(C::kDone, 0) || !ok;
+      if (ok && nt == 1 && n > 0) ok = wait_all(C::kDqFree, (n - 1) & 1);
+      ok = ok && issue_dq(g0 + nt - 1, s_prev, nt == 1);
+      if (ok) tc_commit_if(on, bar(C::kDqDone));
+      g0 += nt;
+      ++n;
     }
-  } else if (warp < 8) {
-    // ---- elementwise: thread <-> (query row, half of a step's columns) ----
-    const int wg = warp >> 2, quarter = warp & 3;
-    const int row = quarter * 32 + lane, iq = q0 + row;
+    if (!ok) {  // leave nothing in flight: an extra phase of a barrier no one else waits for now
+      failed = true;
+      tc_commit_if(on, bar(C::kSDone));
+      wait_all(C::kSDone, 0);
+      wait_all(C::kSDone, 1);
+    }
+  } else if (warp >= 8) {
+    // ---- auxiliary warpgroup, thread <-> query row: Q and dO of the next
+    // item into tensor memory, its LSE and delta, and dQ of the last one out ----
+    const int quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    float* const stat = reinterpret_cast<float*>(gbase + C::kOffStat);
-    auto wait_all = [&](int i, uint32_t parity) {
-      return __all_sync(kFull, wait_phase(bar(i), parity, kWaitLimitNs));
+    const uint8_t* const q_row = gbase + C::kOffQ + row * 128;
+    const uint8_t* const do_row = gbase + C::kOffDo + row * 128;
+    const uint64_t once = l2_policy_evict_first();
+    // 16-byte chunk c of a row of a staged tile
+    auto chunk = [&](const uint8_t* r, int c) {
+      return *reinterpret_cast<const uint4*>(r + (c >> 3) * kAtomBlk + (((c & 7) ^ (row & 7)) << 4));
     };
-    const bool in = iq < p.M;
-    const int64_t off = ((static_cast<int64_t>(b) * p.M + (in ? iq : 0)) * p.H + h) * D;
-    if (wg == 0) {
-      row_to_tmem<D>(lane_addr + C::kColQ, in ? p.Q + off : nullptr);
-    } else {
-      // dO to tensor memory; delta, LSE in base 2
-      float dl = 0.f, l2 = INFINITY;
+    auto load = [&](const DqItem& it) {  // one thread
+      mbar_arrive_expect_tx(bar(C::kStaged), 2 * kBlk * D * 2);
+      for (int a = 0; a < C::kAtoms; ++a)
+        for (int r = 0; r < 2; ++r) {  // rows past M arrive as zeros
+          tma_load_4d(base + C::kOffQ + a * kAtomBlk + r * kAtomStep, &tmQ, bar(C::kStaged), a * 64,
+                      it.h, it.q0 + r * kStep, it.b, once);
+          tma_load_4d(base + C::kOffDo + a * kAtomBlk + r * kAtomStep, &tmDo, bar(C::kStaged),
+                      a * 64, it.h, it.q0 + r * kStep, it.b, once);
+        }
+    };
+    auto out = [&](const DqItem& it, bool zero) {  // dQ rows of an item
+      const int iq = it.q0 + row;
+      const int64_t off = ((static_cast<int64_t>(it.b) * p.M + iq) * p.H + it.h) * D;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t r[32];
+        if (zero) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) r[e] = 0u;
+        } else {
+          tc_ld32(lane_addr + C::kColDq + 32 * c, r);
+          tc_wait_ld();
+          if (c == D / 32 - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::kDqFree));
+          }
+        }
+        if (iq < p.M) store_row32<BF16>(p.dQ, off, 32 * c, p.g32, r, p.scale * Shift<BF16>::kSInv);
+      }
+    };
+    uint32_t n = 0;
+    DqItem last{};
+    uint32_t k = 0;
+    auto next = [&](uint32_t from) {  // the next round with an item that has keys
+      for (; from < rounds; ++from)
+        if (item_of(from) < items && dq_item(p, item_of(from)).nt > 0) break;
+      return from;
+    };
+    uint32_t kn = next(0);
+    if (kn < rounds && threadIdx.x == 8 * 32) load(dq_item(p, item_of(kn)));
+    for (; k < rounds && !failed; ++k) {
+      const uint32_t x = item_of(k);
+      if (x >= items) continue;
+      const DqItem it = dq_item(p, x);
+      const int iq = it.q0 + row;
+      float l2 = INFINITY, dl = 0.f;
+      if (it.nt > 0) {
+        if (!wait_all(C::kStaged, n & 1)) {
+          failed = true;
+          break;
+        }
+        if (iq < p.M) {
+          const int64_t off = ((static_cast<int64_t>(it.b) * p.M + iq) * p.H + it.h) * D;
+          const float l = p.LSE[(static_cast<int64_t>(it.b) * p.H + it.h) * p.M + iq];
+          float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 v = chunk(do_row, c);
+            const uint4 o = reinterpret_cast<const uint4*>(p.O + off)[c];
+            const uint32_t vv[4] = {v.x, v.y, v.z, v.w}, oo[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              acc[e] = fmaf(lo16<BF16>(vv[e]), lo16<BF16>(oo[e]), acc[e]);
+              acc[e] = fmaf(hi16<BF16>(vv[e]), hi16<BF16>(oo[e]), acc[e]);
+            }
+          }
+          if (l != -INFINITY) {  // else: a row without keys
+            l2 = l * 1.4426950408889634f;
+            dl = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+          }
+        }
+        stat[(n & 1) * 2 * kBlk + row] = l2;
+        stat[(n & 1) * 2 * kBlk + kBlk + row] = dl;
+      }
+      if (iq < p.Mp) {  // (a tile without keys: no pair reads them)
+        const int64_t at = (static_cast<int64_t>(it.b) * p.H + it.h) * p.Mp + iq;
+        p.nlse2[at] = Shift<BF16>::kP - l2;
+        p.ndelta[at] = -dl * Shift<BF16>::kSInv;
+      }
+      if (it.nt == 0) {
+        out(it, true);
+        continue;
+      }
+      if (n > 0 && !wait_all(C::kSDone, (n - 1) & 1)) {
+        failed = true;
+        break;
+      }
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
         uint32_t r[32];
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          uint4 v = make_uint4(0, 0, 0, 0), o = v;
-          if (in) {
-            v = reinterpret_cast<const uint4*>(p.dO + off)[8 * c + q];
-            o = reinterpret_cast<const uint4*>(p.O + off)[8 * c + q];
-          }
-          const uint32_t vv[4] = {v.x, v.y, v.z, v.w}, oo[4] = {o.x, o.y, o.z, o.w};
+          const uint4 v = chunk(q_row, 8 * c + q);
+          r[4 * q] = v.x, r[4 * q + 1] = v.y, r[4 * q + 2] = v.z, r[4 * q + 3] = v.w;
+        }
+        tc_st32(lane_addr + C::kColQ + 32 * c, r);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            dl = fmaf(lo16<BF16>(vv[e]), lo16<BF16>(oo[e]), dl);
-            dl = fmaf(hi16<BF16>(vv[e]), hi16<BF16>(oo[e]), dl);
-            r[4 * q + e] = vv[e];
-          }
+        for (int q = 0; q < 8; ++q) {
+          const uint4 v = chunk(do_row, 8 * c + q);
+          r[4 * q] = v.x, r[4 * q + 1] = v.y, r[4 * q + 2] = v.z, r[4 * q + 3] = v.w;
         }
         tc_st32(lane_addr + C::kColDo + 32 * c, r);
       }
-      if (in) {
-        const float l = p.LSE[(static_cast<int64_t>(b) * p.H + h) * p.M + iq];
-        if (l != -INFINITY) l2 = l * 1.4426950408889634f;
-        else dl = 0.f;
-      }
-      stat[row] = l2;
-      stat[kBlk + row] = dl;
-      if (iq < p.Mp) {
-        const int64_t at = (static_cast<int64_t>(b) * p.H + h) * p.Mp + iq;
-        p.nlse2[at] = Shift<BF16>::kP - l2;
-        p.ndelta[at] = -dl * Shift<BF16>::kSInv;
-      }
-    }
-    tc_wait_st();
-    tc_fence_before();
-    mbar_arrive(bar(C::kReady));
-    bar_sync(1, 256);
-    const float neg = -(stat[row] - Shift<BF16>::kS), dl = stat[kBlk + row];
-    const uint64_t sl2_2 = pair(p.sl2, p.sl2), neg_2 = pair(neg, neg), ndl_2 = pair(-dl, -dl);
-    const int lo_i = max(0, iq - p.left), hi_i = min(p.N - 1, iq + p.right);
-    const int in_lo = max(0, q_last - p.left), in_hi = min(p.N - 1, q0 + p.right);
-    for (int i = 0; i < nt; ++i) {
-      if (!wait_all(C::kSFull + (i & 1), (i >> 1) & 1)) {
-        failed = true;
-        break;
-      }
-      tc_fence_after();
-      const uint32_t sa = lane_addr + C::kColS + (i & 1) * kStep + 32 * wg;
-      uint32_t s[32], d[32];
-      tc_ld32(sa, s);
-      tc_ld32(lane_addr + C::kColP + (i & 1) * kStep + 32 * wg, d);
-      tc_wait_ld();
-      const int j0 = (t0 + i) * kStep;
-      uint64_t v[16];
-#pragma unroll
-      for (int c = 0; c < 16; ++c)
-        v[c] = mul2(ex2_2(fma2(pair(s[2 * c], s[2 * c + 1]), sl2_2, neg_2)),
-                    add2(pair(d[2 * c], d[2 * c + 1]), ndl_2));
-      if (j0 < in_lo || j0 + kStep - 1 > in_hi) {  // the same for the whole CTA
-        const int jc = j0 + 32 * wg;
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          float2 f = unpair(v[c]);
-          if (jc + 2 * c < lo_i || jc + 2 * c > hi_i) f.x = 0.f;
-          if (jc + 2 * c + 1 < lo_i || jc + 2 * c + 1 > hi_i) f.y = 0.f;
-          v[c] = pair(f.x, f.y);
-        }
-      }
-      uint32_t w[16];
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const float2 f = unpair(v[c]);
-        w[c] = pack2_t<BF16>(f.x, f.y);
-      }
-      tc_st16(sa, w);
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(C::kDsFull + (i & 1)));
-    }
-    if (!failed) {
-      if (nt > 0 && !wait_all(C::kDone, 0)) failed = true;
-    }
-    if (!failed) {
-      tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        const int col = wg * (D / 2) + 32 * c;
-        uint32_t r[32];
-        if (nt > 0) {
-          tc_ld32(lane_addr + C::kColDq + col, r);
-          tc_wait_ld();
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) r[e] = 0u;
+      if (lane == 0) mbar_arrive(bar(C::kReady));
+      bar_sync(1, 128);  // all four warps have read the staged rows
+      kn = next(k + 1);
+      if (kn < rounds && threadIdx.x == 8 * 32) load(dq_item(p, item_of(kn)));
+      if (n > 0) {
+        if (!wait_all(C::kDqDone, (n - 1) & 1)) {
+          failed = true;
+          break;
         }
-        if (in) store_row32<BF16>(p.dQ, off, col, p.g32, r, p.scale * Shift<BF16>::kSInv);
+        out(last, false);
       }
+      last = it;
+      ++n;
+    }
+    if (!failed && n > 0) {
+      if (wait_all(C::kDqDone, (n - 1) & 1))
+        out(last, false);
+      else
+        failed = true;
+    }
+    if (failed && threadIdx.x == 8 * 32) {  // a load may still be in flight
+      wait_phase(bar(C::kStaged), n & 1, kWaitLimitNs);
+      wait_phase(bar(C::kStaged), (n + 1) & 1, kWaitLimitNs);
+    }
+  } else {
+    // ---- elementwise: thread <-> (query row, half of a step's columns) ----
+    const int wg = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint64_t sl2_2 = pair(p.sl2, p.sl2);
+    uint32_t g0 = 0, n = 0;
+    for (uint32_t k = 0; k < rounds && !failed; ++k) {
+      const uint32_t x = item_of(k);
+      if (x >= items) continue;
+      const DqItem it = dq_item(p, x);
+      if (it.nt == 0) continue;
+      if (!wait_all(C::kReady, n & 1)) {
+        failed = true;
+        break;
+      }
+      const float neg = Shift<BF16>::kS - stat[(n & 1) * 2 * kBlk + row];
+      const float dl = stat[(n & 1) * 2 * kBlk + kBlk + row];
+      const uint64_t neg_2 = pair(neg, neg), ndl_2 = pair(-dl, -dl);
+      const int iq = it.q0 + row;
+      const int lo_i = max(0, iq - p.left), hi_i = min(p.N - 1, iq + p.right);
+      const int in_lo = max(0, it.q_last - p.left), in_hi = min(p.N - 1, it.q0 + p.right);
+      for (int i = 0; i < it.nt; ++i) {
+        const uint32_t g = g0 + i;
+        if (!wait_all(C::kSFull + (g & 1), (g >> 1) & 1)) {
+          failed = true;
+          break;
+        }
+        const uint32_t sa = lane_addr + C::kColS + (g & 1) * kStep + 32 * wg;
+        uint32_t s[32], d[32];
+        tc_ld32(sa, s);
+        tc_ld32(lane_addr + C::kColP + (g & 1) * kStep + 32 * wg, d);
+        tc_wait_ld();
+        const int j0 = (it.t0 + i) * kStep;
+        uint64_t v[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+          v[c] = mul2(ex2_2(fma2(pair(s[2 * c], s[2 * c + 1]), sl2_2, neg_2)),
+                      add2(pair(d[2 * c], d[2 * c + 1]), ndl_2));
+        if (j0 < in_lo || j0 + kStep - 1 > in_hi) {  // the same for the whole CTA
+          const int jc = j0 + 32 * wg;
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            float2 f = unpair(v[c]);
+            if (jc + 2 * c < lo_i || jc + 2 * c > hi_i) f.x = 0.f;
+            if (jc + 2 * c + 1 < lo_i || jc + 2 * c + 1 > hi_i) f.y = 0.f;
+            v[c] = pair(f.x, f.y);
+          }
+        }
+        uint32_t w[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const float2 f = unpair(v[c]);
+          w[c] = pack2_t<BF16>(f.x, f.y);
+        }
+        tc_st16(sa, w);
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::kDsFull + (g & 1)));
+      }
+      g0 += it.nt;
+      ++n;
     }
   }
 
   if (failed) report_timeout();
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 13) {
     __syncwarp();
     tc_fence_after();
     tc_dealloc(tmem, kTmemAll);
@@ -859,7 +1011,9 @@ int launch_swa_bwd(const SwaBwdProblem& p, cudaStream_t st) {
     return NSA_ERR_LAUNCH;
   const int64_t qi = static_cast<int64_t>(p.B) * p.H * p.qtiles;
   const int64_t ki = static_cast<int64_t>(p.B) * p.Hkv * p.ktiles * p.splits;
-  dq<<<static_cast<unsigned>(qi), kThreads, DqCfg<D>::kSmem, st>>>(p, tk, tv);
+  // one CTA per SM, items dealt to them
+  dq<<<static_cast<unsigned>(qi < kSms ? qi : kSms), kDqThreads, DqCfg<D>::kSmem, st>>>(p, tk, tv,
+                                                                                       tq, td);
   if (cudaGetLastError() != cudaSuccess) return NSA_ERR_LAUNCH;
   dkv<<<static_cast<unsigned>(ki), kThreads, DkvCfg<D>::kSmem, st>>>(p, tq, td);
   if (cudaGetLastError() != cudaSuccess) return NSA_ERR_LAUNCH;
@@ -946,6 +1100,7 @@ extern "C" int nsa_swa_bwd(const void* Q, const void* K, const void* V, const vo
   p.qtiles = static_cast<int>((M + kBlk - 1) / kBlk);
   p.ktiles = static_cast<int>((N + kBlk - 1) / kBlk);
   p.splits = swa_bwd_splits(B, M, N, H, H_kv, w.left, w.right);
+  p.dq_items = static_cast<int>(B * H * p.qtiles);
   p.left = static_cast<int>(w.left);
   p.right = static_cast<int>(w.right);
   p.scale = scale > 0.f ? scale : 1.0f / sqrtf(static_cast<float>(D));
