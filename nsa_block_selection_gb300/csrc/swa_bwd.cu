@@ -87,6 +87,7 @@ struct SwaBwdProblem {
   int left, right;  // clamped to [0, M] and [0, N]: unbounded in effect
   float sl2, scale;
   bool g32;  // gradients fp32 instead of the inputs' type
+  bool wide;  // gradients (and parts) 32-byte aligned
 };
 
 __device__ __forceinline__ void bar_sync(int id, int threads) {
@@ -128,6 +129,28 @@ __device__ __forceinline__ uint64_t ex2_2(uint64_t x) {
   return pair(ex2(v.x), ex2(v.y));
 }
 
+// Bit c set: column c of 32 lies in [lo, hi].
+__device__ __forceinline__ uint32_t seen_bits(int lo, int hi) {
+  const uint32_t below = hi < 0 ? 0u : hi >= 31 ? ~0u : (2u << hi) - 1u;
+  return lo <= 0 ? below : lo > 31 ? 0u : below & (~0u << lo);
+}
+
+// Zeroes the 16-bit entries of 32 columns whose bit is clear, whatever they
+// hold: four bits at a time are multiplied onto the sign bits of a word's
+// bytes, and byte permutes that repeat those signs make the masks. (A compare
+// and a select for every entry took 650 clocks a step longer.)
+__device__ __forceinline__ void keep_seen(uint32_t (&w)[16], uint32_t bits) {
+#pragma unroll
+  for (int g = 0; g < 8; ++g) {
+    const uint32_t y = ((bits >> (4 * g)) & 0xfu) * 0x10204080u;
+    uint32_t a, b;
+    asm("prmt.b32 %0, %1, 0, 0x9988;\n" : "=r"(a) : "r"(y));
+    asm("prmt.b32 %0, %1, 0, 0xbbaa;\n" : "=r"(b) : "r"(y));
+    w[2 * g] &= a;
+    w[2 * g + 1] &= b;
+  }
+}
+
 template <bool BF16>
 __device__ __forceinline__ float lo16(uint32_t v) {
   if constexpr (BF16) return __uint_as_float(v << 16);
@@ -156,27 +179,43 @@ __device__ __forceinline__ void row_to_tmem(uint32_t taddr, const uint16_t* row)
   }
 }
 
-// 32 fp32 columns times `f`, stored from column `col` of a row of gradients.
+// 32 fp32 columns times `f`, stored from column `col` of a row of gradients;
+// wide: 32-byte stores (whole sectors, half the instructions).
+__device__ __forceinline__ void store_words(void* dst, const uint32_t* w, int words, bool wide) {
+#pragma unroll
+  for (int q = 0; q < words / 8; ++q) {
+    uint32_t* const d = static_cast<uint32_t*>(dst) + 8 * q;
+    const uint32_t* const x = w + 8 * q;
+    if (wide) {
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(d), "r"(x[0]),
+                   "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                   : "memory");
+    } else {
+      reinterpret_cast<uint4*>(d)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+      reinterpret_cast<uint4*>(d)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+    }
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void pack32(uint32_t* w, const uint32_t* r, float f) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    w[e] = pack2_t<BF16>(__uint_as_float(r[2 * e]) * f, __uint_as_float(r[2 * e + 1]) * f);
+}
+
 template <bool BF16>
 __device__ __forceinline__ void store_row32(void* base, int64_t row_off, int col, bool g32,
-                                            const uint32_t* r, float f) {
+                                            const uint32_t* r, float f, bool wide) {
   if (g32) {
-    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(base) + row_off + col);
+    uint32_t w[32];
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-      dst[q] = make_float4(__uint_as_float(r[4 * q]) * f, __uint_as_float(r[4 * q + 1]) * f,
-                           __uint_as_float(r[4 * q + 2]) * f, __uint_as_float(r[4 * q + 3]) * f);
+    for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+    store_words(static_cast<float*>(base) + row_off + col, w, 32, wide);
   } else {
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + row_off + col);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        w[e] = pack2_t<BF16>(__uint_as_float(r[8 * q + 2 * e]) * f,
-                             __uint_as_float(r[8 * q + 2 * e + 1]) * f);
-      dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+    uint32_t w[16];
+    pack32<BF16>(w, r, f);
+    store_words(static_cast<uint16_t*>(base) + row_off + col, w, 16, wide);
   }
 }
 
@@ -187,12 +226,13 @@ struct DqCfg {
   static constexpr int kAtoms = D / 64;
   static constexpr int kTile = kStep * D * 2;      // one K or V tile
   static constexpr int kStages = D == 128 ? 4 : 6;
-  static constexpr int kOffQ = kStages * 2 * kTile;      // the next item's Q and dO
+  static constexpr int kOffQ = kStages * 2 * kTile;      // the next item's O, then its Q; dO
   static constexpr int kOffDo = kOffQ + kBlk * D * 2;
   static constexpr int kOffStat = kOffDo + kBlk * D * 2;  // 2 x (LSE in base 2, delta) of the rows
   static constexpr int kOffBar = kOffStat + 4 * kBlk * 4;
-  static constexpr int kFull = 0, kEmpty = kStages, kStaged = 2 * kStages, kReady = kStaged + 1,
-                       kSDone = kReady + 1, kSFull = kSDone + 1, kDsFull = kSFull + 2,
+  static constexpr int kFull = 0, kEmpty = kStages, kOStaged = 2 * kStages, kQStaged = kOStaged + 1,
+                       kQReady = kQStaged + 1, kDoReady = kQReady + 1, kSDone = kDoReady + 1,
+                       kDpDone = kSDone + 1, kSFull = kDpDone + 1, kDsFull = kSFull + 2,
                        kDqDone = kDsFull + 2, kDqFree = kDqDone + 1, kNumBars = kDqFree + 1;
   static constexpr int kOffTmem = kOffBar + kNumBars * 8;
   static constexpr int kSmem = kOffTmem + 16 + 1024;
@@ -234,6 +274,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     swa_bwd_dq_kernel(const SwaBwdProblem p, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CUtensorMap tmQ,
+                      const __grid_constant__ CUtensorMap tmO,
                       const __grid_constant__ CUtensorMap tmDo) {
   using C = DqCfg<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -247,9 +288,12 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       mbar_init(bar(C::kFull + s), 1);
       mbar_init(bar(C::kEmpty + s), 1);
     }
-    mbar_init(bar(C::kStaged), 1);
-    mbar_init(bar(C::kReady), 4);
+    mbar_init(bar(C::kOStaged), 1);
+    mbar_init(bar(C::kQStaged), 1);
+    mbar_init(bar(C::kQReady), 4);
+    mbar_init(bar(C::kDoReady), 4);
     mbar_init(bar(C::kSDone), 1);
+    mbar_init(bar(C::kDpDone), 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(C::kSFull + s), 1);
       mbar_init(bar(C::kDsFull + s), 8);
@@ -323,21 +367,27 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       }
     }
   } else if (warp == 13) {
-    // ---- MMA issuer (the whole warp, one lane elected): S_i, dP_i, dQ_{i-1} ----
+    // ---- MMA issuer (the whole warp, one lane elected): S_g, dP_g, dQ_{g-1},
+    // the steps of all items as one stream ----
     constexpr uint32_t id_s = umma_idesc_f16(kBlk, kStep, BF16, false);
     constexpr uint32_t id_q = umma_idesc_f16(kBlk, D, BF16, true);
     const uint32_t on = elect_one();
     int s = 0, s_prev = 0;
-    uint32_t ph = 0, g0 = 0, n = 0;
-    auto issue_dq = [&](uint32_t g, int stage, bool start) -> bool {
-      if (!wait_all(C::kDsFull + (g & 1), (g >> 1) & 1)) return false;
-      const uint32_t ds = tmem + C::kColS + (g & 1) * kStep;
-      const uint32_t kb = base + stage * 2 * C::kTile;
+    uint32_t ph = 0, g = 0, n = 0;
+    bool start = false, last = false;  // dQ_{g-1} is its item's first, last
+    uint32_t n_prev = 0;               // and its item
+    auto issue_dq = [&](uint32_t gq) -> bool {
+      // (an item's first dQ overwrites the item's before)
+      if (start && n_prev > 0 && !wait_all(C::kDqFree, (n_prev - 1) & 1)) return false;
+      if (!wait_all(C::kDsFull + (gq & 1), (gq >> 1) & 1)) return false;
+      const uint32_t ds = tmem + C::kColS + (gq & 1) * kStep;
+      const uint32_t kb = base + s_prev * 2 * C::kTile;
 #pragma unroll
       for (int kk = 0; kk < kStep / 16; ++kk)  // dS of keys 0..31 at column 0, 32..63 at 32
         tc_mma_ts_if(on, tmem + C::kColDq, ds + (kk >> 1) * 32 + (kk & 1) * 8,
                      umma_desc_sw128(kb + kk * 2048, kAtomStep), id_q, (!start || kk > 0) ? 1u : 0u);
-      tc_commit_if(on, bar(C::kEmpty + stage));
+      tc_commit_if(on, bar(C::kEmpty + s_prev));
+      if (last) tc_commit_if(on, bar(C::kDqDone));
       return true;
     };
     bool ok = true;
@@ -345,11 +395,9 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       const uint32_t x = item_of(k);
       if (x >= items) continue;
       const int nt = dq_item(p, x).nt;
-      if (nt == 0) continue;
-      ok = wait_all(C::kReady, n & 1);
-      for (int i = 0; i < nt && ok; ++i) {
-        const uint32_t g = g0 + i;
-        ok = wait_all(C::kFull + s, ph);
+      for (int i = 0; i < nt && ok; ++i, ++g) {
+        if (i == 0) ok = wait_all(C::kQReady, n & 1);
+        ok = ok && wait_all(C::kFull + s, ph);
         if (!ok) break;
         const uint32_t kb = base + s * 2 * C::kTile, vb = kb + C::kTile;
 #pragma unroll
@@ -357,119 +405,137 @@ __global__ void __launch_bounds__(kDqThreads, 1)
           tc_mma_ts_if(on, tmem + C::kColS + (g & 1) * kStep, tmem + C::kColQ + 8 * kk,
                        umma_desc_sw128(kb + (kk >> 2) * kAtomStep + (kk & 3) * 32, 16), id_s,
                        kk > 0 ? 1u : 0u);
+        if (i == nt - 1) tc_commit_if(on, bar(C::kSDone));  // Q has been read
+        if (i == 0) ok = wait_all(C::kDoReady, n & 1);
+        if (!ok) break;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           tc_mma_ts_if(on, tmem + C::kColP + (g & 1) * kStep, tmem + C::kColDo + 8 * kk,
                        umma_desc_sw128(vb + (kk >> 2) * kAtomStep + (kk & 3) * 32, 16), id_s,
                        kk > 0 ? 1u : 0u);
         tc_commit_if(on, bar(C::kSFull + (g & 1)));
-        if (i == nt - 1) tc_commit_if(on, bar(C::kSDone));  // Q and dO have been read
-        if (i > 0) {
-          // (the item's first dQ overwrites the last item's)
-          if (i == 1 && n > 0) ok = wait_all(C::kDqFree, (n - 1) & 1);
-          ok = ok && issue_dq(g - 1, s_prev, i == 1);
-        }
+        if (i == nt - 1) tc_commit_if(on, bar(C::kDpDone));
+        if (g > 0) ok = issue_dq(g - 1);
+        start = i == 0;
+        last = i == nt - 1;
+        n_prev = n;
         s_prev = s;
         if (++s == C::kStages) {
           s = 0;
           ph ^= 1;
         }
       }
-      if (ok && nt == 1 && n > 0) ok = wait_all(C::kDqFree, (n - 1) & 1);
-      ok = ok && issue_dq(g0 + nt - 1, s_prev, nt == 1);
-      if (ok) tc_commit_if(on, bar(C::kDqDone));
-      g0 += nt;
-      ++n;
+      if (nt > 0) ++n;
     }
-    if (!ok) {  // leave nothing in flight: an extra phase of a barrier no one else waits for now
+    if (ok && g > 0) ok = issue_dq(g - 1);
+    if (!ok) {  // leave nothing in flight: one more phase of a barrier
       failed = true;
       tc_commit_if(on, bar(C::kSDone));
       wait_all(C::kSDone, 0);
       wait_all(C::kSDone, 1);
     }
   } else if (warp >= 8) {
-    // ---- auxiliary warpgroup, thread <-> query row: Q and dO of the next
-    // item into tensor memory, its LSE and delta, and dQ of the last one out ----
+    // ---- auxiliary warpgroup, thread <-> query row: delta and LSE of the
+    // next item, its Q and dO into tensor memory, and dQ of the last one out.
+    // O and dO are staged while an item runs, delta is formed, Q follows in
+    // O's place; Q moves once the item's last S, dO once its last dP is done. ----
     const int quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint8_t* const q_row = gbase + C::kOffQ + row * 128;
     const uint8_t* const do_row = gbase + C::kOffDo + row * 128;
+    const bool leader = threadIdx.x == 8 * 32;
     const uint64_t once = l2_policy_evict_first();
     // 16-byte chunk c of a row of a staged tile
     auto chunk = [&](const uint8_t* r, int c) {
       return *reinterpret_cast<const uint4*>(r + (c >> 3) * kAtomBlk + (((c & 7) ^ (row & 7)) << 4));
     };
-    auto load = [&](const DqItem& it) {  // one thread
-      mbar_arrive_expect_tx(bar(C::kStaged), 2 * kBlk * D * 2);
+    auto load = [&](const CUtensorMap* tm, int off, int b, const DqItem& it) {
       for (int a = 0; a < C::kAtoms; ++a)
-        for (int r = 0; r < 2; ++r) {  // rows past M arrive as zeros
-          tma_load_4d(base + C::kOffQ + a * kAtomBlk + r * kAtomStep, &tmQ, bar(C::kStaged), a * 64,
-                      it.h, it.q0 + r * kStep, it.b, once);
-          tma_load_4d(base + C::kOffDo + a * kAtomBlk + r * kAtomStep, &tmDo, bar(C::kStaged),
-                      a * 64, it.h, it.q0 + r * kStep, it.b, once);
-        }
+        for (int r = 0; r < 2; ++r)  // rows past M arrive as zeros
+          tma_load_4d(base + off + a * kAtomBlk + r * kAtomStep, tm, bar(b), a * 64, it.h,
+                      it.q0 + r * kStep, it.b, once);
     };
+    auto load_o = [&](const DqItem& it) {  // one thread
+      mbar_arrive_expect_tx(bar(C::kOStaged), 2 * kBlk * D * 2);
+      load(&tmO, C::kOffQ, C::kOStaged, it);
+      load(&tmDo, C::kOffDo, C::kOStaged, it);
+    };
+    const float f_out = p.scale * Shift<BF16>::kSInv;
     auto out = [&](const DqItem& it, bool zero) {  // dQ rows of an item
       const int iq = it.q0 + row;
       const int64_t off = ((static_cast<int64_t>(it.b) * p.M + iq) * p.H + it.h) * D;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t r[32];
+      auto column = [&](int c, uint32_t (&r)[32]) {
         if (zero) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) r[e] = 0u;
-        } else {
-          tc_ld32(lane_addr + C::kColDq + 32 * c, r);
-          tc_wait_ld();
-          if (c == D / 32 - 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(C::kDqFree));
-          }
+          return;
         }
-        if (iq < p.M) store_row32<BF16>(p.dQ, off, 32 * c, p.g32, r, p.scale * Shift<BF16>::kSInv);
+        tc_ld32(lane_addr + C::kColDq + 32 * c, r);
+        tc_wait_ld();
+        if (c == D / 32 - 1) {  // the next item may start its dQ
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::kDqFree));
+        }
+      };
+      uint32_t r[32];
+      if (p.g32) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          column(c, r);
+          if (iq < p.M) store_row32<BF16>(p.dQ, off, 32 * c, true, r, f_out, p.wide);
+        }
+      } else {  // everything out of tensor memory first
+        uint32_t w[D / 2];
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          column(c, r);
+          pack32<BF16>(w + 16 * c, r, f_out);
+        }
+        if (iq < p.M) store_words(static_cast<uint16_t*>(p.dQ) + off, w, D / 2, p.wide);
       }
     };
     uint32_t n = 0;
     DqItem last{};
-    uint32_t k = 0;
     auto next = [&](uint32_t from) {  // the next round with an item that has keys
       for (; from < rounds; ++from)
         if (item_of(from) < items && dq_item(p, item_of(from)).nt > 0) break;
       return from;
     };
     uint32_t kn = next(0);
-    if (kn < rounds && threadIdx.x == 8 * 32) load(dq_item(p, item_of(kn)));
-    for (; k < rounds && !failed; ++k) {
+    if (kn < rounds && leader) load_o(dq_item(p, item_of(kn)));
+    for (uint32_t k = 0; k < rounds && !failed; ++k) {
       const uint32_t x = item_of(k);
       if (x >= items) continue;
       const DqItem it = dq_item(p, x);
       const int iq = it.q0 + row;
       float l2 = INFINITY, dl = 0.f;
       if (it.nt > 0) {
-        if (!wait_all(C::kStaged, n & 1)) {
+        const float l = iq < p.M ? p.LSE[(static_cast<int64_t>(it.b) * p.H + it.h) * p.M + iq]
+                                 : -INFINITY;
+        if (!wait_all(C::kOStaged, n & 1)) {
           failed = true;
           break;
         }
-        if (iq < p.M) {
-          const int64_t off = ((static_cast<int64_t>(it.b) * p.M + iq) * p.H + it.h) * D;
-          const float l = p.LSE[(static_cast<int64_t>(it.b) * p.H + it.h) * p.M + iq];
-          float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 v = chunk(do_row, c);
-            const uint4 o = reinterpret_cast<const uint4*>(p.O + off)[c];
-            const uint32_t vv[4] = {v.x, v.y, v.z, v.w}, oo[4] = {o.x, o.y, o.z, o.w};
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = chunk(do_row, c), o = chunk(q_row, c);
+          const uint32_t vv[4] = {v.x, v.y, v.z, v.w}, oo[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              acc[e] = fmaf(lo16<BF16>(vv[e]), lo16<BF16>(oo[e]), acc[e]);
-              acc[e] = fmaf(hi16<BF16>(vv[e]), hi16<BF16>(oo[e]), acc[e]);
-            }
+          for (int e = 0; e < 4; ++e) {
+            acc[e] = fmaf(lo16<BF16>(vv[e]), lo16<BF16>(oo[e]), acc[e]);
+            acc[e] = fmaf(hi16<BF16>(vv[e]), hi16<BF16>(oo[e]), acc[e]);
           }
-          if (l != -INFINITY) {  // else: a row without keys
-            l2 = l * 1.4426950408889634f;
-            dl = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-          }
+        }
+        bar_sync(1, 128);  // every row of O has been read
+        if (leader) {
+          mbar_arrive_expect_tx(bar(C::kQStaged), kBlk * D * 2);
+          load(&tmQ, C::kOffQ, C::kQStaged, it);
+        }
+        if (l != -INFINITY) {  // else: a row without keys
+          l2 = l * 1.4426950408889634f;
+          dl = (acc[0] + acc[1]) + (acc[2] + acc[3]);
         }
         stat[(n & 1) * 2 * kBlk + row] = l2;
         stat[(n & 1) * 2 * kBlk + kBlk + row] = dl;
@@ -483,33 +549,32 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         out(it, true);
         continue;
       }
-      if (n > 0 && !wait_all(C::kSDone, (n - 1) & 1)) {
+      // a staged row into tensor memory; the barrier tells the MMA warp
+      auto move = [&](const uint8_t* src, uint32_t col, int done, int ready) -> bool {
+        uint32_t r[D / 2];
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = chunk(src, c);
+          r[4 * c] = v.x, r[4 * c + 1] = v.y, r[4 * c + 2] = v.z, r[4 * c + 3] = v.w;
+        }
+        if (n > 0 && !wait_all(done, (n - 1) & 1)) return false;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          tc_st32(lane_addr + col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&r[32 * c]));
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(ready));
+        return true;
+      };
+      if (!wait_all(C::kQStaged, n & 1) || !move(q_row, C::kColQ, C::kSDone, C::kQReady) ||
+          !move(do_row, C::kColDo, C::kDpDone, C::kDoReady)) {
         failed = true;
         break;
       }
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        uint32_t r[32];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const uint4 v = chunk(q_row, 8 * c + q);
-          r[4 * q] = v.x, r[4 * q + 1] = v.y, r[4 * q + 2] = v.z, r[4 * q + 3] = v.w;
-        }
-        tc_st32(lane_addr + C::kColQ + 32 * c, r);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const uint4 v = chunk(do_row, 8 * c + q);
-          r[4 * q] = v.x, r[4 * q + 1] = v.y, r[4 * q + 2] = v.z, r[4 * q + 3] = v.w;
-        }
-        tc_st32(lane_addr + C::kColDo + 32 * c, r);
-      }
-      tc_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(C::kReady));
       bar_sync(1, 128);  // all four warps have read the staged rows
       kn = next(k + 1);
-      if (kn < rounds && threadIdx.x == 8 * 32) load(dq_item(p, item_of(kn)));
+      if (kn < rounds && leader) load_o(dq_item(p, item_of(kn)));
       if (n > 0) {
         if (!wait_all(C::kDqDone, (n - 1) & 1)) {
           failed = true;
@@ -526,9 +591,11 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       else
         failed = true;
     }
-    if (failed && threadIdx.x == 8 * 32) {  // a load may still be in flight
-      wait_phase(bar(C::kStaged), n & 1, kWaitLimitNs);
-      wait_phase(bar(C::kStaged), (n + 1) & 1, kWaitLimitNs);
+    if (failed && leader) {  // a load may still be in flight
+      wait_phase(bar(C::kOStaged), 0, kWaitLimitNs);
+      wait_phase(bar(C::kOStaged), 1, kWaitLimitNs);
+      wait_phase(bar(C::kQStaged), 0, kWaitLimitNs);
+      wait_phase(bar(C::kQStaged), 1, kWaitLimitNs);
     }
   } else {
     // ---- elementwise: thread <-> (query row, half of a step's columns) ----
@@ -541,7 +608,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       if (x >= items) continue;
       const DqItem it = dq_item(p, x);
       if (it.nt == 0) continue;
-      if (!wait_all(C::kReady, n & 1)) {
+      if (!wait_all(C::kDoReady, n & 1)) {
         failed = true;
         break;
       }
@@ -568,22 +635,14 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         for (int c = 0; c < 16; ++c)
           v[c] = mul2(ex2_2(fma2(pair(s[2 * c], s[2 * c + 1]), sl2_2, neg_2)),
                       add2(pair(d[2 * c], d[2 * c + 1]), ndl_2));
-        if (j0 < in_lo || j0 + kStep - 1 > in_hi) {  // the same for the whole CTA
-          const int jc = j0 + 32 * wg;
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            float2 f = unpair(v[c]);
-            if (jc + 2 * c < lo_i || jc + 2 * c > hi_i) f.x = 0.f;
-            if (jc + 2 * c + 1 < lo_i || jc + 2 * c + 1 > hi_i) f.y = 0.f;
-            v[c] = pair(f.x, f.y);
-          }
-        }
         uint32_t w[16];
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
           const float2 f = unpair(v[c]);
           w[c] = pack2_t<BF16>(f.x, f.y);
         }
+        if (j0 < in_lo || j0 + kStep - 1 > in_hi)  // the same for the whole CTA
+          keep_seen(w, seen_bits(lo_i - j0 - 32 * wg, hi_i - j0 - 32 * wg));
         tc_st16(sa, w);
         tc_wait_st();
         tc_fence_before();
@@ -829,6 +888,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < 8; ++c) nl[c] = nl2[c];
       const bool edge =
           j0 < i0 + kStep - 1 - p.left || j0 + kBlk - 1 > i0 + p.right || i0 + kStep > p.M;
+      const uint32_t seen = edge ? seen_bits(lo_j - ic, hi_j - ic) : 0u;
       uint32_t s[32];
       uint64_t pr[16];
       if (!wait_all(C::kSFull + 2 * wg + (n & 1), (n >> 1) & 1)) {
@@ -843,15 +903,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         pr[2 * c] = ex2_2(fma2(pair(s[4 * c], s[4 * c + 1]), sl2_2, nl[c].x));
         pr[2 * c + 1] = ex2_2(fma2(pair(s[4 * c + 2], s[4 * c + 3]), sl2_2, nl[c].y));
       }
-      auto hide = [&]() {
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          float2 f = unpair(pr[c]);
-          if (ic + 2 * c < lo_j || ic + 2 * c > hi_j) f.x = 0.f;
-          if (ic + 2 * c + 1 < lo_j || ic + 2 * c + 1 > hi_j) f.y = 0.f;
-          pr[c] = pair(f.x, f.y);
-        }
-      };
       auto pack = [&](uint32_t (&w)[16]) {
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
@@ -859,9 +910,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           w[c] = pack2_t<BF16>(f.x, f.y);
         }
       };
-      if (edge) hide();
       uint32_t w[16];
       pack(w);
+      if (edge) keep_seen(w, seen);
       tc_st16(sa, w);
       tc_wait_st();
       tc_fence_before();
@@ -881,8 +932,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         pr[2 * c] = mul2(pr[2 * c], BF16 ? add2(x, d.x) : fma2(x, shift_2, d.x));
         pr[2 * c + 1] = mul2(pr[2 * c + 1], BF16 ? add2(y, d.y) : fma2(y, shift_2, d.y));
       }
-      if (edge) hide();  // again: 0 times an infinite dP of a hidden pair is not 0
       pack(w);
+      if (edge) keep_seen(w, seen);
       tc_st16(da, w);
       tc_wait_st();
       tc_fence_before();
@@ -911,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) r[e] = 0u;
         }
-        if (in) store_row32<BF16>(dst, off, 32 * c, f32, r, f);
+        if (in) store_row32<BF16>(dst, off, 32 * c, f32, r, f, p.wide);
       }
     }
   }
@@ -996,10 +1047,11 @@ template <int D, bool BF16>
 int launch_swa_bwd(const SwaBwdProblem& p, cudaStream_t st) {
   constexpr CUtensorMapDataType dt =
       BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  CUtensorMap tk, tv, tq, td;
+  CUtensorMap tk, tv, tq, td, to;
   if (!encode_kv_map(&tk, p.K, p.B, p.N, p.Hkv, D, kStep, dt) ||
       !encode_kv_map(&tv, p.V, p.B, p.N, p.Hkv, D, kStep, dt) ||
       !encode_kv_map(&tq, p.Q, p.B, p.M, p.H, D, kStep, dt) ||
+      !encode_kv_map(&to, p.O, p.B, p.M, p.H, D, kStep, dt) ||
       !encode_kv_map(&td, p.dO, p.B, p.M, p.H, D, kStep, dt))
     return NSA_ERR_LAUNCH;
   auto dq = swa_bwd_dq_kernel<D, BF16>;
@@ -1013,7 +1065,7 @@ int launch_swa_bwd(const SwaBwdProblem& p, cudaStream_t st) {
   const int64_t ki = static_cast<int64_t>(p.B) * p.Hkv * p.ktiles * p.splits;
   // one CTA per SM, items dealt to them
   dq<<<static_cast<unsigned>(qi < kSms ? qi : kSms), kDqThreads, DqCfg<D>::kSmem, st>>>(p, tk, tv,
-                                                                                       tq, td);
+                                                                                       tq, to, td);
   if (cudaGetLastError() != cudaSuccess) return NSA_ERR_LAUNCH;
   dkv<<<static_cast<unsigned>(ki), kThreads, DkvCfg<D>::kSmem, st>>>(p, tq, td);
   if (cudaGetLastError() != cudaSuccess) return NSA_ERR_LAUNCH;
@@ -1106,6 +1158,7 @@ extern "C" int nsa_swa_bwd(const void* Q, const void* K, const void* V, const vo
   p.scale = scale > 0.f ? scale : 1.0f / sqrtf(static_cast<float>(D));
   p.sl2 = p.scale * 1.4426950408889634f;
   p.g32 = grad_dtype == NSA_F32;
+  p.wide = !mis(dQ, 32) && !mis(dK, 32) && !mis(dV, 32) && !mis(workspace, 32);
   const int64_t stat = B * H * p.Mp;
   p.nlse2 = static_cast<float*>(workspace);
   p.ndelta = p.nlse2 + stat;
