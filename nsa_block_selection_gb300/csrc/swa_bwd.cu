@@ -94,6 +94,14 @@ __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
 }
 
+// A matrix descriptor moved by `bytes`: the address field takes the sum as
+// it is (shared memory ends below its 2^18 bytes), and an addition leaves the
+// issuing warp less to do per MMA than building the descriptor again.
+__device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) {
+  const uint32_t lo = static_cast<uint32_t>(desc) + (bytes >> 4);
+  return (desc & 0xffffffff00000000ull) | lo;
+}
+
 // Two fp32 operations an instruction.
 __device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
   uint64_t r;
@@ -374,6 +382,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     const uint32_t on = elect_one();
     int s = 0, s_prev = 0;
     uint32_t ph = 0, g = 0, n = 0;
+    const uint64_t k_major = umma_desc_sw128(base, 16);
+    const uint64_t mn_major = umma_desc_sw128(base, kAtomStep);
     bool start = false, last = false;  // dQ_{g-1} is its item's first, last
     uint32_t n_prev = 0;               // and its item
     auto issue_dq = [&](uint32_t gq) -> bool {
@@ -381,11 +391,11 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       if (start && n_prev > 0 && !wait_all(C::kDqFree, (n_prev - 1) & 1)) return false;
       if (!wait_all(C::kDsFull + (gq & 1), (gq >> 1) & 1)) return false;
       const uint32_t ds = tmem + C::kColS + (gq & 1) * kStep;
-      const uint32_t kb = base + s_prev * 2 * C::kTile;
+      const uint64_t kd = desc_at(mn_major, s_prev * 2 * C::kTile);
 #pragma unroll
       for (int kk = 0; kk < kStep / 16; ++kk)  // dS of keys 0..31 at column 0, 32..63 at 32
         tc_mma_ts_if(on, tmem + C::kColDq, ds + (kk >> 1) * 32 + (kk & 1) * 8,
-                     umma_desc_sw128(kb + kk * 2048, kAtomStep), id_q, (!start || kk > 0) ? 1u : 0u);
+                     desc_at(kd, kk * 2048), id_q, (!start || kk > 0) ? 1u : 0u);
       tc_commit_if(on, bar(C::kEmpty + s_prev));
       if (last) tc_commit_if(on, bar(C::kDqDone));
       return true;
@@ -399,20 +409,18 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         if (i == 0) ok = wait_all(C::kQReady, n & 1);
         ok = ok && wait_all(C::kFull + s, ph);
         if (!ok) break;
-        const uint32_t kb = base + s * 2 * C::kTile, vb = kb + C::kTile;
+        const uint64_t kd = desc_at(k_major, s * 2 * C::kTile), vd = desc_at(kd, C::kTile);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           tc_mma_ts_if(on, tmem + C::kColS + (g & 1) * kStep, tmem + C::kColQ + 8 * kk,
-                       umma_desc_sw128(kb + (kk >> 2) * kAtomStep + (kk & 3) * 32, 16), id_s,
-                       kk > 0 ? 1u : 0u);
+                       desc_at(kd, (kk >> 2) * kAtomStep + (kk & 3) * 32), id_s, kk > 0 ? 1u : 0u);
         if (i == nt - 1) tc_commit_if(on, bar(C::kSDone));  // Q has been read
         if (i == 0) ok = wait_all(C::kDoReady, n & 1);
         if (!ok) break;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           tc_mma_ts_if(on, tmem + C::kColP + (g & 1) * kStep, tmem + C::kColDo + 8 * kk,
-                       umma_desc_sw128(vb + (kk >> 2) * kAtomStep + (kk & 3) * 32, 16), id_s,
-                       kk > 0 ? 1u : 0u);
+                       desc_at(vd, (kk >> 2) * kAtomStep + (kk & 3) * 32), id_s, kk > 0 ? 1u : 0u);
         tc_commit_if(on, bar(C::kSFull + (g & 1)));
         if (i == nt - 1) tc_commit_if(on, bar(C::kDpDone));
         if (g > 0) ok = issue_dq(g - 1);
@@ -799,23 +807,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto slot = [&](int n, int w) {
         return s_col + (C::kBuf == 2 ? (n & 1) * kStep : 0) + w * kHalf;
       };
-      auto half = [&](int stage, int w) {
-        return base + stage * C::kStagePitch + w * (kHalf * 128);
-      };
+      auto half = [&](int stage, int w) { return stage * C::kStagePitch + w * (kHalf * 128); };
+      const uint64_t k_major = umma_desc_sw128(base + s_tile, 16);
+      const uint64_t mn_major = umma_desc_sw128(base + d_tile, kAtomStep);
       auto form = [&](int n, int w, int stage) {
-        const uint32_t b0 = half(stage, w) + s_tile, d = slot(n, w);
+        const uint64_t b0 = desc_at(k_major, half(stage, w));
+        const uint32_t d = slot(n, w);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           tc_mma_ts_if(on, d, a_col + 8 * kk,
-                       umma_desc_sw128(b0 + (kk >> 2) * kAtomStep + (kk & 3) * 32, 16), id_s,
-                       kk > 0 ? 1u : 0u);
+                       desc_at(b0, (kk >> 2) * kAtomStep + (kk & 3) * 32), id_s, kk > 0 ? 1u : 0u);
         tc_commit_if(on, bar(s_bar + 2 * w + (n & 1)));
       };
       auto add = [&](int n, int w, int stage) {
-        const uint32_t b0 = half(stage, w) + d_tile, a = slot(n, w);
+        const uint64_t b0 = desc_at(mn_major, half(stage, w));
+        const uint32_t a = slot(n, w);
 #pragma unroll
         for (int kk = 0; kk < kHalf / 16; ++kk)
-          tc_mma_ts_if(on, d_col, a + 8 * kk, umma_desc_sw128(b0 + kk * 2048, kAtomStep), id_d,
+          tc_mma_ts_if(on, d_col, a + 8 * kk, desc_at(b0, kk * 2048), id_d,
                        (n > 0 || w > 0 || kk > 0) ? 1u : 0u);
       };
       int st = 0, sl = 0;  // stages of the steps n and n + kBuf
