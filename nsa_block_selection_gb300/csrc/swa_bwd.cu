@@ -837,10 +837,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         form(n, 1, sl);
         ++sl;
       }
-      if (ok && nt > C::kBuf) ok = wait_all(C::kFull + sl, ph);
       for (int n = 0; n < nt && ok; ++n) {
         const int m = n + C::kBuf;
-        ok = wait_all(p_bar + (n & 1), (n >> 1) & 1);
+        // P (dS) of the first half and the tiles of step m: one question for
+        // both, as a wait that is over still takes some 100 clocks
+        const int pb = p_bar + (n & 1), fb = m < nt ? C::kFull + sl : pb;
+        const uint32_t pp = (n >> 1) & 1, fp = m < nt ? ph : pp;
+        const bool x1 = mbar_try_wait(bar(pb), pp), x2 = mbar_try_wait(bar(fb), fp);
+        if (__all_sync(kFull, x1 && x2))
+          tc_fence_after();
+        else
+          ok = wait_all(pb, pp) && wait_all(fb, fp);
         if (!ok) break;
         add(n, 0, st);
         if (m < nt) form(m, 0, sl);
@@ -854,7 +861,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           sl = 0;
           ph ^= 1;
         }
-        if (m + 1 < nt) ok = wait_all(C::kFull + sl, ph);  // ahead of the wait for P (dS)
       }
       tc_commit_if(on, bar(C::kDone));
       failed = !wait_all(C::kDone, 0) || !ok;
