@@ -57,7 +57,7 @@ namespace {
 constexpr int kBlk = 128;       // queries (dQ) or keys (dK, dV) of a CTA: the M of its products
 constexpr int kStep = 64;       // keys (dQ) or queries (dK, dV) of a step
 constexpr int kHalf = kStep / 2;  // queries of a step that one warpgroup takes
-constexpr int kThreads = 352;   // 8 elementwise warps, the TMA warp, two MMA warps
+constexpr int kDkvThreads = 480;  // 8 elementwise and 4 auxiliary warps, the TMA warp, two MMA warps
 constexpr int kDqThreads = 448;  // 8 elementwise and 4 auxiliary warps, the TMA warp, the MMA warp
 constexpr int kAtomStep = kStep * 128;  // bytes of 64 rows x 64 entries
 constexpr int kAtomBlk = kBlk * 128;
@@ -81,9 +81,10 @@ struct SwaBwdProblem {
   void *dQ, *dK, *dV;
   float* nlse2;   // [B, H, Mp]: Shift::kP - LSE log2 e; -inf for rows without keys
   float* ndelta;  // [B, H, Mp]: -delta 2^(kS - kP)
-  float* part;   // [splits, 2, B, N, Hkv, D], or NULL
+  float* part;   // [parts, 2 (dK, dV), kBlk, D], or NULL
   int B, M, N, H, Hkv, hpg, Mp, qtiles, ktiles, splits;
-  int dq_items;  // B H qtiles
+  int dq_items;               // B H qtiles
+  int whole_tiles, dkv_items;  // key tiles that are not cut, and all items of the dK, dV kernel
   int left, right;  // clamped to [0, M] and [0, N]: unbounded in effect
   float sl2, scale;
   bool g32;  // gradients fp32 instead of the inputs' type
@@ -168,23 +169,6 @@ template <bool BF16>
 __device__ __forceinline__ float hi16(uint32_t v) {
   if constexpr (BF16) return __uint_as_float(v & 0xffff0000u);
   return __half2float(__ushort_as_half(static_cast<unsigned short>(v >> 16)));
-}
-
-// Row of D 16-bit entries -> this thread's lane of tensor memory (two entries
-// a column: an A operand). NULL: a row of zeros.
-template <int D>
-__device__ __forceinline__ void row_to_tmem(uint32_t taddr, const uint16_t* row) {
-#pragma unroll
-  for (int c = 0; c < D / 64; ++c) {
-    uint32_t r[32];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (row != nullptr) v = reinterpret_cast<const uint4*>(row)[8 * c + q];
-      r[4 * q] = v.x, r[4 * q + 1] = v.y, r[4 * q + 2] = v.z, r[4 * q + 3] = v.w;
-    }
-    tc_st32(taddr + 32 * c, r);
-  }
 }
 
 // 32 fp32 columns times `f`, stored from column `col` of a row of gradients;
@@ -680,12 +664,23 @@ struct DkvCfg {
   static constexpr int kTile = kStep * D * 2;      // one Q or dO tile
   static constexpr int kStage = 2 * kTile + 2 * kStep * 4;  // and the nlse2, ndelta of its queries
   static constexpr int kStagePitch = (kStage + 1023) / 1024 * 1024;
-  static constexpr int kStages = D == 128 ? 6 : 8;
+  static constexpr int kStages = D == 128 ? 4 : 6;
   static constexpr int kBuf = D == 128 ? 1 : 2;  // buffers of S and of dP
-  static constexpr int kOffBar = kStages * kStagePitch;
-  static constexpr int kFull = 0, kEmpty = kStages, kReady = 2 * kStages, kSFull = kReady + 1,
-                       kPFull = kSFull + 4, kDpFull = kPFull + 4, kDsFull = kDpFull + 4,
-                       kDone = kDsFull + 4, kNumBars = kDone + 1;
+  // Groups of a step: at D = 128, with one buffer, each warpgroup's 32 queries
+  // are a group of their own, so that one's products run during the other's
+  // exponentials (16k, window (4096, 0): 2.41 ms against 2.65). At D = 64 the
+  // products are half as long, there are two buffers, and the waits of twice
+  // the groups cost more than they hide.
+  static constexpr int kGroups = D == 128 ? 2 : 1;
+  static constexpr int kCols = kStep / kGroups;
+  static constexpr int kOffK = kStages * kStagePitch;  // the next item's K and V
+  static constexpr int kOffV = kOffK + kBlk * D * 2;
+  static constexpr int kOffBar = kOffV + kBlk * D * 2;
+  static constexpr int kFull = 0, kEmpty = kStages, kStaged = 2 * kStages, kKReady = kStaged + 1,
+                       kVReady = kKReady + 1, kSDone = kVReady + 1, kDpDone = kSDone + 1,
+                       kDvDone = kDpDone + 1, kDkDone = kDvDone + 1, kDvFree = kDkDone + 1,
+                       kDkFree = kDvFree + 1, kSFull = kDkFree + 1, kPFull = kSFull + 4,
+                       kDpFull = kPFull + 4, kDsFull = kDpFull + 4, kNumBars = kDsFull + 4;
   static constexpr int kOffTmem = kOffBar + kNumBars * 8;
   static constexpr int kSmem = kOffTmem + 16 + 1024;
   static_assert(kSmem <= 232448 && kSmem > 118784, "one CTA per SM");
@@ -694,10 +689,56 @@ struct DkvCfg {
   static_assert(3 * D + 2 * kBuf * kStep <= 512, "tensor memory");
 };
 
+// One item of the dK, dV kernel: 128 keys of a KV head, and the steps of its
+// query heads and query blocks of 64 that see them (numbered head after
+// head), or a part of those steps.
+struct DkvItem {
+  int b, g, j0, u0, nq;   // u0, nq: first block of queries and their number, for each head
+  int h, u, nt;           // first head and block of the item, and its steps
+  int part;               // its place among the parts, or -1
+};
+
+// Tiles in order of falling work (as far as the window's sides tell), the
+// (batch, KV head) pairs fastest: neighbouring tiles, which read the same
+// queries, run at the same time. The last tiles are cut into parts.
+__device__ __forceinline__ DkvItem dkv_item(const SwaBwdProblem& p, uint32_t x) {
+  DkvItem it;
+  uint32_t tile = x, sp = 0;
+  it.part = -1;
+  if (x >= static_cast<uint32_t>(p.whole_tiles)) {
+    it.part = static_cast<int>(x) - p.whole_tiles;
+    tile = p.whole_tiles + static_cast<uint32_t>(it.part) / static_cast<uint32_t>(p.splits);
+    sp = static_cast<uint32_t>(it.part) % static_cast<uint32_t>(p.splits);
+  }
+  const uint32_t pairs = static_cast<uint32_t>(p.B * p.Hkv);
+  const uint32_t bg = tile % pairs;
+  int kt = static_cast<int>(tile / pairs);
+  if (p.right > p.left) kt = p.ktiles - 1 - kt;
+  it.g = static_cast<int>(bg % static_cast<uint32_t>(p.Hkv));
+  it.b = static_cast<int>(bg / static_cast<uint32_t>(p.Hkv));
+  it.j0 = kt * kBlk;
+  const int j_last = min(it.j0 + kBlk, p.N) - 1;
+  const int ilo = max(0, it.j0 - p.right), ihi = min(p.M - 1, j_last + p.left);
+  it.u0 = ilo / kStep;
+  it.nq = ihi >= ilo ? ihi / kStep - it.u0 + 1 : 0;
+  const int all = it.nq * p.hpg;  // at most 2^31 (checked on the host)
+  int first = 0;
+  it.nt = all;
+  if (it.part >= 0) {
+    first = static_cast<int>(static_cast<int64_t>(all) * sp / p.splits);
+    it.nt = static_cast<int>(static_cast<int64_t>(all) * (sp + 1) / p.splits) - first;
+  }
+  it.h = it.g * p.hpg + (it.nq > 0 ? first / it.nq : 0);
+  it.u = it.nq > 0 ? first % it.nq : 0;
+  return it;
+}
+
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kDkvThreads, 1)
     swa_bwd_dkv_kernel(const SwaBwdProblem p, const __grid_constant__ CUtensorMap tmQ,
-                       const __grid_constant__ CUtensorMap tmDo) {
+                       const __grid_constant__ CUtensorMap tmDo,
+                       const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV) {
   using C = DkvCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -710,17 +751,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(C::kFull + s), 1);
       mbar_init(bar(C::kEmpty + s), 2);
     }
-    mbar_init(bar(C::kReady), 256);
+    mbar_init(bar(C::kStaged), 1);
+    mbar_init(bar(C::kKReady), 4);
+    mbar_init(bar(C::kVReady), 4);
+    mbar_init(bar(C::kSDone), 1);
+    mbar_init(bar(C::kDpDone), 1);
+    mbar_init(bar(C::kDvDone), 1);
+    mbar_init(bar(C::kDkDone), 1);
+    mbar_init(bar(C::kDvFree), 4);
+    mbar_init(bar(C::kDkFree), 4);
     for (int s = 0; s < 4; ++s) {
       mbar_init(bar(C::kSFull + s), 1);
-      mbar_init(bar(C::kPFull + s), 4);
+      mbar_init(bar(C::kPFull + s), 8 / C::kGroups);
       mbar_init(bar(C::kDpFull + s), 1);
-      mbar_init(bar(C::kDsFull + s), 4);
+      mbar_init(bar(C::kDsFull + s), 8 / C::kGroups);
     }
-    mbar_init(bar(C::kDone), 2);
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == 13) {
     tc_alloc(base + C::kOffTmem, kTmemAll);
     tc_relinquish();
   }
@@ -728,256 +776,405 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + C::kOffTmem);
-
-  // the CTA's item: (b, KV head, key tile, part), and its steps, numbered
-  // head after head over the query steps that see the tile
-  uint32_t x = blockIdx.x;
-  const int sp = static_cast<int>(x % static_cast<uint32_t>(p.splits));
-  x /= static_cast<uint32_t>(p.splits);
-  const int kt = static_cast<int>(x % static_cast<uint32_t>(p.ktiles));
-  x /= static_cast<uint32_t>(p.ktiles);
-  const int g = static_cast<int>(x % static_cast<uint32_t>(p.Hkv));
-  const int b = static_cast<int>(x / static_cast<uint32_t>(p.Hkv));
-  const int j0 = kt * kBlk, j_last = min(j0 + kBlk, p.N) - 1;
-  const int ilo = max(0, j0 - p.right), ihi = min(p.M - 1, j_last + p.left);
-  const int u0 = ilo / kStep, nq = ihi >= ilo ? ihi / kStep - u0 + 1 : 0;
-  const int64_t all = static_cast<int64_t>(nq) * p.hpg;
-  const int64_t first = all * sp / p.splits;
-  const int nt = static_cast<int>(all * (sp + 1) / p.splits - first);
-  const int h_first = nq > 0 ? g * p.hpg + static_cast<int>(first / nq) : 0;
-  const int u_first = nq > 0 ? static_cast<int>(first % nq) : 0;
   bool failed = false;
+  auto wait_all = [&](int i, uint32_t parity) {
+    const bool r = __all_sync(kFull, wait_phase(bar(i), parity, kWaitLimitNs));
+    tc_fence_after();
+    return r;
+  };
+  const uint32_t items = static_cast<uint32_t>(p.dkv_items);
+  const uint32_t rounds = (items + gridDim.x - 1) / gridDim.x;
+  auto item_of = [&](uint32_t k) {  // dealt in snake order, as in the dQ kernel
+    return k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  };
+  auto next = [&](uint32_t from) {  // the next round with an item that has steps
+    for (; from < rounds; ++from)
+      if (item_of(from) < items && dkv_item(p, item_of(from)).nt > 0) break;
+    return from;
+  };
 
-  if (warp == 8) {
-    if (lane == 0 && nt > 0) {
-      // ---- TMA producer ----
+  if (warp == 12) {
+    if (lane == 0) {
+      // ---- TMA producer: Q and dO of 64 queries, their nlse2 and ndelta ----
       tma_prefetch_desc(&tmQ);
       tma_prefetch_desc(&tmDo);
       const uint64_t keep = l2_policy_evict_last();
-      int h = h_first, u = u_first, n = 0;
-      for (; n < nt; ++n) {
-        const int s = n % C::kStages;
-        if (n >= C::kStages &&
-            !wait_phase(bar(C::kEmpty + s), (n / C::kStages - 1) & 1, kWaitLimitNs)) {
+      int s = 0, in_flight = 0;
+      uint32_t ph = 1;  // of the wait for an empty stage: the first round passes
+      for (uint32_t k = next(0); k < rounds && !failed; k = next(k + 1)) {
+        const DkvItem it = dkv_item(p, item_of(k));
+        int h = it.h, u = it.u;
+        for (int n = 0; n < it.nt; ++n) {
+          if (!wait_phase(bar(C::kEmpty + s), ph, kWaitLimitNs)) {
+            failed = true;
+            break;
+          }
+          const uint32_t full = bar(C::kFull + s), dst = base + s * C::kStagePitch;
+          const int i0 = (it.u0 + u) * kStep;
+          mbar_arrive_expect_tx(full, C::kStage);
+          for (int a = 0; a < C::kAtoms; ++a) {
+            tma_load_4d(dst + a * kAtomStep, &tmQ, full, a * 64, h, i0, it.b, keep);
+            tma_load_4d(dst + C::kTile + a * kAtomStep, &tmDo, full, a * 64, h, i0, it.b, keep);
+          }
+          const int64_t at = (static_cast<int64_t>(it.b) * p.H + h) * p.Mp + i0;
+          bulk_load(dst + 2 * C::kTile, p.nlse2 + at, kStep * 4, full);
+          bulk_load(dst + 2 * C::kTile + kStep * 4, p.ndelta + at, kStep * 4, full);
+          if (++u == it.nq) {
+            u = 0;
+            ++h;
+          }
+          if (in_flight < C::kStages) ++in_flight;
+          if (++s == C::kStages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      if (failed) {  // leave nothing in flight: the last loads of the stages before s
+        for (int k = 0; k < in_flight; ++k) {
+          s = s == 0 ? C::kStages - 1 : s - 1;
+          if (s == C::kStages - 1) ph ^= 1;
+          wait_phase(bar(C::kFull + s), ph ^ 1, kWaitLimitNs);
+        }
+      }
+    }
+  } else if (warp == 13 || warp == 14) {
+    // ---- MMA issuers (a whole warp each, one lane elected). Warp 13 forms S
+    // and dV, warp 14 dP and dK: P overwrites its S and dS its dP, so the
+    // two share no tensor memory, each accumulator is added to in one
+    // order, and one warp's waits pass while the other's products run.
+    // With two groups, group w of a step (queries 32 w .. 32 w + 31) belongs to
+    // warpgroup w.
+    // The steps of all items are one stream: S (dP) is formed kBuf steps ahead. ----
+    constexpr uint32_t id_s = umma_idesc_f16(kBlk, C::kCols, BF16, false);
+    constexpr uint32_t id_d = umma_idesc_f16(kBlk, D, BF16, true);
+    const uint32_t on = elect_one();
+    const bool is_v = warp == 13;
+    const uint32_t a_col = tmem + (is_v ? C::kColK : C::kColV);
+    const uint32_t s_col = tmem + (is_v ? C::kColS : C::kColP);
+    const uint32_t d_col = tmem + (is_v ? C::kColDv : C::kColDk);
+    // in a stage: the tile that forms S (dP), and the one dV (dK) sums over
+    const uint64_t k_major = umma_desc_sw128(base + (is_v ? 0 : C::kTile), 16);
+    const uint64_t mn_major = umma_desc_sw128(base + (is_v ? C::kTile : 0), kAtomStep);
+    const int s_bar = is_v ? C::kSFull : C::kDpFull, p_bar = is_v ? C::kPFull : C::kDsFull;
+    const int a_ready = is_v ? C::kKReady : C::kVReady, a_done = is_v ? C::kSDone : C::kDpDone;
+    const int d_done = is_v ? C::kDvDone : C::kDkDone, d_free = is_v ? C::kDvFree : C::kDkFree;
+    auto slot = [&](uint32_t n, int w) {
+      return s_col + (C::kBuf == 2 ? (n & 1) * kStep : 0) + w * C::kCols;
+    };
+    auto rows_of = [&](int stage, int w) { return stage * C::kStagePitch + w * (C::kCols * 128); };
+    auto form = [&](uint32_t n, int w, int stage) {
+      const uint64_t b0 = desc_at(k_major, rows_of(stage, w));
+      const uint32_t d = slot(n, w);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        tc_mma_ts_if(on, d, a_col + 8 * kk, desc_at(b0, (kk >> 2) * kAtomStep + (kk & 3) * 32), id_s,
+                     kk > 0 ? 1u : 0u);
+      tc_commit_if(on, bar(s_bar + 2 * w + (n & 1)));
+    };
+    auto add = [&](uint32_t n, int w, int stage, bool start) {
+      const uint64_t b0 = desc_at(mn_major, rows_of(stage, w));
+      const uint32_t a = slot(n, w);
+#pragma unroll
+      for (int kk = 0; kk < C::kCols / 16; ++kk)  // P, dS: queries 0..31 at column 0, 32..63 at 32
+        tc_mma_ts_if(on, d_col, a + (kk >> 1) * 32 + (kk & 1) * 8, desc_at(b0, kk * 2048), id_d,
+                     (!start || kk > 0) ? 1u : 0u);
+    };
+    // n, st: the step that is added and its stage; sl, ph: stage and phase of
+    // the step that is formed; na: the item's number
+    uint32_t n = 0, na = 0, ph = 0;
+    int st = 0, sl = 0;
+    auto next_stage = [&]() {
+      if (++sl == C::kStages) {
+        sl = 0;
+        ph ^= 1;
+      }
+    };
+    // P (dS) of the first half of step n and, if `more`, the tiles of the step
+    // that is formed: one question for both, as a wait that is over still
+    // takes some 100 clocks
+    auto wait_first = [&](bool more) -> bool {
+      const int pb = p_bar + (n & 1), fb = more ? C::kFull + sl : pb;
+      const uint32_t pp = (n >> 1) & 1, fp = more ? ph : pp;
+      const bool x1 = mbar_try_wait(bar(pb), pp), x2 = mbar_try_wait(bar(fb), fp);
+      if (__all_sync(kFull, x1 && x2)) {
+        tc_fence_after();
+        return true;
+      }
+      return wait_all(pb, pp) && wait_all(fb, fp);
+    };
+    auto added = [&]() {
+      tc_commit_if(on, bar(C::kEmpty + st));
+      if (++st == C::kStages) st = 0;
+      ++n;
+    };
+    bool ok = true;
+    uint32_t k = next(0);
+    int nt = k < rounds ? dkv_item(p, item_of(k)).nt : 0;
+    int ahead = 0;  // steps of the item that are formed already
+    for (; nt > 0 && ok; ++na) {
+      const uint32_t k2 = next(k + 1);
+      const int nt2 = k2 < rounds ? dkv_item(p, item_of(k2)).nt : 0;
+      if (ahead == 0) ok = wait_all(a_ready, na & 1);
+      for (; ahead < C::kBuf && ahead < nt && ok; ++ahead) {
+        ok = wait_all(C::kFull + sl, ph);
+        if (!ok) break;
+#pragma unroll
+        for (int w = 0; w < C::kGroups; ++w) form(n + ahead, w, sl);
+        if (ahead + 1 == nt) tc_commit_if(on, bar(a_done));
+        next_stage();
+      }
+      int i = 0;
+      for (; i + C::kBuf < nt && ok; ++i) {
+        ok = wait_first(true);
+        // (an item's first product overwrites the accumulator of the item before)
+        if (i == 0 && na > 0) ok = ok && wait_all(d_free, (na - 1) & 1);
+        if (!ok) break;
+        const uint32_t m = n + C::kBuf;
+        add(n, 0, st, i == 0);
+        form(m, 0, sl);
+        if constexpr (C::kGroups == 2) {
+          ok = wait_all(p_bar + 2 + (n & 1), (n >> 1) & 1);
+          if (!ok) break;
+          add(n, 1, st, false);
+          form(m, 1, sl);
+        }
+        if (i + C::kBuf + 1 == nt) tc_commit_if(on, bar(a_done));
+        next_stage();
+        added();
+      }
+      // the item's last steps; each is followed by a first step of the next
+      // item, whose K (V) may have to wait for sums to be read out: nothing
+      // of this step comes after it
+      ahead = 0;
+      for (; i < nt && ok; ++i) {
+        ok = wait_first(false);
+        if (i == 0 && na > 0) ok = ok && wait_all(d_free, (na - 1) & 1);
+        if (!ok) break;
+        add(n, 0, st, i == 0);
+        if constexpr (C::kGroups == 2) {
+          ok = wait_all(p_bar + 2 + (n & 1), (n >> 1) & 1);
+          if (!ok) break;
+          add(n, 1, st, false);
+        }
+        added();
+        if (i + 1 == nt) tc_commit_if(on, bar(d_done));
+        if (ahead < C::kBuf && ahead < nt2) {
+          if (ahead == 0) ok = wait_all(a_ready, (na + 1) & 1);
+          ok = ok && wait_all(C::kFull + sl, ph);
+          if (!ok) break;
+          const uint32_t m = n + (nt - 1 - i) + ahead;  // (n is the step after this one)
+#pragma unroll
+          for (int w = 0; w < C::kGroups; ++w) form(m, w, sl);
+          if (ahead + 1 == nt2) tc_commit_if(on, bar(a_done));
+          next_stage();
+          ++ahead;
+        }
+      }
+      k = k2;
+      nt = nt2;
+    }
+    if (!ok) {  // leave nothing in flight: one more phase of a barrier
+      failed = true;
+      tc_commit_if(on, bar(a_done));
+      wait_all(a_done, 0);
+      wait_all(a_done, 1);
+    }
+  } else if (warp >= 8 && warp < 12) {
+    // ---- auxiliary warpgroup, thread <-> key row: K and V of the next item
+    // into tensor memory (K once the item's last S, V once its last dP is
+    // done), dV and dK of the last one out ----
+    const int quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const bool leader = warp == 8 && lane == 0;
+    const uint64_t once = l2_policy_evict_first();
+    auto load = [&](const DkvItem& it) {  // one thread
+      mbar_arrive_expect_tx(bar(C::kStaged), 2 * kBlk * D * 2);
+      for (int a = 0; a < C::kAtoms; ++a)
+        for (int r = 0; r < 2; ++r) {  // rows past N arrive as zeros
+          tma_load_4d(base + C::kOffK + a * kAtomBlk + r * kAtomStep, &tmK, bar(C::kStaged), a * 64,
+                      it.g, it.j0 + r * kStep, it.b, once);
+          tma_load_4d(base + C::kOffV + a * kAtomBlk + r * kAtomStep, &tmV, bar(C::kStaged), a * 64,
+                      it.g, it.j0 + r * kStep, it.b, once);
+        }
+    };
+    // one accumulator's rows out; is_v: dV
+    auto out = [&](const DkvItem& it, bool is_v, bool zero) {
+      const int j = it.j0 + row;
+      const float f = is_v ? Shift<BF16>::kPInv : p.scale * Shift<BF16>::kSInv;
+      void* dst = is_v ? p.dV : p.dK;
+      int64_t off = ((static_cast<int64_t>(it.b) * p.N + j) * p.Hkv + it.g) * D;
+      bool f32 = p.g32;
+      if (it.part >= 0) {
+        dst = p.part;
+        off = ((static_cast<int64_t>(it.part) * 2 + (is_v ? 1 : 0)) * kBlk + row) * D;
+        f32 = true;
+      }
+      auto column = [&](int c, uint32_t (&r)[32]) {
+        if (zero) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) r[e] = 0u;
+          return;
+        }
+        tc_ld32(lane_addr + (is_v ? C::kColDv : C::kColDk) + 32 * c, r);
+        tc_wait_ld();
+        if (c == D / 32 - 1) {  // the next item may start
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(is_v ? C::kDvFree : C::kDkFree));
+        }
+      };
+      uint32_t r[32];
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        column(c, r);
+        if (j < p.N) store_row32<BF16>(dst, off, 32 * c, f32, r, f, p.wide);
+      }
+    };
+    uint32_t n = 0;
+    DkvItem last{};
+    auto out_last = [&]() -> bool {
+      if (!wait_all(C::kDvDone, (n - 1) & 1)) return false;
+      out(last, true, false);
+      if (!wait_all(C::kDkDone, (n - 1) & 1)) return false;
+      out(last, false, false);
+      return true;
+    };
+    uint32_t kn = next(0);
+    if (kn < rounds && leader) load(dkv_item(p, item_of(kn)));
+    for (uint32_t k = 0; k < rounds && !failed; ++k) {
+      const uint32_t x = item_of(k);
+      if (x >= items) continue;
+      const DkvItem it = dkv_item(p, x);
+      if (it.nt == 0) {  // no query sees the keys
+        out(it, true, true);
+        out(it, false, true);
+        continue;
+      }
+      // a staged row into tensor memory; the barrier tells the MMA warp
+      auto move = [&](int off, uint32_t col, int done, int ready) -> bool {
+        const uint8_t* const src = gbase + off + row * 128;
+        uint32_t r[D / 2];
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = *reinterpret_cast<const uint4*>(src + (c >> 3) * kAtomBlk +
+                                                          (((c & 7) ^ (row & 7)) << 4));
+          r[4 * c] = v.x, r[4 * c + 1] = v.y, r[4 * c + 2] = v.z, r[4 * c + 3] = v.w;
+        }
+        if (n > 0 && !wait_all(done, (n - 1) & 1)) return false;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          tc_st32(lane_addr + col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&r[32 * c]));
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(ready));
+        return true;
+      };
+      if (!wait_all(C::kStaged, n & 1) || !move(C::kOffK, C::kColK, C::kSDone, C::kKReady) ||
+          !move(C::kOffV, C::kColV, C::kDpDone, C::kVReady)) {
+        failed = true;
+        break;
+      }
+      bar_sync(1, 128);  // all four warps have read the staged rows
+      kn = next(k + 1);
+      if (kn < rounds && leader) load(dkv_item(p, item_of(kn)));
+      if (n > 0 && !out_last()) {
+        failed = true;
+        break;
+      }
+      last = it;
+      ++n;
+    }
+    if (!failed && n > 0 && !out_last()) failed = true;
+    if (failed && leader) {  // a load may still be in flight
+      wait_phase(bar(C::kStaged), 0, kWaitLimitNs);
+      wait_phase(bar(C::kStaged), 1, kWaitLimitNs);
+    }
+  } else if (warp < 8) {
+    // ---- elementwise: thread <-> (key row, half of a step's queries) ----
+    const int wg = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const int gb = C::kGroups == 2 ? 2 * wg : 0;  // its group's barriers
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint64_t sl2_2 = pair(p.sl2, p.sl2);
+    const uint64_t shift_2 = pair(Shift<BF16>::kSInv, Shift<BF16>::kSInv);
+    uint32_t n = 0, ph = 0;
+    int st = 0;
+    for (uint32_t k = next(0); k < rounds && !failed; k = next(k + 1)) {
+      const DkvItem it = dkv_item(p, item_of(k));
+      const int j = it.j0 + row;
+      const int lo_j = j - p.right, hi_j = min(j + p.left, p.M - 1);  // the queries that see key j
+      int u = it.u;
+      for (int t = 0; t < it.nt; ++t, ++n) {
+        const int i0 = (it.u0 + u) * kStep, ic = i0 + kHalf * wg;
+        if (++u == it.nq) u = 0;
+        // The stage's nlse2 and ndelta first, while S is being formed: a wait
+        // costs some 100 clocks even when it is over, and S is on the chain.
+        if (!wait_all(C::kFull + st, ph)) {
           failed = true;
           break;
         }
-        const uint32_t full = bar(C::kFull + s), dst = base + s * C::kStagePitch;
-        const int i0 = (u0 + u) * kStep;
-        mbar_arrive_expect_tx(full, C::kStage);
-        for (int a = 0; a < C::kAtoms; ++a) {
-          tma_load_4d(dst + a * kAtomStep, &tmQ, full, a * 64, h, i0, b, keep);
-          tma_load_4d(dst + C::kTile + a * kAtomStep, &tmDo, full, a * 64, h, i0, b, keep);
-        }
-        const int64_t at = (static_cast<int64_t>(b) * p.H + h) * p.Mp + i0;
-        bulk_load(dst + 2 * C::kTile, p.nlse2 + at, kStep * 4, full);
-        bulk_load(dst + 2 * C::kTile + kStep * 4, p.ndelta + at, kStep * 4, full);
-        if (++u == nq) {
-          u = 0;
-          ++h;
-        }
-      }
-      if (failed) {  // leave nothing in flight
-        for (int k = max(0, n - C::kStages); k < n; ++k)
-          wait_phase(bar(C::kFull + k % C::kStages), (k / C::kStages) & 1, kWaitLimitNs);
-      }
-    }
-  } else if (warp >= 9) {
-    if (nt > 0) {
-      // ---- MMA issuers (a whole warp each, one lane elected). Warp 9 forms S
-      // and dV, warp 10 dP and dK: P overwrites its S and dS its dP, so the
-      // two share no tensor memory, each accumulator is added to in one
-      // order, and one warp's waits pass while the other's products run.
-      // Half w of a step (queries 32 w .. 32 w + 31) belongs to warpgroup w. ----
-      constexpr uint32_t id_s = umma_idesc_f16(kBlk, kHalf, BF16, false);
-      constexpr uint32_t id_d = umma_idesc_f16(kBlk, D, BF16, true);
-      const uint32_t on = elect_one();
-      auto wait_all = [&](int i, uint32_t parity) {
-        const bool r = __all_sync(kFull, wait_phase(bar(i), parity, kWaitLimitNs));
-        tc_fence_after();
-        return r;
-      };
-      const bool is_v = warp == 9;
-      const uint32_t a_col = tmem + (is_v ? C::kColK : C::kColV);
-      const uint32_t s_col = tmem + (is_v ? C::kColS : C::kColP);
-      const uint32_t d_col = tmem + (is_v ? C::kColDv : C::kColDk);
-      // in a stage: the tile that forms S (dP), and the one dV (dK) sums over
-      const uint32_t s_tile = is_v ? 0 : C::kTile, d_tile = is_v ? C::kTile : 0;
-      const int s_bar = is_v ? C::kSFull : C::kDpFull, p_bar = is_v ? C::kPFull : C::kDsFull;
-      auto slot = [&](int n, int w) {
-        return s_col + (C::kBuf == 2 ? (n & 1) * kStep : 0) + w * kHalf;
-      };
-      auto half = [&](int stage, int w) { return stage * C::kStagePitch + w * (kHalf * 128); };
-      const uint64_t k_major = umma_desc_sw128(base + s_tile, 16);
-      const uint64_t mn_major = umma_desc_sw128(base + d_tile, kAtomStep);
-      auto form = [&](int n, int w, int stage) {
-        const uint64_t b0 = desc_at(k_major, half(stage, w));
-        const uint32_t d = slot(n, w);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          tc_mma_ts_if(on, d, a_col + 8 * kk,
-                       desc_at(b0, (kk >> 2) * kAtomStep + (kk & 3) * 32), id_s, kk > 0 ? 1u : 0u);
-        tc_commit_if(on, bar(s_bar + 2 * w + (n & 1)));
-      };
-      auto add = [&](int n, int w, int stage) {
-        const uint64_t b0 = desc_at(mn_major, half(stage, w));
-        const uint32_t a = slot(n, w);
-#pragma unroll
-        for (int kk = 0; kk < kHalf / 16; ++kk)
-          tc_mma_ts_if(on, d_col, a + 8 * kk, desc_at(b0, kk * 2048), id_d,
-                       (n > 0 || w > 0 || kk > 0) ? 1u : 0u);
-      };
-      int st = 0, sl = 0;  // stages of the steps n and n + kBuf
-      uint32_t ph = 0;
-      bool ok = wait_all(C::kReady, 0);
-      for (int n = 0; n < C::kBuf && n < nt && ok; ++n) {
-        ok = wait_all(C::kFull + sl, ph);
-        if (!ok) break;
-        form(n, 0, sl);
-        form(n, 1, sl);
-        ++sl;
-      }
-      for (int n = 0; n < nt && ok; ++n) {
-        const int m = n + C::kBuf;
-        // P (dS) of the first half and the tiles of step m: one question for
-        // both, as a wait that is over still takes some 100 clocks
-        const int pb = p_bar + (n & 1), fb = m < nt ? C::kFull + sl : pb;
-        const uint32_t pp = (n >> 1) & 1, fp = m < nt ? ph : pp;
-        const bool x1 = mbar_try_wait(bar(pb), pp), x2 = mbar_try_wait(bar(fb), fp);
-        if (__all_sync(kFull, x1 && x2))
-          tc_fence_after();
-        else
-          ok = wait_all(pb, pp) && wait_all(fb, fp);
-        if (!ok) break;
-        add(n, 0, st);
-        if (m < nt) form(m, 0, sl);
-        ok = wait_all(p_bar + 2 + (n & 1), (n >> 1) & 1);
-        if (!ok) break;
-        add(n, 1, st);
-        tc_commit_if(on, bar(C::kEmpty + st));
-        if (m < nt) form(m, 1, sl);
-        if (++st == C::kStages) st = 0;
-        if (++sl == C::kStages) {
-          sl = 0;
+        const uint32_t sa =
+            lane_addr + C::kColS + (C::kBuf == 2 ? (n & 1) * kStep : 0) + kHalf * wg;
+        const uint32_t da = sa + C::kBuf * kStep;
+        const ulonglong2* nl2 = reinterpret_cast<const ulonglong2*>(
+            gbase + st * C::kStagePitch + 2 * C::kTile + kHalf * wg * 4);
+        const ulonglong2* ndl = nl2 + kStep / 4;
+        if (++st == C::kStages) {
+          st = 0;
           ph ^= 1;
         }
-      }
-      tc_commit_if(on, bar(C::kDone));
-      failed = !wait_all(C::kDone, 0) || !ok;
-    }
-  } else {
-    // ---- elementwise: thread <-> (key row, half of a step's queries) ----
-    const int wg = warp >> 2, quarter = warp & 3;
-    const int row = quarter * 32 + lane, j = j0 + row;
-    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    auto wait_all = [&](int i, uint32_t parity) {
-      return __all_sync(kFull, wait_phase(bar(i), parity, kWaitLimitNs));
-    };
-    const bool in = j < p.N;
-    const int64_t off = ((static_cast<int64_t>(b) * p.N + (in ? j : 0)) * p.Hkv + g) * D;
-    const uint16_t* const kv = wg == 0 ? p.K : p.V;
-    row_to_tmem<D>(lane_addr + (wg == 0 ? C::kColK : C::kColV), in ? kv + off : nullptr);
-    tc_wait_st();
-    tc_fence_before();
-    mbar_arrive(bar(C::kReady));
-    const int lo_j = j - p.right, hi_j = min(j + p.left, p.M - 1);  // the queries that see key j
-    const uint64_t sl2_2 = pair(p.sl2, p.sl2);
-    const uint64_t shift_2 = pair(Shift<BF16>::kSInv, Shift<BF16>::kSInv);
-    int u = u_first;
-    for (int n = 0; n < nt; ++n) {
-      const int i0 = (u0 + u) * kStep, ic = i0 + 32 * wg;
-      if (++u == nq) u = 0;
-      // The stage's nlse2 and ndelta first, while S is being formed: a wait
-      // costs some 100 clocks even when it is over, and S is on the chain.
-      if (!wait_all(C::kFull + n % C::kStages, (n / C::kStages) & 1)) {
-        failed = true;
-        break;
-      }
-      const uint32_t sa = lane_addr + C::kColS + (C::kBuf == 2 ? (n & 1) * kStep : 0) + 32 * wg;
-      const uint32_t da = sa + C::kBuf * kStep;
-      const ulonglong2* nl2 = reinterpret_cast<const ulonglong2*>(
-          gbase + (n % C::kStages) * C::kStagePitch + 2 * C::kTile + 32 * wg * 4);
-      const ulonglong2* ndl = nl2 + kStep / 4;
-      ulonglong2 nl[8];
-#pragma unroll
-      for (int c = 0; c < 8; ++c) nl[c] = nl2[c];
-      const bool edge =
-          j0 < i0 + kStep - 1 - p.left || j0 + kBlk - 1 > i0 + p.right || i0 + kStep > p.M;
-      const uint32_t seen = edge ? seen_bits(lo_j - ic, hi_j - ic) : 0u;
-      uint32_t s[32];
-      uint64_t pr[16];
-      if (!wait_all(C::kSFull + 2 * wg + (n & 1), (n >> 1) & 1)) {
-        failed = true;
-        break;
-      }
-      tc_fence_after();
-      tc_ld32(sa, s);
-      tc_wait_ld();
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        pr[2 * c] = ex2_2(fma2(pair(s[4 * c], s[4 * c + 1]), sl2_2, nl[c].x));
-        pr[2 * c + 1] = ex2_2(fma2(pair(s[4 * c + 2], s[4 * c + 3]), sl2_2, nl[c].y));
-      }
-      auto pack = [&](uint32_t (&w)[16]) {
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const float2 f = unpair(pr[c]);
-          w[c] = pack2_t<BF16>(f.x, f.y);
+        const bool edge =
+            it.j0 < i0 + kStep - 1 - p.left || it.j0 + kBlk - 1 > i0 + p.right || i0 + kStep > p.M;
+        const uint32_t seen = edge ? seen_bits(lo_j - ic, hi_j - ic) : 0u;
+        uint32_t s[32];
+        uint64_t pr[16];
+        if (!wait_all(C::kSFull + gb + (n & 1), (n >> 1) & 1)) {
+          failed = true;
+          break;
         }
-      };
-      uint32_t w[16];
-      pack(w);
-      if (edge) keep_seen(w, seen);
-      tc_st16(sa, w);
-      tc_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(C::kPFull + 2 * wg + (n & 1)));
-      if (!wait_all(C::kDpFull + 2 * wg + (n & 1), (n >> 1) & 1)) {
-        failed = true;
-        break;
-      }
-      tc_fence_after();
-      tc_ld32(da, s);
-      tc_wait_ld();
+        tc_ld32(sa, s);
+        tc_wait_ld();
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const ulonglong2 d = ndl[c];  // -delta of 4 queries
-        const uint64_t x = pair(s[4 * c], s[4 * c + 1]), y = pair(s[4 * c + 2], s[4 * c + 3]);
-        pr[2 * c] = mul2(pr[2 * c], BF16 ? add2(x, d.x) : fma2(x, shift_2, d.x));
-        pr[2 * c + 1] = mul2(pr[2 * c + 1], BF16 ? add2(y, d.y) : fma2(y, shift_2, d.y));
-      }
-      pack(w);
-      if (edge) keep_seen(w, seen);
-      tc_st16(da, w);
-      tc_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(C::kDsFull + 2 * wg + (n & 1)));
-    }
-    if (!failed && nt > 0 && !wait_all(C::kDone, 0)) failed = true;
-    if (!failed) {
-      tc_fence_after();
-      // warpgroup 0 stores dV, 1 dK
-      const float f = wg == 0 ? Shift<BF16>::kPInv : p.scale * Shift<BF16>::kSInv;
-      void* dst = wg == 0 ? p.dV : p.dK;
-      bool f32 = p.g32;
-      if (p.part != nullptr) {
-        const int64_t n = static_cast<int64_t>(p.B) * p.N * p.Hkv * D;
-        dst = p.part + (2 * sp + (wg == 0 ? 1 : 0)) * n;
-        f32 = true;
-      }
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t r[32];
-        if (nt > 0) {
-          tc_ld32(lane_addr + (wg == 0 ? C::kColDv : C::kColDk) + 32 * c, r);
-          tc_wait_ld();
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) r[e] = 0u;
+        for (int c = 0; c < 8; ++c) {
+          pr[2 * c] = ex2_2(fma2(pair(s[4 * c], s[4 * c + 1]), sl2_2, nl2[c].x));
+          pr[2 * c + 1] = ex2_2(fma2(pair(s[4 * c + 2], s[4 * c + 3]), sl2_2, nl2[c].y));
         }
-        if (in) store_row32<BF16>(dst, off, 32 * c, f32, r, f, p.wide);
+        auto pack = [&](uint32_t (&w)[16]) {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float2 f = unpair(pr[c]);
+            w[c] = pack2_t<BF16>(f.x, f.y);
+          }
+        };
+        uint32_t w[16];
+        pack(w);
+        if (edge) keep_seen(w, seen);
+        tc_st16(sa, w);
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::kPFull + gb + (n & 1)));
+        if (!wait_all(C::kDpFull + gb + (n & 1), (n >> 1) & 1)) {
+          failed = true;
+          break;
+        }
+        tc_ld32(da, s);
+        tc_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const ulonglong2 d = ndl[c];  // -delta of 4 queries
+          const uint64_t x = pair(s[4 * c], s[4 * c + 1]), y = pair(s[4 * c + 2], s[4 * c + 3]);
+          pr[2 * c] = mul2(pr[2 * c], BF16 ? add2(x, d.x) : fma2(x, shift_2, d.x));
+          pr[2 * c + 1] = mul2(pr[2 * c + 1], BF16 ? add2(y, d.y) : fma2(y, shift_2, d.y));
+        }
+        pack(w);
+        if (edge) keep_seen(w, seen);
+        tc_st16(da, w);
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::kDsFull + gb + (n & 1)));
       }
     }
   }
@@ -985,36 +1182,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (failed) report_timeout();
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 13) {
     __syncwarp();
     tc_fence_after();
     tc_dealloc(tmem, kTmemAll);
   }
 }
 
-// dK and dV from the parts, added in order; 8 entries a thread.
-template <bool BF16>
-__global__ void __launch_bounds__(256)
-    swa_bwd_join_kernel(const float* part, int splits, int64_t n, void* dK, void* dV, bool g32) {
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
-  if (i >= n) return;
-  const int which = blockIdx.y;  // 0 dK, 1 dV
+// dK and dV of the tiles that were cut, their parts added in order; 8 entries
+// a thread.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) swa_bwd_join_kernel(const SwaBwdProblem p) {
+  constexpr int kRowThreads = D / 8;
+  const int e = threadIdx.x % kRowThreads * 8;
+  const int row = static_cast<int>(blockIdx.y) * (256 / kRowThreads) + threadIdx.x / kRowThreads;
+  const int which = blockIdx.z;  // 0 dK, 1 dV
+  const DkvItem it = dkv_item(p, p.whole_tiles + blockIdx.x * static_cast<uint32_t>(p.splits));
+  const int j = it.j0 + row;
+  if (j >= p.N) return;
   float f[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = 0.f;
-  for (int s = 0; s < splits; ++s) {
-    const float4* src = reinterpret_cast<const float4*>(part + (2 * s + which) * n + i);
+  for (int i = 0; i < 8; ++i) f[i] = 0.f;
+  for (int s = 0; s < p.splits; ++s) {
+    const float4* src = reinterpret_cast<const float4*>(
+        p.part + ((static_cast<int64_t>(it.part + s) * 2 + which) * kBlk + row) * D + e);
     const float4 a = src[0], c = src[1];
     f[0] += a.x, f[1] += a.y, f[2] += a.z, f[3] += a.w;
     f[4] += c.x, f[5] += c.y, f[6] += c.z, f[7] += c.w;
   }
-  void* dst = which == 0 ? dK : dV;
-  if (g32) {
-    float4* o = reinterpret_cast<float4*>(static_cast<float*>(dst) + i);
+  void* dst = which == 0 ? p.dK : p.dV;
+  const int64_t at = ((static_cast<int64_t>(it.b) * p.N + j) * p.Hkv + it.g) * D + e;
+  if (p.g32) {
+    float4* o = reinterpret_cast<float4*>(static_cast<float*>(dst) + at);
     o[0] = make_float4(f[0], f[1], f[2], f[3]);
     o[1] = make_float4(f[4], f[5], f[6], f[7]);
   } else {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + i) =
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + at) =
         make_uint4(pack2_t<BF16>(f[0], f[1]), pack2_t<BF16>(f[2], f[3]), pack2_t<BF16>(f[4], f[5]),
                    pack2_t<BF16>(f[6], f[7]));
   }
@@ -1023,6 +1226,7 @@ __global__ void __launch_bounds__(256)
 // ---------------------------------------------------------------- host
 
 constexpr int kSms = 152;
+constexpr int kItemSteps = 3, kMinSteps = 4, kJoinSteps = 6;
 
 int check_swa_bwd(int64_t B, int64_t M, int64_t N, int64_t H, int64_t H_kv, int64_t D) {
   if (B < 0 || M < 0 || N < 0 || H <= 0 || H_kv <= 0) return NSA_ERR_SHAPE;
@@ -1030,24 +1234,48 @@ int check_swa_bwd(int64_t B, int64_t M, int64_t N, int64_t H, int64_t H_kv, int6
   if (D != 64 && D != 128) return NSA_ERR_HEAD_DIM;
   const int64_t lim = int64_t(1) << 29;
   if (M > lim || N > lim || H > 65536 || B > 65536) return NSA_ERR_SHAPE;
-  const int64_t top = (int64_t(1) << 31) - 1;
-  if (B * H * ((M + kBlk - 1) / kBlk) > top || B * H * ((N + kBlk - 1) / kBlk) > top)
+  const int64_t top = (int64_t(1) << 31) - 1 - (1 << 20);  // items, steps of a tile
+  if (B * H * ((M + kStep - 1) / kStep + 1) > top || B * H * ((N + kBlk - 1) / kBlk) > top)
     return NSA_ERR_SHAPE;
   return NSA_OK;
 }
 
-// Parts of the dK, dV steps of a key tile: as many as give every SM an item,
-// with at least 4 steps to each of them.
-int swa_bwd_splits(int64_t B, int64_t M, int64_t N, int64_t H, int64_t H_kv, int64_t left,
+// How the key tiles are cut: `whole` of them are items of their own, the
+// others (the last) are cut into `splits` parts of their steps, so that the SMs
+// do not wait for a last, mostly empty round. Uneven tiles (a causal window
+// over the whole sequence) are left alone once they are more than the SMs:
+// their last ones are short.
+struct KeyTiles {
+  int64_t tiles, whole;
+  int splits;
+  int64_t items() const { return whole + (tiles - whole) * splits; }
+  int64_t parts() const { return (tiles - whole) * splits; }
+};
+
+KeyTiles key_tiles(int64_t B, int64_t M, int64_t N, int64_t H, int64_t H_kv, int64_t left,
                    int64_t right) {
-  const int64_t items = B * H_kv * ((N + kBlk - 1) / kBlk);
-  if (items == 0 || items >= kSms) return 1;
+  KeyTiles k{B * H_kv * ((N + kBlk - 1) / kBlk), 0, 1};
+  k.whole = k.tiles;
+  const int64_t rest = k.tiles % kSms;
   int64_t rows = left + right + kBlk;  // queries that see a key tile
+  const bool even = rows <= M || (left >= M && right >= N);
+  if (k.tiles == 0 || rest == 0 || (k.tiles > kSms && !even)) return k;
   if (rows > M) rows = M;
   const int64_t steps = (rows + kStep - 1) / kStep * (H / H_kv);
-  int64_t s = (kSms + items - 1) / items;
-  if (s > steps / 4) s = steps / 4;
-  return static_cast<int>(s < 1 ? 1 : s);
+  // the rest's time in steps for each number of parts: rounds of parts, each
+  // with kItemSteps steps' worth of its own
+  double best = steps + kItemSteps;
+  for (int s = 2; s <= 16 && steps / s >= kMinSteps; ++s) {
+    const double t = static_cast<double>((rest * s + kSms - 1) / kSms) *
+                         (static_cast<double>(steps) / s + kItemSteps) +
+                     kJoinSteps;
+    if (t < best) {
+      best = t;
+      k.whole = k.tiles - rest;
+      k.splits = s;
+    }
+  }
+  return k;
 }
 
 struct WindowSides {
@@ -1077,17 +1305,18 @@ int launch_swa_bwd(const SwaBwdProblem& p, cudaStream_t st) {
           cudaSuccess)
     return NSA_ERR_LAUNCH;
   const int64_t qi = static_cast<int64_t>(p.B) * p.H * p.qtiles;
-  const int64_t ki = static_cast<int64_t>(p.B) * p.Hkv * p.ktiles * p.splits;
+  const int64_t ki = p.dkv_items;
   // one CTA per SM, items dealt to them
   dq<<<static_cast<unsigned>(qi < kSms ? qi : kSms), kDqThreads, DqCfg<D>::kSmem, st>>>(p, tk, tv,
                                                                                        tq, to, td);
   if (cudaGetLastError() != cudaSuccess) return NSA_ERR_LAUNCH;
-  dkv<<<static_cast<unsigned>(ki), kThreads, DkvCfg<D>::kSmem, st>>>(p, tq, td);
+  dkv<<<static_cast<unsigned>(ki < kSms ? ki : kSms), kDkvThreads, DkvCfg<D>::kSmem, st>>>(
+      p, tq, td, tk, tv);
   if (cudaGetLastError() != cudaSuccess) return NSA_ERR_LAUNCH;
   if (p.part != nullptr) {
-    const int64_t n = static_cast<int64_t>(p.B) * p.N * p.Hkv * D;
-    const dim3 grid(static_cast<unsigned>((n / 8 + 255) / 256), 2);
-    swa_bwd_join_kernel<BF16><<<grid, 256, 0, st>>>(p.part, p.splits, n, p.dK, p.dV, p.g32);
+    const dim3 grid(static_cast<unsigned>(p.B * p.Hkv * p.ktiles - p.whole_tiles), kBlk * D / 8 / 256,
+                    2);
+    swa_bwd_join_kernel<D, BF16><<<grid, 256, 0, st>>>(p);
     if (cudaGetLastError() != cudaSuccess) return NSA_ERR_LAUNCH;
   }
   return NSA_OK;
@@ -1108,8 +1337,7 @@ extern "C" int64_t nsa_swa_bwd_workspace_bytes(int64_t B, int64_t M, int64_t N, 
   if (B == 0 || M == 0 || N == 0) return 0;
   const WindowSides w = clamp_window(M, N, window_left, window_right);
   const int64_t Mp = (M + kStep - 1) / kStep * kStep;
-  const int splits = swa_bwd_splits(B, M, N, H, H_kv, w.left, w.right);
-  return 2 * B * H * Mp * 4 + (splits > 1 ? splits * 2 * B * N * H_kv * D * 4 : 0);
+  return 2 * B * H * Mp * 4 + key_tiles(B, M, N, H, H_kv, w.left, w.right).parts() * 2 * kBlk * D * 4;
 }
 
 extern "C" int nsa_swa_bwd(const void* Q, const void* K, const void* V, const void* O,
@@ -1166,7 +1394,10 @@ extern "C" int nsa_swa_bwd(const void* Q, const void* K, const void* V, const vo
   p.Mp = static_cast<int>((M + kStep - 1) / kStep * kStep);
   p.qtiles = static_cast<int>((M + kBlk - 1) / kBlk);
   p.ktiles = static_cast<int>((N + kBlk - 1) / kBlk);
-  p.splits = swa_bwd_splits(B, M, N, H, H_kv, w.left, w.right);
+  const KeyTiles tiles = key_tiles(B, M, N, H, H_kv, w.left, w.right);
+  p.splits = tiles.splits;
+  p.whole_tiles = static_cast<int>(tiles.whole);
+  p.dkv_items = static_cast<int>(tiles.items());
   p.dq_items = static_cast<int>(B * H * p.qtiles);
   p.left = static_cast<int>(w.left);
   p.right = static_cast<int>(w.right);
@@ -1177,7 +1408,7 @@ extern "C" int nsa_swa_bwd(const void* Q, const void* K, const void* V, const vo
   const int64_t stat = B * H * p.Mp;
   p.nlse2 = static_cast<float*>(workspace);
   p.ndelta = p.nlse2 + stat;
-  p.part = p.splits > 1 ? p.ndelta + stat : nullptr;
+  p.part = tiles.parts() > 0 ? p.ndelta + stat : nullptr;
   const bool bf = dtype == NSA_BF16;
   if (D == 64) return bf ? launch_swa_bwd<64, true>(p, st) : launch_swa_bwd<64, false>(p, st);
   return bf ? launch_swa_bwd<128, true>(p, st) : launch_swa_bwd<128, false>(p, st);

@@ -51,11 +51,14 @@ def test_null_and_misaligned(lib, which):
 def test_workspace(lib):
     f = lib.nsa_swa_bwd_workspace_bytes
     stat = 2 * 2 * 16 * 320 * 4
-    # 12 key tiles of (batch, KV head): 13 parts would give every SM one, and
-    # (64 + 128 queries) / 64 x 8 heads = 24 steps give 6 of 4
-    assert f(2, 300, 300, 16, 2, 128, 64, 0) == stat + 6 * 2 * 2 * 300 * 2 * 128 * 4
-    # as many key tiles as SMs: no parts
-    assert f(1, 8192, 8192, 64, 8, 128, 512, 0) == 2 * 64 * 8192 * 4
+    tile = 2 * 128 * 128 * 4  # fp32 dK and dV of 128 keys
+    # 12 key tiles of (batch, KV head), 3 query blocks x 8 heads = 24 steps each:
+    # cut into 6 parts of 4
+    assert f(2, 300, 300, 16, 2, 128, 64, 0) == stat + 12 * 6 * tile
+    # 8 x 64 tiles = 3 rounds of 152 and 56 more, cut in two
+    assert f(1, 8192, 8192, 64, 8, 128, 512, 0) == 2 * 64 * 8192 * 4 + 56 * 2 * tile
+    # uneven tiles, more than the SMs: whole
+    assert f(1, 8192, 8192, 64, 8, 128, -1, 0) == 2 * 64 * 8192 * 4
     assert f(1, 0, 300, 16, 2, 128, -1, -1) == 0 and f(1, 300, 0, 16, 2, 128, -1, -1) == 0
     assert f(1, 300, 300, 15, 2, 128, -1, -1) == -5 and f(1, 300, 300, 16, 2, 80, -1, -1) == -4
     need = f(2, 300, 300, 16, 2, 128, 64, 0)
