@@ -1110,7 +1110,16 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         if (++u == it.nq) u = 0;
         // The stage's nlse2 and ndelta first, while S is being formed: a wait
         // costs some 100 clocks even when it is over, and S is on the chain.
-        if (!wait_all(C::kFull + st, ph)) {
+        // With two buffers S and dP are mostly there: one question for all.
+        bool there = false;
+        if constexpr (C::kBuf == 2) {
+          const bool x0 = mbar_try_wait(bar(C::kFull + st), ph);
+          const bool x1 = mbar_try_wait(bar(C::kSFull + gb + (n & 1)), (n >> 1) & 1);
+          const bool x2 = mbar_try_wait(bar(C::kDpFull + gb + (n & 1)), (n >> 1) & 1);
+          there = __all_sync(kFull, x0 && x1 && x2);
+          if (there) tc_fence_after();
+        }
+        if (!there && !wait_all(C::kFull + st, ph)) {
           failed = true;
           break;
         }
@@ -1129,7 +1138,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         const uint32_t seen = edge ? seen_bits(lo_j - ic, hi_j - ic) : 0u;
         uint32_t s[32];
         uint64_t pr[16];
-        if (!wait_all(C::kSFull + gb + (n & 1), (n >> 1) & 1)) {
+        if (!there && !wait_all(C::kSFull + gb + (n & 1), (n >> 1) & 1)) {
           failed = true;
           break;
         }
@@ -1155,7 +1164,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::kPFull + gb + (n & 1)));
-        if (!wait_all(C::kDpFull + gb + (n & 1), (n >> 1) & 1)) {
+        if (!there && !wait_all(C::kDpFull + gb + (n & 1), (n >> 1) & 1)) {
           failed = true;
           break;
         }
