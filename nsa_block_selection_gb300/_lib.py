@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -123,7 +124,7 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.nsa_qk_norm_rope_bwd.argtypes = [vp] * 13 + [i64] * 8 + [f32, c_int, c_int, c_int, c_int,
                                                                  vp, vp, i64, vp]
     if path is None:
-        _fill_dtype_codes()
+        _bind_torch()
         _lib = lib
     return lib
 
@@ -495,29 +496,27 @@ def swa_bwd(q, k, v, o, lse, do, window=(-1, -1), scale: Optional[float] = None,
     ones). ``workspace`` (CUDA uint8, swa_bwd_workspace_bytes) is allocated
     when omitted; calls that may overlap need one each.
     """
-    import torch
-
     lib = _lib or load()
     dt, qs, ks = q.dtype, q.shape, k.shape
-    if dt is not torch.bfloat16 and dt is not torch.float16:
+    if dt not in _F16_KINDS:
         raise TypeError(f"q must be fp16 or bf16, got {dt}")
     if len(qs) != 4 or len(ks) != 4 or qs[0] != ks[0] or qs[3] != ks[3]:
         raise ValueError("shape mismatch: q [B,M,H,D], k/v [B,N,H_kv,D]")
     B, M, H, D = qs
     N, Hkv = ks[1], ks[2]
     if grad_dtype is None:
-        given = [t for t in (dq, dk, dv) if t is not None]
-        grad_dtype = given[0].dtype if given else dt
-    if grad_dtype is not torch.float32 and grad_dtype is not dt:
+        grad_dtype = next((t.dtype for t in (dq, dk, dv) if t is not None), dt)
+    if grad_dtype is not _torch.float32 and grad_dtype is not dt:
         raise TypeError(f"gradients must be fp32 or {dt}, got {grad_dtype}")
+    like = {} if grad_dtype is dt else {"dtype": grad_dtype}
     if dq is None:
-        dq = torch.empty_like(q, dtype=grad_dtype)
+        dq = _torch.empty_like(q, **like)
     if dk is None:
-        dk = torch.empty_like(k, dtype=grad_dtype)
+        dk = _torch.empty_like(k, **like)
     if dv is None:
-        dv = torch.empty_like(k, dtype=grad_dtype)
+        dv = _torch.empty_like(k, **like)
     named = (("q", q, dt, qs), ("k", k, dt, ks), ("v", v, dt, ks), ("o", o, dt, qs),
-             ("lse", lse, torch.float32, (B, H, M)), ("do", do, dt, qs),
+             ("lse", lse, _torch.float32, (B, H, M)), ("do", do, dt, qs),
              ("dq", dq, grad_dtype, qs), ("dk", dk, grad_dtype, ks), ("dv", dv, grad_dtype, ks))
     for name, t, want, shape in named:
         if t.dtype is not want:
@@ -530,21 +529,19 @@ def swa_bwd(q, k, v, o, lse, do, window=(-1, -1), scale: Optional[float] = None,
             raise ValueError(f"{name} must be a contiguous tensor on q's CUDA device")
     left, right = (int(window[0]), int(window[1])) if window is not None else (-1, -1)
     if workspace is None:
-        need = lib.nsa_swa_bwd_workspace_bytes(B, M, N, H, Hkv, D, left, right)
-        if need < 0:
-            raise NsaError(need, "nsa_swa_bwd_workspace_bytes")
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    if workspace.get_device() != dev:
-        raise ValueError("workspace must be on q's CUDA device")
-    with _on_device(dev):
-        # scale: the ABI takes <= 0 for 1/sqrt(D)
-        st = lib.nsa_swa_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                             lse.data_ptr(), do.data_ptr(), dq.data_ptr(), dk.data_ptr(),
-                             dv.data_ptr(), B, M, N, H, Hkv, D, left, right,
-                             0.0 if scale is None else scale, _DTYPE_CODES[dt],
-                             _DTYPE_CODES[grad_dtype], workspace.data_ptr(),
-                             workspace.numel() * workspace.element_size(),
-                             _raw_stream(stream, dev))
+        nbytes = lib.nsa_swa_bwd_workspace_bytes(B, M, N, H, Hkv, D, left, right)
+        if nbytes < 0:
+            raise NsaError(nbytes, "nsa_swa_bwd_workspace_bytes")
+        workspace = _torch.empty(nbytes, dtype=_torch.uint8, device=q.device)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+        if workspace.get_device() != dev:
+            raise ValueError("workspace must be on q's CUDA device")
+    # scale: the ABI takes <= 0 for 1/sqrt(D)
+    st = _launch(dev, stream, lib.nsa_swa_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                 o.data_ptr(), lse.data_ptr(), do.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+                 dv.data_ptr(), B, M, N, H, Hkv, D, left, right, 0.0 if scale is None else scale,
+                 _DTYPE_CODES[dt], _DTYPE_CODES[grad_dtype], workspace.data_ptr(), nbytes)
     if st != NSA_OK:
         raise NsaError(st, "nsa_swa_bwd")
     return dq, dk, dv
@@ -566,74 +563,95 @@ def rope_tables(rows: int, rot_dim: int, base: float = 10000.0, device="cuda"):
     return ang.cos().float(), ang.sin().float()
 
 
-class _on_device:
-    """Makes a CUDA device current for a launch; does nothing where it is."""
-
-    def __init__(self, index):
-        self.index = index
-
-    def __enter__(self):
-        import torch
-
-        self.prev = torch._C._cuda_getDevice()
-        if self.prev != self.index:
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        import torch
-
-        if self.prev != self.index:
-            torch.cuda.set_device(self.prev)
+# The calls below may be a single token's work, beside which every property
+# read and every import statement counts: torch is looked up once, each
+# property is read once, and names are given only where a check failed.
+_torch = None
+_F16_KINDS = ()
+_DTYPE_CODES = {}
 
 
-def _raw_stream(stream, index):
-    """The cudaStream_t of ``stream``, or of the device's current stream."""
+def _bind_torch():
+    global _torch, _F16_KINDS
     import torch
 
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    _torch = torch
+    _F16_KINDS = (torch.float16, torch.bfloat16)
+    _DTYPE_CODES.update({torch.float16: NSA_F16, torch.bfloat16: NSA_BF16, torch.float32: NSA_F32})
 
 
-def _check_rope(named, weights, cos, sin, positions):
+def _launch(dev, stream, fn, *args):
+    """fn(*args, cudaStream_t) with device ``dev`` current."""
+    c = _torch._C
+    st = c._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if c._cuda_getDevice() == dev:
+        return fn(*args, st)
+    with _torch.cuda.device(dev):
+        return fn(*args, st)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _dense_like(t):
+    """An uninitialised contiguous tensor of t's shape and type."""
+    e = _torch.empty_like(t)
+    return e if e.is_contiguous() else \
+        _torch.empty_like(t, memory_format=_torch.contiguous_format)
+
+
+def _refuse_tensor(name, t, dtypes, shape, dev):
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {dtypes}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}")
+    raise ValueError(f"{name} must be on q's CUDA device, with a contiguous last dimension")
+
+
+def _check_rope(named, q_weight, k_weight, cos, sin, positions):
     """Checks shared by the norm-and-rotation calls; ``named``: (name, tensor,
     allowed dtypes), of q's and k's shapes in turn. Returns the sizes and codes
-    that the calls pass on. These calls may be a token's work: what is checked
-    here costs microseconds beside them, so each property is read once."""
-    import torch
-
+    that the calls pass on, and the element strides (None: all contiguous)."""
     q, k = named[0][1], named[1][1]
     dt, qs, ks = q.dtype, q.shape, k.shape
-    if dt is not torch.bfloat16 and dt is not torch.float16:
+    if dt not in _F16_KINDS:
         raise TypeError(f"q must be fp16 or bf16, got {dt}")
     if len(qs) != 4 or len(ks) != 4 or qs[0] != ks[0] or qs[1] != ks[1] or qs[3] != ks[3]:
         raise ValueError("shape mismatch: q [B,M,H,D], k [B,M,G,D]")
     B, M, H, D = qs
+    G = ks[2]
     dev = q.get_device()
-    shape = ks
-    for name, t, dtypes in named:
-        shape = qs if shape is ks else ks
-        if t.dtype not in dtypes:
-            raise TypeError(f"{name} must be one of {dtypes}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name} must have the shape {tuple(shape)}")
-    for name, t, _ in named:
-        if t.get_device() != dev or dev < 0:
-            raise ValueError(f"{name} must be on q's CUDA device")
-        if not t.is_contiguous() and t.stride(3) != 1:
-            raise ValueError(f"{name} must have a contiguous last dimension")
+    plain = True
+    for i, (name, t, dtypes) in enumerate(named):
+        if t.dtype not in dtypes or t.shape != (ks if i & 1 else qs):
+            _refuse_tensor(name, t, dtypes, ks if i & 1 else qs, dev)
+    for i, (name, t, dtypes) in enumerate(named):
+        c = t.is_contiguous()
+        plain = plain and c
+        if t.get_device() != dev or dev < 0 or not (c or t.stride(3) == 1):
+            _refuse_tensor(name, t, dtypes, ks if i & 1 else qs, dev)
+    strides = None
+    if not plain:  # (the stride of a dimension of one is never used)
+        strides = array("q")
+        for i, (_, t, _) in enumerate(named):
+            b, m, h, _ = t.stride()
+            strides.extend((b if B > 1 else 0, m if M > 1 else 0,
+                            h if (G if i & 1 else H) > 1 else 0))
     wdt = None
-    for name, w in weights:
+    for w in (q_weight, k_weight):
         if w is None:
             continue
-        if (w.dtype is not torch.float32 and w.dtype is not dt) or \
+        if (w.dtype is not _torch.float32 and w.dtype is not dt) or \
                 (wdt is not None and w.dtype is not wdt):
-            raise TypeError(f"{name} must be fp32 or {dt}, and both weights alike")
+            raise TypeError(f"the weights must be fp32 or {dt}, both alike")
         wdt = w.dtype
         if w.shape != (D,) or not w.is_contiguous() or w.get_device() != dev:
-            raise ValueError(f"{name} must be a contiguous [D] tensor on q's device")
+            raise ValueError("a weight must be a contiguous [D] tensor on q's device")
     R = rows = 0
     if cos is not None and sin is not None:
         cs = cos.shape
-        if cos.dtype is not torch.float32 or sin.dtype is not torch.float32:
+        if cos.dtype is not _torch.float32 or sin.dtype is not _torch.float32:
             raise TypeError("cos and sin must be fp32")
         if len(cs) != 2 or cs != sin.shape or not cos.is_contiguous() or \
                 not sin.is_contiguous() or cos.get_device() != dev or sin.get_device() != dev:
@@ -643,7 +661,7 @@ def _check_rope(named, weights, cos, sin, positions):
         raise ValueError("pass both tables or neither")
     pstride = 0
     if positions is not None:
-        if positions.dtype is not torch.int32:
+        if positions.dtype is not _torch.int32:
             raise TypeError(f"positions must be int32, got {positions.dtype}")
         ps = positions.shape
         if ps == (B, M):
@@ -652,41 +670,8 @@ def _check_rope(named, weights, cos, sin, positions):
             raise ValueError("positions must be [M] or [B, M]")
         if not positions.is_contiguous() or positions.get_device() != dev:
             raise ValueError("positions must be a contiguous tensor on q's device")
-    return dev, B, M, H, ks[2], D, R, rows, pstride, _DTYPE_CODES[dt], \
-        NSA_F32 if wdt is None else _DTYPE_CODES[wdt]
-
-
-_DTYPE_CODES = {}
-
-
-def _fill_dtype_codes():
-    import torch
-
-    _DTYPE_CODES.update({torch.float16: NSA_F16, torch.bfloat16: NSA_BF16,
-                         torch.float32: NSA_F32})
-
-
-_STRIDES12, _STRIDES18 = ctypes.c_int64 * 12, ctypes.c_int64 * 18
-
-
-def _strides(kind, *tensors):
-    """(b, m, head) element strides of [B, M, heads, D] tensors; None if all
-    are contiguous. The stride of a dimension of one is never used."""
-    for t in tensors:
-        if not t.is_contiguous():
-            break
-    else:
-        return None
-    s = []
-    for t in tensors:
-        sb, sm, sh, _ = t.stride()
-        B, M, H, _ = t.shape
-        s += (sb if B > 1 else 0, sm if M > 1 else 0, sh if H > 1 else 0)
-    return kind(*s)
-
-
-def _at(t):
-    return None if t is None else t.data_ptr()
+    return dev, (B, M, H, G, D, R, rows, pstride), _DTYPE_CODES[dt], \
+        NSA_F32 if wdt is None else _DTYPE_CODES[wdt], strides
 
 
 def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
@@ -706,24 +691,19 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positio
     marks padding, whose output rows are zero. The outputs may be the inputs.
     Returns (q_out, k_out).
     """
-    import torch
-
     lib = _lib or load()
     if q_out is None:
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        q_out = _dense_like(q)
     if k_out is None:
-        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        k_out = _dense_like(k)
     own = (q.dtype,)
-    dev, B, M, H, G, D, R, rows, ps, code, wcode = _check_rope(
-        (("q", q, own), ("k", k, own), ("q_out", q_out, own), ("k_out", k_out, own)),
-        (("q_weight", q_weight), ("k_weight", k_weight)), cos, sin, positions)
-    with _on_device(dev):
-        st = lib.nsa_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(),
-                                  _at(q_weight), _at(k_weight), _at(cos), _at(sin),
-                                  _at(positions), B, M, H, G, D, R, rows, ps, eps,
-                                  1 if interleaved else 0, code, wcode,
-                                  _strides(_STRIDES12, q, k, q_out, k_out),
-                                  _raw_stream(stream, dev))
+    dev, sizes, code, wcode, strides = _check_rope(
+        (("q", q, own), ("k", k, own), ("q_out", q_out, own), ("k_out", k_out, own)), q_weight,
+        k_weight, cos, sin, positions)
+    st = _launch(dev, stream, lib.nsa_qk_norm_rope, q.data_ptr(), k.data_ptr(), q_out.data_ptr(),
+                 k_out.data_ptr(), _at(q_weight), _at(k_weight), _at(cos), _at(sin),
+                 _at(positions), *sizes, eps, 1 if interleaved else 0, code, wcode,
+                 None if strides is None else strides.buffer_info()[0])
     if st != NSA_OK:
         raise NsaError(st, "nsa_qk_norm_rope")
     return q_out, k_out
@@ -750,44 +730,43 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, cos=Non
     ``workspace`` (CUDA uint8, norm_rope_bwd_workspace_bytes) is allocated
     when omitted.
     """
-    import torch
-
     lib = _lib or load()
     if dq is None:
-        dq = torch.empty_like(q, memory_format=torch.contiguous_format)
+        dq = _dense_like(q)
     if dk is None:
-        dk = torch.empty_like(k, memory_format=torch.contiguous_format)
+        dk = _dense_like(k)
     own = (q.dtype,)
-    dev, B, M, H, G, D, R, rows, ps, code, wcode = _check_rope(
-        (("q", q, own), ("k", k, own), ("dq_out", dq_out, (torch.float32, q.dtype)),
-         ("dk_out", dk_out, (dq_out.dtype,)), ("dq", dq, own), ("dk", dk, own)),
-        (("q_weight", q_weight), ("k_weight", k_weight)), cos, sin, positions)
+    dev, sizes, code, wcode, strides = _check_rope(
+        (("q", q, own), ("k", k, own), ("dq_out", dq_out, (_torch.float32, q.dtype)),
+         ("dk_out", dk_out, (dq_out.dtype,)), ("dq", dq, own), ("dk", dk, own)), q_weight,
+        k_weight, cos, sin, positions)
     nbytes = 0
     if weight_grads:
+        D = sizes[4]
         if dq_weight is None:
-            dq_weight = torch.empty(D, dtype=torch.float32, device=q.device)
+            dq_weight = _torch.empty(D, dtype=_torch.float32, device=q.device)
         if dk_weight is None:
-            dk_weight = torch.empty(D, dtype=torch.float32, device=q.device)
-        for name, w in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
-            if w.dtype is not torch.float32 or w.shape != (D,) or not w.is_contiguous() or \
+            dk_weight = _torch.empty(D, dtype=_torch.float32, device=q.device)
+        for w in (dq_weight, dk_weight):
+            if w.dtype is not _torch.float32 or w.shape != (D,) or not w.is_contiguous() or \
                     w.get_device() != dev:
-                raise ValueError(f"{name} must be a contiguous fp32 [D] tensor on q's device")
+                raise ValueError("a weight's gradient must be a contiguous fp32 [D] tensor on "
+                                 "q's device")
         if workspace is None:
-            workspace = torch.empty(norm_rope_bwd_workspace_bytes(B, M, D), dtype=torch.uint8,
-                                    device=q.device)
-        if workspace.get_device() != dev:
-            raise ValueError("workspace must be on q's CUDA device")
-        nbytes = workspace.numel() * workspace.element_size()
+            nbytes = norm_rope_bwd_workspace_bytes(sizes[0], sizes[1], D)
+            workspace = _torch.empty(nbytes, dtype=_torch.uint8, device=q.device)
+        else:
+            nbytes = workspace.numel() * workspace.element_size()
+            if workspace.get_device() != dev:
+                raise ValueError("workspace must be on q's CUDA device")
     else:
         dq_weight = dk_weight = workspace = None
-    with _on_device(dev):
-        st = lib.nsa_qk_norm_rope_bwd(
-            q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(),
-            dk.data_ptr(), _at(dq_weight), _at(dk_weight), _at(q_weight), _at(k_weight), _at(cos),
-            _at(sin), _at(positions), B, M, H, G, D, R, rows, ps, eps, 1 if interleaved else 0,
-            code, wcode, _DTYPE_CODES[dq_out.dtype],
-            _strides(_STRIDES18, q, k, dq_out, dk_out, dq, dk), _at(workspace), nbytes,
-            _raw_stream(stream, dev))
+    st = _launch(dev, stream, lib.nsa_qk_norm_rope_bwd, q.data_ptr(), k.data_ptr(),
+                 dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+                 _at(dq_weight), _at(dk_weight), _at(q_weight), _at(k_weight), _at(cos), _at(sin),
+                 _at(positions), *sizes, eps, 1 if interleaved else 0, code, wcode,
+                 _DTYPE_CODES[dq_out.dtype],
+                 None if strides is None else strides.buffer_info()[0], _at(workspace), nbytes)
     if st != NSA_OK:
         raise NsaError(st, "nsa_qk_norm_rope_bwd")
     return dq, dk, dq_weight, dk_weight
