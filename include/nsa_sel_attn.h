@@ -558,8 +558,7 @@ int nsa_qk_norm_rope(const void* Q, const void* K, void* Qo, void* Ko, const voi
 
 /*
  * nsa_qk_norm_rope_bwd_workspace_bytes -- device workspace of
- * nsa_qk_norm_rope_bwd: one partial sum of the two weight gradients per CTA
- * (at most 304). Negative nsa_status for invalid sizes. Pure host arithmetic.
+ * nsa_qk_norm_rope_bwd: a partial weight gradient of each of up to 304 CTAs. Negative nsa_status for invalid sizes. Pure host arithmetic.
  */
 int64_t nsa_qk_norm_rope_bwd_workspace_bytes(int64_t B, int64_t M, int64_t D);
 

@@ -34,6 +34,7 @@ namespace {
 
 constexpr int kRopeThreads = 128;      // forward CTAs: 4 warps, each a unit of its own
 constexpr int kRopeBwdThreads = 256;   // backward CTAs: 8 warps that share one dw partial
+constexpr int kRopeBwdPerSm = 3;       // and how many of them an SM holds
 constexpr int kRopeSms = 152;
 
 struct RopeRows {
@@ -251,184 +252,240 @@ struct RopeBwdRows {
   const void* w;
   int64_t xb, xm, xh, gb, gm, gh, db, dm, dh;
   int heads;
+  int segs, per;      // a token's heads are cut into segs units of per heads
+  int64_t units;
+  int ctas;           // CTAs that work on this tensor
 };
 
 struct RopeBwdProblem {
   RopeProblem a;  // tables, positions, flags (its q and k are unused)
   RopeBwdRows q, k;
-  float* part;    // [CTAs, 2, D] partial dw, or NULL
+  float* part;    // [q.ctas + k.ctas, D] partial dw, or NULL
 };
 
-template <int D, bool BF16, bool G32, int UN>
-__device__ __forceinline__ void norm_rope_bwd_rows(const RopeProblem& p, const RopeBwdRows& t, int b,
-                                                   int m, bool live, bool rot, int c0, int c1,
-                                                   const float* c, const float* s, float* dw) {
-  constexpr int LPR = D / 16, RPW = 32 / LPR;
-  const int sub = (threadIdx.x & 31) / LPR;
-  const uint8_t* x = t.x + 2 * (b * t.xb + m * t.xm);
-  const uint8_t* dy = t.dy + (G32 ? 4 : 2) * (b * t.gb + m * t.gm);
-  uint8_t* dx = t.dx + 2 * (b * t.db + m * t.dm);
-  if (!live) {  // padding: a zero gradient
-    for (int row = sub; row < t.heads; row += RPW) {
-      uint4* dst = reinterpret_cast<uint4*>(dx + 2 * row * t.dh);
-      dst[c0] = dst[c1] = make_uint4(0, 0, 0, 0);
-    }
-    return;
-  }
-  float w[16];
-  load_weights<BF16>(t.w, p.w32, c0, c1, w);
-  for (int r = 0; r < t.heads; r += RPW * UN) {
-    uint4 v[UN][2], g[UN][G32 ? 4 : 2];
-#pragma unroll
-    for (int u = 0; u < UN; ++u) {
-      const int row = r + u * RPW + sub;
-      v[u][0] = v[u][1] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int i = 0; i < (G32 ? 4 : 2); ++i) g[u][i] = make_uint4(0, 0, 0, 0);
-      if (row < t.heads) {
-        const uint4* src = reinterpret_cast<const uint4*>(x + 2 * row * t.xh);
-        v[u][0] = src[c0];
-        v[u][1] = src[c1];
-        if constexpr (G32) {
-          const uint4* gr = reinterpret_cast<const uint4*>(dy + 4 * row * t.gh);
-          g[u][0] = gr[2 * c0];
-          g[u][1] = gr[2 * c0 + 1];
-          g[u][2] = gr[2 * c1];
-          g[u][3] = gr[2 * c1 + 1];
-        } else {
-          const uint4* gr = reinterpret_cast<const uint4*>(dy + 2 * row * t.gh);
-          g[u][0] = gr[c0];
-          g[u][1] = gr[c1];
-        }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < UN; ++u) {
-      const int row = r + u * RPW + sub;
-      float f[16], y[16];
-      unpack8<BF16>(v[u][0], f);
-      unpack8<BF16>(v[u][1], f + 8);
-      if constexpr (G32) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          y[4 * i] = __uint_as_float(g[u][i].x);
-          y[4 * i + 1] = __uint_as_float(g[u][i].y);
-          y[4 * i + 2] = __uint_as_float(g[u][i].z);
-          y[4 * i + 3] = __uint_as_float(g[u][i].w);
-        }
-      } else {
-        unpack8<BF16>(g[u][0], y);
-        unpack8<BF16>(g[u][1], y + 8);
-      }
-      if (rot) {
-        float ns[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ns[i] = -s[i];
-        turn(y, c, ns, p.interleaved);
-      }
-      float sq = 0.f, gx = 0.f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        sq = fmaf(f[i], f[i], sq);
-        gx = fmaf(y[i] * w[i], f[i], gx);
-      }
-      sq = row_sum<LPR>(sq);
-      gx = row_sum<LPR>(gx);
-      const float rs = rsqrtf(sq * (1.f / D) + p.eps);
-      // rows past the heads hold zeros; with eps = 0 their rs is infinite
-      if (row < t.heads) {
-        const float k = gx * rs * rs * (1.f / D);  // mean(g w xhat) rs
-        float d[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          dw[i] = fmaf(y[i], f[i] * rs, dw[i]);
-          d[i] = rs * fmaf(-f[i], k, y[i] * w[i]);
-        }
-        uint4* dst = reinterpret_cast<uint4*>(dx + 2 * row * t.dh);
-        dst[c0] = pack8<BF16>(d);
-        dst[c1] = pack8<BF16>(d + 8);
-      }
-    }
+// The backward's lanes hold half as much of a row as the forward's, two
+// chunks of 4 entries: with the sums of dw, the weights and two inputs to keep,
+// 16 entries a lane left 16 warps an SM, too few loads in flight and too few
+// row sums to overlap (32,768 tokens of 64 + 8 heads at D = 128: 373 us).
+__device__ __forceinline__ void row_quads(int t, int half, int& c0, int& c1) {
+  const int pc = half >> 2;  // chunks of a half
+  if (t < pc) {
+    c0 = t;
+    c1 = t + pc;
+  } else {
+    c0 = 2 * t;
+    c1 = 2 * t + 1;
   }
 }
 
-// Sum of the 16 lane values over a warp's row groups, added by the lanes of
-// the first group into shared [D], warp after warp (a fixed order).
-template <int D>
-__device__ __forceinline__ void block_dw(const float* dw, int c0, int c1, float* sh) {
-  constexpr int LPR = D / 16;
-  float v[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    v[i] = dw[i];
-#pragma unroll
-    for (int o = LPR; o < 32; o <<= 1) v[i] += __shfl_xor_sync(kFull, v[i], o);
-  }
-  for (int wi = 0; wi < kRopeBwdThreads / 32; ++wi) {
-    if ((threadIdx.x >> 5) == wi && (threadIdx.x & 31) < LPR) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        sh[8 * c0 + i] = wi == 0 ? v[i] : sh[8 * c0 + i] + v[i];
-        sh[8 * c1 + i] = wi == 0 ? v[8 + i] : sh[8 * c1 + i] + v[8 + i];
-      }
-    }
-    __syncthreads();
-  }
+template <bool BF16>
+__device__ __forceinline__ void unpack4(const uint2& v, float* f) {
+  const float2 a = unpack2<BF16>(v.x), b = unpack2<BF16>(v.y);
+  f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
 }
 
-// Warps walk the tokens; a CTA leaves one dw partial per norm.
+__device__ __forceinline__ void load4(const float* p, float* f) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+}
+
+template <int LPR>
+__device__ __forceinline__ float wide_row_sum(float v) {
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+// A CTA works on the rows of Q or of K (so that a lane carries one norm's
+// sums) and leaves one partial dw. Warps walk the units.
 template <int D, bool BF16, bool G32, int UN>
-__global__ void __launch_bounds__(kRopeBwdThreads, 2)
-    norm_rope_bwd_kernel(const RopeBwdProblem pr) {
+__global__ void __launch_bounds__(kRopeBwdThreads, kRopeBwdPerSm)
+    norm_rope_bwd_kernel(const __grid_constant__ RopeBwdProblem pr) {
   const RopeProblem& p = pr.a;
-  constexpr int kWarps = kRopeBwdThreads / 32;
-  __shared__ float sh[2][D];
+  constexpr int LPR = D / 8, RPW = 32 / LPR, kWarps = kRopeBwdThreads / 32;
+  __shared__ float sh[kWarps][D];
+  const bool is_k = blockIdx.x >= static_cast<unsigned>(pr.q.ctas);
+  const RopeBwdRows& t = is_k ? pr.k : pr.q;
+  const int cta = static_cast<int>(blockIdx.x) - (is_k ? pr.q.ctas : 0);
   int c0, c1;
-  const int t = (threadIdx.x & 31) % (D / 16);
-  row_chunks(t, p.half, c0, c1);
-  const bool rot = t < (p.half >> 3);
-  float dwq[16], dwk[16];
+  const int lane = threadIdx.x & 31, tl = lane % LPR, sub = lane / LPR;
+  row_quads(tl, p.half, c0, c1);
+  const bool rot = tl < (p.half >> 2);
+  float dw[8], w[8];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) dwq[i] = dwk[i] = 0.f;
-  const int64_t tokens = static_cast<int64_t>(p.B) * p.M;
-  for (int64_t tok = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); tok < tokens;
-       tok += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const int b = static_cast<int>(static_cast<uint32_t>(tok) / static_cast<uint32_t>(p.M));
-    const int m = static_cast<int>(static_cast<uint32_t>(tok) - static_cast<uint32_t>(b) * p.M);
+  for (int i = 0; i < 8; ++i) {
+    dw[i] = 0.f;
+    w[i] = 1.f;
+  }
+  if (t.w != nullptr) {
+    if (p.w32) {
+      load4(static_cast<const float*>(t.w) + 4 * c0, w);
+      load4(static_cast<const float*>(t.w) + 4 * c1, w + 4);
+    } else {
+      unpack4<BF16>(static_cast<const uint2*>(t.w)[c0], w);
+      unpack4<BF16>(static_cast<const uint2*>(t.w)[c1], w + 4);
+    }
+  }
+  for (int64_t u = static_cast<int64_t>(cta) * kWarps + (threadIdx.x >> 5); u < t.units;
+       u += static_cast<int64_t>(t.ctas) * kWarps) {
+    const uint32_t tok = static_cast<uint32_t>(u) / static_cast<uint32_t>(t.segs);
+    const int seg = static_cast<int>(static_cast<uint32_t>(u) - tok * t.segs);
+    const int b = static_cast<int>(tok / static_cast<uint32_t>(p.M));
+    const int m = static_cast<int>(tok - static_cast<uint32_t>(b) * p.M);
+    const int r0 = seg * t.per, r1 = min(r0 + t.per, t.heads);
     const int64_t at = token_position(p, b, m);
-    const bool live = at >= 0;
-    float c[8], s[8];
-    if (live && rot) load_angles(p, at, c0, c1, c, s);
-    norm_rope_bwd_rows<D, BF16, G32, UN>(p, pr.q, b, m, live, rot, c0, c1, c, s, dwq);
-    norm_rope_bwd_rows<D, BF16, G32, UN>(p, pr.k, b, m, live, rot, c0, c1, c, s, dwk);
+    uint8_t* const dx = t.dx + 2 * (b * t.db + m * t.dm);
+    if (at < 0) {  // padding: a zero gradient
+      for (int row = r0 + sub; row < r1; row += RPW) {
+        uint2* dst = reinterpret_cast<uint2*>(dx + 2 * row * t.dh);
+        dst[c0] = dst[c1] = make_uint2(0, 0);
+      }
+      continue;
+    }
+    float c[4], s[4];
+    if (rot) {
+      const float* ct = p.cos_t + at * p.half;
+      const float* st = p.sin_t + at * p.half;
+      if (p.interleaved) {  // pairs 0, 1 of the first chunk, 2, 3 of the second
+        const float2 ca = *reinterpret_cast<const float2*>(ct + 2 * c0);
+        const float2 cb = *reinterpret_cast<const float2*>(ct + 2 * c1);
+        const float2 sa = *reinterpret_cast<const float2*>(st + 2 * c0);
+        const float2 sb = *reinterpret_cast<const float2*>(st + 2 * c1);
+        c[0] = ca.x, c[1] = ca.y, c[2] = cb.x, c[3] = cb.y;
+        s[0] = sa.x, s[1] = sa.y, s[2] = sb.x, s[3] = sb.y;
+      } else {
+        load4(ct + 4 * c0, c);
+        load4(st + 4 * c0, s);
+      }
+    }
+    const uint8_t* const x = t.x + 2 * (b * t.xb + m * t.xm);
+    const uint8_t* const dy = t.dy + (G32 ? 4 : 2) * (b * t.gb + m * t.gm);
+    for (int r = r0; r < r1; r += RPW * UN) {
+      uint2 v[UN][2];
+      uint4 g4[UN][G32 ? 2 : 1];  // fp32: the two chunks; 16 bits: both in one
+#pragma unroll
+      for (int k = 0; k < UN; ++k) {
+        const int row = r + k * RPW + sub;
+        v[k][0] = v[k][1] = make_uint2(0, 0);
+#pragma unroll
+        for (int i = 0; i < (G32 ? 2 : 1); ++i) g4[k][i] = make_uint4(0, 0, 0, 0);
+        if (row < r1) {
+          const uint2* src = reinterpret_cast<const uint2*>(x + 2 * row * t.xh);
+          v[k][0] = src[c0];
+          v[k][1] = src[c1];
+          if constexpr (G32) {
+            const uint4* gr = reinterpret_cast<const uint4*>(dy + 4 * row * t.gh);
+            g4[k][0] = gr[c0];
+            g4[k][1] = gr[c1];
+          } else {
+            const uint2* gr = reinterpret_cast<const uint2*>(dy + 2 * row * t.gh);
+            const uint2 ga = gr[c0], gb = gr[c1];
+            g4[k][0] = make_uint4(ga.x, ga.y, gb.x, gb.y);
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < UN; ++k) {
+        const int row = r + k * RPW + sub;
+        float f[8], y[8];
+        unpack4<BF16>(v[k][0], f);
+        unpack4<BF16>(v[k][1], f + 4);
+        if constexpr (G32) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            y[4 * i] = __uint_as_float(g4[k][i].x);
+            y[4 * i + 1] = __uint_as_float(g4[k][i].y);
+            y[4 * i + 2] = __uint_as_float(g4[k][i].z);
+            y[4 * i + 3] = __uint_as_float(g4[k][i].w);
+          }
+        } else {
+          unpack4<BF16>(make_uint2(g4[k][0].x, g4[k][0].y), y);
+          unpack4<BF16>(make_uint2(g4[k][0].z, g4[k][0].w), y + 4);
+        }
+        if (rot) {  // the opposite turn: (a, b) -> (a c + b s, b c - a s)
+          if (p.interleaved) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float a = y[2 * j], e = y[2 * j + 1];
+              y[2 * j] = a * c[j] + e * s[j];
+              y[2 * j + 1] = e * c[j] - a * s[j];
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float a = y[j], e = y[j + 4];
+              y[j] = a * c[j] + e * s[j];
+              y[j + 4] = e * c[j] - a * s[j];
+            }
+          }
+        }
+        float sq = 0.f, gx = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          sq = fmaf(f[i], f[i], sq);
+          gx = fmaf(y[i] * w[i], f[i], gx);
+        }
+        sq = wide_row_sum<LPR>(sq);
+        gx = wide_row_sum<LPR>(gx);
+        // rows past the heads hold zeros (with eps = 0 their rs is infinite)
+        if (row < r1) {
+          const float rs = rsqrtf(sq * (1.f / D) + p.eps);
+          const float kx = gx * rs * rs * (1.f / D);  // mean(g w xhat) rs
+          float d[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            dw[i] = fmaf(y[i], f[i] * rs, dw[i]);
+            d[i] = rs * fmaf(-f[i], kx, y[i] * w[i]);
+          }
+          uint2* dst = reinterpret_cast<uint2*>(dx + 2 * row * t.dh);
+          dst[c0] = make_uint2(pack2_t<BF16>(d[0], d[1]), pack2_t<BF16>(d[2], d[3]));
+          dst[c1] = make_uint2(pack2_t<BF16>(d[4], d[5]), pack2_t<BF16>(d[6], d[7]));
+        }
+      }
+    }
   }
   if (pr.part == nullptr) return;
-  block_dw<D>(dwq, c0, c1, sh[0]);
-  block_dw<D>(dwk, c0, c1, sh[1]);
-  for (int i = threadIdx.x; i < 2 * D; i += kRopeBwdThreads)
-    pr.part[static_cast<int64_t>(blockIdx.x) * (2 * D) + i] = sh[i / D][i % D];
+  // the row groups of a warp, then the warps, in a fixed order
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+#pragma unroll
+    for (int o = LPR; o < 32; o <<= 1) dw[i] += __shfl_xor_sync(kFull, dw[i], o);
+  }
+  if (sub == 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sh[threadIdx.x >> 5][4 * c0 + i] = dw[i];
+      sh[threadIdx.x >> 5][4 * c1 + i] = dw[4 + i];
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) v += sh[i][threadIdx.x];
+    pr.part[static_cast<int64_t>(blockIdx.x) * D + threadIdx.x] = v;
+  }
 }
 
-// dw from the CTAs' partials: a CTA sums 32 columns, 32 rows of partials side
-// by side, in a fixed order.
+// dw from the CTAs' partials: a CTA sums 32 columns of dwq or dwk, 32 rows of
+// partials side by side, in a fixed order.
 template <int D>
 __global__ void __launch_bounds__(1024)
-    norm_rope_dw_kernel(const float* part, int parts, float* dwq, float* dwk) {
+    norm_rope_dw_kernel(const float* part, int q_ctas, int k_ctas, float* dwq, float* dwk) {
   __shared__ float sh[32][33];
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-  const int col = blockIdx.x * 32 + x;
+  const bool is_k = blockIdx.y == 1;
+  const float* src = part + (is_k ? static_cast<int64_t>(q_ctas) * D : 0) + blockIdx.x * 32 + x;
+  const int rows = is_k ? k_ctas : q_ctas;
   float v = 0.f;
-  for (int r = y; r < parts; r += 32) v += part[static_cast<int64_t>(r) * (2 * D) + col];
+  for (int r = y; r < rows; r += 32) v += src[static_cast<int64_t>(r) * D];
   sh[y][x] = v;
   __syncthreads();
   v = sh[x][y];  // the 32 sums of column y of this CTA
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-  if (x == 0) {
-    const int out = blockIdx.x * 32 + y;
-    float* dst = out < D ? dwq : dwk;
-    if (dst != nullptr) dst[out < D ? out : out - D] = v;
-  }
+  float* dst = is_k ? dwk : dwq;
+  if (x == 0 && dst != nullptr) dst[blockIdx.x * 32 + y] = v;
 }
 
 // ---- host ---------------------------------------------------------------
@@ -486,12 +543,29 @@ int check_tables(const float* cos_t, const float* sin_t, const int32_t* position
   return aligned(positions, 4) ? NSA_OK : NSA_ERR_ALIGN;
 }
 
-// CTAs of the backward, each with one dw partial: enough warps for the
-// loads of every SM (2 CTAs of 8 warps an SM at its registers), one warp a
-// token below that.
-int rope_bwd_ctas(int64_t tokens) {
-  const int64_t c = (tokens + kRopeBwdThreads / 32 - 1) / (kRopeBwdThreads / 32);
-  return static_cast<int>(c < 2 * kRopeSms ? c : 2 * kRopeSms);
+// Most CTAs of the backward, each with one dw partial: what the SMs hold at
+// once, for Q and K together; one of each at least.
+constexpr int kRopeBwdCtas = kRopeBwdPerSm * kRopeSms;
+
+int rope_bwd_most_ctas(int64_t B, int64_t M) {
+  const int64_t tokens = B * M;
+  return tokens == 0 ? 0 : kRopeBwdCtas;
+}
+
+// A token's heads in units of `per` (a multiple of a warp's rows): whole
+// tokens when they alone give every warp of `ctas` one, else as few heads as
+// it takes. Fewer CTAs where the units do not fill them.
+void plan_rope_rows(RopeBwdRows& t, int64_t tokens, int rows_per_warp, int ctas) {
+  const int64_t warps = static_cast<int64_t>(ctas) * (kRopeBwdThreads / 32);
+  const int64_t most = (t.heads + rows_per_warp - 1) / rows_per_warp;
+  int64_t segs = (warps + tokens - 1) / tokens;
+  if (segs > most) segs = most;
+  const int64_t per = ((t.heads + segs - 1) / segs + rows_per_warp - 1) / rows_per_warp * rows_per_warp;
+  t.per = static_cast<int>(per);
+  t.segs = static_cast<int>((t.heads + per - 1) / per);
+  t.units = tokens * t.segs;
+  const int64_t need = (t.units + kRopeBwdThreads / 32 - 1) / (kRopeBwdThreads / 32);
+  t.ctas = static_cast<int>(need < ctas ? need : ctas);
 }
 
 template <int D, bool BF16>
@@ -517,12 +591,18 @@ int launch_norm_rope(const RopeProblem& p, cudaStream_t st) {
 }
 
 template <int D, bool BF16, bool G32>
-int launch_norm_rope_bwd(const RopeBwdProblem& p, float* dwq, float* dwk, cudaStream_t st) {
-  const int ctas = rope_bwd_ctas(static_cast<int64_t>(p.a.B) * p.a.M);
-  norm_rope_bwd_kernel<D, BF16, G32, 1><<<ctas, kRopeBwdThreads, 0, st>>>(p);
+int launch_norm_rope_bwd(RopeBwdProblem& p, float* dwq, float* dwk, cudaStream_t st) {
+  constexpr int RPW = 32 / (D / 8);
+  const int64_t tokens = static_cast<int64_t>(p.a.B) * p.a.M;
+  const int64_t gq = (p.q.heads + RPW - 1) / RPW, gk = (p.k.heads + RPW - 1) / RPW;
+  int k_ctas = static_cast<int>((kRopeBwdCtas * gk + (gq + gk) / 2) / (gq + gk));
+  k_ctas = k_ctas < 1 ? 1 : k_ctas > kRopeBwdCtas - 1 ? kRopeBwdCtas - 1 : k_ctas;
+  plan_rope_rows(p.q, tokens, RPW, kRopeBwdCtas - k_ctas);
+  plan_rope_rows(p.k, tokens, RPW, k_ctas);
+  norm_rope_bwd_kernel<D, BF16, G32, G32 ? 2 : 2><<<p.q.ctas + p.k.ctas, kRopeBwdThreads, 0, st>>>(p);
   if (cudaGetLastError() != cudaSuccess) return NSA_ERR_LAUNCH;
   if (p.part != nullptr) {
-    norm_rope_dw_kernel<D><<<2 * D / 32, 1024, 0, st>>>(p.part, ctas, dwq, dwk);
+    norm_rope_dw_kernel<D><<<dim3(D / 32, 2), 1024, 0, st>>>(p.part, p.q.ctas, p.k.ctas, dwq, dwk);
     if (cudaGetLastError() != cudaSuccess) return NSA_ERR_LAUNCH;
   }
   return NSA_OK;
@@ -575,7 +655,7 @@ extern "C" int64_t nsa_qk_norm_rope_bwd_workspace_bytes(int64_t B, int64_t M, in
   using namespace nsa;
   const int rc = check_rope(B, M, 1, 1, D, 0, 0, 0, 0.f, NSA_F16, NSA_F32);
   if (rc != NSA_OK) return rc;
-  return (static_cast<int64_t>(rope_bwd_ctas(B * M)) * 2 * D * 4 + 255) / 256 * 256;
+  return static_cast<int64_t>(rope_bwd_most_ctas(B, M)) * D * 4;
 }
 
 extern "C" int nsa_qk_norm_rope_bwd(
@@ -623,9 +703,9 @@ extern "C" int nsa_qk_norm_rope_bwd(
   p.a.w32 = weight_dtype == NSA_F32;
   p.a.eps = eps;
   p.q = {static_cast<const uint8_t*>(Q), static_cast<const uint8_t*>(dQo), static_cast<uint8_t*>(dQ),
-         wq, s[0], s[1], s[2], s[6], s[7], s[8], s[12], s[13], s[14], static_cast<int>(H)};
+         wq, s[0], s[1], s[2], s[6], s[7], s[8], s[12], s[13], s[14], static_cast<int>(H), 0, 0, 0, 0};
   p.k = {static_cast<const uint8_t*>(K), static_cast<const uint8_t*>(dKo), static_cast<uint8_t*>(dK),
-         wk, s[3], s[4], s[5], s[9], s[10], s[11], s[15], s[16], s[17], static_cast<int>(G)};
+         wk, s[3], s[4], s[5], s[9], s[10], s[11], s[15], s[16], s[17], static_cast<int>(G), 0, 0, 0, 0};
   p.part = want_dw ? static_cast<float*>(workspace) : nullptr;
   const bool bf = dtype == NSA_BF16, g32 = grad_dtype == NSA_F32;
   if (D == 64) {
