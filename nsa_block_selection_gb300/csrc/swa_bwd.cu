@@ -1108,18 +1108,18 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       for (int t = 0; t < it.nt; ++t, ++n) {
         const int i0 = (it.u0 + u) * kStep, ic = i0 + kHalf * wg;
         if (++u == it.nq) u = 0;
-        // The stage's nlse2 and ndelta first, while S is being formed: a wait
-        // costs some 100 clocks even when it is over, and S is on the chain.
-        // With two buffers S and dP are mostly there: one question for all.
-        bool there = false;
-        if constexpr (C::kBuf == 2) {
-          const bool x0 = mbar_try_wait(bar(C::kFull + st), ph);
-          const bool x1 = mbar_try_wait(bar(C::kSFull + gb + (n & 1)), (n >> 1) & 1);
-          const bool x2 = mbar_try_wait(bar(C::kDpFull + gb + (n & 1)), (n >> 1) & 1);
-          there = __all_sync(kFull, x0 && x1 && x2);
-          if (there) tc_fence_after();
-        }
-        if (!there && !wait_all(C::kFull + st, ph)) {
+        // S and the stage's nlse2 and ndelta (and, with two buffers, dP, which
+        // is mostly there as well): one question for all. A wait of its own
+        // for the stage took 330 of a step's 1300 clocks, although it was over:
+        // barrier operations are slow beside the operand traffic.
+        const int sb = C::kSFull + gb + (n & 1), db = C::kDpFull + gb + (n & 1);
+        const uint32_t np = (n >> 1) & 1;
+        const bool x0 = mbar_try_wait(bar(C::kFull + st), ph), x1 = mbar_try_wait(bar(sb), np);
+        const bool x2 = C::kBuf == 2 ? mbar_try_wait(bar(db), np) : false;
+        const bool dp_there = C::kBuf == 2 && __all_sync(kFull, x2);
+        if (__all_sync(kFull, x0 && x1)) {
+          tc_fence_after();
+        } else if (!wait_all(C::kFull + st, ph) || !wait_all(sb, np)) {
           failed = true;
           break;
         }
@@ -1138,10 +1138,6 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         const uint32_t seen = edge ? seen_bits(lo_j - ic, hi_j - ic) : 0u;
         uint32_t s[32];
         uint64_t pr[16];
-        if (!there && !wait_all(C::kSFull + gb + (n & 1), (n >> 1) & 1)) {
-          failed = true;
-          break;
-        }
         tc_ld32(sa, s);
         tc_wait_ld();
 #pragma unroll
@@ -1164,7 +1160,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::kPFull + gb + (n & 1)));
-        if (!there && !wait_all(C::kDpFull + gb + (n & 1), (n >> 1) & 1)) {
+        if (!dp_there && !wait_all(db, np)) {
           failed = true;
           break;
         }
