@@ -497,7 +497,8 @@ int64_t nsa_swa_bwd_workspace_bytes(int64_t B, int64_t M, int64_t N, int64_t H, 
  * share a tile with visible ones: K must be finite in the 64-key tiles that
  * hold a key some query of a 128-query tile sees, Q and dO in the 64-query
  * tiles that hold a query which sees some key of a 128-key tile (as V must for
- * the forward, in 128-key tiles). M and N are at most 2^29.
+ * the forward, in 128-key tiles). M and N are at most 2^29. The outputs must
+ * not overlap the inputs.
  *
  * Asynchronous: two kernels on `stream` (three where dK, dV are joined from
  * parts), no allocation; calls that may overlap need workspaces of their own.
@@ -558,7 +559,7 @@ int nsa_qk_norm_rope(const void* Q, const void* K, void* Qo, void* Ko, const voi
 
 /*
  * nsa_qk_norm_rope_bwd_workspace_bytes -- device workspace of
- * nsa_qk_norm_rope_bwd: a partial weight gradient of each of up to 304 CTAs. Negative nsa_status for invalid sizes. Pure host arithmetic.
+ * nsa_qk_norm_rope_bwd: a partial weight gradient of each of up to 456 CTAs. Negative nsa_status for invalid sizes. Pure host arithmetic.
  */
 int64_t nsa_qk_norm_rope_bwd_workspace_bytes(int64_t B, int64_t M, int64_t D);
 

@@ -478,6 +478,49 @@ def swa_fwd(q, k, v, window=(-1, -1), scale: Optional[float] = None, out=None, l
     return out, lse
 
 
+# The calls below may be a single token's work, beside which every property
+# read and every import statement counts: torch is looked up once, each
+# property is read once, and names are given only where a check failed.
+_torch = None
+_F16_KINDS = ()
+_DTYPE_CODES = {}
+
+
+def _bind_torch():
+    global _torch, _F16_KINDS
+    import torch
+
+    _torch = torch
+    _F16_KINDS = (torch.float16, torch.bfloat16)
+    _DTYPE_CODES.update({torch.float16: NSA_F16, torch.bfloat16: NSA_BF16, torch.float32: NSA_F32})
+
+
+def _launch(dev, fn, *args):
+    """fn(*args, cudaStream_t) on device ``dev`` and its current stream."""
+    c = _torch._C
+    if c._cuda_getDevice() == dev:
+        return fn(*args, c._cuda_getCurrentRawStream(dev))
+    with _torch.cuda.device(dev):
+        return fn(*args, c._cuda_getCurrentRawStream(dev))
+
+
+def _on_stream(call):
+    """A ``stream`` argument for a call that runs on the current stream: what
+    the call allocates (a workspace that it drops on return among it) then
+    comes from that stream's memory, and waits for that stream's work."""
+    import functools
+
+    @functools.wraps(call)
+    def run(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        load()
+        with _torch.cuda.stream(stream):
+            return call(*args, **kw)
+
+    return run
+
+
 def swa_bwd_workspace_bytes(B, M, N, H, H_kv, D, window=(-1, -1)) -> int:
     n = load().nsa_swa_bwd_workspace_bytes(B, M, N, H, H_kv, D, int(window[0]), int(window[1]))
     if n < 0:
@@ -485,8 +528,9 @@ def swa_bwd_workspace_bytes(B, M, N, H, H_kv, D, window=(-1, -1)) -> int:
     return int(n)
 
 
+@_on_stream
 def swa_bwd(q, k, v, o, lse, do, window=(-1, -1), scale: Optional[float] = None, dq=None, dk=None,
-            dv=None, grad_dtype=None, workspace=None, stream=None):
+            dv=None, grad_dtype=None, workspace=None):
     """Gradients of :func:`swa_fwd` (nsa_swa_bwd): returns (dQ, dK, dV).
 
     q, k, v, ``window`` and ``scale`` as passed to the forward, ``o`` and
@@ -494,7 +538,9 @@ def swa_bwd(q, k, v, o, lse, do, window=(-1, -1), scale: Optional[float] = None,
     [B, M, H, D]); all contiguous on one CUDA device. The gradients are of
     q's dtype, or fp32 with ``grad_dtype=torch.float32`` (or preallocated
     ones). ``workspace`` (CUDA uint8, swa_bwd_workspace_bytes) is allocated
-    when omitted; calls that may overlap need one each.
+    when omitted; calls that may overlap need one each. Runs on torch's current
+    stream, or on ``stream`` (a keyword; what it allocates is then allocated
+    on it too).
     """
     lib = _lib or load()
     dt, qs, ks = q.dtype, q.shape, k.shape
@@ -538,7 +584,7 @@ def swa_bwd(q, k, v, o, lse, do, window=(-1, -1), scale: Optional[float] = None,
         if workspace.get_device() != dev:
             raise ValueError("workspace must be on q's CUDA device")
     # scale: the ABI takes <= 0 for 1/sqrt(D)
-    st = _launch(dev, stream, lib.nsa_swa_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+    st = _launch(dev, lib.nsa_swa_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                  o.data_ptr(), lse.data_ptr(), do.data_ptr(), dq.data_ptr(), dk.data_ptr(),
                  dv.data_ptr(), B, M, N, H, Hkv, D, left, right, 0.0 if scale is None else scale,
                  _DTYPE_CODES[dt], _DTYPE_CODES[grad_dtype], workspace.data_ptr(), nbytes)
@@ -561,33 +607,6 @@ def rope_tables(rows: int, rot_dim: int, base: float = 10000.0, device="cuda"):
     freq = float(base) ** (-torch.arange(half, dtype=torch.float64, device=device) / half)
     ang = torch.arange(rows, dtype=torch.float64, device=device)[:, None] * freq
     return ang.cos().float(), ang.sin().float()
-
-
-# The calls below may be a single token's work, beside which every property
-# read and every import statement counts: torch is looked up once, each
-# property is read once, and names are given only where a check failed.
-_torch = None
-_F16_KINDS = ()
-_DTYPE_CODES = {}
-
-
-def _bind_torch():
-    global _torch, _F16_KINDS
-    import torch
-
-    _torch = torch
-    _F16_KINDS = (torch.float16, torch.bfloat16)
-    _DTYPE_CODES.update({torch.float16: NSA_F16, torch.bfloat16: NSA_BF16, torch.float32: NSA_F32})
-
-
-def _launch(dev, stream, fn, *args):
-    """fn(*args, cudaStream_t) with device ``dev`` current."""
-    c = _torch._C
-    st = c._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if c._cuda_getDevice() == dev:
-        return fn(*args, st)
-    with _torch.cuda.device(dev):
-        return fn(*args, st)
 
 
 def _at(t):
@@ -674,9 +693,9 @@ def _check_rope(named, q_weight, k_weight, cos, sin, positions):
         NSA_F32 if wdt is None else _DTYPE_CODES[wdt], strides
 
 
+@_on_stream
 def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
-                 eps: float = 1e-6, interleaved: bool = False, q_out=None, k_out=None,
-                 stream=None):
+                 eps: float = 1e-6, interleaved: bool = False, q_out=None, k_out=None):
     """RMS norm of every query and key head and the position rotation, in one
     pass (nsa_qk_norm_rope).
 
@@ -689,7 +708,8 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positio
     ``interleaved``; None: no rotation. ``positions``: int32 [B, M] or [M]
     table rows of the tokens (None: 0 .. M - 1); a position outside the table
     marks padding, whose output rows are zero. The outputs may be the inputs.
-    Returns (q_out, k_out).
+    Runs on torch's current stream, or on ``stream`` (a keyword; the outputs
+    are then allocated on it too). Returns (q_out, k_out).
     """
     lib = _lib or load()
     if q_out is None:
@@ -700,7 +720,7 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positio
     dev, sizes, code, wcode, strides = _check_rope(
         (("q", q, own), ("k", k, own), ("q_out", q_out, own), ("k_out", k_out, own)), q_weight,
         k_weight, cos, sin, positions)
-    st = _launch(dev, stream, lib.nsa_qk_norm_rope, q.data_ptr(), k.data_ptr(), q_out.data_ptr(),
+    st = _launch(dev, lib.nsa_qk_norm_rope, q.data_ptr(), k.data_ptr(), q_out.data_ptr(),
                  k_out.data_ptr(), _at(q_weight), _at(k_weight), _at(cos), _at(sin),
                  _at(positions), *sizes, eps, 1 if interleaved else 0, code, wcode,
                  None if strides is None else strides.buffer_info()[0])
@@ -716,10 +736,11 @@ def norm_rope_bwd_workspace_bytes(B, M, D) -> int:
     return n
 
 
+@_on_stream
 def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, cos=None, sin=None,
                      positions=None, eps: float = 1e-6, interleaved: bool = False, dq=None,
                      dk=None, dq_weight=None, dk_weight=None, weight_grads: bool = True,
-                     workspace=None, stream=None):
+                     workspace=None):
     """Gradients of :func:`qk_norm_rope` (nsa_qk_norm_rope_bwd).
 
     q, k and the arguments after them are the forward's; ``dq_out``,
@@ -728,7 +749,7 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, cos=Non
     the forward. Returns (dq, dk, dq_weight, dk_weight): dq, dk of q's dtype,
     the weights' gradients fp32 [D] (None with ``weight_grads=False``).
     ``workspace`` (CUDA uint8, norm_rope_bwd_workspace_bytes) is allocated
-    when omitted.
+    when omitted. ``stream``: as in the forward.
     """
     lib = _lib or load()
     if dq is None:
@@ -761,7 +782,7 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, cos=Non
                 raise ValueError("workspace must be on q's CUDA device")
     else:
         dq_weight = dk_weight = workspace = None
-    st = _launch(dev, stream, lib.nsa_qk_norm_rope_bwd, q.data_ptr(), k.data_ptr(),
+    st = _launch(dev, lib.nsa_qk_norm_rope_bwd, q.data_ptr(), k.data_ptr(),
                  dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(),
                  _at(dq_weight), _at(dk_weight), _at(q_weight), _at(k_weight), _at(cos), _at(sin),
                  _at(positions), *sizes, eps, 1 if interleaved else 0, code, wcode,

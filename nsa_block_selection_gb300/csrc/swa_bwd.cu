@@ -95,6 +95,12 @@ __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
 }
 
+// An auxiliary warp waits for a whole item of `steps` steps at a time, which
+// 1 s may not hold: 20 us more for each of them (they take under 1 us).
+__device__ __forceinline__ uint64_t item_limit_ns(int steps) {
+  return kWaitLimitNs + 20000ull * static_cast<uint64_t>(steps);
+}
+
 // A matrix descriptor moved by `bytes`: the address field takes the sum as
 // it is (shared memory ends below its 2^18 bytes), and an addition leaves the
 // issuing warp less to do per MMA than building the descriptor again.
@@ -549,7 +555,11 @@ __global__ void __launch_bounds__(kDqThreads, 1)
           const uint4 v = chunk(src, c);
           r[4 * c] = v.x, r[4 * c + 1] = v.y, r[4 * c + 2] = v.z, r[4 * c + 3] = v.w;
         }
-        if (n > 0 && !wait_all(done, (n - 1) & 1)) return false;
+        if (n > 0) {
+          if (!__all_sync(kFull, wait_phase(bar(done), (n - 1) & 1, item_limit_ns(last.nt))))
+            return false;
+          tc_fence_after();
+        }
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
           tc_st32(lane_addr + col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&r[32 * c]));
@@ -1061,7 +1071,11 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                                                           (((c & 7) ^ (row & 7)) << 4));
           r[4 * c] = v.x, r[4 * c + 1] = v.y, r[4 * c + 2] = v.z, r[4 * c + 3] = v.w;
         }
-        if (n > 0 && !wait_all(done, (n - 1) & 1)) return false;
+        if (n > 0) {
+          if (!__all_sync(kFull, wait_phase(bar(done), (n - 1) & 1, item_limit_ns(last.nt))))
+            return false;
+          tc_fence_after();
+        }
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
           tc_st32(lane_addr + col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&r[32 * c]));
@@ -1231,7 +1245,10 @@ __global__ void __launch_bounds__(256) swa_bwd_join_kernel(const SwaBwdProblem p
 // ---------------------------------------------------------------- host
 
 constexpr int kSms = 152;
+// In steps of the dK, dV kernel (0.7 us): what an item costs beside its steps, the
+// fewest steps of a part, the launch of the join and a part's 128 KB through it.
 constexpr int kItemSteps = 3, kMinSteps = 4, kJoinSteps = 6;
+constexpr double kPartSteps = 0.05;
 
 int check_swa_bwd(int64_t B, int64_t M, int64_t N, int64_t H, int64_t H_kv, int64_t D) {
   if (B < 0 || M < 0 || N < 0 || H <= 0 || H_kv <= 0) return NSA_ERR_SHAPE;
@@ -1273,7 +1290,7 @@ KeyTiles key_tiles(int64_t B, int64_t M, int64_t N, int64_t H, int64_t H_kv, int
   for (int s = 2; s <= 16 && steps / s >= kMinSteps; ++s) {
     const double t = static_cast<double>((rest * s + kSms - 1) / kSms) *
                          (static_cast<double>(steps) / s + kItemSteps) +
-                     kJoinSteps;
+                     kJoinSteps + kPartSteps * rest * s;
     if (t < best) {
       best = t;
       k.whole = k.tiles - rest;

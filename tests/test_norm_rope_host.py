@@ -70,8 +70,8 @@ def test_gradient_type_and_workspace(lib):
     need = _lib.norm_rope_bwd_workspace_bytes(2, 100, 128)
     assert _bwd(lib, ws_bytes=need - 1) == -9
     f = lib.nsa_qk_norm_rope_bwd_workspace_bytes
-    assert f(2, 100, 128) == 304 * 128 * 4
-    assert f(1, 1 << 20, 64) == 304 * 64 * 4
+    assert f(2, 100, 128) == 456 * 128 * 4
+    assert f(1, 1 << 20, 64) == 456 * 64 * 4
     assert f(1, 100, 80) == -4 and f(-1, 100, 64) == -2 and f(0, 0, 64) == 0
 
 

@@ -265,6 +265,58 @@ def test_large_sampled(D, window):
     assert ((out[2][0, :, g].double() - dv).abs() <= bound).all()
 
 
+def test_offsets_past_32_bits():
+    """More than 2^31 entries of Q: the last queries against the same rows on
+    their own (a slice that starts at a multiple of both tiles, so that every
+    sum is the same one)."""
+    import torch
+
+    from nsa_block_selection_gb300 import swa_bwd
+
+    M, H, D, window, cut = 131_200, 128, 128, (64, 0), 130_560
+    g = torch.Generator(device="cuda").manual_seed(18)
+    big = [torch.empty(1, M, H, D, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    q, o, do = (t.normal_(generator=g) for t in big)
+    k, v = (torch.randn(1, M, 1, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    lse = torch.full((1, H, M), 8.0, device="cuda")
+    assert q.numel() > 2 ** 31
+    a = swa_bwd(q, k, v, o, lse, do, window=window)
+    tail = [t[:, cut:].contiguous() for t in (q, k, v, o)] + [lse[:, :, cut:].contiguous(),
+                                                             do[:, cut:].contiguous()]
+    b = swa_bwd(*tail, window=window)
+    assert torch.equal(a[0][:, cut + 128:], b[0][:, 128:])  # (whose windows lie in the slice)
+    assert torch.isfinite(a[0][:, cut + 128:]).all() and a[0][:, -1].abs().max() > 0
+    for x, y in ((a[1], b[1]), (a[2], b[2])):
+        # the last tiles may be cut into other parts: one rounding apart
+        x, y = x[:, cut:].float(), y.float()
+        assert ((x - y).abs() <= 2.0 ** -7 * y.abs().clamp(min=1e-3)).all()
+
+
+def test_own_stream_allocations():
+    """On a side stream, what the call allocates and drops is not handed to the
+    current stream's work while the side stream still runs."""
+    import torch
+
+    from nsa_block_selection_gb300 import swa_bwd
+
+    t = _problem(1, 2000, 2000, 8, 2, 128, "bf16", (300, 0), 19)
+    want = swa_bwd(*t, window=(300, 0))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    busy = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            for _ in range(4):
+                busy = busy @ busy  # the side stream is late
+        got = swa_bwd(*t, window=(300, 0), stream=side)
+        junk = [torch.full((1 << 22,), float("nan"), device="cuda") for _ in range(8)]
+        torch.cuda.current_stream().wait_stream(side)
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
+        del junk
+
+
 def test_refusals_on_the_device():
     import torch
 

@@ -55,8 +55,8 @@ def test_workspace(lib):
     # 12 key tiles of (batch, KV head), 3 query blocks x 8 heads = 24 steps each:
     # cut into 6 parts of 4
     assert f(2, 300, 300, 16, 2, 128, 64, 0) == stat + 12 * 6 * tile
-    # 8 x 64 tiles = 3 rounds of 152 and 56 more, cut into 5 parts: 2 rounds of a fifth
-    assert f(1, 8192, 8192, 64, 8, 128, 512, 0) == 2 * 64 * 8192 * 4 + 56 * 5 * tile
+    # 8 x 64 tiles = 3 rounds of 152 and 56 more, cut in two
+    assert f(1, 8192, 8192, 64, 8, 128, 512, 0) == 2 * 64 * 8192 * 4 + 56 * 2 * tile
     # uneven tiles, more than the SMs: whole
     assert f(1, 8192, 8192, 64, 8, 128, -1, 0) == 2 * 64 * 8192 * 4
     assert f(1, 0, 300, 16, 2, 128, -1, -1) == 0 and f(1, 300, 0, 16, 2, 128, -1, -1) == 0
