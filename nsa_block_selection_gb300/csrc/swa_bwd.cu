@@ -141,27 +141,19 @@ __device__ __forceinline__ uint64_t ex2_2(uint64_t x) {
   return pair(ex2(v.x), ex2(v.y));
 }
 
-// 32 or 16 columns of this thread's lane.
-__device__ __forceinline__ void tc_ld(uint32_t taddr, uint32_t (&r)[32]) { tc_ld32(taddr, r); }
-__device__ __forceinline__ void tc_ld(uint32_t taddr, uint32_t (&r)[16]) { tc_ld16(taddr, r); }
-// 16 or 8.
-__device__ __forceinline__ void tc_st(uint32_t taddr, const uint32_t (&r)[16]) { tc_st16(taddr, r); }
-__device__ __forceinline__ void tc_st(uint32_t taddr, const uint32_t (&r)[8]) { tc_st8(taddr, r); }
-
 // Bit c set: column c of 32 lies in [lo, hi].
 __device__ __forceinline__ uint32_t seen_bits(int lo, int hi) {
   const uint32_t below = hi < 0 ? 0u : hi >= 31 ? ~0u : (2u << hi) - 1u;
   return lo <= 0 ? below : lo > 31 ? 0u : below & (~0u << lo);
 }
 
-// Zeroes the 16-bit entries of 2 N columns whose bit is clear, whatever they
+// Zeroes the 16-bit entries of 32 columns whose bit is clear, whatever they
 // hold: four bits at a time are multiplied onto the sign bits of a word's
 // bytes, and byte permutes that repeat those signs make the masks. (A compare
 // and a select for every entry took 650 clocks a step longer.)
-template <int N>
-__device__ __forceinline__ void keep_seen(uint32_t (&w)[N], uint32_t bits) {
+__device__ __forceinline__ void keep_seen(uint32_t (&w)[16], uint32_t bits) {
 #pragma unroll
-  for (int g = 0; g < N / 2; ++g) {
+  for (int g = 0; g < 8; ++g) {
     const uint32_t y = ((bits >> (4 * g)) & 0xfu) * 0x10204080u;
     uint32_t a, b;
     asm("prmt.b32 %0, %1, 0, 0x9988;\n" : "=r"(a) : "r"(y));
@@ -171,26 +163,16 @@ __device__ __forceinline__ void keep_seen(uint32_t (&w)[N], uint32_t bits) {
   }
 }
 
-// The elementwise warps of a kernel: two warpgroups, 32 columns of a step's 64
-// to a thread, keep up with the products at D = 128. At D = 64 the products
-// take half as long and the elementwise work bounds the kernels: there are two
-// such pairs, for the even and the odd steps (S and dP have two buffers), so
-// that one pair's waits pass during the other's arithmetic; their threads go
-// through their columns 16 at a time, to fit 80 registers.
-// (2 x 16 heads, 1500 x 2048, dense, D = 64: dK/dV @DKV@, dQ @DQ@.)
-template <int D>
-struct Ew {
-  static constexpr bool kAlt = D == 64;
-  static constexpr int kWarps = kAlt ? 16 : 8;
-  static constexpr int kChunk = kAlt ? 16 : 32;  // columns at a time
-  // the other warps
-  static constexpr int kAux = kWarps, kTma = kAux + 4, kMma = kTma + 1;
-  // where the 16 columns kk of a step's P or dS lie, as an A operand: the
-  // 16-bit columns are written over the first half of their chunk's 32-bit ones
-  static __device__ __forceinline__ uint32_t a_col(int kk) {
-    return kAlt ? kk * 16 : (kk >> 1) * 32 + (kk & 1) * 8;
-  }
-};
+// Warps of both kernels: two elementwise warpgroups, each with 32 of a step's
+// 64 columns to a thread, an auxiliary warpgroup, the TMA warp, the MMA warps.
+// (At D = 64, where the elementwise work bounds the kernels, two pairs of
+// warpgroups for the even and the odd steps took 65 to 69 us against 69 for
+// dK/dV of 2 x 16 heads of 1500 x 2048, and 48 against 47 for dQ: not kept.)
+constexpr int kAuxWarp = 8, kTmaWarp = 12, kMmaWarp = 13;
+
+// The 16 columns kk of a step's P or dS as an A operand: each warpgroup writes
+// its 16-bit columns over the first half of its 32-bit ones.
+__device__ __forceinline__ uint32_t step_col(int kk) { return (kk >> 1) * 32 + (kk & 1) * 8; }
 
 template <bool BF16>
 __device__ __forceinline__ float lo16(uint32_t v) {
@@ -294,14 +276,13 @@ __device__ __forceinline__ DqItem dq_item(const SwaBwdProblem& p, uint32_t x) {
 }
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(32 * (Ew<D>::kMma + 1), 1)
+__global__ void __launch_bounds__(32 * (kMmaWarp + 1), 1)
     swa_bwd_dq_kernel(const SwaBwdProblem p, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CUtensorMap tmQ,
                       const __grid_constant__ CUtensorMap tmO,
                       const __grid_constant__ CUtensorMap tmDo) {
   using C = DqCfg<D>;
-  using E = Ew<D>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -327,7 +308,7 @@ __global__ void __launch_bounds__(32 * (Ew<D>::kMma + 1), 1)
     mbar_init(bar(C::kDqFree), 4);
     fence_mbar_init();
   }
-  if (warp == E::kMma) {
+  if (warp == kMmaWarp) {
     tc_alloc(base + C::kOffTmem, kTmemAll);
     tc_relinquish();
   }
@@ -350,7 +331,7 @@ __global__ void __launch_bounds__(32 * (Ew<D>::kMma + 1), 1)
     return k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
   };
 
-  if (warp == E::kTma) {
+  if (warp == kTmaWarp) {
     if (lane == 0) {
       // ---- TMA producer: K and V tiles of 64 keys ----
       tma_prefetch_desc(&tmK);
@@ -391,7 +372,7 @@ __global__ void __launch_bounds__(32 * (Ew<D>::kMma + 1), 1)
         }
       }
     }
-  } else if (warp == E::kMma) {
+  } else if (warp == kMmaWarp) {
     // ---- MMA issuer (the whole warp, one lane elected): S_g, dP_g, dQ_{g-1},
     // the steps of all items as one stream ----
     constexpr uint32_t id_s = umma_idesc_f16(kBlk, kStep, BF16, false);
@@ -411,7 +392,7 @@ __global__ void __launch_bounds__(32 * (Ew<D>::kMma + 1), 1)
       const uint64_t kd = desc_at(mn_major, s_prev * 2 * C::kTile);
 #pragma unroll
       for (int kk = 0; kk < kStep / 16; ++kk)
-        tc_mma_ts_if(on, tmem + C::kColDq, ds + E::a_col(kk),
+        tc_mma_ts_if(on, tmem + C::kColDq, ds + step_col(kk),
                      desc_at(kd, kk * 2048), id_q, (!start || kk > 0) ? 1u : 0u);
       tc_commit_if(on, bar(C::kEmpty + s_prev));
       if (last) tc_commit_if(on, bar(C::kDqDone));
@@ -459,7 +440,7 @@ __global__ void __launch_bounds__(32 * (Ew<D>::kMma + 1), 1)
       wait_all(C::kSDone, 0);
       wait_all(C::kSDone, 1);
     }
-  } else if (warp >= E::kAux) {
+  } else if (warp >= kAuxWarp) {
     // ---- auxiliary warpgroup, thread <-> query row: delta and LSE of the
     // next item, its Q and dO into tensor memory, and dQ of the last one out.
     // O and dO are staged while an item runs, delta is formed, Q follows in
@@ -468,7 +449,7 @@ __global__ void __launch_bounds__(32 * (Ew<D>::kMma + 1), 1)
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint8_t* const q_row = gbase + C::kOffQ + row * 128;
     const uint8_t* const do_row = gbase + C::kOffDo + row * 128;
-    const bool leader = warp == E::kAux && lane == 0;
+    const bool leader = warp == kAuxWarp && lane == 0;
     const uint64_t once = l2_policy_evict_first();
     // 16-byte chunk c of a row of a staged tile
     auto chunk = [&](const uint8_t* r, int c) {
@@ -628,8 +609,7 @@ __global__ void __launch_bounds__(32 * (Ew<D>::kMma + 1), 1)
     }
   } else {
     // ---- elementwise: thread <-> (query row, half of a step's columns) ----
-    const int wg = (warp >> 2) & 1, quarter = warp & 3, row = quarter * 32 + lane;
-    const uint32_t mine = E::kAlt ? static_cast<uint32_t>(warp >> 3) : 0;  // even or odd steps
+    const int wg = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint64_t sl2_2 = pair(p.sl2, p.sl2);
     uint32_t g0 = 0, n = 0;
@@ -650,7 +630,6 @@ __global__ void __launch_bounds__(32 * (Ew<D>::kMma + 1), 1)
       const int in_lo = max(0, it.q_last - p.left), in_hi = min(p.N - 1, it.q0 + p.right);
       for (int i = 0; i < it.nt; ++i) {
         const uint32_t g = g0 + i;
-        if (E::kAlt && (g & 1) != mine) continue;
         if (!wait_all(C::kSFull + (g & 1), (g >> 1) & 1)) {
           failed = true;
           break;
@@ -660,22 +639,18 @@ __global__ void __launch_bounds__(32 * (Ew<D>::kMma + 1), 1)
         const int jc = (it.t0 + i) * kStep + 32 * wg;
         const bool edge = jc - 32 * wg < in_lo || jc - 32 * wg + kStep - 1 > in_hi;  // CTA-wide
         const uint32_t seen = edge ? seen_bits(lo_i - jc, hi_i - jc) : 0u;
+        uint32_t s[32], d[32], w[16];
+        tc_ld32(sa, s);
+        tc_ld32(da, d);
+        tc_wait_ld();
 #pragma unroll
-        for (int o = 0; o < 32; o += E::kChunk) {
-          uint32_t s[E::kChunk], d[E::kChunk], w[E::kChunk / 2];
-          tc_ld(sa + o, s);
-          tc_ld(da + o, d);
-          tc_wait_ld();
-#pragma unroll
-          for (int c = 0; c < E::kChunk / 2; ++c) {
-            const float2 f =
-                unpair(mul2(ex2_2(fma2(pair(s[2 * c], s[2 * c + 1]), sl2_2, neg_2)),
-                            add2(pair(d[2 * c], d[2 * c + 1]), ndl_2)));
-            w[c] = pack2_t<BF16>(f.x, f.y);
-          }
-          if (edge) keep_seen(w, seen >> o);
-          tc_st(sa + o, w);
+        for (int c = 0; c < 16; ++c) {
+          const float2 f = unpair(mul2(ex2_2(fma2(pair(s[2 * c], s[2 * c + 1]), sl2_2, neg_2)),
+                                       add2(pair(d[2 * c], d[2 * c + 1]), ndl_2)));
+          w[c] = pack2_t<BF16>(f.x, f.y);
         }
+        if (edge) keep_seen(w, seen);
+        tc_st16(sa, w);
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -689,7 +664,7 @@ __global__ void __launch_bounds__(32 * (Ew<D>::kMma + 1), 1)
   if (failed) report_timeout();
   tc_fence_before();
   __syncthreads();
-  if (warp == E::kMma) {
+  if (warp == kMmaWarp) {
     __syncwarp();
     tc_fence_after();
     tc_dealloc(tmem, kTmemAll);
@@ -774,13 +749,12 @@ __device__ __forceinline__ DkvItem dkv_item(const SwaBwdProblem& p, uint32_t x) 
 }
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(32 * (Ew<D>::kMma + 2), 1)
+__global__ void __launch_bounds__(32 * (kMmaWarp + 2), 1)
     swa_bwd_dkv_kernel(const SwaBwdProblem p, const __grid_constant__ CUtensorMap tmQ,
                        const __grid_constant__ CUtensorMap tmDo,
                        const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV) {
   using C = DkvCfg<D>;
-  using E = Ew<D>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -809,7 +783,7 @@ __global__ void __launch_bounds__(32 * (Ew<D>::kMma + 2), 1)
     }
     fence_mbar_init();
   }
-  if (warp == E::kMma) {
+  if (warp == kMmaWarp) {
     tc_alloc(base + C::kOffTmem, kTmemAll);
     tc_relinquish();
   }
@@ -834,7 +808,7 @@ __global__ void __launch_bounds__(32 * (Ew<D>::kMma + 2), 1)
     return from;
   };
 
-  if (warp == E::kTma) {
+  if (warp == kTmaWarp) {
     if (lane == 0) {
       // ---- TMA producer: Q and dO of 64 queries, their nlse2 and ndelta ----
       tma_prefetch_desc(&tmQ);
@@ -879,7 +853,7 @@ __global__ void __launch_bounds__(32 * (Ew<D>::kMma + 2), 1)
         }
       }
     }
-  } else if (warp >= E::kMma) {
+  } else if (warp >= kMmaWarp) {
     // ---- MMA issuers (a whole warp each, one lane elected). The first forms S
     // and dV, the second dP and dK: P overwrites its S and dS its dP, so the
     // two share no tensor memory, each accumulator is added to in one
@@ -890,7 +864,7 @@ __global__ void __launch_bounds__(32 * (Ew<D>::kMma + 2), 1)
     constexpr uint32_t id_s = umma_idesc_f16(kBlk, C::kCols, BF16, false);
     constexpr uint32_t id_d = umma_idesc_f16(kBlk, D, BF16, true);
     const uint32_t on = elect_one();
-    const bool is_v = warp == E::kMma;
+    const bool is_v = warp == kMmaWarp;
     const uint32_t a_col = tmem + (is_v ? C::kColK : C::kColV);
     const uint32_t s_col = tmem + (is_v ? C::kColS : C::kColP);
     const uint32_t d_col = tmem + (is_v ? C::kColDv : C::kColDk);
@@ -918,7 +892,7 @@ __global__ void __launch_bounds__(32 * (Ew<D>::kMma + 2), 1)
       const uint32_t a = slot(n, w);
 #pragma unroll
       for (int kk = 0; kk < C::kCols / 16; ++kk)
-        tc_mma_ts_if(on, d_col, a + E::a_col(kk), desc_at(b0, kk * 2048), id_d,
+        tc_mma_ts_if(on, d_col, a + step_col(kk), desc_at(b0, kk * 2048), id_d,
                      (!start || kk > 0) ? 1u : 0u);
     };
     // n, st: the step that is added and its stage; sl, ph: stage and phase of
@@ -1021,13 +995,13 @@ __global__ void __launch_bounds__(32 * (Ew<D>::kMma + 2), 1)
       wait_all(a_done, 0);
       wait_all(a_done, 1);
     }
-  } else if (warp >= E::kAux) {
+  } else if (warp >= kAuxWarp) {
     // ---- auxiliary warpgroup, thread <-> key row: K and V of the next item
     // into tensor memory (K once the item's last S, V once its last dP is
     // done), dV and dK of the last one out ----
     const int quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const bool leader = warp == E::kAux && lane == 0;
+    const bool leader = warp == kAuxWarp && lane == 0;
     const uint64_t once = l2_policy_evict_first();
     auto load = [&](const DkvItem& it) {  // one thread
       mbar_arrive_expect_tx(bar(C::kStaged), 2 * kBlk * D * 2);
@@ -1138,9 +1112,8 @@ __global__ void __launch_bounds__(32 * (Ew<D>::kMma + 2), 1)
     }
   } else {
     // ---- elementwise: thread <-> (key row, half of a step's queries) ----
-    const int wg = (warp >> 2) & 1, quarter = warp & 3, row = quarter * 32 + lane;
-    const uint32_t mine = E::kAlt ? static_cast<uint32_t>(warp >> 3) : 0;  // even or odd steps
-    const int gb = C::kGroups == 2 ? 2 * wg : 0;                          // its group's barriers
+    const int wg = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const int gb = C::kGroups == 2 ? 2 * wg : 0;  // its group's barriers
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint64_t sl2_2 = pair(p.sl2, p.sl2);
     const uint64_t shift_2 = pair(Shift<BF16>::kSInv, Shift<BF16>::kSInv);
@@ -1160,15 +1133,14 @@ __global__ void __launch_bounds__(32 * (Ew<D>::kMma + 2), 1)
           st = 0;
           ph ^= 1;
         }
-        if (E::kAlt && (n & 1) != mine) continue;
         // S and the stage's nlse2 and ndelta (and, with two buffers, dP): one
         // question for all. A wait of its own for the stage took 330 of a step's
         // 1300 clocks, although it was over: barrier operations are slow
         // beside the operand traffic.
         const int sb = C::kSFull + gb + (n & 1), db = C::kDpFull + gb + (n & 1);
         const bool x0 = mbar_try_wait(bar(C::kFull + stage), fp), x1 = mbar_try_wait(bar(sb), np);
-        const bool x2 = E::kAlt && mbar_try_wait(bar(db), np);
-        const bool dp_there = E::kAlt && __all_sync(kFull, x2);
+        const bool x2 = C::kBuf == 2 && mbar_try_wait(bar(db), np);
+        const bool dp_there = C::kBuf == 2 && __all_sync(kFull, x2);
         if (__all_sync(kFull, x0 && x1)) {
           tc_fence_after();
         } else if (!wait_all(C::kFull + stage, fp) || !wait_all(sb, np)) {
@@ -1184,16 +1156,15 @@ __global__ void __launch_bounds__(32 * (Ew<D>::kMma + 2), 1)
         const bool edge =
             it.j0 < i0 + kStep - 1 - p.left || it.j0 + kBlk - 1 > i0 + p.right || i0 + kStep > p.M;
         const uint32_t seen = edge ? seen_bits(lo_j - ic, hi_j - ic) : 0u;
-        // 16-bit words of a chunk's columns over the first half of its columns
-        auto store = [&](uint32_t at, const uint64_t* v, int o) {
-          uint32_t w[E::kChunk / 2];
+        auto store = [&](uint32_t at, const uint64_t (&v)[16]) {
+          uint32_t w[16];
 #pragma unroll
-          for (int c = 0; c < E::kChunk / 2; ++c) {
+          for (int c = 0; c < 16; ++c) {
             const float2 f = unpair(v[c]);
             w[c] = pack2_t<BF16>(f.x, f.y);
           }
-          if (edge) keep_seen(w, seen >> o);
-          tc_st(at + o, w);
+          if (edge) keep_seen(w, seen);
+          tc_st16(at, w);
         };
         auto arrive = [&](int b) {
           tc_wait_st();
@@ -1201,41 +1172,32 @@ __global__ void __launch_bounds__(32 * (Ew<D>::kMma + 2), 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(b + gb + (n & 1)));
         };
-        uint64_t pr[16];  // P, kept for dS
+        uint32_t s[32];
+        uint64_t pr[16];  // P, then dS
+        tc_ld32(sa, s);
+        tc_wait_ld();
 #pragma unroll
-        for (int o = 0; o < 32; o += E::kChunk) {
-          uint32_t s[E::kChunk];
-          tc_ld(sa + o, s);
-          tc_wait_ld();
-#pragma unroll
-          for (int c = 0; c < E::kChunk / 4; ++c) {
-            const ulonglong2 l = nl2[o / 4 + c];  // Shift::kP - lse2 of 4 queries
-            pr[o / 2 + 2 * c] = ex2_2(fma2(pair(s[4 * c], s[4 * c + 1]), sl2_2, l.x));
-            pr[o / 2 + 2 * c + 1] = ex2_2(fma2(pair(s[4 * c + 2], s[4 * c + 3]), sl2_2, l.y));
-          }
-          store(sa, pr + o / 2, o);
+        for (int c = 0; c < 8; ++c) {
+          const ulonglong2 l = nl2[c];  // Shift::kP - lse2 of 4 queries
+          pr[2 * c] = ex2_2(fma2(pair(s[4 * c], s[4 * c + 1]), sl2_2, l.x));
+          pr[2 * c + 1] = ex2_2(fma2(pair(s[4 * c + 2], s[4 * c + 3]), sl2_2, l.y));
         }
+        store(sa, pr);
         arrive(C::kPFull);
         if (!dp_there && !wait_all(db, np)) {
           failed = true;
           break;
         }
+        tc_ld32(da, s);
+        tc_wait_ld();
 #pragma unroll
-        for (int o = 0; o < 32; o += E::kChunk) {
-          uint32_t s[E::kChunk];
-          tc_ld(da + o, s);
-          tc_wait_ld();
-          uint64_t ds[E::kChunk / 2];
-#pragma unroll
-          for (int c = 0; c < E::kChunk / 4; ++c) {
-            const ulonglong2 d = ndl[o / 4 + c];  // -delta of 4 queries
-            const uint64_t x = pair(s[4 * c], s[4 * c + 1]), y = pair(s[4 * c + 2], s[4 * c + 3]);
-            ds[2 * c] = mul2(pr[o / 2 + 2 * c], BF16 ? add2(x, d.x) : fma2(x, shift_2, d.x));
-            ds[2 * c + 1] =
-                mul2(pr[o / 2 + 2 * c + 1], BF16 ? add2(y, d.y) : fma2(y, shift_2, d.y));
-          }
-          store(da, ds, o);
+        for (int c = 0; c < 8; ++c) {
+          const ulonglong2 d = ndl[c];  // -delta of 4 queries
+          const uint64_t x = pair(s[4 * c], s[4 * c + 1]), y = pair(s[4 * c + 2], s[4 * c + 3]);
+          pr[2 * c] = mul2(pr[2 * c], BF16 ? add2(x, d.x) : fma2(x, shift_2, d.x));
+          pr[2 * c + 1] = mul2(pr[2 * c + 1], BF16 ? add2(y, d.y) : fma2(y, shift_2, d.y));
         }
+        store(da, pr);
         arrive(C::kDsFull);
       }
     }
@@ -1244,7 +1206,7 @@ __global__ void __launch_bounds__(32 * (Ew<D>::kMma + 2), 1)
   if (failed) report_timeout();
   tc_fence_before();
   __syncthreads();
-  if (warp == E::kMma) {
+  if (warp == kMmaWarp) {
     __syncwarp();
     tc_fence_after();
     tc_dealloc(tmem, kTmemAll);
@@ -1373,10 +1335,10 @@ int launch_swa_bwd(const SwaBwdProblem& p, cudaStream_t st) {
   const int64_t qi = static_cast<int64_t>(p.B) * p.H * p.qtiles;
   const int64_t ki = p.dkv_items;
   // one CTA per SM, items dealt to them
-  dq<<<static_cast<unsigned>(qi < kSms ? qi : kSms), 32 * (Ew<D>::kMma + 1), DqCfg<D>::kSmem, st>>>(p, tk, tv,
+  dq<<<static_cast<unsigned>(qi < kSms ? qi : kSms), 32 * (kMmaWarp + 1), DqCfg<D>::kSmem, st>>>(p, tk, tv,
                                                                                        tq, to, td);
   if (cudaGetLastError() != cudaSuccess) return NSA_ERR_LAUNCH;
-  dkv<<<static_cast<unsigned>(ki < kSms ? ki : kSms), 32 * (Ew<D>::kMma + 2), DkvCfg<D>::kSmem, st>>>(
+  dkv<<<static_cast<unsigned>(ki < kSms ? ki : kSms), 32 * (kMmaWarp + 2), DkvCfg<D>::kSmem, st>>>(
       p, tq, td, tk, tv);
   if (cudaGetLastError() != cudaSuccess) return NSA_ERR_LAUNCH;
   if (p.part != nullptr) {
