@@ -11,12 +11,22 @@
 //   dw += g xhat,   dx = r (g w - xhat mean(g w xhat)).
 // All of it is fp32, rounded once when a result is stored.
 //
-// The bytes bound both: each row is read once and written once. A row is held
-// by D / 16 lanes, 16 entries each, as two 16-byte chunks that hold both
-// entries of every pair: lane t takes chunks t and t + R/16 while t < R/16,
-// and two consecutive chunks of the tail after that, so the rotation needs no
-// exchange between lanes in either pairing and the only shuffles are the
-// row sums (3 steps at D = 128, 2 at 64). A warp covers 32 / (D/16) rows at a time.
+// The bytes bound both: each row is read once and written once. In the forward
+// a row is held by D / 16 lanes, 16 entries each, as two 16-byte chunks that
+// hold both entries of every pair: lane t takes chunks t and t + R/16 while
+// t < R/16, and two consecutive chunks of the tail after that, so the rotation
+// needs no exchange between lanes in either pairing and the only shuffles are
+// the row sums (3 steps at D = 128, 2 at 64). The backward does the same with
+// D / 8 lanes of two 8-byte chunks. A warp has 4 (D = 128) or 8 row slots in
+// the forward and 2 or 4 in the backward; with many heads they walk the heads
+// of one token, whose angles they share, with few they hold several tokens.
+//
+// Measured, bf16, 64 + 8 heads of D = 128: 65,536 tokens forward 389 us
+// (6.2 TB/s, 92 % of a copy), 32,768 tokens backward 341 us (5.4 TB/s, 79 %:
+// of the instruction slots 56 % are taken, and 24 warps an SM, what 80
+// registers a thread allow, keep too few loads in flight for more). Short
+// calls are bound by their launches: a token of 64 + 8 heads takes 5 us on
+// the device, most of it the launch.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -36,6 +46,20 @@ constexpr int kRopeThreads = 128;      // forward CTAs: 4 warps, each a unit of 
 constexpr int kRopeBwdThreads = 256;   // backward CTAs: 8 warps that share one dw partial
 constexpr int kRopeBwdPerSm = 3;       // and how many of them an SM holds
 constexpr int kRopeSms = 152;
+// The forward gives every row slot its own token and head up to this many
+// groups of slots a token, or this many groups in all; beyond, a warp walks a
+// token's heads with one set of angles and weights. Both measured, 32,768
+// tokens of 24 + 8 heads at D = 64 (4 groups): 71 us against 85, 32 + 4 (5
+// groups): 87 and 87, 32 + 4 at D = 128 (9 groups): 153 against 126; 1000
+// tokens of that: 13 against 17.
+constexpr int kFewPerToken = 4;
+constexpr int64_t kFewGroups = 64 * kRopeSms;
+// What a unit of the backward that walks a token's heads costs, beside a
+// group of slots that hold several tokens: its position and angles, and each
+// group of the heads. Shares of the CTAs by these against shares by groups of
+// slots alone: 32,768 tokens of 32 + 4 heads at D = 64 105 us against 143,
+// of 64 + 8 at D = 128 341 against 353.
+constexpr double kUnitCost = 0.9, kGroupCost = 0.4;
 
 struct RopeRows {
   const uint8_t* x;  // one of Q, K: element strides over (b, m, h)
@@ -245,6 +269,101 @@ __global__ void __launch_bounds__(kRopeThreads)
                                 c1, c, s);
 }
 
+// How a warp's row slots map to (token, head) where a token has few heads: one
+// token to a group of slots, or several, with the heads rounded up to a power
+// of two; more heads than slots take several groups.
+struct RowGroups {
+  int per_token;   // groups of a token (1 where tokens share a group)
+  int shift;       // log2 of the slots of a token, where tokens share a group
+  int64_t groups;
+};
+
+template <int RPW>
+__device__ __forceinline__ void group_row(const RowGroups& g, uint32_t q, int sub, uint32_t& tok,
+                                          int& head) {
+  if (g.per_token > 1) {
+    tok = q / static_cast<uint32_t>(g.per_token);
+    head = static_cast<int>(q - tok * g.per_token) * RPW + sub;
+  } else {
+    tok = q * (static_cast<uint32_t>(RPW) >> g.shift) + (static_cast<uint32_t>(sub) >> g.shift);
+    head = sub & ((1 << g.shift) - 1);
+  }
+}
+
+// The forward where a token has few heads: a warp takes UN groups of slots,
+// each lane with the position and the angles of its own token, all loaded
+// together. (A warp per token leaves row slots empty and pays the latencies of
+// position, angles and rows for each: 32,768 tokens of 1 + 1 heads at D = 64
+// 73 us against 15, of 8 + 2 76 against 39.)
+template <int D, bool BF16, int UN>
+__global__ void __launch_bounds__(kRopeThreads)
+    norm_rope_few_kernel(const RopeProblem p, const RowGroups rg) {
+  constexpr int LPR = D / 16, RPW = 32 / LPR;
+  const int lane = threadIdx.x & 31, sub = lane / LPR, tl = lane % LPR;
+  const int64_t q0 =
+      (static_cast<int64_t>(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5)) * UN;
+  if (q0 >= rg.groups) return;
+  int c0, c1;
+  row_chunks(tl, p.half, c0, c1);
+  const bool rot = tl < (p.half >> 3);
+  const uint32_t tokens = static_cast<uint32_t>(p.B) * static_cast<uint32_t>(p.M);
+  uint4 v[UN][2];
+  uint8_t* y[UN];
+  int64_t at[UN];
+  bool is_k[UN];
+#pragma unroll
+  for (int u = 0; u < UN; ++u) {
+    uint32_t tok;
+    int head;
+    group_row<RPW>(rg, static_cast<uint32_t>(q0) + u, sub, tok, head);
+    const bool in = q0 + u < rg.groups && tok < tokens && head < p.q.heads + p.k.heads;
+    is_k[u] = head >= p.q.heads;
+    y[u] = nullptr;
+    at[u] = -1;
+    v[u][0] = v[u][1] = make_uint4(0, 0, 0, 0);
+    if (in) {
+      const int b = static_cast<int>(tok / static_cast<uint32_t>(p.M));
+      const int m = static_cast<int>(tok - static_cast<uint32_t>(b) * p.M);
+      const int64_t h = is_k[u] ? head - p.q.heads : head;
+      at[u] = token_position(p, b, m);
+      y[u] = is_k[u] ? p.k.y + 2 * (b * p.k.yb + m * p.k.ym + h * p.k.yh)
+                     : p.q.y + 2 * (b * p.q.yb + m * p.q.ym + h * p.q.yh);
+      if (at[u] >= 0) {  // (padding is not read)
+        const uint4* src = reinterpret_cast<const uint4*>(
+            is_k[u] ? p.k.x + 2 * (b * p.k.xb + m * p.k.xm + h * p.k.xh)
+                    : p.q.x + 2 * (b * p.q.xb + m * p.q.xm + h * p.q.xh));
+        v[u][0] = src[c0];
+        v[u][1] = src[c1];
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < UN; ++u) {
+    float f[16], w[16], c[8], s[8];
+    if (at[u] >= 0) {
+      if (rot) load_angles(p, at[u], c0, c1, c, s);
+      load_weights<BF16>(is_k[u] ? p.k.w : p.q.w, p.w32, c0, c1, w);
+    }
+    unpack8<BF16>(v[u][0], f);
+    unpack8<BF16>(v[u][1], f + 8);
+    float sq = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sq = fmaf(f[i], f[i], sq);
+    sq = row_sum<LPR>(sq);
+    if (at[u] >= 0) {  // a padding token's rows are zero
+      const float rs = rsqrtf(sq * (1.f / D) + p.eps);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) f[i] *= rs * w[i];
+      if (rot) turn(f, c, s, p.interleaved);
+    }
+    if (y[u] != nullptr) {
+      uint4* dst = reinterpret_cast<uint4*>(y[u]);
+      dst[c0] = pack8<BF16>(f);
+      dst[c1] = pack8<BF16>(f + 8);
+    }
+  }
+}
+
 struct RopeBwdRows {
   const uint8_t* x;   // Q or K as the forward read it
   const uint8_t* dy;  // gradient of the forward's result, in the grad type
@@ -254,6 +373,8 @@ struct RopeBwdRows {
   int heads;
   int segs, per;      // a token's heads are cut into segs units of per heads
   int64_t units;
+  bool few;           // the row slots of a warp hold several tokens instead
+  RowGroups groups;
   int ctas;           // CTAs that work on this tensor
 };
 
@@ -296,38 +417,161 @@ __device__ __forceinline__ float wide_row_sum(float v) {
   return v;
 }
 
-// A CTA works on the rows of Q or of K (so that a lane carries one norm's
-// sums) and leaves one partial dw. Warps walk the units.
-template <int D, bool BF16, bool G32, int UN>
-__global__ void __launch_bounds__(kRopeBwdThreads, kRopeBwdPerSm)
-    norm_rope_bwd_kernel(const __grid_constant__ RopeBwdProblem pr) {
-  const RopeProblem& p = pr.a;
-  constexpr int LPR = D / 8, RPW = 32 / LPR, kWarps = kRopeBwdThreads / 32;
-  __shared__ float sh[kWarps][D];
-  const bool is_k = blockIdx.x >= static_cast<unsigned>(pr.q.ctas);
-  const RopeBwdRows& t = is_k ? pr.k : pr.q;
-  const int cta = static_cast<int>(blockIdx.x) - (is_k ? pr.q.ctas : 0);
-  int c0, c1;
-  const int lane = threadIdx.x & 31, tl = lane % LPR, sub = lane / LPR;
-  row_quads(tl, p.half, c0, c1);
-  const bool rot = tl < (p.half >> 2);
-  float dw[8], w[8];
+// What a lane of the backward holds of one row, and what it does with it.
+template <bool BF16, bool G32>
+struct BwdRow {
+  uint2 v[2];
+  uint4 g[G32 ? 2 : 1];  // fp32: the two chunks; 16 bits: both in one
+
+  __device__ __forceinline__ void zero() {
+    v[0] = v[1] = make_uint2(0, 0);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    dw[i] = 0.f;
-    w[i] = 1.f;
+    for (int i = 0; i < (G32 ? 2 : 1); ++i) g[i] = make_uint4(0, 0, 0, 0);
   }
-  if (t.w != nullptr) {
-    if (p.w32) {
-      load4(static_cast<const float*>(t.w) + 4 * c0, w);
-      load4(static_cast<const float*>(t.w) + 4 * c1, w + 4);
+  __device__ __forceinline__ void load(const uint8_t* x, const uint8_t* dy, int c0, int c1) {
+    const uint2* src = reinterpret_cast<const uint2*>(x);
+    v[0] = src[c0];
+    v[1] = src[c1];
+    if constexpr (G32) {
+      const uint4* gr = reinterpret_cast<const uint4*>(dy);
+      g[0] = gr[c0];
+      g[1] = gr[c1];
     } else {
-      unpack4<BF16>(static_cast<const uint2*>(t.w)[c0], w);
-      unpack4<BF16>(static_cast<const uint2*>(t.w)[c1], w + 4);
+      const uint2* gr = reinterpret_cast<const uint2*>(dy);
+      const uint2 ga = gr[c0], gb = gr[c1];
+      g[0] = make_uint4(ga.x, ga.y, gb.x, gb.y);
     }
   }
-  for (int64_t u = static_cast<int64_t>(cta) * kWarps + (threadIdx.x >> 5); u < t.units;
-       u += static_cast<int64_t>(t.ctas) * kWarps) {
+  // dx, stored at dst, and the row's share of dw (neither when the slot is
+  // not in use)
+  template <int D>
+  __device__ __forceinline__ void work(const RopeProblem& p, bool rot, const float* c,
+                                       const float* s, const float* w, float* dw, bool in,
+                                       uint8_t* base, int64_t off, int c0, int c1) const {
+    float f[8], y[8];
+    unpack4<BF16>(v[0], f);
+    unpack4<BF16>(v[1], f + 4);
+    if constexpr (G32) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        y[4 * i] = __uint_as_float(g[i].x);
+        y[4 * i + 1] = __uint_as_float(g[i].y);
+        y[4 * i + 2] = __uint_as_float(g[i].z);
+        y[4 * i + 3] = __uint_as_float(g[i].w);
+      }
+    } else {
+      unpack4<BF16>(make_uint2(g[0].x, g[0].y), y);
+      unpack4<BF16>(make_uint2(g[0].z, g[0].w), y + 4);
+    }
+    if (rot) {  // the opposite turn: (a, b) -> (a c + b s, b c - a s)
+      if (p.interleaved) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float a = y[2 * j], e = y[2 * j + 1];
+          y[2 * j] = a * c[j] + e * s[j];
+          y[2 * j + 1] = e * c[j] - a * s[j];
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float a = y[j], e = y[j + 4];
+          y[j] = a * c[j] + e * s[j];
+          y[j + 4] = e * c[j] - a * s[j];
+        }
+      }
+    }
+    float sq = 0.f, gx = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      sq = fmaf(f[i], f[i], sq);
+      gx = fmaf(y[i] * w[i], f[i], gx);
+    }
+    sq = wide_row_sum<D / 8>(sq);
+    gx = wide_row_sum<D / 8>(gx);
+    // slots without a row hold zeros (with eps = 0 their rs is infinite)
+    if (in) {
+      const float rs = rsqrtf(sq * (1.f / D) + p.eps);
+      const float kx = gx * rs * rs * (1.f / D);  // mean(g w xhat) rs
+      float d[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        dw[i] = fmaf(y[i], f[i] * rs, dw[i]);
+        d[i] = rs * fmaf(-f[i], kx, y[i] * w[i]);
+      }
+      uint2* o = reinterpret_cast<uint2*>(base + off);
+      o[c0] = make_uint2(pack2_t<BF16>(d[0], d[1]), pack2_t<BF16>(d[2], d[3]));
+      o[c1] = make_uint2(pack2_t<BF16>(d[4], d[5]), pack2_t<BF16>(d[6], d[7]));
+    }
+  }
+};
+
+// The 4 angles of a lane's pairs.
+__device__ __forceinline__ void load_angles4(const RopeProblem& p, int64_t at, int c0, int c1,
+                                             float* c, float* s) {
+  const float* ct = p.cos_t + at * p.half;
+  const float* st = p.sin_t + at * p.half;
+  if (p.interleaved) {  // pairs 0, 1 of the first chunk, 2, 3 of the second
+    const float2 ca = *reinterpret_cast<const float2*>(ct + 2 * c0);
+    const float2 cb = *reinterpret_cast<const float2*>(ct + 2 * c1);
+    const float2 sa = *reinterpret_cast<const float2*>(st + 2 * c0);
+    const float2 sb = *reinterpret_cast<const float2*>(st + 2 * c1);
+    c[0] = ca.x, c[1] = ca.y, c[2] = cb.x, c[3] = cb.y;
+    s[0] = sa.x, s[1] = sa.y, s[2] = sb.x, s[3] = sb.y;
+  } else {
+    load4(ct + 4 * c0, c);
+    load4(st + 4 * c0, s);
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void load_weights8(const RopeProblem& p, const void* w, int c0, int c1,
+                                              float* f) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = 1.f;
+  if (w == nullptr) return;
+  if (p.w32) {
+    load4(static_cast<const float*>(w) + 4 * c0, f);
+    load4(static_cast<const float*>(w) + 4 * c1, f + 4);
+  } else {
+    unpack4<BF16>(static_cast<const uint2*>(w)[c0], f);
+    unpack4<BF16>(static_cast<const uint2*>(w)[c1], f + 4);
+  }
+}
+
+// A CTA's partial dw from its lanes' sums: the row slots of a warp, then the
+// warps, in a fixed order.
+template <int D>
+__device__ __forceinline__ void cta_dw(float* dw, int c0, int c1, float (*sh)[D], float* part) {
+  constexpr int LPR = D / 8, kWarps = kRopeBwdThreads / 32;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+#pragma unroll
+    for (int o = LPR; o < 32; o <<= 1) dw[i] += __shfl_xor_sync(kFull, dw[i], o);
+  }
+  if ((threadIdx.x & 31) < LPR) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sh[threadIdx.x >> 5][4 * c0 + i] = dw[i];
+      sh[threadIdx.x >> 5][4 * c1 + i] = dw[4 + i];
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) v += sh[i][threadIdx.x];
+    part[static_cast<int64_t>(blockIdx.x) * D + threadIdx.x] = v;
+  }
+}
+
+// A warp's walk over the rows of one tensor, a token's heads at a time.
+template <int D, bool BF16, bool G32, int UN>
+__device__ __forceinline__ void bwd_tokens(const RopeProblem& p, const RopeBwdRows& t, int64_t first,
+                                           int64_t stride, int sub, int c0, int c1, bool rot,
+                                           const float* w, float* dw) {
+  constexpr int RPW = 32 / (D / 8);
+  for (int64_t u = first; u < t.units;
+       u += static_cast<int64_t>(t.ctas) * (kRopeBwdThreads / 32)) {
     const uint32_t tok = static_cast<uint32_t>(u) / static_cast<uint32_t>(t.segs);
     const int seg = static_cast<int>(static_cast<uint32_t>(u) - tok * t.segs);
     const int b = static_cast<int>(tok / static_cast<uint32_t>(p.M));
@@ -343,128 +587,95 @@ __global__ void __launch_bounds__(kRopeBwdThreads, kRopeBwdPerSm)
       continue;
     }
     float c[4], s[4];
-    if (rot) {
-      const float* ct = p.cos_t + at * p.half;
-      const float* st = p.sin_t + at * p.half;
-      if (p.interleaved) {  // pairs 0, 1 of the first chunk, 2, 3 of the second
-        const float2 ca = *reinterpret_cast<const float2*>(ct + 2 * c0);
-        const float2 cb = *reinterpret_cast<const float2*>(ct + 2 * c1);
-        const float2 sa = *reinterpret_cast<const float2*>(st + 2 * c0);
-        const float2 sb = *reinterpret_cast<const float2*>(st + 2 * c1);
-        c[0] = ca.x, c[1] = ca.y, c[2] = cb.x, c[3] = cb.y;
-        s[0] = sa.x, s[1] = sa.y, s[2] = sb.x, s[3] = sb.y;
-      } else {
-        load4(ct + 4 * c0, c);
-        load4(st + 4 * c0, s);
-      }
-    }
+    if (rot) load_angles4(p, at, c0, c1, c, s);
     const uint8_t* const x = t.x + 2 * (b * t.xb + m * t.xm);
     const uint8_t* const dy = t.dy + (G32 ? 4 : 2) * (b * t.gb + m * t.gm);
     for (int r = r0; r < r1; r += RPW * UN) {
-      uint2 v[UN][2];
-      uint4 g4[UN][G32 ? 2 : 1];  // fp32: the two chunks; 16 bits: both in one
+      BwdRow<BF16, G32> d[UN];
 #pragma unroll
       for (int k = 0; k < UN; ++k) {
         const int row = r + k * RPW + sub;
-        v[k][0] = v[k][1] = make_uint2(0, 0);
-#pragma unroll
-        for (int i = 0; i < (G32 ? 2 : 1); ++i) g4[k][i] = make_uint4(0, 0, 0, 0);
-        if (row < r1) {
-          const uint2* src = reinterpret_cast<const uint2*>(x + 2 * row * t.xh);
-          v[k][0] = src[c0];
-          v[k][1] = src[c1];
-          if constexpr (G32) {
-            const uint4* gr = reinterpret_cast<const uint4*>(dy + 4 * row * t.gh);
-            g4[k][0] = gr[c0];
-            g4[k][1] = gr[c1];
-          } else {
-            const uint2* gr = reinterpret_cast<const uint2*>(dy + 2 * row * t.gh);
-            const uint2 ga = gr[c0], gb = gr[c1];
-            g4[k][0] = make_uint4(ga.x, ga.y, gb.x, gb.y);
-          }
-        }
+        d[k].zero();
+        if (row < r1) d[k].load(x + 2 * row * t.xh, dy + (G32 ? 4 : 2) * row * t.gh, c0, c1);
       }
 #pragma unroll
       for (int k = 0; k < UN; ++k) {
         const int row = r + k * RPW + sub;
-        float f[8], y[8];
-        unpack4<BF16>(v[k][0], f);
-        unpack4<BF16>(v[k][1], f + 4);
-        if constexpr (G32) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            y[4 * i] = __uint_as_float(g4[k][i].x);
-            y[4 * i + 1] = __uint_as_float(g4[k][i].y);
-            y[4 * i + 2] = __uint_as_float(g4[k][i].z);
-            y[4 * i + 3] = __uint_as_float(g4[k][i].w);
-          }
-        } else {
-          unpack4<BF16>(make_uint2(g4[k][0].x, g4[k][0].y), y);
-          unpack4<BF16>(make_uint2(g4[k][0].z, g4[k][0].w), y + 4);
-        }
-        if (rot) {  // the opposite turn: (a, b) -> (a c + b s, b c - a s)
-          if (p.interleaved) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float a = y[2 * j], e = y[2 * j + 1];
-              y[2 * j] = a * c[j] + e * s[j];
-              y[2 * j + 1] = e * c[j] - a * s[j];
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float a = y[j], e = y[j + 4];
-              y[j] = a * c[j] + e * s[j];
-              y[j + 4] = e * c[j] - a * s[j];
-            }
-          }
-        }
-        float sq = 0.f, gx = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          sq = fmaf(f[i], f[i], sq);
-          gx = fmaf(y[i] * w[i], f[i], gx);
-        }
-        sq = wide_row_sum<LPR>(sq);
-        gx = wide_row_sum<LPR>(gx);
-        // rows past the heads hold zeros (with eps = 0 their rs is infinite)
-        if (row < r1) {
-          const float rs = rsqrtf(sq * (1.f / D) + p.eps);
-          const float kx = gx * rs * rs * (1.f / D);  // mean(g w xhat) rs
-          float d[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            dw[i] = fmaf(y[i], f[i] * rs, dw[i]);
-            d[i] = rs * fmaf(-f[i], kx, y[i] * w[i]);
-          }
-          uint2* dst = reinterpret_cast<uint2*>(dx + 2 * row * t.dh);
-          dst[c0] = make_uint2(pack2_t<BF16>(d[0], d[1]), pack2_t<BF16>(d[2], d[3]));
-          dst[c1] = make_uint2(pack2_t<BF16>(d[4], d[5]), pack2_t<BF16>(d[6], d[7]));
-        }
+        d[k].template work<D>(p, rot, c, s, w, dw, row < r1, dx, 2 * row * t.dh, c0, c1);
       }
     }
   }
-  if (pr.part == nullptr) return;
-  // the row groups of a warp, then the warps, in a fixed order
+}
+
+// The same where a token has no more heads than a warp has row slots, UN
+// neighbouring groups of slots at a time (32,768 tokens of 1 + 1 heads at
+// D = 64: 50 us a token at a time, 21 here). With an fp32 gradient one: two
+// spill.
+template <int D, bool BF16, bool G32, int UN>
+__device__ __forceinline__ void bwd_groups(const RopeProblem& p, const RopeBwdRows& t, int64_t first,
+                                           int64_t stride, int sub, int c0, int c1, bool rot,
+                                           const float* w, float* dw) {
+  constexpr int RPW = 32 / (D / 8);
+  const uint32_t tokens = static_cast<uint32_t>(p.B) * static_cast<uint32_t>(p.M);
+  for (int64_t q = first * UN; q < t.groups.groups; q += stride * UN) {
+    BwdRow<BF16, G32> d[UN];
+    uint8_t* dst[UN];
+    float c[UN][4], s[UN][4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-#pragma unroll
-    for (int o = LPR; o < 32; o <<= 1) dw[i] += __shfl_xor_sync(kFull, dw[i], o);
-  }
-  if (sub == 0) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      sh[threadIdx.x >> 5][4 * c0 + i] = dw[i];
-      sh[threadIdx.x >> 5][4 * c1 + i] = dw[4 + i];
+    for (int k = 0; k < UN; ++k) {
+      uint32_t tok;
+      int head;
+      group_row<RPW>(t.groups, static_cast<uint32_t>(q) + k, sub, tok, head);
+      d[k].zero();
+      dst[k] = nullptr;
+      if (q + k < t.groups.groups && tok < tokens && head < t.heads) {
+        const int b = static_cast<int>(tok / static_cast<uint32_t>(p.M));
+        const int m = static_cast<int>(tok - static_cast<uint32_t>(b) * p.M);
+        const int64_t at = token_position(p, b, m), h = head;
+        uint8_t* const o = t.dx + 2 * (b * t.db + m * t.dm + h * t.dh);
+        if (at >= 0) {
+          dst[k] = o;
+          d[k].load(t.x + 2 * (b * t.xb + m * t.xm + h * t.xh),
+                    t.dy + (G32 ? 4 : 2) * (b * t.gb + m * t.gm + h * t.gh), c0, c1);
+          if (rot) load_angles4(p, at, c0, c1, c[k], s[k]);
+        } else {  // padding: a zero gradient
+          reinterpret_cast<uint2*>(o)[c0] = reinterpret_cast<uint2*>(o)[c1] = make_uint2(0, 0);
+        }
+      }
     }
-  }
-  __syncthreads();
-  if (threadIdx.x < D) {
-    float v = 0.f;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) v += sh[i][threadIdx.x];
-    pr.part[static_cast<int64_t>(blockIdx.x) * D + threadIdx.x] = v;
+    for (int k = 0; k < UN; ++k)
+      d[k].template work<D>(p, rot && dst[k] != nullptr, c[k], s[k], w, dw, dst[k] != nullptr, dst[k], 0,
+                            c0, c1);
   }
+}
+
+// A CTA works on the rows of Q or of K (so that a lane carries one norm's
+// sums) and leaves one partial dw. Warps walk the units.
+template <int D, bool BF16, bool G32, bool FEW>
+__global__ void __launch_bounds__(kRopeBwdThreads, kRopeBwdPerSm)
+    norm_rope_bwd_kernel(const __grid_constant__ RopeBwdProblem pr) {
+  const RopeProblem& p = pr.a;
+  constexpr int LPR = D / 8, kWarps = kRopeBwdThreads / 32;
+  __shared__ float sh[kWarps][D];
+  const bool is_k = blockIdx.x >= static_cast<unsigned>(pr.q.ctas);
+  const RopeBwdRows& t = is_k ? pr.k : pr.q;
+  const int cta = static_cast<int>(blockIdx.x) - (is_k ? pr.q.ctas : 0);
+  int c0, c1;
+  const int lane = threadIdx.x & 31, tl = lane % LPR, sub = lane / LPR;
+  row_quads(tl, p.half, c0, c1);
+  const bool rot = tl < (p.half >> 2);
+  float dw[8], w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) dw[i] = 0.f;
+  load_weights8<BF16>(p, t.w, c0, c1, w);
+  const int64_t first = static_cast<int64_t>(cta) * kWarps + (threadIdx.x >> 5);
+  const int64_t stride = static_cast<int64_t>(t.ctas) * kWarps;
+  if (FEW && t.few)
+    bwd_groups<D, BF16, G32, G32 ? 1 : 2>(p, t, first, stride, sub, c0, c1, rot, w, dw);
+  else
+    bwd_tokens<D, BF16, G32, 2>(p, t, first, stride, sub, c0, c1, rot, w, dw);
+  if (pr.part != nullptr) cta_dw<D>(dw, c0, c1, sh, pr.part);
 }
 
 // dw from the CTAs' partials: a CTA sums 32 columns of dwq or dwk, 32 rows of
@@ -552,10 +763,37 @@ int rope_bwd_most_ctas(int64_t B, int64_t M) {
   return tokens == 0 ? 0 : kRopeBwdCtas;
 }
 
+RowGroups plan_row_groups(int heads, int64_t tokens, int slots) {
+  RowGroups g{1, 0, 0};
+  if (heads > slots) {
+    g.per_token = (heads + slots - 1) / slots;
+    g.groups = tokens * g.per_token;
+  } else {
+    while ((1 << g.shift) < heads) ++g.shift;
+    const int64_t shared = slots >> g.shift;  // tokens of a group
+    g.groups = (tokens + shared - 1) / shared;
+  }
+  return g;
+}
+
+// What a tensor's rows cost the backward, in groups of row slots, and whether
+// the slots hold several tokens.
+double rope_bwd_cost(RopeBwdRows& t, int64_t tokens, int slots) {
+  t.few = t.heads <= slots;
+  t.groups = plan_row_groups(t.heads, tokens, slots);
+  if (t.few) return static_cast<double>(t.groups.groups);
+  return static_cast<double>(tokens) * (kUnitCost + kGroupCost * ((t.heads + slots - 1) / slots));
+}
+
 // A token's heads in units of `per` (a multiple of a warp's rows): whole
 // tokens when they alone give every warp of `ctas` one, else as few heads as
 // it takes. Fewer CTAs where the units do not fill them.
 void plan_rope_rows(RopeBwdRows& t, int64_t tokens, int rows_per_warp, int ctas) {
+  if (t.few) {
+    const int64_t need = (t.groups.groups + kRopeBwdThreads / 32 - 1) / (kRopeBwdThreads / 32);
+    t.ctas = static_cast<int>(need < ctas ? need : ctas);
+    return;
+  }
   const int64_t warps = static_cast<int64_t>(ctas) * (kRopeBwdThreads / 32);
   const int64_t most = (t.heads + rows_per_warp - 1) / rows_per_warp;
   int64_t segs = (warps + tokens - 1) / tokens;
@@ -573,6 +811,16 @@ int launch_norm_rope(const RopeProblem& p, cudaStream_t st) {
   constexpr int RPW = 32 / (D / 16), UN = 4;
   const int rows = p.q.heads + p.k.heads;
   const int64_t tokens = static_cast<int64_t>(p.B) * p.M;
+  const RowGroups g = plan_row_groups(rows, tokens, RPW);
+  if (rows <= kFewPerToken * RPW || g.groups <= kFewGroups) {
+    constexpr int FUN = 2;
+    if (g.groups < (int64_t(1) << 32)) {
+      const int64_t per_cta = kRopeThreads / 32 * FUN;
+      norm_rope_few_kernel<D, BF16, FUN>
+          <<<static_cast<unsigned>((g.groups + per_cta - 1) / per_cta), kRopeThreads, 0, st>>>(p, g);
+      return cudaGetLastError() == cudaSuccess ? NSA_OK : NSA_ERR_LAUNCH;
+    }
+  }
   // rows per warp: a whole token when the tokens alone give every SM 16
   // warps, else as few rows as it takes to get there
   const int64_t want = 16 * kRopeSms;
@@ -594,12 +842,17 @@ template <int D, bool BF16, bool G32>
 int launch_norm_rope_bwd(RopeBwdProblem& p, float* dwq, float* dwk, cudaStream_t st) {
   constexpr int RPW = 32 / (D / 8);
   const int64_t tokens = static_cast<int64_t>(p.a.B) * p.a.M;
-  const int64_t gq = (p.q.heads + RPW - 1) / RPW, gk = (p.k.heads + RPW - 1) / RPW;
-  int k_ctas = static_cast<int>((kRopeBwdCtas * gk + (gq + gk) / 2) / (gq + gk));
+  // the CTAs, by what the rows of Q and of K cost
+  const double cq = rope_bwd_cost(p.q, tokens, RPW), ck = rope_bwd_cost(p.k, tokens, RPW);
+  int k_ctas = static_cast<int>(kRopeBwdCtas * ck / (cq + ck) + 0.5);
   k_ctas = k_ctas < 1 ? 1 : k_ctas > kRopeBwdCtas - 1 ? kRopeBwdCtas - 1 : k_ctas;
   plan_rope_rows(p.q, tokens, RPW, kRopeBwdCtas - k_ctas);
   plan_rope_rows(p.k, tokens, RPW, k_ctas);
-  norm_rope_bwd_kernel<D, BF16, G32, G32 ? 2 : 2><<<p.q.ctas + p.k.ctas, kRopeBwdThreads, 0, st>>>(p);
+  const int ctas = p.q.ctas + p.k.ctas;
+  if (p.q.few || p.k.few)
+    norm_rope_bwd_kernel<D, BF16, G32, true><<<ctas, kRopeBwdThreads, 0, st>>>(p);
+  else
+    norm_rope_bwd_kernel<D, BF16, G32, false><<<ctas, kRopeBwdThreads, 0, st>>>(p);
   if (cudaGetLastError() != cudaSuccess) return NSA_ERR_LAUNCH;
   if (p.part != nullptr) {
     norm_rope_dw_kernel<D><<<dim3(D / 32, 2), 1024, 0, st>>>(p.part, p.q.ctas, p.k.ctas, dwq, dwk);

@@ -152,6 +152,41 @@ def test_backward_matches_oracle(B, M, H, G, D, dtype, rot, inter, fused, pad, w
         assert torch.equal(a, b)
 
 
+FEW = [
+    # heads of a token that fill, share, or run over the row slots of a warp
+    (1, 1, 64), (2, 1, 64), (3, 2, 64), (4, 4, 64), (5, 3, 64), (20, 12, 64),
+    (1, 1, 128), (2, 2, 128), (3, 1, 128), (9, 2, 128),
+]
+
+
+@pytest.mark.parametrize("H,G,D", FEW)
+@pytest.mark.parametrize("B,M,dtype,rot,inter", [(1, 1, "bf16", 64, False), (3, 5, "f16", 32, True),
+                                                 (2, 601, "bf16", 64, False)])
+def test_few_heads(B, M, dtype, rot, inter, H, G, D):
+    """Several tokens to a warp: partial groups, padding among them, outputs
+    with room around every row, which stays as it was."""
+    import torch
+
+    from nsa_block_selection_gb300 import qk_norm_rope, qk_norm_rope_bwd
+
+    case = _case(B, M, H, G, D, dtype, rot, 21, pad=M > 1)
+    q, k, wq, wk, cos, sin, pos = case
+    room = [torch.full((B, M + 1, h + 1, D), 7.0, device="cuda", dtype=q.dtype)
+            for h in (H, G, H, G)]
+    outs = [t[:, :M, :h] for t, h in zip(room, (H, G, H, G))]
+    qk_norm_rope(q, k, wq, wk, cos, sin, pos, eps=1e-5, interleaved=inter, q_out=outs[0],
+                 k_out=outs[1])
+    _check_fwd(case, dtype, 1e-5, inter, outs[0], outs[1])
+    g = torch.Generator(device="cuda").manual_seed(22)
+    for grad in (dtype, "f32"):
+        grads = [torch.randn(x.shape, generator=g, device="cuda").to(_dt(grad)) for x in (q, k)]
+        out = qk_norm_rope_bwd(q, k, *grads, wq, wk, cos, sin, pos, eps=1e-5,
+                               interleaved=inter, dq=outs[2], dk=outs[3])
+        _check_bwd(case, grads, dtype, 1e-5, inter, out)
+    for t, h in zip(room, (H, G, H, G)):
+        assert (t[:, M:] == 7).all() and (t[:, :, h:] == 7).all()
+
+
 def test_positions_by_default_shared_and_far():
     import torch
 
