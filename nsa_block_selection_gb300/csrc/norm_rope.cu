@@ -22,7 +22,7 @@
 // of one token, whose angles they share, with few they hold several tokens.
 //
 // Measured, bf16, 64 + 8 heads of D = 128: 65,536 tokens forward 389 us
-// (6.2 TB/s, 92 % of a copy), 32,768 tokens backward 341 us (5.4 TB/s, 79 %:
+// (6.2 TB/s, 92 % of a copy), 32,768 tokens backward 336 us (5.4 TB/s, 80 %:
 // of the instruction slots 56 % are taken, and 24 warps an SM, what 80
 // registers a thread allow, keep too few loads in flight for more). Short
 // calls are bound by their launches: a token of 64 + 8 heads takes 5 us on
@@ -57,9 +57,9 @@ constexpr int64_t kFewGroups = 64 * kRopeSms;
 // What a unit of the backward that walks a token's heads costs, beside a
 // group of slots that hold several tokens: its position and angles, and each
 // group of the heads. Shares of the CTAs by these against shares by groups of
-// slots alone: 32,768 tokens of 32 + 4 heads at D = 64 105 us against 143,
-// of 64 + 8 at D = 128 341 against 353.
-constexpr double kUnitCost = 0.9, kGroupCost = 0.4;
+// slots alone: 32,768 tokens of 32 + 4 heads at D = 64 102 us against 143,
+// of 64 + 8 at D = 128 338 against 351.
+constexpr double kUnitCost = 0.5, kGroupCost = 0.6;
 
 struct RopeRows {
   const uint8_t* x;  // one of Q, K: element strides over (b, m, h)
