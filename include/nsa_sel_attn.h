@@ -462,8 +462,9 @@ int nsa_swa_fwd(const void* Q, const void* K, const void* V, void* O, float* LSE
 
 /*
  * nsa_swa_bwd_workspace_bytes -- device workspace of nsa_swa_bwd: LSE and
- * delta of every (batch, head, query), and, where the key tiles are fewer than
- * the SMs, fp32 parts of dK and dV. Negative nsa_status for invalid sizes.
+ * delta of every (batch, head, query), and, where tiles of keys or of queries
+ * are cut because they do not fill the SMs, fp32 parts of dK and dV (at most
+ * 9728 tiles of 128 KB at D = 128) and of dQ (half of that). Negative nsa_status for invalid sizes.
  * Pure host arithmetic.
  */
 int64_t nsa_swa_bwd_workspace_bytes(int64_t B, int64_t M, int64_t N, int64_t H, int64_t H_kv,
@@ -500,8 +501,8 @@ int64_t nsa_swa_bwd_workspace_bytes(int64_t B, int64_t M, int64_t N, int64_t H, 
  * the forward, in 128-key tiles). M and N are at most 2^29. The outputs must
  * not overlap the inputs.
  *
- * Asynchronous: two kernels on `stream` (three where dK, dV are joined from
- * parts), no allocation; calls that may overlap need workspaces of their own.
+ * Asynchronous: two kernels on `stream` (up to four where gradients are joined
+ * from parts), no allocation; calls that may overlap need workspaces of their own.
  * Errors before launch as nsa_swa_fwd, plus NSA_ERR_WORKSPACE. With no query,
  * or no key, the gradients are zeroed and no workspace is needed. A timed-out
  * device wait is reported by nsa_sync_status.

@@ -17,23 +17,43 @@
 // reach here, in an order that changes from run to run. Here every sum is
 // made in tensor memory in a fixed order: equal calls give equal bits.
 //
-//  1. swa_bwd_dq_kernel: one CTA per 128 queries of a head, walking the key
-//     tiles of 64 that their windows touch. Q and dO stay in tensor memory as
-//     the A operands of S = Q K^T and dP = dO V^T; dS overwrites S there and
-//     is the A operand of dQ += dS K. Taking every A from tensor memory
-//     leaves 64 B a clock of shared-memory reads for B: with A in shared
-//     memory the 64-column products would need 192 of the 128 there are.
-//     S and dP have two buffers each, so the tensor pipe runs S and dP of the
-//     next tile and dQ of the previous one while eight warps form dS. It also
-//     leaves LSE log2 e and delta of every query for the second kernel.
-//  2. swa_bwd_dkv_kernel: one CTA per 128 keys of a KV head (or per part of
-//     its query heads and queries, where there are too few keys for the SMs),
-//     walking its (query head, 64 queries) steps: S^T = K Q^T, dP^T = V dO^T,
-//     dV += P^T dO, dK += dS^T Q. K (and V at D = 64) is kept in tensor memory.
-//     What the two accumulators leave of it holds three 64-column slots that
-//     S, dP of successive steps take in turn: S of the next step is formed
-//     while dP of this one is in use, and dP of the next where P was.
-//  3. swa_bwd_join_kernel: where step 2 was split, the sum of its fp32 parts.
+// Both kernels are persistent, one CTA to an SM (tensor memory holds one set
+// of accumulators), their items dealt in rounds in snake order, and their
+// steps of all items one stream: the operands of an item are staged while the
+// one before runs, and its gradients leave while the next one runs. Every A
+// operand stays in tensor memory, which leaves 64 B a clock of shared-memory
+// reads for B: with A in shared memory the 64-column products would need 192
+// of the 128 there are (measured: 33 clocks a product against 49).
+//
+//  1. swa_bwd_dq_kernel: an item is 128 queries of a head (or, with few query
+//     tiles, a part of their keys), a step 64 keys. Q and dO are the A operands
+//     of S = Q K^T and dP = dO V^T; dS overwrites S and is the A operand of
+//     dQ += dS K. S and dP have two buffers each, so the tensor pipe runs S and
+//     dP of the next step and dQ of the previous one while eight warps form dS.
+//     Four auxiliary warps form delta and move Q and dO in and dQ out. LSE
+//     log2 e and delta of every query are left for the second kernel.
+//  2. swa_bwd_dkv_kernel: an item is 128 keys of a KV head (or a part of its
+//     steps), a step 64 queries of a head: S^T = K Q^T, dP^T = V dO^T,
+//     dV += P^T dO, dK += dS^T Q. K and V are the A operands of the first two;
+//     P overwrites S, dS dP. At D = 128 the accumulators leave one buffer for
+//     each of S and dP, so a step is two groups of 32 queries: one's products
+//     run during the other's exponentials; at D = 64 there are two buffers. Two
+//     warps issue, (S, dV) and (dP, dK): the waits of one pass while the
+//     other's products run.
+//  3. swa_bwd_join_dq_kernel, swa_bwd_join_kernel: where tiles were cut, the sum
+//     of their fp32 parts.
+//
+// What bounds it. D = 128: the tensor pipe, busy 68 % (dQ) and 69 % (dK, dV) of
+// the clocks at 8192 tokens of 64 + 8 heads, window (512, 0), where the items
+// have 10 to 64 steps: 163 and 222 us, 5 us of joining, DRAM at 3.1 and 1.6 TB/s;
+// a step's products take 512 (dQ: 384) clocks and its
+// barriers, of which one that is over still takes a warp 100 to 300 clocks,
+// are most of the rest. 16,384 tokens, window (4096, 0): 1.52 and 2.15 ms,
+// 1.4 PFLOP/s over the 7 products; back to back the clock falls to 1.6 to
+// 1.9 GHz at the power limit. D = 64: the elementwise warps (2 x 16 heads of
+// 1500 x 2048: 47 and 69 us), as the products are half as long and the
+// exponentials are not. Short calls: their launches and the latency of a
+// few dependent steps (2 x 1000 tokens, 8 + 2 heads: 9, 21 and 5 us).
 //
 // Every mbarrier wait is bounded (1 s); a role that gives up sets the status
 // word, waits for its own copies, and every role reaches the teardown, which
@@ -78,9 +98,10 @@ struct SwaBwdProblem {
   void *dQ, *dK, *dV;
   float* nlse2;   // [B, H, Mp]: Shift::kP - LSE log2 e; -inf for rows without keys
   float* ndelta;  // [B, H, Mp]: -delta 2^(kS - kP)
-  float* part;   // [parts, 2 (dK, dV), kBlk, D], or NULL
+  float* part;    // [parts, 2 (dK, dV), kBlk, D], or NULL
+  float* part_q;  // [parts, kBlk, D] of dQ, or NULL
   int B, M, N, H, Hkv, hpg, Mp, qtiles, ktiles, splits;
-  int dq_items;               // B H qtiles
+  int dq_whole, dq_splits, dq_items;  // the same for the query tiles of the dQ kernel
   int whole_tiles, dkv_items;  // key tiles that are not cut, and all items of the dK, dV kernel
   int left, right;  // clamped to [0, M] and [0, N]: unbounded in effect
   float sl2, scale;
@@ -250,16 +271,28 @@ struct DqCfg {
 };
 
 // One item of the dQ kernel: 128 queries of a head, and the key tiles of 64
-// that their windows touch.
+// that their windows touch, or a part of those.
 struct DqItem {
   int b, g, h, q0, q_last, t0, nt;
+  int part;   // its place among the parts, or -1
+  bool stat;  // leaves the rows' LSE and delta
 };
 
 // Items in the order (b, KV head, query tile, head): heads fastest, so that
 // the CTAs of a moment share K and V in L2; later tiles, which see more keys
-// under a causal window, first.
+// under a causal window, first. CUT: the last ones are cut into parts. (In a
+// kernel of its own: one for both took 427 us instead of 398 for the whole call
+// at 8k, window (512, 0), where nothing is cut.)
+template <bool CUT>
 __device__ __forceinline__ DqItem dq_item(const SwaBwdProblem& p, uint32_t x) {
   DqItem it;
+  uint32_t sp = 0;
+  it.part = -1;
+  if (CUT && x >= static_cast<uint32_t>(p.dq_whole)) {
+    it.part = static_cast<int>(x) - p.dq_whole;
+    x = p.dq_whole + static_cast<uint32_t>(it.part) / static_cast<uint32_t>(p.dq_splits);
+    sp = static_cast<uint32_t>(it.part) % static_cast<uint32_t>(p.dq_splits);
+  }
   const int hh = static_cast<int>(x % static_cast<uint32_t>(p.hpg));
   x /= static_cast<uint32_t>(p.hpg);
   const int qt = p.qtiles - 1 - static_cast<int>(x % static_cast<uint32_t>(p.qtiles));
@@ -271,11 +304,19 @@ __device__ __forceinline__ DqItem dq_item(const SwaBwdProblem& p, uint32_t x) {
   it.q_last = min(it.q0 + kBlk, p.M) - 1;
   const int jlo = max(0, it.q0 - p.left), jhi = min(p.N - 1, it.q_last + p.right);
   it.t0 = jlo / kStep;
-  it.nt = jhi >= jlo ? jhi / kStep - it.t0 + 1 : 0;
+  const int all = jhi >= jlo ? jhi / kStep - it.t0 + 1 : 0;
+  it.nt = all;
+  it.stat = true;
+  if (CUT && it.part >= 0) {
+    const int first = static_cast<int>(static_cast<int64_t>(all) * sp / p.dq_splits);
+    it.nt = static_cast<int>(static_cast<int64_t>(all) * (sp + 1) / p.dq_splits) - first;
+    it.t0 += first;
+    it.stat = first == 0 && (it.nt > 0 || (all == 0 && sp == 0));
+  }
   return it;
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool CUT>
 __global__ void __launch_bounds__(32 * (kMmaWarp + 1), 1)
     swa_bwd_dq_kernel(const SwaBwdProblem p, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV,
@@ -343,7 +384,7 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 1), 1)
       for (uint32_t k = 0; k < rounds && !failed; ++k) {
         const uint32_t x = item_of(k);
         if (x >= items) continue;
-        const DqItem it = dq_item(p, x);
+        const DqItem it = dq_item<CUT>(p, x);
         for (int i = 0; i < it.nt; ++i) {
           if (!wait_phase(bar(C::kEmpty + s), ph, kWaitLimitNs)) {
             failed = true;
@@ -402,7 +443,7 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 1), 1)
     for (uint32_t k = 0; k < rounds && ok; ++k) {
       const uint32_t x = item_of(k);
       if (x >= items) continue;
-      const int nt = dq_item(p, x).nt;
+      const int nt = dq_item<CUT>(p, x).nt;
       for (int i = 0; i < nt && ok; ++i, ++g) {
         if (i == 0) ok = wait_all(C::kQReady, n & 1);
         ok = ok && wait_all(C::kFull + s, ph);
@@ -469,7 +510,10 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 1), 1)
     const float f_out = p.scale * Shift<BF16>::kSInv;
     auto out = [&](const DqItem& it, bool zero) {  // dQ rows of an item
       const int iq = it.q0 + row;
-      const int64_t off = ((static_cast<int64_t>(it.b) * p.M + iq) * p.H + it.h) * D;
+      const bool part = CUT && it.part >= 0, f32 = p.g32 || part;
+      void* const dst = part ? p.part_q : p.dQ;
+      const int64_t off = part ? (static_cast<int64_t>(it.part) * kBlk + row) * D
+                               : ((static_cast<int64_t>(it.b) * p.M + iq) * p.H + it.h) * D;
       auto column = [&](int c, uint32_t (&r)[32]) {
         if (zero) {
 #pragma unroll
@@ -485,11 +529,11 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 1), 1)
         }
       };
       uint32_t r[32];
-      if (p.g32) {
+      if (f32) {
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           column(c, r);
-          if (iq < p.M) store_row32<BF16>(p.dQ, off, 32 * c, true, r, f_out, p.wide);
+          if (iq < p.M) store_row32<BF16>(dst, off, 32 * c, true, r, f_out, p.wide);
         }
       } else {  // everything out of tensor memory first
         uint32_t w[D / 2];
@@ -498,22 +542,22 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 1), 1)
           column(c, r);
           pack32<BF16>(w + 16 * c, r, f_out);
         }
-        if (iq < p.M) store_words(static_cast<uint16_t*>(p.dQ) + off, w, D / 2, p.wide);
+        if (iq < p.M) store_words(static_cast<uint16_t*>(dst) + off, w, D / 2, p.wide);
       }
     };
     uint32_t n = 0;
     DqItem last{};
     auto next = [&](uint32_t from) {  // the next round with an item that has keys
       for (; from < rounds; ++from)
-        if (item_of(from) < items && dq_item(p, item_of(from)).nt > 0) break;
+        if (item_of(from) < items && dq_item<CUT>(p, item_of(from)).nt > 0) break;
       return from;
     };
     uint32_t kn = next(0);
-    if (kn < rounds && leader) load_o(dq_item(p, item_of(kn)));
+    if (kn < rounds && leader) load_o(dq_item<CUT>(p, item_of(kn)));
     for (uint32_t k = 0; k < rounds && !failed; ++k) {
       const uint32_t x = item_of(k);
       if (x >= items) continue;
-      const DqItem it = dq_item(p, x);
+      const DqItem it = dq_item<CUT>(p, x);
       const int iq = it.q0 + row;
       float l2 = INFINITY, dl = 0.f;
       if (it.nt > 0) {
@@ -546,7 +590,7 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 1), 1)
         stat[(n & 1) * 2 * kBlk + row] = l2;
         stat[(n & 1) * 2 * kBlk + kBlk + row] = dl;
       }
-      if (iq < p.Mp) {  // (a tile without keys: no pair reads them)
+      if ((!CUT || it.stat) && iq < p.Mp) {  // (a tile without keys: no pair reads them)
         const int64_t at = (static_cast<int64_t>(it.b) * p.H + it.h) * p.Mp + iq;
         p.nlse2[at] = Shift<BF16>::kP - l2;
         p.ndelta[at] = -dl * Shift<BF16>::kSInv;
@@ -584,7 +628,7 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 1), 1)
       }
       bar_sync(1, 128);  // all four warps have read the staged rows
       kn = next(k + 1);
-      if (kn < rounds && leader) load_o(dq_item(p, item_of(kn)));
+      if (kn < rounds && leader) load_o(dq_item<CUT>(p, item_of(kn)));
       if (n > 0) {
         if (!wait_all(C::kDqDone, (n - 1) & 1)) {
           failed = true;
@@ -616,7 +660,7 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 1), 1)
     for (uint32_t k = 0; k < rounds && !failed; ++k) {
       const uint32_t x = item_of(k);
       if (x >= items) continue;
-      const DqItem it = dq_item(p, x);
+      const DqItem it = dq_item<CUT>(p, x);
       if (it.nt == 0) continue;
       if (!wait_all(C::kDoReady, n & 1)) {
         failed = true;
@@ -683,7 +727,8 @@ struct DkvCfg {
   static constexpr int kBuf = D == 128 ? 1 : 2;  // buffers of S and of dP
   // Groups of a step: at D = 128, with one buffer, each warpgroup's 32 queries
   // are a group of their own, so that one's products run during the other's
-  // exponentials (16k, window (4096, 0): 2.41 ms against 2.65). At D = 64 the
+  // exponentials (16k, window (4096, 0), before one warp's issue was split in
+  // two: 2.41 ms against 2.65). At D = 64 the
   // products are half as long, there are two buffers, and the waits of twice
   // the groups cost more than they hide.
   static constexpr int kGroups = D == 128 ? 2 : 1;
@@ -1213,30 +1258,22 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 2), 1)
   }
 }
 
-// dK and dV of the tiles that were cut, their parts added in order; 8 entries
-// a thread.
-template <int D, bool BF16>
-__global__ void __launch_bounds__(256) swa_bwd_join_kernel(const SwaBwdProblem p) {
-  constexpr int kRowThreads = D / 8;
-  const int e = threadIdx.x % kRowThreads * 8;
-  const int row = static_cast<int>(blockIdx.y) * (256 / kRowThreads) + threadIdx.x / kRowThreads;
-  const int which = blockIdx.z;  // 0 dK, 1 dV
-  const DkvItem it = dkv_item(p, p.whole_tiles + blockIdx.x * static_cast<uint32_t>(p.splits));
-  const int j = it.j0 + row;
-  if (j >= p.N) return;
+// Gradients of the tiles that were cut, their parts added in order; 8 entries a
+// thread. The parts of a tile are `pitch` entries apart.
+template <bool BF16>
+__device__ __forceinline__ void join_parts(const float* part, int64_t pitch, int parts, void* dst,
+                                           int64_t at, bool g32) {
   float f[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) f[i] = 0.f;
-  for (int s = 0; s < p.splits; ++s) {
-    const float4* src = reinterpret_cast<const float4*>(
-        p.part + ((static_cast<int64_t>(it.part + s) * 2 + which) * kBlk + row) * D + e);
+#pragma unroll 4
+  for (int s = 0; s < parts; ++s, part += pitch) {
+    const float4* src = reinterpret_cast<const float4*>(part);
     const float4 a = src[0], c = src[1];
     f[0] += a.x, f[1] += a.y, f[2] += a.z, f[3] += a.w;
     f[4] += c.x, f[5] += c.y, f[6] += c.z, f[7] += c.w;
   }
-  void* dst = which == 0 ? p.dK : p.dV;
-  const int64_t at = ((static_cast<int64_t>(it.b) * p.N + j) * p.Hkv + it.g) * D + e;
-  if (p.g32) {
+  if (g32) {
     float4* o = reinterpret_cast<float4*>(static_cast<float*>(dst) + at);
     o[0] = make_float4(f[0], f[1], f[2], f[3]);
     o[1] = make_float4(f[4], f[5], f[6], f[7]);
@@ -1247,13 +1284,42 @@ __global__ void __launch_bounds__(256) swa_bwd_join_kernel(const SwaBwdProblem p
   }
 }
 
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) swa_bwd_join_kernel(const SwaBwdProblem p) {
+  constexpr int kRowThreads = D / 8;
+  const int e = threadIdx.x % kRowThreads * 8;
+  const int row = static_cast<int>(blockIdx.y) * (256 / kRowThreads) + threadIdx.x / kRowThreads;
+  const int which = blockIdx.z;  // 0 dK, 1 dV
+  const DkvItem it = dkv_item(p, p.whole_tiles + blockIdx.x * static_cast<uint32_t>(p.splits));
+  const int j = it.j0 + row;
+  if (j >= p.N) return;
+  join_parts<BF16>(p.part + ((static_cast<int64_t>(it.part) * 2 + which) * kBlk + row) * D + e,
+                   2 * kBlk * D, p.splits, which == 0 ? p.dK : p.dV,
+                   ((static_cast<int64_t>(it.b) * p.N + j) * p.Hkv + it.g) * D + e, p.g32);
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) swa_bwd_join_dq_kernel(const SwaBwdProblem p) {
+  constexpr int kRowThreads = D / 8;
+  const int e = threadIdx.x % kRowThreads * 8;
+  const int row = static_cast<int>(blockIdx.y) * (256 / kRowThreads) + threadIdx.x / kRowThreads;
+  const DqItem it = dq_item<true>(p, p.dq_whole + blockIdx.x * static_cast<uint32_t>(p.dq_splits));
+  const int i = it.q0 + row;
+  if (i >= p.M) return;
+  join_parts<BF16>(p.part_q + (static_cast<int64_t>(it.part) * kBlk + row) * D + e, kBlk * D,
+                   p.dq_splits, p.dQ,
+                   ((static_cast<int64_t>(it.b) * p.M + i) * p.H + it.h) * D + e, p.g32);
+}
+
 // ---------------------------------------------------------------- host
 
 constexpr int kSms = 152;
 // In steps of the dK, dV kernel (0.7 us): what an item costs beside its steps, the
-// fewest steps of a part, the launch of the join and a part's 128 KB through it.
+// fewest steps of a part, the launch of the join and a part's 128 KB
+// through it.
 constexpr int kItemSteps = 3, kMinSteps = 4, kJoinSteps = 6;
 constexpr double kPartSteps = 0.05;
+constexpr int kMaxSplits = 64;
 
 int check_swa_bwd(int64_t B, int64_t M, int64_t N, int64_t H, int64_t H_kv, int64_t D) {
   if (B < 0 || M < 0 || N < 0 || H <= 0 || H_kv <= 0) return NSA_ERR_SHAPE;
@@ -1267,33 +1333,28 @@ int check_swa_bwd(int64_t B, int64_t M, int64_t N, int64_t H, int64_t H_kv, int6
   return NSA_OK;
 }
 
-// How the key tiles are cut: `whole` of them are items of their own, the
-// others (the last) are cut into `splits` parts of their steps, so that the SMs
-// do not wait for a last, mostly empty round. Uneven tiles (a causal window
+// How the tiles of a kernel are cut: `whole` of them are items of their own,
+// the others (the last) are cut into `splits` parts of their steps, so that the
+// SMs do not wait for a last, mostly empty round. Uneven tiles (a causal window
 // over the whole sequence) are left alone once they are more than the SMs:
 // their last ones are short.
-struct KeyTiles {
+struct Cut {
   int64_t tiles, whole;
   int splits;
   int64_t items() const { return whole + (tiles - whole) * splits; }
   int64_t parts() const { return (tiles - whole) * splits; }
 };
 
-KeyTiles key_tiles(int64_t B, int64_t M, int64_t N, int64_t H, int64_t H_kv, int64_t left,
-                   int64_t right) {
-  KeyTiles k{B * H_kv * ((N + kBlk - 1) / kBlk), 0, 1};
-  k.whole = k.tiles;
+// `save`: the share of the kernel that cutting has to save.
+Cut cut_tiles(int64_t tiles, int64_t steps, bool even, double save) {
+  Cut k{tiles, tiles, 1};
   const int64_t rest = k.tiles % kSms;
-  int64_t rows = left + right + kBlk;  // queries that see a key tile
-  const bool even = rows <= M || (left >= M && right >= N);
   if (k.tiles == 0 || rest == 0 || (k.tiles > kSms && !even)) return k;
-  if (rows > M) rows = M;
-  const int64_t steps = (rows + kStep - 1) / kStep * (H / H_kv);
   // the rest's time in steps for each number of parts: rounds of parts, each
   // with kItemSteps steps' worth of its own
   const double item = steps + kItemSteps, full = static_cast<double>(k.tiles / kSms) * item;
-  double best = 0.95 * (full + item) - full;  // cutting has to save 5 % of the kernel
-  for (int s = 2; s <= 16 && steps / s >= kMinSteps; ++s) {
+  double best = (1 - save) * (full + item) - full;
+  for (int s = 2; s <= kMaxSplits && steps / s >= kMinSteps; ++s) {
     const double t = static_cast<double>((rest * s + kSms - 1) / kSms) *
                          (static_cast<double>(steps) / s + kItemSteps) +
                      kJoinSteps + kPartSteps * rest * s;
@@ -1304,6 +1365,24 @@ KeyTiles key_tiles(int64_t B, int64_t M, int64_t N, int64_t H, int64_t H_kv, int
     }
   }
   return k;
+}
+
+// Of the dK, dV kernel, whose key tiles' steps are those of all query heads, and
+// of the dQ kernel, whose steps take some 7 % longer when it can be cut: 4 heads
+// of 2048 x 2048 would save 11 % by the rule and lost 2 of 55 us, a head of
+// 4096 x 4096, causal, gained 6 to 12 of 66, 8 of 128 x 32,768 went from 300 to 84.
+Cut key_tiles(int64_t B, int64_t M, int64_t N, int64_t H, int64_t H_kv, int64_t left,
+              int64_t right) {
+  const int64_t rows = left + right + kBlk;  // queries that see a key tile
+  return cut_tiles(B * H_kv * ((N + kBlk - 1) / kBlk),
+                   ((rows < M ? rows : M) + kStep - 1) / kStep * (H / H_kv),
+                   rows <= M || (left >= M && right >= N), 0.05);
+}
+
+Cut query_tiles(int64_t B, int64_t M, int64_t N, int64_t H, int64_t left, int64_t right) {
+  const int64_t keys = left + right + kBlk;  // keys that a query tile sees
+  return cut_tiles(B * H * ((M + kBlk - 1) / kBlk), ((keys < N ? keys : N) + kStep - 1) / kStep,
+                   keys <= N || (left >= M && right >= N), 0.2);
 }
 
 struct WindowSides {
@@ -1325,15 +1404,14 @@ int launch_swa_bwd(const SwaBwdProblem& p, cudaStream_t st) {
       !encode_kv_map(&to, p.O, p.B, p.M, p.H, D, kStep, dt) ||
       !encode_kv_map(&td, p.dO, p.B, p.M, p.H, D, kStep, dt))
     return NSA_ERR_LAUNCH;
-  auto dq = swa_bwd_dq_kernel<D, BF16>;
+  auto dq = p.part_q != nullptr ? swa_bwd_dq_kernel<D, BF16, true> : swa_bwd_dq_kernel<D, BF16, false>;
   auto dkv = swa_bwd_dkv_kernel<D, BF16>;
   if (cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, DqCfg<D>::kSmem) !=
           cudaSuccess ||
       cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, DkvCfg<D>::kSmem) !=
           cudaSuccess)
     return NSA_ERR_LAUNCH;
-  const int64_t qi = static_cast<int64_t>(p.B) * p.H * p.qtiles;
-  const int64_t ki = p.dkv_items;
+  const int64_t qi = p.dq_items, ki = p.dkv_items;
   // one CTA per SM, items dealt to them
   dq<<<static_cast<unsigned>(qi < kSms ? qi : kSms), 32 * (kMmaWarp + 1), DqCfg<D>::kSmem, st>>>(p, tk, tv,
                                                                                        tq, to, td);
@@ -1341,6 +1419,11 @@ int launch_swa_bwd(const SwaBwdProblem& p, cudaStream_t st) {
   dkv<<<static_cast<unsigned>(ki < kSms ? ki : kSms), 32 * (kMmaWarp + 2), DkvCfg<D>::kSmem, st>>>(
       p, tq, td, tk, tv);
   if (cudaGetLastError() != cudaSuccess) return NSA_ERR_LAUNCH;
+  if (p.part_q != nullptr) {
+    const dim3 grid(static_cast<unsigned>(p.B * p.H * p.qtiles - p.dq_whole), kBlk * D / 8 / 256);
+    swa_bwd_join_dq_kernel<D, BF16><<<grid, 256, 0, st>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return NSA_ERR_LAUNCH;
+  }
   if (p.part != nullptr) {
     const dim3 grid(static_cast<unsigned>(p.B * p.Hkv * p.ktiles - p.whole_tiles), kBlk * D / 8 / 256,
                     2);
@@ -1365,7 +1448,10 @@ extern "C" int64_t nsa_swa_bwd_workspace_bytes(int64_t B, int64_t M, int64_t N, 
   if (B == 0 || M == 0 || N == 0) return 0;
   const WindowSides w = clamp_window(M, N, window_left, window_right);
   const int64_t Mp = (M + kStep - 1) / kStep * kStep;
-  return 2 * B * H * Mp * 4 + key_tiles(B, M, N, H, H_kv, w.left, w.right).parts() * 2 * kBlk * D * 4;
+  return 2 * B * H * Mp * 4 +
+         (key_tiles(B, M, N, H, H_kv, w.left, w.right).parts() * 2 +
+          query_tiles(B, M, N, H, w.left, w.right).parts()) *
+             kBlk * D * 4;
 }
 
 extern "C" int nsa_swa_bwd(const void* Q, const void* K, const void* V, const void* O,
@@ -1422,11 +1508,14 @@ extern "C" int nsa_swa_bwd(const void* Q, const void* K, const void* V, const vo
   p.Mp = static_cast<int>((M + kStep - 1) / kStep * kStep);
   p.qtiles = static_cast<int>((M + kBlk - 1) / kBlk);
   p.ktiles = static_cast<int>((N + kBlk - 1) / kBlk);
-  const KeyTiles tiles = key_tiles(B, M, N, H, H_kv, w.left, w.right);
-  p.splits = tiles.splits;
-  p.whole_tiles = static_cast<int>(tiles.whole);
-  p.dkv_items = static_cast<int>(tiles.items());
-  p.dq_items = static_cast<int>(B * H * p.qtiles);
+  const Cut keys_cut = key_tiles(B, M, N, H, H_kv, w.left, w.right);
+  p.splits = keys_cut.splits;
+  p.whole_tiles = static_cast<int>(keys_cut.whole);
+  p.dkv_items = static_cast<int>(keys_cut.items());
+  const Cut queries_cut = query_tiles(B, M, N, H, w.left, w.right);
+  p.dq_splits = queries_cut.splits;
+  p.dq_whole = static_cast<int>(queries_cut.whole);
+  p.dq_items = static_cast<int>(queries_cut.items());
   p.left = static_cast<int>(w.left);
   p.right = static_cast<int>(w.right);
   p.scale = scale > 0.f ? scale : 1.0f / sqrtf(static_cast<float>(D));
@@ -1436,7 +1525,9 @@ extern "C" int nsa_swa_bwd(const void* Q, const void* K, const void* V, const vo
   const int64_t stat = B * H * p.Mp;
   p.nlse2 = static_cast<float*>(workspace);
   p.ndelta = p.nlse2 + stat;
-  p.part = tiles.parts() > 0 ? p.ndelta + stat : nullptr;
+  float* const parts = p.ndelta + stat;
+  p.part = keys_cut.parts() > 0 ? parts : nullptr;
+  p.part_q = queries_cut.parts() > 0 ? parts + keys_cut.parts() * 2 * kBlk * D : nullptr;
   const bool bf = dtype == NSA_BF16;
   if (D == 64) return bf ? launch_swa_bwd<64, true>(p, st) : launch_swa_bwd<64, false>(p, st);
   return bf ? launch_swa_bwd<128, true>(p, st) : launch_swa_bwd<128, false>(p, st);

@@ -102,6 +102,31 @@ def test_lengths(M, N, window):
     _check(t, window, "bf16", _run(t, window, "bf16"), what=f"{M}x{N} {window}")
 
 
+CUT = [
+    # few query tiles and many keys, and the other way: both kernels cut into
+    # parts, some without a step (a causal window's short tiles)
+    (1, 1, 4100, 1, 1, 64, "bf16", (-1, -1)),
+    (1, 130, 2500, 3, 1, 128, "f16", (0, -1)),
+    (2, 200, 3000, 2, 2, 128, "bf16", (-1, 2000)),
+    (1, 2100, 2100, 1, 1, 128, "bf16", (-1, 0)),
+    (1, 2050, 2049, 2, 1, 64, "f16", (5, -1)),
+    (1, 4100, 40, 8, 1, 128, "bf16", (-1, -1)),
+    (1, 1500, 5, 3, 1, 64, "bf16", (100, 1400)),
+]
+
+
+@pytest.mark.parametrize("B,M,N,H,G,D,dtype,window", CUT)
+@pytest.mark.parametrize("grad", ["f32", None])
+def test_cut_tiles(B, M, N, H, G, D, dtype, window, grad):
+    import torch
+
+    t = _problem(B, M, N, H, G, D, dtype, window, 31)
+    out = _run(t, window, dtype, grad)
+    _check(t, window, dtype, out, grad, what=f"{M}x{N} {window}")
+    for x, y in zip(out, _run(t, window, dtype, grad)):
+        assert torch.equal(x, y)
+
+
 @pytest.mark.parametrize("H,G", [(4, 4), (6, 2), (3, 1), (16, 1), (5, 5)])
 @pytest.mark.parametrize("grad", ["f32", None])
 def test_head_groups_scale_and_fp32_gradients(H, G, grad):

@@ -59,6 +59,9 @@ def test_workspace(lib):
     assert f(1, 8192, 8192, 64, 8, 128, 512, 0) == 2 * 64 * 8192 * 4 + 56 * 2 * tile
     # uneven tiles, more than the SMs: whole
     assert f(1, 8192, 8192, 64, 8, 128, -1, 0) == 2 * 64 * 8192 * 4
+    # 8 query tiles of 512 steps, cut into 19 parts, one for each SM, beside
+    # 256 key tiles of 16 steps: 152 and 104 more, whole
+    assert f(1, 128, 32768, 8, 1, 128, -1, -1) == 2 * 8 * 128 * 4 + 8 * 19 * tile // 2
     assert f(1, 0, 300, 16, 2, 128, -1, -1) == 0 and f(1, 300, 0, 16, 2, 128, -1, -1) == 0
     assert f(1, 300, 300, 15, 2, 128, -1, -1) == -5 and f(1, 300, 300, 16, 2, 80, -1, -1) == -4
     need = f(2, 300, 300, 16, 2, 128, 64, 0)
