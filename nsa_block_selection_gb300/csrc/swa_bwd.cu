@@ -45,15 +45,15 @@
 //
 // What bounds it. D = 128: the tensor pipe, busy 68 % (dQ) and 69 % (dK, dV) of
 // the clocks at 8192 tokens of 64 + 8 heads, window (512, 0), where the items
-// have 10 to 64 steps: 163 and 222 us, 5 us of joining, DRAM at 3.1 and 1.6 TB/s;
+// have 10 to 64 steps: 166 and 226 us, 6 us of joining, DRAM at 3.1 and 1.6 TB/s;
 // a step's products take 512 (dQ: 384) clocks and its
 // barriers, of which one that is over still takes a warp 100 to 300 clocks,
 // are most of the rest. 16,384 tokens, window (4096, 0): 1.52 and 2.15 ms,
-// 1.4 PFLOP/s over the 7 products; back to back the clock falls to 1.6 to
+// 1.8 PFLOP/s over the 7 products; back to back the clock falls to 1.6 to
 // 1.9 GHz at the power limit. D = 64: the elementwise warps (2 x 16 heads of
 // 1500 x 2048: 47 and 69 us), as the products are half as long and the
 // exponentials are not. Short calls: their launches and the latency of a
-// few dependent steps (2 x 1000 tokens, 8 + 2 heads: 9, 21 and 5 us).
+// few dependent steps (2 x 1000 tokens, 8 + 2 heads: 12, 19 and 6 us).
 //
 // Every mbarrier wait is bounded (1 s); a role that gives up sets the status
 // word, waits for its own copies, and every role reaches the teardown, which
@@ -1315,9 +1315,9 @@ __global__ void __launch_bounds__(256) swa_bwd_join_dq_kernel(const SwaBwdProble
 
 constexpr int kSms = 152;
 // In steps of the dK, dV kernel (0.7 us): what an item costs beside its steps, the
-// fewest steps of a part, the launch of the join and a part's 128 KB
+// fewest steps of a part, the join (on the host too) and a part's 128 KB
 // through it.
-constexpr int kItemSteps = 3, kMinSteps = 4, kJoinSteps = 6;
+constexpr int kItemSteps = 3, kMinSteps = 4, kJoinSteps = 8;
 constexpr double kPartSteps = 0.05;
 constexpr int kMaxSplits = 64;
 
