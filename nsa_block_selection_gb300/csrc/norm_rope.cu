@@ -22,8 +22,8 @@
 // of one token, whose angles they share, with few they hold several tokens.
 //
 // Measured, bf16, 64 + 8 heads of D = 128: 65,536 tokens forward 389 us
-// (6.2 TB/s, 92 % of a copy), 32,768 tokens backward 336 us (5.4 TB/s, 80 %:
-// of the instruction slots 56 % are taken, and 24 warps an SM, what 80
+// (6.2 TB/s, 92 % of a copy), 32,768 tokens backward 333 us (5.5 TB/s, 81 %:
+// of the instruction slots 58 % are taken, and 24 warps an SM, what 80
 // registers a thread allow, keep too few loads in flight for more). Short
 // calls are bound by their launches: a token of 64 + 8 heads takes 5 us on
 // the device, most of it the launch.
