@@ -463,8 +463,8 @@ int nsa_swa_fwd(const void* Q, const void* K, const void* V, void* O, float* LSE
 /*
  * nsa_swa_bwd_workspace_bytes -- device workspace of nsa_swa_bwd: LSE and
  * delta of every (batch, head, query), and, where tiles of keys or of queries
- * are cut because they do not fill the SMs, fp32 parts of dK and dV (at most
- * 9728 tiles of 128 KB at D = 128) and of dQ (half of that). Negative nsa_status for invalid sizes.
+ * are cut because they do not fill the SMs, fp32 parts of dK and dV (128 KB each
+ * at D = 128, some 152 to 304 of them as a rule) and of dQ (64 KB). Negative nsa_status for invalid sizes.
  * Pure host arithmetic.
  */
 int64_t nsa_swa_bwd_workspace_bytes(int64_t B, int64_t M, int64_t N, int64_t H, int64_t H_kv,
@@ -560,7 +560,8 @@ int nsa_qk_norm_rope(const void* Q, const void* K, void* Qo, void* Ko, const voi
 
 /*
  * nsa_qk_norm_rope_bwd_workspace_bytes -- device workspace of
- * nsa_qk_norm_rope_bwd: a partial weight gradient of each of up to 456 CTAs. Negative nsa_status for invalid sizes. Pure host arithmetic.
+ * nsa_qk_norm_rope_bwd: a partial weight gradient of each of up to 456 CTAs.
+ * Negative nsa_status for invalid sizes. Pure host arithmetic.
  */
 int64_t nsa_qk_norm_rope_bwd_workspace_bytes(int64_t B, int64_t M, int64_t D);
 

@@ -515,6 +515,9 @@ def _on_stream(call):
         if stream is None:
             return call(*args, **kw)
         load()
+        q = args[0] if args else kw["q"]
+        if stream.device != q.device:
+            raise ValueError(f"stream must be one of q's device ({q.device}), got {stream.device}")
         with _torch.cuda.stream(stream):
             return call(*args, **kw)
 

@@ -150,3 +150,21 @@ def test_rope_tables():
     assert abs(sin[p, i].item() - np.sin(ang)) < 2 ** -24
     with pytest.raises(ValueError):
         rope_tables(10, 7)
+
+
+def test_stream_of_another_device_is_refused():
+    """Before anything is launched or made current."""
+    import types
+
+    import torch
+
+    from nsa_block_selection_gb300 import qk_norm_rope, qk_norm_rope_bwd
+
+    q, k = torch.zeros(1, 4, 2, 64).half(), torch.zeros(1, 4, 1, 64).half()
+    other = types.SimpleNamespace(device=torch.device("cuda:7"))
+    with pytest.raises(ValueError, match="stream"):
+        qk_norm_rope(q, k, stream=other)
+    with pytest.raises(ValueError, match="stream"):
+        qk_norm_rope(q=q, k=k, stream=other)
+    with pytest.raises(ValueError, match="stream"):
+        qk_norm_rope_bwd(q, k, q, k, stream=other)

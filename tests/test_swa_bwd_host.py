@@ -92,3 +92,16 @@ def test_binding_refuses():
         swa_bwd(q, k, k, q, lse[:, :, :7], q)
     with pytest.raises(ValueError):  # not on a GPU
         swa_bwd(q, k, k, q, lse, q)
+
+
+def test_stream_of_another_device_is_refused():
+    import types
+
+    import torch
+
+    from nsa_block_selection_gb300 import swa_bwd
+
+    q, k = torch.zeros(1, 8, 4, 64).bfloat16(), torch.zeros(1, 8, 2, 64).bfloat16()
+    other = types.SimpleNamespace(device=torch.device("cuda:7"))
+    with pytest.raises(ValueError, match="stream"):
+        swa_bwd(q, k, k, q, torch.zeros(1, 4, 8), q, stream=other)
