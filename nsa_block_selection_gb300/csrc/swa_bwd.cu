@@ -258,7 +258,7 @@ struct DqCfg {
   static constexpr int kOffStat = kOffDo + kBlk * D * 2;  // 2 x (LSE in base 2, delta) of the rows
   static constexpr int kOffBar = kOffStat + 4 * kBlk * 4;
   static constexpr int kFull = 0, kEmpty = kStages, kOStaged = 2 * kStages, kQStaged = kOStaged + 1,
-                       kQReady = kQStaged + 1, kDoReady = kQReady + 1, kSDone = kDoReady + 1,
+                       kQReady = kQStaged + 1, kDoReady = kQReady + 1, kSDone = kDoReady + 2,
                        kDpDone = kSDone + 1, kSFull = kDpDone + 1, kDsFull = kSFull + 2,
                        kDqDone = kDsFull + 2, kDqFree = kDqDone + 1, kNumBars = kDqFree + 1;
   static constexpr int kOffTmem = kOffBar + kNumBars * 8;
@@ -338,7 +338,10 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 1), 1)
     mbar_init(bar(C::kOStaged), 1);
     mbar_init(bar(C::kQStaged), 1);
     mbar_init(bar(C::kQReady), 4);
+    // two, for even and odd items: an elementwise warp may ask for an item's
+    // when the next item's dO is there already
     mbar_init(bar(C::kDoReady), 4);
+    mbar_init(bar(C::kDoReady + 1), 4);
     mbar_init(bar(C::kSDone), 1);
     mbar_init(bar(C::kDpDone), 1);
     for (int s = 0; s < 2; ++s) {
@@ -454,7 +457,7 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 1), 1)
           tc_mma_ts_if(on, tmem + C::kColS + (g & 1) * kStep, tmem + C::kColQ + 8 * kk,
                        desc_at(kd, (kk >> 2) * kAtomStep + (kk & 3) * 32), id_s, kk > 0 ? 1u : 0u);
         if (i == nt - 1) tc_commit_if(on, bar(C::kSDone));  // Q has been read
-        if (i == 0) ok = wait_all(C::kDoReady, n & 1);
+        if (i == 0) ok = wait_all(C::kDoReady + (n & 1), (n >> 1) & 1);
         if (!ok) break;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
@@ -622,7 +625,7 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 1), 1)
         return true;
       };
       if (!wait_all(C::kQStaged, n & 1) || !move(q_row, C::kColQ, C::kSDone, C::kQReady) ||
-          !move(do_row, C::kColDo, C::kDpDone, C::kDoReady)) {
+          !move(do_row, C::kColDo, C::kDpDone, C::kDoReady + static_cast<int>(n & 1))) {
         failed = true;
         break;
       }
@@ -662,7 +665,7 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 1), 1)
       if (x >= items) continue;
       const DqItem it = dq_item<CUT>(p, x);
       if (it.nt == 0) continue;
-      if (!wait_all(C::kDoReady, n & 1)) {
+      if (!wait_all(C::kDoReady + (n & 1), (n >> 1) & 1)) {
         failed = true;
         break;
       }
