@@ -463,9 +463,9 @@ int nsa_swa_fwd(const void* Q, const void* K, const void* V, void* O, float* LSE
 /*
  * nsa_swa_bwd_workspace_bytes -- device workspace of nsa_swa_bwd: LSE and
  * delta of every (batch, head, query), and, where tiles of keys or of queries
- * are cut because they do not fill the SMs, fp32 parts of dK and dV (128 KB each
- * at D = 128, some 152 to 304 of them as a rule) and of dQ (64 KB). Negative nsa_status for invalid sizes.
- * Pure host arithmetic.
+ * are cut because they do not fill the SMs, fp32 parts of dK and dV (128 KB
+ * each at D = 128, some 152 to 304 of them as a rule) and of dQ (64 KB).
+ * Negative nsa_status for invalid sizes. Pure host arithmetic.
  */
 int64_t nsa_swa_bwd_workspace_bytes(int64_t B, int64_t M, int64_t N, int64_t H, int64_t H_kv,
                                     int64_t D, int64_t window_left, int64_t window_right);

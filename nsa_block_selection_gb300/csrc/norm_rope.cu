@@ -956,9 +956,11 @@ extern "C" int nsa_qk_norm_rope_bwd(
   p.a.w32 = weight_dtype == NSA_F32;
   p.a.eps = eps;
   p.q = {static_cast<const uint8_t*>(Q), static_cast<const uint8_t*>(dQo), static_cast<uint8_t*>(dQ),
-         wq, s[0], s[1], s[2], s[6], s[7], s[8], s[12], s[13], s[14], static_cast<int>(H), 0, 0, 0, 0};
+         wq, s[0], s[1], s[2], s[6], s[7], s[8], s[12], s[13], s[14],
+         static_cast<int>(H)};
   p.k = {static_cast<const uint8_t*>(K), static_cast<const uint8_t*>(dKo), static_cast<uint8_t*>(dK),
-         wk, s[3], s[4], s[5], s[9], s[10], s[11], s[15], s[16], s[17], static_cast<int>(G), 0, 0, 0, 0};
+         wk, s[3], s[4], s[5], s[9], s[10], s[11], s[15], s[16], s[17],
+         static_cast<int>(G)};
   p.part = want_dw ? static_cast<float*>(workspace) : nullptr;
   const bool bf = dtype == NSA_BF16, g32 = grad_dtype == NSA_F32;
   if (D == 64) {

@@ -84,18 +84,9 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
 }
 
 // The same from a warp that stays converged: every lane passes the same
-// operands and the one with `on` set issues. Descriptors and addresses then
-// live in uniform registers; issued from under a lane == 0 branch each MMA
-// costs 60 to 80 clocks of moves to them, more than a 64-column MMA takes.
-__device__ __forceinline__ void tc_mma_if(uint32_t on, uint32_t d_tmem, uint64_t a, uint64_t b,
-                                          uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
-      : "memory");
-}
-
+// operands and the one with `on` set issues. Issued from under a lane == 0
+// branch an MMA costs the warp 60 to 80 clocks more, twice what a 64-column
+// MMA takes.
 __device__ __forceinline__ void tc_mma_ts_if(uint32_t on, uint32_t d_tmem, uint32_t a_tmem,
                                              uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
