@@ -46,14 +46,15 @@ constexpr int kRopeThreads = 128;      // forward CTAs: 4 warps, each a unit of 
 constexpr int kRopeBwdThreads = 256;   // backward CTAs: 8 warps that share one dw partial
 constexpr int kRopeBwdPerSm = 3;       // and how many of them an SM holds
 constexpr int kRopeSms = 152;
-// The forward gives every row slot its own token and head up to this many
-// groups of slots a token, or this many groups in all; beyond, a warp walks a
-// token's heads with one set of angles and weights. Both measured, 32,768
-// tokens of 24 + 8 heads at D = 64 (4 groups): 71 us against 85, 32 + 4 (5
-// groups): 87 and 87, 32 + 4 at D = 128 (9 groups): 153 against 126; 1000
-// tokens of that: 13 against 17.
-constexpr int kFewPerToken = 4;
-constexpr int64_t kFewGroups = 64 * kRopeSms;
+constexpr int kFewPerSm = 7;  // CTAs of norm_rope_few_kernel that an SM holds
+// The forward gives every row slot its own token up to this many groups of
+// slots a token, or this many groups in all; beyond, a warp walks a token's
+// heads with one set of angles. Both measured, 32,768 tokens of 32 + 4 heads at
+// D = 64 (5 groups): 77 us against 87, of 24 + 8 at D = 128 (8): 120 and 122, of
+// 32 + 4 at D = 128 (9): 132 against 126; 1000 tokens of 64 + 8 at D = 128
+// (18,000 groups): 16 against 18, 4096 tokens of those (73,728): 40 against 38.
+constexpr int kFewPerToken = 8;
+constexpr int64_t kFewGroups = 128 * kRopeSms;
 // What a unit of the backward that walks a token's heads costs, beside a
 // group of slots that hold several tokens: its position and angles, and each
 // group of the heads. Shares of the CTAs by these against shares by groups of
@@ -273,91 +274,80 @@ __global__ void __launch_bounds__(kRopeThreads)
 // token to a group of slots, or several, with the heads rounded up to a power
 // of two; more heads than slots take several groups.
 struct RowGroups {
-  int per_token;   // groups of a token (1 where tokens share a group)
-  int shift;       // log2 of the slots of a token, where tokens share a group
+  int per_token;  // groups of a token (1 where tokens share a group)
+  int shift;      // log2 of the slots of a token, where tokens share a group
   int64_t groups;
 };
 
-template <int RPW>
-__device__ __forceinline__ void group_row(const RowGroups& g, uint32_t q, int sub, uint32_t& tok,
-                                          int& head) {
-  if (g.per_token > 1) {
-    tok = q / static_cast<uint32_t>(g.per_token);
-    head = static_cast<int>(q - tok * g.per_token) * RPW + sub;
-  } else {
-    tok = q * (static_cast<uint32_t>(RPW) >> g.shift) + (static_cast<uint32_t>(sub) >> g.shift);
-    head = sub & ((1 << g.shift) - 1);
-  }
-}
-
-// The forward where a token has few heads: a warp takes UN groups of slots,
-// each lane with the position and the angles of its own token, all loaded
-// together. (A warp per token leaves row slots empty and pays the latencies of
+// The forward where a token has few heads: a row slot of a warp keeps its head,
+// and the head's weights, and walks the tokens, each with its own position and
+// angles. (A warp per token leaves row slots empty and pays the latencies of
 // position, angles and rows for each: 32,768 tokens of 1 + 1 heads at D = 64
-// 73 us against 15, of 8 + 2 76 against 39.)
-template <int D, bool BF16, int UN>
-__global__ void __launch_bounds__(kRopeThreads)
+// 73 us against 13, of 8 + 2 76 against 36. Two rows in flight a lane leave 16
+// to 20 warps an SM: 40 for the latter, with 28 warps of one row it is 36;
+// loading the next position early gave nothing.)
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kRopeThreads, kFewPerSm)
     norm_rope_few_kernel(const RopeProblem p, const RowGroups rg) {
   constexpr int LPR = D / 16, RPW = 32 / LPR;
   const int lane = threadIdx.x & 31, sub = lane / LPR, tl = lane % LPR;
-  const int64_t q0 =
-      (static_cast<int64_t>(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5)) * UN;
-  if (q0 >= rg.groups) return;
+  // this warp's place among the groups of a token, and where its walk begins
+  const uint32_t groups = static_cast<uint32_t>(rg.per_token);
+  const uint32_t wid = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t walks = gridDim.x * (kRopeThreads / 32) / groups;
+  const uint32_t first = wid / groups;
+  if (first >= walks) return;
+  // slots of a group that hold one token, and tokens of a group
+  const int wide = rg.per_token > 1 ? RPW : 1 << rg.shift;
+  const uint32_t sets = static_cast<uint32_t>(RPW / wide);
+  const int head = static_cast<int>(wid - first * groups) * RPW + (sub & (wide - 1));
+  const bool is_k = head >= p.q.heads, slot = head < p.q.heads + p.k.heads;
+  const RopeRows& t = is_k ? p.k : p.q;
+  const int64_t h = is_k ? head - p.q.heads : head;
   int c0, c1;
   row_chunks(tl, p.half, c0, c1);
   const bool rot = tl < (p.half >> 3);
-  const uint32_t tokens = static_cast<uint32_t>(p.B) * static_cast<uint32_t>(p.M);
-  uint4 v[UN][2];
-  uint8_t* y[UN];
-  int64_t at[UN];
-  bool is_k[UN];
-#pragma unroll
-  for (int u = 0; u < UN; ++u) {
-    uint32_t tok;
-    int head;
-    group_row<RPW>(rg, static_cast<uint32_t>(q0) + u, sub, tok, head);
-    const bool in = q0 + u < rg.groups && tok < tokens && head < p.q.heads + p.k.heads;
-    is_k[u] = head >= p.q.heads;
-    y[u] = nullptr;
-    at[u] = -1;
-    v[u][0] = v[u][1] = make_uint4(0, 0, 0, 0);
+  float w[16];
+  load_weights<BF16>(t.w, p.w32, c0, c1, w);
+  const uint8_t* const x = t.x + 2 * h * t.xh;
+  uint8_t* const y = t.y + 2 * h * t.yh;
+  const uint64_t tokens = static_cast<uint64_t>(p.B) * p.M;
+  // (all lanes of a warp go through the loop together: row_sum needs them)
+  for (uint64_t begin = static_cast<uint64_t>(first) * sets; begin < tokens;
+       begin += static_cast<uint64_t>(walks) * sets) {
+    const uint64_t tok = begin + static_cast<uint32_t>(sub / wide);
+    const bool in = slot && tok < tokens;
+    bool live = false;
+    int64_t yo = 0;
+    float f[16], c[8], s[8];
+    uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
     if (in) {
-      const int b = static_cast<int>(tok / static_cast<uint32_t>(p.M));
-      const int m = static_cast<int>(tok - static_cast<uint32_t>(b) * p.M);
-      const int64_t h = is_k[u] ? head - p.q.heads : head;
-      at[u] = token_position(p, b, m);
-      y[u] = is_k[u] ? p.k.y + 2 * (b * p.k.yb + m * p.k.ym + h * p.k.yh)
-                     : p.q.y + 2 * (b * p.q.yb + m * p.q.ym + h * p.q.yh);
-      if (at[u] >= 0) {  // (padding is not read)
-        const uint4* src = reinterpret_cast<const uint4*>(
-            is_k[u] ? p.k.x + 2 * (b * p.k.xb + m * p.k.xm + h * p.k.xh)
-                    : p.q.x + 2 * (b * p.q.xb + m * p.q.xm + h * p.q.xh));
-        v[u][0] = src[c0];
-        v[u][1] = src[c1];
+      const int b = static_cast<int>(static_cast<uint32_t>(tok) / static_cast<uint32_t>(p.M));
+      const int m = static_cast<int>(static_cast<uint32_t>(tok) - static_cast<uint32_t>(b) * p.M);
+      const int64_t at = token_position(p, b, m);
+      yo = 2 * (b * t.yb + m * t.ym);
+      live = at >= 0;
+      if (live) {  // (padding is not read)
+        const uint4* src = reinterpret_cast<const uint4*>(x + 2 * (b * t.xb + m * t.xm));
+        v0 = src[c0];
+        v1 = src[c1];
+        if (rot) load_angles(p, at, c0, c1, c, s);
       }
     }
-  }
-#pragma unroll
-  for (int u = 0; u < UN; ++u) {
-    float f[16], w[16], c[8], s[8];
-    if (at[u] >= 0) {
-      if (rot) load_angles(p, at[u], c0, c1, c, s);
-      load_weights<BF16>(is_k[u] ? p.k.w : p.q.w, p.w32, c0, c1, w);
-    }
-    unpack8<BF16>(v[u][0], f);
-    unpack8<BF16>(v[u][1], f + 8);
+    unpack8<BF16>(v0, f);
+    unpack8<BF16>(v1, f + 8);
     float sq = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) sq = fmaf(f[i], f[i], sq);
     sq = row_sum<LPR>(sq);
-    if (at[u] >= 0) {  // a padding token's rows are zero
+    if (live) {  // a padding token's rows are zero
       const float rs = rsqrtf(sq * (1.f / D) + p.eps);
 #pragma unroll
       for (int i = 0; i < 16; ++i) f[i] *= rs * w[i];
       if (rot) turn(f, c, s, p.interleaved);
     }
-    if (y[u] != nullptr) {
-      uint4* dst = reinterpret_cast<uint4*>(y[u]);
+    if (in) {
+      uint4* dst = reinterpret_cast<uint4*>(y + yo);
       dst[c0] = pack8<BF16>(f);
       dst[c1] = pack8<BF16>(f + 8);
     }
@@ -415,6 +405,14 @@ __device__ __forceinline__ float wide_row_sum(float v) {
 #pragma unroll
   for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
   return v;
+}
+
+// The token and head of a row slot in group q.
+template <int RPW>
+__device__ __forceinline__ void group_row(const RowGroups& g, uint32_t q, int sub, uint32_t& tok,
+                                          int& head) {
+  tok = q * (static_cast<uint32_t>(RPW) >> g.shift) + (static_cast<uint32_t>(sub) >> g.shift);
+  head = sub & ((1 << g.shift) - 1);
 }
 
 // What a lane of the backward holds of one row, and what it does with it.
@@ -813,13 +811,15 @@ int launch_norm_rope(const RopeProblem& p, cudaStream_t st) {
   const int64_t tokens = static_cast<int64_t>(p.B) * p.M;
   const RowGroups g = plan_row_groups(rows, tokens, RPW);
   if (rows <= kFewPerToken * RPW || g.groups <= kFewGroups) {
-    constexpr int FUN = 2;
-    if (g.groups < (int64_t(1) << 32)) {
-      const int64_t per_cta = kRopeThreads / 32 * FUN;
-      norm_rope_few_kernel<D, BF16, FUN>
-          <<<static_cast<unsigned>((g.groups + per_cta - 1) / per_cta), kRopeThreads, 0, st>>>(p, g);
-      return cudaGetLastError() == cudaSuccess ? NSA_OK : NSA_ERR_LAUNCH;
-    }
+    // a warp for every group of all tokens, or as many as the SMs hold, but one
+    // for each group of a token
+    constexpr int64_t kWarps = kRopeThreads / 32;
+    int64_t warps = g.groups;
+    if (warps > kFewPerSm * kRopeSms * kWarps) warps = kFewPerSm * kRopeSms * kWarps;
+    if (warps < g.per_token) warps = g.per_token;
+    norm_rope_few_kernel<D, BF16>
+        <<<static_cast<unsigned>((warps + kWarps - 1) / kWarps), kRopeThreads, 0, st>>>(p, g);
+    return cudaGetLastError() == cudaSuccess ? NSA_OK : NSA_ERR_LAUNCH;
   }
   // rows per warp: a whole token when the tokens alone give every SM 16
   // warps, else as few rows as it takes to get there
