@@ -25,7 +25,7 @@
 // (6.2 TB/s, 92 % of a copy), 32,768 tokens backward 333 us (5.5 TB/s, 81 %:
 // of the instruction slots 58 % are taken, and 24 warps an SM, what 80
 // registers a thread allow, keep too few loads in flight for more). Short
-// calls are bound by their launches: a token of 64 + 8 heads takes 5 us on
+// calls are bound by their launches: a token of 64 + 8 heads takes 4 us on
 // the device, most of it the launch.
 
 #include <cuda_bf16.h>
