@@ -504,24 +504,14 @@ def _launch(dev, fn, *args):
         return fn(*args, c._cuda_getCurrentRawStream(dev))
 
 
-def _on_stream(call):
-    """A ``stream`` argument for a call that runs on the current stream: what
-    the call allocates (a workspace that it drops on return among it) then
-    comes from that stream's memory, and waits for that stream's work."""
-    import functools
-
-    @functools.wraps(call)
-    def run(*args, stream=None, **kw):
-        if stream is None:
-            return call(*args, **kw)
-        load()
-        q = args[0] if args else kw["q"]
-        if stream.device != q.device:
-            raise ValueError(f"stream must be one of q's device ({q.device}), got {stream.device}")
-        with _torch.cuda.stream(stream):
-            return call(*args, **kw)
-
-    return run
+def _on_stream(stream, call, q, *args):
+    """call(q, *args) with ``stream`` current: what the call allocates (a
+    workspace that it drops on return among it) then comes from that stream's
+    memory, and waits for that stream's work."""
+    if stream.device != q.device:
+        raise ValueError(f"stream must be one of q's device ({q.device}), got {stream.device}")
+    with _torch.cuda.stream(stream):
+        return call(q, *args)
 
 
 def swa_bwd_workspace_bytes(B, M, N, H, H_kv, D, window=(-1, -1)) -> int:
@@ -531,9 +521,8 @@ def swa_bwd_workspace_bytes(B, M, N, H, H_kv, D, window=(-1, -1)) -> int:
     return int(n)
 
 
-@_on_stream
 def swa_bwd(q, k, v, o, lse, do, window=(-1, -1), scale: Optional[float] = None, dq=None, dk=None,
-            dv=None, grad_dtype=None, workspace=None):
+            dv=None, grad_dtype=None, workspace=None, *, stream=None):
     """Gradients of :func:`swa_fwd` (nsa_swa_bwd): returns (dQ, dK, dV).
 
     q, k, v, ``window`` and ``scale`` as passed to the forward, ``o`` and
@@ -546,6 +535,9 @@ def swa_bwd(q, k, v, o, lse, do, window=(-1, -1), scale: Optional[float] = None,
     on it too).
     """
     lib = _lib or load()
+    if stream is not None:
+        return _on_stream(stream, swa_bwd, q, k, v, o, lse, do, window, scale, dq, dk, dv,
+                          grad_dtype, workspace)
     dt, qs, ks = q.dtype, q.shape, k.shape
     if dt not in _F16_KINDS:
         raise TypeError(f"q must be fp16 or bf16, got {dt}")
@@ -696,9 +688,9 @@ def _check_rope(named, q_weight, k_weight, cos, sin, positions):
         NSA_F32 if wdt is None else _DTYPE_CODES[wdt], strides
 
 
-@_on_stream
 def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
-                 eps: float = 1e-6, interleaved: bool = False, q_out=None, k_out=None):
+                 eps: float = 1e-6, interleaved: bool = False, q_out=None, k_out=None, *,
+                 stream=None):
     """RMS norm of every query and key head and the position rotation, in one
     pass (nsa_qk_norm_rope).
 
@@ -715,6 +707,9 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positio
     are then allocated on it too). Returns (q_out, k_out).
     """
     lib = _lib or load()
+    if stream is not None:
+        return _on_stream(stream, qk_norm_rope, q, k, q_weight, k_weight, cos, sin, positions, eps,
+                          interleaved, q_out, k_out)
     if q_out is None:
         q_out = _dense_like(q)
     if k_out is None:
@@ -739,11 +734,10 @@ def norm_rope_bwd_workspace_bytes(B, M, D) -> int:
     return n
 
 
-@_on_stream
 def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, cos=None, sin=None,
                      positions=None, eps: float = 1e-6, interleaved: bool = False, dq=None,
                      dk=None, dq_weight=None, dk_weight=None, weight_grads: bool = True,
-                     workspace=None):
+                     workspace=None, *, stream=None):
     """Gradients of :func:`qk_norm_rope` (nsa_qk_norm_rope_bwd).
 
     q, k and the arguments after them are the forward's; ``dq_out``,
@@ -755,6 +749,10 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, cos=Non
     when omitted. ``stream``: as in the forward.
     """
     lib = _lib or load()
+    if stream is not None:
+        return _on_stream(stream, qk_norm_rope_bwd, q, k, dq_out, dk_out, q_weight, k_weight, cos,
+                          sin, positions, eps, interleaved, dq, dk, dq_weight, dk_weight,
+                          weight_grads, workspace)
     if dq is None:
         dq = _dense_like(q)
     if dk is None:
