@@ -618,10 +618,10 @@ int nsa_sync_status(void* stream);
 /*
  * nsa_selftest_wait_timeout -- test hook for the bounded waits.
  *
- * Launches one warp on `stream` that waits on a barrier nothing will ever
- * complete; after `limit_ns` (1e3 .. 2e9) it gives up and sets the status
- * word, so the next nsa_sync_status() returns NSA_ERR_TIMEOUT. Touches no
- * other memory. Returns NSA_ERR_SHAPE for a limit out of range.
+ * Launches four warps on `stream`, one of which waits on a barrier nothing will
+ * ever complete; after `limit_ns` (1e3 .. 2e9) it gives up, the others learn of
+ * it and one of them sets the status word, so the next nsa_sync_status()
+ * returns NSA_ERR_TIMEOUT. Touches no other memory. Returns NSA_ERR_SHAPE for a limit out of range.
  */
 int nsa_selftest_wait_timeout(int64_t limit_ns, void* stream);
 

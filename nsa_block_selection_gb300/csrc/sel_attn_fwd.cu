@@ -439,9 +439,11 @@ __global__ void __launch_bounds__(WARPS * 32, NSA_MIN_BLOCKS)
   }
 }
 
-// A one-warp kernel whose mbarrier never completes: exercises the bounded
-// wait and the status word without touching any other memory.
-__global__ void selftest_timeout_kernel(uint64_t limit_ns) {
+// Four warps, of which one waits for an mbarrier that never completes:
+// exercises the bounded wait, the vote by which its neighbours learn of it, and
+// the status word, without touching any other memory. Warp 3, which waited for
+// nothing, reports.
+__global__ void __launch_bounds__(128) selftest_timeout_kernel(uint64_t limit_ns) {
   __shared__ __align__(8) uint64_t bar;
   const uint32_t a = smem_u32(&bar);
   if (threadIdx.x == 0) {
@@ -449,8 +451,9 @@ __global__ void selftest_timeout_kernel(uint64_t limit_ns) {
     fence_mbar_init();
   }
   __syncwarp();
-  const bool ok = wait_phase(a, 0, limit_ns);
-  if (!__all_sync(kFull, ok) && threadIdx.x == 0) report_timeout();
+  bool ok = true;
+  if (threadIdx.x < 32) ok = __all_sync(kFull, wait_phase(a, 0, limit_ns));
+  if (!bar_vote(1, 128, ok) && threadIdx.x == 96) report_timeout();
 }
 
 // ---- host side ---------------------------------------------------------------
@@ -643,7 +646,7 @@ int nsa_sel_attn_fwd_shared(const void* Q, const void* K, const void* V,
 
 int nsa_selftest_wait_timeout(int64_t limit_ns, void* stream) {
   if (limit_ns < 1000 || limit_ns > 2000000000) return NSA_ERR_SHAPE;
-  nsa::selftest_timeout_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(
+  nsa::selftest_timeout_kernel<<<1, 128, 0, static_cast<cudaStream_t>(stream)>>>(
       static_cast<uint64_t>(limit_ns));
   return cudaGetLastError() == cudaSuccess ? NSA_OK : NSA_ERR_LAUNCH;
 }

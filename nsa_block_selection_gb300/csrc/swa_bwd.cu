@@ -57,7 +57,9 @@
 //
 // Every mbarrier wait is bounded (1 s); a role that gives up sets the status
 // word, waits for its own copies, and every role reaches the teardown, which
-// frees the tensor memory.
+// frees the tensor memory. The auxiliary warps, which time their waits each for
+// itself, vote at their named barriers: one that gave up goes on to the next
+// vote, after which all four leave.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -108,10 +110,6 @@ struct SwaBwdProblem {
   bool g32;  // gradients fp32 instead of the inputs' type
   bool wide;  // gradients (and parts) 32-byte aligned
 };
-
-__device__ __forceinline__ void bar_sync(int id, int threads) {
-  asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
-}
 
 // An auxiliary warp waits for a whole item of `steps` steps at a time, which
 // 1 s may not hold: 20 us more for each of them (they take under 1 us).
@@ -550,6 +548,7 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 1), 1)
     };
     uint32_t n = 0;
     DqItem last{};
+    bool ok = true;  // no wait of this warp has given up
     auto next = [&](uint32_t from) {  // the next round with an item that has keys
       for (; from < rounds; ++from)
         if (item_of(from) < items && dq_item<CUT>(p, item_of(from)).nt > 0) break;
@@ -566,10 +565,7 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 1), 1)
       if (it.nt > 0) {
         const float l = iq < p.M ? p.LSE[(static_cast<int64_t>(it.b) * p.H + it.h) * p.M + iq]
                                  : -INFINITY;
-        if (!wait_all(C::kOStaged, n & 1)) {
-          failed = true;
-          break;
-        }
+        ok = ok && wait_all(C::kOStaged, n & 1);
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
@@ -581,7 +577,10 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 1), 1)
             acc[e] = fmaf(hi16<BF16>(vv[e]), hi16<BF16>(oo[e]), acc[e]);
           }
         }
-        bar_sync(1, 128);  // every row of O has been read
+        if (!bar_vote(1, 128, ok)) {  // every row of O has been read
+          failed = true;
+          break;
+        }
         if (leader) {
           mbar_arrive_expect_tx(bar(C::kQStaged), kBlk * D * 2);
           load(&tmQ, C::kOffQ, C::kQStaged, it);
@@ -624,30 +623,26 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 1), 1)
         if (lane == 0) mbar_arrive(bar(ready));
         return true;
       };
-      if (!wait_all(C::kQStaged, n & 1) || !move(q_row, C::kColQ, C::kSDone, C::kQReady) ||
-          !move(do_row, C::kColDo, C::kDpDone, C::kDoReady + static_cast<int>(n & 1))) {
+      ok = wait_all(C::kQStaged, n & 1) && move(q_row, C::kColQ, C::kSDone, C::kQReady) &&
+           move(do_row, C::kColDo, C::kDpDone, C::kDoReady + static_cast<int>(n & 1));
+      if (!bar_vote(1, 128, ok)) {  // all four warps have read the staged rows
         failed = true;
         break;
       }
-      bar_sync(1, 128);  // all four warps have read the staged rows
       kn = next(k + 1);
       if (kn < rounds && leader) load_o(dq_item<CUT>(p, item_of(kn)));
       if (n > 0) {
-        if (!wait_all(C::kDqDone, (n - 1) & 1)) {
-          failed = true;
-          break;
-        }
-        out(last, false);
+        ok = wait_all(C::kDqDone, (n - 1) & 1);
+        if (ok) out(last, false);
       }
       last = it;
       ++n;
     }
     if (!failed && n > 0) {
-      if (wait_all(C::kDqDone, (n - 1) & 1))
-        out(last, false);
-      else
-        failed = true;
+      ok = ok && wait_all(C::kDqDone, (n - 1) & 1);
+      if (ok) out(last, false);
     }
+    failed = !ok || failed;
     if (failed && leader) {  // a load may still be in flight
       wait_phase(bar(C::kOStaged), 0, kWaitLimitNs);
       wait_phase(bar(C::kOStaged), 1, kWaitLimitNs);
@@ -1096,6 +1091,7 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 2), 1)
     };
     uint32_t n = 0;
     DkvItem last{};
+    bool ok = true;  // no wait of this warp has given up
     auto out_last = [&]() -> bool {
       if (!wait_all(C::kDvDone, (n - 1) & 1)) return false;
       out(last, true, false);
@@ -1138,22 +1134,21 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 2), 1)
         if (lane == 0) mbar_arrive(bar(ready));
         return true;
       };
-      if (!wait_all(C::kStaged, n & 1) || !move(C::kOffK, C::kColK, C::kSDone, C::kKReady) ||
-          !move(C::kOffV, C::kColV, C::kDpDone, C::kVReady)) {
+      ok = ok && wait_all(C::kStaged, n & 1) &&
+           move(C::kOffK, C::kColK, C::kSDone, C::kKReady) &&
+           move(C::kOffV, C::kColV, C::kDpDone, C::kVReady);
+      if (!bar_vote(1, 128, ok)) {  // all four warps have read the staged rows
         failed = true;
         break;
       }
-      bar_sync(1, 128);  // all four warps have read the staged rows
       kn = next(k + 1);
       if (kn < rounds && leader) load(dkv_item(p, item_of(kn)));
-      if (n > 0 && !out_last()) {
-        failed = true;
-        break;
-      }
+      ok = n == 0 || out_last();
       last = it;
       ++n;
     }
-    if (!failed && n > 0 && !out_last()) failed = true;
+    if (!failed && n > 0) ok = ok && out_last();
+    failed = !ok || failed;
     if (failed && leader) {  // a load may still be in flight
       wait_phase(bar(C::kStaged), 0, kWaitLimitNs);
       wait_phase(bar(C::kStaged), 1, kWaitLimitNs);
