@@ -111,8 +111,9 @@ struct SwaBwdProblem {
   bool wide;  // gradients (and parts) 32-byte aligned
 };
 
-// An auxiliary warp waits for a whole item of `steps` steps at a time, which
-// 1 s may not hold: 20 us more for each of them (they take under 1 us).
+// An auxiliary warp waits for a whole item of `steps` steps at a time, at its
+// last item from the item's start on, which 1 s may not hold: 20 us more for
+// each of them (they take under 1 us).
 __device__ __forceinline__ uint64_t item_limit_ns(int steps) {
   return kWaitLimitNs + 20000ull * static_cast<uint64_t>(steps);
 }
@@ -549,6 +550,12 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 1), 1)
     uint32_t n = 0;
     DqItem last{};
     bool ok = true;  // no wait of this warp has given up
+    auto wait_last = [&](int b) {  // for something of the last item
+      const bool r =
+          __all_sync(kFull, wait_phase(bar(b), (n - 1) & 1, item_limit_ns(last.nt)));
+      tc_fence_after();
+      return r;
+    };
     auto next = [&](uint32_t from) {  // the next round with an item that has keys
       for (; from < rounds; ++from)
         if (item_of(from) < items && dq_item<CUT>(p, item_of(from)).nt > 0) break;
@@ -609,11 +616,7 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 1), 1)
           const uint4 v = chunk(src, c);
           r[4 * c] = v.x, r[4 * c + 1] = v.y, r[4 * c + 2] = v.z, r[4 * c + 3] = v.w;
         }
-        if (n > 0) {
-          if (!__all_sync(kFull, wait_phase(bar(done), (n - 1) & 1, item_limit_ns(last.nt))))
-            return false;
-          tc_fence_after();
-        }
+        if (n > 0 && !wait_last(done)) return false;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
           tc_st32(lane_addr + col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&r[32 * c]));
@@ -632,14 +635,14 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 1), 1)
       kn = next(k + 1);
       if (kn < rounds && leader) load_o(dq_item<CUT>(p, item_of(kn)));
       if (n > 0) {
-        ok = wait_all(C::kDqDone, (n - 1) & 1);
+        ok = wait_last(C::kDqDone);
         if (ok) out(last, false);
       }
       last = it;
       ++n;
     }
     if (!failed && n > 0) {
-      ok = ok && wait_all(C::kDqDone, (n - 1) & 1);
+      ok = ok && wait_last(C::kDqDone);
       if (ok) out(last, false);
     }
     failed = !ok || failed;
@@ -1092,10 +1095,16 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 2), 1)
     uint32_t n = 0;
     DkvItem last{};
     bool ok = true;  // no wait of this warp has given up
+    auto wait_last = [&](int b) {  // for something of the last item
+      const bool r =
+          __all_sync(kFull, wait_phase(bar(b), (n - 1) & 1, item_limit_ns(last.nt)));
+      tc_fence_after();
+      return r;
+    };
     auto out_last = [&]() -> bool {
-      if (!wait_all(C::kDvDone, (n - 1) & 1)) return false;
+      if (!wait_last(C::kDvDone)) return false;
       out(last, true, false);
-      if (!wait_all(C::kDkDone, (n - 1) & 1)) return false;
+      if (!wait_last(C::kDkDone)) return false;
       out(last, false, false);
       return true;
     };
@@ -1120,11 +1129,7 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 2), 1)
                                                           (((c & 7) ^ (row & 7)) << 4));
           r[4 * c] = v.x, r[4 * c + 1] = v.y, r[4 * c + 2] = v.z, r[4 * c + 3] = v.w;
         }
-        if (n > 0) {
-          if (!__all_sync(kFull, wait_phase(bar(done), (n - 1) & 1, item_limit_ns(last.nt))))
-            return false;
-          tc_fence_after();
-        }
+        if (n > 0 && !wait_last(done)) return false;
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
           tc_st32(lane_addr + col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&r[32 * c]));
