@@ -488,9 +488,10 @@ int64_t nsa_swa_bwd_workspace_bytes(int64_t B, int64_t M, int64_t N, int64_t H, 
  * over the visible pairs (dK and dV over the query heads of the KV head too).
  * The products run on the 5th-generation tensor cores with fp32 sums in tensor
  * memory; p and dS are rounded to dtype before the products they enter. Every
- * sum has a fixed order: equal calls give equal bits. With fp16 inputs p and dS
- * are carried times 2^12 and 2^6, so small ones keep their precision; dS is
- * then finite while |dP - delta| < 1023.
+ * sum has a fixed order: equal calls give equal bits. With fp16 inputs p is
+ * carried times 2^12, and dS times a power of two that every row of dQ and of dK
+ * takes from the norms of the dO and V rows that its tiles hold, so that dS
+ * neither overflows nor loses bits, whatever the scale of dO.
  *
  * A query without keys (LSE = -inf) gets dQ = 0 and adds nothing to dK, dV; a
  * key that no query sees gets dK = dV = 0. p and dS of hidden pairs are exactly
@@ -501,8 +502,8 @@ int64_t nsa_swa_bwd_workspace_bytes(int64_t B, int64_t M, int64_t N, int64_t H, 
  * the forward, in 128-key tiles). M and N are at most 2^29. The outputs must
  * not overlap the inputs.
  *
- * Asynchronous: two kernels on `stream` (up to four where gradients are joined
- * from parts), no allocation; calls that may overlap need workspaces of their own.
+ * Asynchronous: two kernels on `stream` (three with fp16 inputs, and up to two
+ * more where gradients are joined from parts), no allocation; calls that may overlap need workspaces of their own.
  * Errors before launch as nsa_swa_fwd, plus NSA_ERR_WORKSPACE. With no query,
  * or no key, the gradients are zeroed and no workspace is needed. A timed-out
  * device wait is reported by nsa_sync_status.

@@ -25,6 +25,7 @@
 // reads for B: with A in shared memory the 64-column products would need 192
 // of the 128 there are (measured: 33 clocks a product against 49).
 //
+//  0. swa_bwd_vmax_kernel (fp16 alone): the largest |v| of every key tile.
 //  1. swa_bwd_dq_kernel: an item is 128 queries of a head (or, with few query
 //     tiles, a part of their keys), a step 64 keys. Q and dO are the A operands
 //     of S = Q K^T and dP = dO V^T; dS overwrites S and is the A operand of
@@ -82,24 +83,53 @@ constexpr int kAtomStep = kStep * 128;  // bytes of 64 rows x 64 entries
 constexpr int kAtomBlk = kBlk * 128;
 constexpr uint32_t kTmemAll = 512;
 
-// fp16 has no exponents below 2^-14 at full precision, and over thousands of
-// keys p is smaller than that: with fp16 inputs p is carried as 2^12 p (at
-// most 4096) and dS as 2^6 dS (finite while |dP - delta| < 1023), both
-// exact factors that the epilogues divide out. bf16 needs neither.
+// fp16 has no exponents below 2^-14 at full precision and none above 2^15. Over
+// thousands of keys p is smaller than the one: with fp16 inputs it is carried as
+// 2^12 p (at most 4096). dS, as large as dO and V make it, may pass either: it is
+// carried as 2^e dS, with an e of its own for every row of dQ and of dK (an
+// accumulator's row has one scale), the largest for which a bound of |dP - delta|
+// stays below 2^15 (p <= 1; a factor of 2 is left for roundings). By
+// Cauchy-Schwarz, |dP - delta| <= |dO_i| |v_j| + |delta_i|, with the largest |v|
+// of the key tiles of a row of dQ, and the largest |dO| and |delta| of the query
+// blocks of a row of dK. All are exact factors that the epilogues divide out.
+// bf16 needs none of it.
 template <bool BF16>
 struct Shift {
   static constexpr float kP = BF16 ? 0.f : 12.f;
-  static constexpr float kS = BF16 ? 0.f : 6.f;
   static constexpr float kPInv = BF16 ? 1.f : 1.f / 4096.f;
-  static constexpr float kSInv = BF16 ? 1.f : 1.f / 64.f;   // also 2^(kS - kP)
 };
+constexpr int kTopExp = 40;  // of e, where the bound is small or 0
+
+// e for a bound. (One that is not finite comes of a dO, O or V that is not,
+// which the products carry into the gradients whatever e is.)
+__device__ __forceinline__ int shift_for(float bound) {
+  if (!(bound < INFINITY)) return 0;
+  return min(kTopExp, 14 - (static_cast<int>(__float_as_uint(bound) >> 23) - 127));
+}
+__device__ __forceinline__ float pow2(int e) {  // |e| < 127
+  return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+}
+// The bit of the largest |dO| that row i of 32 keeps: four rows that a lane reads
+// together hold one of each byte.
+__device__ __forceinline__ int top_bit(int i) { return (i & 3) * 8 + (i >> 2); }
+// Non-negative numbers order as their bits; one that is not finite counts as 0
+// (a row that hidden pairs alone use may hold anything).
+__device__ __forceinline__ uint32_t finite_bits(float x) {
+  return x < INFINITY ? __float_as_uint(x) : 0u;
+}
 
 struct SwaBwdProblem {
   const uint16_t *Q, *K, *V, *O, *dO;
   const float* LSE;
   void *dQ, *dK, *dV;
   float* nlse2;   // [B, H, Mp]: Shift::kP - LSE log2 e; -inf for rows without keys
-  float* ndelta;  // [B, H, Mp]: -delta 2^(kS - kP)
+  // [B, H, Mp]: -delta. fp16: the last bits of 32 rows' (which delta, good to some
+  // 2^-20, can spare) are the largest |dO| of those rows, a float: top_bit().
+  float* ndelta;
+  // fp16: the largest |v| of every key tile, until dV is written, in the first
+  // 4 bytes of the tile's first row of dV
+  const float* vmax;
+  int64_t vmax_b, vmax_t, vmax_g;  // its strides over (batch, key tile, KV head)
   float* part;    // [parts, 2 (dK, dV), kBlk, D], or NULL
   float* part_q;  // [parts, kBlk, D] of dQ, or NULL
   int B, M, N, H, Hkv, hpg, Mp, qtiles, ktiles, splits;
@@ -245,6 +275,57 @@ __device__ __forceinline__ void store_row32(void* base, int64_t row_off, int col
   }
 }
 
+// ---------------------------------------------------------------- fp16: |v|
+
+// The largest |v| of every key tile of a KV head, which the dQ kernel bounds dS
+// by: a CTA a tile, 16 rows a warp. One pass over V; left in dV's rows, which
+// are not written before the dK, dV kernel, so that the call needs no more
+// workspace than it does with bf16. What the powers of two cost, this launch
+// and the products by them in the dK, dV kernel, replayed from a graph: 2 x 1000
+// tokens of 8 + 2 heads 29 -> 33 us, 8192 of 64 + 8 (window 512) 404 -> 420,
+// D = 64, 2 x 16 heads of 1500 x 2048, 114 -> 121. With a fixed 2^6, |dP - delta|
+// of 1023 overflowed, which a dO of standard deviation 200 reaches.
+template <int D>
+__global__ void __launch_bounds__(256) swa_bwd_vmax_kernel(const SwaBwdProblem p, float* vmax) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // of a row; rows of a warp at a time
+  __shared__ uint32_t sh[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int kt = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.ktiles));
+  const int bg = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.ktiles));
+  const int b = bg / p.Hkv, g = bg - b * p.Hkv;
+  uint4 v[16 / kRows];
+#pragma unroll
+  for (int r = 0; r < 16 / kRows; ++r) {
+    const int j = kt * kBlk + warp * 16 + r * kRows + lane / kLanes;
+    v[r] = make_uint4(0, 0, 0, 0);
+    if (j < p.N)
+      v[r] = reinterpret_cast<const uint4*>(
+          p.V + ((static_cast<int64_t>(b) * p.N + j) * p.Hkv + g) * D)[lane % kLanes];
+  }
+  uint32_t top = 0u;
+#pragma unroll
+  for (int r = 0; r < 16 / kRows; ++r) {
+    const uint32_t vv[4] = {v[r].x, v[r].y, v[r].z, v[r].w};
+    float sq = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      sq = fmaf(lo16<false>(vv[e]), lo16<false>(vv[e]), sq);
+      sq = fmaf(hi16<false>(vv[e]), hi16<false>(vv[e]), sq);
+    }
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(kFull, sq, o);
+    top = max(top, finite_bits(sq));
+  }
+  top = __reduce_max_sync(kFull, top);
+  if (lane == 0) sh[warp] = top;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int w = 1; w < 8; ++w) top = max(top, sh[w]);
+    vmax[b * p.vmax_b + kt * p.vmax_t + g * p.vmax_g] = sqrtf(__uint_as_float(top));
+  }
+}
+
 // ---------------------------------------------------------------- dQ
 
 template <int D>
@@ -254,8 +335,10 @@ struct DqCfg {
   static constexpr int kStages = D == 128 ? 4 : 6;
   static constexpr int kOffQ = kStages * 2 * kTile;      // the next item's O, then its Q; dO
   static constexpr int kOffDo = kOffQ + kBlk * D * 2;
-  static constexpr int kOffStat = kOffDo + kBlk * D * 2;  // 2 x (LSE in base 2, delta) of the rows
-  static constexpr int kOffBar = kOffStat + 4 * kBlk * 4;
+  // 2 x (LSE in base 2 less the shift of dS, delta) of the rows; fp16: and the
+  // factor of dQ
+  static constexpr int kOffStat = kOffDo + kBlk * D * 2, kOffOut = kOffStat + 4 * kBlk * 4;
+  static constexpr int kOffBar = kOffOut + 2 * kBlk * 4;
   static constexpr int kFull = 0, kEmpty = kStages, kOStaged = 2 * kStages, kQStaged = kOStaged + 1,
                        kQReady = kQStaged + 1, kDoReady = kQReady + 1, kSDone = kDoReady + 2,
                        kDpDone = kSDone + 1, kSFull = kDpDone + 1, kDsFull = kSFull + 2,
@@ -509,8 +592,9 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 1), 1)
       load(&tmO, C::kOffQ, C::kOStaged, it);
       load(&tmDo, C::kOffDo, C::kOStaged, it);
     };
-    const float f_out = p.scale * Shift<BF16>::kSInv;
-    auto out = [&](const DqItem& it, bool zero) {  // dQ rows of an item
+    float* const factor = reinterpret_cast<float*>(gbase + C::kOffOut) + row;
+    uint32_t n = 0;
+    auto out = [&](const DqItem& it, bool zero) {  // dQ rows of an item, the last one if not zero
       const int iq = it.q0 + row;
       const bool part = CUT && it.part >= 0, f32 = p.g32 || part;
       void* const dst = part ? p.part_q : p.dQ;
@@ -530,6 +614,7 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 1), 1)
           if (lane == 0) mbar_arrive(bar(C::kDqFree));
         }
       };
+      const float f_out = BF16 || zero ? p.scale : factor[((n - 1) & 1) * kBlk];
       uint32_t r[32];
       if (f32) {
 #pragma unroll
@@ -547,7 +632,6 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 1), 1)
         if (iq < p.M) store_words(static_cast<uint16_t*>(dst) + off, w, D / 2, p.wide);
       }
     };
-    uint32_t n = 0;
     DqItem last{};
     bool ok = true;  // no wait of this warp has given up
     auto wait_last = [&](int b) {  // for something of the last item
@@ -569,7 +653,15 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 1), 1)
       const DqItem it = dq_item<CUT>(p, x);
       const int iq = it.q0 + row;
       float l2 = INFINITY, dl = 0.f;
+      uint32_t top = 0u;  // fp16: the largest |dO| of the warp's rows
       if (it.nt > 0) {
+        // fp16: the largest |v| of the item's key tiles, read before what follows
+        // and used after it
+        const float* const vsrc = p.vmax + it.b * p.vmax_b + it.g * p.vmax_g;
+        const int vlast = (it.t0 + it.nt - 1) / 2;
+        int vt = it.t0 / 2 + lane;
+        float vm = 0.f;
+        if (!BF16 && vt <= vlast) vm = vsrc[vt * p.vmax_t];
         const float l = iq < p.M ? p.LSE[(static_cast<int64_t>(it.b) * p.H + it.h) * p.M + iq]
                                  : -INFINITY;
         ok = ok && wait_all(C::kOStaged, n & 1);
@@ -596,13 +688,35 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 1), 1)
           l2 = l * 1.4426950408889634f;
           dl = (acc[0] + acc[1]) + (acc[2] + acc[3]);
         }
-        stat[(n & 1) * 2 * kBlk + row] = l2;
+        float e = 0.f;
+        if constexpr (!BF16) {  // (while Q arrives)
+          float sq[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 v = chunk(do_row, c);
+            const uint32_t vv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              sq[i] = fmaf(lo16<BF16>(vv[i]), lo16<BF16>(vv[i]), sq[i]);
+              sq[i] = fmaf(hi16<BF16>(vv[i]), hi16<BF16>(vv[i]), sq[i]);
+            }
+          }
+          while ((vt += 32) <= vlast) vm = fmaxf(vm, vsrc[vt * p.vmax_t]);
+          vm = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(vm)));
+          const float norm = sqrtf((sq[0] + sq[1]) + (sq[2] + sq[3]));
+          const int shift = shift_for(fmaf(norm, vm, fabsf(dl)));
+          e = static_cast<float>(shift);
+          factor[(n & 1) * kBlk] = p.scale * pow2(-shift);
+          top = __reduce_max_sync(kFull, l2 != INFINITY ? finite_bits(norm) : 0u);
+        }
+        stat[(n & 1) * 2 * kBlk + row] = l2 - e;
         stat[(n & 1) * 2 * kBlk + kBlk + row] = dl;
       }
       if ((!CUT || it.stat) && iq < p.Mp) {  // (a tile without keys: no pair reads them)
         const int64_t at = (static_cast<int64_t>(it.b) * p.H + it.h) * p.Mp + iq;
         p.nlse2[at] = Shift<BF16>::kP - l2;
-        p.ndelta[at] = -dl * Shift<BF16>::kSInv;
+        p.ndelta[at] =
+            BF16 ? -dl : __uint_as_float((__float_as_uint(-dl) & ~1u) | ((top >> top_bit(lane)) & 1u));
       }
       if (it.nt == 0) {
         out(it, true);
@@ -667,7 +781,7 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 1), 1)
         failed = true;
         break;
       }
-      const float neg = Shift<BF16>::kS - stat[(n & 1) * 2 * kBlk + row];
+      const float neg = -stat[(n & 1) * 2 * kBlk + row];
       const float dl = stat[(n & 1) * 2 * kBlk + kBlk + row];
       const uint64_t neg_2 = pair(neg, neg), ndl_2 = pair(-dl, -dl);
       const int iq = it.q0 + row;
@@ -736,12 +850,16 @@ struct DkvCfg {
   static constexpr int kCols = kStep / kGroups;
   static constexpr int kOffK = kStages * kStagePitch;  // the next item's K and V
   static constexpr int kOffV = kOffK + kBlk * D * 2;
-  static constexpr int kOffBar = kOffV + kBlk * D * 2;
+  // fp16: 2 x 2^(e - 12) of the rows (P carries 2^12 already), the warps' largest
+  // |dO| and |delta|
+  static constexpr int kOffShift = kOffV + kBlk * D * 2, kOffTop = kOffShift + 2 * kBlk * 4;
+  static constexpr int kOffBar = kOffTop + 2 * 4 * 4;
   static constexpr int kFull = 0, kEmpty = kStages, kStaged = 2 * kStages, kKReady = kStaged + 1,
                        kVReady = kKReady + 1, kSDone = kVReady + 1, kDpDone = kSDone + 1,
                        kDvDone = kDpDone + 1, kDkDone = kDvDone + 1, kDvFree = kDkDone + 1,
                        kDkFree = kDvFree + 1, kSFull = kDkFree + 1, kPFull = kSFull + 4,
-                       kDpFull = kPFull + 4, kDsFull = kDpFull + 4, kNumBars = kDsFull + 4;
+                       kDpFull = kPFull + 4, kDsFull = kDpFull + 4, kShift = kDsFull + 4,
+                       kNumBars = kShift + 2;
   static constexpr int kOffTmem = kOffBar + kNumBars * 8;
   static constexpr int kSmem = kOffTmem + 16 + 1024;
   static_assert(kSmem <= 232448 && kSmem > 118784, "one CTA per SM");
@@ -827,6 +945,9 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 2), 1)
       mbar_init(bar(C::kDpFull + s), 1);
       mbar_init(bar(C::kDsFull + s), 8 / C::kGroups);
     }
+    // two, for even and odd items, as in the dQ kernel
+    mbar_init(bar(C::kShift), 4);
+    mbar_init(bar(C::kShift + 1), 4);
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -1059,10 +1180,11 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 2), 1)
                       it.g, it.j0 + r * kStep, it.b, once);
         }
     };
+    float f_out = p.scale, f_next = p.scale;  // of the last item's dK, of the next one's
     // one accumulator's rows out; is_v: dV
     auto out = [&](const DkvItem& it, bool is_v, bool zero) {
       const int j = it.j0 + row;
-      const float f = is_v ? Shift<BF16>::kPInv : p.scale * Shift<BF16>::kSInv;
+      const float f = is_v ? Shift<BF16>::kPInv : f_out;
       void* dst = is_v ? p.dV : p.dK;
       int64_t off = ((static_cast<int64_t>(it.b) * p.N + j) * p.Hkv + it.g) * D;
       bool f32 = p.g32;
@@ -1139,8 +1261,71 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 2), 1)
         if (lane == 0) mbar_arrive(bar(ready));
         return true;
       };
-      ok = ok && wait_all(C::kStaged, n & 1) &&
-           move(C::kOffK, C::kColK, C::kSDone, C::kKReady) &&
+      ok = ok && wait_all(C::kStaged, n & 1);
+      if constexpr (!BF16) {
+        // the largest |dO| and |delta| of the item's steps, a step to 16 lanes, the
+        // warps' loads four at a time
+        uint32_t* const tops = reinterpret_cast<uint32_t*>(gbase + C::kOffTop);
+        const int w = warp - kAuxWarp;
+        uint32_t top = 0u, delta = 0u;
+        for (int i = w; 2 * i < it.nt; i += 16) {
+          uint4 x[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int step = 2 * (i + 4 * j) + (lane >> 4);
+            const uint32_t at = static_cast<uint32_t>(it.u + step), nq = it.nq;
+            x[j] = make_uint4(0, 0, 0, 0);
+            if (step < it.nt)
+              x[j] = *reinterpret_cast<const uint4*>(
+                  p.ndelta + (static_cast<int64_t>(it.b) * p.H + it.h + at / nq) * p.Mp +
+                  static_cast<int64_t>(it.u0 + at % nq) * kStep + 4 * (lane & 15));
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t xx[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+            uint32_t word = 0u;  // of the 8 lanes that hold the same 32 rows
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t bits = __ballot_sync(kFull, (xx[c] & 1u) != 0u);
+              word |= ((bits >> (lane & 24)) & 0xffu) << (8 * c);
+              delta = max(delta, finite_bits(fabsf(__uint_as_float(xx[c]))));
+            }
+            top = max(top, word);
+          }
+        }
+        top = __reduce_max_sync(kFull, top);
+        delta = __reduce_max_sync(kFull, delta);
+        if (lane == 0) {
+          tops[w] = top;
+          tops[4 + w] = delta;
+        }
+        if (!bar_vote(1, 128, ok)) {
+          failed = true;
+          break;
+        }
+        float sq[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint8_t* const v_row = gbase + C::kOffV + row * 128;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = *reinterpret_cast<const uint4*>(v_row + (c >> 3) * kAtomBlk +
+                                                          (((c & 7) ^ (row & 7)) << 4));
+          const uint32_t vv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            sq[e] = fmaf(lo16<BF16>(vv[e]), lo16<BF16>(vv[e]), sq[e]);
+            sq[e] = fmaf(hi16<BF16>(vv[e]), hi16<BF16>(vv[e]), sq[e]);
+          }
+        }
+        const uint32_t t = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+        const uint32_t d = max(max(tops[4], tops[5]), max(tops[6], tops[7]));
+        const float norm = sqrtf((sq[0] + sq[1]) + (sq[2] + sq[3]));
+        const int e = shift_for(fmaf(norm, __uint_as_float(t), __uint_as_float(d)));
+        f_next = p.scale * pow2(-e);
+        reinterpret_cast<float*>(gbase + C::kOffShift)[(n & 1) * kBlk + row] = pow2(e - 12);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::kShift + static_cast<int>(n & 1)));
+      }
+      ok = ok && move(C::kOffK, C::kColK, C::kSDone, C::kKReady) &&
            move(C::kOffV, C::kColV, C::kDpDone, C::kVReady);
       if (!bar_vote(1, 128, ok)) {  // all four warps have read the staged rows
         failed = true;
@@ -1150,6 +1335,7 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 2), 1)
       if (kn < rounds && leader) load(dkv_item(p, item_of(kn)));
       ok = n == 0 || out_last();
       last = it;
+      f_out = f_next;
       ++n;
     }
     if (!failed && n > 0) ok = ok && out_last();
@@ -1164,13 +1350,22 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 2), 1)
     const int gb = C::kGroups == 2 ? 2 * wg : 0;  // its group's barriers
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint64_t sl2_2 = pair(p.sl2, p.sl2);
-    const uint64_t shift_2 = pair(Shift<BF16>::kSInv, Shift<BF16>::kSInv);
-    uint32_t n = 0, ph = 0;
+    uint32_t n = 0, ph = 0, na = 0;  // steps, phase of their stages, items
     int st = 0;
     for (uint32_t k = next(0); k < rounds && !failed; k = next(k + 1)) {
       const DkvItem it = dkv_item(p, item_of(k));
       const int j = it.j0 + row;
       const int lo_j = j - p.right, hi_j = min(j + p.left, p.M - 1);  // the queries that see key j
+      uint64_t shift_2 = 0;
+      if constexpr (!BF16) {
+        if (!wait_all(C::kShift + static_cast<int>(na & 1), (na >> 1) & 1)) {
+          failed = true;
+          break;
+        }
+        const float f = reinterpret_cast<const float*>(gbase + C::kOffShift)[(na & 1) * kBlk + row];
+        shift_2 = pair(f, f);
+        ++na;
+      }
       int u = it.u;
       for (int t = 0; t < it.nt; ++t, ++n) {
         const int i0 = (it.u0 + u) * kStep, ic = i0 + 32 * wg;
@@ -1242,8 +1437,12 @@ __global__ void __launch_bounds__(32 * (kMmaWarp + 2), 1)
         for (int c = 0; c < 8; ++c) {
           const ulonglong2 d = ndl[c];  // -delta of 4 queries
           const uint64_t x = pair(s[4 * c], s[4 * c + 1]), y = pair(s[4 * c + 2], s[4 * c + 3]);
-          pr[2 * c] = mul2(pr[2 * c], BF16 ? add2(x, d.x) : fma2(x, shift_2, d.x));
-          pr[2 * c + 1] = mul2(pr[2 * c + 1], BF16 ? add2(y, d.y) : fma2(y, shift_2, d.y));
+          if constexpr (!BF16) {
+            pr[2 * c] = mul2(pr[2 * c], shift_2);
+            pr[2 * c + 1] = mul2(pr[2 * c + 1], shift_2);
+          }
+          pr[2 * c] = mul2(pr[2 * c], add2(x, d.x));
+          pr[2 * c + 1] = mul2(pr[2 * c + 1], add2(y, d.y));
         }
         store(da, pr);
         arrive(C::kDsFull);
@@ -1414,6 +1613,11 @@ int launch_swa_bwd(const SwaBwdProblem& p, cudaStream_t st) {
       cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, DkvCfg<D>::kSmem) !=
           cudaSuccess)
     return NSA_ERR_LAUNCH;
+  if constexpr (!BF16) {
+    swa_bwd_vmax_kernel<D><<<static_cast<unsigned>(p.B * p.Hkv * p.ktiles), 256, 0, st>>>(
+        p, static_cast<float*>(p.dV));
+    if (cudaGetLastError() != cudaSuccess) return NSA_ERR_LAUNCH;
+  }
   const int64_t qi = p.dq_items, ki = p.dkv_items;
   // one CTA per SM, items dealt to them
   dq<<<static_cast<unsigned>(qi < kSms ? qi : kSms), 32 * (kMmaWarp + 1), DqCfg<D>::kSmem, st>>>(p, tk, tv,
@@ -1525,6 +1729,10 @@ extern "C" int nsa_swa_bwd(const void* Q, const void* K, const void* V, const vo
   p.sl2 = p.scale * 1.4426950408889634f;
   p.g32 = grad_dtype == NSA_F32;
   p.wide = !mis(dQ, 32) && !mis(dK, 32) && !mis(dV, 32) && !mis(workspace, 32);
+  p.vmax = static_cast<const float*>(dV);
+  p.vmax_g = D * ge / 4;
+  p.vmax_t = kBlk * H_kv * p.vmax_g;
+  p.vmax_b = N * H_kv * p.vmax_g;
   const int64_t stat = B * H * p.Mp;
   p.nlse2 = static_cast<float*>(workspace);
   p.ndelta = p.nlse2 + stat;
