@@ -547,8 +547,12 @@ enum SwaPairBar : int {
   kPOFull = 14,    // 2: the item's last PV of the head has completed
   kPOEmpty = 16,   // 2: the head's softmax warps have read its O
   kPOStaged = 18,  // 2 (TMA_O): the head's softmax warps have staged its O tile
-  kPOSmemFree = 20,  // (TMA_O) the last O tile store has read the staging buffer
-  kPNumBars = 21
+  // 2 (TMA_O): the store of the head's O tile has read the staging buffer. One for
+  // each head: with one for both, a head with items without keys, which take
+  // no time, could ask for the store before its own last one was done, two phases
+  // behind, and was let through.
+  kPOSmemFree = 20,
+  kPNumBars = 22
 };
 
 constexpr int kSwaPairThreads = 384;
@@ -616,8 +620,8 @@ __global__ void __launch_bounds__(kSwaPairThreads, 1)
       mbar_init(bar(kPOFull + s), 1);
       mbar_init(bar(kPOEmpty + s), 4 * 32);
       mbar_init(bar(kPOStaged + s), 4 * 32);
+      mbar_init(bar(kPOSmemFree + s), 1);
     }
-    mbar_init(bar(kPOSmemFree), 1);
     fence_mbar_init();
   }
   if (warp == 9) {
@@ -794,7 +798,7 @@ __global__ void __launch_bounds__(kSwaPairThreads, 1)
             tma_store_4d(&tmO, base + C::kOffO + a * C::kAtomBytes, a * 64, it.h + hx, it.q0, it.b);
           bulk_commit_group();
           bulk_wait_group_read0();
-          mbar_arrive(bar(kPOSmemFree));
+          mbar_arrive(bar(kPOSmemFree + hx));
         }
         ++ne;
       }
@@ -953,10 +957,12 @@ __global__ void __launch_bounds__(kSwaPairThreads, 1)
       const float inv = l > 0.f ? 1.f / l : 0.f;
       if constexpr (TMA_O) {
         // stage the O row (128B-swizzled, one 64-column atom after the
-        // other) once the previous tile store, of either head, has read the
-        // buffer: the tiles go A, B of every item
-        const int e = 2 * ne + hx;
-        if (e >= 1 && !wait_all(kPOSmemFree, static_cast<uint32_t>((e - 1) & 1))) {
+        // other) once the previous tile's store has read the buffer: the tiles
+        // go A, B of every item, so that is the other head's, of the item
+        // before for A and of this one for B
+        const int before = ne - 1 + hx;
+        if (before >= 0 &&
+            !wait_all(kPOSmemFree + 1 - hx, static_cast<uint32_t>(before & 1))) {
           failed = true;
           break;
         }
