@@ -124,7 +124,6 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.nsa_qk_norm_rope_bwd.argtypes = [vp] * 13 + [i64] * 8 + [f32, c_int, c_int, c_int, c_int,
                                                                  vp, vp, i64, vp]
     if path is None:
-        _bind_torch()
         _lib = lib
     return lib
 
@@ -480,19 +479,24 @@ def swa_fwd(q, k, v, window=(-1, -1), scale: Optional[float] = None, out=None, l
 
 # The calls below may be a single token's work, beside which every property
 # read and every import statement counts: torch is looked up once, each
-# property is read once, and names are given only where a check failed.
+# property is read once, and names are given only where a check failed. _bound
+# is the library once torch is there too (load() itself needs no torch).
+_bound = None
 _torch = None
 _F16_KINDS = ()
 _DTYPE_CODES = {}
 
 
-def _bind_torch():
-    global _torch, _F16_KINDS
+def _bind():
+    global _bound, _torch, _F16_KINDS
     import torch
 
+    lib = load()
     _torch = torch
     _F16_KINDS = (torch.float16, torch.bfloat16)
     _DTYPE_CODES.update({torch.float16: NSA_F16, torch.bfloat16: NSA_BF16, torch.float32: NSA_F32})
+    _bound = lib
+    return lib
 
 
 def _launch(dev, fn, *args):
@@ -534,7 +538,7 @@ def swa_bwd(q, k, v, o, lse, do, window=(-1, -1), scale: Optional[float] = None,
     stream, or on ``stream`` (a keyword; what it allocates is then allocated
     on it too).
     """
-    lib = _lib or load()
+    lib = _bound or _bind()
     if stream is not None:
         return _on_stream(stream, swa_bwd, q, k, v, o, lse, do, window, scale, dq, dk, dv,
                           grad_dtype, workspace)
@@ -706,7 +710,7 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positio
     Runs on torch's current stream, or on ``stream`` (a keyword; the outputs
     are then allocated on it too). Returns (q_out, k_out).
     """
-    lib = _lib or load()
+    lib = _bound or _bind()
     if stream is not None:
         return _on_stream(stream, qk_norm_rope, q, k, q_weight, k_weight, cos, sin, positions, eps,
                           interleaved, q_out, k_out)
@@ -748,7 +752,7 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, cos=Non
     ``workspace`` (CUDA uint8, norm_rope_bwd_workspace_bytes) is allocated
     when omitted. ``stream``: as in the forward.
     """
-    lib = _lib or load()
+    lib = _bound or _bind()
     if stream is not None:
         return _on_stream(stream, qk_norm_rope_bwd, q, k, dq_out, dk_out, q_weight, k_weight, cos,
                           sin, positions, eps, interleaved, dq, dk, dq_weight, dk_weight,
