@@ -580,8 +580,8 @@ def swa_bwd(q, k, v, o, lse, do, window=(-1, -1), scale: Optional[float] = None,
         workspace = _torch.empty(nbytes, dtype=_torch.uint8, device=q.device)
     else:
         nbytes = workspace.numel() * workspace.element_size()
-        if workspace.get_device() != dev:
-            raise ValueError("workspace must be on q's CUDA device")
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on q's CUDA device")
     # scale: the ABI takes <= 0 for 1/sqrt(D)
     st = _launch(dev, lib.nsa_swa_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                  o.data_ptr(), lse.data_ptr(), do.data_ptr(), dq.data_ptr(), dk.data_ptr(),
@@ -783,8 +783,8 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, cos=Non
             workspace = _torch.empty(nbytes, dtype=_torch.uint8, device=q.device)
         else:
             nbytes = workspace.numel() * workspace.element_size()
-            if workspace.get_device() != dev:
-                raise ValueError("workspace must be on q's CUDA device")
+            if workspace.get_device() != dev or not workspace.is_contiguous():
+                raise ValueError("workspace must be a contiguous tensor on q's CUDA device")
     else:
         dq_weight = dk_weight = workspace = None
     st = _launch(dev, lib.nsa_qk_norm_rope_bwd, q.data_ptr(), k.data_ptr(),
