@@ -400,13 +400,6 @@ __device__ __forceinline__ void load4(const float* p, float* f) {
   f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
 }
 
-template <int LPR>
-__device__ __forceinline__ float wide_row_sum(float v) {
-#pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-  return v;
-}
-
 // The token and head of a row slot in group q.
 template <int RPW>
 __device__ __forceinline__ void group_row(const RowGroups& g, uint32_t q, int sub, uint32_t& tok,
@@ -484,8 +477,8 @@ struct BwdRow {
       sq = fmaf(f[i], f[i], sq);
       gx = fmaf(y[i] * w[i], f[i], gx);
     }
-    sq = wide_row_sum<D / 8>(sq);
-    gx = wide_row_sum<D / 8>(gx);
+    sq = row_sum<D / 8>(sq);
+    gx = row_sum<D / 8>(gx);
     // slots without a row hold zeros (with eps = 0 their rs is infinite)
     if (in) {
       const float rs = rsqrtf(sq * (1.f / D) + p.eps);
@@ -565,9 +558,10 @@ __device__ __forceinline__ void cta_dw(float* dw, int c0, int c1, float (*sh)[D]
 // A warp's walk over the rows of one tensor, a token's heads at a time.
 template <int D, bool BF16, bool G32, int UN>
 __device__ __forceinline__ void bwd_tokens(const RopeProblem& p, const RopeBwdRows& t, int64_t first,
-                                           int64_t stride, int sub, int c0, int c1, bool rot,
-                                           const float* w, float* dw) {
+                                           int sub, int c0, int c1, bool rot, const float* w,
+                                           float* dw) {
   constexpr int RPW = 32 / (D / 8);
+  // (the step formed here: kept in registers across the loop it cost 1 %)
   for (int64_t u = first; u < t.units;
        u += static_cast<int64_t>(t.ctas) * (kRopeBwdThreads / 32)) {
     const uint32_t tok = static_cast<uint32_t>(u) / static_cast<uint32_t>(t.segs);
@@ -607,8 +601,10 @@ __device__ __forceinline__ void bwd_tokens(const RopeProblem& p, const RopeBwdRo
 
 // The same where a token has no more heads than a warp has row slots, UN
 // neighbouring groups of slots at a time (32,768 tokens of 1 + 1 heads at
-// D = 64: 50 us a token at a time, 21 here). With an fp32 gradient one: two
-// spill.
+// D = 64: 50 us a token at a time, 21 here), with an fp32 gradient one. At 80
+// registers all of the backward's forms spill a little: this one 48 to 64 bytes a
+// thread with 16-bit gradients, 8 to 16 with fp32 ones, of which two groups at
+// a time would spill 124 to 144.
 template <int D, bool BF16, bool G32, int UN>
 __device__ __forceinline__ void bwd_groups(const RopeProblem& p, const RopeBwdRows& t, int64_t first,
                                            int64_t stride, int sub, int c0, int c1, bool rot,
@@ -668,11 +664,11 @@ __global__ void __launch_bounds__(kRopeBwdThreads, kRopeBwdPerSm)
   for (int i = 0; i < 8; ++i) dw[i] = 0.f;
   load_weights8<BF16>(p, t.w, c0, c1, w);
   const int64_t first = static_cast<int64_t>(cta) * kWarps + (threadIdx.x >> 5);
-  const int64_t stride = static_cast<int64_t>(t.ctas) * kWarps;
   if (FEW && t.few)
-    bwd_groups<D, BF16, G32, G32 ? 1 : 2>(p, t, first, stride, sub, c0, c1, rot, w, dw);
+    bwd_groups<D, BF16, G32, G32 ? 1 : 2>(p, t, first, static_cast<int64_t>(t.ctas) * kWarps, sub, c0,
+                                          c1, rot, w, dw);
   else
-    bwd_tokens<D, BF16, G32, 2>(p, t, first, stride, sub, c0, c1, rot, w, dw);
+    bwd_tokens<D, BF16, G32, 2>(p, t, first, sub, c0, c1, rot, w, dw);
   if (pr.part != nullptr) cta_dw<D>(dw, c0, c1, sh, pr.part);
 }
 
@@ -830,9 +826,10 @@ int launch_norm_rope(const RopeProblem& p, cudaStream_t st) {
   int64_t per = (rows + segs - 1) / segs;
   per = (per + RPW - 1) / RPW * RPW;
   segs = (rows + per - 1) / per;
+  // (under 2^32, as the kernel takes them: there are fewer than 2^31 tokens, and
+  // with more than one segment each no more than some 2 x 16 x 152 units)
   const int64_t units = tokens * segs;
   const int64_t blocks = (units + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
-  if (units >= (int64_t(1) << 32)) return NSA_ERR_SHAPE;
   norm_rope_kernel<D, BF16, UN><<<static_cast<unsigned>(blocks), kRopeThreads, 0, st>>>(
       p, static_cast<int>(segs), static_cast<int>(per), units);
   return cudaGetLastError() == cudaSuccess ? NSA_OK : NSA_ERR_LAUNCH;
