@@ -439,7 +439,9 @@ def swa_fwd(q, k, v, window=(-1, -1), scale: Optional[float] = None, out=None, l
     q: bf16 or fp16 [B, M, H, D]; k, v: [B, N, H_kv, D] of q's dtype, all
     contiguous on one CUDA device. ``window`` = (left, right): query i sees
     keys [i - left, i + right]; a negative side is unbounded. Returns
-    (O [B, M, H, D] in q's dtype, LSE fp32 [B, H, M] or None).
+    (O [B, M, H, D] in q's dtype, LSE fp32 [B, H, M] or None). ``stream`` is
+    where the kernel runs (default: torch's current stream); outputs that the
+    call allocates come from the current stream's memory all the same.
     """
     import torch
 

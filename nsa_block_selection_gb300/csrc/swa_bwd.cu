@@ -46,15 +46,18 @@
 //
 // What bounds it. D = 128: the tensor pipe, busy 68 % (dQ) and 69 % (dK, dV) of
 // the clocks at 8192 tokens of 64 + 8 heads, window (512, 0), where the items
-// have 10 to 64 steps: 166 and 226 us, 6 us of joining, DRAM at 3.1 and 1.6 TB/s;
-// a step's products take 512 (dQ: 384) clocks and its
-// barriers, of which one that is over still takes a warp 100 to 300 clocks,
-// are most of the rest. 16,384 tokens, window (4096, 0): 1.52 and 2.15 ms,
-// 1.8 PFLOP/s over the 7 products; back to back the clock falls to 1.6 to
-// 1.9 GHz at the power limit. D = 64: the elementwise warps (2 x 16 heads of
-// 1500 x 2048: 47 and 69 us), as the products are half as long and the
-// exponentials are not. Short calls: their launches and the latency of a
-// few dependent steps (2 x 1000 tokens, 8 + 2 heads: 12, 19 and 6 us).
+// have 10 (dQ) and 80 steps (40 where cut): 165 and 225 us, 6 us of joining,
+// DRAM at 3.1 and 1.6 TB/s; a step's products take 1024 (dQ: 768) of its some
+// 1530 (1160) clocks, and its barriers, of which one that is over still takes a
+// warp 100 to 300 clocks, are most of the rest. 16,384 tokens, window (4096, 0):
+// 1.51 and 2.13 ms, 1.8 PFLOP/s over the 7 products; back to back the clock
+// falls to 1.6 to 1.9 GHz at the power limit. D = 64 (2 x 16 heads of
+// 1500 x 2048: 48 and 70 us): neither the products (396 and 528 of a step's some
+// 1000 and 1450 clocks) nor the exponentials (256); what is left is the chain of
+// a step from S to its last barrier, and whole tiles in rounds, 96 steps for
+// an SM where an even share is 81. Short calls: launches one after another and
+// the latency of a few dependent steps (2 x 1000 tokens, 8 + 2 heads: 12, 19 and
+// 6 us, with fp16 inputs 13, 22, 6 and 5 for the largest |v|).
 //
 // Every mbarrier wait is bounded (1 s); a role that gives up sets the status
 // word, waits for its own copies, and every role reaches the teardown, which
@@ -215,9 +218,9 @@ __device__ __forceinline__ void keep_seen(uint32_t (&w)[16], uint32_t bits) {
 
 // Warps of both kernels: two elementwise warpgroups, each with 32 of a step's
 // 64 columns to a thread, an auxiliary warpgroup, the TMA warp, the MMA warps.
-// (At D = 64, where the elementwise work bounds the kernels, two pairs of
-// warpgroups for the even and the odd steps took 65 to 69 us against 69 for
-// dK/dV of 2 x 16 heads of 1500 x 2048, and 48 against 47 for dQ: not kept.)
+// (At D = 64 two pairs of warpgroups for the even and the odd steps took 66 us
+// against 68 for dK/dV of 2 x 16 heads of 1500 x 2048, and 48 against 47 for dQ:
+// not kept. At D = 128 the dQ kernel's forms spill 8 to 16 bytes a thread.)
 constexpr int kAuxWarp = 8, kTmaWarp = 12, kMmaWarp = 13;
 
 // The 16 columns kk of a step's P or dS as an A operand: each warpgroup writes
@@ -235,8 +238,8 @@ __device__ __forceinline__ float hi16(uint32_t v) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(v >> 16)));
 }
 
-// 32 fp32 columns times `f`, stored from column `col` of a row of gradients;
-// wide: 32-byte stores (whole sectors, half the instructions).
+// `words` words of a row; wide: 32-byte stores (whole sectors, half the
+// instructions).
 __device__ __forceinline__ void store_words(void* dst, const uint32_t* w, int words, bool wide) {
 #pragma unroll
   for (int q = 0; q < words / 8; ++q) {
@@ -260,6 +263,7 @@ __device__ __forceinline__ void pack32(uint32_t* w, const uint32_t* r, float f) 
     w[e] = pack2_t<BF16>(__uint_as_float(r[2 * e]) * f, __uint_as_float(r[2 * e + 1]) * f);
 }
 
+// 32 fp32 columns times `f`, stored from column `col` of a row of gradients.
 template <bool BF16>
 __device__ __forceinline__ void store_row32(void* base, int64_t row_off, int col, bool g32,
                                             const uint32_t* r, float f, bool wide) {
@@ -1572,7 +1576,7 @@ Cut cut_tiles(int64_t tiles, int64_t steps, bool even, double save) {
 // Of the dK, dV kernel, whose key tiles' steps are those of all query heads, and
 // of the dQ kernel, whose steps take some 7 % longer when it can be cut: 4 heads
 // of 2048 x 2048 would save 11 % by the rule and lost 2 of 55 us, a head of
-// 4096 x 4096, causal, gained 6 to 12 of 66, 8 of 128 x 32,768 went from 300 to 84.
+// 4096 x 4096, causal, gained 6 to 12 of 66, 8 of 128 x 32,768 went from 300 to 87.
 Cut key_tiles(int64_t B, int64_t M, int64_t N, int64_t H, int64_t H_kv, int64_t left,
               int64_t right) {
   const int64_t rows = left + right + kBlk;  // queries that see a key tile

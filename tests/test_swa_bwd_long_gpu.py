@@ -34,6 +34,14 @@ def _room(gib):
         pytest.skip(f"needs {gib} GiB of free device memory")
 
 
+@pytest.fixture(autouse=True)
+def _give_back():
+    import torch
+
+    yield
+    torch.cuda.empty_cache()
+
+
 def _terms(q, k, v, o, do, lse):
     """p, dS and what fp32 errors of dS are relative to, of all pairs of rows."""
     import torch
