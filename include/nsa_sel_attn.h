@@ -500,7 +500,7 @@ int64_t nsa_swa_bwd_workspace_bytes(int64_t B, int64_t M, int64_t N, int64_t H, 
  * hold a key some query of a 128-query tile sees, Q and dO in the 64-query
  * tiles that hold a query which sees some key of a 128-key tile (as V must for
  * the forward, in 128-key tiles). M and N are at most 2^29. The outputs must
- * not overlap the inputs.
+ * not overlap the inputs or one another.
  *
  * Asynchronous: two kernels on `stream` (three with fp16 inputs, and up to two
  * more where gradients are joined from parts), no allocation; calls that may overlap need workspaces of their own.
