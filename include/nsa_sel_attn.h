@@ -63,10 +63,12 @@ typedef enum nsa_status {
                                buffer of nsa_sel_attn_bwd_noalloc (64 MiB)    */
   NSA_ERR_DTYPE = -11,      /* element type combination not supported by
                                nsa_sel_attn_fwd_ex                            */
-  NSA_ERR_BOUNDS = -12      /* (library built with NSA_DEBUG_BOUNDS only) a
+  NSA_ERR_BOUNDS = -12,     /* (library built with NSA_DEBUG_BOUNDS only) a
                                kernel's own bounds check found a tile outside
                                the keys its row may read; reported by
                                nsa_sync_status                                */
+  NSA_ERR_PAGE_SIZE = -13   /* a cache's page_size is no power of two from 16
+                               to 1024                                        */
 } nsa_status;
 
 /* Element types of nsa_sel_attn_fwd_ex. */
@@ -598,6 +600,147 @@ int nsa_qk_norm_rope_bwd(const void* Q, const void* K, const void* dQo, const vo
                          int interleaved, int dtype, int weight_dtype, int grad_dtype,
                          const int64_t* strides, void* workspace, int64_t workspace_bytes,
                          void* stream);
+
+/*
+ * A paged cache of keys and values (device memory of the caller's).
+ *
+ * `pages` pages hold page_size token rows for each of G KV heads of D entries.
+ * A sequence has its tokens where its row of a page table says: position p of
+ * sequence b is row p % page_size of page page_table[b * table_cols +
+ * p / page_size]. An entry outside [0, pages) (-1, say) is a page that the
+ * sequence does not have: one that it has not come to, or one given back
+ * behind a window. Sequences may share pages that are only read.
+ *
+ *   k, v           bits 16: the 16-bit rows [pages, page_size, G, D], with
+ *                  element strides k_strides, v_strides over (page, token,
+ *                  head), D contiguous; multiples of 8 in [0, 2^36], and not 0
+ *                  for a dimension of more than one.
+ *                  bits 4: bytes [pages, page_size, G, D / 2], contiguous (the
+ *                  strides are not used); byte i holds entry 2 i in its lower
+ *                  and entry 2 i + 1 in its upper four bits
+ *   k_scale,       bits 4: bf16 [pages, G, page_size, 2], contiguous: (step,
+ *   v_scale        low) of a row, whose entries are low + step * code. A step
+ *                  is 0 (all codes are 0), 2^-60 or more, or NaN.
+ *                  bits 16: not used
+ *   page_size      a power of two from 16 to 1024 (else NSA_ERR_PAGE_SIZE);
+ *                  table_cols * page_size is at most 2^30
+ *   bits           16 or 4 (else NSA_ERR_DTYPE)
+ *
+ * All pointers are 16-byte aligned. Every field is 8 bytes wide.
+ */
+typedef struct nsa_kv_cache {
+  void* k;
+  void* v;
+  void* k_scale;
+  void* v_scale;
+  int64_t pages;
+  int64_t page_size;
+  int64_t k_strides[3];
+  int64_t v_strides[3];
+  int64_t bits;
+} nsa_kv_cache;
+
+/*
+ * nsa_kv_append -- the RMS norm of every new query and key head and the
+ * position rotation, as nsa_qk_norm_rope, with K and V written into the cache:
+ * what a layer that answers does between its projections and nsa_paged_attn.
+ *
+ *   Q, Qo          device, dtype, [B, M, H, D]; Qo may be Q (same strides);
+ *                  H = 0: neither is used
+ *   K, V           device, dtype, [B, M, G, D]
+ *   cache,         the cache, written, and int32 [B, table_cols]
+ *   page_table
+ *   wq, wk, cos_table, sin_table, positions, R, table_rows, positions_stride,
+ *   interleaved, dtype, weight_dtype     as for nsa_qk_norm_rope
+ *   eps            >= 0: the norm's; < 0: no norm (wq, wk NULL)
+ *   strides        host array of 12 element strides, (b, m, head) of K, V, Q
+ *                  and Qo, or NULL for contiguous; rules as for
+ *                  nsa_qk_norm_rope. All can be slices of one projection.
+ *
+ * A 16-bit cache has the type of K and V. A 4-bit row is made of the row
+ * rounded to that type: low = bf16(min), step = bf16((max - low) / 15), 0 where
+ * that is below 2^-60, code = clamp(rint((x - low) / step), 0, 15); a row with
+ * an entry that is not finite, or whose range passes fp32's, reads as NaN.
+ *
+ * A token of negative position, or (R > 0) of one past the angle tables, is
+ * padding: its Q row is zero and nothing is stored. A token in a page that the
+ * sequence does not have is not stored; its Q row is formed. Two tokens of a
+ * call must not have the same place. Rows of the cache that no token is stored
+ * to are left as they are.
+ *
+ * One kernel on `stream`; allocates nothing and keeps no state. Errors before
+ * launch as nsa_qk_norm_rope, plus the cache's.
+ */
+int nsa_kv_append(const void* Q, const void* K, const void* V, void* Qo,
+                  const nsa_kv_cache* cache, const int32_t* page_table, const void* wq,
+                  const void* wk, const float* cos_table, const float* sin_table,
+                  const int32_t* positions, int64_t B, int64_t M, int64_t H, int64_t G, int64_t D,
+                  int64_t R, int64_t table_rows, int64_t positions_stride, int64_t table_cols,
+                  float eps, int interleaved, int dtype, int weight_dtype, const int64_t* strides,
+                  void* stream);
+
+/*
+ * nsa_kv_read -- rows of the cache as K and V tensors, as nsa_sel_attn_fwd and
+ * nsa_swa_fwd take them.
+ *
+ *   positions      as for nsa_kv_append: (b, m) reads the row of that position
+ *   K, V           device, dtype, [B, M, G, D], contiguous (output); dtype is
+ *                  the type of a 16-bit cache, either one for a 4-bit cache
+ *                  (low + step * code, rounded once)
+ *
+ * A negative position, or one in a page that the sequence does not have, gives
+ * rows of zeros. One kernel on `stream`. B M G is at most 2^34.
+ */
+int nsa_kv_read(const nsa_kv_cache* cache, const int32_t* page_table, const int32_t* positions,
+                void* K, void* V, int64_t B, int64_t M, int64_t G, int64_t D,
+                int64_t positions_stride, int64_t table_cols, int dtype, void* stream);
+
+/*
+ * nsa_paged_attn_workspace_bytes -- device workspace of nsa_paged_attn: 0 where
+ * M H/G rows make more than 1024 row tiles (of 8 rows, or 16 where there are
+ * more than 8) in the batch, else up to 10 MB, whatever the lengths.
+ * Negative nsa_status for invalid sizes. Pure host arithmetic.
+ */
+int64_t nsa_paged_attn_workspace_bytes(int64_t B, int64_t M, int64_t H, int64_t G, int64_t D);
+
+/*
+ * nsa_paged_attn -- attention of new tokens over the cache: the decoding step
+ * (M = 1), drafted tokens, or a piece of a prompt, after nsa_kv_append has
+ * stored their own keys and values.
+ *
+ *   Q              device, dtype, [B, M, H, D]; q_strides: host array of 3
+ *                  element strides (b, m, head), multiples of 8, or NULL
+ *   positions      device, int32, not NULL: as for nsa_kv_append; negative:
+ *                  padding
+ *   O              device, dtype, [B, M, H, D], contiguous (output)
+ *   LSE            device, fp32, [B, H, M] (output), or NULL
+ *   window_left,   query at position p sees key j of its sequence iff j <= p,
+ *   sinks          and j >= p - window_left (negative: no bound) or j < sinks,
+ *                  and the sequence has j's page
+ *   scale          score multiplier; <= 0 selects 1/sqrt(D)
+ *   workspace      device memory of nsa_paged_attn_workspace_bytes() bytes,
+ *                  16-byte aligned (else NSA_ERR_WORKSPACE, NSA_ERR_ALIGN);
+ *                  calls that may overlap need one each
+ *
+ * H is a multiple of G. p is rounded to 16 bits before the product with V (to
+ * dtype, or fp16 over a 4-bit cache), sums are fp32, O is rounded once. LSE is
+ * the natural log of sum(exp(scale q.k)) over the visible keys. A query that
+ * sees no key, or is padding, gets O = 0, LSE = -inf.
+ * Keys and values that no query of the sequence sees may hold anything. A V row
+ * (or the scales of a 4-bit row) that some query of 8, or 16, rows sees is
+ * multiplied by 0 for those that do not, and has to be finite.
+ *
+ * Every sum has an order that the sizes and positions alone decide: equal calls
+ * give equal bits. Two kernels on `stream` (one without a workspace), no
+ * allocation. Errors before launch: as nsa_swa_fwd, the cache's and the
+ * workspace's. A timed-out device wait is reported by nsa_sync_status.
+ */
+int nsa_paged_attn(const void* Q, const nsa_kv_cache* cache, const int32_t* page_table,
+                   const int32_t* positions, void* O, float* LSE, int64_t B, int64_t M, int64_t H,
+                   int64_t G, int64_t D, int64_t positions_stride, int64_t table_cols,
+                   int64_t window_left, int64_t sinks, float scale, int dtype,
+                   const int64_t* q_strides, void* workspace, int64_t workspace_bytes,
+                   void* stream);
 
 /*
  * nsa_sync_status -- wait for `stream`, then read and clear the device status

@@ -22,10 +22,12 @@ The C ABI is declared in ``include/nsa_sel_attn.h``; ``inputs`` draws the
 seeded synthetic workloads.
 """
 
-from ._lib import (NsaError, load, qk_norm_rope, qk_norm_rope_bwd, rope_tables,  # noqa: F401
+from ._lib import (KvCache, NsaError, kv_append, kv_cache, kv_read, load, paged_attn,   # noqa: F401
+                   qk_norm_rope, qk_norm_rope_bwd, rope_tables,
                    sel_attn_bwd, sel_attn_fwd, sel_attn_fwd_host, sel_attn_fwd_shared,
                    status_string, swa_bwd, swa_fwd, topk_blocks)
 
 __all__ = ["sel_attn_fwd", "sel_attn_fwd_shared", "sel_attn_bwd", "sel_attn_fwd_host",
            "topk_blocks", "swa_fwd", "swa_bwd", "qk_norm_rope", "qk_norm_rope_bwd", "rope_tables",
+           "KvCache", "kv_cache", "kv_append", "kv_read", "paged_attn",
            "load", "status_string", "NsaError"]

@@ -28,7 +28,8 @@ EXPORTS = ("nsa_status_string", "nsa_version", "nsa_sel_attn_fwd", "nsa_sel_attn
            "nsa_probe_l2_gather", "nsa_probe_l2_gather_bytes", "nsa_probe_gather_rows",
            "nsa_probe_reduce_rows", "nsa_sel_attn_fwd_host_ex", "nsa_sel_attn_bwd_ex",
            "nsa_qk_norm_rope", "nsa_qk_norm_rope_bwd", "nsa_qk_norm_rope_bwd_workspace_bytes",
-           "nsa_swa_bwd", "nsa_swa_bwd_workspace_bytes")
+           "nsa_swa_bwd", "nsa_swa_bwd_workspace_bytes", "nsa_kv_append", "nsa_kv_read",
+           "nsa_paged_attn", "nsa_paged_attn_workspace_bytes")
 
 _lib = None
 
@@ -123,6 +124,14 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.nsa_qk_norm_rope_bwd.restype = c_int
     lib.nsa_qk_norm_rope_bwd.argtypes = [vp] * 13 + [i64] * 8 + [f32, c_int, c_int, c_int, c_int,
                                                                  vp, vp, i64, vp]
+    lib.nsa_kv_append.restype = c_int
+    lib.nsa_kv_append.argtypes = [vp] * 11 + [i64] * 9 + [f32, c_int, c_int, c_int, vp, vp]
+    lib.nsa_kv_read.restype = c_int
+    lib.nsa_kv_read.argtypes = [vp] * 5 + [i64] * 6 + [c_int, vp]
+    lib.nsa_paged_attn_workspace_bytes.restype = i64
+    lib.nsa_paged_attn_workspace_bytes.argtypes = [i64] * 5
+    lib.nsa_paged_attn.restype = c_int
+    lib.nsa_paged_attn.argtypes = [vp] * 6 + [i64] * 9 + [f32, c_int, vp, vp, i64, vp]
     if path is None:
         _lib = lib
     return lib
@@ -798,6 +807,292 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, cos=Non
     if st != NSA_OK:
         raise NsaError(st, "nsa_qk_norm_rope_bwd")
     return dq, dk, dq_weight, dk_weight
+
+
+class KvCache:
+    """A paged cache of keys and values, as :func:`kv_append` fills it and
+    :func:`paged_attn` reads it: the tensors, which stay the caller's.
+
+    16 bits: ``k``, ``v`` fp16 or bf16 [pages, page_size, G, D]; strided views
+    (of one tensor that holds both, say) with a contiguous last dimension and
+    strides that are multiples of 8. 4 bits: ``k``, ``v`` uint8
+    [pages, page_size, G, D/2] and ``k_scale``, ``v_scale`` bf16
+    [pages, G, page_size, 2], all contiguous: byte i of a row holds the codes of
+    entries 2i (lower four bits) and 2i + 1, an entry is low + step * code, and
+    a scale is (step, low). page_size: a power of two from 16 to 1024.
+
+    Sequences own pages through a page table, int32 [B, cols]: position p of
+    sequence b is row p % page_size of page table[b, p // page_size]; an entry
+    outside [0, pages), -1 say, is a page that the sequence does not have.
+    """
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "bits", "pages", "page_size", "kv_heads",
+                 "head_dim", "_device", "_tail")
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if _torch is None:
+            _bind()
+        if k.dim() != 4 or k.shape != v.shape or k.dtype is not v.dtype:
+            raise ValueError("k and v must be alike, [pages, page_size, G, D]")
+        dev = k.get_device()
+        if (k_scale is None) != (v_scale is None):
+            raise ValueError("pass both scales (4 bits) or neither (16 bits)")
+        pages, page, G, D = k.shape
+        if k_scale is None:
+            if k.dtype not in _F16_KINDS:
+                raise TypeError(f"a 16-bit cache must be fp16 or bf16, got {k.dtype}")
+            strides = []
+            for name, t in (("k", k), ("v", v)):
+                if t.get_device() != dev or dev < 0 or t.stride(3) != 1:
+                    raise ValueError(f"{name} must be on k's CUDA device, with a contiguous last "
+                                     "dimension")
+                # (the stride of a dimension of one is never used)
+                strides += [s if n > 1 else 0 for n, s in zip(t.shape[:3], t.stride()[:3])]
+            self.bits = 16
+        else:
+            D *= 2
+            if k.dtype is not _torch.uint8:
+                raise TypeError(f"a 4-bit cache must be uint8, got {k.dtype}")
+            for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+                if t.dtype is not _torch.bfloat16:
+                    raise TypeError(f"{name} must be bf16, got {t.dtype}")
+                if t.shape != (pages, G, page, 2):
+                    raise ValueError(f"{name} must be [pages, G, page_size, 2]")
+            for name, t in (("k", k), ("v", v), ("k_scale", k_scale), ("v_scale", v_scale)):
+                if t.get_device() != dev or dev < 0 or not t.is_contiguous():
+                    raise ValueError(f"{name} must be a contiguous tensor on k's CUDA device")
+            strides = [0] * 6
+            self.bits = 4
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.page_size, self.kv_heads, self.head_dim = pages, page, G, D
+        self._device = dev
+        self._tail = (pages, page, *strides, self.bits)
+
+    def _struct(self):
+        """nsa_kv_cache: thirteen 8-byte fields."""
+        if self.bits == 16:
+            return array("Q", (self.k.data_ptr(), self.v.data_ptr(), 0, 0, *self._tail))
+        return array("Q", (self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(),
+                           self.v_scale.data_ptr(), *self._tail))
+
+
+def kv_cache(pages: int, page_size: int, kv_heads: int, head_dim: int, dtype=None, bits: int = 16,
+             device="cuda") -> KvCache:
+    """An empty :class:`KvCache` of ``pages`` pages: ``dtype`` (bf16 by default)
+    rows with ``bits`` 16, 4-bit rows with 4. What pages hold before tokens are
+    stored is not defined, and is never seen."""
+    import torch
+
+    if bits == 16:
+        dt = torch.bfloat16 if dtype is None else dtype
+        shape = (pages, page_size, kv_heads, head_dim)
+        return KvCache(*(torch.empty(shape, dtype=dt, device=device) for _ in range(2)))
+    if bits != 4:
+        raise ValueError(f"bits must be 16 or 4, got {bits}")
+    shape = (pages, page_size, kv_heads, head_dim // 2)
+    scale = (pages, kv_heads, page_size, 2)
+    return KvCache(*(torch.empty(shape, dtype=torch.uint8, device=device) for _ in range(2)),
+                   *(torch.empty(scale, dtype=torch.bfloat16, device=device) for _ in range(2)))
+
+
+def _check_places(cache, page_table, positions, B, M, dev, need=False):
+    """Checks of a cache's page table and positions; returns (columns, the
+    stride of positions over the batch)."""
+    if cache._device != dev:
+        raise ValueError("the cache must be on the tensors' CUDA device")
+    if page_table.dtype is not _torch.int32:
+        raise TypeError(f"page_table must be int32, got {page_table.dtype}")
+    ts = page_table.shape
+    if len(ts) != 2 or ts[0] != B:
+        raise ValueError("page_table must be [B, cols]")
+    if page_table.get_device() != dev or not page_table.is_contiguous():
+        raise ValueError("page_table must be a contiguous tensor on the cache's device")
+    if positions is None:
+        if need:
+            raise ValueError("positions are needed: [M] or [B, M]")
+        return ts[1], 0
+    if positions.dtype is not _torch.int32:
+        raise TypeError(f"positions must be int32, got {positions.dtype}")
+    ps = positions.shape
+    if ps != (B, M) and ps != (M,):
+        raise ValueError("positions must be [M] or [B, M]")
+    if positions.get_device() != dev or not positions.is_contiguous():
+        raise ValueError("positions must be a contiguous tensor on the cache's device")
+    return ts[1], M if len(ps) == 2 else 0
+
+
+def kv_append(q, k, v, cache: KvCache, page_table, positions=None, q_weight=None, k_weight=None,
+              cos=None, sin=None, eps: Optional[float] = 1e-6, interleaved: bool = False,
+              q_out=None, *, stream=None):
+    """Norm and rotation of new query and key heads, as :func:`qk_norm_rope`,
+    with K and V stored in a paged cache (nsa_kv_append).
+
+    q: fp16 or bf16 [B, M, H, D] (or None); k, v: [B, M, G, D] of q's dtype, and
+    of the cache's where that has 16 bits; strided views are taken as in
+    qk_norm_rope. ``page_table``: int32 [B, cols]. ``positions``, weights,
+    tables, ``interleaved``: as in qk_norm_rope; ``eps`` None: no norm (and no
+    weights), the rotation alone. Padding tokens, and tokens whose page the
+    sequence does not have, are not stored. Two tokens of a call must not have
+    the same place. Runs on torch's current stream, or on ``stream``. Returns
+    q_out (None without q).
+    """
+    lib = _bound or _bind()
+    if stream is not None:
+        return _on_stream(stream, lambda k: kv_append(
+            q, k, v, cache, page_table, positions, q_weight, k_weight, cos, sin, eps, interleaved,
+            q_out), k)
+    if q is None:
+        q = q_out = k[:, :, :0]
+        H = 0
+    else:
+        if q_out is None:
+            q_out = _dense_like(q)
+        H = q.shape[2]
+    own = (k.dtype,)
+    dev, sizes, code, wcode, strides = _check_rope(
+        (("q", q, own), ("k", k, own), ("q_out", q_out, own), ("v", v, own)), q_weight, k_weight,
+        cos, sin, positions)
+    B, M, _, G, D, R, rows, pstride = sizes
+    if cache.kv_heads != G or cache.head_dim != D or (cache.bits == 16
+                                                      and cache.k.dtype is not k.dtype):
+        raise ValueError("the cache must have k's heads and entries, and with 16 bits its dtype")
+    if eps is None:
+        if q_weight is not None or k_weight is not None:
+            raise ValueError("weights belong to the norm (eps)")
+        eps = -1.0
+    elif not eps >= 0:
+        raise ValueError("eps must be >= 0, or None: no norm")
+    cols, _ = _check_places(cache, page_table, positions, B, M, dev)
+    if strides is not None:  # (q, k, q_out, v) -> (k, v, q, q_out)
+        s = strides
+        strides = s[3:6] + s[9:12] + s[0:3] + s[6:9]
+    kv = cache._struct()
+    st = _launch(dev, lib.nsa_kv_append, q.data_ptr() if H else None, k.data_ptr(), v.data_ptr(),
+                 q_out.data_ptr() if H else None, kv.buffer_info()[0], page_table.data_ptr(),
+                 _at(q_weight), _at(k_weight), _at(cos), _at(sin), _at(positions), B, M, H, G, D, R,
+                 rows, pstride, cols, eps, 1 if interleaved else 0, code, wcode,
+                 None if strides is None else strides.buffer_info()[0])
+    if st != NSA_OK:
+        raise NsaError(st, "nsa_kv_append")
+    return q_out if H else None
+
+
+def kv_read(cache: KvCache, page_table, positions, dtype=None, k_out=None, v_out=None, *,
+            stream=None):
+    """Rows of a paged cache as K and V (nsa_kv_read): [B, M, G, D] of the
+    tokens at ``positions``, int32 [B, M] or [M], as :func:`sel_attn_fwd` and
+    :func:`swa_fwd` take them. Zeros where a position is negative or its page
+    one that the sequence does not have. ``dtype``: the cache's own with 16 bits;
+    with 4 bits fp16 or bf16 (the default). Returns (k, v)."""
+    lib = _bound or _bind()
+    if stream is not None:
+        return _on_stream(stream, lambda _: kv_read(cache, page_table, positions, dtype, k_out,
+                                                    v_out), cache.k)
+    if dtype is None:
+        dtype = k_out.dtype if k_out is not None else \
+            cache.k.dtype if cache.bits == 16 else _torch.bfloat16
+    if dtype not in _F16_KINDS or (cache.bits == 16 and dtype is not cache.k.dtype):
+        raise TypeError("dtype must be the cache's, or with 4 bits fp16 or bf16, got "
+                        f"{dtype}")
+    B = page_table.shape[0]
+    M = positions.shape[-1] if positions.dim() else 0
+    dev = cache._device
+    cols, pstride = _check_places(cache, page_table, positions, B, M, dev, need=True)
+    shape = (B, M, cache.kv_heads, cache.head_dim)
+    if k_out is None:
+        k_out = _torch.empty(shape, dtype=dtype, device=cache.k.device)
+    if v_out is None:
+        v_out = _torch.empty(shape, dtype=dtype, device=cache.k.device)
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or \
+                t.get_device() != dev:
+            raise ValueError(f"{name} must be a contiguous {dtype} {shape} tensor on the cache's "
+                             "device")
+    kv = cache._struct()
+    st = _launch(dev, lib.nsa_kv_read, kv.buffer_info()[0], page_table.data_ptr(),
+                 positions.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), B, M, cache.kv_heads,
+                 cache.head_dim, pstride, cols, _DTYPE_CODES[dtype])
+    if st != NSA_OK:
+        raise NsaError(st, "nsa_kv_read")
+    return k_out, v_out
+
+
+def paged_attn_workspace_bytes(B, M, H, G, D) -> int:
+    n = (_lib or load()).nsa_paged_attn_workspace_bytes(B, M, H, G, D)
+    if n < 0:
+        raise NsaError(int(n), "nsa_paged_attn_workspace_bytes")
+    return n
+
+
+def paged_attn(q, cache: KvCache, page_table, positions, window=(-1, 0), sinks: int = 0,
+               scale: Optional[float] = None, out=None, lse=None, return_lse: bool = True,
+               workspace=None, *, stream=None):
+    """Attention of new tokens over a paged cache that holds their own keys and
+    values too (nsa_paged_attn): a decoding step (M = 1), drafted tokens, or a
+    piece of a prompt.
+
+    q: fp16 or bf16 [B, M, H, D] (strided views as in :func:`kv_append`), of the
+    cache's dtype where that has 16 bits; ``page_table`` int32 [B, cols],
+    ``positions`` int32 [B, M] or [M], negative: padding. The query at position
+    p sees the keys j <= p of its sequence with j >= p - left or j < ``sinks``
+    (the first tokens, which stay visible behind the window), as far as the
+    sequence has their pages; ``window`` = (left, 0), left negative: unbounded.
+    Returns (O [B, M, H, D] of q's dtype, LSE fp32 [B, H, M] or None); O = 0 and
+    LSE = -inf where a query sees nothing. ``workspace`` (CUDA uint8,
+    paged_attn_workspace_bytes) is allocated when omitted; calls that may
+    overlap need one each. Runs on torch's current stream, or on ``stream``.
+    """
+    lib = _bound or _bind()
+    if stream is not None:
+        return _on_stream(stream, paged_attn, q, cache, page_table, positions, window, sinks, scale,
+                          out, lse, return_lse, workspace)
+    dt, qs = q.dtype, q.shape
+    if dt not in _F16_KINDS:
+        raise TypeError(f"q must be fp16 or bf16, got {dt}")
+    if len(qs) != 4 or qs[3] != cache.head_dim:
+        raise ValueError("q must be [B, M, H, D] with the cache's D")
+    if cache.bits == 16 and cache.k.dtype is not dt:
+        raise TypeError(f"q must be of the cache's dtype {cache.k.dtype}, got {dt}")
+    B, M, H, D = qs
+    dev = q.get_device()
+    if dev < 0 or not (q.is_contiguous() or q.stride(3) == 1):
+        raise ValueError("q must be a CUDA tensor with a contiguous last dimension")
+    cols, pstride = _check_places(cache, page_table, positions, B, M, dev, need=True)
+    left, right = window
+    if right != 0:
+        raise ValueError("window must be (left, 0): the cache ends at the queries")
+    if out is None:
+        out = _torch.empty(qs, dtype=dt, device=q.device)
+    elif out.dtype is not dt or out.shape != qs or not out.is_contiguous() or \
+            out.get_device() != dev:
+        raise ValueError(f"out must be a contiguous {dt} [B, M, H, D] tensor on q's device")
+    if lse is None:
+        if return_lse:
+            lse = _torch.empty((B, H, M), dtype=_torch.float32, device=q.device)
+    elif lse.dtype is not _torch.float32 or lse.shape != (B, H, M) or not lse.is_contiguous() or \
+            lse.get_device() != dev:
+        raise ValueError("lse must be a contiguous fp32 [B, H, M] tensor on q's device")
+    strides = None
+    if not q.is_contiguous():
+        b, m, h, _ = q.stride()
+        strides = array("q", (b if B > 1 else 0, m if M > 1 else 0, h if H > 1 else 0))
+    if workspace is None:
+        nbytes = paged_attn_workspace_bytes(B, M, H, cache.kv_heads, D)
+        if nbytes:
+            workspace = _torch.empty(nbytes, dtype=_torch.uint8, device=q.device)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on q's CUDA device")
+    kv = cache._struct()
+    # scale: the ABI takes <= 0 for 1/sqrt(D)
+    st = _launch(dev, lib.nsa_paged_attn, q.data_ptr(), kv.buffer_info()[0], page_table.data_ptr(),
+                 positions.data_ptr(), out.data_ptr(), _at(lse), B, M, H, cache.kv_heads, D, pstride,
+                 cols, left, sinks, 0.0 if scale is None else scale, _DTYPE_CODES[dt],
+                 None if strides is None else strides.buffer_info()[0], _at(workspace), nbytes)
+    if st != NSA_OK:
+        raise NsaError(st, "nsa_paged_attn")
+    return out, lse
 
 
 def probe_l2_gather(k, v, g: int, block_size: int, ctas: int, warps_per_cta: int,

@@ -38,6 +38,7 @@
 #include "common.cuh"
 #include "nsa_sel_attn.h"
 #include "ptx.cuh"
+#include "rope.cuh"
 
 namespace nsa {
 namespace {
@@ -61,140 +62,6 @@ constexpr int64_t kFewGroups = 128 * kRopeSms;
 // slots alone: 32,768 tokens of 32 + 4 heads at D = 64 102 us against 143,
 // of 64 + 8 at D = 128 338 against 351.
 constexpr double kUnitCost = 0.5, kGroupCost = 0.6;
-
-struct RopeRows {
-  const uint8_t* x;  // one of Q, K: element strides over (b, m, h)
-  uint8_t* y;
-  const void* w;
-  int64_t xb, xm, xh, yb, ym, yh;
-  int heads;
-};
-
-struct RopeProblem {
-  RopeRows q, k;
-  const float* cos_t;
-  const float* sin_t;
-  const int32_t* pos;
-  int64_t pos_b, table_rows;
-  int B, M, half;  // half = R / 2
-  bool interleaved, w32;
-  float eps;
-};
-
-// The two chunks of 8 entries that lane t of a row holds.
-__device__ __forceinline__ void row_chunks(int t, int half, int& c0, int& c1) {
-  const int pc = half >> 3;  // chunks of a half
-  if (t < pc) {
-    c0 = t;
-    c1 = t + pc;
-  } else {
-    c0 = 2 * t;  // 2 pc + 2 (t - pc)
-    c1 = 2 * t + 1;
-  }
-}
-
-template <bool BF16>
-__device__ __forceinline__ float2 unpack2(uint32_t v) {
-  if constexpr (BF16) {
-    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
-  } else {
-    return __half22float2(*reinterpret_cast<const __half2*>(&v));
-  }
-}
-
-template <bool BF16>
-__device__ __forceinline__ void unpack8(const uint4& v, float* f) {
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 p = unpack2<BF16>(u[i]);
-    f[2 * i] = p.x;
-    f[2 * i + 1] = p.y;
-  }
-}
-
-template <bool BF16>
-__device__ __forceinline__ uint4 pack8(const float* f) {
-  return make_uint4(pack2_t<BF16>(f[0], f[1]), pack2_t<BF16>(f[2], f[3]),
-                    pack2_t<BF16>(f[4], f[5]), pack2_t<BF16>(f[6], f[7]));
-}
-
-__device__ __forceinline__ void load8(const float* p, float* f) {
-  const float4 a = *reinterpret_cast<const float4*>(p);
-  const float4 b = *reinterpret_cast<const float4*>(p + 4);
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-  f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-}
-
-// The 16 weights of this lane's chunks (1 without a weight).
-template <bool BF16>
-__device__ __forceinline__ void load_weights(const void* w, bool w32, int c0, int c1, float* f) {
-  if (w == nullptr) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) f[i] = 1.f;
-  } else if (w32) {
-    load8(static_cast<const float*>(w) + 8 * c0, f);
-    load8(static_cast<const float*>(w) + 8 * c1, f + 8);
-  } else {
-    const uint4* p = static_cast<const uint4*>(w);
-    unpack8<BF16>(p[c0], f);
-    unpack8<BF16>(p[c1], f + 8);
-  }
-}
-
-// The 8 angles of the lane's 8 pairs. Halves: pair j is entries j of the two
-// chunks. Interleaved: pairs 0..3 are the entries (2j, 2j + 1) of the first
-// chunk, 4..7 those of the second.
-__device__ __forceinline__ void load_angles(const RopeProblem& p, int64_t at, int c0, int c1,
-                                            float* c, float* s) {
-  const float* ct = p.cos_t + at * p.half;
-  const float* st = p.sin_t + at * p.half;
-  if (p.interleaved) {
-    const float4 a = *reinterpret_cast<const float4*>(ct + 4 * c0);
-    const float4 b = *reinterpret_cast<const float4*>(ct + 4 * c1);
-    const float4 d = *reinterpret_cast<const float4*>(st + 4 * c0);
-    const float4 e = *reinterpret_cast<const float4*>(st + 4 * c1);
-    c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w, c[4] = b.x, c[5] = b.y, c[6] = b.z, c[7] = b.w;
-    s[0] = d.x, s[1] = d.y, s[2] = d.z, s[3] = d.w, s[4] = e.x, s[5] = e.y, s[6] = e.z, s[7] = e.w;
-  } else {
-    load8(ct + 8 * c0, c);
-    load8(st + 8 * c0, s);
-  }
-}
-
-// (a, b) -> (a c - b s, b c + a s) on the lane's 8 pairs.
-__device__ __forceinline__ void turn(float* f, const float* c, const float* s, bool interleaved) {
-  if (interleaved) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float a = f[2 * j], b = f[2 * j + 1];
-      f[2 * j] = a * c[j] - b * s[j];
-      f[2 * j + 1] = b * c[j] + a * s[j];
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float a = f[j], b = f[j + 8];
-      f[j] = a * c[j] - b * s[j];
-      f[j + 8] = b * c[j] + a * s[j];
-    }
-  }
-}
-
-template <int LPR>
-__device__ __forceinline__ float row_sum(float v) {
-#pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-  return v;
-}
-
-// A token's position, or -1 for padding (outside the table).
-__device__ __forceinline__ int64_t token_position(const RopeProblem& p, int b, int m) {
-  int64_t at = m;
-  if (p.pos != nullptr) at = p.pos[b * p.pos_b + m];
-  if (at < 0 || (p.half > 0 && at >= p.table_rows)) return -1;
-  return at;
-}
 
 // Rows [r0, r1) of one token's heads, UN groups of rows in flight per warp.
 template <int D, bool BF16, int UN>
@@ -269,15 +136,6 @@ __global__ void __launch_bounds__(kRopeThreads)
     norm_rope_rows<D, BF16, UN>(p, p.k, b, m, max(r0 - p.q.heads, 0), r1 - p.q.heads, live, rot, c0,
                                 c1, c, s);
 }
-
-// How a warp's row slots map to (token, head) where a token has few heads: one
-// token to a group of slots, or several, with the heads rounded up to a power
-// of two; more heads than slots take several groups.
-struct RowGroups {
-  int per_token;  // groups of a token (1 where tokens share a group)
-  int shift;      // log2 of the slots of a token, where tokens share a group
-  int64_t groups;
-};
 
 // The forward where a token has few heads: a row slot of a warp keeps its head,
 // and the head's weights, and walks the tokens, each with its own position and
@@ -695,59 +553,6 @@ __global__ void __launch_bounds__(1024)
 
 // ---- host ---------------------------------------------------------------
 
-bool aligned(const void* p, uintptr_t a) {
-  return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
-}
-
-int check_rope(int64_t B, int64_t M, int64_t H, int64_t G, int64_t D, int64_t R, int64_t table_rows,
-               int64_t positions_stride, float eps, int dtype, int weight_dtype) {
-  if (B < 0 || M < 0 || H <= 0 || G <= 0) return NSA_ERR_SHAPE;
-  if (D != 64 && D != 128) return NSA_ERR_HEAD_DIM;
-  if (R < 0 || R > D || R % 16 != 0) return NSA_ERR_SHAPE;
-  if (table_rows < 0 || table_rows > (int64_t(1) << 31) || positions_stride < 0)
-    return NSA_ERR_SHAPE;
-  if (!(eps >= 0.f) || std::isinf(eps)) return NSA_ERR_SHAPE;
-  const int64_t lim = int64_t(1) << 30;
-  if (B > lim || M > lim || H > 65536 || G > 65536) return NSA_ERR_SHAPE;
-  if (B * M >= (int64_t(1) << 31)) return NSA_ERR_SHAPE;
-  if (dtype != NSA_F16 && dtype != NSA_BF16) return NSA_ERR_DTYPE;
-  if (weight_dtype != NSA_F32 && weight_dtype != dtype) return NSA_ERR_DTYPE;
-  return NSA_OK;
-}
-
-// n groups of 3 element strides; NULL: contiguous rows of D. The last two
-// groups are written: a stride of 0 would put several rows in one place.
-int take_strides(const int64_t* strides, int n, const int64_t* heads, int64_t B, int64_t M,
-                 int64_t D, int64_t* out) {
-  for (int i = 0; i < n; ++i) {
-    if (strides == nullptr) {
-      out[3 * i] = M * heads[i] * D;
-      out[3 * i + 1] = heads[i] * D;
-      out[3 * i + 2] = D;
-    } else {
-      for (int j = 0; j < 3; ++j) {
-        const int64_t s = strides[3 * i + j];
-        if (s < 0 || s > (int64_t(1) << 40)) return NSA_ERR_SHAPE;
-        if (s % 8 != 0) return NSA_ERR_ALIGN;
-        const int64_t extent = j == 0 ? B : j == 1 ? M : heads[i];
-        if (i >= n - 2 && s == 0 && extent > 1) return NSA_ERR_SHAPE;
-        out[3 * i + j] = s;
-      }
-    }
-  }
-  return NSA_OK;
-}
-
-int check_tables(const float* cos_t, const float* sin_t, const int32_t* positions, int64_t M,
-                 int64_t R, int64_t table_rows) {
-  if (R > 0) {
-    if (table_rows > 0 && (!cos_t || !sin_t)) return NSA_ERR_NULL;
-    if (!aligned(cos_t, 16) || !aligned(sin_t, 16)) return NSA_ERR_ALIGN;
-    if (positions == nullptr && M > table_rows) return NSA_ERR_SHAPE;
-  }
-  return aligned(positions, 4) ? NSA_OK : NSA_ERR_ALIGN;
-}
-
 // Most CTAs of the backward, each with one dw partial: what the SMs hold at
 // once, for Q and K together; one of each at least.
 constexpr int kRopeBwdCtas = kRopeBwdPerSm * kRopeSms;
@@ -755,19 +560,6 @@ constexpr int kRopeBwdCtas = kRopeBwdPerSm * kRopeSms;
 int rope_bwd_most_ctas(int64_t B, int64_t M) {
   const int64_t tokens = B * M;
   return tokens == 0 ? 0 : kRopeBwdCtas;
-}
-
-RowGroups plan_row_groups(int heads, int64_t tokens, int slots) {
-  RowGroups g{1, 0, 0};
-  if (heads > slots) {
-    g.per_token = (heads + slots - 1) / slots;
-    g.groups = tokens * g.per_token;
-  } else {
-    while ((1 << g.shift) < heads) ++g.shift;
-    const int64_t shared = slots >> g.shift;  // tokens of a group
-    g.groups = (tokens + shared - 1) / shared;
-  }
-  return g;
 }
 
 // What a tensor's rows cost the backward, in groups of row slots, and whether
