@@ -697,8 +697,8 @@ int nsa_kv_read(const nsa_kv_cache* cache, const int32_t* page_table, const int3
 
 /*
  * nsa_paged_attn_workspace_bytes -- device workspace of nsa_paged_attn: 0 where
- * M H/G rows make more than 1024 row tiles (of 8 rows, or 16 where there are
- * more than 8) in the batch, else up to 10 MB, whatever the lengths.
+ * M H/G rows make more than 512 row tiles (of 8 rows, or 16 where there are
+ * more than 8) in the batch, else up to 20 MB, whatever the lengths.
  * Negative nsa_status for invalid sizes. Pure host arithmetic.
  */
 int64_t nsa_paged_attn_workspace_bytes(int64_t B, int64_t M, int64_t H, int64_t G, int64_t D);
@@ -711,7 +711,7 @@ int64_t nsa_paged_attn_workspace_bytes(int64_t B, int64_t M, int64_t H, int64_t 
  *   Q              device, dtype, [B, M, H, D]; q_strides: host array of 3
  *                  element strides (b, m, head), multiples of 8, or NULL
  *   positions      device, int32, not NULL: as for nsa_kv_append; negative:
- *                  padding
+ *                  padding; at most 2^31 - 32
  *   O              device, dtype, [B, M, H, D], contiguous (output)
  *   LSE            device, fp32, [B, H, M] (output), or NULL
  *   window_left,   query at position p sees key j of its sequence iff j <= p,

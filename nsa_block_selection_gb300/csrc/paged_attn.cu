@@ -15,21 +15,29 @@
 // (mma.sync m16n8k16). A decoding step has 8 rows or fewer, of which a 128-row
 // tcgen05 tile would be 1/16 full; what bounds the call is the cache's bytes.
 //
-// Keys. A warp takes 16-key tiles, which lie in one page each, through a ring of
-// its own of shared-memory slots that lane 0 fills with TMA copies; a CTA's four
-// warps take its tiles in turn and are joined in shared memory at the end of an
-// item (row tile and KV head). The tiles of all items are dealt to the CTAs in
-// equal, contiguous shares, whatever the lengths of the sequences: positions
-// are on the device, so every CTA forms the running count of the items' tiles
-// for itself. An item that a share's border cuts leaves fp32 pieces, which
-// paged_attn_join_kernel adds in a fixed order: equal calls give equal bits.
+// Keys. A warp takes 16-key tiles, which lie in one page each; the four warps of
+// a CTA take its tiles in turn and are joined in shared memory at the end of an
+// item (a row tile and a KV head, or a few neighbouring KV heads). The tiles of
+// all items are dealt to the CTAs in equal, contiguous shares, whatever the
+// lengths of the sequences: positions are on the device, so every CTA forms the
+// running count of the items' tiles for itself. An item that a share's border
+// cuts leaves fp32 pieces, which paged_attn_join_kernel adds in a fixed order:
+// equal calls give equal bits.
 //
-// 4 bits. k = low + step c gives q.k = step (q.c) + low sum(q): the codes
+// 16 bits: tiles come by TMA through a ring of shared-memory slots of the warp's
+// own, ldmatrix makes the operands.
+//
+// 4 bits: k = low + step c gives q.k = step (q.c) + low sum(q): the codes
 // themselves enter the product, as fp16 subnormals (c 2^-24, or 16 c 2^-24 for
 // the upper four bits of a byte, which Q's entries are divided by 16 for): a
 // mask, or a shift and a mask, makes two entries. Q's rows are scaled by a power
-// of two into fp16's range. For V, 2^(x + log2 step - r) c is summed, so r
-// follows x + log2(step), and p = that / step; sum p low is added at the end.
+// of two into fp16's range. For V, p' = 2^(x + log2 step - r) is the product's
+// operand (r follows x + log2 step), p = p' / step, and with
+// v = (low + 8 step) + step (c - 8) the sum of p (low + 8 step) - 8 p' is added
+// at the end, p' as rounded, so that its rounding falls on c - 8. A slot of the
+// CTA's one ring holds 128 rows, 32 for each warp, and the warps issue the copies
+// in turn: neighbouring heads of a token lie in one 128-byte line, so a CTA takes
+// two or four of them at once.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -51,30 +59,36 @@ namespace {
 constexpr int kPaWarps = 4;
 constexpr int kPaThreads = 32 * kPaWarps;
 constexpr int kPaTile = 16;       // keys of a tile
-constexpr int kPaItems = 1024;    // row tiles of a batch that shares are formed of
+constexpr int kPaSlotRows = 128;  // (head, key) rows of a 4-bit slot
+constexpr int kPaItems = 512;     // row tiles of a batch that shares are formed of
 constexpr int kPaSms = 152;
-constexpr int kPaLeast = 8;       // tiles of a share at least
+constexpr int kPaMostPerSm = 4;
+constexpr int kPaLeast = 128;     // keys of a share at least
 constexpr float kPaSlack = 8.0f;
 
 template <int D, bool Q4, int NT>
 struct PaCfg {
-  static constexpr int kStages = Q4 ? 4 : 2;
   static constexpr int kPerSm = Q4 && (D == 64 || NT == 1) ? 4 : 3;  // CTAs
-  static constexpr int kRowBytes = Q4 ? D / 2 : 2 * D;
-  static constexpr int kKv = kPaTile * kRowBytes;          // one K or V tile
-  static constexpr int kScales = Q4 ? 2 * kPaTile * 4 : 0;  // (step, low) of K, of V
-  static constexpr int kBytes = 2 * kKv + kScales;         // copied for a tile
-  static constexpr int kSlot = Q4 ? 2 * kKv : kBytes;
-  static constexpr int kOffScale = kPaWarps * kStages * kSlot;
+  // 16 bits: a ring for each warp, 16 keys of K and V in a slot. 4 bits: one for
+  // the CTA, 128 rows of K and V and their scales in a slot, 32 for each warp.
+  static constexpr int kStages = Q4 ? 3 : 2;
+  static constexpr int kRings = Q4 ? 1 : kPaWarps;
+  static constexpr int kKv = Q4 ? kPaSlotRows * (D / 2) : kPaTile * 2 * D;  // K's (or V's) part
+  static constexpr int kScales = Q4 ? kPaSlotRows * 4 : 0;
+  static constexpr int kSlot = 2 * kKv + 2 * kScales;
+  static constexpr int kRing = kRings * kStages * kSlot;
+  static constexpr int kKeys = Q4 ? kPaSlotRows / kPaTile : 1;  // first keys kept for a slot
   static constexpr int kPad = D + 4;  // row stride of the joined O, in floats
   static constexpr int kJoin = kPaWarps * 8 * NT * kPad * 4;
-  static constexpr int kRing = kOffScale + kPaWarps * kStages * kScales;
   static constexpr int kOffStat = kRing > kJoin ? kRing : kJoin;  // 2 floats a warp and row
   static constexpr int kOffBar = kOffStat + kPaWarps * 8 * NT * 8;
-  static constexpr int kOffKey = kOffBar + kPaWarps * kStages * 8;
-  static constexpr int kOffCount = kOffKey + kPaWarps * kStages * 4;
+  static constexpr int kOffKey = kOffBar + kRings * kStages * 16;  // (full, empty)
+  static constexpr int kOffCount = kOffKey + kRings * kStages * kKeys * 4;
   static constexpr int kSmem = kOffCount + (kPaItems + 1) * 4 + 1024;
 };
+
+// First key of a tile that is not there, past every position.
+constexpr int kNoKey = 0x7ffffff0, kPaFar = 0x7fffffe0;
 
 struct PagedProblem {
   KvPages c;
@@ -84,35 +98,45 @@ struct PagedProblem {
   float* lse;          // [B, H, M] or NULL
   const int32_t* pos;
   int64_t pos_b;
-  float* piece;       // [2 gridDim.x][8 NT][D], then [..][8 NT][2] (reference, sum)
-  int64_t* count;     // [items + 1]: running tiles of the items, and a share's tiles
+  // [2 ctas][rows of an item][D], then [2 ctas][rows of an item][2] (reference, sum)
+  float* piece;
+  int64_t* count;     // [items + 1]: running steps of the items, and a share's steps
   int B, M, H, G, hpg, rows, tiles, items;  // rows of a KV head, row tiles, B * tiles
   int left, sinks, ctas;
+  int heads_item, groups;  // KV heads of an item, G / heads_item
+  int step_shift;          // keys of a step: 16; 4 bits: 128 / heads_item
+  int split;               // 4 bits: copies that a step's keys take (small pages)
   float sl2;
   bool cut;
 };
 
-// What a row tile of a sequence has to read: n 16-key tiles, of which the first
-// `st` start at key 0 and the others `jump` tiles further on.
+// What a row tile of a sequence has to read: n steps of 1 << shift keys, of which
+// the first `st` start at key 0 and the others `jump` steps further on.
 struct PaSpan {
-  int n, st, jump;
+  int n, st, jump, shift;
   int lo_pos, hi_pos;  // smallest and largest position of its queries
+  __device__ __forceinline__ int key(int t) const { return (t < st ? t : t + jump) << shift; }
 };
+
+// A query's position (one at the end of int32 as kPaFar: kNoKey is past them all).
+__device__ __forceinline__ int pa_position(const PagedProblem& p, int b, int m) {
+  return min(__ldg(p.pos + b * p.pos_b + m), kPaFar);
+}
 
 __device__ __forceinline__ PaSpan pa_span(const PagedProblem& p, int b, int rt, int rows_tile) {
   const int r0 = rt * rows_tile, r1 = min(r0 + rows_tile, p.rows) - 1;
-  PaSpan s{0, 0, 0, 0x7fffffff, -1};
+  PaSpan s{0, 0, 0, p.step_shift, 0x7fffffff, -1};
   const int m1 = r1 / p.hpg;
   for (int m = r0 / p.hpg; m <= m1; ++m) {
-    const int at = __ldg(p.pos + b * p.pos_b + m);
+    const int at = pa_position(p, b, m);
     if (at < 0) continue;
     s.lo_pos = min(s.lo_pos, at);
     s.hi_pos = max(s.hi_pos, at);
   }
   if (s.hi_pos < 0) return s;
-  const int last = min(s.hi_pos, (p.c.cols << p.c.shift) - 1) / kPaTile;  // (at most 2^30 tokens)
-  const int first = (p.left < s.lo_pos ? s.lo_pos - p.left : 0) / kPaTile;
-  s.st = min((p.sinks + kPaTile - 1) / kPaTile, last + 1);
+  const int last = min(s.hi_pos, (p.c.cols << p.c.shift) - 1) >> s.shift;  // (at most 2^30 tokens)
+  const int first = (p.left < s.lo_pos ? s.lo_pos - p.left : 0) >> s.shift;
+  s.st = min((p.sinks + (1 << s.shift) - 1) >> s.shift, last + 1);
   if (first <= s.st) {
     s.n = last + 1;
   } else if (first > last) {  // the window lies behind the table's end
@@ -124,230 +148,107 @@ __device__ __forceinline__ PaSpan pa_span(const PagedProblem& p, int b, int rt, 
   return s;
 }
 
-template <bool BF16>
-__device__ __forceinline__ float half_of(uint32_t v, int hi) {
-  const uint32_t h = hi ? v >> 16 : v & 0xffffu;
-  if constexpr (BF16) return __uint_as_float(h << 16);
-  return __half2float(__ushort_as_half(static_cast<unsigned short>(h)));
+// What the queries of a row tile see of a key.
+struct PaSight {
+  int lo_pos, hi_pos, left, sinks;
+  // no query sees it: its row may hold anything
+  __device__ __forceinline__ bool nobody(int key) const {
+    return key > hi_pos || (key < lo_pos - left && key >= sinks);
+  }
+  // every query sees the tile from n0 on
+  __device__ __forceinline__ bool all(int n0) const {
+    return n0 + kPaTile - 1 <= lo_pos && (n0 >= hi_pos - left || n0 + kPaTile <= sinks);
+  }
+  // no query sees a key of the tile
+  __device__ __forceinline__ bool nothing(int n0) const {
+    return n0 > hi_pos || (n0 + kPaTile - 1 < lo_pos - left && n0 >= sinks);
+  }
+  __device__ __forceinline__ bool hidden(int key, int pos) const {
+    return key > pos || (key < pos - left && key >= sinks);
+  }
+};
+
+// A CTA's share of the steps of all items, KV-head groups innermost.
+struct PaShare {
+  int64_t begin, end;  // steps
+  int64_t at;          // the first step of the item that holds `begin`
+  int item, group;
+};
+
+template <int kRowsTile>
+__device__ __forceinline__ PaShare pa_share(const PagedProblem& p, int* count, int* sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // the running count of the items' steps, a run of items to a thread
+  const int run = (p.items + kPaThreads - 1) / kPaThreads;
+  const int i0 = min(static_cast<int>(threadIdx.x) * run, p.items), i1 = min(i0 + run, p.items);
+  int mine = 0;
+  for (int i = i0; i < i1; ++i) {
+    count[i] = mine;
+    mine += pa_span(p, i / p.tiles, i % p.tiles, kRowsTile).n;
+  }
+  int scan = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kFull, scan, o);
+    if (lane >= o) scan += v;
+  }
+  if (lane == 31) sums[warp] = scan;
+  __syncthreads();
+  int before = scan - mine;
+  for (int w = 0; w < warp; ++w) before += sums[w];
+  for (int i = i0; i < i1; ++i) count[i] += before;
+  if (i0 < i1 && i1 == p.items) count[p.items] = before + mine;
+  __syncthreads();
+  const int64_t all = static_cast<int64_t>(count[p.items]) * p.groups;
+  int64_t per = (all + p.ctas - 1) / p.ctas;
+  per = max(per, static_cast<int64_t>(kPaLeast >> p.step_shift));
+  PaShare s{min(all, static_cast<int64_t>(blockIdx.x) * per), 0, 0, 0, 0};
+  s.end = min(all, s.begin + per);
+  if (blockIdx.x == 0) {
+    for (int i = threadIdx.x; i <= p.items; i += kPaThreads) p.count[i] = count[i];
+    if (threadIdx.x == 0) p.count[p.items + 1] = per;
+  }
+  if (s.begin < s.end) {  // the item that holds step `begin`
+    int lo = 0, hi = p.items - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (static_cast<int64_t>(count[mid]) * p.groups <= s.begin) lo = mid;
+      else hi = mid - 1;
+    }
+    s.item = lo;
+    const int n = count[lo + 1] - count[lo];
+    const int64_t first = static_cast<int64_t>(count[lo]) * p.groups;
+    s.group = static_cast<int>((s.begin - first) / n);
+    s.at = first + static_cast<int64_t>(s.group) * n;
+  }
+  return s;
 }
 
-// MMA row i of a 4-bit tile is key swap(i): with the lowest two bits swapped the
-// loads of V by pairs of keys meet no bank twice.
-__device__ __forceinline__ int swap01(int i) { return (i & ~3) | ((i & 1) << 1) | ((i >> 1) & 1); }
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
 
-template <int D, bool BF16, bool Q4, int NT>
-__global__ void __launch_bounds__(kPaThreads, PaCfg<D, Q4, NT>::kPerSm)
-    paged_attn_kernel(const PagedProblem p, const __grid_constant__ CUtensorMap tmK,
-                      const __grid_constant__ CUtensorMap tmV) {
-  using C = PaCfg<D, Q4, NT>;
-  constexpr int kRowsTile = 8 * NT;
-  constexpr int KS = D / 16;  // k steps of S
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* const gbase = smem_raw + (base - raw);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = lane >> 2, c = lane & 3;
-  int* const count = reinterpret_cast<int*>(gbase + C::kOffCount);
-  int* const keys = reinterpret_cast<int*>(gbase + C::kOffKey) + warp * C::kStages;
-  const uint32_t bars = base + C::kOffBar + warp * C::kStages * 8;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kPaWarps * C::kStages; ++i) mbar_init(base + C::kOffBar + 8 * i, 1);
-    fence_mbar_init();
-    tma_prefetch_desc(&tmK);
-    tma_prefetch_desc(&tmV);
-  }
-  // the share of this CTA: tiles [begin, end) of all items, KV heads innermost
-  int64_t begin = 0, end = 0, per = 0;
-  int item = 0, head = 0;  // (sequence, row tile), KV head
-  int64_t at = 0;          // the item's first tile
-  if (p.cut) {
-    // the running count of the items' tiles, a run of items to a thread
-    int* const sums = reinterpret_cast<int*>(gbase + C::kOffStat);
-    const int run = (p.items + kPaThreads - 1) / kPaThreads;
-    const int i0 = min(static_cast<int>(threadIdx.x) * run, p.items), i1 = min(i0 + run, p.items);
-    int mine = 0;
-    for (int i = i0; i < i1; ++i) {
-      count[i] = mine;
-      mine += pa_span(p, i / p.tiles, i % p.tiles, kRowsTile).n;
-    }
-    int scan = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(kFull, scan, o);
-      if (lane >= o) scan += v;
-    }
-    if (lane == 31) sums[warp] = scan;
-    __syncthreads();
-    int before = scan - mine;
-    for (int w = 0; w < warp; ++w) before += sums[w];
-    for (int i = i0; i < i1; ++i) count[i] += before;
-    if (i0 < i1 && i1 == p.items) count[p.items] = before + mine;
-    __syncthreads();
-    const int64_t all = static_cast<int64_t>(count[p.items]) * p.G;
-    per = (all + p.ctas - 1) / p.ctas;
-    if (per < kPaLeast) per = kPaLeast;
-    begin = min(all, static_cast<int64_t>(blockIdx.x) * per);
-    end = min(all, begin + per);
-    if (blockIdx.x == 0) {
-      for (int i = threadIdx.x; i <= p.items; i += kPaThreads) p.count[i] = count[i];
-      if (threadIdx.x == 0) p.count[p.items + 1] = per;
-    }
-    if (begin < end) {  // the item that holds tile `begin`
-      int lo = 0, hi = p.items - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (static_cast<int64_t>(count[mid]) * p.G <= begin) lo = mid;
-        else hi = mid - 1;
-      }
-      item = lo;
-      const int n = count[item + 1] - count[item];
-      head = static_cast<int>((begin - static_cast<int64_t>(count[item]) * p.G) / n);
-      at = static_cast<int64_t>(count[item]) * p.G + static_cast<int64_t>(head) * n;
-    }
-  } else {
-    item = blockIdx.x / p.G;
-    head = blockIdx.x - item * p.G;
-    __syncthreads();
-  }
-  const uint64_t policy = p.tiles > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
-  bool failed = false;
-  uint32_t issued = 0, done = 0;  // tiles of this warp, over all items
-  for (bool more = !p.cut || begin < end; more;) {
-    const int b = item / p.tiles, rt = item - b * p.tiles;
-    const PaSpan sp = pa_span(p, b, rt, kRowsTile);
-    const int t0 = p.cut ? static_cast<int>(max(begin - at, static_cast<int64_t>(0))) : 0;
-    const int t1 = p.cut ? static_cast<int>(min(end - at, static_cast<int64_t>(sp.n))) : sp.n;
+// The state of one warp's rows: column 2 c + j of n-tile nt belongs to lanes of
+// c = lane % 4; rows of O^T to lane / 4.
+template <int D, int NT>
+struct PaRows {
+  float acc[NT][D / 16][4];
+  float ref[NT][2], neg[NT][2], l[NT][2];
+  float base_v[NT][2];  // 4 bits: sum of p (low + 8 step) - 8 p'
+  int pos[NT][2];
 
-    // ---- this warp's tiles t0 + warp, + kPaWarps, ...: pages of 32 at a time
-    int ahead = t0 + warp, left_in = 0, page_id = -1;
-    auto issue = [&]() -> bool {  // the next tile that has a page, into its slot
-      for (;;) {
-        if (ahead >= t1) return false;
-        if (left_in == 0) {
-          const int t = ahead + lane * kPaWarps;
-          page_id = -1;
-          if (t < t1) {
-            const int64_t key = static_cast<int64_t>(t < sp.st ? t : t + sp.jump) * kPaTile;
-            page_id = page_of(p.c, b, key);
-          }
-          left_in = 32;
-        }
-        const int page = __shfl_sync(kFull, page_id, 32 - left_in);
-        const int t = ahead;
-        ahead += kPaWarps;
-        --left_in;
-        if (page < 0) continue;
-        const int key = (t < sp.st ? t : t + sp.jump) * kPaTile;
-        if (lane == 0) {
-          const int s = issued % C::kStages;
-          const uint32_t bar = bars + 8 * s;
-          const uint32_t dst = base + (warp * C::kStages + s) * C::kSlot;
-          const int off = key & ((1 << p.c.shift) - 1);
-          keys[s] = key;
-          mbar_arrive_expect_tx(bar, C::kBytes);
-          if constexpr (Q4) {
-            tma_load_4d(dst, &tmK, bar, 0, head, off, page, policy);
-            tma_load_4d(dst + C::kKv, &tmV, bar, 0, head, off, page, policy);
-            const uint32_t sc = base + C::kOffScale + (warp * C::kStages + s) * C::kScales;
-            const int64_t so = ((page * static_cast<int64_t>(p.G) + head) << p.c.shift) + off;
-            bulk_load(sc, p.c.ks + so, kPaTile * 4, bar);
-            bulk_load(sc + kPaTile * 4, p.c.vs + so, kPaTile * 4, bar);
-          } else {
-#pragma unroll
-            for (int a = 0; a < D / 64; ++a) {
-              tma_load_4d(dst + a * kBoxBytes, &tmK, bar, a * 64, head, off, page, policy);
-              tma_load_4d(dst + C::kKv + a * kBoxBytes, &tmV, bar, a * 64, head, off, page, policy);
-            }
-          }
-        }
-        ++issued;
-        return true;
-      }
-    };
-    if (!failed) {
-      for (int s = 0; s < C::kStages; ++s)
-        if (!issue()) break;
-    }
-
-    // ---- the rows: Q as B operand, and the positions of this lane's columns
-    uint32_t qf[NT][KS][2];
-    int col_pos[NT][2];
-    float ka[NT][2], kb[NT][2];  // 4 bits: x = step dot ka + low kb
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int row = rt * kRowsTile + nt * 8 + r;
-      const int m = row / p.hpg;
-      const bool in = row < p.rows;
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(
-          p.q + 2 * (b * p.qb + m * p.qm + (head * p.hpg + row - m * p.hpg) * p.qh));
-      if constexpr (!Q4) {
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          qf[nt][k][0] = in ? src[8 * k + c] : 0u;
-          qf[nt][k][1] = in ? src[8 * k + 4 + c] : 0u;
-        }
-      } else {
-        // this lane's D / 4 entries, from (D / 4) c on
-        constexpr int W = D / 32;  // words of a row of codes that a lane holds
-        uint4 v[W];
-        float top = 0.f;
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-          v[j] = in ? reinterpret_cast<const uint4*>(src)[c * W + j] : make_uint4(0, 0, 0, 0);
-          const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            top = fmaxf(top, fmaxf(fabsf(half_of<BF16>(u[i], 0)), fabsf(half_of<BF16>(u[i], 1))));
-        }
-        top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
-        // 2^e: the largest entry between 2^13 and 2^14 (a row that is not
-        // finite, or zero, as it is)
-        int e = 0;
-        if (top > 0.f && top < INFINITY)
-          e = min(13 - (static_cast<int>(__float_as_uint(top) >> 23) - 127), 100);
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-          const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-          float f[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            f[i] = __half2float(__float2half_rn(half_of<BF16>(u[i >> 1], i & 1) * up));
-            sum += f[i];
-          }
-          // entries (0, 4), (1, 5) / 16 and (2, 6), (3, 7) / 16: the order of
-          // the codes under the masks
-          constexpr float k16 = 1.f / 16.f;
-          qf[nt][2 * j][0] = pack_half2(f[0], f[4]);
-          qf[nt][2 * j][1] = pack_half2(f[1] * k16, f[5] * k16);
-          qf[nt][2 * j + 1][0] = pack_half2(f[2], f[6]);
-          qf[nt][2 * j + 1][1] = pack_half2(f[3] * k16, f[7] * k16);
-        }
-        sum += __shfl_xor_sync(kFull, sum, 1);
-        sum += __shfl_xor_sync(kFull, sum, 2);
-        const float back = p.sl2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float f = __shfl_sync(kFull, back, 4 * (2 * c + j));
-          ka[nt][j] = f * 16777216.f;
-          kb[nt][j] = f * __shfl_sync(kFull, sum, 4 * (2 * c + j));
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int rw = rt * kRowsTile + nt * 8 + 2 * c + j;
-        col_pos[nt][j] = rw < p.rows ? __ldg(p.pos + b * p.pos_b + rw / p.hpg) : -1;
-      }
-    }
-    float acc[NT][KS][4];
-    float ref[NT][2], neg[NT][2], l[NT][2], base_v[NT][2];  // base_v: sum of p low
+  __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int i = 0; i < KS; ++i)
+      for (int i = 0; i < D / 16; ++i)
         acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -355,249 +256,588 @@ __global__ void __launch_bounds__(kPaThreads, PaCfg<D, Q4, NT>::kPerSm)
         neg[nt][j] = l[nt][j] = base_v[nt][j] = 0.f;
       }
     }
-    const int in_lo = sp.hi_pos - p.left;  // keys in [in_lo, lo_pos] are seen by every row
+  }
 
-    while (!failed && done != issued) {
-      const int s = done % C::kStages;
-      if (!__all_sync(kFull, wait_phase(bars + 8 * s, (done / C::kStages) & 1, kWaitLimitNs))) {
-        failed = true;
-        break;
+  // Moves the references that an element of x exceeds by more than the slack.
+  template <int TILES>
+  __device__ __forceinline__ void follow(const float (&x)[TILES][NT][4]) {
+    float top[NT][2];
+    bool move = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        top[nt][j] = fmaxf(x[0][nt][j], x[0][nt][j + 2]);
+#pragma unroll
+        for (int u = 1; u < TILES; ++u)
+          top[nt][j] = fmaxf(top[nt][j], fmaxf(x[u][nt][j], x[u][nt][j + 2]));
+        move = move || top[nt][j] > ref[nt][j] + kPaSlack;
       }
-      const int n0 = keys[s];
-      const uint32_t slot = base + (warp * C::kStages + s) * C::kSlot;
-      // this lane's two keys: rows r and r + 8 of S^T
-      const int key0 = n0 + (Q4 ? swap01(r) : r);
-      auto tile = [&](auto edge_c) {
-        constexpr bool EDGE = decltype(edge_c)::value;
-        [[maybe_unused]] uint32_t ksc[2], vsc[2];  // (step, low) of the two keys
-        if constexpr (Q4) {
-          const uint32_t* sc =
-              reinterpret_cast<const uint32_t*>(gbase + C::kOffScale +
-                                                (warp * C::kStages + s) * C::kScales) + (key0 - n0);
-          ksc[0] = sc[0], ksc[1] = sc[8], vsc[0] = sc[kPaTile], vsc[1] = sc[kPaTile + 8];
+    if (!__any_sync(kFull, move)) return;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float mx = top[nt][j];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+        if (mx > ref[nt][j] + kPaSlack) {  // (alike in the lanes of a column)
+          const float f = ex2(ref[nt][j] - mx);  // 0 while nothing was seen
+          l[nt][j] *= f;
+          base_v[nt][j] *= f;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            acc[nt][i][j] *= f;
+            acc[nt][i][j + 2] *= f;
+          }
+          ref[nt][j] = mx;
+          neg[nt][j] = -mx;
         }
-        if constexpr (EDGE) {
-          // rows that no query sees may hold anything: V's (or the scales) as zeros
-          auto nobody = [&](int key) {
-            return key > sp.hi_pos || (key < sp.lo_pos - p.left && key >= p.sinks);
-          };
-          if constexpr (Q4) {
+      }
+    }
+  }
+};
+
+// ---- 16 bits -----------------------------------------------------------
+
+// One tile of the ring: S^T, the softmax step and O^T. EDGE: some query does not
+// see some key of it.
+template <int D, bool BF16, int NT, bool EDGE>
+__device__ __forceinline__ void pa_tile16(PaRows<D, NT>& a, const uint32_t (&qf)[NT][D / 16][2],
+                                          uint32_t slot, int n0, const PaSight& see, float sl2) {
+  constexpr int KS = D / 16;
+  const int lane = threadIdx.x & 31, r = lane >> 2;
+  const uint32_t vt = slot + kPaTile * 2 * D;
+  if constexpr (EDGE) {
+    // V rows that no query sees may hold anything: they become zeros
+    for (int i = lane; i < kPaTile * (D / 8); i += 32) {
+      const int row = i / (D / 8), ch = i % (D / 8);
+      if (see.nobody(n0 + row))
+        st_shared_zero16(vt + (ch >> 3) * kBoxBytes + row * 128 + (ch & 7) * 16);
+    }
+    fence_proxy_async_smem();  // (before the slot's next copy)
+    __syncwarp();
+  }
+  float sc[NT][2][4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-              if (nobody(key0 + 8 * j)) ksc[j] = vsc[j] = 0u;
-          } else {
-            for (int i = lane; i < kPaTile * (D / 8); i += 32) {
-              const int row = i / (D / 8), ch = i % (D / 8);
-              if (nobody(n0 + row))
-                st_shared_zero16(slot + C::kKv + (ch >> 3) * kBoxBytes + row * 128 + (ch & 7) * 16);
-            }
-            fence_proxy_async_smem();  // (before the slot's next copy)
-            __syncwarp();
-          }
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sc[nt][0][i] = sc[nt][1][i] = 0.f;
+  const int krow = (lane & 7) + (lane & 8);
+#pragma unroll
+  for (int k = 0; k < KS; ++k) {
+    const int ch = 2 * k + (lane >> 4);
+    uint32_t a0, a1, a2, a3;
+    ldsm_x4(slot + (ch >> 3) * kBoxBytes + krow * 128 + (((ch & 7) ^ (krow & 7)) << 4), a0, a1, a2,
+            a3);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      mma_16816_t<BF16>(sc[nt][k & 1], a0, a1, a2, a3, qf[nt][k][0], qf[nt][k][1]);
+  }
+  // element i: key n0 + r + 8 (i / 2), column 2 c + i % 2
+  float x[1][NT][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[0][nt][i] = (sc[nt][0][i] + sc[nt][1][i]) * sl2;
+      if (EDGE && see.hidden(n0 + r + 8 * (i >> 1), a.pos[nt][i & 1])) x[0][nt][i] = -INFINITY;
+    }
+  a.follow(x);
+  uint32_t pf[NT][2];  // P^T as B operand
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float e[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      e[i] = ex2(x[0][nt][i] + a.neg[nt][i & 1]);
+      a.l[nt][i & 1] += e[i];
+    }
+    pf[nt][0] = movmatrix_t(pack2_t<BF16>(e[0], e[1]));
+    pf[nt][1] = movmatrix_t(pack2_t<BF16>(e[2], e[3]));
+  }
+  const int vrow = (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+  for (int i = 0; i < KS; ++i) {
+    const int ch = 2 * i + ((lane >> 3) & 1);
+    uint32_t a0, a1, a2, a3;
+    ldsm_x4_t(vt + (ch >> 3) * kBoxBytes + vrow * 128 + (((ch & 7) ^ (vrow & 7)) << 4), a0, a1, a2,
+              a3);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      mma_16816_t<BF16>(a.acc[nt][i], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+  }
+}
+
+// ---- 4 bits ------------------------------------------------------------
+
+// Key of MMA row i of a tile. Any order serves; in this one the 16- and 8-byte
+// loads of 128-byte swizzled rows meet no bank twice.
+__device__ __forceinline__ int pa_row4(int i) { return (i & 14) ^ (i & 1 ? 5 : 0); }
+
+// Where a lane's words of a tile lie in a slot: K's of rows r and r + 8 of S^T
+// (the c-th quarter of a row), V's for its rows 2 c, 2 c + 1, 2 c + 8, 2 c + 9 (the
+// r-th eighth of a row), and the scales of rows r and r + 8.
+struct PaLanes {
+  uint32_t k[2], v[4], scale;
+};
+
+// S^T of a tile as x in the log2 domain, with log2 of V's step; mid and rstep: V's
+// low + 8 step and 1 / step of the lane's two keys.
+template <int D, int NT, bool EDGE>
+__device__ __forceinline__ void pa_scores4(const PaRows<D, NT>& a, const uint8_t* kt,
+                                           const uint8_t* scales, const PaLanes& at, int n0,
+                                           const uint32_t (&qf)[NT][D / 16][2],
+                                           const float (&ka)[NT][2], const float (&kb)[NT][2],
+                                           const PaSight& see, float (&x)[NT][4], float (&mid)[2],
+                                           float (&rstep)[2]) {
+  constexpr int W = D / 32;
+  const int key = n0 + pa_row4((threadIdx.x & 31) >> 2);
+  float sc[NT][2][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sc[nt][0][i] = sc[nt][1][i] = 0.f;
+  uint32_t w[2][W];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    if constexpr (D == 128) {
+      const uint4 v = *reinterpret_cast<const uint4*>(kt + at.k[j]);
+      w[j][0] = v.x, w[j][1] = v.y, w[j][W - 2] = v.z, w[j][W - 1] = v.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(kt + at.k[j]);
+      w[j][0] = v.x, w[j][1] = v.y;
+    }
+  }
+  uint32_t ks[2], vs[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    ks[j] = *reinterpret_cast<const uint32_t*>(scales + at.scale + 32 * j);
+    vs[j] = *reinterpret_cast<const uint32_t*>(scales + kPaSlotRows * 4 + at.scale + 32 * j);
+    // keys that no query sees may hold anything
+    if (EDGE && see.nobody(key + 8 * j)) ks[j] = vs[j] = 0u;
+  }
+#pragma unroll
+  for (int j = 0; j < W; ++j) {
+    const uint32_t u = w[0][j], v = w[1][j], u8 = u >> 8, v8 = v >> 8;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      mma_16816(sc[nt][0], u & 0x000f000fu, v & 0x000f000fu, u & 0x00f000f0u, v & 0x00f000f0u,
+                qf[nt][2 * j][0], qf[nt][2 * j][1]);
+      mma_16816(sc[nt][1], u8 & 0x000f000fu, v8 & 0x000f000fu, u8 & 0x00f000f0u, v8 & 0x00f000f0u,
+                qf[nt][2 * j + 1][0], qf[nt][2 * j + 1][1]);
+    }
+  }
+  float kstep[2], klow[2], lstep[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    kstep[j] = __uint_as_float(ks[j] << 16);
+    klow[j] = __uint_as_float(ks[j] & 0xffff0000u);
+    const float step = __uint_as_float(vs[j] << 16);
+    mid[j] = fmaf(8.f, step, __uint_as_float(vs[j] & 0xffff0000u));
+    const float any = step == 0.f ? 1.f : step;  // (all codes are 0 then)
+    rstep[j] = rcp_approx(any);
+    lstep[j] = lg2_approx(any);
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[nt][i] = fmaf(kstep[i >> 1] * ka[nt][i & 1], sc[nt][0][i] + sc[nt][1][i],
+                      fmaf(klow[i >> 1], kb[nt][i & 1], lstep[i >> 1]));
+      if (EDGE && see.hidden(key + 8 * (i >> 1), a.pos[nt][i & 1])) x[nt][i] = -INFINITY;
+    }
+}
+
+// p' of a tile, its sums, and O^T.
+template <int D, int NT, bool EDGE>
+__device__ __forceinline__ void pa_values4(PaRows<D, NT>& a, const uint8_t* vt, const PaLanes& at,
+                                           int n0, const PaSight& see, const float (&x)[NT][4],
+                                           const float (&mid)[2], const float (&rstep)[2]) {
+  constexpr int W = D / 64;
+  const int key = n0 + pa_row4((threadIdx.x & 31) >> 2);
+  uint32_t w[4][W];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (D == 128) {
+      const uint2 v = *reinterpret_cast<const uint2*>(vt + at.v[j]);
+      w[j][0] = v.x, w[j][W - 1] = v.y;
+    } else {
+      w[j][0] = *reinterpret_cast<const uint32_t*>(vt + at.v[j]);
+    }
+  }
+  uint32_t pf[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float e[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e[i] = ex2(x[nt][i] + a.neg[nt][i & 1]);
+    const uint32_t p0 = pack_half2(e[0], e[1]), p1 = pack_half2(e[2], e[3]);
+    const float2 r0 = unpack2<false>(p0), r1 = unpack2<false>(p1);
+    const float rounded[4] = {r0.x, r0.y, r1.x, r1.y};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float md = mid[i >> 1], pr = e[i] * rstep[i >> 1];
+      if (EDGE && see.hidden(key + 8 * (i >> 1), a.pos[nt][i & 1])) md = pr = 0.f;
+      a.l[nt][i & 1] += pr;
+      a.base_v[nt][i & 1] = fmaf(rounded[i], -8.f, fmaf(pr, md, a.base_v[nt][i & 1]));
+    }
+    pf[nt][0] = movmatrix_t(p0);
+    pf[nt][1] = movmatrix_t(p1);
+  }
+#pragma unroll
+  for (int j = 0; j < W; ++j) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {  // entries 0..3, 4..7 of a word, two keys each
+      const uint32_t sel = half ? 0x7632u : 0x5410u;
+      const uint32_t u = __byte_perm(w[0][j], w[1][j], sel);
+      const uint32_t v = __byte_perm(w[2][j], w[3][j], sel);
+      const uint32_t u8 = u >> 8, v8 = v >> 8;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        mma_16816(a.acc[nt][4 * j + 2 * half], u & 0x000f000fu, u & 0x00f000f0u, v & 0x000f000fu,
+                  v & 0x00f000f0u, pf[nt][0], pf[nt][1]);
+        mma_16816(a.acc[nt][4 * j + 2 * half + 1], u8 & 0x000f000fu, u8 & 0x00f000f0u,
+                  v8 & 0x000f000fu, v8 & 0x00f000f0u, pf[nt][0], pf[nt][1]);
+      }
+    }
+  }
+}
+
+// A warp's 32 keys of a slot: two tiles, at once where the registers hold both.
+template <int D, int NT, bool EDGE>
+__device__ __forceinline__ void pa_step4(PaRows<D, NT>& a, const uint8_t* slot,
+                                         const uint8_t* scales, const PaLanes& at, int row_bytes,
+                                         const int (&n0)[2], const uint32_t (&qf)[NT][D / 16][2],
+                                         const float (&ka)[NT][2], const float (&kb)[NT][2],
+                                         const PaSight& see) {
+  constexpr int kTogether = NT == 1 ? 2 : 1;
+#pragma unroll
+  for (int u0 = 0; u0 < 2; u0 += kTogether) {
+    float x[kTogether][NT][4], mid[kTogether][2], rstep[kTogether][2];
+#pragma unroll
+    for (int u = 0; u < kTogether; ++u)
+      pa_scores4<D, NT, EDGE>(a, slot + (u0 + u) * kPaTile * row_bytes,
+                              scales + (u0 + u) * kPaTile * 4, at, n0[u0 + u], qf, ka, kb, see, x[u],
+                              mid[u], rstep[u]);
+    a.follow(x);
+#pragma unroll
+    for (int u = 0; u < kTogether; ++u)
+      pa_values4<D, NT, EDGE>(
+          a, slot + kPaSlotRows * (D / 2) + (u0 + u) * kPaTile * row_bytes, at, n0[u0 + u], see,
+          x[u], mid[u], rstep[u]);
+  }
+}
+
+// Q's rows of a row tile as B operands. 4 bits: scaled by 2^e into fp16, in the
+// order of the codes under the masks; x = step dot ka + low kb.
+template <int D, bool BF16, bool Q4, int NT>
+__device__ __forceinline__ void pa_queries(const PagedProblem& p, int b, int rt, int head,
+                                           uint32_t (&qf)[NT][D / 16][2], float (&ka)[NT][2],
+                                           float (&kb)[NT][2]) {
+  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int row = rt * 8 * NT + nt * 8 + r;
+    const int m = row / p.hpg;
+    const bool in = row < p.rows;
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(
+        p.q + 2 * (b * p.qb + m * p.qm + (head * p.hpg + row - m * p.hpg) * p.qh));
+    if constexpr (!Q4) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        qf[nt][k][0] = in ? src[8 * k + c] : 0u;
+        qf[nt][k][1] = in ? src[8 * k + 4 + c] : 0u;
+      }
+    } else {
+      constexpr int W = D / 32;  // words of codes, and 8 entries of q each, of this lane
+      uint4 v[W];
+      float top = 0.f;
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        v[j] = in ? reinterpret_cast<const uint4*>(src)[c * W + j] : make_uint4(0, 0, 0, 0);
+        float f[8];
+        unpack8<BF16>(v[j], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
+      }
+      top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+      // the largest entry between 2^13 and 2^14 (a row that is not finite, or
+      // zero, as it is)
+      int e = 0;
+      if (top > 0.f && top < INFINITY)
+        e = min(13 - (static_cast<int>(__float_as_uint(top) >> 23) - 127), 100);
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        float f[8];
+        unpack8<BF16>(v[j], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          f[i] = __half2float(__float2half_rn(f[i] * up));
+          sum += f[i];
         }
-        // S^T = K Q^T
-        float sc4[NT][2][4];
+        // entries (0, 4), (1, 5) / 16 and (2, 6), (3, 7) / 16
+        constexpr float k16 = 1.f / 16.f;
+        qf[nt][2 * j][0] = pack_half2(f[0], f[4]);
+        qf[nt][2 * j][1] = pack_half2(f[1] * k16, f[5] * k16);
+        qf[nt][2 * j + 1][0] = pack_half2(f[2], f[6]);
+        qf[nt][2 * j + 1][1] = pack_half2(f[3] * k16, f[7] * k16);
+      }
+      sum += __shfl_xor_sync(kFull, sum, 1);
+      sum += __shfl_xor_sync(kFull, sum, 2);
+      const float back = p.sl2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+      for (int j = 0; j < 2; ++j) {
+        const float f = __shfl_sync(kFull, back, 4 * (2 * c + j));
+        ka[nt][j] = f * 16777216.f;
+        kb[nt][j] = f * __shfl_sync(kFull, sum, 4 * (2 * c + j));
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ float pa_lse(float ref, float sum) {
+  return sum == 0.f ? -INFINITY : (ref + __log2f(sum)) * 0.69314718055994530942f;
+}
+
+template <int D, bool BF16, bool Q4, int NT>
+__global__ void __launch_bounds__(kPaThreads, PaCfg<D, Q4, NT>::kPerSm)
+    paged_attn_kernel(const PagedProblem p, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV) {
+  using C = PaCfg<D, Q4, NT>;
+  constexpr int kRowsTile = 8 * NT;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const gbase = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = lane >> 2, c = lane & 3;
+  int* const count = reinterpret_cast<int*>(gbase + C::kOffCount);
+  float* const stat = reinterpret_cast<float*>(gbase + C::kOffStat);
+  const int ring = Q4 ? 0 : warp;
+  int* const keys = reinterpret_cast<int*>(gbase + C::kOffKey) + ring * C::kStages * C::kKeys;
+  const uint32_t bars = base + C::kOffBar + ring * C::kStages * 16;  // full, then empty
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kRings; ++i)
+      for (int st = 0; st < C::kStages; ++st) {
+        const uint32_t bar = base + C::kOffBar + (2 * i * C::kStages + st) * 8;
+        mbar_init(bar, Q4 ? p.split : 1);
+        if (Q4) mbar_init(bar + C::kStages * 8, kPaWarps);
+      }
+    fence_mbar_init();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  PaShare sh{0, 0, 0, 0, 0};
+  if (p.cut) {
+    sh = pa_share<kRowsTile>(p, count, reinterpret_cast<int*>(stat));
+  } else {
+    sh.item = blockIdx.x / p.groups;
+    sh.group = blockIdx.x - sh.item * p.groups;
+    __syncthreads();
+  }
+  // the warps of a head, this one's place among them, and its head of the item
+  const int warps_head = kPaWarps / p.heads_item, warp_in = warp % warps_head;
+  const int head_in = warp / warps_head;
+  // (with several row tiles the keys are read again)
+  const uint64_t policy = p.tiles > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
+  [[maybe_unused]] PaLanes lanes{};
+  [[maybe_unused]] int row_bytes = 0;
+  if constexpr (Q4) {
+    // a row holds a token's codes of the item's heads: 128 or 64 bytes, swizzled
+    // by TMA, or 32
+    row_bytes = p.heads_item * (D / 2);
+    auto at = [&](int row, int byte) {
+      const uint32_t o = row * row_bytes + head_in * (D / 2) + byte;
+      const uint32_t swizzle = row_bytes == 128 ? 7u : row_bytes == 64 ? 3u : 0u;
+      return (o ^ ((o >> 7 & swizzle) << 4)) + static_cast<uint32_t>(warp_in * 32 * row_bytes);
+    };
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sc4[nt][0][i] = sc4[nt][1][i] = 0.f;
-        if constexpr (!Q4) {
-          const int krow = (lane & 7) + (lane & 8);
+    for (int j = 0; j < 2; ++j) lanes.k[j] = at(pa_row4(r) + 8 * j, c * (D / 8));
 #pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            const int ch = 2 * k + (lane >> 4);
-            uint32_t a0, a1, a2, a3;
-            ldsm_x4(slot + (ch >> 3) * kBoxBytes + krow * 128 + (((ch & 7) ^ (krow & 7)) << 4), a0,
-                    a1, a2, a3);
+    for (int j = 0; j < 4; ++j)
+      lanes.v[j] = at(pa_row4(2 * c + (j & 1)) + 8 * (j >> 1), r * (D / 16));
+    lanes.scale = 4 * ((head_in << p.step_shift) + warp_in * 32 + pa_row4(r));
+  }
+  bool failed = false;
+  uint32_t issued = 0, done = 0;  // slots of the ring, over all items
+  for (bool more = !p.cut || sh.begin < sh.end; more;) {
+    const int b = sh.item / p.tiles, rt = sh.item - b * p.tiles;
+    const int head = sh.group * p.heads_item + head_in;
+    const PaSpan sp = pa_span(p, b, rt, kRowsTile);
+    const int t0 = p.cut ? static_cast<int>(max(sh.begin - sh.at, static_cast<int64_t>(0))) : 0;
+    const int t1 =
+        p.cut ? static_cast<int>(min(sh.end - sh.at, static_cast<int64_t>(sp.n))) : sp.n;
+    const PaSight see{sp.lo_pos, sp.hi_pos, p.left, p.sinks};
+
+    const int in_page = (1 << p.c.shift) - 1;
+    PaRows<D, NT> a;
+    a.clear();
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_16816_t<BF16>(sc4[nt][k & 1], a0, a1, a2, a3, qf[nt][k][0], qf[nt][k][1]);
-          }
-        } else {
-          constexpr int W = D / 32;
-          uint32_t w[2][W];
-          const int row = key0 - n0;
-          if constexpr (D == 128) {
-            const uint32_t o = slot - base + row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
-            const uint4 x = *reinterpret_cast<const uint4*>(gbase + o);
-            const uint4 y = *reinterpret_cast<const uint4*>(gbase + o + 512);
-            w[0][0] = x.x, w[0][1] = x.y, w[0][2] = x.z, w[0][3] = x.w;
-            w[1][0] = y.x, w[1][1] = y.y, w[1][2] = y.z, w[1][3] = y.w;
-          } else {
-            const uint32_t o = slot - base + row * 32 + c * 8;
-            const uint2 x = *reinterpret_cast<const uint2*>(gbase + o);
-            const uint2 y = *reinterpret_cast<const uint2*>(gbase + o + 256);
-            w[0][0] = x.x, w[0][1] = x.y, w[1][0] = y.x, w[1][1] = y.y;
-          }
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < W; ++j) {
-            const uint32_t u = w[0][j], v = w[1][j], u8 = u >> 8, v8 = v >> 8;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma_16816(sc4[nt][0], u & 0x000f000fu, v & 0x000f000fu, u & 0x00f000f0u,
-                        v & 0x00f000f0u, qf[nt][2 * j][0], qf[nt][2 * j][1]);
-              mma_16816(sc4[nt][1], u8 & 0x000f000fu, v8 & 0x000f000fu, u8 & 0x00f000f0u,
-                        v8 & 0x00f000f0u, qf[nt][2 * j + 1][0], qf[nt][2 * j + 1][1]);
-            }
-          }
-        }
-        // x in the log2 domain; element i: key key0 + 8 (i / 2), column 2 c + i % 2
-        float x[NT][4];
-        [[maybe_unused]] float rstep[2], lstep[2], lowv[2];
-        if constexpr (Q4) {
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float step = __uint_as_float(vsc[j] << 16);
-            lowv[j] = __uint_as_float(vsc[j] & 0xffff0000u);
-            const bool none = step == 0.f;  // all codes are 0: any step serves
-            rstep[j] = none ? 1.f : __frcp_rn(step);
-            lstep[j] = none ? 0.f : __log2f(step);
-          }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float dot = sc4[nt][0][i] + sc4[nt][1][i];
-            if constexpr (Q4) {
-              const float step = __uint_as_float(ksc[i >> 1] << 16);
-              const float low = __uint_as_float(ksc[i >> 1] & 0xffff0000u);
-              x[nt][i] = fmaf(step * ka[nt][i & 1], dot, fmaf(low, kb[nt][i & 1], lstep[i >> 1]));
-            } else {
-              x[nt][i] = dot * p.sl2;
-            }
-            if constexpr (EDGE) {
-              const int key = key0 + 8 * (i >> 1), q = col_pos[nt][i & 1];
-              if (key > q || (key < q - p.left && key >= p.sinks)) x[nt][i] = -INFINITY;
-            }
-          }
-        }
-        // the reference moves when an element exceeds it by more than the slack
-        bool move = false;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            move = move || fmaxf(x[nt][j], x[nt][j + 2]) > ref[nt][j] + kPaSlack;
-        if (__any_sync(kFull, move)) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float mx = fmaxf(x[nt][j], x[nt][j + 2]);
-#pragma unroll
-              for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-              if (mx > ref[nt][j] + kPaSlack) {  // (alike in the lanes of a column)
-                const float f = ex2(ref[nt][j] - mx);  // 0 while nothing was seen
-                l[nt][j] *= f;
-                base_v[nt][j] *= f;
-#pragma unroll
-                for (int i = 0; i < KS; ++i) {
-                  acc[nt][i][j] *= f;
-                  acc[nt][i][j + 2] *= f;
-                }
-                ref[nt][j] = mx;
-                neg[nt][j] = -mx;
-              }
-            }
-          }
-        }
-        uint32_t pf[NT][2];  // P^T as B operand
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float e[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            e[i] = ex2(x[nt][i] + neg[nt][i & 1]);
-            if constexpr (Q4) {
-              float pr = e[i] * rstep[i >> 1], lw = lowv[i >> 1];
-              if constexpr (EDGE) {
-                const int key = key0 + 8 * (i >> 1), q = col_pos[nt][i & 1];
-                if (key > q || (key < q - p.left && key >= p.sinks)) pr = lw = 0.f;
-              }
-              l[nt][i & 1] += pr;
-              base_v[nt][i & 1] = fmaf(pr, lw, base_v[nt][i & 1]);
-            } else {
-              l[nt][i & 1] += e[i];
-            }
-          }
-          pf[nt][0] = movmatrix_t(pack2_t<BF16 && !Q4>(e[0], e[1]));
-          pf[nt][1] = movmatrix_t(pack2_t<BF16 && !Q4>(e[2], e[3]));
-        }
-        // O^T += V^T P^T
-        if constexpr (!Q4) {
-          const int vrow = (lane & 7) + ((lane >> 4) << 3);
-#pragma unroll
-          for (int i = 0; i < KS; ++i) {
-            const int ch = 2 * i + ((lane >> 3) & 1);
-            uint32_t a0, a1, a2, a3;
-            ldsm_x4_t(slot + C::kKv + (ch >> 3) * kBoxBytes + vrow * 128 +
-                          (((ch & 7) ^ (vrow & 7)) << 4),
-                      a0, a1, a2, a3);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_16816_t<BF16>(acc[nt][i], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
-          }
-        } else {
-          // keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9 of S^T's rows; words W r .. of each
-          constexpr int W = D / 64;
-          uint32_t w[4][W];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int row = swap01(2 * c + (j & 1)) + 8 * (j >> 1);
-            if constexpr (D == 128) {
-              const uint32_t o = slot - base + C::kKv + row * 64 +
-                                 (((r >> 1) ^ ((row >> 1) & 3)) << 4) + (r & 1) * 8;
-              const uint2 v = *reinterpret_cast<const uint2*>(gbase + o);
-              w[j][0] = v.x;
-              w[j][W - 1] = v.y;
-            } else {
-              w[j][0] = *reinterpret_cast<const uint32_t*>(gbase + (slot - base) + C::kKv +
-                                                           row * 32 + r * 4);
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < W; ++j) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {  // entries 0..3, 4..7 of the word
-              const uint32_t sel = half ? 0x7632u : 0x5410u;
-              const uint32_t u = __byte_perm(w[0][j], w[1][j], sel);
-              const uint32_t v = __byte_perm(w[2][j], w[3][j], sel);
-              const uint32_t u8 = u >> 8, v8 = v >> 8;
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                mma_16816(acc[nt][4 * j + 2 * half], u & 0x000f000fu, u & 0x00f000f0u,
-                          v & 0x000f000fu, v & 0x00f000f0u, pf[nt][0], pf[nt][1]);
-                mma_16816(acc[nt][4 * j + 2 * half + 1], u8 & 0x000f000fu, u8 & 0x00f000f0u,
-                          v8 & 0x000f000fu, v8 & 0x00f000f0u, pf[nt][0], pf[nt][1]);
-              }
-            }
-          }
+      for (int j = 0; j < 2; ++j) {
+        const int rw = rt * kRowsTile + nt * 8 + 2 * c + j;
+        a.pos[nt][j] = rw < p.rows ? pa_position(p, b, rw / p.hpg) : -1;
+      }
+    uint32_t qf[NT][D / 16][2];
+    float ka[NT][2], kb[NT][2];
+
+    if constexpr (Q4) {
+      // The warps issue the item's steps in turn: step t is warp t % 4's. Lane j
+      // of a window of 32 holds where the j-th copy of this warp's steps lies
+      // (`split` to a step), looked up one window ahead, and issues it.
+      const int steps = t1 - t0;
+      const int split_shift = __ffs(p.split) - 1;
+      const int rows = 1 << (p.step_shift - split_shift);  // tokens of a copy
+      int key_l = -1, page_l = -1, key_next = -1, page_next = -1;
+      auto look = [&](int j) {
+        const int t = (j >> split_shift) * kPaWarps + warp, part = j & (p.split - 1);
+        page_next = -1;
+        if (t < steps) {
+          key_next = sp.key(t0 + t) + part * rows;
+          page_next = page_of(p.c, b, key_next);
         }
       };
-      const int n1 = n0 + kPaTile - 1;
-      if (n1 <= sp.lo_pos && (n0 >= in_lo || n1 < p.sinks))
-        tile(std::false_type{});
-      else
-        tile(std::true_type{});
-      __syncwarp();  // the slot has been read
-      ++done;
-      issue();
+      auto issue = [&](int t) {  // (t % 4 = warp: this warp's turn)
+        const uint32_t g = issued + t;  // of the ring
+        const int s = g % C::kStages;
+        const uint32_t bar = bars + 8 * s;
+        // the step that had the slot has been read by all warps
+        if (g >= C::kStages &&
+            !__all_sync(kFull, wait_phase(bar + 8 * C::kStages, (g / C::kStages - 1) & 1,
+                                          kWaitLimitNs))) {
+          failed = true;
+          return;
+        }
+        const int e = (t / kPaWarps << split_shift) & 31;
+        if (e == 0) {
+          key_l = key_next;
+          page_l = page_next;
+          look((t / kPaWarps << split_shift) + 32 + lane);
+        }
+        if (lane >= e && lane < e + p.split) {
+          const int first = (lane - e) * rows;  // of the copy's rows, in the step
+          for (int i = 0; i < rows; i += kPaTile)
+            keys[s * C::kKeys + (first + i) / kPaTile] = page_l < 0 ? -1 : key_l + i;
+          if (page_l < 0) {
+            mbar_arrive(bar);  // a page that is not there
+          } else {
+            const int off = key_l & in_page, h0 = sh.group * p.heads_item;
+            const uint32_t dst = base + s * C::kSlot;
+            mbar_arrive_expect_tx(bar, 2 * p.heads_item * rows * (D / 2 + 4));
+            tma_load_4d(dst + first * row_bytes, &tmK, bar, h0 * (D / 2), off, page_l, 0, policy);
+            tma_load_4d(dst + C::kKv + first * row_bytes, &tmV, bar, h0 * (D / 2), off, page_l, 0,
+                        policy);
+            for (int h = 0; h < p.heads_item; ++h) {
+              const int64_t so =
+                  ((page_l * static_cast<int64_t>(p.G) + h0 + h) << p.c.shift) + off;
+              const uint32_t sc = dst + 2 * C::kKv + 4 * ((h << p.step_shift) + first);
+              bulk_load(sc, p.c.ks + so, rows * 4, bar);
+              bulk_load(sc + C::kScales, p.c.vs + so, rows * 4, bar);
+            }
+          }
+        }
+        __syncwarp();
+      };
+      look(lane);
+      for (int t = 0; t < C::kStages - 1 && t < steps && !failed; ++t)
+        if (t % kPaWarps == warp) issue(t);
+      pa_queries<D, BF16, true, NT>(p, b, rt, head, qf, ka, kb);
+      for (int t = 0; t < steps && !failed; ++t) {
+        const uint32_t g = issued + t;
+        const int s = g % C::kStages;
+        if (!__all_sync(kFull, wait_phase(bars + 8 * s, (g / C::kStages) & 1, kWaitLimitNs))) {
+          failed = true;
+          break;
+        }
+        const int k0 = s * C::kKeys + 2 * warp_in;
+        const int n0[2] = {keys[k0], keys[k0 + 1]};
+        const uint8_t* const slot = gbase + s * C::kSlot;
+        const uint8_t* const scales = slot + 2 * C::kKv;
+        if (n0[0] >= 0 && n0[1] >= 0 && see.all(n0[0]) && see.all(n0[1])) {
+          pa_step4<D, NT, false>(a, slot, scales, lanes, row_bytes, n0, qf, ka, kb, see);
+        } else if (n0[0] >= 0 || n0[1] >= 0) {
+          const int n1[2] = {n0[0] < 0 ? kNoKey : n0[0], n0[1] < 0 ? kNoKey : n0[1]};
+          if (!see.nothing(n1[0]) || !see.nothing(n1[1]))
+            pa_step4<D, NT, true>(a, slot, scales, lanes, row_bytes, n1, qf, ka, kb, see);
+        }
+        __syncwarp();  // the slot has been read
+        if (lane == 0) mbar_arrive(bars + 8 * (C::kStages + s));
+        const int next = t + C::kStages - 1;
+        if (next < steps && next % kPaWarps == warp) issue(next);
+      }
+      issued += steps;
+    } else {
+      // This warp's tiles are t0 + warp_in + warps_head k. Lane j of a window of
+      // 32 holds the page of the j-th, looked up one window ahead.
+      int tile_k = 0, page_l = -1, page_next = -1;
+      auto look = [&](int k) {
+        const int t = t0 + warp_in + warps_head * k;
+        page_next = t < t1 ? page_of(p.c, b, sp.key(t)) : -1;
+      };
+      look(lane);
+      auto issue = [&]() {  // the next tile that has a page, into its slot
+        int key = -1, page = -1;
+        for (int t; page < 0 && (t = t0 + warp_in + warps_head * tile_k) < t1; ++tile_k) {
+          if ((tile_k & 31) == 0) {
+            page_l = page_next;
+            look(tile_k + 32 + lane);
+          }
+          page = __shfl_sync(kFull, page_l, tile_k & 31);
+          key = sp.key(t);
+        }
+        if (page < 0) return;
+        if (lane == 0) {
+          const int s = issued % C::kStages, off = key & in_page;
+          const uint32_t bar = bars + 8 * s;
+          const uint32_t dst = base + (warp * C::kStages + s) * C::kSlot;
+          keys[s] = key;
+          mbar_arrive_expect_tx(bar, C::kSlot);
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i) {
+            tma_load_4d(dst + i * kBoxBytes, &tmK, bar, i * 64, head, off, page, policy);
+            tma_load_4d(dst + C::kKv + i * kBoxBytes, &tmV, bar, i * 64, head, off, page, policy);
+          }
+        }
+        ++issued;
+      };
+      if (!failed)
+        for (int s = 0; s < C::kStages; ++s) issue();
+      pa_queries<D, BF16, false, NT>(p, b, rt, head, qf, ka, kb);
+      while (!failed && done != issued) {
+        const int s = done % C::kStages;
+        if (!__all_sync(kFull, wait_phase(bars + 8 * s, (done / C::kStages) & 1, kWaitLimitNs))) {
+          failed = true;
+          break;
+        }
+        const int n0 = keys[s];
+        const uint32_t slot = base + (warp * C::kStages + s) * C::kSlot;
+        if (see.all(n0))
+          pa_tile16<D, BF16, NT, false>(a, qf, slot, n0, see, p.sl2);
+        else
+          pa_tile16<D, BF16, NT, true>(a, qf, slot, n0, see, p.sl2);
+        __syncwarp();  // the slot has been read
+        ++done;
+        issue();
+      }
     }
 
-    // ---- the four warps' results, joined in shared memory
+    // ---- the warps' results, joined in shared memory
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
-          l[nt][j] += __shfl_xor_sync(kFull, l[nt][j], o);
-          base_v[nt][j] += __shfl_xor_sync(kFull, base_v[nt][j], o);
+          a.l[nt][j] += __shfl_xor_sync(kFull, a.l[nt][j], o);
+          a.base_v[nt][j] += __shfl_xor_sync(kFull, a.base_v[nt][j], o);
         }
     __syncthreads();  // every warp is done with the ring
     float* const joined = reinterpret_cast<float*>(gbase);
-    float* const stat = reinterpret_cast<float*>(gbase + C::kOffStat);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -605,21 +845,21 @@ __global__ void __launch_bounds__(kPaThreads, PaCfg<D, Q4, NT>::kPerSm)
         const int row = nt * 8 + 2 * c + j;
         float* const dst = joined + (warp * kRowsTile + row) * C::kPad;
 #pragma unroll
-        for (int i = 0; i < KS; ++i) {
+        for (int i = 0; i < D / 16; ++i) {
           if constexpr (Q4) {
-            // words W r + i / 4 of a row, entries 2 (i % 4) and the one after,
-            // which the mask left 16 times as large
+            // word D / 64 r + i / 4 of a row, entries 2 (i % 4) and the one
+            // after, which the mask left 16 times as large
             const int d = 8 * (D / 64 * r + (i >> 2)) + 2 * (i & 3);
-            dst[d] = fmaf(acc[nt][i][j], 16777216.f, base_v[nt][j]);
-            dst[d + 1] = fmaf(acc[nt][i][j + 2], 1048576.f, base_v[nt][j]);
+            dst[d] = fmaf(a.acc[nt][i][j], 16777216.f, a.base_v[nt][j]);
+            dst[d + 1] = fmaf(a.acc[nt][i][j + 2], 1048576.f, a.base_v[nt][j]);
           } else {
-            dst[16 * i + r] = acc[nt][i][j];
-            dst[16 * i + r + 8] = acc[nt][i][j + 2];
+            dst[16 * i + r] = a.acc[nt][i][j];
+            dst[16 * i + r + 8] = a.acc[nt][i][j + 2];
           }
         }
         if (r == 0) {
-          stat[2 * (warp * kRowsTile + row)] = ref[nt][j];
-          stat[2 * (warp * kRowsTile + row) + 1] = l[nt][j];
+          stat[2 * (warp * kRowsTile + row)] = a.ref[nt][j];
+          stat[2 * (warp * kRowsTile + row) + 1] = a.l[nt][j];
         }
       }
     __syncthreads();
@@ -627,18 +867,19 @@ __global__ void __launch_bounds__(kPaThreads, PaCfg<D, Q4, NT>::kPerSm)
     // a piece of an item that begins in this share: slot 2 CTA + 1; that
     // goes on from an earlier one: 2 CTA
     const int64_t slot_id = 2 * static_cast<int64_t>(blockIdx.x) + (t0 == 0 ? 1 : 0);
-    for (int i = threadIdx.x; i < kRowsTile * (D / 2); i += kPaThreads) {
-      const int row = i / (D / 2), d = 2 * (i % (D / 2));
+    const int piece_rows = p.heads_item * kRowsTile;
+    for (int i = threadIdx.x; i < piece_rows * (D / 2); i += kPaThreads) {
+      const int prow = i / (D / 2), d = 2 * (i % (D / 2));
+      const int hd = prow / kRowsTile, row = prow % kRowsTile;  // head of the item, row
       const int rw = rt * kRowsTile + row;
       if (rw >= p.rows) continue;
+      const int w0 = hd * warps_head, w1 = w0 + warps_head;
       float m = -INFINITY, sum = 0.f, o0 = 0.f, o1 = 0.f;
-#pragma unroll
-      for (int w = 0; w < kPaWarps; ++w) m = fmaxf(m, stat[2 * (w * kRowsTile + row)]);
-#pragma unroll
-      for (int w = 0; w < kPaWarps; ++w) {
-        const float rw_ref = stat[2 * (w * kRowsTile + row)];
+      for (int w = w0; w < w1; ++w) m = fmaxf(m, stat[2 * (w * kRowsTile + row)]);
+      for (int w = w0; w < w1; ++w) {
+        const float ref = stat[2 * (w * kRowsTile + row)];
         // (a warp that saw nothing has a sum of 0, or NaN where scores are)
-        const float f = rw_ref == m ? 1.f : ex2(rw_ref - m);
+        const float f = ref == m ? 1.f : ex2(ref - m);
         const float2 v =
             *reinterpret_cast<const float2*>(joined + (w * kRowsTile + row) * C::kPad + d);
         sum = fmaf(f, stat[2 * (w * kRowsTile + row) + 1], sum);
@@ -646,103 +887,135 @@ __global__ void __launch_bounds__(kPaThreads, PaCfg<D, Q4, NT>::kPerSm)
         o1 = fmaf(f, v.y, o1);
       }
       if (whole) {
-        const int mq = rw / p.hpg, h = head * p.hpg + rw - mq * p.hpg;
+        const int mq = rw / p.hpg;
+        const int h = (sh.group * p.heads_item + hd) * p.hpg + rw - mq * p.hpg;
         if (__ldg(p.pos + b * p.pos_b + mq) < 0) sum = o0 = o1 = 0.f;  // padding
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         reinterpret_cast<uint32_t*>(
             p.o + ((static_cast<int64_t>(b) * p.M + mq) * p.H + h) * D)[d >> 1] =
             pack2_t<BF16>(o0 * inv, o1 * inv);
         if (d == 0 && p.lse != nullptr)
-          p.lse[(static_cast<int64_t>(b) * p.H + h) * p.M + mq] =
-              sum == 0.f ? -INFINITY : (m + __log2f(sum)) * 0.69314718055994530942f;
+          p.lse[(static_cast<int64_t>(b) * p.H + h) * p.M + mq] = pa_lse(m, sum);
       } else {
-        float* const dst = p.piece + (slot_id * kRowsTile + row) * D + d;
+        float* const dst = p.piece + (slot_id * piece_rows + prow) * D + d;
         *reinterpret_cast<float2*>(dst) = make_float2(o0, o1);
         if (d == 0) {
           float* const st =
-              p.piece + (2 * static_cast<int64_t>(p.ctas) * D + 2 * slot_id) * kRowsTile + 2 * row;
+              p.piece + (2 * static_cast<int64_t>(p.ctas) * D + 2 * slot_id) * piece_rows + 2 * prow;
           st[0] = m;
           st[1] = sum;
         }
       }
     }
-    fence_proxy_async_smem();  // the ring's next copies come after these reads and writes
+    fence_proxy_async_smem();  // the ring's next copies come after this
     __syncthreads();
     if (!p.cut) break;
     // the next item of the share
-    at += sp.n;
-    if (++head == p.G) {
-      head = 0;
-      do ++item;
-      while (item < p.items && count[item + 1] == count[item]);
+    sh.at += sp.n;
+    if (++sh.group == p.groups) {
+      sh.group = 0;
+      do ++sh.item;
+      while (sh.item < p.items && count[sh.item + 1] == count[sh.item]);
     }
-    more = at < end;
+    more = sh.at < sh.end;
   }
   if (failed) {
     // leave nothing in flight
-    for (; done != issued; ++done)
-      wait_phase(bars + 8 * (done % C::kStages), (done / C::kStages) & 1, kWaitLimitNs);
+    if constexpr (Q4) {
+      for (uint32_t g = issued > C::kStages ? issued - C::kStages : 0; g < issued; ++g)
+        wait_phase(bars + 8 * (g % C::kStages), (g / C::kStages) & 1, kWaitLimitNs);
+    } else {
+      for (; done != issued; ++done)
+        wait_phase(bars + 8 * (done % C::kStages), (done / C::kStages) & 1, kWaitLimitNs);
+    }
     if (lane == 0) report_timeout();
   }
 }
 
 // Items that shares have cut: their pieces joined in order; items without a
-// tile: zeros. A CTA a row; a piece to each of kJoinSets sets of threads in turn.
-constexpr int kJoinSets = 4;
+// tile: zeros. A CTA takes `rows_cta` rows of an item, D / 4 threads a row and
+// piece; with fewer rows than its threads could take, the pieces are dealt to
+// sets of them.
+constexpr int kJoinThreads = 256;
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kJoinSets * D / 2)
-    paged_attn_join_kernel(const PagedProblem p, int rows_tile) {
-  __shared__ float weight[4 * kPaSms + 2];
-  __shared__ float2 part[kJoinSets][D / 2];
-  const int item = blockIdx.x / p.G, head = blockIdx.x - item * p.G;
-  const int row = blockIdx.y;
+__global__ void __launch_bounds__(kJoinThreads)
+    paged_attn_join_kernel(const PagedProblem p, int rows_tile, int rows_cta) {
+  __shared__ float weight[8][kPaMostPerSm * kPaSms + 2];  // of a row's pieces
+  __shared__ float4 part[kJoinThreads];
+  __shared__ float2 total[8];  // (reference, sum) of a row
+  const int item = blockIdx.x / p.groups, group = blockIdx.x - item * p.groups;
+  const int piece_rows = p.heads_item * rows_tile;
   const int b = item / p.tiles, rt = item - b * p.tiles;
-  const int rw = rt * rows_tile + row;
-  if (rw >= p.rows) return;
-  const int64_t c0 = p.count[item], per = p.count[p.items + 1];
-  const int64_t n = p.count[item + 1] - c0;
-  const int64_t at = c0 * p.G + head * n;
-  const int first = static_cast<int>(at / per), last = n > 0 ? static_cast<int>((at + n - 1) / per) : first;
+  const int64_t c0 = p.count[item], c1 = p.count[item + 1], per = p.count[p.items + 1];
+  const int64_t n = c1 - c0;
+  const int64_t at = c0 * p.groups + group * n;
+  const int first = static_cast<int>(at / per);
+  const int last = n > 0 ? static_cast<int>((at + n - 1) / per) : first;
   if (n > 0 && first == last) return;  // whole in one share
-  const int d = threadIdx.x % (D / 2), set = threadIdx.x / (D / 2);
   const int pieces = n > 0 ? last - first + 1 : 0;
-  const float* const stats = p.piece + 2 * static_cast<int64_t>(p.ctas) * rows_tile * D;
+  const float* const stats = p.piece + 2 * static_cast<int64_t>(p.ctas) * piece_rows * D;
   auto slot = [&](int i) { return 2 * static_cast<int64_t>(first + i) + (i == 0 ? 1 : 0); };
-  auto stat = [&](int i, int k) { return stats[(slot(i) * rows_tile + row) * 2 + k]; };
-  // the largest reference, then every piece's weight (all threads alike)
-  float m = -INFINITY;
-  for (int i = threadIdx.x & 31; i < pieces; i += 32) m = fmaxf(m, stat(i, 0));
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int prow0 = blockIdx.y * rows_cta;
+  // a warp a row: the largest reference, the pieces' weights and the sum
+  if (warp < rows_cta) {
+    const int prow = prow0 + warp;
+    auto stat = [&](int i) {
+      return *reinterpret_cast<const float2*>(stats + (slot(i) * piece_rows + prow) * 2);
+    };
+    float m = -INFINITY, sum = 0.f;
+    const bool in = rt * rows_tile + prow % rows_tile < p.rows;  // (others have no piece)
+    if (in) {
+      for (int i = lane; i < pieces; i += 32) m = fmaxf(m, stat(i).x);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-  for (int i = threadIdx.x; i < pieces; i += kJoinSets * D / 2) {
-    const float ref = stat(i, 0);
-    weight[i] = ref == m ? 1.f : ex2(ref - m);
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+      for (int i = lane; i < pieces; i += 32) {
+        const float2 s = stat(i);
+        const float w = s.x == m ? 1.f : ex2(s.x - m);
+        weight[warp][i] = w;
+        sum = fmaf(w, s.y, sum);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    }
+    if (lane == 0) total[warp] = make_float2(m, sum);
   }
   __syncthreads();
-  float2 o = make_float2(0.f, 0.f);
-  for (int i = set; i < pieces; i += kJoinSets) {
-    const float2 v =
-        reinterpret_cast<const float2*>(p.piece + (slot(i) * rows_tile + row) * D)[d];
-    o.x = fmaf(weight[i], v.x, o.x);
-    o.y = fmaf(weight[i], v.y, o.y);
+  constexpr int kLanes = D / 4;  // threads of a row
+  const int sets = kJoinThreads / (kLanes * rows_cta);
+  const int d = threadIdx.x % kLanes, lrow = threadIdx.x / kLanes % rows_cta;
+  const int set = threadIdx.x / (kLanes * rows_cta);
+  const int prow = prow0 + lrow, hd = prow / rows_tile;
+  const int rw = rt * rows_tile + prow - hd * rows_tile;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (rw < p.rows) {
+    for (int i = set; i < pieces; i += sets) {
+      const float4 v =
+          reinterpret_cast<const float4*>(p.piece + (slot(i) * piece_rows + prow) * D)[d];
+      const float w = weight[lrow][i];
+      o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y);
+      o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+    }
   }
-  part[set][d] = o;
+  part[threadIdx.x] = o;
   __syncthreads();
-  if (set != 0) return;
-  float sum = 0.f;
-  for (int i = 0; i < pieces; ++i) sum = fmaf(weight[i], stat(i, 1), sum);
-  o = make_float2(0.f, 0.f);
-#pragma unroll
-  for (int k = 0; k < kJoinSets; ++k) o.x += part[k][d].x, o.y += part[k][d].y;
-  const int mq = rw / p.hpg, h = head * p.hpg + rw - mq * p.hpg;
-  if (__ldg(p.pos + b * p.pos_b + mq) < 0) sum = o.x = o.y = 0.f;  // padding
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  reinterpret_cast<uint32_t*>(p.o + ((static_cast<int64_t>(b) * p.M + mq) * p.H + h) * D)[d] =
-      pack2_t<BF16>(o.x * inv, o.y * inv);
+  if (set != 0 || rw >= p.rows) return;
+  for (int k = 1; k < sets; ++k) {
+    const float4 v = part[threadIdx.x + k * kLanes * rows_cta];
+    o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+  }
+  float2 t = total[lrow];
+  const int mq = rw / p.hpg, h = (group * p.heads_item + hd) * p.hpg + rw - mq * p.hpg;
+  if (__ldg(p.pos + b * p.pos_b + mq) < 0) {  // padding
+    t.y = 0.f;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  const float inv = t.y == 0.f ? 0.f : 1.f / t.y;
+  reinterpret_cast<uint2*>(p.o + ((static_cast<int64_t>(b) * p.M + mq) * p.H + h) * D)[d] =
+      make_uint2(pack2_t<BF16>(o.x * inv, o.y * inv), pack2_t<BF16>(o.z * inv, o.w * inv));
   if (d == 0 && p.lse != nullptr)
-    p.lse[(static_cast<int64_t>(b) * p.H + h) * p.M + mq] =
-        sum == 0.f ? -INFINITY : (m + __log2f(sum)) * 0.69314718055994530942f;
+    p.lse[(static_cast<int64_t>(b) * p.H + h) * p.M + mq] = pa_lse(t.x, t.y);
 }
 
 // ---- host ---------------------------------------------------------------
@@ -750,18 +1023,31 @@ __global__ void __launch_bounds__(kJoinSets * D / 2)
 // Row tiles: 8 rows where a KV head has no more, else 16.
 int rows_of_tile(int64_t rows) { return rows <= 8 ? 8 : 16; }
 
-bool encode_code_map(CUtensorMap* tm, const void* ptr, const KvPages& c, int64_t G, int64_t D) {
+// KV heads of an item. The rows of a 4-bit cache are 64 or 32 bytes for each
+// head of a token, but what comes from memory is 128: neighbouring heads are
+// read by the warps of one CTA at the same time.
+int heads_of_item(int64_t G, int64_t D, int64_t bits) {
+  if (bits == 16) return 1;
+  return D == 64 && G % 4 == 0 ? 4 : G % 2 == 0 ? 2 : 1;
+}
+
+// The codes of `heads` neighbouring KV heads, 128, 64 or 32 bytes, of `tokens`
+// tokens; a token's heads lie side by side.
+bool encode_code_map(CUtensorMap* tm, const void* ptr, const KvPages& c, int64_t G, int64_t D,
+                     int heads, int tokens) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
-  const cuuint64_t row = static_cast<cuuint64_t>(D / 2), page = cuuint64_t(1) << c.shift;
-  const cuuint64_t dims[4] = {row, static_cast<cuuint64_t>(G), page,
-                              static_cast<cuuint64_t>(c.pages)};
-  const cuuint64_t strides[3] = {row, row * G, row * G * page};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(row), 1, kPaTile, 1};
+  const cuuint64_t row = static_cast<cuuint64_t>(G * (D / 2)), page = cuuint64_t(1) << c.shift;
+  const cuuint32_t wide = static_cast<cuuint32_t>(heads * (D / 2));
+  const cuuint64_t dims[4] = {row, page, static_cast<cuuint64_t>(c.pages), 1};
+  const cuuint64_t strides[3] = {row, row * page, row * page * c.pages};
+  const cuuint32_t box[4] = {wide, static_cast<cuuint32_t>(tokens), 1, 1};
   const cuuint32_t one[4] = {1, 1, 1, 1};
   return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(ptr), dims, strides, box, one,
              CU_TENSOR_MAP_INTERLEAVE_NONE,
-             D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
+             wide == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+             : wide == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                          : CU_TENSOR_MAP_SWIZZLE_NONE,
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -778,19 +1064,26 @@ int check_paged(int64_t B, int64_t M, int64_t H, int64_t G, int64_t D, int dtype
 template <int D, bool BF16, bool Q4, int NT>
 int launch_paged(PagedProblem& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
   using C = PaCfg<D, Q4, NT>;
-  static_assert(C::kSmem * C::kPerSm <= 232448, "CTAs of an SM");
-  static_assert(C::kPerSm <= 4, "pieces in the workspace");
+  static_assert((C::kSmem + 1024) * C::kPerSm <= 233472, "CTAs of an SM");
+  static_assert(C::kPerSm <= kPaMostPerSm, "pieces in the workspace");
   auto kern = paged_attn_kernel<D, BF16, Q4, NT>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) !=
       cudaSuccess)
     return NSA_ERR_LAUNCH;
   p.ctas = C::kPerSm * kPaSms;
-  const int64_t blocks = p.cut ? p.ctas : static_cast<int64_t>(p.items) * p.G;
+  const int64_t blocks = p.cut ? p.ctas : static_cast<int64_t>(p.items) * p.groups;
   kern<<<static_cast<unsigned>(blocks), kPaThreads, C::kSmem, st>>>(p, tk, tv);
   if (cudaGetLastError() != cudaSuccess) return NSA_ERR_LAUNCH;
   if (p.cut) {
+    // rows of a CTA: as many as leave a CTA for each SM, so that few items
+    // have their many pieces added by many threads
+    const int rows = p.heads_item * 8 * NT;
+    int rows_cta = 1024 / D;  // a thread for every four entries
+    while (rows_cta > 1 && static_cast<int64_t>(p.items) * p.groups * (rows / rows_cta) < kPaSms)
+      rows_cta >>= 1;
+    if (rows_cta > 8) rows_cta = 8;
     paged_attn_join_kernel<D, BF16>
-        <<<dim3(p.items * p.G, 8 * NT), kJoinSets * D / 2, 0, st>>>(p, 8 * NT);
+        <<<dim3(p.items * p.groups, rows / rows_cta), kJoinThreads, 0, st>>>(p, 8 * NT, rows_cta);
     if (cudaGetLastError() != cudaSuccess) return NSA_ERR_LAUNCH;
   }
   return NSA_OK;
@@ -800,7 +1093,11 @@ template <int D, bool BF16>
 int launch_paged_d(PagedProblem& p, const nsa_kv_cache* kv, cudaStream_t st) {
   CUtensorMap tk, tv;
   if (kv->bits == 4) {
-    if (!encode_code_map(&tk, p.c.k, p.c, p.G, D) || !encode_code_map(&tv, p.c.v, p.c, p.G, D))
+    const int wide = kPaSlotRows / p.heads_item, page = 1 << p.c.shift;
+    const int tokens = wide < page ? wide : page;
+    p.split = wide / tokens;
+    if (!encode_code_map(&tk, p.c.k, p.c, p.G, D, p.heads_item, tokens) ||
+        !encode_code_map(&tv, p.c.v, p.c, p.G, D, p.heads_item, tokens))
       return NSA_ERR_LAUNCH;
   } else {
     constexpr CUtensorMapDataType dt =
@@ -834,7 +1131,7 @@ extern "C" int64_t nsa_paged_attn_workspace_bytes(int64_t B, int64_t M, int64_t 
   const int64_t items = B * ((rows + tile - 1) / tile);
   if (items == 0 || items > kPaItems) return 0;
   // two pieces of every share, and the running counts
-  return 2 * 4 * kPaSms * tile * (D + 2) * 4 + (kPaItems + 2) * 8;
+  return 2 * kPaMostPerSm * kPaSms * heads_of_item(G, D, 4) * tile * (D + 2) * 4 + (kPaItems + 2) * 8;
 }
 
 extern "C" int nsa_paged_attn(const void* Q, const nsa_kv_cache* cache, const int32_t* page_table,
@@ -875,6 +1172,9 @@ extern "C" int nsa_paged_attn(const void* Q, const nsa_kv_cache* cache, const in
   p.G = static_cast<int>(G);
   p.hpg = static_cast<int>(H / G);
   p.rows = static_cast<int>(M * (H / G));
+  p.heads_item = heads_of_item(G, D, cache->bits);
+  p.groups = p.G / p.heads_item;
+  p.step_shift = cache->bits == 16 ? 4 : p.heads_item == 1 ? 7 : p.heads_item == 2 ? 6 : 5;
   const int tile = rows_of_tile(p.rows);
   p.tiles = (p.rows + tile - 1) / tile;
   p.items = static_cast<int>(B * p.tiles);
