@@ -63,7 +63,12 @@ constexpr int kPaSlotRows = 128;  // (head, key) rows of a 4-bit slot
 constexpr int kPaItems = 512;     // row tiles of a batch that shares are formed of
 constexpr int kPaSms = 152;
 constexpr int kPaMostPerSm = 4;
-constexpr int kPaLeast = 128;     // keys of a share at least
+// What an item costs beside its keys, in keys: its positions, pages and first
+// copies one after the other, and the joining of the warps, some 4 us where 16
+// keys take 0.3. (Shares by keys alone: a CTA with seven short items took 34 us
+// where the others took 13.)
+constexpr int kPaItemCost = 192;
+constexpr int kPaLeast = 320;     // keys of a share at least, that cost among them
 constexpr float kPaSlack = 8.0f;
 
 template <int D, bool Q4, int NT>
@@ -105,6 +110,7 @@ struct PagedProblem {
   int left, sinks, ctas;
   int heads_item, groups;  // KV heads of an item, G / heads_item
   int step_shift;          // keys of a step: 16; 4 bits: 128 / heads_item
+  int item_cost;           // kPaItemCost in steps
   int split;               // 4 bits: copies that a step's keys take (small pages)
   float sl2;
   bool cut;
@@ -184,7 +190,8 @@ __device__ __forceinline__ PaShare pa_share(const PagedProblem& p, int* count, i
   int mine = 0;
   for (int i = i0; i < i1; ++i) {
     count[i] = mine;
-    mine += pa_span(p, i / p.tiles, i % p.tiles, kRowsTile).n;
+    const int n = pa_span(p, i / p.tiles, i % p.tiles, kRowsTile).n;
+    mine += n > 0 ? n + p.item_cost : 0;
   }
   int scan = mine;
 #pragma unroll
@@ -216,7 +223,7 @@ __device__ __forceinline__ PaShare pa_share(const PagedProblem& p, int* count, i
       else hi = mid - 1;
     }
     s.item = lo;
-    const int n = count[lo + 1] - count[lo];
+    const int n = count[lo + 1] - count[lo];  // (its cost among them)
     const int64_t first = static_cast<int64_t>(count[lo]) * p.groups;
     s.group = static_cast<int>((s.begin - first) / n);
     s.at = first + static_cast<int64_t>(s.group) * n;
@@ -371,6 +378,19 @@ __device__ __forceinline__ void pa_tile16(PaRows<D, NT>& a, const uint32_t (&qf)
 
 // ---- 4 bits ------------------------------------------------------------
 
+// mma_16816, or the same from zero (without registers to be cleared first).
+__device__ __forceinline__ void pa_mma_from(bool zero, float (&d)[4], uint32_t a0, uint32_t a1,
+                                            uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  if (zero)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};\n"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    mma_16816(d, a0, a1, a2, a3, b0, b1);
+}
+
 // Key of MMA row i of a tile. Any order serves; in this one the 16- and 8-byte
 // loads of 128-byte swizzled rows meet no bank twice.
 __device__ __forceinline__ int pa_row4(int i) { return (i & 14) ^ (i & 1 ? 5 : 0); }
@@ -394,10 +414,6 @@ __device__ __forceinline__ void pa_scores4(const PaRows<D, NT>& a, const uint8_t
   constexpr int W = D / 32;
   const int key = n0 + pa_row4((threadIdx.x & 31) >> 2);
   float sc[NT][2][4];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sc[nt][0][i] = sc[nt][1][i] = 0.f;
   uint32_t w[2][W];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -422,10 +438,10 @@ __device__ __forceinline__ void pa_scores4(const PaRows<D, NT>& a, const uint8_t
     const uint32_t u = w[0][j], v = w[1][j], u8 = u >> 8, v8 = v >> 8;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      mma_16816(sc[nt][0], u & 0x000f000fu, v & 0x000f000fu, u & 0x00f000f0u, v & 0x00f000f0u,
-                qf[nt][2 * j][0], qf[nt][2 * j][1]);
-      mma_16816(sc[nt][1], u8 & 0x000f000fu, v8 & 0x000f000fu, u8 & 0x00f000f0u, v8 & 0x00f000f0u,
-                qf[nt][2 * j + 1][0], qf[nt][2 * j + 1][1]);
+      pa_mma_from(j == 0, sc[nt][0], u & 0x000f000fu, v & 0x000f000fu, u & 0x00f000f0u,
+                  v & 0x00f000f0u, qf[nt][2 * j][0], qf[nt][2 * j][1]);
+      pa_mma_from(j == 0, sc[nt][1], u8 & 0x000f000fu, v8 & 0x000f000fu, u8 & 0x00f000f0u,
+                  v8 & 0x00f000f0u, qf[nt][2 * j + 1][0], qf[nt][2 * j + 1][1]);
     }
   }
   float kstep[2], klow[2], lstep[2];
@@ -492,13 +508,16 @@ __device__ __forceinline__ void pa_values4(PaRows<D, NT>& a, const uint8_t* vt, 
       const uint32_t sel = half ? 0x7632u : 0x5410u;
       const uint32_t u = __byte_perm(w[0][j], w[1][j], sel);
       const uint32_t v = __byte_perm(w[2][j], w[3][j], sel);
-      const uint32_t u8 = u >> 8, v8 = v >> 8;
+      // whole bytes, lower code + 16 x upper (the sum of the uppers is taken off
+      // at the end): a byte moved into place needs no mask
+      const uint32_t u0 = u & 0x00ff00ffu, u1 = __byte_perm(u, 0u, 0x4341u);
+      const uint32_t v0 = v & 0x00ff00ffu, v1 = __byte_perm(v, 0u, 0x4341u);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        mma_16816(a.acc[nt][4 * j + 2 * half], u & 0x000f000fu, u & 0x00f000f0u, v & 0x000f000fu,
-                  v & 0x00f000f0u, pf[nt][0], pf[nt][1]);
-        mma_16816(a.acc[nt][4 * j + 2 * half + 1], u8 & 0x000f000fu, u8 & 0x00f000f0u,
-                  v8 & 0x000f000fu, v8 & 0x00f000f0u, pf[nt][0], pf[nt][1]);
+        mma_16816(a.acc[nt][4 * j + 2 * half], u0, u & 0x00f000f0u, v0, v & 0x00f000f0u, pf[nt][0],
+                  pf[nt][1]);
+        mma_16816(a.acc[nt][4 * j + 2 * half + 1], u1, u1 & 0x00f000f0u, v1, v1 & 0x00f000f0u,
+                  pf[nt][0], pf[nt][1]);
       }
     }
   }
@@ -632,6 +651,7 @@ __global__ void __launch_bounds__(kPaThreads, PaCfg<D, Q4, NT>::kPerSm)
     tma_prefetch_desc(&tmV);
   }
   PaShare sh{0, 0, 0, 0, 0};
+  asm volatile("griddepcontrol.launch_dependents;\n");  // the join waits for this grid's end
   if (p.cut) {
     sh = pa_share<kRowsTile>(p, count, reinterpret_cast<int*>(stat));
   } else {
@@ -664,13 +684,20 @@ __global__ void __launch_bounds__(kPaThreads, PaCfg<D, Q4, NT>::kPerSm)
   }
   bool failed = false;
   uint32_t issued = 0, done = 0;  // slots of the ring, over all items
+  [[maybe_unused]] uint32_t stage = 0, phase = 0;  // 4 bits: of the next slot to be read
   for (bool more = !p.cut || sh.begin < sh.end; more;) {
     const int b = sh.item / p.tiles, rt = sh.item - b * p.tiles;
     const int head = sh.group * p.heads_item + head_in;
     const PaSpan sp = pa_span(p, b, rt, kRowsTile);
-    const int t0 = p.cut ? static_cast<int>(max(sh.begin - sh.at, static_cast<int64_t>(0))) : 0;
-    const int t1 =
-        p.cut ? static_cast<int>(min(sh.end - sh.at, static_cast<int64_t>(sp.n))) : sp.n;
+    // steps [t0, t1) of the item, after its cost
+    int t0 = 0, t1 = sp.n;
+    if (p.cut) {
+      const int64_t first = sh.at + p.item_cost;
+      t0 = static_cast<int>(min(max(sh.begin - first, static_cast<int64_t>(0)),
+                                static_cast<int64_t>(sp.n)));
+      t1 = static_cast<int>(min(max(sh.end - first, static_cast<int64_t>(0)),
+                                static_cast<int64_t>(sp.n)));
+    }
     const PaSight see{sp.lo_pos, sp.hi_pos, p.left, p.sinks};
 
     const int in_page = (1 << p.c.shift) - 1;
@@ -721,8 +748,10 @@ __global__ void __launch_bounds__(kPaThreads, PaCfg<D, Q4, NT>::kPerSm)
         }
         if (lane >= e && lane < e + p.split) {
           const int first = (lane - e) * rows;  // of the copy's rows, in the step
+          // each tile's first key, and whether every query sees all of it (bit 0)
           for (int i = 0; i < rows; i += kPaTile)
-            keys[s * C::kKeys + (first + i) / kPaTile] = page_l < 0 ? -1 : key_l + i;
+            keys[s * C::kKeys + (first + i) / kPaTile] =
+                page_l < 0 ? kNoKey : key_l + i + (see.all(key_l + i) ? 1 : 0);
           if (page_l < 0) {
             mbar_arrive(bar);  // a page that is not there
           } else {
@@ -748,25 +777,25 @@ __global__ void __launch_bounds__(kPaThreads, PaCfg<D, Q4, NT>::kPerSm)
         if (t % kPaWarps == warp) issue(t);
       pa_queries<D, BF16, true, NT>(p, b, rt, head, qf, ka, kb);
       for (int t = 0; t < steps && !failed; ++t) {
-        const uint32_t g = issued + t;
-        const int s = g % C::kStages;
-        if (!__all_sync(kFull, wait_phase(bars + 8 * s, (g / C::kStages) & 1, kWaitLimitNs))) {
+        if (!__all_sync(kFull, wait_phase(bars + 8 * stage, phase, kWaitLimitNs))) {
           failed = true;
           break;
         }
-        const int k0 = s * C::kKeys + 2 * warp_in;
-        const int n0[2] = {keys[k0], keys[k0 + 1]};
-        const uint8_t* const slot = gbase + s * C::kSlot;
+        const int k0 = keys[stage * C::kKeys + 2 * warp_in];
+        const int k1 = keys[stage * C::kKeys + 2 * warp_in + 1];
+        const int n0[2] = {k0 & ~1, k1 & ~1};
+        const uint8_t* const slot = gbase + stage * C::kSlot;
         const uint8_t* const scales = slot + 2 * C::kKv;
-        if (n0[0] >= 0 && n0[1] >= 0 && see.all(n0[0]) && see.all(n0[1])) {
+        if (k0 & k1 & 1)
           pa_step4<D, NT, false>(a, slot, scales, lanes, row_bytes, n0, qf, ka, kb, see);
-        } else if (n0[0] >= 0 || n0[1] >= 0) {
-          const int n1[2] = {n0[0] < 0 ? kNoKey : n0[0], n0[1] < 0 ? kNoKey : n0[1]};
-          if (!see.nothing(n1[0]) || !see.nothing(n1[1]))
-            pa_step4<D, NT, true>(a, slot, scales, lanes, row_bytes, n1, qf, ka, kb, see);
-        }
+        else if (!see.nothing(n0[0]) || !see.nothing(n0[1]))
+          pa_step4<D, NT, true>(a, slot, scales, lanes, row_bytes, n0, qf, ka, kb, see);
         __syncwarp();  // the slot has been read
-        if (lane == 0) mbar_arrive(bars + 8 * (C::kStages + s));
+        if (lane == 0) mbar_arrive(bars + 8 * (C::kStages + stage));
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
         const int next = t + C::kStages - 1;
         if (next < steps && next % kPaWarps == warp) issue(next);
       }
@@ -826,6 +855,7 @@ __global__ void __launch_bounds__(kPaThreads, PaCfg<D, Q4, NT>::kPerSm)
       }
     }
 
+    if (t0 == t1 && p.cut) break;  // (the share ends within an item's cost)
     // ---- the warps' results, joined in shared memory
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -847,10 +877,10 @@ __global__ void __launch_bounds__(kPaThreads, PaCfg<D, Q4, NT>::kPerSm)
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           if constexpr (Q4) {
-            // word D / 64 r + i / 4 of a row, entries 2 (i % 4) and the one
-            // after, which the mask left 16 times as large
+            // byte i % 4 of word D / 64 r + i / 4 of a row: the whole byte, and its
+            // upper code 16 times as large
             const int d = 8 * (D / 64 * r + (i >> 2)) + 2 * (i & 3);
-            dst[d] = fmaf(a.acc[nt][i][j], 16777216.f, a.base_v[nt][j]);
+            dst[d] = fmaf(a.acc[nt][i][j] - a.acc[nt][i][j + 2], 16777216.f, a.base_v[nt][j]);
             dst[d + 1] = fmaf(a.acc[nt][i][j + 2], 1048576.f, a.base_v[nt][j]);
           } else {
             dst[16 * i + r] = a.acc[nt][i][j];
@@ -911,7 +941,7 @@ __global__ void __launch_bounds__(kPaThreads, PaCfg<D, Q4, NT>::kPerSm)
     __syncthreads();
     if (!p.cut) break;
     // the next item of the share
-    sh.at += sp.n;
+    sh.at += sp.n + p.item_cost;
     if (++sh.group == p.groups) {
       sh.group = 0;
       do ++sh.item;
@@ -944,12 +974,14 @@ __global__ void __launch_bounds__(kJoinThreads)
   __shared__ float weight[8][kPaMostPerSm * kPaSms + 2];  // of a row's pieces
   __shared__ float4 part[kJoinThreads];
   __shared__ float2 total[8];  // (reference, sum) of a row
+  // (launched while the kernel before is at its end; its results are there from here on)
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int item = blockIdx.x / p.groups, group = blockIdx.x - item * p.groups;
   const int piece_rows = p.heads_item * rows_tile;
   const int b = item / p.tiles, rt = item - b * p.tiles;
   const int64_t c0 = p.count[item], c1 = p.count[item + 1], per = p.count[p.items + 1];
-  const int64_t n = c1 - c0;
-  const int64_t at = c0 * p.groups + group * n;
+  const int64_t n = c1 - c0 - p.item_cost;  // (below 0: no step)
+  const int64_t at = c0 * p.groups + group * (c1 - c0) + p.item_cost;
   const int first = static_cast<int>(at / per);
   const int last = n > 0 ? static_cast<int>((at + n - 1) / per) : first;
   if (n > 0 && first == last) return;  // whole in one share
@@ -1082,9 +1114,18 @@ int launch_paged(PagedProblem& p, const CUtensorMap& tk, const CUtensorMap& tv, 
     while (rows_cta > 1 && static_cast<int64_t>(p.items) * p.groups * (rows / rows_cta) < kPaSms)
       rows_cta >>= 1;
     if (rows_cta > 8) rows_cta = 8;
-    paged_attn_join_kernel<D, BF16>
-        <<<dim3(p.items * p.groups, rows / rows_cta), kJoinThreads, 0, st>>>(p, 8 * NT, rows_cta);
-    if (cudaGetLastError() != cudaSuccess) return NSA_ERR_LAUNCH;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.items * p.groups), rows / rows_cta);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<D, BF16>, PagedProblem(p), 8 * NT,
+                           rows_cta) != cudaSuccess)
+      return NSA_ERR_LAUNCH;
   }
   return NSA_OK;
 }
@@ -1175,10 +1216,11 @@ extern "C" int nsa_paged_attn(const void* Q, const nsa_kv_cache* cache, const in
   p.heads_item = heads_of_item(G, D, cache->bits);
   p.groups = p.G / p.heads_item;
   p.step_shift = cache->bits == 16 ? 4 : p.heads_item == 1 ? 7 : p.heads_item == 2 ? 6 : 5;
+  p.item_cost = (kPaItemCost + (1 << p.step_shift) - 1) >> p.step_shift;
   const int tile = rows_of_tile(p.rows);
   p.tiles = (p.rows + tile - 1) / tile;
   p.items = static_cast<int>(B * p.tiles);
-  p.cut = need > 0 && p.items * (table_cols * cache->page_size / kPaTile) < int64_t(1) << 31;
+  p.cut = need > 0 && p.items * (table_cols * cache->page_size / kPaTile + 16) < int64_t(1) << 31;
   // a window that reaches behind key 0 from any position; sinks as many as a table's tokens
   const int64_t far = 0x7fffffff, most = int64_t(1) << 30;
   p.left = static_cast<int>(window_left < 0 || window_left > far ? far : window_left);
