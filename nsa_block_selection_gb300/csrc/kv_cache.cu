@@ -34,7 +34,10 @@ namespace nsa {
 namespace {
 
 constexpr int kKvThreads = 128;
-constexpr int kAppendPerSm = 6;
+constexpr int kAppendPerSm = 6, kAppendPerSm4 = 4;  // CTAs of kv_append_kernel
+// Beyond so many groups of row slots a token, and in all, a warp takes a token.
+constexpr int kAppendFewPerToken = 8;
+constexpr int64_t kAppendFewGroups = 128 * 152;
 constexpr int kKvSms = 152;
 
 struct AppendProblem {
@@ -65,10 +68,134 @@ __device__ __forceinline__ uint32_t codes8(const float* f, float low, float step
   return w;
 }
 
-// A row slot of a warp keeps its head (of Q, K or V) and the head's weights, and
+// The 16-bit row f (packed in v0, v1) as a 4-bit row of the cache. All lanes of the
+// warp; `write`: this one's row has a place.
+template <int D, bool BF16>
+__device__ __forceinline__ void store_codes(const uint4& v0, const uint4& v1, int c0, int c1, int tl,
+                                            uint8_t* row, uint32_t* scale, bool write) {
+  constexpr int LPR = D / 16;
+  float f[16];
+  unpack8<BF16>(v0, f);
+  unpack8<BF16>(v1, f + 8);
+  float lo = f[0], hi = f[0], bad = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    lo = fminf(lo, f[i]);
+    hi = fmaxf(hi, f[i]);
+    bad = fmaf(f[i], 0.f, bad);  // NaN where an entry is not finite
+  }
+  lo = row_min<LPR>(lo);
+  hi = -row_min<LPR>(-hi);
+  bad = row_sum<LPR>(bad);
+  const float low = __bfloat162float(__float2bfloat16_rn(lo));
+  float step = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(hi - low, 15.f)));
+  const bool some = step >= kLeastStep;
+  if (!some) step = 0.f;
+  // a row that is not finite, or too wide for fp32, reads as NaN
+  if (!(bad == 0.f) || !(hi - low < INFINITY)) step = __uint_as_float(0x7fc00000u);
+  const bool fine = some && step < INFINITY;
+  if (write) {
+    uint32_t* const dst = reinterpret_cast<uint32_t*>(row);
+    dst[c0] = codes8(f, low, step, fine);
+    dst[c1] = codes8(f + 8, low, step, fine);
+    if (tl == 0) *scale = pack_bf162(step, low);
+  }
+}
+
+// K's or V's rows [r0, r1) of one token, UN groups of rows in flight per warp.
+template <int D, bool BF16, bool Q4, bool V, int UN>
+__device__ __forceinline__ void append_rows(const AppendProblem& p, const uint8_t* x, int64_t xh,
+                                            int r0, int r1, int page, int off, bool rot, int c0,
+                                            int c1, const float* c, const float* s) {
+  constexpr int LPR = D / 16, RPW = 32 / LPR;
+  const int sub = (threadIdx.x & 31) / LPR, tl = (threadIdx.x & 31) % LPR;
+  uint8_t* const y = V ? p.c.v + page * p.c.vp + off * p.c.vt : p.c.k + page * p.c.kp + off * p.c.kt;
+  const int64_t yh = V ? p.c.vh : p.c.kh;
+  float w[16];
+  if (!V && p.norm) load_weights<BF16>(p.r.k.w, p.r.w32, c0, c1, w);
+  for (int r = r0; r < r1; r += RPW * UN) {
+    uint4 v[UN][2];
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const int row = r + u * RPW + sub;
+      v[u][0] = v[u][1] = make_uint4(0, 0, 0, 0);
+      if (row < r1) {
+        const uint4* src = reinterpret_cast<const uint4*>(x + 2 * row * xh);
+        v[u][0] = src[c0];
+        v[u][1] = src[c1];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const int row = r + u * RPW + sub;
+      if constexpr (!V) {
+        float f[16];
+        unpack8<BF16>(v[u][0], f);
+        unpack8<BF16>(v[u][1], f + 8);
+        if (p.norm) {
+          float sq = 0.f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sq = fmaf(f[i], f[i], sq);
+          sq = row_sum<LPR>(sq);
+          const float rs = rsqrtf(sq * (1.f / D) + p.r.eps);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) f[i] *= rs * w[i];
+        }
+        if (rot) turn(f, c, s, p.r.interleaved);
+        v[u][0] = pack8<BF16>(f);
+        v[u][1] = pack8<BF16>(f + 8);
+      }
+      if constexpr (Q4) {
+        const int64_t so = ((page * static_cast<int64_t>(p.r.k.heads) + row) << p.c.shift) + off;
+        store_codes<D, BF16>(v[u][0], v[u][1], c0, c1, tl, y + row * yh, (V ? p.c.vs : p.c.ks) + so,
+                             row < r1);
+      } else if (row < r1) {
+        uint4* const dst = reinterpret_cast<uint4*>(y + row * yh);
+        dst[c0] = v[u][0];
+        dst[c1] = v[u][1];
+      }
+    }
+  }
+}
+
+// Many heads: one warp per unit of `per` rows of the H + 2 G of a token (Q's, K's,
+// V's), which share its position, page and angles, as norm_rope_kernel.
+template <int D, bool BF16, bool Q4, int UN>
+__global__ void __launch_bounds__(kKvThreads)
+    kv_append_token_kernel(const AppendProblem p, int segs, int per, int64_t units) {
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kKvThreads / 32) + (threadIdx.x >> 5);
+  if (unit >= units) return;
+  const uint32_t tok = static_cast<uint32_t>(unit) / static_cast<uint32_t>(segs);
+  const int seg = static_cast<int>(static_cast<uint32_t>(unit) - tok * segs);
+  const int b = static_cast<int>(tok / static_cast<uint32_t>(p.r.M));
+  const int m = static_cast<int>(tok - static_cast<uint32_t>(b) * p.r.M);
+  const int64_t at = token_position(p.r, b, m);
+  const bool live = at >= 0;
+  const int H = p.r.q.heads, G = p.r.k.heads;
+  int c0, c1;
+  const int t = (threadIdx.x & 31) % (D / 16);
+  row_chunks(t, p.r.half, c0, c1);
+  const bool rot = t < (p.r.half >> 3);
+  float c[8], s[8];
+  if (live && rot) load_angles(p.r, at, c0, c1, c, s);
+  const int r0 = seg * per, r1 = min(r0 + per, H + 2 * G);
+  const int page = live && r1 > H ? page_of(p.c, b, at) : -1;
+  const int off = static_cast<int>(at) & ((1 << p.c.shift) - 1);
+  if (r0 < H)
+    norm_rope_rows<D, BF16, UN>(p.r, p.r.q, b, m, r0, min(r1, H), live, rot, c0, c1, c, s, p.norm);
+  if (page < 0) return;
+  if (r1 > H && r0 < H + G)
+    append_rows<D, BF16, Q4, false, 2>(p, p.r.k.x + 2 * (b * p.r.k.xb + m * p.r.k.xm), p.r.k.xh,
+                                       max(r0 - H, 0), min(r1 - H, G), page, off, rot, c0, c1, c, s);
+  if (r1 > H + G)
+    append_rows<D, BF16, Q4, true, 2>(p, p.v + 2 * (b * p.vb + m * p.vm), p.vh, max(r0 - H - G, 0),
+                                      r1 - H - G, page, off, false, c0, c1, c, s);
+}
+
+// Few heads, or few tokens: a row slot of a warp keeps its head (of Q, K or V) and the head's weights, and
 // walks the tokens, as in norm_rope_few_kernel.
 template <int D, bool BF16, bool Q4>
-__global__ void __launch_bounds__(kKvThreads, kAppendPerSm)
+__global__ void __launch_bounds__(kKvThreads, Q4 ? kAppendPerSm4 : kAppendPerSm)
     kv_append_kernel(const AppendProblem p, const RowGroups rg) {
   constexpr int LPR = D / 16, RPW = 32 / LPR;
   const int lane = threadIdx.x & 31, sub = lane / LPR, tl = lane % LPR;
@@ -151,34 +278,10 @@ __global__ void __launch_bounds__(kKvThreads, kAppendPerSm)
       v1 = pack8<BF16>(f + 8);
     }
     if constexpr (Q4) {
-      // K and V: the 16-bit row in 4 bits (a warp of query rows alone passes)
-      if (__any_sync(kFull, write && !is_q)) {
-        unpack8<BF16>(v0, f);
-        unpack8<BF16>(v1, f + 8);
-        float lo = f[0], hi = f[0], bad = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          lo = fminf(lo, f[i]);
-          hi = fmaxf(hi, f[i]);
-          bad = fmaf(f[i], 0.f, bad);  // NaN where an entry is not finite
-        }
-        lo = row_min<LPR>(lo);
-        hi = -row_min<LPR>(-hi);
-        bad = row_sum<LPR>(bad);
-        const float low = __bfloat162float(__float2bfloat16_rn(lo));
-        float step = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(hi - low, 15.f)));
-        const bool some = step >= kLeastStep;
-        if (!some) step = 0.f;
-        // a row that is not finite, or too wide for fp32, reads as NaN
-        if (!(bad == 0.f) || !(hi - low < INFINITY)) step = __uint_as_float(0x7fc00000u);
-        const bool fine = some && step < INFINITY;
-        if (write && !is_q) {
-          uint32_t* const dst = reinterpret_cast<uint32_t*>(y + yo);
-          dst[c0] = codes8(f, low, step, fine);
-          dst[c1] = codes8(f + 8, low, step, fine);
-          if (tl == 0) (is_v ? p.c.vs : p.c.ks)[so] = pack_bf162(step, low);
-        }
-      }
+      // (a warp of query rows alone passes)
+      if (__any_sync(kFull, write && !is_q))
+        store_codes<D, BF16>(v0, v1, c0, c1, tl, y + yo, (is_v ? p.c.vs : p.c.ks) + so,
+                             write && !is_q);
       write = write && is_q;
     }
     if (write) {
@@ -195,7 +298,7 @@ struct ReadProblem {
   uint8_t *k, *v;  // [B, M, G, D]
   int64_t pos_b;
   int M, G;
-  int64_t chunks;  // 16-byte chunks of K (and of V)
+  uint32_t tokens;
 };
 
 // 8 entries of a 4-bit row.
@@ -208,38 +311,57 @@ __device__ __forceinline__ uint4 from_codes(uint32_t w, uint32_t scale) {
   return pack8<BF16>(f);
 }
 
-// A thread a chunk of 8 entries of K and of V.
+// A group of `lanes` lanes takes a token, whose position and page it looks up once,
+// and then four chunks of 8 entries of K and of V a lane at a time. (A chunk a
+// thread, each looking up its own, left too little in flight: 65,536 tokens of 8
+// heads from 4 bits 77 us; four chunks of four tokens a thread 70.)
+constexpr int kReadChunks = 4;
+
 template <int D, bool BF16, bool Q4>
-__global__ void __launch_bounds__(256) kv_read_kernel(const ReadProblem p) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= p.chunks) return;
-  const int t = static_cast<int>(i % (D / 8));
-  const int64_t row = i / (D / 8);
-  const uint32_t tok = static_cast<uint32_t>(row / p.G);
-  const int g = static_cast<int>(row - static_cast<int64_t>(tok) * p.G);
+__global__ void __launch_bounds__(256) kv_read_kernel(const ReadProblem p, int lanes) {
+  // (under 2^31 tokens, in 32-bit numbers of CTAs and 64-bit ones of threads)
+  const uint32_t tok = static_cast<uint32_t>(
+      (static_cast<uint64_t>(blockIdx.x) * 256u + threadIdx.x) / static_cast<uint32_t>(lanes));
+  if (tok >= p.tokens) return;
   const int b = static_cast<int>(tok / static_cast<uint32_t>(p.M));
   const int m = static_cast<int>(tok - static_cast<uint32_t>(b) * p.M);
-  const int64_t at = p.pos == nullptr ? m : p.pos[b * p.pos_b + m];
+  const int at = __ldg(p.pos + b * p.pos_b + m);
   const int page = at >= 0 ? page_of(p.c, b, at) : -1;
-  uint4 k = make_uint4(0, 0, 0, 0), v = k;
-  if (page >= 0) {
-    const int64_t off = at & ((1 << p.c.shift) - 1);
-    const uint8_t* const ks = p.c.k + page * p.c.kp + off * p.c.kt + g * p.c.kh;
-    const uint8_t* const vs = p.c.v + page * p.c.vp + off * p.c.vt + g * p.c.vh;
-    if constexpr (Q4) {
-      const int64_t so = ((page * static_cast<int64_t>(p.G) + g) << p.c.shift) + off;
-      const uint32_t kw = reinterpret_cast<const uint32_t*>(ks)[t];
-      const uint32_t vw = reinterpret_cast<const uint32_t*>(vs)[t];
-      const uint32_t kc = p.c.ks[so], vc = p.c.vs[so];
-      k = from_codes<BF16>(kw, kc);
-      v = from_codes<BF16>(vw, vc);
-    } else {
-      k = reinterpret_cast<const uint4*>(ks)[t];
-      v = reinterpret_cast<const uint4*>(vs)[t];
+  const int off = at & ((1 << p.c.shift) - 1);
+  const uint8_t* const ks = p.c.k + page * p.c.kp + off * p.c.kt;
+  const uint8_t* const vs = p.c.v + page * p.c.vp + off * p.c.vt;
+  const int64_t so = ((page * static_cast<int64_t>(p.G)) << p.c.shift) + off;
+  const int chunks = p.G * (D / 8);
+  const int64_t out = static_cast<int64_t>(tok) * chunks;
+  for (int i0 = static_cast<int>(threadIdx.x) & (lanes - 1); i0 < chunks; i0 += kReadChunks * lanes) {
+    uint4 k[kReadChunks], v[kReadChunks];  // 4 bits: a word of codes and the scale
+#pragma unroll
+    for (int u = 0; u < kReadChunks; ++u) {
+      const int i = i0 + u * lanes, g = i / (D / 8), t = i % (D / 8);
+      k[u] = v[u] = make_uint4(0, 0, 0, 0);
+      if (page >= 0 && i < chunks) {
+        if constexpr (Q4) {
+          k[u].x = reinterpret_cast<const uint32_t*>(ks + g * p.c.kh)[t];
+          v[u].x = reinterpret_cast<const uint32_t*>(vs + g * p.c.vh)[t];
+          const int64_t s = so + (static_cast<int64_t>(g) << p.c.shift);
+          k[u].y = p.c.ks[s];
+          v[u].y = p.c.vs[s];
+        } else {
+          k[u] = reinterpret_cast<const uint4*>(ks + g * p.c.kh)[t];
+          v[u] = reinterpret_cast<const uint4*>(vs + g * p.c.vh)[t];
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kReadChunks; ++u) {
+      const int i = i0 + u * lanes;
+      if (i < chunks) {
+        // (no page: codes and scales of 0 are zeros)
+        reinterpret_cast<uint4*>(p.k)[out + i] = Q4 ? from_codes<BF16>(k[u].x, k[u].y) : k[u];
+        reinterpret_cast<uint4*>(p.v)[out + i] = Q4 ? from_codes<BF16>(v[u].x, v[u].y) : v[u];
+      }
     }
   }
-  reinterpret_cast<uint4*>(p.k)[i] = k;
-  reinterpret_cast<uint4*>(p.v)[i] = v;
 }
 
 template <int D, bool BF16, bool Q4>
@@ -248,8 +370,24 @@ int launch_append(const AppendProblem& p, cudaStream_t st) {
   constexpr int64_t kWarps = kKvThreads / 32;
   const int64_t tokens = static_cast<int64_t>(p.r.B) * p.r.M;
   const RowGroups g = plan_row_groups(p.r.q.heads + 2 * p.r.k.heads, tokens, RPW);
+  const int rows = p.r.q.heads + 2 * p.r.k.heads;
+  if (rows > kAppendFewPerToken * RPW && g.groups > kAppendFewGroups) {
+    // as launch_norm_rope: a whole token a warp, or as few rows as give every SM 16 warps
+    int64_t segs = (16 * kKvSms + tokens - 1) / tokens;
+    const int64_t most = (rows + RPW - 1) / RPW;
+    if (segs > most) segs = most;
+    int64_t per = (rows + segs - 1) / segs;
+    per = (per + RPW - 1) / RPW * RPW;
+    segs = (rows + per - 1) / per;
+    const int64_t units = tokens * segs;
+    kv_append_token_kernel<D, BF16, Q4, 4>
+        <<<static_cast<unsigned>((units + kWarps - 1) / kWarps), kKvThreads, 0, st>>>(
+            p, static_cast<int>(segs), static_cast<int>(per), units);
+    return cudaGetLastError() == cudaSuccess ? NSA_OK : NSA_ERR_LAUNCH;
+  }
   int64_t warps = g.groups;
-  if (warps > kAppendPerSm * kKvSms * kWarps) warps = kAppendPerSm * kKvSms * kWarps;
+  constexpr int64_t kMost = (Q4 ? kAppendPerSm4 : kAppendPerSm) * kKvSms * kWarps;
+  if (warps > kMost) warps = kMost;
   if (warps < g.per_token) warps = g.per_token;
   kv_append_kernel<D, BF16, Q4>
       <<<static_cast<unsigned>((warps + kWarps - 1) / kWarps), kKvThreads, 0, st>>>(p, g);
@@ -258,11 +396,14 @@ int launch_append(const AppendProblem& p, cudaStream_t st) {
 
 template <int D, bool BF16>
 int launch_read(const ReadProblem& p, bool q4, cudaStream_t st) {
-  const unsigned blocks = static_cast<unsigned>((p.chunks + 255) / 256);
+  int lanes = 32;  // a token's chunks, or a warp
+  while (lanes / 2 >= p.G * (D / 8)) lanes /= 2;
+  const unsigned blocks =
+      static_cast<unsigned>((static_cast<int64_t>(p.tokens) * lanes + 255) / 256);
   if (q4)
-    kv_read_kernel<D, BF16, true><<<blocks, 256, 0, st>>>(p);
+    kv_read_kernel<D, BF16, true><<<blocks, 256, 0, st>>>(p, lanes);
   else
-    kv_read_kernel<D, BF16, false><<<blocks, 256, 0, st>>>(p);
+    kv_read_kernel<D, BF16, false><<<blocks, 256, 0, st>>>(p, lanes);
   return cudaGetLastError() == cudaSuccess ? NSA_OK : NSA_ERR_LAUNCH;
 }
 
@@ -331,7 +472,7 @@ extern "C" int nsa_kv_read(const nsa_kv_cache* cache, const int32_t* page_table,
   if (rc != NSA_OK) return rc;
   if (B * M * G > (int64_t(1) << 34)) return NSA_ERR_SHAPE;
   if (B == 0 || M == 0) return NSA_OK;
-  if (!K || !V) return NSA_ERR_NULL;
+  if (!K || !V || !positions) return NSA_ERR_NULL;
   if (!aligned(K, 16) || !aligned(V, 16) || !aligned(positions, 4)) return NSA_ERR_ALIGN;
   ReadProblem p{};
   if ((rc = take_cache(cache, page_table, table_cols, B, G, D, false, &p.c)) != NSA_OK) return rc;
@@ -341,7 +482,7 @@ extern "C" int nsa_kv_read(const nsa_kv_cache* cache, const int32_t* page_table,
   p.v = static_cast<uint8_t*>(V);
   p.M = static_cast<int>(M);
   p.G = static_cast<int>(G);
-  p.chunks = B * M * G * (D / 8);
+  p.tokens = static_cast<uint32_t>(B * M);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = dtype == NSA_BF16, q4 = cache->bits == 4;
   if (D == 64) return bf ? launch_read<64, true>(p, q4, st) : launch_read<64, false>(p, q4, st);

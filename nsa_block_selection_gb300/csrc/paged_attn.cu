@@ -68,6 +68,7 @@ constexpr int kPaMostPerSm = 4;
 // keys take 0.3. (Shares by keys alone: a CTA with seven short items took 34 us
 // where the others took 13.)
 constexpr int kPaItemCost = 192;
+constexpr int kPaWhole = 512;     // keys of an item that is never cut
 constexpr int kPaLeast = 320;     // keys of a share at least, that cost among them
 constexpr float kPaSlack = 8.0f;
 
@@ -963,22 +964,45 @@ __global__ void __launch_bounds__(kPaThreads, PaCfg<D, Q4, NT>::kPerSm)
 }
 
 // Items that shares have cut: their pieces joined in order; items without a
-// tile: zeros. A CTA takes `rows_cta` rows of an item, D / 4 threads a row and
-// piece; with fewer rows than its threads could take, the pieces are dealt to
-// sets of them.
+// step: zeros. A CTA takes `rows_cta` rows of an item, D / 4 threads a row; the
+// pieces are dealt to the sets of threads that are left. A thread merges its
+// pieces as it loads them, statistics and values at once, four in flight: the
+// kernel is a chain of latencies (the counts, the pieces, the sets).
 constexpr int kJoinThreads = 256;
+
+struct PaPiece {
+  float m = -INFINITY, sum = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+
+  __device__ __forceinline__ void add(float2 s, float4 v) {
+    const float top = fmaxf(m, s.x);
+    const float f = m == top ? 1.f : ex2(m - top), g = s.x == top ? 1.f : ex2(s.x - top);
+    m = top;
+    sum = fmaf(sum, f, s.y * g);
+    o.x = fmaf(o.x, f, v.x * g), o.y = fmaf(o.y, f, v.y * g);
+    o.z = fmaf(o.z, f, v.z * g), o.w = fmaf(o.w, f, v.w * g);
+  }
+};
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kJoinThreads)
     paged_attn_join_kernel(const PagedProblem p, int rows_tile, int rows_cta) {
-  __shared__ float weight[8][kPaMostPerSm * kPaSms + 2];  // of a row's pieces
+  constexpr int kLanes = D / 4;  // threads of a row
   __shared__ float4 part[kJoinThreads];
-  __shared__ float2 total[8];  // (reference, sum) of a row
-  // (launched while the kernel before is at its end; its results are there from here on)
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  __shared__ float2 part_stat[kJoinThreads];
   const int item = blockIdx.x / p.groups, group = blockIdx.x - item * p.groups;
   const int piece_rows = p.heads_item * rows_tile;
   const int b = item / p.tiles, rt = item - b * p.tiles;
+  const int sets = kJoinThreads / (kLanes * rows_cta);
+  const int d = threadIdx.x % kLanes, lrow = threadIdx.x / kLanes % rows_cta;
+  const int set = threadIdx.x / (kLanes * rows_cta);
+  const int prow = blockIdx.y * rows_cta + lrow, hd = prow / rows_tile;
+  const int rw = rt * rows_tile + prow - hd * rows_tile;
+  const bool in = rw < p.rows;
+  const int mq = rw / p.hpg, h = (group * p.heads_item + hd) * p.hpg + rw - mq * p.hpg;
+  const bool padding = in && __ldg(p.pos + b * p.pos_b + mq) < 0;
+  // (launched while the kernel before is at its end; its results are there from here on)
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int64_t c0 = p.count[item], c1 = p.count[item + 1], per = p.count[p.items + 1];
   const int64_t n = c1 - c0 - p.item_cost;  // (below 0: no step)
   const int64_t at = c0 * p.groups + group * (c1 - c0) + p.item_cost;
@@ -987,67 +1011,40 @@ __global__ void __launch_bounds__(kJoinThreads)
   if (n > 0 && first == last) return;  // whole in one share
   const int pieces = n > 0 ? last - first + 1 : 0;
   const float* const stats = p.piece + 2 * static_cast<int64_t>(p.ctas) * piece_rows * D;
-  auto slot = [&](int i) { return 2 * static_cast<int64_t>(first + i) + (i == 0 ? 1 : 0); };
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int prow0 = blockIdx.y * rows_cta;
-  // a warp a row: the largest reference, the pieces' weights and the sum
-  if (warp < rows_cta) {
-    const int prow = prow0 + warp;
-    auto stat = [&](int i) {
-      return *reinterpret_cast<const float2*>(stats + (slot(i) * piece_rows + prow) * 2);
-    };
-    float m = -INFINITY, sum = 0.f;
-    const bool in = rt * rows_tile + prow % rows_tile < p.rows;  // (others have no piece)
-    if (in) {
-      for (int i = lane; i < pieces; i += 32) m = fmaxf(m, stat(i).x);
+  PaPiece a;
+  if (in) {
+    for (int i0 = set; i0 < pieces; i0 += 4 * sets) {
+      float2 s[4];
+      float4 v[4];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-      for (int i = lane; i < pieces; i += 32) {
-        const float2 s = stat(i);
-        const float w = s.x == m ? 1.f : ex2(s.x - m);
-        weight[warp][i] = w;
-        sum = fmaf(w, s.y, sum);
+      for (int k = 0; k < 4; ++k) {
+        const int i = i0 + k * sets;
+        s[k] = make_float2(-INFINITY, 0.f);
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < pieces) {
+          const int64_t row = (2 * static_cast<int64_t>(first + i) + (i == 0 ? 1 : 0)) * piece_rows + prow;
+          s[k] = *reinterpret_cast<const float2*>(stats + row * 2);
+          v[k] = reinterpret_cast<const float4*>(p.piece + row * D)[d];
+        }
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-    }
-    if (lane == 0) total[warp] = make_float2(m, sum);
-  }
-  __syncthreads();
-  constexpr int kLanes = D / 4;  // threads of a row
-  const int sets = kJoinThreads / (kLanes * rows_cta);
-  const int d = threadIdx.x % kLanes, lrow = threadIdx.x / kLanes % rows_cta;
-  const int set = threadIdx.x / (kLanes * rows_cta);
-  const int prow = prow0 + lrow, hd = prow / rows_tile;
-  const int rw = rt * rows_tile + prow - hd * rows_tile;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (rw < p.rows) {
-    for (int i = set; i < pieces; i += sets) {
-      const float4 v =
-          reinterpret_cast<const float4*>(p.piece + (slot(i) * piece_rows + prow) * D)[d];
-      const float w = weight[lrow][i];
-      o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y);
-      o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+      for (int k = 0; k < 4; ++k) a.add(s[k], v[k]);
     }
   }
-  part[threadIdx.x] = o;
+  part[threadIdx.x] = a.o;
+  part_stat[threadIdx.x] = make_float2(a.m, a.sum);
   __syncthreads();
-  if (set != 0 || rw >= p.rows) return;
+  if (set != 0 || !in) return;
   for (int k = 1; k < sets; ++k) {
-    const float4 v = part[threadIdx.x + k * kLanes * rows_cta];
-    o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+    const int t = threadIdx.x + k * kLanes * rows_cta;
+    a.add(part_stat[t], part[t]);
   }
-  float2 t = total[lrow];
-  const int mq = rw / p.hpg, h = (group * p.heads_item + hd) * p.hpg + rw - mq * p.hpg;
-  if (__ldg(p.pos + b * p.pos_b + mq) < 0) {  // padding
-    t.y = 0.f;
-    o = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  const float inv = t.y == 0.f ? 0.f : 1.f / t.y;
+  if (padding) a = PaPiece{};
+  const float inv = a.sum == 0.f ? 0.f : 1.f / a.sum;
   reinterpret_cast<uint2*>(p.o + ((static_cast<int64_t>(b) * p.M + mq) * p.H + h) * D)[d] =
-      make_uint2(pack2_t<BF16>(o.x * inv, o.y * inv), pack2_t<BF16>(o.z * inv, o.w * inv));
+      make_uint2(pack2_t<BF16>(a.o.x * inv, a.o.y * inv), pack2_t<BF16>(a.o.z * inv, a.o.w * inv));
   if (d == 0 && p.lse != nullptr)
-    p.lse[(static_cast<int64_t>(b) * p.H + h) * p.M + mq] = pa_lse(t.x, t.y);
+    p.lse[(static_cast<int64_t>(b) * p.H + h) * p.M + mq] = pa_lse(a.m, a.sum);
 }
 
 // ---- host ---------------------------------------------------------------
@@ -1220,11 +1217,18 @@ extern "C" int nsa_paged_attn(const void* Q, const nsa_kv_cache* cache, const in
   const int tile = rows_of_tile(p.rows);
   p.tiles = (p.rows + tile - 1) / tile;
   p.items = static_cast<int>(B * p.tiles);
-  p.cut = need > 0 && p.items * (table_cols * cache->page_size / kPaTile + 16) < int64_t(1) << 31;
+  // where every query sees few keys an item is short enough for one CTA, without a
+  // second kernel
+  int64_t most = table_cols * cache->page_size;
+  if (M == 1 && window_left >= 0 && window_left < most) {
+    const int64_t seen = window_left + 1 + sinks;
+    if (seen < most) most = seen;
+  }
+  p.cut = need > 0 && most > kPaWhole && p.items * (table_cols * cache->page_size / kPaTile + 16) < int64_t(1) << 31;
   // a window that reaches behind key 0 from any position; sinks as many as a table's tokens
-  const int64_t far = 0x7fffffff, most = int64_t(1) << 30;
+  const int64_t far = 0x7fffffff, tokens = int64_t(1) << 30;
   p.left = static_cast<int>(window_left < 0 || window_left > far ? far : window_left);
-  p.sinks = static_cast<int>(sinks > most ? most : sinks);
+  p.sinks = static_cast<int>(sinks > tokens ? tokens : sinks);
   const float sc = scale > 0.f ? scale : 1.0f / sqrtf(static_cast<float>(D));
   p.sl2 = sc * 1.4426950408889634f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -151,6 +151,56 @@ __device__ __forceinline__ int64_t token_position(const RopeProblem& p, int b, i
   return at;
 }
 
+// Rows [r0, r1) of one token's heads, UN groups of rows in flight per warp.
+template <int D, bool BF16, int UN>
+__device__ __forceinline__ void norm_rope_rows(const RopeProblem& p, const RopeRows& t, int b, int m,
+                                               int r0, int r1, bool live, bool rot, int c0, int c1,
+                                               const float* c, const float* s, bool norm = true) {
+  constexpr int LPR = D / 16, RPW = 32 / LPR;
+  const int sub = (threadIdx.x & 31) / LPR;
+  const uint8_t* x = t.x + 2 * (b * t.xb + m * t.xm);
+  uint8_t* y = t.y + 2 * (b * t.yb + m * t.ym);
+  float w[16];
+  if (live) load_weights<BF16>(t.w, p.w32, c0, c1, w);
+  for (int r = r0; r < r1; r += RPW * UN) {
+    uint4 v[UN][2];
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const int row = r + u * RPW + sub;
+      v[u][0] = v[u][1] = make_uint4(0, 0, 0, 0);
+      if (live && row < r1) {
+        const uint4* src = reinterpret_cast<const uint4*>(x + 2 * row * t.xh);
+        v[u][0] = src[c0];
+        v[u][1] = src[c1];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const int row = r + u * RPW + sub;
+      float f[16];
+      unpack8<BF16>(v[u][0], f);
+      unpack8<BF16>(v[u][1], f + 8);
+      if (norm) {
+        float sq = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sq = fmaf(f[i], f[i], sq);
+        sq = row_sum<LPR>(sq);
+        if (live) {  // a padding token's rows are zero
+          const float rs = rsqrtf(sq * (1.f / D) + p.eps);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) f[i] *= rs * w[i];
+        }
+      }
+      if (live && rot) turn(f, c, s, p.interleaved);
+      if (row < r1) {
+        uint4* dst = reinterpret_cast<uint4*>(y + 2 * row * t.yh);
+        dst[c0] = pack8<BF16>(f);
+        dst[c1] = pack8<BF16>(f + 8);
+      }
+    }
+  }
+}
+
 // How a warp's row slots map to (token, head) where a token has few heads: one
 // token to a group of slots, or several, with the heads rounded up to a power
 // of two; more heads than slots take several groups.
