@@ -696,12 +696,14 @@ int nsa_kv_read(const nsa_kv_cache* cache, const int32_t* page_table, const int3
                 int64_t positions_stride, int64_t table_cols, int dtype, void* stream);
 
 /*
- * nsa_paged_attn_workspace_bytes -- device workspace of nsa_paged_attn: 0 where
- * M H/G rows make more than 512 row tiles (of 8 rows, or 16 where there are
- * more than 8) in the batch, else up to 20 MB, whatever the lengths.
+ * nsa_paged_attn_workspace_bytes -- device workspace of nsa_paged_attn for a page
+ * table of `tokens` = table_cols * page_size tokens: 0 where a query sees at most
+ * 512 keys, or M H/G rows make more than 512 row tiles (of 8 rows, or 16 where
+ * there are more than 8) in the batch; else up to 20 MB, whatever the lengths.
  * Negative nsa_status for invalid sizes. Pure host arithmetic.
  */
-int64_t nsa_paged_attn_workspace_bytes(int64_t B, int64_t M, int64_t H, int64_t G, int64_t D);
+int64_t nsa_paged_attn_workspace_bytes(int64_t B, int64_t M, int64_t H, int64_t G, int64_t D,
+                                       int64_t tokens, int64_t window_left, int64_t sinks);
 
 /*
  * nsa_paged_attn -- attention of new tokens over the cache: the decoding step

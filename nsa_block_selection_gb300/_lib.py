@@ -129,7 +129,7 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.nsa_kv_read.restype = c_int
     lib.nsa_kv_read.argtypes = [vp] * 5 + [i64] * 6 + [c_int, vp]
     lib.nsa_paged_attn_workspace_bytes.restype = i64
-    lib.nsa_paged_attn_workspace_bytes.argtypes = [i64] * 5
+    lib.nsa_paged_attn_workspace_bytes.argtypes = [i64] * 8
     lib.nsa_paged_attn.restype = c_int
     lib.nsa_paged_attn.argtypes = [vp] * 6 + [i64] * 9 + [f32, c_int, vp, vp, i64, vp]
     if path is None:
@@ -832,41 +832,45 @@ class KvCache:
     def __init__(self, k, v, k_scale=None, v_scale=None):
         if _torch is None:
             _bind()
-        if k.dim() != 4 or k.shape != v.shape or k.dtype is not v.dtype:
+        shape, dev = k.shape, k.get_device()
+        if len(shape) != 4 or v.shape != shape or v.dtype is not k.dtype:
             raise ValueError("k and v must be alike, [pages, page_size, G, D]")
-        dev = k.get_device()
-        if (k_scale is None) != (v_scale is None):
-            raise ValueError("pass both scales (4 bits) or neither (16 bits)")
-        pages, page, G, D = k.shape
-        if k_scale is None:
+        pages, page, G, D = shape
+        if k_scale is None and v_scale is None:
             if k.dtype not in _F16_KINDS:
                 raise TypeError(f"a 16-bit cache must be fp16 or bf16, got {k.dtype}")
-            strides = []
-            for name, t in (("k", k), ("v", v)):
-                if t.get_device() != dev or dev < 0 or t.stride(3) != 1:
-                    raise ValueError(f"{name} must be on k's CUDA device, with a contiguous last "
-                                     "dimension")
-                # (the stride of a dimension of one is never used)
-                strides += [s if n > 1 else 0 for n, s in zip(t.shape[:3], t.stride()[:3])]
+            a, b, c, last = k.stride()
+            d, e, f, last_v = v.stride()
+            if dev < 0 or v.get_device() != dev or last != 1 or last_v != 1:
+                raise ValueError("k and v must be on one CUDA device, with a contiguous last "
+                                 "dimension")
+            # (the stride of a dimension of one is never used)
+            if pages < 2:
+                a = d = 0
+            if G < 2:
+                c = f = 0
+            self._tail = (pages, page, a, b, c, d, e, f, 16)
             self.bits = 16
+        elif k_scale is None or v_scale is None:
+            raise ValueError("pass both scales (4 bits) or neither (16 bits)")
         else:
-            D *= 2
             if k.dtype is not _torch.uint8:
                 raise TypeError(f"a 4-bit cache must be uint8, got {k.dtype}")
-            for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-                if t.dtype is not _torch.bfloat16:
-                    raise TypeError(f"{name} must be bf16, got {t.dtype}")
-                if t.shape != (pages, G, page, 2):
-                    raise ValueError(f"{name} must be [pages, G, page_size, 2]")
-            for name, t in (("k", k), ("v", v), ("k_scale", k_scale), ("v_scale", v_scale)):
+            bf16, scales = _torch.bfloat16, (pages, G, page, 2)
+            if k_scale.dtype is not bf16 or v_scale.dtype is not bf16:
+                raise TypeError("k_scale and v_scale must be bf16")
+            if k_scale.shape != scales or v_scale.shape != scales:
+                raise ValueError("k_scale and v_scale must be [pages, G, page_size, 2]")
+            for t in (k, v, k_scale, v_scale):
                 if t.get_device() != dev or dev < 0 or not t.is_contiguous():
-                    raise ValueError(f"{name} must be a contiguous tensor on k's CUDA device")
-            strides = [0] * 6
+                    raise ValueError("a 4-bit cache's tensors must be contiguous, on one CUDA "
+                                     "device")
+            D *= 2
+            self._tail = (pages, page, 0, 0, 0, 0, 0, 0, 4)
             self.bits = 4
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.page_size, self.kv_heads, self.head_dim = pages, page, G, D
         self._device = dev
-        self._tail = (pages, page, *strides, self.bits)
 
     def _struct(self):
         """nsa_kv_cache: thirteen 8-byte fields."""
@@ -941,18 +945,16 @@ def kv_append(q, k, v, cache: KvCache, page_table, positions=None, q_weight=None
         return _on_stream(stream, lambda k: kv_append(
             q, k, v, cache, page_table, positions, q_weight, k_weight, cos, sin, eps, interleaved,
             q_out), k)
-    if q is None:
-        q = q_out = k[:, :, :0]
-        H = 0
-    else:
-        if q_out is None:
-            q_out = _dense_like(q)
-        H = q.shape[2]
     own = (k.dtype,)
-    dev, sizes, code, wcode, strides = _check_rope(
-        (("q", q, own), ("k", k, own), ("q_out", q_out, own), ("v", v, own)), q_weight, k_weight,
-        cos, sin, positions)
-    B, M, _, G, D, R, rows, pstride = sizes
+    named = [("q", k[:, :, :0] if q is None else q, own), ("k", k, own)]
+    if q is not None and q_out is not None:
+        named.append(("q_out", q_out, own))
+        named.append(("v", v, own))
+    else:  # (places of q's shape and of k's take turns)
+        named.append(named[0])
+        named.append(("v", v, own))
+    dev, sizes, code, wcode, strides = _check_rope(named, q_weight, k_weight, cos, sin, positions)
+    B, M, H, G, D, R, rows, pstride = sizes
     if cache.kv_heads != G or cache.head_dim != D or (cache.bits == 16
                                                       and cache.k.dtype is not k.dtype):
         raise ValueError("the cache must have k's heads and entries, and with 16 bits its dtype")
@@ -963,10 +965,14 @@ def kv_append(q, k, v, cache: KvCache, page_table, positions=None, q_weight=None
     elif not eps >= 0:
         raise ValueError("eps must be >= 0, or None: no norm")
     cols, _ = _check_places(cache, page_table, positions, B, M, dev)
+    new = H and q_out is None
     if strides is not None:  # (q, k, q_out, v) -> (k, v, q, q_out)
         s = strides
-        strides = s[3:6] + s[9:12] + s[0:3] + s[6:9]
+        strides = s[3:6] + s[9:12] + s[0:3] + \
+            (array("q", (M * H * D, H * D, D)) if new else s[6:9])
     kv = cache._struct()
+    if new:
+        q_out = _torch.empty((B, M, H, D), dtype=q.dtype, device=q.device)
     st = _launch(dev, lib.nsa_kv_append, q.data_ptr() if H else None, k.data_ptr(), v.data_ptr(),
                  q_out.data_ptr() if H else None, kv.buffer_info()[0], page_table.data_ptr(),
                  _at(q_weight), _at(k_weight), _at(cos), _at(sin), _at(positions), B, M, H, G, D, R,
@@ -999,11 +1005,16 @@ def kv_read(cache: KvCache, page_table, positions, dtype=None, k_out=None, v_out
     dev = cache._device
     cols, pstride = _check_places(cache, page_table, positions, B, M, dev, need=True)
     shape = (B, M, cache.kv_heads, cache.head_dim)
+    given = []
     if k_out is None:
         k_out = _torch.empty(shape, dtype=dtype, device=cache.k.device)
+    else:
+        given.append(("k_out", k_out))
     if v_out is None:
-        v_out = _torch.empty(shape, dtype=dtype, device=cache.k.device)
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        v_out = _torch.empty_like(k_out)
+    else:
+        given.append(("v_out", v_out))
+    for name, t in given:
         if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or \
                 t.get_device() != dev:
             raise ValueError(f"{name} must be a contiguous {dtype} {shape} tensor on the cache's "
@@ -1017,8 +1028,9 @@ def kv_read(cache: KvCache, page_table, positions, dtype=None, k_out=None, v_out
     return k_out, v_out
 
 
-def paged_attn_workspace_bytes(B, M, H, G, D) -> int:
-    n = (_lib or load()).nsa_paged_attn_workspace_bytes(B, M, H, G, D)
+def paged_attn_workspace_bytes(B, M, H, G, D, tokens, window=(-1, 0), sinks=0) -> int:
+    """``tokens``: what a sequence's row of the page table can hold."""
+    n = (_lib or load()).nsa_paged_attn_workspace_bytes(B, M, H, G, D, tokens, window[0], sinks)
     if n < 0:
         raise NsaError(int(n), "nsa_paged_attn_workspace_bytes")
     return n
@@ -1039,7 +1051,7 @@ def paged_attn(q, cache: KvCache, page_table, positions, window=(-1, 0), sinks: 
     sequence has their pages; ``window`` = (left, 0), left negative: unbounded.
     Returns (O [B, M, H, D] of q's dtype, LSE fp32 [B, H, M] or None); O = 0 and
     LSE = -inf where a query sees nothing. ``workspace`` (CUDA uint8,
-    paged_attn_workspace_bytes) is allocated when omitted; calls that may
+    paged_attn_workspace_bytes) is allocated when omitted and needed; calls that may
     overlap need one each. Runs on torch's current stream, or on ``stream``.
     """
     lib = _bound or _bind()
@@ -1077,7 +1089,10 @@ def paged_attn(q, cache: KvCache, page_table, positions, window=(-1, 0), sinks: 
         b, m, h, _ = q.stride()
         strides = array("q", (b if B > 1 else 0, m if M > 1 else 0, h if H > 1 else 0))
     if workspace is None:
-        nbytes = paged_attn_workspace_bytes(B, M, H, cache.kv_heads, D)
+        nbytes = lib.nsa_paged_attn_workspace_bytes(B, M, H, cache.kv_heads, D,
+                                                    cols * cache.page_size, left, sinks)
+        if nbytes < 0:
+            raise NsaError(nbytes, "nsa_paged_attn_workspace_bytes")
         if nbytes:
             workspace = _torch.empty(nbytes, dtype=_torch.uint8, device=q.device)
     else:

@@ -1161,15 +1161,25 @@ int paged_read_and_clear_status(unsigned int* value) { return read_and_clear_sta
 }  // namespace nsa
 
 extern "C" int64_t nsa_paged_attn_workspace_bytes(int64_t B, int64_t M, int64_t H, int64_t G,
-                                                  int64_t D) {
+                                                  int64_t D, int64_t tokens, int64_t window_left,
+                                                  int64_t sinks) {
   using namespace nsa;
   const int rc = check_paged(B, M, H, G, D, NSA_F16);
   if (rc != NSA_OK) return rc;
+  if (tokens < 0 || sinks < 0) return NSA_ERR_SHAPE;
   const int64_t rows = M * (H / G), tile = rows_of_tile(rows);
   const int64_t items = B * ((rows + tile - 1) / tile);
   if (items == 0 || items > kPaItems) return 0;
+  // where every query sees few keys an item is short enough for one CTA, without a
+  // second kernel
+  if (M == 1 && window_left >= 0 && window_left < tokens && sinks < tokens &&
+      window_left + 1 + sinks < tokens)
+    tokens = window_left + 1 + sinks;
+  // (and the running count of steps has 32 bits)
+  if (tokens <= kPaWhole || items * (tokens / kPaTile + 16) >= int64_t(1) << 31) return 0;
   // two pieces of every share, and the running counts
-  return 2 * kPaMostPerSm * kPaSms * heads_of_item(G, D, 4) * tile * (D + 2) * 4 + (kPaItems + 2) * 8;
+  return 2 * kPaMostPerSm * kPaSms * heads_of_item(G, D, 4) * tile * (D + 2) * 4 +
+         (kPaItems + 2) * 8;
 }
 
 extern "C" int nsa_paged_attn(const void* Q, const nsa_kv_cache* cache, const int32_t* page_table,
@@ -1190,12 +1200,12 @@ extern "C" int nsa_paged_attn(const void* Q, const nsa_kv_cache* cache, const in
     return NSA_ERR_ALIGN;
   PagedProblem p{};
   if ((rc = take_cache(cache, page_table, table_cols, B, G, D, true, &p.c)) != NSA_OK) return rc;
-  const int64_t need = nsa_paged_attn_workspace_bytes(B, M, H, G, D);
+  const int64_t need = nsa_paged_attn_workspace_bytes(
+      B, M, H, G, D, table_cols * cache->page_size, window_left, sinks);
   if (need > 0) {
     if (!workspace || workspace_bytes < need) return NSA_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return NSA_ERR_ALIGN;
   }
-  // (the running count of tiles is 32 bits wide)
   p.q = static_cast<const uint8_t*>(Q);
   p.qb = s[0], p.qm = s[1], p.qh = s[2];
   p.o = static_cast<uint16_t*>(O);
@@ -1217,14 +1227,7 @@ extern "C" int nsa_paged_attn(const void* Q, const nsa_kv_cache* cache, const in
   const int tile = rows_of_tile(p.rows);
   p.tiles = (p.rows + tile - 1) / tile;
   p.items = static_cast<int>(B * p.tiles);
-  // where every query sees few keys an item is short enough for one CTA, without a
-  // second kernel
-  int64_t most = table_cols * cache->page_size;
-  if (M == 1 && window_left >= 0 && window_left < most) {
-    const int64_t seen = window_left + 1 + sinks;
-    if (seen < most) most = seen;
-  }
-  p.cut = need > 0 && most > kPaWhole && p.items * (table_cols * cache->page_size / kPaTile + 16) < int64_t(1) << 31;
+  p.cut = need > 0;
   // a window that reaches behind key 0 from any position; sinks as many as a table's tokens
   const int64_t far = 0x7fffffff, tokens = int64_t(1) << 30;
   p.left = static_cast<int>(window_left < 0 || window_left > far ? far : window_left);

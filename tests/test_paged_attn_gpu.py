@@ -120,8 +120,8 @@ def test_more_row_tiles_than_are_cut(bits):
 
     B, M = 130, 8  # 8 row tiles of 16 rows each
     q, cache, table, pos = _problem(2, M, 16, 1, 64, "f16", bits, 16, [90, 33], 21)
-    assert _lib.paged_attn_workspace_bytes(B, M, 16, 1, 64) == 0
-    assert _lib.paged_attn_workspace_bytes(2, M, 16, 1, 64) > 0
+    assert _lib.paged_attn_workspace_bytes(B, M, 16, 1, 64, 4096) == 0
+    assert _lib.paged_attn_workspace_bytes(2, M, 16, 1, 64, 4096) > 0
     few = _run(q, cache, table, pos, -1, 0, "f16")
     at = torch.arange(B, device="cuda") % 2
     many = _run(q[at].contiguous(), cache, table[at].contiguous(), pos[at].contiguous(), -1, 0, "f16")
