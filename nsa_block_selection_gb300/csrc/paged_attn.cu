@@ -32,9 +32,9 @@
 // the upper four bits of a byte, which Q's entries are divided by 16 for): a
 // mask, or a shift and a mask, makes two entries. Q's rows are scaled by a power
 // of two into fp16's range. For V, p' = 2^(x + log2 step - r) is the product's
-// operand (r follows x + log2 step), p = p' / step, and with
-// v = (low + 8 step) + step (c - 8) the sum of p (low + 8 step) - 8 p' is added
-// at the end, p' as rounded, so that its rounding falls on c - 8. A slot of the
+// operand (r follows x + log2 step) and p = p' / step; with
+// v = (low + 8 step) + step (c - 8) it sums p' (c - 8), and p (low + 8 step) is
+// summed beside it. A slot of the
 // CTA's one ring holds 128 rows, 32 for each warp, and the warps issue the copies
 // in turn: neighbouring heads of a token lie in one 128-byte line, so a CTA takes
 // two or four of them at once.
@@ -67,14 +67,17 @@ constexpr int kPaMostPerSm = 4;
 // copies one after the other, and the joining of the warps, some 4 us where 16
 // keys take 0.3. (Shares by keys alone: a CTA with seven short items took 34 us
 // where the others took 13.)
-constexpr int kPaItemCost = 192;
-constexpr int kPaWhole = 512;     // keys of an item that is never cut
-constexpr int kPaLeast = 320;     // keys of a share at least, that cost among them
+constexpr int kPaItemCost = 320;
+// Keys of an item that is never cut, and where there is an item for every SM.
+constexpr int kPaWhole = 512, kPaWholeMany = 2048;
+constexpr int kPaLeast = 448;     // keys of a share at least, that cost among them
 constexpr float kPaSlack = 8.0f;
 
 template <int D, bool Q4, int NT>
 struct PaCfg {
-  static constexpr int kPerSm = Q4 && (D == 64 || NT == 1) ? 4 : 3;  // CTAs
+  // CTAs of an SM. 16 bits: 128 KB of copies in flight (a token over 65,536 keys 44
+  // us; three CTAs 48); 4 bits: registers for two tiles at once
+  static constexpr int kPerSm = !Q4 ? 2 : D == 64 ? 4 : NT == 1 ? 3 : 2;
   // 16 bits: a ring for each warp, 16 keys of K and V in a slot. 4 bits: one for
   // the CTA, 128 rows of K and V and their scales in a slot, 32 for each warp.
   static constexpr int kStages = Q4 ? 3 : 2;
@@ -249,7 +252,7 @@ template <int D, int NT>
 struct PaRows {
   float acc[NT][D / 16][4];
   float ref[NT][2], neg[NT][2], l[NT][2];
-  float base_v[NT][2];  // 4 bits: sum of p (low + 8 step) - 8 p'
+  float base_v[NT][2];  // 4 bits: sum of p (low + 8 step)
   int pos[NT][2];
 
   __device__ __forceinline__ void clear() {
@@ -466,7 +469,13 @@ __device__ __forceinline__ void pa_scores4(const PaRows<D, NT>& a, const uint8_t
     }
 }
 
-// p' of a tile, its sums, and O^T.
+// p' of a tile, its sums, and O^T. The codes lose their mean in the product, by
+// operands of -8 (-128 for the upper ones): sums of p' c, all of one sign, would
+// grow with the keys, and what every addition to them loses with them, while
+// their difference from 8 sum p' does not. (Flat attention over 8192 keys: 0.6 %
+// of O instead of 0.17 with lower and upper codes in one sum.)
+constexpr uint32_t kLess8 = 0x80088008u, kLess128 = 0x80808080u;
+
 template <int D, int NT, bool EDGE>
 __device__ __forceinline__ void pa_values4(PaRows<D, NT>& a, const uint8_t* vt, const PaLanes& at,
                                            int n0, const PaSight& see, const float (&x)[NT][4],
@@ -490,14 +499,12 @@ __device__ __forceinline__ void pa_values4(PaRows<D, NT>& a, const uint8_t* vt, 
 #pragma unroll
     for (int i = 0; i < 4; ++i) e[i] = ex2(x[nt][i] + a.neg[nt][i & 1]);
     const uint32_t p0 = pack_half2(e[0], e[1]), p1 = pack_half2(e[2], e[3]);
-    const float2 r0 = unpack2<false>(p0), r1 = unpack2<false>(p1);
-    const float rounded[4] = {r0.x, r0.y, r1.x, r1.y};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float md = mid[i >> 1], pr = e[i] * rstep[i >> 1];
       if (EDGE && see.hidden(key + 8 * (i >> 1), a.pos[nt][i & 1])) md = pr = 0.f;
       a.l[nt][i & 1] += pr;
-      a.base_v[nt][i & 1] = fmaf(rounded[i], -8.f, fmaf(pr, md, a.base_v[nt][i & 1]));
+      a.base_v[nt][i & 1] = fmaf(pr, md, a.base_v[nt][i & 1]);
     }
     pf[nt][0] = movmatrix_t(p0);
     pf[nt][1] = movmatrix_t(p1);
@@ -509,15 +516,16 @@ __device__ __forceinline__ void pa_values4(PaRows<D, NT>& a, const uint8_t* vt, 
       const uint32_t sel = half ? 0x7632u : 0x5410u;
       const uint32_t u = __byte_perm(w[0][j], w[1][j], sel);
       const uint32_t v = __byte_perm(w[2][j], w[3][j], sel);
-      // whole bytes, lower code + 16 x upper (the sum of the uppers is taken off
-      // at the end): a byte moved into place needs no mask
-      const uint32_t u0 = u & 0x00ff00ffu, u1 = __byte_perm(u, 0u, 0x4341u);
-      const uint32_t v0 = v & 0x00ff00ffu, v1 = __byte_perm(v, 0u, 0x4341u);
+      const uint32_t u8 = u >> 8, v8 = v >> 8;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        mma_16816(a.acc[nt][4 * j + 2 * half], u0, u & 0x00f000f0u, v0, v & 0x00f000f0u, pf[nt][0],
+        float(&lo)[4] = a.acc[nt][4 * j + 2 * half];
+        float(&hi)[4] = a.acc[nt][4 * j + 2 * half + 1];
+        mma_16816(lo, kLess8, kLess128, kLess8, kLess128, pf[nt][0], pf[nt][1]);
+        mma_16816(lo, u & 0x000f000fu, u & 0x00f000f0u, v & 0x000f000fu, v & 0x00f000f0u, pf[nt][0],
                   pf[nt][1]);
-        mma_16816(a.acc[nt][4 * j + 2 * half + 1], u1, u1 & 0x00f000f0u, v1, v1 & 0x00f000f0u,
+        mma_16816(hi, kLess8, kLess128, kLess8, kLess128, pf[nt][0], pf[nt][1]);
+        mma_16816(hi, u8 & 0x000f000fu, u8 & 0x00f000f0u, v8 & 0x000f000fu, v8 & 0x00f000f0u,
                   pf[nt][0], pf[nt][1]);
       }
     }
@@ -531,7 +539,7 @@ __device__ __forceinline__ void pa_step4(PaRows<D, NT>& a, const uint8_t* slot,
                                          const int (&n0)[2], const uint32_t (&qf)[NT][D / 16][2],
                                          const float (&ka)[NT][2], const float (&kb)[NT][2],
                                          const PaSight& see) {
-  constexpr int kTogether = NT == 1 ? 2 : 1;
+  constexpr int kTogether = D == 64 && NT == 2 ? 1 : 2;
 #pragma unroll
   for (int u0 = 0; u0 < 2; u0 += kTogether) {
     float x[kTogether][NT][4], mid[kTogether][2], rstep[kTogether][2];
@@ -878,10 +886,10 @@ __global__ void __launch_bounds__(kPaThreads, PaCfg<D, Q4, NT>::kPerSm)
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           if constexpr (Q4) {
-            // byte i % 4 of word D / 64 r + i / 4 of a row: the whole byte, and its
-            // upper code 16 times as large
+            // byte i % 4 of word D / 64 r + i / 4 of a row: its lower code, and its
+            // upper, 16 times as large
             const int d = 8 * (D / 64 * r + (i >> 2)) + 2 * (i & 3);
-            dst[d] = fmaf(a.acc[nt][i][j] - a.acc[nt][i][j + 2], 16777216.f, a.base_v[nt][j]);
+            dst[d] = fmaf(a.acc[nt][i][j], 16777216.f, a.base_v[nt][j]);
             dst[d + 1] = fmaf(a.acc[nt][i][j + 2], 1048576.f, a.base_v[nt][j]);
           } else {
             dst[16 * i + r] = a.acc[nt][i][j];
@@ -1176,7 +1184,9 @@ extern "C" int64_t nsa_paged_attn_workspace_bytes(int64_t B, int64_t M, int64_t 
       window_left + 1 + sinks < tokens)
     tokens = window_left + 1 + sinks;
   // (and the running count of steps has 32 bits)
-  if (tokens <= kPaWhole || items * (tokens / kPaTile + 16) >= int64_t(1) << 31) return 0;
+  if (tokens <= (items * (G / heads_of_item(G, D, 4)) >= kPaSms ? kPaWholeMany : kPaWhole) ||
+      items * (tokens / kPaTile + 32) >= int64_t(1) << 31)
+    return 0;
   // two pieces of every share, and the running counts
   return 2 * kPaMostPerSm * kPaSms * heads_of_item(G, D, 4) * tile * (D + 2) * 4 +
          (kPaItems + 2) * 8;
