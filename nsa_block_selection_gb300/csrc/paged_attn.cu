@@ -1184,7 +1184,7 @@ extern "C" int64_t nsa_paged_attn_workspace_bytes(int64_t B, int64_t M, int64_t 
       window_left + 1 + sinks < tokens)
     tokens = window_left + 1 + sinks;
   // (and the running count of steps has 32 bits)
-  if (tokens <= (items * (G / heads_of_item(G, D, 4)) >= kPaSms ? kPaWholeMany : kPaWhole) ||
+  if (tokens <= (items * G >= kPaSms ? kPaWholeMany : kPaWhole) ||
       items * (tokens / kPaTile + 32) >= int64_t(1) << 31)
     return 0;
   // two pieces of every share, and the running counts
