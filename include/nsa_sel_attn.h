@@ -711,7 +711,8 @@ int64_t nsa_paged_attn_workspace_bytes(int64_t B, int64_t M, int64_t H, int64_t 
  * stored their own keys and values.
  *
  *   Q              device, dtype, [B, M, H, D]; q_strides: host array of 3
- *                  element strides (b, m, head), multiples of 8, or NULL
+ *                  element strides (b, m, head), multiples of 8 and not 0 for a
+ *                  dimension of more than one, or NULL
  *   positions      device, int32, not NULL: as for nsa_kv_append; negative:
  *                  padding; at most 2^31 - 32
  *   O              device, dtype, [B, M, H, D], contiguous (output)

@@ -17,7 +17,6 @@
 #include "rope.cuh"
 
 namespace nsa {
-namespace {
 
 // A step below this is stored as 0, and the row is its low alone: a step's
 // reciprocal, and the logarithm that the attention folds it into p by, stay
@@ -83,5 +82,4 @@ inline int take_cache(const nsa_kv_cache* kv, const int32_t* table, int64_t cols
   return NSA_OK;
 }
 
-}  // namespace
 }  // namespace nsa

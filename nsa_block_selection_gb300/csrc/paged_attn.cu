@@ -50,28 +50,12 @@
 #include "common.cuh"
 #include "kv_cache.cuh"
 #include "nsa_sel_attn.h"
+#include "paged_attn.cuh"
 #include "ptx.cuh"
 #include "status.cuh"
 
 namespace nsa {
 namespace {
-
-constexpr int kPaWarps = 4;
-constexpr int kPaThreads = 32 * kPaWarps;
-constexpr int kPaTile = 16;       // keys of a tile
-constexpr int kPaSlotRows = 128;  // (head, key) rows of a 4-bit slot
-constexpr int kPaItems = 512;     // row tiles of a batch that shares are formed of
-constexpr int kPaSms = 152;
-constexpr int kPaMostPerSm = 4;
-// What an item costs beside its keys, in keys: its positions, pages and first
-// copies one after the other, and the joining of the warps, some 4 us where 16
-// keys take 0.3. (Shares by keys alone: a CTA with seven short items took 34 us
-// where the others took 13.)
-constexpr int kPaItemCost = 320;
-// Keys of an item that is never cut, and where there is an item for every SM.
-constexpr int kPaWhole = 512, kPaWholeMany = 2048;
-constexpr int kPaLeast = 448;     // keys of a share at least, that cost among them
-constexpr float kPaSlack = 8.0f;
 
 template <int D, bool Q4, int NT>
 struct PaCfg {
@@ -95,156 +79,6 @@ struct PaCfg {
   static constexpr int kOffCount = kOffKey + kRings * kStages * kKeys * 4;
   static constexpr int kSmem = kOffCount + (kPaItems + 1) * 4 + 1024;
 };
-
-// First key of a tile that is not there, past every position.
-constexpr int kNoKey = 0x7ffffff0, kPaFar = 0x7fffffe0;
-
-struct PagedProblem {
-  KvPages c;
-  const uint8_t* q;
-  int64_t qb, qm, qh;  // element strides
-  uint16_t* o;         // [B, M, H, D]
-  float* lse;          // [B, H, M] or NULL
-  const int32_t* pos;
-  int64_t pos_b;
-  // [2 ctas][rows of an item][D], then [2 ctas][rows of an item][2] (reference, sum)
-  float* piece;
-  int64_t* count;     // [items + 1]: running steps of the items, and a share's steps
-  int B, M, H, G, hpg, rows, tiles, items;  // rows of a KV head, row tiles, B * tiles
-  int left, sinks, ctas;
-  int heads_item, groups;  // KV heads of an item, G / heads_item
-  int step_shift;          // keys of a step: 16; 4 bits: 128 / heads_item
-  int item_cost;           // kPaItemCost in steps
-  int split;               // 4 bits: copies that a step's keys take (small pages)
-  float sl2;
-  bool cut;
-};
-
-// What a row tile of a sequence has to read: n steps of 1 << shift keys, of which
-// the first `st` start at key 0 and the others `jump` steps further on.
-struct PaSpan {
-  int n, st, jump, shift;
-  int lo_pos, hi_pos;  // smallest and largest position of its queries
-  __device__ __forceinline__ int key(int t) const { return (t < st ? t : t + jump) << shift; }
-};
-
-// A query's position (one at the end of int32 as kPaFar: kNoKey is past them all).
-__device__ __forceinline__ int pa_position(const PagedProblem& p, int b, int m) {
-  return min(__ldg(p.pos + b * p.pos_b + m), kPaFar);
-}
-
-__device__ __forceinline__ PaSpan pa_span(const PagedProblem& p, int b, int rt, int rows_tile) {
-  const int r0 = rt * rows_tile, r1 = min(r0 + rows_tile, p.rows) - 1;
-  PaSpan s{0, 0, 0, p.step_shift, 0x7fffffff, -1};
-  const int m1 = r1 / p.hpg;
-  for (int m = r0 / p.hpg; m <= m1; ++m) {
-    const int at = pa_position(p, b, m);
-    if (at < 0) continue;
-    s.lo_pos = min(s.lo_pos, at);
-    s.hi_pos = max(s.hi_pos, at);
-  }
-  if (s.hi_pos < 0) return s;
-  const int last = min(s.hi_pos, (p.c.cols << p.c.shift) - 1) >> s.shift;  // (at most 2^30 tokens)
-  const int first = (p.left < s.lo_pos ? s.lo_pos - p.left : 0) >> s.shift;
-  s.st = min((p.sinks + (1 << s.shift) - 1) >> s.shift, last + 1);
-  if (first <= s.st) {
-    s.n = last + 1;
-  } else if (first > last) {  // the window lies behind the table's end
-    s.n = s.st;
-  } else {
-    s.jump = first - s.st;
-    s.n = s.st + last - first + 1;
-  }
-  return s;
-}
-
-// What the queries of a row tile see of a key.
-struct PaSight {
-  int lo_pos, hi_pos, left, sinks;
-  // no query sees it: its row may hold anything
-  __device__ __forceinline__ bool nobody(int key) const {
-    return key > hi_pos || (key < lo_pos - left && key >= sinks);
-  }
-  // every query sees the tile from n0 on
-  __device__ __forceinline__ bool all(int n0) const {
-    return n0 + kPaTile - 1 <= lo_pos && (n0 >= hi_pos - left || n0 + kPaTile <= sinks);
-  }
-  // no query sees a key of the tile
-  __device__ __forceinline__ bool nothing(int n0) const {
-    return n0 > hi_pos || (n0 + kPaTile - 1 < lo_pos - left && n0 >= sinks);
-  }
-  __device__ __forceinline__ bool hidden(int key, int pos) const {
-    return key > pos || (key < pos - left && key >= sinks);
-  }
-};
-
-// A CTA's share of the steps of all items, KV-head groups innermost.
-struct PaShare {
-  int64_t begin, end;  // steps
-  int64_t at;          // the first step of the item that holds `begin`
-  int item, group;
-};
-
-template <int kRowsTile>
-__device__ __forceinline__ PaShare pa_share(const PagedProblem& p, int* count, int* sums) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // the running count of the items' steps, a run of items to a thread
-  const int run = (p.items + kPaThreads - 1) / kPaThreads;
-  const int i0 = min(static_cast<int>(threadIdx.x) * run, p.items), i1 = min(i0 + run, p.items);
-  int mine = 0;
-  for (int i = i0; i < i1; ++i) {
-    count[i] = mine;
-    const int n = pa_span(p, i / p.tiles, i % p.tiles, kRowsTile).n;
-    mine += n > 0 ? n + p.item_cost : 0;
-  }
-  int scan = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(kFull, scan, o);
-    if (lane >= o) scan += v;
-  }
-  if (lane == 31) sums[warp] = scan;
-  __syncthreads();
-  int before = scan - mine;
-  for (int w = 0; w < warp; ++w) before += sums[w];
-  for (int i = i0; i < i1; ++i) count[i] += before;
-  if (i0 < i1 && i1 == p.items) count[p.items] = before + mine;
-  __syncthreads();
-  const int64_t all = static_cast<int64_t>(count[p.items]) * p.groups;
-  int64_t per = (all + p.ctas - 1) / p.ctas;
-  per = max(per, static_cast<int64_t>(kPaLeast >> p.step_shift));
-  PaShare s{min(all, static_cast<int64_t>(blockIdx.x) * per), 0, 0, 0, 0};
-  s.end = min(all, s.begin + per);
-  if (blockIdx.x == 0) {
-    for (int i = threadIdx.x; i <= p.items; i += kPaThreads) p.count[i] = count[i];
-    if (threadIdx.x == 0) p.count[p.items + 1] = per;
-  }
-  if (s.begin < s.end) {  // the item that holds step `begin`
-    int lo = 0, hi = p.items - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (static_cast<int64_t>(count[mid]) * p.groups <= s.begin) lo = mid;
-      else hi = mid - 1;
-    }
-    s.item = lo;
-    const int n = count[lo + 1] - count[lo];  // (its cost among them)
-    const int64_t first = static_cast<int64_t>(count[lo]) * p.groups;
-    s.group = static_cast<int>((s.begin - first) / n);
-    s.at = first + static_cast<int64_t>(s.group) * n;
-  }
-  return s;
-}
-
-__device__ __forceinline__ float rcp_approx(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float lg2_approx(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // The state of one warp's rows: column 2 c + j of n-tile nt belongs to lanes of
 // c = lane % 4; rows of O^T to lane / 4.
@@ -454,8 +288,8 @@ __device__ __forceinline__ void pa_scores4(const PaRows<D, NT>& a, const uint8_t
     kstep[j] = __uint_as_float(ks[j] << 16);
     klow[j] = __uint_as_float(ks[j] & 0xffff0000u);
     const float step = __uint_as_float(vs[j] << 16);
-    mid[j] = fmaf(8.f, step, __uint_as_float(vs[j] & 0xffff0000u));
-    const float any = step == 0.f ? 1.f : step;  // (all codes are 0 then)
+    const float any = step == 0.f ? 1.f : step;  // (all codes are 0 then: any step serves)
+    mid[j] = fmaf(8.f, any, __uint_as_float(vs[j] & 0xffff0000u));
     rstep[j] = rcp_approx(any);
     lstep[j] = lg2_approx(any);
   }
@@ -627,10 +461,6 @@ __device__ __forceinline__ void pa_queries(const PagedProblem& p, int b, int rt,
   }
 }
 
-__device__ __forceinline__ float pa_lse(float ref, float sum) {
-  return sum == 0.f ? -INFINITY : (ref + __log2f(sum)) * 0.69314718055994530942f;
-}
-
 template <int D, bool BF16, bool Q4, int NT>
 __global__ void __launch_bounds__(kPaThreads, PaCfg<D, Q4, NT>::kPerSm)
     paged_attn_kernel(const PagedProblem p, const __grid_constant__ CUtensorMap tmK,
@@ -662,7 +492,7 @@ __global__ void __launch_bounds__(kPaThreads, PaCfg<D, Q4, NT>::kPerSm)
   PaShare sh{0, 0, 0, 0, 0};
   asm volatile("griddepcontrol.launch_dependents;\n");  // the join waits for this grid's end
   if (p.cut) {
-    sh = pa_share<kRowsTile>(p, count, reinterpret_cast<int*>(stat));
+    sh = pa_share<kPaThreads>(p, kRowsTile, count, reinterpret_cast<int*>(stat));
   } else {
     sh.item = blockIdx.x / p.groups;
     sh.group = blockIdx.x - sh.item * p.groups;
@@ -1006,7 +836,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int set = threadIdx.x / (kLanes * rows_cta);
   const int prow = blockIdx.y * rows_cta + lrow, hd = prow / rows_tile;
   const int rw = rt * rows_tile + prow - hd * rows_tile;
-  const bool in = rw < p.rows;
+  const bool in = prow < piece_rows && rw < p.rows;
   const int mq = rw / p.hpg, h = (group * p.heads_item + hd) * p.hpg + rw - mq * p.hpg;
   const bool padding = in && __ldg(p.pos + b * p.pos_b + mq) < 0;
   // (launched while the kernel before is at its end; its results are there from here on)
@@ -1057,8 +887,13 @@ __global__ void __launch_bounds__(kJoinThreads)
 
 // ---- host ---------------------------------------------------------------
 
-// Row tiles: 8 rows where a KV head has no more, else 16.
-int rows_of_tile(int64_t rows) { return rows <= 8 ? 8 : 16; }
+// Row tiles: 8 rows where a KV head has no more, else 16; from kTcRows rows on
+// whole queries of up to 128 (paged_attn_tc_kernel).
+constexpr int64_t kTcRows = 17;
+bool many_rows(int64_t rows, int64_t hpg) { return rows >= kTcRows && hpg <= 128; }
+int rows_of_tile(int64_t rows, int64_t hpg) {
+  return rows <= 8 ? 8 : many_rows(rows, hpg) ? tc_rows_of_tile(hpg) : 16;
+}
 
 // KV heads of an item. The rows of a 4-bit cache are 64 or 32 bytes for each
 // head of a token, but what comes from memory is 128: neighbouring heads are
@@ -1093,8 +928,34 @@ int check_paged(int64_t B, int64_t M, int64_t H, int64_t G, int64_t D, int dtype
   if (rc != NSA_OK) return rc;
   if (H % G != 0) return NSA_ERR_GROUPS;
   if (M * (H / G) >= int64_t(1) << 30) return NSA_ERR_SHAPE;
-  const int64_t rows = M * (H / G), tile = rows_of_tile(rows);
+  const int64_t rows = M * (H / G), tile = rows_of_tile(rows, H / G);
   if (B * ((rows + tile - 1) / tile) * G >= int64_t(1) << 31) return NSA_ERR_SHAPE;
+  return NSA_OK;
+}
+
+// The pieces of items that shares have cut.
+template <int D, bool BF16>
+int launch_join(const PagedProblem& p, int rows_tile, cudaStream_t st) {
+  if (!p.cut) return NSA_OK;
+  // rows of a CTA: as many as leave a CTA for each SM, so that few items
+  // have their many pieces added by many threads
+  const int rows = p.heads_item * rows_tile;
+  int rows_cta = 1024 / D;  // a thread for every four entries
+  while (rows_cta > 1 && static_cast<int64_t>(p.items) * p.groups * (rows / rows_cta) < kPaSms)
+    rows_cta >>= 1;
+  if (rows_cta > 8) rows_cta = 8;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.items * p.groups), (rows + rows_cta - 1) / rows_cta);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<D, BF16>, PagedProblem(p), rows_tile,
+                         rows_cta) != cudaSuccess)
+    return NSA_ERR_LAUNCH;
   return NSA_OK;
 }
 
@@ -1111,32 +972,15 @@ int launch_paged(PagedProblem& p, const CUtensorMap& tk, const CUtensorMap& tv, 
   const int64_t blocks = p.cut ? p.ctas : static_cast<int64_t>(p.items) * p.groups;
   kern<<<static_cast<unsigned>(blocks), kPaThreads, C::kSmem, st>>>(p, tk, tv);
   if (cudaGetLastError() != cudaSuccess) return NSA_ERR_LAUNCH;
-  if (p.cut) {
-    // rows of a CTA: as many as leave a CTA for each SM, so that few items
-    // have their many pieces added by many threads
-    const int rows = p.heads_item * 8 * NT;
-    int rows_cta = 1024 / D;  // a thread for every four entries
-    while (rows_cta > 1 && static_cast<int64_t>(p.items) * p.groups * (rows / rows_cta) < kPaSms)
-      rows_cta >>= 1;
-    if (rows_cta > 8) rows_cta = 8;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.items * p.groups), rows / rows_cta);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<D, BF16>, PagedProblem(p), 8 * NT,
-                           rows_cta) != cudaSuccess)
-      return NSA_ERR_LAUNCH;
-  }
-  return NSA_OK;
+  return launch_join<D, BF16>(p, 8 * NT, st);
 }
 
 template <int D, bool BF16>
 int launch_paged_d(PagedProblem& p, const nsa_kv_cache* kv, cudaStream_t st) {
+  if (many_rows(p.rows, p.hpg)) {
+    const int rc = launch_paged_tc(p, kv, D, BF16, st);
+    return rc != NSA_OK ? rc : launch_join<D, BF16>(p, tc_rows_of_tile(p.hpg), st);
+  }
   CUtensorMap tk, tv;
   if (kv->bits == 4) {
     const int wide = kPaSlotRows / p.heads_item, page = 1 << p.c.shift;
@@ -1155,7 +999,7 @@ int launch_paged_d(PagedProblem& p, const nsa_kv_cache* kv, cudaStream_t st) {
                                p.c.vt / 2, p.c.vh / 2))
       return NSA_ERR_LAUNCH;
   }
-  if (rows_of_tile(p.rows) == 8)
+  if (p.rows <= 8)
     return kv->bits == 4 ? launch_paged<D, BF16, true, 1>(p, tk, tv, st)
                          : launch_paged<D, BF16, false, 1>(p, tk, tv, st);
   return kv->bits == 4 ? launch_paged<D, BF16, true, 2>(p, tk, tv, st)
@@ -1164,7 +1008,14 @@ int launch_paged_d(PagedProblem& p, const nsa_kv_cache* kv, cudaStream_t st) {
 
 }  // namespace
 
-int paged_read_and_clear_status(unsigned int* value) { return read_and_clear_status(value); }
+int paged_read_and_clear_status(unsigned int* value) {
+  unsigned int tc = 0u;
+  const int rc = read_and_clear_status(value);
+  if (rc != NSA_OK) return rc;
+  const int rt = paged_tc_read_and_clear_status(&tc);
+  *value |= tc;
+  return rt;
+}
 
 }  // namespace nsa
 
@@ -1175,7 +1026,7 @@ extern "C" int64_t nsa_paged_attn_workspace_bytes(int64_t B, int64_t M, int64_t 
   const int rc = check_paged(B, M, H, G, D, NSA_F16);
   if (rc != NSA_OK) return rc;
   if (tokens < 0 || sinks < 0) return NSA_ERR_SHAPE;
-  const int64_t rows = M * (H / G), tile = rows_of_tile(rows);
+  const int64_t rows = M * (H / G), tile = rows_of_tile(rows, H / G);
   const int64_t items = B * ((rows + tile - 1) / tile);
   if (items == 0 || items > kPaItems) return 0;
   // where every query sees few keys an item is short enough for one CTA, without a
@@ -1188,8 +1039,9 @@ extern "C" int64_t nsa_paged_attn_workspace_bytes(int64_t B, int64_t M, int64_t 
       items * (tokens / kPaTile + 32) >= int64_t(1) << 31)
     return 0;
   // two pieces of every share, and the running counts
-  return 2 * kPaMostPerSm * kPaSms * heads_of_item(G, D, 4) * tile * (D + 2) * 4 +
-         (kPaItems + 2) * 8;
+  const int64_t pieces = many_rows(rows, H / G) ? 2 * kPaSms * tile
+                                                : 2 * kPaMostPerSm * kPaSms * heads_of_item(G, D, 4) * tile;
+  return pieces * (D + 2) * 4 + (kPaItems + 2) * 8;
 }
 
 extern "C" int nsa_paged_attn(const void* Q, const nsa_kv_cache* cache, const int32_t* page_table,
@@ -1203,7 +1055,7 @@ extern "C" int nsa_paged_attn(const void* Q, const nsa_kv_cache* cache, const in
   if (rc != NSA_OK) return rc;
   if (positions_stride < 0 || sinks < 0) return NSA_ERR_SHAPE;
   int64_t s[3];
-  if ((rc = take_strides(q_strides, 1, &H, B, M, D, s, 0)) != NSA_OK) return rc;
+  if ((rc = take_strides(q_strides, 1, &H, B, M, D, s, 1)) != NSA_OK) return rc;
   if (B == 0 || M == 0) return NSA_OK;
   if (!Q || !O || !positions) return NSA_ERR_NULL;
   if (!aligned(Q, 16) || !aligned(O, 16) || !aligned(LSE, 4) || !aligned(positions, 4))
@@ -1230,11 +1082,13 @@ extern "C" int nsa_paged_attn(const void* Q, const nsa_kv_cache* cache, const in
   p.G = static_cast<int>(G);
   p.hpg = static_cast<int>(H / G);
   p.rows = static_cast<int>(M * (H / G));
-  p.heads_item = heads_of_item(G, D, cache->bits);
+  const bool many = many_rows(p.rows, p.hpg);
+  p.heads_item = many ? 1 : heads_of_item(G, D, cache->bits);
   p.groups = p.G / p.heads_item;
-  p.step_shift = cache->bits == 16 ? 4 : p.heads_item == 1 ? 7 : p.heads_item == 2 ? 6 : 5;
-  p.item_cost = (kPaItemCost + (1 << p.step_shift) - 1) >> p.step_shift;
-  const int tile = rows_of_tile(p.rows);
+  p.step_shift =
+      many ? 7 : cache->bits == 16 ? 4 : p.heads_item == 1 ? 7 : p.heads_item == 2 ? 6 : 5;
+  p.item_cost = ((many ? kTcItemCost : kPaItemCost) + (1 << p.step_shift) - 1) >> p.step_shift;
+  const int tile = rows_of_tile(p.rows, p.hpg);
   p.tiles = (p.rows + tile - 1) / tile;
   p.items = static_cast<int>(B * p.tiles);
   p.cut = need > 0;

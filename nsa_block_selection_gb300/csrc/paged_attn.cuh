@@ -1,0 +1,198 @@
+// What the kernels of the attention over pages share: the problem, what a row tile
+// sees and has to read, and the CTAs' shares of it.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+#include "kv_cache.cuh"
+#include "nsa_sel_attn.h"
+
+namespace nsa {
+
+constexpr int kPaWarps = 4;
+constexpr int kPaThreads = 32 * kPaWarps;
+constexpr int kPaTile = 16;       // keys of a tile
+constexpr int kPaSlotRows = 128;  // (head, key) rows of a 4-bit slot
+constexpr int kPaItems = 512;     // row tiles of a batch that shares are formed of
+constexpr int kPaSms = 152;
+constexpr int kPaMostPerSm = 4;
+// What an item costs beside its keys, in keys: its positions, pages and first
+// copies one after the other, and the joining of the warps, some 4 us where 16
+// keys take 0.3. (Shares by keys alone: a CTA with seven short items took 34 us
+// where the others took 13.)
+constexpr int kPaItemCost = 320;
+// Keys of an item that is never cut, and where there is an item for every SM.
+constexpr int kPaWhole = 512, kPaWholeMany = 2048;
+constexpr int kTcItemCost = 768;  // the same of paged_attn_tc_kernel, whose steps are faster
+constexpr int kPaLeast = 448;     // keys of a share at least, that cost among them
+constexpr float kPaSlack = 8.0f;
+
+// First key of a tile that is not there, past every position.
+constexpr int kNoKey = 0x7ffffff0, kPaFar = 0x7fffffe0;
+
+struct PagedProblem {
+  KvPages c;
+  const uint8_t* q;
+  int64_t qb, qm, qh;  // element strides
+  uint16_t* o;         // [B, M, H, D]
+  float* lse;          // [B, H, M] or NULL
+  const int32_t* pos;
+  int64_t pos_b;
+  // [2 ctas][rows of an item][D], then [2 ctas][rows of an item][2] (reference, sum)
+  float* piece;
+  int64_t* count;     // [items + 1]: running steps of the items, and a share's steps
+  int B, M, H, G, hpg, rows, tiles, items;  // rows of a KV head, row tiles, B * tiles
+  int left, sinks, ctas;
+  int heads_item, groups;  // KV heads of an item, G / heads_item
+  int step_shift;          // keys of a step: 16; 4 bits: 128 / heads_item
+  int item_cost;           // kPaItemCost in steps
+  int split;               // 4 bits: copies that a step's keys take (small pages)
+  float sl2;
+  bool cut;
+};
+
+// What a row tile of a sequence has to read: n steps of 1 << shift keys, of which
+// the first `st` start at key 0 and the others `jump` steps further on.
+struct PaSpan {
+  int n, st, jump, shift;
+  int lo_pos, hi_pos;  // smallest and largest position of its queries
+  __device__ __forceinline__ int key(int t) const { return (t < st ? t : t + jump) << shift; }
+};
+
+// A query's position (one at the end of int32 as kPaFar: kNoKey is past them all).
+__device__ __forceinline__ int pa_position(const PagedProblem& p, int b, int m) {
+  return min(__ldg(p.pos + b * p.pos_b + m), kPaFar);
+}
+
+__device__ __forceinline__ PaSpan pa_span(const PagedProblem& p, int b, int rt, int rows_tile) {
+  const int r0 = rt * rows_tile, r1 = min(r0 + rows_tile, p.rows) - 1;
+  PaSpan s{0, 0, 0, p.step_shift, 0x7fffffff, -1};
+  const int m1 = r1 / p.hpg;
+  for (int m = r0 / p.hpg; m <= m1; ++m) {
+    const int at = pa_position(p, b, m);
+    if (at < 0) continue;
+    s.lo_pos = min(s.lo_pos, at);
+    s.hi_pos = max(s.hi_pos, at);
+  }
+  if (s.hi_pos < 0) return s;
+  const int last = min(s.hi_pos, (p.c.cols << p.c.shift) - 1) >> s.shift;  // (at most 2^30 tokens)
+  const int first = (p.left < s.lo_pos ? s.lo_pos - p.left : 0) >> s.shift;
+  s.st = min((p.sinks + (1 << s.shift) - 1) >> s.shift, last + 1);
+  if (first <= s.st) {
+    s.n = last + 1;
+  } else if (first > last) {  // the window lies behind the table's end
+    s.n = s.st;
+  } else {
+    s.jump = first - s.st;
+    s.n = s.st + last - first + 1;
+  }
+  return s;
+}
+
+// What the queries of a row tile see of a key.
+struct PaSight {
+  int lo_pos, hi_pos, left, sinks;
+  // no query sees it: its row may hold anything
+  __device__ __forceinline__ bool nobody(int key) const {
+    return key > hi_pos || (key < lo_pos - left && key >= sinks);
+  }
+  // every query sees the tile from n0 on
+  __device__ __forceinline__ bool all(int n0) const {
+    return n0 + kPaTile - 1 <= lo_pos && (n0 >= hi_pos - left || n0 + kPaTile <= sinks);
+  }
+  // no query sees a key of the tile
+  __device__ __forceinline__ bool nothing(int n0) const {
+    return n0 > hi_pos || (n0 + kPaTile - 1 < lo_pos - left && n0 >= sinks);
+  }
+  __device__ __forceinline__ bool hidden(int key, int pos) const {
+    return key > pos || (key < pos - left && key >= sinks);
+  }
+};
+
+// A CTA's share of the steps of all items, KV-head groups innermost.
+struct PaShare {
+  int64_t begin, end;  // steps
+  int64_t at;          // the first step of the item that holds `begin`
+  int item, group;
+};
+
+// `count` [items + 1] and `sums` (one of each warp) are shared memory; all threads of
+// a CTA of kThreads.
+template <int kThreads>
+__device__ __forceinline__ PaShare pa_share(const PagedProblem& p, int rows_tile, int* count,
+                                            int* sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // the running count of the items' steps, a run of items to a thread
+  const int run = (p.items + kThreads - 1) / kThreads;
+  const int i0 = min(static_cast<int>(threadIdx.x) * run, p.items), i1 = min(i0 + run, p.items);
+  int mine = 0;
+  for (int i = i0; i < i1; ++i) {
+    count[i] = mine;
+    const int n = pa_span(p, i / p.tiles, i % p.tiles, rows_tile).n;
+    mine += n > 0 ? n + p.item_cost : 0;
+  }
+  int scan = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kFull, scan, o);
+    if (lane >= o) scan += v;
+  }
+  if (lane == 31) sums[warp] = scan;
+  __syncthreads();
+  int before = scan - mine;
+  for (int w = 0; w < warp; ++w) before += sums[w];
+  for (int i = i0; i < i1; ++i) count[i] += before;
+  if (i0 < i1 && i1 == p.items) count[p.items] = before + mine;
+  __syncthreads();
+  const int64_t all = static_cast<int64_t>(count[p.items]) * p.groups;
+  int64_t per = (all + p.ctas - 1) / p.ctas;
+  per = max(per, static_cast<int64_t>(kPaLeast >> p.step_shift));
+  PaShare s{min(all, static_cast<int64_t>(blockIdx.x) * per), 0, 0, 0, 0};
+  s.end = min(all, s.begin + per);
+  if (blockIdx.x == 0) {
+    for (int i = threadIdx.x; i <= p.items; i += kThreads) p.count[i] = count[i];
+    if (threadIdx.x == 0) p.count[p.items + 1] = per;
+  }
+  if (s.begin < s.end) {  // the item that holds step `begin`
+    int lo = 0, hi = p.items - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (static_cast<int64_t>(count[mid]) * p.groups <= s.begin) lo = mid;
+      else hi = mid - 1;
+    }
+    s.item = lo;
+    const int n = count[lo + 1] - count[lo];  // (its cost among them)
+    const int64_t first = static_cast<int64_t>(count[lo]) * p.groups;
+    s.group = static_cast<int>((s.begin - first) / n);
+    s.at = first + static_cast<int64_t>(s.group) * n;
+  }
+  return s;
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float pa_lse(float ref, float sum) {
+  return sum == 0.f ? -INFINITY : (ref + __log2f(sum)) * 0.69314718055994530942f;
+}
+
+// Rows of the tiles of paged_attn_tc_kernel: 128, or as many as whole queries have.
+inline int tc_rows_of_tile(int64_t hpg) { return static_cast<int>(128 / hpg * hpg); }
+
+// The tensor-core kernel for many rows (paged_attn_tc.cu); fills p.ctas.
+int launch_paged_tc(PagedProblem& p, const nsa_kv_cache* kv, int64_t D, bool bf16,
+                    cudaStream_t st);
+int paged_tc_read_and_clear_status(unsigned int* value);
+
+}  // namespace nsa

@@ -1,0 +1,801 @@
+// Attention over pages with many rows a KV head (a piece of a prompt, drafted
+// tokens) on the 5th-generation tensor cores, for sm_103a. The mathematics and the
+// items' shares are paged_attn.cu's; here a row tile is up to 128 (query, head) rows
+// of a KV head, the M of the products, and a step 128 keys:
+//   S (128 rows x 128 keys) = Q K^T,  O (128 rows x D) += P V,
+// with S, P and O in tensor memory, as in swa_fwd.cu's kernel of one head: warp 1
+// issues S_0, S_1, PV_0, S_2, PV_1, ... over all of the CTA's items, four softmax
+// warps have a row a thread.
+//
+// 16 bits: warp 0 brings a step's K and V by TMA, a copy a page (or a part of one); a
+// page that the sequence does not have is asked for outside the map and arrives as
+// zeros. V's rows that no query sees are zeroed by the softmax warps before P is
+// handed over, so whatever they hold never meets a product.
+//
+// 4 bits: four loader warps have a key a thread. They load its codes a step ahead and
+// write c - 8, exact in fp16, as the operands' rows; five numbers of a key (steps,
+// the middles low + 8 step, log2 of V's step) go beside them, and a key that nobody
+// sees gets -inf for x and zeros. With k = mid + step (c - 8):
+//   x = step ka (q'.(c - 8)) + mid kb + log2 step_v,  p' = 2^(x - r),
+//   l += p' / step_v,  O = sum p' (c - 8) + sum p' mid_v / step_v,
+// q' = 2^e q in fp16, written by the softmax warps, ka and kb the row's factors.
+//
+// What bounds it: the softmax warps, one row a thread: 128 x 128 entries take them
+// some 7 (16 bits) and 12 (4 bits) instructions an entry.
+//
+// Every mbarrier wait is bounded (1 s); a role that gives up sets the status word
+// and leaves its loop, so every role reaches the teardown, which frees the tensor
+// memory.
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "common.cuh"
+#include "kv_cache.cuh"
+#include "nsa_sel_attn.h"
+#include "paged_attn.cuh"
+#include "ptx.cuh"
+#include "tc.cuh"
+
+namespace nsa {
+namespace {
+
+constexpr int kTcKeys = 128;
+constexpr uint32_t kTcTmem = 512, kColS = 0, kColO = 256, kColP = 384;
+
+enum TcBar : int {
+  kQFull = 0,    // 2 Q buffers
+  kQEmpty = 2,   // 2: every QK^T of the item that used Q buffer b has completed
+  kKFull = 4,    // 2 K stages
+  kKEmpty = 6,   // 2
+  kVFull = 8,    // 2 V stages
+  kVEmpty = 10,  // 2
+  kSFull = 12,   // 2 S buffers
+  kPFull = 14,   // 2 P buffers
+  kPvDone = 16,  // 2
+  kOEmpty = 18,  // the softmax warps have read O of the item before
+  // 4: a step's facts for the softmax (which pages are there, or the keys' numbers).
+  // Four, as K of the step after the next may come before its softmax begins.
+  kInfo = 19,
+  kTcBars = 23
+};
+
+template <int D, bool Q4>
+struct TcCfg {
+  // warps: 0 TMA (16 bits), 1 MMA, softmax; 4 bits in warpgroups: (., MMA, ., .),
+  // softmax, loaders
+  [[maybe_unused]] static constexpr int kSoftWarp = 4, kLoadWarp = 8;
+  static constexpr int kThreads = Q4 ? 384 : 192;
+  [[maybe_unused]] static constexpr int kAtoms = D / 64;
+  static constexpr int kAtomBytes = 128 * 128;
+  static constexpr int kTile = 128 * D * 2;  // Q, K or V
+  static constexpr int kOffK = 2 * kTile, kOffV = 4 * kTile;
+  static constexpr int kOffInfo = 6 * kTile;  // 4 x (5 numbers of each key, or a mask)
+  static constexpr int kInfoBytes = Q4 ? 5 * kTcKeys * 4 : 16;
+  static constexpr int kOffBar = kOffInfo + 4 * kInfoBytes;
+  static constexpr int kOffTmem = kOffBar + kTcBars * 8;
+  static constexpr int kOffCount = kOffTmem + 8;
+  static constexpr int kUsed = kOffCount + (kPaItems + 1) * 4 + 64 + 1024;
+  // at least 116 KB, so that one CTA holds an SM (all 512 tensor-memory columns)
+  static constexpr int kSmem = kUsed > 118784 ? kUsed : 118784;
+  static_assert(kSmem <= 232448, "one CTA an SM");
+};
+
+// The items of a CTA, one after the other, the same for every role. A whole warp
+// calls it: positions are read by its lanes.
+struct TcWalk {
+  PaShare sh;
+  PaSpan sp;
+  int b, rt, t0, t1;
+  bool more;
+
+  __device__ __forceinline__ void load(const PagedProblem& p, int rows_tile) {
+    b = sh.item / p.tiles;
+    rt = sh.item - b * p.tiles;
+    sp = pa_span(p, b, rt, rows_tile);
+    t0 = 0;
+    t1 = sp.n;
+    if (p.cut) {
+      const int64_t first = sh.at + p.item_cost, n = sp.n, zero = 0;
+      t0 = static_cast<int>(min(max(sh.begin - first, zero), n));
+      t1 = static_cast<int>(min(max(sh.end - first, zero), n));
+    }
+  }
+  __device__ __forceinline__ void start(const PagedProblem& p, const PaShare& share,
+                                        int rows_tile) {
+    sh = share;
+    if (!p.cut) {
+      sh.item = blockIdx.x / p.groups;
+      sh.group = blockIdx.x - sh.item * p.groups;
+    }
+    more = !p.cut || sh.begin < sh.end;
+    if (more) load(p, rows_tile);
+  }
+  __device__ __forceinline__ void next(const PagedProblem& p, const int* count, int rows_tile) {
+    if (!p.cut) {
+      const int64_t x = static_cast<int64_t>(sh.item) * p.groups + sh.group + gridDim.x;
+      more = x < static_cast<int64_t>(p.items) * p.groups;
+      sh.item = static_cast<int>(x / p.groups);
+      sh.group = static_cast<int>(x - static_cast<int64_t>(sh.item) * p.groups);
+    } else {
+      sh.at += sp.n + p.item_cost;
+      if (++sh.group == p.groups) {
+        sh.group = 0;
+        do ++sh.item;
+        while (sh.item < p.items && count[sh.item + 1] == count[sh.item]);
+      }
+      more = sh.at < sh.end;
+    }
+    if (more) load(p, rows_tile);
+  }
+};
+
+// Two codes of the bits under 0x000f000f as fp16 c - 8.
+__device__ __forceinline__ uint32_t less8(uint32_t two) {
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&two),
+                            __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408)));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// The 8 codes of a word as a 16-byte chunk, in the order 0, 4, 1, 5, 2, 6, 3, 7.
+__device__ __forceinline__ uint4 codes_chunk(uint32_t w) {
+  constexpr uint32_t kMask = 0x000f000fu, k1024 = 0x64006400u;
+  return make_uint4(less8((w & kMask) | k1024), less8((w >> 4 & kMask) | k1024),
+                    less8((w >> 8 & kMask) | k1024), less8((w >> 12 & kMask) | k1024));
+}
+// Place of entry i of 8 in that order.
+__device__ __forceinline__ constexpr int code_place(int i) { return i < 4 ? 2 * i : 2 * i - 7; }
+
+template <int D, bool BF16, bool Q4>
+__global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
+    paged_attn_tc_kernel(const PagedProblem p, int rows_tile, const __grid_constant__ CUtensorMap tmQ,
+                         const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmV) {
+  using C = TcCfg<D, Q4>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const gbase = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto bar = [&](int i) { return base + C::kOffBar + 8u * static_cast<uint32_t>(i); };
+  int* const count = reinterpret_cast<int*>(gbase + C::kOffCount);
+  int* const sums = count + kPaItems + 1;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(kQFull + s), Q4 ? 128 : 1);
+      mbar_init(bar(kQEmpty + s), 1);
+      mbar_init(bar(kKFull + s), Q4 ? 128 : 1);
+      mbar_init(bar(kKEmpty + s), 1);
+      mbar_init(bar(kVFull + s), Q4 ? 128 : 1);
+      mbar_init(bar(kVEmpty + s), 1);
+      mbar_init(bar(kSFull + s), 1);
+      mbar_init(bar(kPFull + s), 128);
+      mbar_init(bar(kPvDone + s), 1);
+    }
+    mbar_init(bar(kOEmpty), 128);
+    for (int s = 0; s < 4; ++s) mbar_init(bar(kInfo + s), Q4 ? 128 : 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tc_alloc(base + C::kOffTmem, kTcTmem);
+    tc_relinquish();
+  }
+  asm volatile("griddepcontrol.launch_dependents;\n");  // the join waits for this grid's end
+  PaShare share{0, 0, 0, 0, 0};
+  if (p.cut) share = pa_share<C::kThreads>(p, rows_tile, count, sums);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + C::kOffTmem);
+  bool failed = false;
+  TcWalk it;
+  it.start(p, share, rows_tile);
+  int64_t gt = 0;  // steps of the items before
+  int n = 0;       // items with steps before
+
+  auto producer = [&]() {
+    // ---- TMA producer (16 bits): the whole warp keeps step, lane 0 copies ----
+    if constexpr (!Q4) {
+      const uint64_t keep = p.tiles > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
+      const uint64_t once = l2_policy_evict_first();
+      const int rows = min(kTcKeys, 1 << p.c.shift);  // keys of a copy
+      const int split = kTcKeys / rows;
+      for (; it.more && !failed; it.next(p, count, rows_tile)) {
+        const int nt = it.t1 - it.t0;
+        if (nt <= 0) continue;
+        const int qb = n & 1;
+        // the pages of step t's copies, one a lane
+        auto look = [&](int t) {
+          return t < it.t1 && lane < split ? page_of(p.c, it.b, it.sp.key(t) + lane * rows) : -1;
+        };
+        int page_next = look(it.t0);
+        bool ok = true;
+        if (lane == 0) {
+          ok = n < 2 || wait_phase(bar(kQEmpty + qb), ((n - 2) >> 1) & 1, kWaitLimitNs);
+          if (ok) {
+            mbar_arrive_expect_tx(bar(kQFull + qb), rows_tile * D * 2);
+            for (int a = 0; a < C::kAtoms; ++a)
+              tma_load_4d(base + qb * C::kTile + a * C::kAtomBytes, &tmQ, bar(kQFull + qb), a * 64,
+                          it.sh.group * p.hpg, it.rt * (rows_tile / p.hpg), it.b, once);
+          }
+        }
+        for (int i = 0; i < nt; ++i) {
+          const int64_t g = gt + i;
+          const int s = static_cast<int>(g & 1);
+          const uint32_t prev = static_cast<uint32_t>(((g - 2) >> 1) & 1);
+          const int page = page_next;
+          const uint32_t there = __ballot_sync(kFull, lane < split && page >= 0);
+          page_next = look(it.t0 + i + 1);
+          const int off = it.sp.key(it.t0 + i) & ((1 << p.c.shift) - 1);
+          ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
+          if (!ok) break;
+          if (lane == 0) {
+            ok = g < 2 || wait_phase(bar(kKEmpty + s), prev, kWaitLimitNs);
+            if (ok) {
+              *reinterpret_cast<uint32_t*>(gbase + C::kOffInfo + (g & 3) * C::kInfoBytes) = there;
+              mbar_arrive(bar(kInfo + static_cast<int>(g & 3)));
+              mbar_arrive_expect_tx(bar(kKFull + s), C::kTile);
+            }
+          }
+          ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
+          if (!ok) break;
+          for (int j = 0; j < split; ++j) {
+            const int pg = __shfl_sync(kFull, page, j);
+            if (lane == 0)
+              for (int a = 0; a < C::kAtoms; ++a)
+                tma_load_4d(base + C::kOffK + s * C::kTile + a * C::kAtomBytes + j * rows * 128, &tmK,
+                            bar(kKFull + s), a * 64, it.sh.group, split > 1 ? 0 : off,
+                            pg < 0 ? p.c.pages : pg, keep);
+          }
+          if (lane == 0) {
+            ok = g < 2 || wait_phase(bar(kVEmpty + s), prev, kWaitLimitNs);
+            if (ok) mbar_arrive_expect_tx(bar(kVFull + s), C::kTile);
+          }
+          ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
+          if (!ok) break;
+          for (int j = 0; j < split; ++j) {
+            const int pg = __shfl_sync(kFull, page, j);
+            if (lane == 0)
+              for (int a = 0; a < C::kAtoms; ++a)
+                tma_load_4d(base + C::kOffV + s * C::kTile + a * C::kAtomBytes + j * rows * 128, &tmV,
+                            bar(kVFull + s), a * 64, it.sh.group, split > 1 ? 0 : off,
+                            pg < 0 ? p.c.pages : pg, keep);
+          }
+        }
+        failed = __shfl_sync(kFull, ok ? 0 : 1, 0) != 0;
+        gt += nt;
+        ++n;
+      }
+      if (failed) {  // leave nothing in flight
+        if (lane == 0)
+          for (int s = 0; s < 2; ++s)
+            for (int ph = 0; ph < 2; ++ph) {
+              wait_phase(bar(kKFull + s), ph, kWaitLimitNs / 8);
+              wait_phase(bar(kVFull + s), ph, kWaitLimitNs / 8);
+            }
+        __syncwarp();
+      }
+    }
+  };
+  auto issuer = [&]() {
+    // ---- MMA issuer: the steps of all items as one stream ----
+    constexpr bool kBf = BF16 && !Q4;
+    constexpr uint32_t idesc_s = umma_idesc_f16(128, kTcKeys, kBf, false);
+    constexpr uint32_t idesc_o = umma_idesc_f16(128, D, kBf, true);
+    auto issue_s = [&](int64_t g, int qb) -> bool {
+      const int s = static_cast<int>(g & 1);
+      if (!wait_phase(bar(kKFull + s), static_cast<uint32_t>((g >> 1) & 1), kWaitLimitNs))
+        return false;
+      tc_fence_after();
+      const uint32_t d = tmem + kColS + static_cast<uint32_t>(s) * kTcKeys;
+      const uint32_t q = base + qb * C::kTile, k = base + C::kOffK + s * C::kTile;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk >> 2) * C::kAtomBytes + (kk & 3) * 32;
+        tc_mma(d, umma_desc_sw128(q + off, 16), umma_desc_sw128(k + off, 16), idesc_s,
+               kk > 0 ? 1u : 0u);
+      }
+      tc_commit(bar(kKEmpty + s));
+      tc_commit(bar(kSFull + s));
+      return true;
+    };
+    auto issue_pv = [&](int64_t g, bool first, int item) -> bool {
+      const int s = static_cast<int>(g & 1);
+      const uint32_t ph = static_cast<uint32_t>((g >> 1) & 1);
+      if (!wait_phase(bar(kPFull + s), ph, kWaitLimitNs)) return false;
+      if (!wait_phase(bar(kVFull + s), ph, kWaitLimitNs)) return false;
+      if (first && item >= 1 && !wait_phase(bar(kOEmpty), (item - 1) & 1, kWaitLimitNs))
+        return false;
+      tc_fence_after();
+      const uint32_t v = base + C::kOffV + s * C::kTile;
+      const uint32_t pcol = tmem + kColP + static_cast<uint32_t>(s) * (kTcKeys / 2);
+#pragma unroll
+      for (int kk = 0; kk < kTcKeys / 16; ++kk)
+        tc_mma_ts(tmem + kColO, pcol + 8 * kk, umma_desc_sw128(v + kk * 2048, C::kAtomBytes),
+                  idesc_o, (!first || kk > 0) ? 1u : 0u);
+      tc_commit(bar(kVEmpty + s));
+      tc_commit(bar(kPvDone + s));
+      return true;
+    };
+    bool ok = true;
+    int64_t pend = -1;  // the step whose PV is still to be issued
+    bool pend_first = false;
+    int pend_n = 0;
+    for (; it.more && !failed; it.next(p, count, rows_tile)) {
+      const int nt = it.t1 - it.t0;
+      if (nt <= 0) continue;
+      if (lane == 0) {
+        const int qb = n & 1;
+        // (4 bits: Q comes from the softmax warps once they have the last item's O,
+        // so its last PV cannot wait for this item's first S)
+        if (Q4 && pend >= 0) {
+          ok = issue_pv(pend, pend_first, pend_n);
+          pend = -1;
+        }
+        ok = ok && wait_phase(bar(kQFull + qb), (n >> 1) & 1, kWaitLimitNs);
+        for (int i = 0; i < nt && ok; ++i) {
+          ok = issue_s(gt + i, qb);
+          if (ok && i == nt - 1) tc_commit(bar(kQEmpty + qb));
+          if (ok && pend >= 0) ok = issue_pv(pend, pend_first, pend_n);
+          pend = gt + i;
+          pend_first = i == 0;
+          pend_n = n;
+        }
+      }
+      failed = __shfl_sync(kFull, ok ? 0 : 1, 0) != 0;
+      gt += nt;
+      ++n;
+    }
+    if (lane == 0 && !failed && pend >= 0) ok = issue_pv(pend, pend_first, pend_n);
+    failed = __shfl_sync(kFull, ok ? 0 : 1, 0) != 0;
+  };
+  auto softmax = [&]() {
+    // ---- softmax: thread <-> row of the item's tile ----
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    auto wait_all = [&](int b, uint32_t parity) {
+      return __all_sync(kFull, wait_phase(bar(b), parity, kWaitLimitNs));
+    };
+    for (; it.more && !failed; it.next(p, count, rows_tile)) {
+      const int nt = it.t1 - it.t0;
+      if (nt <= 0 && p.cut) continue;  // (nothing of it in this share)
+      const int rw = it.rt * rows_tile + row;
+      const bool mine = row < rows_tile && rw < p.rows;
+      const int mq = rw / p.hpg, h = it.sh.group * p.hpg + rw - mq * p.hpg;
+      const int pos = mine ? pa_position(p, it.b, mq) : -1;
+      const PaSight see{it.sp.lo_pos, it.sp.hi_pos, p.left, p.sinks};
+      float ka = p.sl2, kb = 0.f;
+      if constexpr (Q4) {
+        if (nt > 0) {
+          // Q's row: 2^e q in fp16 (the largest entry between 2^13 and 2^14)
+          const int qb = n & 1;
+          if (n >= 2 && !wait_all(kQEmpty + qb, ((n - 2) >> 1) & 1)) {
+            failed = true;
+            break;
+          }
+          const uint4* const src = reinterpret_cast<const uint4*>(
+              p.q + 2 * (it.b * p.qb + mq * p.qm + h * p.qh));
+          float top = 0.f;
+          if (mine) {
+#pragma unroll 4
+            for (int i = 0; i < D / 8; ++i) {
+              float f[8];
+              unpack8<BF16>(src[i], f);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(f[j]));
+            }
+          }
+          int e = 0;
+          if (top > 0.f && top < INFINITY)
+            e = min(13 - (static_cast<int>(__float_as_uint(top) >> 23) - 127), 100);
+          const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+          float sum = 0.f;
+          uint8_t* const dst = gbase + qb * C::kTile + row * 128;
+#pragma unroll 4
+          for (int i = 0; i < D / 8; ++i) {
+            float f[8];
+            unpack8<BF16>(mine ? src[i] : make_uint4(0, 0, 0, 0), f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              f[j] = __half2float(__float2half_rn(f[j] * up));
+              sum += f[j];
+            }
+            *reinterpret_cast<uint4*>(dst + (i >> 3) * C::kAtomBytes + (((i & 7) ^ (row & 7)) << 4)) =
+                make_uint4(pack_half2(f[0], f[4]), pack_half2(f[1], f[5]), pack_half2(f[2], f[6]),
+                           pack_half2(f[3], f[7]));
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(bar(kQFull + qb));
+          ka = p.sl2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          kb = ka * sum;
+        }
+      }
+      float ref = -INFINITY, neg = 0.f, l = 0.f, mid_sum = 0.f;
+      for (int i = 0; i < nt; ++i) {
+        const int64_t g = gt + i;
+        const int sb = static_cast<int>(g & 1);
+        if (!wait_all(kSFull + sb, static_cast<uint32_t>((g >> 1) & 1)) ||
+            !wait_all(kInfo + static_cast<int>(g & 3), static_cast<uint32_t>((g >> 2) & 1))) {
+          failed = true;
+          break;
+        }
+        tc_fence_after();
+        uint32_t sr[kTcKeys];
+#pragma unroll
+        for (int c = 0; c < kTcKeys / 32; ++c)
+          tc_ld32(lane_addr + kColS + sb * kTcKeys + 32 * c,
+                  *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * c]));
+        tc_wait_ld();
+        const int n0 = it.sp.key(it.t0 + i);
+        const uint8_t* const info = gbase + C::kOffInfo + (g & 3) * C::kInfoBytes;
+        const bool inside = n0 + kTcKeys - 1 <= see.lo_pos &&
+                            (n0 >= see.hi_pos - see.left || n0 + kTcKeys <= see.sinks);
+        if constexpr (Q4) {
+          // (keys that are not there, or that nobody sees, have -inf already)
+          const float4* const num = reinterpret_cast<const float4*>(info);
+#pragma unroll
+          for (int c = 0; c < kTcKeys / 4; ++c) {
+            // (no loads of numbers further ahead than the registers hold)
+            if (c % 4 == 0) asm volatile("" ::: "memory");
+            const float4 st = num[c], md = num[32 + c], lg = num[64 + c];
+            const float a4[4] = {st.x, st.y, st.z, st.w}, m4[4] = {md.x, md.y, md.z, md.w},
+                        l4[4] = {lg.x, lg.y, lg.z, lg.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              sr[4 * c + j] = __float_as_uint(
+                  fmaf(a4[j] * ka, __uint_as_float(sr[4 * c + j]), fmaf(m4[j], kb, l4[j])));
+          }
+          if (!inside) {
+#pragma unroll
+            for (int j = 0; j < kTcKeys; ++j)
+              if (see.hidden(n0 + j, pos)) sr[j] = __float_as_uint(-INFINITY);
+          }
+        } else {
+          const uint32_t there = *reinterpret_cast<const uint32_t*>(info);
+          const int rows = min(kTcKeys, 1 << p.c.shift), split = kTcKeys / rows;
+          if (!inside || there != (1u << split) - 1u) {
+            // bit j: the page of keys 16 j .. of the step is there
+            uint32_t have = 0u;
+#pragma unroll
+            for (int j = 0; j < kTcKeys / 16; ++j)
+              have |= (there >> (16 * j / rows) & 1u) << j;
+#pragma unroll
+            for (int j = 0; j < kTcKeys; ++j)
+              if (!(have >> (j >> 4) & 1u) || see.hidden(n0 + j, pos))
+                sr[j] = __float_as_uint(-INFINITY);
+            // V rows that no query sees may hold anything (this thread's: key `row`)
+            if (!wait_all(kVFull + sb, static_cast<uint32_t>((g >> 1) & 1))) {
+              failed = true;
+              break;
+            }
+            if (see.nobody(n0 + row)) {
+#pragma unroll
+              for (int c = 0; c < D / 8; ++c)
+                *reinterpret_cast<uint4*>(gbase + C::kOffV + sb * C::kTile + (c >> 3) * C::kAtomBytes +
+                                          row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();  // before P is handed over
+          }
+        }
+        float m8[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m8[j] = __uint_as_float(sr[j]);
+#pragma unroll
+        for (int j = 8; j < kTcKeys; ++j) m8[j & 7] = fmaxf(m8[j & 7], __uint_as_float(sr[j]));
+        float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
+                         fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
+        if constexpr (!Q4) mx *= ka;
+        const bool move = mx > ref + kPaSlack;
+        if (__any_sync(kFull, move)) {
+          const float alpha = move ? ex2(ref - mx) : 1.f;
+          if (i > 0) {
+            if (!wait_all(kPvDone + static_cast<int>((g - 1) & 1),
+                          static_cast<uint32_t>(((g - 1) >> 1) & 1))) {
+              failed = true;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tc_ld32(lane_addr + kColO + 32 * c, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+              tc_st32(lane_addr + kColO + 32 * c, o);
+            }
+            tc_wait_st();
+          }
+          if (move) {
+            l *= alpha;
+            mid_sum *= alpha;
+            ref = mx;
+            neg = -mx;
+          }
+        }
+        // P buffer sb was last read by the PV of step g - 2
+        if (g >= 2 && !wait_all(kPvDone + sb, static_cast<uint32_t>(((g - 2) >> 1) & 1))) {
+          failed = true;
+          break;
+        }
+        float l4[4] = {0.f, 0.f, 0.f, 0.f}, s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h2 = 0; h2 < 2; ++h2) {
+          uint32_t pw[32];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            float e[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float x = __uint_as_float(sr[64 * h2 + 4 * c + j]);
+              e[j] = Q4 ? ex2(x + neg) : ex2(fmaf(x, ka, neg));
+            }
+            if constexpr (Q4) {
+              if (c % 4 == 0) asm volatile("" ::: "memory");
+              const float4* const num = reinterpret_cast<const float4*>(info);
+              const float4 rs = num[96 + 16 * h2 + c], rm = num[128 + 16 * h2 + c];
+              l4[0] = fmaf(e[0], rs.x, l4[0]), l4[1] = fmaf(e[1], rs.y, l4[1]);
+              l4[2] = fmaf(e[2], rs.z, l4[2]), l4[3] = fmaf(e[3], rs.w, l4[3]);
+              s4[0] = fmaf(e[0], rm.x, s4[0]), s4[1] = fmaf(e[1], rm.y, s4[1]);
+              s4[2] = fmaf(e[2], rm.z, s4[2]), s4[3] = fmaf(e[3], rm.w, s4[3]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) l4[j] += e[j];
+            }
+            pw[2 * c] = pack2_t<BF16 && !Q4>(e[0], e[1]);
+            pw[2 * c + 1] = pack2_t<BF16 && !Q4>(e[2], e[3]);
+          }
+          tc_st32(lane_addr + kColP + sb * (kTcKeys / 2) + 32 * h2, pw);
+        }
+        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        if constexpr (Q4) mid_sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(kPFull + sb));
+      }
+      if (failed) break;
+      // epilogue: O into registers, released to the next item's PVs
+      uint32_t o[D];
+      if (nt > 0) {
+        const int64_t gl = gt + nt - 1;
+        if (!wait_all(kPvDone + static_cast<int>(gl & 1), static_cast<uint32_t>((gl >> 1) & 1))) {
+          failed = true;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+          tc_ld32(lane_addr + kColO + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&o[32 * c]));
+        tc_wait_ld();
+        tc_fence_before();
+        mbar_arrive(bar(kOEmpty));
+      } else {
+#pragma unroll
+        for (int j = 0; j < D; ++j) o[j] = 0u;
+      }
+      if constexpr (Q4) {
+        // columns are in the codes' order; p mid_v is added
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          uint32_t t[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            t[j] = __float_as_uint(__uint_as_float(o[8 * c + code_place(j)]) + mid_sum);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[8 * c + j] = t[j];
+        }
+      }
+      if (mine) {
+        if (it.t0 == 0 && it.t1 == it.sp.n) {
+          const bool none = l == 0.f || pos < 0;
+          const float inv = none ? 0.f : 1.f / l;
+          uint4* const dst = reinterpret_cast<uint4*>(
+              p.o + ((static_cast<int64_t>(it.b) * p.M + mq) * p.H + h) * D);
+#pragma unroll
+          for (int q = 0; q < D / 8; ++q) {
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = none ? 0.f : __uint_as_float(o[8 * q + j]) * inv;
+            dst[q] = pack8<BF16>(f);
+          }
+          if (p.lse != nullptr)
+            p.lse[(static_cast<int64_t>(it.b) * p.H + h) * p.M + mq] = none ? -INFINITY
+                                                                            : pa_lse(ref, l);
+        } else {
+          const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (it.t0 == 0 ? 1 : 0);
+          const int64_t prow = slot * rows_tile + row;
+          uint4* const dst = reinterpret_cast<uint4*>(p.piece + prow * D);
+#pragma unroll
+          for (int q = 0; q < D / 4; ++q)
+            dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          reinterpret_cast<float2*>(p.piece + 2 * static_cast<int64_t>(p.ctas) * rows_tile * D)[prow] =
+              make_float2(ref, l);
+        }
+      }
+      gt += nt;
+      if (nt > 0) ++n;
+    }
+  };
+  auto loader = [&]() {
+    // ---- loaders (4 bits): thread <-> key of the step ----
+    if constexpr (Q4) {
+      constexpr int W = D / 32;  // 16-byte words of codes of a row
+      const int key_in = threadIdx.x - 32 * C::kLoadWarp;
+      uint4 kc[W], vc[W];
+      uint32_t ks = 0, vs = 0;
+      bool have = false;
+      auto wait_all = [&](int b, uint32_t parity) {
+        return __all_sync(kFull, wait_phase(bar(b), parity, kWaitLimitNs));
+      };
+      for (; it.more && !failed; it.next(p, count, rows_tile)) {
+        const int nt = it.t1 - it.t0;
+        if (nt <= 0) continue;
+        const PaSight see{it.sp.lo_pos, it.sp.hi_pos, p.left, p.sinks};
+        auto fetch = [&](int t) {
+          have = false;
+          if (t >= it.t1) return;
+          const int key = it.sp.key(t) + key_in;
+          const int page = see.nobody(key) ? -1 : page_of(p.c, it.b, key);
+          if (page < 0) return;
+          have = true;
+          const int off = key & ((1 << p.c.shift) - 1);
+          const int64_t o = page * p.c.kp + off * p.c.kt + it.sh.group * p.c.kh;
+          const uint4* const k = reinterpret_cast<const uint4*>(p.c.k + o);
+          const uint4* const v = reinterpret_cast<const uint4*>(p.c.v + o);
+#pragma unroll
+          for (int j = 0; j < W; ++j) kc[j] = __ldg(k + j);
+#pragma unroll
+          for (int j = 0; j < W; ++j) vc[j] = __ldg(v + j);
+          const int64_t so =
+              ((page * static_cast<int64_t>(p.G) + it.sh.group) << p.c.shift) + off;
+          ks = __ldg(p.c.ks + so);
+          vs = __ldg(p.c.vs + so);
+        };
+        fetch(it.t0);
+        for (int i = 0; i < nt; ++i) {
+          const int64_t g = gt + i;
+          const int s = static_cast<int>(g & 1);
+          const uint32_t prev = static_cast<uint32_t>(((g - 2) >> 1) & 1);
+          if (g >= 2 && !wait_all(kKEmpty + s, prev)) {
+            failed = true;
+            break;
+          }
+          auto store = [&](uint8_t* tile, const uint4 (&w)[W]) {
+            uint8_t* const dst = tile + key_in * 128;
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+              const uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int ch = 4 * j + q;
+                *reinterpret_cast<uint4*>(dst + (ch >> 3) * C::kAtomBytes +
+                                          (((ch & 7) ^ (key_in & 7)) << 4)) =
+                    have ? codes_chunk(u[q]) : make_uint4(0, 0, 0, 0);
+              }
+            }
+          };
+          store(gbase + C::kOffK + s * C::kTile, kc);
+          // the key's numbers: K's step and middle, log2 of V's step, its
+          // reciprocal, and the middle by that
+          const float kstep = __uint_as_float(ks << 16), klow = __uint_as_float(ks & 0xffff0000u);
+          const float vstep = __uint_as_float(vs << 16), vlow = __uint_as_float(vs & 0xffff0000u);
+          const float any = vstep == 0.f ? 1.f : vstep;  // (all codes are 0 then)
+          const float rs = rcp_approx(any);
+          float* const num = reinterpret_cast<float*>(gbase + C::kOffInfo + (g & 3) * C::kInfoBytes);
+          num[key_in] = have ? kstep : 0.f;
+          num[128 + key_in] = have ? fmaf(8.f, kstep, klow) : 0.f;
+          num[256 + key_in] = have ? lg2_approx(any) : -INFINITY;
+          num[384 + key_in] = have ? rs : 0.f;
+          // (without a step the codes of 0 stand for -8 of a step of 1)
+          num[512 + key_in] = have ? fmaf(8.f, any, vlow) * rs : 0.f;
+          fence_proxy_async_smem();
+          mbar_arrive(bar(kInfo + static_cast<int>(g & 3)));
+          mbar_arrive(bar(kKFull + s));
+          if (g >= 2 && !wait_all(kVEmpty + s, prev)) {
+            failed = true;
+            break;
+          }
+          store(gbase + C::kOffV + s * C::kTile, vc);
+          fence_proxy_async_smem();
+          mbar_arrive(bar(kVFull + s));
+          fetch(it.t0 + i + 1);
+        }
+        gt += nt;
+        ++n;
+      }
+    }
+  };
+  if constexpr (Q4) {
+    // 384 threads of 168 registers; 80 + 240 + 184 = 3 x 168
+    if (warp < C::kSoftWarp) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n" ::: "memory");
+      if (warp == 1) issuer();
+    } else if (warp < C::kLoadWarp) {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 240;\n" ::: "memory");
+      softmax();
+    } else {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 184;\n" ::: "memory");
+      loader();
+    }
+  } else {
+    if (warp == 0) producer();
+    else if (warp == 1) issuer();
+    else softmax();
+  }
+
+  if (failed && lane == 0) report_timeout();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tc_dealloc(tmem, kTcTmem);
+  }
+}
+
+template <int D, bool BF16, bool Q4>
+int launch(PagedProblem& p, cudaStream_t st) {
+  using C = TcCfg<D, Q4>;
+  constexpr CUtensorMapDataType dt =
+      BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  CUtensorMap tq, tk, tv;
+  memset(&tq, 0, sizeof(tq));  // (4 bits: none is used)
+  memset(&tk, 0, sizeof(tk));
+  memset(&tv, 0, sizeof(tv));
+  const int rows = tc_rows_of_tile(p.hpg);
+  if constexpr (!Q4) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return NSA_ERR_LAUNCH;
+    // Q as (d, head, query, sequence): the heads of a KV head and whole queries in a box
+    const int64_t sh = p.H > 1 ? p.qh : D, sm = p.M > 1 ? p.qm : p.H * sh,
+                  sb = p.B > 1 ? p.qb : p.M * sm;
+    const cuuint64_t dims[4] = {D, static_cast<cuuint64_t>(p.H), static_cast<cuuint64_t>(p.M),
+                                static_cast<cuuint64_t>(p.B)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(2 * sh), static_cast<cuuint64_t>(2 * sm),
+                                   static_cast<cuuint64_t>(2 * sb)};
+    const cuuint32_t box[4] = {kBoxCols, static_cast<cuuint32_t>(p.hpg),
+                               static_cast<cuuint32_t>(rows / p.hpg), 1};
+    const cuuint32_t one[4] = {1, 1, 1, 1};
+    if (enc(&tq, dt, 4, const_cast<uint8_t*>(p.q), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return NSA_ERR_LAUNCH;
+    const int64_t page = int64_t(1) << p.c.shift;
+    const int keys = page < kTcKeys ? static_cast<int>(page) : kTcKeys;
+    if (!encode_kv_map_strided(&tk, p.c.k, p.c.pages, page, p.G, D, keys, dt, p.c.kp / 2,
+                               p.c.kt / 2, p.c.kh / 2) ||
+        !encode_kv_map_strided(&tv, p.c.v, p.c.pages, page, p.G, D, keys, dt, p.c.vp / 2,
+                               p.c.vt / 2, p.c.vh / 2))
+      return NSA_ERR_LAUNCH;
+  }
+  auto kern = paged_attn_tc_kernel<D, BF16, Q4>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) !=
+      cudaSuccess)
+    return NSA_ERR_LAUNCH;
+  p.ctas = kPaSms;
+  const int64_t all = static_cast<int64_t>(p.items) * p.groups;
+  const int64_t blocks = p.cut || all > kPaSms ? kPaSms : all;
+  kern<<<static_cast<unsigned>(blocks), C::kThreads, C::kSmem, st>>>(p, rows, tq, tk, tv);
+  return cudaGetLastError() == cudaSuccess ? NSA_OK : NSA_ERR_LAUNCH;
+}
+
+}  // namespace
+
+int launch_paged_tc(PagedProblem& p, const nsa_kv_cache* kv, int64_t D, bool bf16,
+                    cudaStream_t st) {
+  const bool q4 = kv->bits == 4;
+  if (D == 64) {
+    if (bf16) return q4 ? launch<64, true, true>(p, st) : launch<64, true, false>(p, st);
+    return q4 ? launch<64, false, true>(p, st) : launch<64, false, false>(p, st);
+  }
+  if (bf16) return q4 ? launch<128, true, true>(p, st) : launch<128, true, false>(p, st);
+  return q4 ? launch<128, false, true>(p, st) : launch<128, false, false>(p, st);
+}
+
+int paged_tc_read_and_clear_status(unsigned int* value) { return read_and_clear_status(value); }
+
+}  // namespace nsa

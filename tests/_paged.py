@@ -106,9 +106,9 @@ def check_attn(q, cache, table, pos, left, sinks, scale, o, lse, dtype):
     v, vlow, vstep = rows_of(cache, "v")
     u, up = U[dtype], U["f16" if cache.bits == 4 else dtype]
     for b in range(B):
-        N = min(int(pn[b].max()) + 1, tn.shape[1] * page)
-        kb, present = sequence_rows(k, tn[b], page, max(N, 0))
-        vb, _ = sequence_rows(v, tn[b], page, max(N, 0))
+        N = max(0, min(int(pn[b].max()) + 1, tn.shape[1] * page))
+        kb, present = sequence_rows(k, tn[b], page, N)
+        vb, _ = sequence_rows(v, tn[b], page, N)
         want, wl, mag, seen = P.attend(qn[b], kb, vb, present, pn[b], left, sinks, sc)
         size, vtop = np.abs(kb), np.abs(vb).max(initial=0.0)
         extra = 0.0

@@ -118,7 +118,7 @@ def test_more_row_tiles_than_are_cut(bits):
 
     from nsa_block_selection_gb300 import _lib
 
-    B, M = 130, 8  # 8 row tiles of 16 rows each
+    B, M = 520, 1
     q, cache, table, pos = _problem(2, M, 16, 1, 64, "f16", bits, 16, [90, 33], 21)
     assert _lib.paged_attn_workspace_bytes(B, M, 16, 1, 64, 4096) == 0
     assert _lib.paged_attn_workspace_bytes(2, M, 16, 1, 64, 4096) > 0
@@ -130,3 +130,68 @@ def test_more_row_tiles_than_are_cut(bits):
     for x in many:
         assert torch.equal(x[0::2], x[:1].expand_as(x[0::2]))
         assert torch.equal(x[1::2], x[1:2].expand_as(x[1::2]))
+
+
+@pytest.mark.parametrize("bits", BITS)
+@pytest.mark.parametrize("D,dtype", [(64, "f16"), (128, "bf16")])
+@pytest.mark.parametrize("M,H,G,page,lens,left,sinks", [
+    (3, 8, 1, 16, [3, 300], -1, 0), (17, 1, 1, 32, [17, 18, 700], -1, 0), (16, 8, 1, 64, [129], -1, 0),
+    (40, 14, 2, 128, [40, 1000], 100, 7), (130, 3, 3, 256, [513, 131], 0, 1), (200, 16, 2, 1024, [1300], -1, 0),
+    (33, 10, 2, 16, [900, 333], 257, 130), (5, 100, 1, 64, [640, 5], -1, 0), (20, 130, 1, 64, [70], -1, 0)])
+def test_many_rows(M, H, G, page, lens, left, sinks, D, dtype, bits):
+    """Row tiles of the tensor cores: heads that 128 rows do not divide by, pages
+    that a step of 128 keys holds several of, steps that are seen in part."""
+    case = _problem(len(lens), M, H, G, D, dtype, bits, page, lens, M + H + page)
+    _check(case, left, sinks, dtype)
+
+
+@pytest.mark.parametrize("bits", BITS)
+def test_many_rows_missing_pages_and_padding(bits):
+    q, cache, table, pos = _problem(4, 24, 8, 2, 128, "bf16", bits, 32, [2500, 24, 400, 999], 31, holes=9)
+    pos[0, 5:9] = -1
+    pos[1] = -3
+    table[2, 4:] = -1
+    out, lse = _run(q, cache, table, pos, -1, 0, "bf16")
+    assert (out[1] == 0).all() and (lse[1] == -float("inf")).all() and (out[0, 5:9] == 0).all()
+    check_attn(q, cache, table, pos, -1, 0, None, out, lse, "bf16")
+    _check((q, cache, table, pos), 300, 40, "bf16")
+
+
+@pytest.mark.parametrize("bits", BITS)
+def test_many_rows_long_and_cut(bits):
+    case = _problem(3, 20, 16, 2, 64, "f16", bits, 64, [9000, 21, 5000], 33)
+    _check(case, -1, 0, "f16")
+    _check(case, 2000, 4, "f16")
+
+
+@pytest.mark.parametrize("bits", BITS)
+@pytest.mark.parametrize("M", [1, 2, 6])
+def test_strided_queries_and_positions_of_a_batch(M, bits):
+    import torch
+
+    q, cache, table, pos = _problem(3, M, 16, 2, 64, "f16", bits, 16, [200, 200, 200], 35)
+    x = torch.randn((3, M, 24, 64), device="cuda").half()
+    x[:, :, 4:20] = q
+    view = x[:, :, 4:20]
+    assert not view.is_contiguous()
+    one = pos[0].contiguous()
+    a, b = _run(q, cache, table, pos, -1, 0, "f16"), _run(view, cache, table, one, -1, 0, "f16")
+    for s, t in zip(a, b):
+        assert torch.equal(s, t)
+
+
+@pytest.mark.parametrize("bits", BITS)
+@pytest.mark.parametrize("B,M,H,G,n", [(50, 5, 32, 8, 100), (90, 3, 16, 2, 700), (6, 18, 16, 16, 3500)])
+def test_many_items_for_a_cta(B, M, H, G, n, bits):
+    """More items than SMs, whole and cut: every CTA goes through several; the
+    same sequence twice gives the same bits."""
+    import torch
+
+    half = _problem(B // 2, M, H, G, 64, "f16", bits, 64, [n - 7 * b % n + M for b in range(B // 2)], 37)
+    q, cache, table, pos = half
+    two = torch.cat((torch.arange(B // 2), torch.arange(B // 2))).cuda()
+    out, lse = _run(q[two].contiguous(), cache, table[two].contiguous(), pos[two].contiguous(), -1, 0, "f16")
+    some = slice(0, min(B // 2, 6))
+    check_attn(q[some], cache, table[some], pos[some], -1, 0, None, out[some], lse[some], "f16")
+    few = _run(*(x[some].contiguous() if x is not cache else x for x in half), -1, 0, "f16")
+    check_attn(q[some], cache, table[some], pos[some], -1, 0, None, *few, "f16")

@@ -107,6 +107,7 @@ def test_attention_refuses(lib):
     assert _attn(lib, {"ws": FAKE + 8}, cols=100) == -6
     assert _attn(lib, strides=[8 * 16 * 128 + 4, 16 * 128, 128]) == -6
     assert _attn(lib, strides=[-8, 16 * 128, 128]) == -2
+    assert _attn(lib, strides=[0, 16 * 128, 128]) == -2
 
 
 @pytest.mark.parametrize("which", ["k", "v", "q", "qo", "kp", "vp", "table", "cos", "sin"])

@@ -284,6 +284,26 @@ def test_sizes_of_values(bits, scale):
     check_attn(q, cache, table, pos, -1, 0, None, out, lse, "bf16")
 
 
+@pytest.mark.parametrize("M", [1, 2, 20])
+def test_rows_without_a_step(M):
+    """Constant rows of K and of V among the others, and only such."""
+    import torch
+
+    g = torch.Generator(device="cuda").manual_seed(16)
+    for share in (0.3, 1.0):
+        cache = make_cache(g, 8, 32, 2, 64, "f16", 4)
+        for name in ("k", "v"):
+            some = torch.rand((8, 32, 2), generator=g, device="cuda") < share
+            getattr(cache, name)[some] = 0
+            scale = getattr(cache, name + "_scale")
+            scale[..., 0].masked_fill_(some.transpose(1, 2), 0.0)
+        table = torch.randperm(8, generator=g, device="cuda")[:7].view(1, 7).int()
+        pos = torch.arange(200 - M, 200, dtype=torch.int32, device="cuda").view(1, M)
+        q = torch.randn((1, M, 16, 64), generator=g, device="cuda").half()
+        out, lse = _attn(q, cache, table, pos, -1, 0)
+        check_attn(q, cache, table, pos, -1, 0, None, out, lse, "f16")
+
+
 @pytest.mark.parametrize("bits", [16, 4])
 def test_flat_attention_over_many_keys(bits):
     """Zero queries: O is the mean of the values, far smaller than they are. Its
