@@ -66,8 +66,8 @@ enum TcBar : int {
 
 template <int D, bool Q4>
 struct TcCfg {
-  // warps: 0 TMA (16 bits), 1 MMA, softmax; 4 bits in warpgroups: (., MMA, ., .),
-  // softmax, loaders
+  // warps: 0 TMA, 1 MMA, 2 to 5 softmax; 4 bits: warpgroups (., MMA, ., .), softmax,
+  // loaders
   [[maybe_unused]] static constexpr int kSoftWarp = 4, kLoadWarp = 8;
   static constexpr int kThreads = Q4 ? 384 : 192;
   [[maybe_unused]] static constexpr int kAtoms = D / 64;
@@ -133,6 +133,46 @@ struct TcWalk {
     if (more) load(p, rows_tile);
   }
 };
+
+// Two fp32 operations an instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// A matrix descriptor moved by `bytes` (shared memory ends below the address field's
+// 2^18 bytes): an addition instead of the descriptor built again.
+__device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) {
+  const uint32_t lo = static_cast<uint32_t>(desc) + (bytes >> 4);
+  return (desc & 0xffffffff00000000ull) | lo;
+}
+
+// Bit c set: column c of 32 lies in [lo, hi].
+__device__ __forceinline__ uint32_t columns(int lo, int hi) {
+  const uint32_t below = hi < 0 ? 0u : hi >= 31 ? ~0u : (2u << hi) - 1u;
+  return lo <= 0 ? below : lo > 31 ? 0u : below & (~0u << lo);
+}
 
 // Two codes of the bits under 0x000f000f as fp16 c - 8.
 __device__ __forceinline__ uint32_t less8(uint32_t two) {
@@ -285,18 +325,20 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
     constexpr bool kBf = BF16 && !Q4;
     constexpr uint32_t idesc_s = umma_idesc_f16(128, kTcKeys, kBf, false);
     constexpr uint32_t idesc_o = umma_idesc_f16(128, D, kBf, true);
+    const uint64_t k_major = umma_desc_sw128(base, 16);
+    const uint64_t mn_major = umma_desc_sw128(base, C::kAtomBytes);
     auto issue_s = [&](int64_t g, int qb) -> bool {
       const int s = static_cast<int>(g & 1);
       if (!wait_phase(bar(kKFull + s), static_cast<uint32_t>((g >> 1) & 1), kWaitLimitNs))
         return false;
       tc_fence_after();
       const uint32_t d = tmem + kColS + static_cast<uint32_t>(s) * kTcKeys;
-      const uint32_t q = base + qb * C::kTile, k = base + C::kOffK + s * C::kTile;
+      const uint64_t q = desc_at(k_major, qb * C::kTile);
+      const uint64_t k = desc_at(k_major, C::kOffK + s * C::kTile);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = (kk >> 2) * C::kAtomBytes + (kk & 3) * 32;
-        tc_mma(d, umma_desc_sw128(q + off, 16), umma_desc_sw128(k + off, 16), idesc_s,
-               kk > 0 ? 1u : 0u);
+        tc_mma(d, desc_at(q, off), desc_at(k, off), idesc_s, kk > 0 ? 1u : 0u);
       }
       tc_commit(bar(kKEmpty + s));
       tc_commit(bar(kSFull + s));
@@ -310,12 +352,12 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
       if (first && item >= 1 && !wait_phase(bar(kOEmpty), (item - 1) & 1, kWaitLimitNs))
         return false;
       tc_fence_after();
-      const uint32_t v = base + C::kOffV + s * C::kTile;
+      const uint64_t v = desc_at(mn_major, C::kOffV + s * C::kTile);
       const uint32_t pcol = tmem + kColP + static_cast<uint32_t>(s) * (kTcKeys / 2);
 #pragma unroll
       for (int kk = 0; kk < kTcKeys / 16; ++kk)
-        tc_mma_ts(tmem + kColO, pcol + 8 * kk, umma_desc_sw128(v + kk * 2048, C::kAtomBytes),
-                  idesc_o, (!first || kk > 0) ? 1u : 0u);
+        tc_mma_ts(tmem + kColO, pcol + 8 * kk, desc_at(v, kk * 2048), idesc_o,
+                  (!first || kk > 0) ? 1u : 0u);
       tc_commit(bar(kVEmpty + s));
       tc_commit(bar(kPvDone + s));
       return true;
@@ -368,6 +410,11 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
       const int mq = rw / p.hpg, h = it.sh.group * p.hpg + rw - mq * p.hpg;
       const int pos = mine ? pa_position(p, it.b, mq) : -1;
       const PaSight see{it.sp.lo_pos, it.sp.hi_pos, p.left, p.sinks};
+      // which of the 32 keys from `key` on this thread's query sees
+      auto seen = [&](int key) {
+        const int hi = pos - key;
+        return columns(hi - p.left, hi) | columns(0, min(hi, p.sinks - key - 1));
+      };
       float ka = p.sl2, kb = 0.f;
       if constexpr (Q4) {
         if (nt > 0) {
@@ -424,37 +471,52 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
           break;
         }
         tc_fence_after();
-        uint32_t sr[kTcKeys];
-#pragma unroll
-        for (int c = 0; c < kTcKeys / 32; ++c)
-          tc_ld32(lane_addr + kColS + sb * kTcKeys + 32 * c,
-                  *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * c]));
-        tc_wait_ld();
         const int n0 = it.sp.key(it.t0 + i);
         const uint8_t* const info = gbase + C::kOffInfo + (g & 3) * C::kInfoBytes;
         const bool inside = n0 + kTcKeys - 1 <= see.lo_pos &&
                             (n0 >= see.hi_pos - see.left || n0 + kTcKeys <= see.sinks);
+        [[maybe_unused]] uint32_t sr[Q4 ? 1 : kTcKeys];
+        float m8[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m8[j] = -INFINITY;
         if constexpr (Q4) {
-          // (keys that are not there, or that nobody sees, have -inf already)
-          const float4* const num = reinterpret_cast<const float4*>(info);
+          // x over S, 32 columns at a time: beside the keys' numbers a row of 128
+          // does not fit the registers. (Keys that are not there, or that nobody
+          // sees, have -inf.)
+          const ulonglong2* const num = reinterpret_cast<const ulonglong2*>(info);
+          const uint64_t ka2 = pair(ka, ka), kb2 = pair(kb, kb);
+#pragma unroll 1
+          for (int c = 0; c < kTcKeys / 32; ++c) {
+            uint32_t x[32];
+            tc_ld32(lane_addr + kColS + sb * kTcKeys + 32 * c, x);
+            tc_wait_ld();
 #pragma unroll
-          for (int c = 0; c < kTcKeys / 4; ++c) {
-            // (no loads of numbers further ahead than the registers hold)
-            if (c % 4 == 0) asm volatile("" ::: "memory");
-            const float4 st = num[c], md = num[32 + c], lg = num[64 + c];
-            const float a4[4] = {st.x, st.y, st.z, st.w}, m4[4] = {md.x, md.y, md.z, md.w},
-                        l4[4] = {lg.x, lg.y, lg.z, lg.w};
+            for (int j = 0; j < 8; ++j) {
+              const ulonglong2 st = num[8 * c + j], md = num[32 + 8 * c + j], lg = num[64 + 8 * c + j];
+              const uint64_t s0 = pair(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1]));
+              const uint64_t s1 = pair(__uint_as_float(x[4 * j + 2]), __uint_as_float(x[4 * j + 3]));
+              const float2 x0 = unpair(fma2(mul2(st.x, ka2), s0, fma2(md.x, kb2, lg.x)));
+              const float2 x1 = unpair(fma2(mul2(st.y, ka2), s1, fma2(md.y, kb2, lg.y)));
+              x[4 * j] = __float_as_uint(x0.x), x[4 * j + 1] = __float_as_uint(x0.y);
+              x[4 * j + 2] = __float_as_uint(x1.x), x[4 * j + 3] = __float_as_uint(x1.y);
+            }
+            if (!inside) {
+              const uint32_t bits = seen(n0 + 32 * c);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              sr[4 * c + j] = __float_as_uint(
-                  fmaf(a4[j] * ka, __uint_as_float(sr[4 * c + j]), fmaf(m4[j], kb, l4[j])));
+              for (int j = 0; j < 32; ++j)
+                if (!(bits >> j & 1u)) x[j] = __float_as_uint(-INFINITY);
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) m8[j & 7] = fmaxf(m8[j & 7], __uint_as_float(x[j]));
+            tc_st32(lane_addr + kColS + sb * kTcKeys + 32 * c, x);
           }
-          if (!inside) {
-#pragma unroll
-            for (int j = 0; j < kTcKeys; ++j)
-              if (see.hidden(n0 + j, pos)) sr[j] = __float_as_uint(-INFINITY);
-          }
+          tc_wait_st();
         } else {
+#pragma unroll
+          for (int c = 0; c < kTcKeys / 32; ++c)
+            tc_ld32(lane_addr + kColS + sb * kTcKeys + 32 * c,
+                    *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * c]));
+          tc_wait_ld();
           const uint32_t there = *reinterpret_cast<const uint32_t*>(info);
           const int rows = min(kTcKeys, 1 << p.c.shift), split = kTcKeys / rows;
           if (!inside || there != (1u << split) - 1u) {
@@ -464,9 +526,13 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
             for (int j = 0; j < kTcKeys / 16; ++j)
               have |= (there >> (16 * j / rows) & 1u) << j;
 #pragma unroll
-            for (int j = 0; j < kTcKeys; ++j)
-              if (!(have >> (j >> 4) & 1u) || see.hidden(n0 + j, pos))
-                sr[j] = __float_as_uint(-INFINITY);
+            for (int c = 0; c < kTcKeys / 32; ++c) {
+              const uint32_t bits = seen(n0 + 32 * c) & ((have >> (2 * c) & 1u ? 0xffffu : 0u) |
+                                                         (have >> (2 * c) & 2u ? ~0xffffu : 0u));
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!(bits >> j & 1u)) sr[32 * c + j] = __float_as_uint(-INFINITY);
+            }
             // V rows that no query sees may hold anything (this thread's: key `row`)
             if (!wait_all(kVFull + sb, static_cast<uint32_t>((g >> 1) & 1))) {
               failed = true;
@@ -480,12 +546,9 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
             }
             fence_proxy_async_smem();  // before P is handed over
           }
+#pragma unroll
+          for (int j = 0; j < kTcKeys; ++j) m8[j & 7] = fmaxf(m8[j & 7], __uint_as_float(sr[j]));
         }
-        float m8[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m8[j] = __uint_as_float(sr[j]);
-#pragma unroll
-        for (int j = 8; j < kTcKeys; ++j) m8[j & 7] = fmaxf(m8[j & 7], __uint_as_float(sr[j]));
         float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
                          fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
         if constexpr (!Q4) mx *= ka;
@@ -522,37 +585,54 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
           failed = true;
           break;
         }
-        float l4[4] = {0.f, 0.f, 0.f, 0.f}, s4[4] = {0.f, 0.f, 0.f, 0.f};
+        uint64_t l2[2] = {0, 0}, s2[2] = {0, 0};  // sums of pairs
+        const uint64_t neg2 = pair(neg, neg), ka2 = pair(ka, ka);
+        // 32 columns: exponentials, their sums and P
+        auto exps = [&](const uint32_t* x, int q) {
+          uint32_t pw[16];
 #pragma unroll
-        for (int h2 = 0; h2 < 2; ++h2) {
-          uint32_t pw[32];
+          for (int c = 0; c < 8; ++c) {
+            uint64_t y[2];
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            float e[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float x = __uint_as_float(sr[64 * h2 + 4 * c + j]);
-              e[j] = Q4 ? ex2(x + neg) : ex2(fmaf(x, ka, neg));
+            for (int j = 0; j < 2; ++j) {
+              y[j] = pair(__uint_as_float(x[4 * c + 2 * j]), __uint_as_float(x[4 * c + 2 * j + 1]));
+              const float2 v = unpair(Q4 ? add2(y[j], neg2) : fma2(y[j], ka2, neg2));
+              const float e0 = ex2(v.x), e1 = ex2(v.y);
+              y[j] = pair(e0, e1);
+              pw[2 * c + j] = pack2_t<BF16 && !Q4>(e0, e1);
             }
             if constexpr (Q4) {
-              if (c % 4 == 0) asm volatile("" ::: "memory");
-              const float4* const num = reinterpret_cast<const float4*>(info);
-              const float4 rs = num[96 + 16 * h2 + c], rm = num[128 + 16 * h2 + c];
-              l4[0] = fmaf(e[0], rs.x, l4[0]), l4[1] = fmaf(e[1], rs.y, l4[1]);
-              l4[2] = fmaf(e[2], rs.z, l4[2]), l4[3] = fmaf(e[3], rs.w, l4[3]);
-              s4[0] = fmaf(e[0], rm.x, s4[0]), s4[1] = fmaf(e[1], rm.y, s4[1]);
-              s4[2] = fmaf(e[2], rm.z, s4[2]), s4[3] = fmaf(e[3], rm.w, s4[3]);
+              const ulonglong2* const num = reinterpret_cast<const ulonglong2*>(info);
+              const ulonglong2 rs = num[96 + 8 * q + c], rm = num[128 + 8 * q + c];
+              l2[0] = fma2(y[0], rs.x, l2[0]);
+              l2[1] = fma2(y[1], rs.y, l2[1]);
+              s2[0] = fma2(y[0], rm.x, s2[0]);
+              s2[1] = fma2(y[1], rm.y, s2[1]);
             } else {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) l4[j] += e[j];
+              l2[0] = add2(l2[0], y[0]);
+              l2[1] = add2(l2[1], y[1]);
             }
-            pw[2 * c] = pack2_t<BF16 && !Q4>(e[0], e[1]);
-            pw[2 * c + 1] = pack2_t<BF16 && !Q4>(e[2], e[3]);
           }
-          tc_st32(lane_addr + kColP + sb * (kTcKeys / 2) + 32 * h2, pw);
+          tc_st16(lane_addr + kColP + sb * (kTcKeys / 2) + 16 * q, pw);
+        };
+        if constexpr (Q4) {
+#pragma unroll 1
+          for (int q = 0; q < kTcKeys / 32; ++q) {
+            uint32_t x[32];
+            tc_ld32(lane_addr + kColS + sb * kTcKeys + 32 * q, x);
+            tc_wait_ld();
+            exps(x, q);
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < kTcKeys / 32; ++q) exps(&sr[32 * q], q);
         }
-        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-        if constexpr (Q4) mid_sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+        const float2 lsum = unpair(add2(l2[0], l2[1]));
+        l += lsum.x + lsum.y;
+        if constexpr (Q4) {
+          const float2 ssum = unpair(add2(s2[0], s2[1]));
+          mid_sum += ssum.x + ssum.y;
+        }
         tc_wait_st();
         tc_fence_before();
         mbar_arrive(bar(kPFull + sb));
@@ -620,14 +700,11 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
       if (nt > 0) ++n;
     }
   };
+  // ---- loaders (4 bits): thread <-> key of the step ----
   auto loader = [&]() {
-    // ---- loaders (4 bits): thread <-> key of the step ----
     if constexpr (Q4) {
       constexpr int W = D / 32;  // 16-byte words of codes of a row
-      const int key_in = threadIdx.x - 32 * C::kLoadWarp;
-      uint4 kc[W], vc[W];
-      uint32_t ks = 0, vs = 0;
-      bool have = false;
+      const int key_in = threadIdx.x & 127;
       auto wait_all = [&](int b, uint32_t parity) {
         return __all_sync(kFull, wait_phase(bar(b), parity, kWaitLimitNs));
       };
@@ -635,77 +712,94 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
         const int nt = it.t1 - it.t0;
         if (nt <= 0) continue;
         const PaSight see{it.sp.lo_pos, it.sp.hi_pos, p.left, p.sinks};
-        auto fetch = [&](int t) {
-          have = false;
+        // a step's page is looked up a step before its codes, and those a step
+        // before they are stored
+        int page_next = -1;
+        bool there_next = false;
+        uint4 k_next[W], v_next[W];
+        uint32_t ks_next = 0, vs_next = 0;
+        auto look = [&](int t) {
+          page_next = -1;
           if (t >= it.t1) return;
           const int key = it.sp.key(t) + key_in;
-          const int page = see.nobody(key) ? -1 : page_of(p.c, it.b, key);
+          if (!see.nobody(key)) page_next = page_of(p.c, it.b, key);
+        };
+        auto fetch = [&](int t) {
+          const int page = page_next;
+          look(t + 1);
+          there_next = page >= 0;
+          // (a key that is not there: any finite row, as p' is 0)
+#pragma unroll
+          for (int j = 0; j < W; ++j) k_next[j] = v_next[j] = make_uint4(0, 0, 0, 0);
           if (page < 0) return;
-          have = true;
-          const int off = key & ((1 << p.c.shift) - 1);
+          const int off = (it.sp.key(t) + key_in) & ((1 << p.c.shift) - 1);
           const int64_t o = page * p.c.kp + off * p.c.kt + it.sh.group * p.c.kh;
           const uint4* const k = reinterpret_cast<const uint4*>(p.c.k + o);
           const uint4* const v = reinterpret_cast<const uint4*>(p.c.v + o);
 #pragma unroll
-          for (int j = 0; j < W; ++j) kc[j] = __ldg(k + j);
+          for (int j = 0; j < W; ++j) k_next[j] = __ldg(k + j);
 #pragma unroll
-          for (int j = 0; j < W; ++j) vc[j] = __ldg(v + j);
-          const int64_t so =
-              ((page * static_cast<int64_t>(p.G) + it.sh.group) << p.c.shift) + off;
-          ks = __ldg(p.c.ks + so);
-          vs = __ldg(p.c.vs + so);
+          for (int j = 0; j < W; ++j) v_next[j] = __ldg(v + j);
+          const int64_t so = ((page * static_cast<int64_t>(p.G) + it.sh.group) << p.c.shift) + off;
+          ks_next = __ldg(p.c.ks + so);
+          vs_next = __ldg(p.c.vs + so);
         };
+        auto store = [&](uint8_t* tile, const uint4 (&w)[W]) {
+          uint8_t* const dst = tile + key_in * 128;
+#pragma unroll
+          for (int j = 0; j < W; ++j) {
+            const uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int ch = 4 * j + q;
+              *reinterpret_cast<uint4*>(dst + (ch >> 3) * C::kAtomBytes +
+                                        (((ch & 7) ^ (key_in & 7)) << 4)) = codes_chunk(u[q]);
+            }
+          }
+          fence_proxy_async_smem();
+        };
+        look(it.t0);
         fetch(it.t0);
         for (int i = 0; i < nt; ++i) {
           const int64_t g = gt + i;
           const int s = static_cast<int>(g & 1);
           const uint32_t prev = static_cast<uint32_t>(((g - 2) >> 1) & 1);
+          uint4 k[W], v[W];
+#pragma unroll
+          for (int j = 0; j < W; ++j) k[j] = k_next[j], v[j] = v_next[j];
+          const bool have = there_next;
+          const float kstep = __uint_as_float(ks_next << 16),
+                      klow = __uint_as_float(ks_next & 0xffff0000u);
+          const float vstep = __uint_as_float(vs_next << 16),
+                      vlow = __uint_as_float(vs_next & 0xffff0000u);
+          fetch(it.t0 + i + 1);
           if (g >= 2 && !wait_all(kKEmpty + s, prev)) {
             failed = true;
             break;
           }
-          auto store = [&](uint8_t* tile, const uint4 (&w)[W]) {
-            uint8_t* const dst = tile + key_in * 128;
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-              const uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const int ch = 4 * j + q;
-                *reinterpret_cast<uint4*>(dst + (ch >> 3) * C::kAtomBytes +
-                                          (((ch & 7) ^ (key_in & 7)) << 4)) =
-                    have ? codes_chunk(u[q]) : make_uint4(0, 0, 0, 0);
-              }
-            }
-          };
-          store(gbase + C::kOffK + s * C::kTile, kc);
-          // the key's numbers: K's step and middle, log2 of V's step, its
-          // reciprocal, and the middle by that
-          const float kstep = __uint_as_float(ks << 16), klow = __uint_as_float(ks & 0xffff0000u);
-          const float vstep = __uint_as_float(vs << 16), vlow = __uint_as_float(vs & 0xffff0000u);
+          // the key's numbers: K's step and middle, log2 of V's step, its reciprocal
+          // and the middle by that. (Their slot was last read by the softmax of
+          // step g - 4, which is over: the S after its PV is.)
           const float any = vstep == 0.f ? 1.f : vstep;  // (all codes are 0 then)
           const float rs = rcp_approx(any);
-          float* const num = reinterpret_cast<float*>(gbase + C::kOffInfo + (g & 3) * C::kInfoBytes);
-          num[key_in] = have ? kstep : 0.f;
-          num[128 + key_in] = have ? fmaf(8.f, kstep, klow) : 0.f;
-          num[256 + key_in] = have ? lg2_approx(any) : -INFINITY;
-          num[384 + key_in] = have ? rs : 0.f;
-          // (without a step the codes of 0 stand for -8 of a step of 1)
-          num[512 + key_in] = have ? fmaf(8.f, any, vlow) * rs : 0.f;
-          fence_proxy_async_smem();
+          float* const num =
+              reinterpret_cast<float*>(gbase + C::kOffInfo + (g & 3) * C::kInfoBytes) + key_in;
+          num[0] = have ? kstep : 0.f;
+          num[128] = have ? fmaf(8.f, kstep, klow) : 0.f;
+          num[256] = have ? lg2_approx(any) : -INFINITY;
+          num[384] = have ? rs : 0.f;
+          num[512] = have ? fmaf(8.f, any, vlow) * rs : 0.f;
           mbar_arrive(bar(kInfo + static_cast<int>(g & 3)));
+          store(gbase + C::kOffK + s * C::kTile, k);
           mbar_arrive(bar(kKFull + s));
           if (g >= 2 && !wait_all(kVEmpty + s, prev)) {
             failed = true;
             break;
           }
-          store(gbase + C::kOffV + s * C::kTile, vc);
-          fence_proxy_async_smem();
+          store(gbase + C::kOffV + s * C::kTile, v);
           mbar_arrive(bar(kVFull + s));
-          fetch(it.t0 + i + 1);
         }
         gt += nt;
-        ++n;
       }
     }
   };
