@@ -26,7 +26,7 @@ constexpr int kPaMostPerSm = 4;
 constexpr int kPaItemCost = 320;
 // Keys of an item that is never cut, and where there is an item for every SM.
 constexpr int kPaWhole = 512, kPaWholeMany = 2048;
-constexpr int kTcItemCost = 768;  // the same of paged_attn_tc_kernel, whose steps are faster
+constexpr int kTcItemCost = 512;  // the same of paged_attn_tc_kernel, whose steps are faster
 constexpr int kPaLeast = 448;     // keys of a share at least, that cost among them
 constexpr float kPaSlack = 8.0f;
 

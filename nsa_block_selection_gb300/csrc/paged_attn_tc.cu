@@ -703,7 +703,9 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
   // ---- loaders (4 bits): thread <-> key of the step ----
   auto loader = [&]() {
     if constexpr (Q4) {
-      constexpr int W = D / 32;  // 16-byte words of codes of a row
+      constexpr int kLanes = D / 32;         // lanes of a row of codes, 16 bytes each
+      constexpr int kRowsAt = 32 / kLanes;   // rows that a warp loads at once
+      constexpr int W = kLanes;              // 16-byte words of a lane
       const int key_in = threadIdx.x & 127;
       auto wait_all = [&](int b, uint32_t parity) {
         return __all_sync(kFull, wait_phase(bar(b), parity, kWaitLimitNs));
@@ -724,36 +726,43 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
           const int key = it.sp.key(t) + key_in;
           if (!see.nobody(key)) page_next = page_of(p.c, it.b, key);
         };
+        // Codes come four lanes to a row (D = 64: two), 16 bytes each: register j
+        // is of row kRowsAt j + lane / kLanes of the warp's 32.
         auto fetch = [&](int t) {
           const int page = page_next;
           look(t + 1);
           there_next = page >= 0;
-          // (a key that is not there: any finite row, as p' is 0)
+          const int first = it.sp.key(t) + (key_in & ~31), in_page = (1 << p.c.shift) - 1;
 #pragma unroll
-          for (int j = 0; j < W; ++j) k_next[j] = v_next[j] = make_uint4(0, 0, 0, 0);
+          for (int j = 0; j < W; ++j) {
+            const int row = kRowsAt * j + lane / kLanes;
+            const int pg = __shfl_sync(kFull, page, row);
+            // (a key that is not there: any finite row, as p' is 0)
+            k_next[j] = v_next[j] = make_uint4(0, 0, 0, 0);
+            if (pg >= 0) {
+              const int64_t o = pg * p.c.kp + ((first + row) & in_page) * p.c.kt +
+                                it.sh.group * p.c.kh + 16 * (lane % kLanes);
+              k_next[j] = __ldg(reinterpret_cast<const uint4*>(p.c.k + o));
+              v_next[j] = __ldg(reinterpret_cast<const uint4*>(p.c.v + o));
+            }
+          }
           if (page < 0) return;
-          const int off = (it.sp.key(t) + key_in) & ((1 << p.c.shift) - 1);
-          const int64_t o = page * p.c.kp + off * p.c.kt + it.sh.group * p.c.kh;
-          const uint4* const k = reinterpret_cast<const uint4*>(p.c.k + o);
-          const uint4* const v = reinterpret_cast<const uint4*>(p.c.v + o);
-#pragma unroll
-          for (int j = 0; j < W; ++j) k_next[j] = __ldg(k + j);
-#pragma unroll
-          for (int j = 0; j < W; ++j) v_next[j] = __ldg(v + j);
-          const int64_t so = ((page * static_cast<int64_t>(p.G) + it.sh.group) << p.c.shift) + off;
+          const int64_t so = ((page * static_cast<int64_t>(p.G) + it.sh.group) << p.c.shift) +
+                             ((first + lane) & in_page);
           ks_next = __ldg(p.c.ks + so);
           vs_next = __ldg(p.c.vs + so);
         };
         auto store = [&](uint8_t* tile, const uint4 (&w)[W]) {
-          uint8_t* const dst = tile + key_in * 128;
 #pragma unroll
           for (int j = 0; j < W; ++j) {
+            const int row = (key_in & ~31) + kRowsAt * j + lane / kLanes;
+            uint8_t* const dst = tile + row * 128;
             const uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const int ch = 4 * j + q;
+              const int ch = 4 * (lane % kLanes) + q;
               *reinterpret_cast<uint4*>(dst + (ch >> 3) * C::kAtomBytes +
-                                        (((ch & 7) ^ (key_in & 7)) << 4)) = codes_chunk(u[q]);
+                                        (((ch & 7) ^ (row & 7)) << 4)) = codes_chunk(u[q]);
             }
           }
           fence_proxy_async_smem();
