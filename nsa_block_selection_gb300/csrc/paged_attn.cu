@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kPaThreads, PaCfg<D, Q4, NT>::kPerSm)
   for (bool more = !p.cut || sh.begin < sh.end; more;) {
     const int b = sh.item / p.tiles, rt = sh.item - b * p.tiles;
     const int head = sh.group * p.heads_item + head_in;
-    const PaSpan sp = pa_span(p, b, rt, kRowsTile);
+    const PaSpan sp = pa_span<true>(p, b, rt, kRowsTile);
     // steps [t0, t1) of the item, after its cost
     int t0 = 0, t1 = sp.n;
     if (p.cut) {
@@ -849,6 +849,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   if (n > 0 && first == last) return;  // whole in one share
   const int pieces = n > 0 ? last - first + 1 : 0;
   const float* const stats = p.piece + 2 * static_cast<int64_t>(p.ctas) * piece_rows * D;
+  const int at_row = p.many ? ((d >> 1) * piece_rows + prow) * 8 + (d & 1) * 4 : prow * D + 4 * d;
   PaPiece a;
   if (in) {
     for (int i0 = set; i0 < pieces; i0 += 4 * sets) {
@@ -860,9 +861,9 @@ __global__ void __launch_bounds__(kJoinThreads)
         s[k] = make_float2(-INFINITY, 0.f);
         v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (i < pieces) {
-          const int64_t row = (2 * static_cast<int64_t>(first + i) + (i == 0 ? 1 : 0)) * piece_rows + prow;
-          s[k] = *reinterpret_cast<const float2*>(stats + row * 2);
-          v[k] = reinterpret_cast<const float4*>(p.piece + row * D)[d];
+          const int64_t slot = 2 * static_cast<int64_t>(first + i) + (i == 0 ? 1 : 0);
+          s[k] = *reinterpret_cast<const float2*>(stats + (slot * piece_rows + prow) * 2);
+          v[k] = *reinterpret_cast<const float4*>(p.piece + slot * piece_rows * D + at_row);
         }
       }
 #pragma unroll
@@ -887,12 +888,19 @@ __global__ void __launch_bounds__(kJoinThreads)
 
 // ---- host ---------------------------------------------------------------
 
-// Row tiles: 8 rows where a KV head has no more, else 16; from kTcRows rows on
-// whole queries of up to 128 (paged_attn_tc_kernel).
-constexpr int64_t kTcRows = 17;
-bool many_rows(int64_t rows, int64_t hpg) { return rows >= kTcRows && hpg <= 128; }
-int rows_of_tile(int64_t rows, int64_t hpg) {
-  return rows <= 8 ? 8 : many_rows(rows, hpg) ? tc_rows_of_tile(hpg) : 16;
+// Row tiles: 8 rows where a KV head has no more, else 16; from kTcRows rows on (4 bits:
+// kTcRows4, as two tiles of 16 are faster there) whole queries of up to 128
+// (paged_attn_tc_kernel). Measured, 8 rows a token, D = 128, tiles of 16 against
+// paged_attn_tc_kernel: 16 sequences of up to 4000 tokens over 16 bits, 16 rows 36
+// and 39 us, 24 rows 53 and 38; of up to 8000 over 4 bits, 24 rows 75 and 91, 32 rows
+// 82 and 90, 40 rows 120 and 82.
+constexpr int64_t kTcRows = 17, kTcRows4 = 33;
+constexpr int64_t kPaCounts = ((kPaItems + 2) * 8 + 127) / 128 * 128;  // bytes of the counts
+bool many_rows(int64_t rows, int64_t hpg, bool q4) {
+  return rows >= (q4 ? kTcRows4 : kTcRows) && hpg <= 128;
+}
+int rows_of_tile(int64_t rows, int64_t hpg, bool q4) {
+  return rows <= 8 ? 8 : many_rows(rows, hpg, q4) ? tc_rows_of_tile(hpg) : 16;
 }
 
 // KV heads of an item. The rows of a 4-bit cache are 64 or 32 bytes for each
@@ -928,9 +936,31 @@ int check_paged(int64_t B, int64_t M, int64_t H, int64_t G, int64_t D, int dtype
   if (rc != NSA_OK) return rc;
   if (H % G != 0) return NSA_ERR_GROUPS;
   if (M * (H / G) >= int64_t(1) << 30) return NSA_ERR_SHAPE;
-  const int64_t rows = M * (H / G), tile = rows_of_tile(rows, H / G);
+  const int64_t rows = M * (H / G), tile = rows_of_tile(rows, H / G, true);
   if (B * ((rows + tile - 1) / tile) * G >= int64_t(1) << 31) return NSA_ERR_SHAPE;
   return NSA_OK;
+}
+
+// Bytes of a call over a cache of 4 or 16 bits; 0: no item is cut.
+int64_t workspace_for(int64_t B, int64_t M, int64_t H, int64_t G, int64_t D, int64_t tokens,
+                      int64_t window_left, int64_t sinks, bool q4) {
+  const int64_t rows = M * (H / G), tile = rows_of_tile(rows, H / G, q4);
+  const int64_t items = B * ((rows + tile - 1) / tile);
+  if (items == 0 || items > kPaItems) return 0;
+  if (tokens > int64_t(1) << 30) tokens = int64_t(1) << 30;
+  // where every query sees few keys an item is short enough for one CTA, without a
+  // second kernel
+  if (M == 1 && window_left >= 0 && window_left < tokens && sinks < tokens &&
+      window_left + 1 + sinks < tokens)
+    tokens = window_left + 1 + sinks;
+  // (and the running count of steps has 32 bits)
+  if (tokens <= (items * G >= kPaSms ? kPaWholeMany : kPaWhole) ||
+      items * (tokens / kPaTile + 32) >= int64_t(1) << 31)
+    return 0;
+  // two pieces of every share, and the running counts
+  const int64_t ctas = many_rows(rows, H / G, q4) ? kPaSms : kPaMostPerSm * kPaSms;
+  const int heads = many_rows(rows, H / G, q4) ? 1 : heads_of_item(G, D, q4 ? 4 : 16);
+  return 2 * ctas * heads * tile * (D + 2) * 4 + kPaCounts;
 }
 
 // The pieces of items that shares have cut.
@@ -977,7 +1007,7 @@ int launch_paged(PagedProblem& p, const CUtensorMap& tk, const CUtensorMap& tv, 
 
 template <int D, bool BF16>
 int launch_paged_d(PagedProblem& p, const nsa_kv_cache* kv, cudaStream_t st) {
-  if (many_rows(p.rows, p.hpg)) {
+  if (p.many) {
     const int rc = launch_paged_tc(p, kv, D, BF16, st);
     return rc != NSA_OK ? rc : launch_join<D, BF16>(p, tc_rows_of_tile(p.hpg), st);
   }
@@ -1026,22 +1056,9 @@ extern "C" int64_t nsa_paged_attn_workspace_bytes(int64_t B, int64_t M, int64_t 
   const int rc = check_paged(B, M, H, G, D, NSA_F16);
   if (rc != NSA_OK) return rc;
   if (tokens < 0 || sinks < 0) return NSA_ERR_SHAPE;
-  const int64_t rows = M * (H / G), tile = rows_of_tile(rows, H / G);
-  const int64_t items = B * ((rows + tile - 1) / tile);
-  if (items == 0 || items > kPaItems) return 0;
-  // where every query sees few keys an item is short enough for one CTA, without a
-  // second kernel
-  if (M == 1 && window_left >= 0 && window_left < tokens && sinks < tokens &&
-      window_left + 1 + sinks < tokens)
-    tokens = window_left + 1 + sinks;
-  // (and the running count of steps has 32 bits)
-  if (tokens <= (items * G >= kPaSms ? kPaWholeMany : kPaWhole) ||
-      items * (tokens / kPaTile + 32) >= int64_t(1) << 31)
-    return 0;
-  // two pieces of every share, and the running counts
-  const int64_t pieces = many_rows(rows, H / G) ? 2 * kPaSms * tile
-                                                : 2 * kPaMostPerSm * kPaSms * heads_of_item(G, D, 4) * tile;
-  return pieces * (D + 2) * 4 + (kPaItems + 2) * 8;
+  const int64_t a = workspace_for(B, M, H, G, D, tokens, window_left, sinks, false);
+  const int64_t b = workspace_for(B, M, H, G, D, tokens, window_left, sinks, true);
+  return a > b ? a : b;
 }
 
 extern "C" int nsa_paged_attn(const void* Q, const nsa_kv_cache* cache, const int32_t* page_table,
@@ -1062,8 +1079,8 @@ extern "C" int nsa_paged_attn(const void* Q, const nsa_kv_cache* cache, const in
     return NSA_ERR_ALIGN;
   PagedProblem p{};
   if ((rc = take_cache(cache, page_table, table_cols, B, G, D, true, &p.c)) != NSA_OK) return rc;
-  const int64_t need = nsa_paged_attn_workspace_bytes(
-      B, M, H, G, D, table_cols * cache->page_size, window_left, sinks);
+  const int64_t need = workspace_for(B, M, H, G, D, table_cols * cache->page_size, window_left,
+                                     sinks, cache->bits == 4);
   if (need > 0) {
     if (!workspace || workspace_bytes < need) return NSA_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return NSA_ERR_ALIGN;
@@ -1075,20 +1092,20 @@ extern "C" int nsa_paged_attn(const void* Q, const nsa_kv_cache* cache, const in
   p.pos = positions;
   p.pos_b = positions_stride;
   p.count = static_cast<int64_t*>(workspace);
-  p.piece = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + (kPaItems + 2) * 8);
+  p.piece = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kPaCounts);
   p.B = static_cast<int>(B);
   p.M = static_cast<int>(M);
   p.H = static_cast<int>(H);
   p.G = static_cast<int>(G);
   p.hpg = static_cast<int>(H / G);
   p.rows = static_cast<int>(M * (H / G));
-  const bool many = many_rows(p.rows, p.hpg);
+  const bool many = p.many = many_rows(p.rows, p.hpg, cache->bits == 4);
   p.heads_item = many ? 1 : heads_of_item(G, D, cache->bits);
   p.groups = p.G / p.heads_item;
   p.step_shift =
       many ? 7 : cache->bits == 16 ? 4 : p.heads_item == 1 ? 7 : p.heads_item == 2 ? 6 : 5;
   p.item_cost = ((many ? kTcItemCost : kPaItemCost) + (1 << p.step_shift) - 1) >> p.step_shift;
-  const int tile = rows_of_tile(p.rows, p.hpg);
+  const int tile = rows_of_tile(p.rows, p.hpg, cache->bits == 4);
   p.tiles = (p.rows + tile - 1) / tile;
   p.items = static_cast<int>(B * p.tiles);
   p.cut = need > 0;

@@ -26,7 +26,10 @@ constexpr int kPaMostPerSm = 4;
 constexpr int kPaItemCost = 320;
 // Keys of an item that is never cut, and where there is an item for every SM.
 constexpr int kPaWhole = 512, kPaWholeMany = 2048;
-constexpr int kTcItemCost = 512;  // the same of paged_attn_tc_kernel, whose steps are faster
+// The same of paged_attn_tc_kernel, whose steps are faster. (512: a prompt of 4096
+// tokens 212 us instead of 197, 2 x 65 tokens after 8900 others 30 instead of 31; 1024:
+// 197 and 33.)
+constexpr int kTcItemCost = 768;
 constexpr int kPaLeast = 448;     // keys of a share at least, that cost among them
 constexpr float kPaSlack = 8.0f;
 
@@ -41,7 +44,8 @@ struct PagedProblem {
   float* lse;          // [B, H, M] or NULL
   const int32_t* pos;
   int64_t pos_b;
-  // [2 ctas][rows of an item][D], then [2 ctas][rows of an item][2] (reference, sum)
+  // [2 ctas][rows of an item][D] (many rows: [2 ctas][D / 8][rows][8], as the rows are
+  // a thread's each), then [2 ctas][rows of an item][2] (reference, sum)
   float* piece;
   int64_t* count;     // [items + 1]: running steps of the items, and a share's steps
   int B, M, H, G, hpg, rows, tiles, items;  // rows of a KV head, row tiles, B * tiles
@@ -51,7 +55,7 @@ struct PagedProblem {
   int item_cost;           // kPaItemCost in steps
   int split;               // 4 bits: copies that a step's keys take (small pages)
   float sl2;
-  bool cut;
+  bool cut, many;  // many rows: paged_attn_tc_kernel
 };
 
 // What a row tile of a sequence has to read: n steps of 1 << shift keys, of which
@@ -67,15 +71,27 @@ __device__ __forceinline__ int pa_position(const PagedProblem& p, int b, int m) 
   return min(__ldg(p.pos + b * p.pos_b + m), kPaFar);
 }
 
+// WARP: a whole warp calls it, a position a lane; else a thread by itself, several
+// loads at once.
+template <bool WARP>
 __device__ __forceinline__ PaSpan pa_span(const PagedProblem& p, int b, int rt, int rows_tile) {
   const int r0 = rt * rows_tile, r1 = min(r0 + rows_tile, p.rows) - 1;
   PaSpan s{0, 0, 0, p.step_shift, 0x7fffffff, -1};
-  const int m1 = r1 / p.hpg;
-  for (int m = r0 / p.hpg; m <= m1; ++m) {
+  const int m0 = r0 / p.hpg, m1 = r1 / p.hpg;
+#pragma unroll 8
+  for (int m = m0 + (WARP ? static_cast<int>(threadIdx.x) & 31 : 0); m <= m1; m += WARP ? 32 : 1) {
     const int at = pa_position(p, b, m);
-    if (at < 0) continue;
-    s.lo_pos = min(s.lo_pos, at);
+    s.lo_pos = min(s.lo_pos, at < 0 ? 0x7fffffff : at);
     s.hi_pos = max(s.hi_pos, at);
+  }
+  if constexpr (WARP) {
+    if (m1 > m0) {
+      s.lo_pos = __reduce_min_sync(kFull, s.lo_pos);
+      s.hi_pos = __reduce_max_sync(kFull, s.hi_pos);
+    } else {
+      s.lo_pos = __shfl_sync(kFull, s.lo_pos, 0);
+      s.hi_pos = __shfl_sync(kFull, s.hi_pos, 0);
+    }
   }
   if (s.hi_pos < 0) return s;
   const int last = min(s.hi_pos, (p.c.cols << p.c.shift) - 1) >> s.shift;  // (at most 2^30 tokens)
@@ -131,7 +147,7 @@ __device__ __forceinline__ PaShare pa_share(const PagedProblem& p, int rows_tile
   int mine = 0;
   for (int i = i0; i < i1; ++i) {
     count[i] = mine;
-    const int n = pa_span(p, i / p.tiles, i % p.tiles, rows_tile).n;
+    const int n = pa_span<false>(p, i / p.tiles, i % p.tiles, rows_tile).n;
     mine += n > 0 ? n + p.item_cost : 0;
   }
   int scan = mine;

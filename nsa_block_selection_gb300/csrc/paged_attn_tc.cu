@@ -3,25 +3,33 @@
 // items' shares are paged_attn.cu's; here a row tile is up to 128 (query, head) rows
 // of a KV head, the M of the products, and a step 128 keys:
 //   S (128 rows x 128 keys) = Q K^T,  O (128 rows x D) += P V,
-// with S, P and O in tensor memory, as in swa_fwd.cu's kernel of one head: warp 1
-// issues S_0, S_1, PV_0, S_2, PV_1, ... over all of the CTA's items, four softmax
-// warps have a row a thread.
+// with S, P and O in tensor memory. Two groups of four softmax warps, a row a thread,
+// take the steps in turn, each with a running maximum, a sum and an O of its own, which
+// they join at the end of an item: one group's exponentials run beside the other's
+// products, and a row tile needs no more rows for it. Warp 1 issues S_0, S_1, PV_0,
+// S_2, PV_1, ... over all of the CTA's items; P lies over its S.
 //
-// 16 bits: warp 0 brings a step's K and V by TMA, a copy a page (or a part of one); a
-// page that the sequence does not have is asked for outside the map and arrives as
-// zeros. V's rows that no query sees are zeroed by the softmax warps before P is
-// handed over, so whatever they hold never meets a product.
+// 16 bits: warp 0 brings a step's K by TMA, warp 2 its V (with both in one warp the
+// copies alone took a warp 1900 clocks a step, and K waited for V's stage), a copy a
+// page, or a part of one, a lane; a page that the sequence does not have is asked for
+// outside the map and arrives as zeros. V's rows that no query sees are zeroed by the
+// softmax warps before P is handed over, so whatever they hold never meets a product.
 //
-// 4 bits: four loader warps have a key a thread. They load its codes a step ahead and
-// write c - 8, exact in fp16, as the operands' rows; five numbers of a key (steps,
-// the middles low + 8 step, log2 of V's step) go beside them, and a key that nobody
-// sees gets -inf for x and zeros. With k = mid + step (c - 8):
+// 4 bits: four loader warps load the codes a step ahead and write c - 8, exact in
+// fp16, as the operands' rows; five numbers of a key (steps, the middles low + 8 step,
+// log2 of V's step) go beside them, and a key that nobody sees gets -inf for x and
+// zeros. With k = mid + step (c - 8):
 //   x = step ka (q'.(c - 8)) + mid kb + log2 step_v,  p' = 2^(x - r),
 //   l += p' / step_v,  O = sum p' (c - 8) + sum p' mid_v / step_v,
 // q' = 2^e q in fp16, written by the softmax warps, ka and kb the row's factors.
 //
-// What bounds it: the softmax warps, one row a thread: 128 x 128 entries take them
-// some 7 (16 bits) and 12 (4 bits) instructions an entry.
+// What bounds it: a step takes some 1500 clocks (16 bits; the products 800 of the
+// tensor cores' time, a group's softmax 2600 for every other step) and 3300 (4 bits:
+// the loaders, some 600 instructions a warp and step); an item's own cost is some
+// 6000. Prompts of 32 + 4 heads of 128: 16,384 tokens 1750 us (1250 TFLOP/s), 4096
+// tokens 197 us (4 bits 322); 3 x 200 tokens of 64 + 8 heads after 8800 others 178 us
+// (308). One group with two S and a P of its own, and one producer warp: 2160, 232
+// (371), 266 (384).
 //
 // Every mbarrier wait is bounded (1 s); a role that gives up sets the status word
 // and leaves its loop, so every role reaches the teardown, which frees the tensor
@@ -33,6 +41,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kv_cache.cuh"
@@ -45,7 +54,8 @@ namespace nsa {
 namespace {
 
 constexpr int kTcKeys = 128;
-constexpr uint32_t kTcTmem = 512, kColS = 0, kColO = 256, kColP = 384;
+// Tensor memory of softmax group x: S (and over it P) at 128 x, O at 256 + 128 x.
+constexpr uint32_t kTcTmem = 512, kColS = 0, kColO = 256;
 
 enum TcBar : int {
   kQFull = 0,    // 2 Q buffers
@@ -57,26 +67,27 @@ enum TcBar : int {
   kSFull = 12,   // 2 S buffers
   kPFull = 14,   // 2 P buffers
   kPvDone = 16,  // 2
-  kOEmpty = 18,  // the softmax warps have read O of the item before
+  kMerge = 18,   // both groups' sums of an item are there
+  kOEmpty = 19,  // the softmax warps have read O of the item before
   // 4: a step's facts for the softmax (which pages are there, or the keys' numbers).
   // Four, as K of the step after the next may come before its softmax begins.
-  kInfo = 19,
-  kTcBars = 23
+  kInfo = 20,
+  kTcBars = 24
 };
 
 template <int D, bool Q4>
 struct TcCfg {
-  // warps: 0 TMA, 1 MMA, 2 to 5 softmax; 4 bits: warpgroups (., MMA, ., .), softmax,
-  // loaders
-  [[maybe_unused]] static constexpr int kSoftWarp = 4, kLoadWarp = 8;
-  static constexpr int kThreads = Q4 ? 384 : 192;
+  // warpgroups: (Q and K, MMA, V, .), two of softmax; 4 bits: and one of loaders
+  static constexpr int kSoftWarp = 4, kLoadWarp = 12;
+  static constexpr int kThreads = Q4 ? 512 : 384;
   [[maybe_unused]] static constexpr int kAtoms = D / 64;
   static constexpr int kAtomBytes = 128 * 128;
   static constexpr int kTile = 128 * D * 2;  // Q, K or V
   static constexpr int kOffK = 2 * kTile, kOffV = 4 * kTile;
   static constexpr int kOffInfo = 6 * kTile;  // 4 x (5 numbers of each key, or a mask)
   static constexpr int kInfoBytes = Q4 ? 5 * kTcKeys * 4 : 16;
-  static constexpr int kOffBar = kOffInfo + 4 * kInfoBytes;
+  static constexpr int kOffStat = kOffInfo + 4 * kInfoBytes;  // a group's rows' 4 floats
+  static constexpr int kOffBar = kOffStat + 2 * 128 * 16;
   static constexpr int kOffTmem = kOffBar + kTcBars * 8;
   static constexpr int kOffCount = kOffTmem + 8;
   static constexpr int kUsed = kOffCount + (kPaItems + 1) * 4 + 64 + 1024;
@@ -96,7 +107,7 @@ struct TcWalk {
   __device__ __forceinline__ void load(const PagedProblem& p, int rows_tile) {
     b = sh.item / p.tiles;
     rt = sh.item - b * p.tiles;
-    sp = pa_span(p, b, rt, rows_tile);
+    sp = pa_span<true>(p, b, rt, rows_tile);
     t0 = 0;
     t1 = sp.n;
     if (p.cut) {
@@ -174,6 +185,22 @@ __device__ __forceinline__ uint32_t columns(int lo, int hi) {
   return lo <= 0 ? below : lo > 31 ? 0u : below & (~0u << lo);
 }
 
+// 32 bytes, in one store where the address allows it.
+__device__ __forceinline__ void store32(void* dst, const uint4& a, const uint4& b) {
+  if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst), "r"(a.x),
+                 "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = a;
+    reinterpret_cast<uint4*>(dst)[1] = b;
+  }
+}
+__device__ __forceinline__ uint4 words(const float* f) {
+  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                    __float_as_uint(f[3]));
+}
+
 // Two codes of the bits under 0x000f000f as fp16 c - 8.
 __device__ __forceinline__ uint32_t less8(uint32_t two) {
   const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&two),
@@ -205,7 +232,7 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
   int* const sums = count + kPaItems + 1;
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(bar(kQFull + s), Q4 ? 128 : 1);
+      mbar_init(bar(kQFull + s), Q4 ? 256 : 1);
       mbar_init(bar(kQEmpty + s), 1);
       mbar_init(bar(kKFull + s), Q4 ? 128 : 1);
       mbar_init(bar(kKEmpty + s), 1);
@@ -215,7 +242,8 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
       mbar_init(bar(kPFull + s), 128);
       mbar_init(bar(kPvDone + s), 1);
     }
-    mbar_init(bar(kOEmpty), 128);
+    mbar_init(bar(kMerge), 256);
+    mbar_init(bar(kOEmpty), 256);
     for (int s = 0; s < 4; ++s) mbar_init(bar(kInfo + s), Q4 ? 128 : 1);
     fence_mbar_init();
   }
@@ -236,86 +264,73 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
   int64_t gt = 0;  // steps of the items before
   int n = 0;       // items with steps before
 
-  auto producer = [&]() {
-    // ---- TMA producer (16 bits): the whole warp keeps step, lane 0 copies ----
+  // ---- TMA producers (16 bits): one warp brings Q and K, one V ----
+  auto producer = [&](auto value_c) {
     if constexpr (!Q4) {
+      constexpr bool V = decltype(value_c)::value;
+      constexpr int kFull_ = V ? kVFull : kKFull, kEmpty_ = V ? kVEmpty : kKEmpty;
+      constexpr int kOff = V ? C::kOffV : C::kOffK;
+      const CUtensorMap* const tm = V ? &tmV : &tmK;
       const uint64_t keep = p.tiles > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
-      const uint64_t once = l2_policy_evict_first();
       const int rows = min(kTcKeys, 1 << p.c.shift);  // keys of a copy
       const int split = kTcKeys / rows;
+      // lane l < split * kAtoms issues atom l % kAtoms of copy l / kAtoms
+      const int part = lane / C::kAtoms, atom = lane % C::kAtoms;
+      const uint32_t dst = base + kOff + atom * C::kAtomBytes + part * rows * 128;
+      auto wait_all = [&](int b, uint32_t parity) {
+        return __all_sync(kFull, wait_phase(bar(b), parity, kWaitLimitNs));
+      };
       for (; it.more && !failed; it.next(p, count, rows_tile)) {
         const int nt = it.t1 - it.t0;
         if (nt <= 0) continue;
-        const int qb = n & 1;
-        // the pages of step t's copies, one a lane
+        // the page of this lane's copy of step t
         auto look = [&](int t) {
-          return t < it.t1 && lane < split ? page_of(p.c, it.b, it.sp.key(t) + lane * rows) : -1;
+          return t < it.t1 && part < split ? page_of(p.c, it.b, it.sp.key(t) + part * rows) : -1;
         };
         int page_next = look(it.t0);
-        bool ok = true;
-        if (lane == 0) {
-          ok = n < 2 || wait_phase(bar(kQEmpty + qb), ((n - 2) >> 1) & 1, kWaitLimitNs);
-          if (ok) {
-            mbar_arrive_expect_tx(bar(kQFull + qb), rows_tile * D * 2);
-            for (int a = 0; a < C::kAtoms; ++a)
-              tma_load_4d(base + qb * C::kTile + a * C::kAtomBytes, &tmQ, bar(kQFull + qb), a * 64,
-                          it.sh.group * p.hpg, it.rt * (rows_tile / p.hpg), it.b, once);
+        if constexpr (!V) {
+          const int qb = n & 1;
+          if (n >= 2 && !wait_all(kQEmpty + qb, ((n - 2) >> 1) & 1)) {
+            failed = true;
+            break;
           }
+          if (lane == 0) mbar_arrive_expect_tx(bar(kQFull + qb), rows_tile * D * 2);
+          __syncwarp();
+          if (lane < C::kAtoms)
+            tma_load_4d(base + qb * C::kTile + lane * C::kAtomBytes, &tmQ, bar(kQFull + qb),
+                        lane * 64, it.sh.group * p.hpg, it.rt * (rows_tile / p.hpg), it.b,
+                        l2_policy_evict_first());
         }
         for (int i = 0; i < nt; ++i) {
           const int64_t g = gt + i;
           const int s = static_cast<int>(g & 1);
-          const uint32_t prev = static_cast<uint32_t>(((g - 2) >> 1) & 1);
           const int page = page_next;
-          const uint32_t there = __ballot_sync(kFull, lane < split && page >= 0);
           page_next = look(it.t0 + i + 1);
           const int off = it.sp.key(it.t0 + i) & ((1 << p.c.shift) - 1);
-          ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
-          if (!ok) break;
+          if (g >= 2 && !wait_all(kEmpty_ + s, static_cast<uint32_t>(((g - 2) >> 1) & 1))) {
+            failed = true;
+            break;
+          }
+          const uint32_t there = __ballot_sync(kFull, page >= 0);
           if (lane == 0) {
-            ok = g < 2 || wait_phase(bar(kKEmpty + s), prev, kWaitLimitNs);
-            if (ok) {
+            if constexpr (!V) {
               *reinterpret_cast<uint32_t*>(gbase + C::kOffInfo + (g & 3) * C::kInfoBytes) = there;
               mbar_arrive(bar(kInfo + static_cast<int>(g & 3)));
-              mbar_arrive_expect_tx(bar(kKFull + s), C::kTile);
             }
+            mbar_arrive_expect_tx(bar(kFull_ + s), C::kTile);
           }
-          ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
-          if (!ok) break;
-          for (int j = 0; j < split; ++j) {
-            const int pg = __shfl_sync(kFull, page, j);
-            if (lane == 0)
-              for (int a = 0; a < C::kAtoms; ++a)
-                tma_load_4d(base + C::kOffK + s * C::kTile + a * C::kAtomBytes + j * rows * 128, &tmK,
-                            bar(kKFull + s), a * 64, it.sh.group, split > 1 ? 0 : off,
-                            pg < 0 ? p.c.pages : pg, keep);
-          }
-          if (lane == 0) {
-            ok = g < 2 || wait_phase(bar(kVEmpty + s), prev, kWaitLimitNs);
-            if (ok) mbar_arrive_expect_tx(bar(kVFull + s), C::kTile);
-          }
-          ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
-          if (!ok) break;
-          for (int j = 0; j < split; ++j) {
-            const int pg = __shfl_sync(kFull, page, j);
-            if (lane == 0)
-              for (int a = 0; a < C::kAtoms; ++a)
-                tma_load_4d(base + C::kOffV + s * C::kTile + a * C::kAtomBytes + j * rows * 128, &tmV,
-                            bar(kVFull + s), a * 64, it.sh.group, split > 1 ? 0 : off,
-                            pg < 0 ? p.c.pages : pg, keep);
-          }
+          __syncwarp();
+          if (part < split)
+            tma_load_4d(dst + s * C::kTile, tm, bar(kFull_ + s), atom * 64, it.sh.group,
+                        split > 1 ? 0 : off, page < 0 ? p.c.pages : page, keep);
         }
-        failed = __shfl_sync(kFull, ok ? 0 : 1, 0) != 0;
         gt += nt;
         ++n;
       }
       if (failed) {  // leave nothing in flight
         if (lane == 0)
           for (int s = 0; s < 2; ++s)
-            for (int ph = 0; ph < 2; ++ph) {
-              wait_phase(bar(kKFull + s), ph, kWaitLimitNs / 8);
-              wait_phase(bar(kVFull + s), ph, kWaitLimitNs / 8);
-            }
+            for (int ph = 0; ph < 2; ++ph) wait_phase(bar(kFull_ + s), ph, kWaitLimitNs / 8);
         __syncwarp();
       }
     }
@@ -327,88 +342,113 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
     constexpr uint32_t idesc_o = umma_idesc_f16(128, D, kBf, true);
     const uint64_t k_major = umma_desc_sw128(base, 16);
     const uint64_t mn_major = umma_desc_sw128(base, C::kAtomBytes);
+    // (the whole warp waits and one lane issues: under a branch an MMA costs more)
+    const uint32_t on = elect_one();
+    auto wait_all = [&](int b, uint32_t parity) {
+      return __all_sync(kFull, wait_phase(bar(b), parity, kWaitLimitNs));
+    };
     auto issue_s = [&](int64_t g, int qb) -> bool {
       const int s = static_cast<int>(g & 1);
-      if (!wait_phase(bar(kKFull + s), static_cast<uint32_t>((g >> 1) & 1), kWaitLimitNs))
-        return false;
+      if (!wait_all(kKFull + s, static_cast<uint32_t>((g >> 1) & 1))) return false;
       tc_fence_after();
-      const uint32_t d = tmem + kColS + static_cast<uint32_t>(s) * kTcKeys;
+      const uint32_t d = tmem + kColS + static_cast<uint32_t>(s) * 128;
       const uint64_t q = desc_at(k_major, qb * C::kTile);
       const uint64_t k = desc_at(k_major, C::kOffK + s * C::kTile);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = (kk >> 2) * C::kAtomBytes + (kk & 3) * 32;
-        tc_mma(d, desc_at(q, off), desc_at(k, off), idesc_s, kk > 0 ? 1u : 0u);
+        tc_mma_if(on, d, desc_at(q, off), desc_at(k, off), idesc_s, kk > 0 ? 1u : 0u);
       }
-      tc_commit(bar(kKEmpty + s));
-      tc_commit(bar(kSFull + s));
+      tc_commit_if(on, bar(kKEmpty + s));
+      tc_commit_if(on, bar(kSFull + s));
       return true;
     };
     auto issue_pv = [&](int64_t g, bool first, int item) -> bool {
       const int s = static_cast<int>(g & 1);
       const uint32_t ph = static_cast<uint32_t>((g >> 1) & 1);
-      if (!wait_phase(bar(kPFull + s), ph, kWaitLimitNs)) return false;
-      if (!wait_phase(bar(kVFull + s), ph, kWaitLimitNs)) return false;
-      if (first && item >= 1 && !wait_phase(bar(kOEmpty), (item - 1) & 1, kWaitLimitNs))
-        return false;
+      if (!wait_all(kPFull + s, ph) || !wait_all(kVFull + s, ph)) return false;
+      if (first && item >= 1 && !wait_all(kOEmpty, (item - 1) & 1)) return false;
       tc_fence_after();
       const uint64_t v = desc_at(mn_major, C::kOffV + s * C::kTile);
-      const uint32_t pcol = tmem + kColP + static_cast<uint32_t>(s) * (kTcKeys / 2);
+      const uint32_t pcol = tmem + kColS + static_cast<uint32_t>(s) * 128;
+      const uint32_t ocol = tmem + kColO + static_cast<uint32_t>(s) * 128;
 #pragma unroll
       for (int kk = 0; kk < kTcKeys / 16; ++kk)
-        tc_mma_ts(tmem + kColO, pcol + 8 * kk, desc_at(v, kk * 2048), idesc_o,
-                  (!first || kk > 0) ? 1u : 0u);
-      tc_commit(bar(kVEmpty + s));
-      tc_commit(bar(kPvDone + s));
+        tc_mma_ts_if(on, ocol, pcol + 8 * kk, desc_at(v, kk * 2048), idesc_o,
+                     (!first || kk > 0) ? 1u : 0u);
+      tc_commit_if(on, bar(kVEmpty + s));
+      tc_commit_if(on, bar(kPvDone + s));
       return true;
     };
     bool ok = true;
-    int64_t pend = -1;  // the step whose PV is still to be issued
-    bool pend_first = false;
-    int pend_n = 0;
-    for (; it.more && !failed; it.next(p, count, rows_tile)) {
+    int64_t pv = 0;  // the next step whose PV is to be issued
+    // of the last two steps: whether they are their group's first of the item, and its number
+    bool first[2] = {false, false};
+    int item[2] = {0, 0};
+    auto values_before = [&](int64_t g) {
+      for (; ok && pv < g; ++pv) {
+        const bool odd = pv & 1;
+        ok = issue_pv(pv, odd ? first[1] : first[0], odd ? item[1] : item[0]);
+      }
+    };
+    for (; it.more && ok; it.next(p, count, rows_tile)) {
       const int nt = it.t1 - it.t0;
       if (nt <= 0) continue;
-      if (lane == 0) {
-        const int qb = n & 1;
-        // (4 bits: Q comes from the softmax warps once they have the last item's O,
-        // so its last PV cannot wait for this item's first S)
-        if (Q4 && pend >= 0) {
-          ok = issue_pv(pend, pend_first, pend_n);
-          pend = -1;
-        }
-        ok = ok && wait_phase(bar(kQFull + qb), (n >> 1) & 1, kWaitLimitNs);
-        for (int i = 0; i < nt && ok; ++i) {
-          ok = issue_s(gt + i, qb);
-          if (ok && i == nt - 1) tc_commit(bar(kQEmpty + qb));
-          if (ok && pend >= 0) ok = issue_pv(pend, pend_first, pend_n);
-          pend = gt + i;
-          pend_first = i == 0;
-          pend_n = n;
+      const int qb = n & 1;
+      // (4 bits: Q comes from the softmax warps once they have the last item's O,
+      // so its last PVs cannot wait for this item's first S)
+      if (Q4) values_before(gt);
+      ok = ok && wait_all(kQFull + qb, (n >> 1) & 1);
+      for (int i = 0; i < nt && ok; ++i) {
+        // S of step g takes the place of step g - 2's P: it is issued after the PV that
+        // reads it, and the tensor pipe runs the MMAs in that order
+        const int64_t g = gt + i;
+        values_before(g - 1);
+        ok = ok && issue_s(g, qb);
+        if (ok && i == nt - 1) tc_commit_if(on, bar(kQEmpty + qb));
+        if (g & 1) {
+          first[1] = i < 2;
+          item[1] = n;
+        } else {
+          first[0] = i < 2;
+          item[0] = n;
         }
       }
-      failed = __shfl_sync(kFull, ok ? 0 : 1, 0) != 0;
       gt += nt;
       ++n;
     }
-    if (lane == 0 && !failed && pend >= 0) ok = issue_pv(pend, pend_first, pend_n);
-    failed = __shfl_sync(kFull, ok ? 0 : 1, 0) != 0;
+    values_before(gt);
+    failed = !ok;
   };
   auto softmax = [&]() {
-    // ---- softmax: thread <-> row of the item's tile ----
-    const int quarter = warp & 3;
+    // ---- softmax: thread <-> row of the item's tile; group 0 has the even steps ----
+    constexpr int kUnroll = Q4 ? 1 : kTcKeys / 32;
+    const int quarter = warp & 3, group = (warp - C::kSoftWarp) >> 2;
     const int row = quarter * 32 + lane;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     auto wait_all = [&](int b, uint32_t parity) {
       return __all_sync(kFull, wait_phase(bar(b), parity, kWaitLimitNs));
     };
-    for (; it.more && !failed; it.next(p, count, rows_tile)) {
-      const int nt = it.t1 - it.t0;
-      if (nt <= 0 && p.cut) continue;  // (nothing of it in this share)
+    // the row's query and head in the item, looked up with it
+    bool next_mine = false;
+    int next_mq = 0, next_h = 0, next_pos = -1;
+    auto place = [&]() {
       const int rw = it.rt * rows_tile + row;
-      const bool mine = row < rows_tile && rw < p.rows;
-      const int mq = rw / p.hpg, h = it.sh.group * p.hpg + rw - mq * p.hpg;
-      const int pos = mine ? pa_position(p, it.b, mq) : -1;
+      next_mine = it.more && row < rows_tile && rw < p.rows;
+      next_mq = rw / p.hpg;
+      next_h = it.sh.group * p.hpg + rw - next_mq * p.hpg;
+      next_pos = next_mine ? pa_position(p, it.b, next_mq) : -1;
+    };
+    place();
+    while (it.more) {
+      const int nt = it.t1 - it.t0;
+      if (nt <= 0 && p.cut) {  // (nothing of it in this share)
+        it.next(p, count, rows_tile);
+        place();
+        continue;
+      }
+      const bool mine = next_mine;
+      const int mq = next_mq, h = next_h, pos = next_pos;
       const PaSight see{it.sp.lo_pos, it.sp.hi_pos, p.left, p.sinks};
       // which of the 32 keys from `key` on this thread's query sees
       auto seen = [&](int key) {
@@ -451,8 +491,9 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
               f[j] = __half2float(__float2half_rn(f[j] * up));
               sum += f[j];
             }
-            *reinterpret_cast<uint4*>(dst + (i >> 3) * C::kAtomBytes + (((i & 7) ^ (row & 7)) << 4)) =
-                make_uint4(pack_half2(f[0], f[4]), pack_half2(f[1], f[5]), pack_half2(f[2], f[6]),
+            if (i / (D / 16) == group)  // (half of the row each)
+              *reinterpret_cast<uint4*>(dst + (i >> 3) * C::kAtomBytes + (((i & 7) ^ (row & 7)) << 4)) =
+                  make_uint4(pack_half2(f[0], f[4]), pack_half2(f[1], f[5]), pack_half2(f[2], f[6]),
                            pack_half2(f[3], f[7]));
           }
           fence_proxy_async_smem();
@@ -462,9 +503,11 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
         }
       }
       float ref = -INFINITY, neg = 0.f, l = 0.f, mid_sum = 0.f;
-      for (int i = 0; i < nt; ++i) {
+      constexpr uint32_t kNoRow = 0xff800000u;  // -inf
+      const int begin = (static_cast<int>(gt) ^ group) & 1;  // the group's first step
+      const int sb = group;
+      for (int i = begin; i < nt; i += 2) {
         const int64_t g = gt + i;
-        const int sb = static_cast<int>(g & 1);
         if (!wait_all(kSFull + sb, static_cast<uint32_t>((g >> 1) & 1)) ||
             !wait_all(kInfo + static_cast<int>(g & 3), static_cast<uint32_t>((g >> 2) & 1))) {
           failed = true;
@@ -475,21 +518,41 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
         const uint8_t* const info = gbase + C::kOffInfo + (g & 3) * C::kInfoBytes;
         const bool inside = n0 + kTcKeys - 1 <= see.lo_pos &&
                             (n0 >= see.hi_pos - see.left || n0 + kTcKeys <= see.sinks);
-        [[maybe_unused]] uint32_t sr[Q4 ? 1 : kTcKeys];
+        // The largest x: S in 32 columns at a time, read again for the exponentials
+        // (a row of 128 beside them does not fit the registers of two groups). Over
+        // S come the x of 4 bits, and -inf where a key is not seen; 16 bits: whose
+        // page is not there (4 bits: the key's numbers say so).
+        bool masked = !inside;
+        [[maybe_unused]] uint32_t have = ~0u;  // bit j: the page of keys 16 j .. of the step is there
+        if constexpr (!Q4) {
+          // (a bit for each of kAtoms copies of a page's keys)
+          const uint32_t there = *reinterpret_cast<const uint32_t*>(info);
+          const int shift = min(7, p.c.shift);
+          if (there != (1u << ((kTcKeys >> shift) * C::kAtoms)) - 1u) {
+            masked = true;
+            have = 0u;
+            for (int j = 0; j < kTcKeys / 16; ++j)
+              have |= (there >> ((16 * j >> shift) * C::kAtoms) & 1u) << j;
+          }
+        }
         float m8[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) m8[j] = -INFINITY;
-        if constexpr (Q4) {
-          // x over S, 32 columns at a time: beside the keys' numbers a row of 128
-          // does not fit the registers. (Keys that are not there, or that nobody
-          // sees, have -inf.)
-          const ulonglong2* const num = reinterpret_cast<const ulonglong2*>(info);
-          const uint64_t ka2 = pair(ka, ka), kb2 = pair(kb, kb);
-#pragma unroll 1
-          for (int c = 0; c < kTcKeys / 32; ++c) {
-            uint32_t x[32];
-            tc_ld32(lane_addr + kColS + sb * kTcKeys + 32 * c, x);
-            tc_wait_ld();
+        const uint32_t s_addr = lane_addr + kColS + sb * kTcKeys;
+        // (16 bits: the next columns come while these are worked on; 4 bits: no registers)
+        constexpr int kAhead = Q4 ? 0 : 1;
+        uint32_t xs[1 + kAhead][32];
+        auto columns_of = [&](int c) { tc_ld32(s_addr + 32 * c, xs[c & kAhead]); };
+        if (kAhead) columns_of(0);
+#pragma unroll kUnroll
+        for (int c = 0; c < kTcKeys / 32; ++c) {
+          uint32_t(&x)[32] = xs[c & kAhead];
+          if (!kAhead) columns_of(c);
+          tc_wait_ld();
+          if (kAhead && c + 1 < kTcKeys / 32) columns_of(c + 1);
+          if constexpr (Q4) {
+            const ulonglong2* const num = reinterpret_cast<const ulonglong2*>(info);
+            const uint64_t ka2 = pair(ka, ka), kb2 = pair(kb, kb);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const ulonglong2 st = num[8 * c + j], md = num[32 + 8 * c + j], lg = num[64 + 8 * c + j];
@@ -500,76 +563,50 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
               x[4 * j] = __float_as_uint(x0.x), x[4 * j + 1] = __float_as_uint(x0.y);
               x[4 * j + 2] = __float_as_uint(x1.x), x[4 * j + 3] = __float_as_uint(x1.y);
             }
-            if (!inside) {
-              const uint32_t bits = seen(n0 + 32 * c);
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!(bits >> j & 1u)) x[j] = __float_as_uint(-INFINITY);
-            }
-#pragma unroll
-            for (int j = 0; j < 32; ++j) m8[j & 7] = fmaxf(m8[j & 7], __uint_as_float(x[j]));
-            tc_st32(lane_addr + kColS + sb * kTcKeys + 32 * c, x);
           }
-          tc_wait_st();
-        } else {
+          if (masked) {
+            uint32_t bits = seen(n0 + 32 * c);
+            if constexpr (!Q4)
+              bits &= (have >> (2 * c) & 1u ? 0xffffu : 0u) | (have >> (2 * c) & 2u ? ~0xffffu : 0u);
 #pragma unroll
-          for (int c = 0; c < kTcKeys / 32; ++c)
-            tc_ld32(lane_addr + kColS + sb * kTcKeys + 32 * c,
-                    *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * c]));
-          tc_wait_ld();
-          const uint32_t there = *reinterpret_cast<const uint32_t*>(info);
-          const int rows = min(kTcKeys, 1 << p.c.shift), split = kTcKeys / rows;
-          if (!inside || there != (1u << split) - 1u) {
-            // bit j: the page of keys 16 j .. of the step is there
-            uint32_t have = 0u;
-#pragma unroll
-            for (int j = 0; j < kTcKeys / 16; ++j)
-              have |= (there >> (16 * j / rows) & 1u) << j;
-#pragma unroll
-            for (int c = 0; c < kTcKeys / 32; ++c) {
-              const uint32_t bits = seen(n0 + 32 * c) & ((have >> (2 * c) & 1u ? 0xffffu : 0u) |
-                                                         (have >> (2 * c) & 2u ? ~0xffffu : 0u));
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!(bits >> j & 1u)) sr[32 * c + j] = __float_as_uint(-INFINITY);
-            }
-            // V rows that no query sees may hold anything (this thread's: key `row`)
-            if (!wait_all(kVFull + sb, static_cast<uint32_t>((g >> 1) & 1))) {
-              failed = true;
-              break;
-            }
-            if (see.nobody(n0 + row)) {
-#pragma unroll
-              for (int c = 0; c < D / 8; ++c)
-                *reinterpret_cast<uint4*>(gbase + C::kOffV + sb * C::kTile + (c >> 3) * C::kAtomBytes +
-                                          row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();  // before P is handed over
+            for (int j = 0; j < 32; ++j)
+              if (!(bits >> j & 1u)) x[j] = kNoRow;
           }
 #pragma unroll
-          for (int j = 0; j < kTcKeys; ++j) m8[j & 7] = fmaxf(m8[j & 7], __uint_as_float(sr[j]));
+          for (int j = 0; j < 32; ++j) m8[j & 7] = fmaxf(m8[j & 7], __uint_as_float(x[j]));
+          if (Q4 || masked) tc_st32(s_addr + 32 * c, x);
+        }
+        if (Q4 || masked) tc_wait_st();
+        if (!Q4 && masked) {
+          // V rows that no query sees may hold anything (this thread's: key `row`)
+          if (!wait_all(kVFull + sb, static_cast<uint32_t>((g >> 1) & 1))) {
+            failed = true;
+            break;
+          }
+          if (see.nobody(n0 + row)) {
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+              *reinterpret_cast<uint4*>(gbase + C::kOffV + sb * C::kTile + (c >> 3) * C::kAtomBytes +
+                                        row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();  // before P is handed over
         }
         float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
                          fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
         if constexpr (!Q4) mx *= ka;
         const bool move = mx > ref + kPaSlack;
+        if (kAhead) columns_of(0);
         if (__any_sync(kFull, move)) {
           const float alpha = move ? ex2(ref - mx) : 1.f;
-          if (i > 0) {
-            if (!wait_all(kPvDone + static_cast<int>((g - 1) & 1),
-                          static_cast<uint32_t>(((g - 1) >> 1) & 1))) {
-              failed = true;
-              break;
-            }
-            tc_fence_after();
+          if (i >= 2) {  // (the group's last PV is over: this S came after it)
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
-              tc_ld32(lane_addr + kColO + 32 * c, o);
+              tc_ld32(lane_addr + kColO + sb * 128 + 32 * c, o);
               tc_wait_ld();
 #pragma unroll
               for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-              tc_st32(lane_addr + kColO + 32 * c, o);
+              tc_st32(lane_addr + kColO + sb * 128 + 32 * c, o);
             }
             tc_wait_st();
           }
@@ -579,11 +616,6 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
             ref = mx;
             neg = -mx;
           }
-        }
-        // P buffer sb was last read by the PV of step g - 2
-        if (g >= 2 && !wait_all(kPvDone + sb, static_cast<uint32_t>(((g - 2) >> 1) & 1))) {
-          failed = true;
-          break;
         }
         uint64_t l2[2] = {0, 0}, s2[2] = {0, 0};  // sums of pairs
         const uint64_t neg2 = pair(neg, neg), ka2 = pair(ka, ka);
@@ -613,19 +645,14 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
               l2[1] = add2(l2[1], y[1]);
             }
           }
-          tc_st16(lane_addr + kColP + sb * (kTcKeys / 2) + 16 * q, pw);
+          tc_st16(lane_addr + kColS + sb * kTcKeys + 16 * q, pw);  // (S of them is read)
         };
-        if constexpr (Q4) {
-#pragma unroll 1
-          for (int q = 0; q < kTcKeys / 32; ++q) {
-            uint32_t x[32];
-            tc_ld32(lane_addr + kColS + sb * kTcKeys + 32 * q, x);
-            tc_wait_ld();
-            exps(x, q);
-          }
-        } else {
-#pragma unroll
-          for (int q = 0; q < kTcKeys / 32; ++q) exps(&sr[32 * q], q);
+#pragma unroll kUnroll
+        for (int q = 0; q < kTcKeys / 32; ++q) {
+          if (!kAhead) columns_of(q);
+          tc_wait_ld();
+          if (kAhead && q + 1 < kTcKeys / 32) columns_of(q + 1);
+          exps(xs[q & kAhead], q);
         }
         const float2 lsum = unpair(add2(l2[0], l2[1]));
         l += lsum.x + lsum.y;
@@ -638,63 +665,90 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
         mbar_arrive(bar(kPFull + sb));
       }
       if (failed) break;
-      // epilogue: O into registers, released to the next item's PVs
-      uint32_t o[D];
+      // epilogue: the groups' sums joined, half of the row's columns each; O is
+      // released to the next item's PVs. (The next item is looked up meanwhile.)
+      const bool whole = it.t0 == 0 && it.t1 == it.sp.n;
+      const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (it.t0 == 0 ? 1 : 0);
+      const int64_t out_row = (static_cast<int64_t>(it.b) * p.M + mq) * p.H + h;
+      const int64_t lse_at = (static_cast<int64_t>(it.b) * p.H + h) * p.M + mq;
+      it.next(p, count, rows_tile);
+      place();
+      float top = -INFINITY, f_own = 0.f, f_other = 0.f;
       if (nt > 0) {
         const int64_t gl = gt + nt - 1;
-        if (!wait_all(kPvDone + static_cast<int>(gl & 1), static_cast<uint32_t>((gl >> 1) & 1))) {
+        if (!wait_all(kPvDone + static_cast<int>(gl & 1), static_cast<uint32_t>((gl >> 1) & 1)) ||
+            (nt > 1 && !wait_all(kPvDone + static_cast<int>((gl - 1) & 1),
+                                 static_cast<uint32_t>(((gl - 1) >> 1) & 1)))) {
+          failed = true;
+          break;
+        }
+        float4* const stat = reinterpret_cast<float4*>(gbase + C::kOffStat);
+        stat[128 * group + row] = make_float4(ref, l, mid_sum, 0.f);
+        mbar_arrive(bar(kMerge));
+        if (!wait_all(kMerge, n & 1)) {
           failed = true;
           break;
         }
         tc_fence_after();
+        const float4 other = stat[128 * (group ^ 1) + row];
+        top = fmaxf(ref, other.x);
+        f_own = ref == top ? 1.f : ex2(ref - top);
+        f_other = other.x == top ? 1.f : ex2(other.x - top);
+        l = fmaf(other.y, f_other, l * f_own);
+        mid_sum = fmaf(other.z, f_other, mid_sum * f_own);
+      }
+      const bool none = whole && (l == 0.f || pos < 0);
+      const float inv = !whole ? 1.f : none ? 0.f : 1.f / l;
+#pragma unroll kUnroll
+      for (int c = 0; c < D / 64; ++c) {
+        float o[32];
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c)
-          tc_ld32(lane_addr + kColO + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&o[32 * c]));
-        tc_wait_ld();
+        for (int j = 0; j < 32; ++j) o[j] = 0.f;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (nt <= 0 || (nt == 1 && x != static_cast<int>(gt & 1))) continue;  // (had no step)
+          const float f = x == group ? f_own : f_other;
+          uint32_t v[32];
+          tc_ld32(lane_addr + kColO + 128 * x + group * (D / 2) + 32 * c, v);
+          tc_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = fmaf(__uint_as_float(v[j]), f, o[j]);
+        }
+        if (mine) {
+          const int64_t col = group * (D / 2) + 32 * c;
+          uint16_t* const dst = p.o + out_row * D + col;
+          float* const piece = p.piece + slot * rows_tile * D + (col * rows_tile + row * 8);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            float e[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              // (4 bits: columns are in the codes' order, and p mid_v is added)
+              const float v = Q4 ? o[16 * q + (j & 8) + code_place(j & 7)] + mid_sum : o[16 * q + j];
+              e[j] = none ? 0.f : v * inv;
+            }
+            if (whole) {
+              const uint4 lo = pack8<BF16>(e), hi = pack8<BF16>(e + 8);
+              store32(dst + 16 * q, lo, hi);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; j += 8)
+                store32(piece + (16 * q + j) * rows_tile, words(e + j), words(e + j + 4));
+            }
+          }
+        }
+        __syncwarp();
+      }
+      if (nt > 0) {
         tc_fence_before();
         mbar_arrive(bar(kOEmpty));
-      } else {
-#pragma unroll
-        for (int j = 0; j < D; ++j) o[j] = 0u;
       }
-      if constexpr (Q4) {
-        // columns are in the codes' order; p mid_v is added
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          uint32_t t[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            t[j] = __float_as_uint(__uint_as_float(o[8 * c + code_place(j)]) + mid_sum);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o[8 * c + j] = t[j];
-        }
-      }
-      if (mine) {
-        if (it.t0 == 0 && it.t1 == it.sp.n) {
-          const bool none = l == 0.f || pos < 0;
-          const float inv = none ? 0.f : 1.f / l;
-          uint4* const dst = reinterpret_cast<uint4*>(
-              p.o + ((static_cast<int64_t>(it.b) * p.M + mq) * p.H + h) * D);
-#pragma unroll
-          for (int q = 0; q < D / 8; ++q) {
-            float f[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = none ? 0.f : __uint_as_float(o[8 * q + j]) * inv;
-            dst[q] = pack8<BF16>(f);
-          }
-          if (p.lse != nullptr)
-            p.lse[(static_cast<int64_t>(it.b) * p.H + h) * p.M + mq] = none ? -INFINITY
-                                                                            : pa_lse(ref, l);
-        } else {
-          const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (it.t0 == 0 ? 1 : 0);
-          const int64_t prow = slot * rows_tile + row;
-          uint4* const dst = reinterpret_cast<uint4*>(p.piece + prow * D);
-#pragma unroll
-          for (int q = 0; q < D / 4; ++q)
-            dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-          reinterpret_cast<float2*>(p.piece + 2 * static_cast<int64_t>(p.ctas) * rows_tile * D)[prow] =
-              make_float2(ref, l);
-        }
+      if (mine && group == 0) {
+        if (!whole)
+          reinterpret_cast<float2*>(p.piece + 2 * static_cast<int64_t>(p.ctas) * rows_tile *
+                                                  D)[slot * rows_tile + row] = make_float2(top, l);
+        else if (p.lse != nullptr)
+          p.lse[lse_at] = none ? -INFINITY : pa_lse(top, l);
       }
       gt += nt;
       if (nt > 0) ++n;
@@ -710,60 +764,68 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
       auto wait_all = [&](int b, uint32_t parity) {
         return __all_sync(kFull, wait_phase(bar(b), parity, kWaitLimitNs));
       };
+      // Register j of a lane is of row kRowsAt j + lane / kLanes of the warp's 32: the
+      // first half of them of keys 0 to 15, in one page, the others of 16 to 31.
+      const int row0 = lane / kLanes, in_page = (1 << p.c.shift) - 1;
+      uint32_t place[4];  // of a word's chunks in the operands
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int ch = 4 * (lane % kLanes) + q;
+        place[q] = ((key_in & ~31) + row0) * 128 + (ch >> 3) * C::kAtomBytes +
+                   (((ch & 7) ^ (row0 & 7)) << 4);
+      }
       for (; it.more && !failed; it.next(p, count, rows_tile)) {
         const int nt = it.t1 - it.t0;
         if (nt <= 0) continue;
         const PaSight see{it.sp.lo_pos, it.sp.hi_pos, p.left, p.sinks};
+        const int32_t* const table = p.c.table + static_cast<int64_t>(it.b) * p.c.cols;
+        const int64_t in_row = row0 * p.c.kt + it.sh.group * p.c.kh + 16 * (lane % kLanes);
         // a step's page is looked up a step before its codes, and those a step
-        // before they are stored
-        int page_next = -1;
+        // before they are stored (and nothing is done with it until then: a warp
+        // waits where it first uses what it has loaded)
+        int id_next = -1;
         bool there_next = false;
         uint4 k_next[W], v_next[W];
         uint32_t ks_next = 0, vs_next = 0;
         auto look = [&](int t) {
-          page_next = -1;
-          if (t >= it.t1) return;
-          const int key = it.sp.key(t) + key_in;
-          if (!see.nobody(key)) page_next = page_of(p.c, it.b, key);
+          id_next = -1;
+          const int col = (it.sp.key(t) + key_in) >> p.c.shift;
+          if (t < it.t1 && col < p.c.cols) id_next = __ldg(table + col);
         };
-        // Codes come four lanes to a row (D = 64: two), 16 bytes each: register j
-        // is of row kRowsAt j + lane / kLanes of the warp's 32.
         auto fetch = [&](int t) {
-          const int page = page_next;
-          look(t + 1);
-          there_next = page >= 0;
-          const int first = it.sp.key(t) + (key_in & ~31), in_page = (1 << p.c.shift) - 1;
+          const int page = id_next < p.c.pages ? id_next : -1;
+          const int key = it.sp.key(t) + key_in, off = key & in_page;
+          there_next = page >= 0 && !see.nobody(key);
+          // (rows that nobody sees come along: the codes are finite, whatever they are)
+          const int64_t at = page * p.c.kp + (off & ~15) * p.c.kt;
 #pragma unroll
-          for (int j = 0; j < W; ++j) {
-            const int row = kRowsAt * j + lane / kLanes;
-            const int pg = __shfl_sync(kFull, page, row);
-            // (a key that is not there: any finite row, as p' is 0)
-            k_next[j] = v_next[j] = make_uint4(0, 0, 0, 0);
-            if (pg >= 0) {
-              const int64_t o = pg * p.c.kp + ((first + row) & in_page) * p.c.kt +
-                                it.sh.group * p.c.kh + 16 * (lane % kLanes);
-              k_next[j] = __ldg(reinterpret_cast<const uint4*>(p.c.k + o));
-              v_next[j] = __ldg(reinterpret_cast<const uint4*>(p.c.v + o));
+          for (int half = 0; half < 2; ++half) {
+            const int pg = __shfl_sync(kFull, page, 16 * half);
+            const int64_t o = __shfl_sync(kFull, at, 16 * half) + in_row;
+#pragma unroll
+            for (int j = 0; j < W / 2; ++j) {
+              uint4 &kw = k_next[half * (W / 2) + j], &vw = v_next[half * (W / 2) + j];
+              kw = vw = make_uint4(0, 0, 0, 0);
+              if (pg >= 0) {
+                kw = __ldg(reinterpret_cast<const uint4*>(p.c.k + o + j * kRowsAt * p.c.kt));
+                vw = __ldg(reinterpret_cast<const uint4*>(p.c.v + o + j * kRowsAt * p.c.kt));
+              }
             }
           }
-          if (page < 0) return;
-          const int64_t so = ((page * static_cast<int64_t>(p.G) + it.sh.group) << p.c.shift) +
-                             ((first + lane) & in_page);
-          ks_next = __ldg(p.c.ks + so);
-          vs_next = __ldg(p.c.vs + so);
+          if (there_next) {
+            const int64_t so = ((page * static_cast<int64_t>(p.G) + it.sh.group) << p.c.shift) + off;
+            ks_next = __ldg(p.c.ks + so);
+            vs_next = __ldg(p.c.vs + so);
+          }
+          look(t + 1);
         };
         auto store = [&](uint8_t* tile, const uint4 (&w)[W]) {
 #pragma unroll
           for (int j = 0; j < W; ++j) {
-            const int row = (key_in & ~31) + kRowsAt * j + lane / kLanes;
-            uint8_t* const dst = tile + row * 128;
             const uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int ch = 4 * (lane % kLanes) + q;
-              *reinterpret_cast<uint4*>(dst + (ch >> 3) * C::kAtomBytes +
-                                        (((ch & 7) ^ (row & 7)) << 4)) = codes_chunk(u[q]);
-            }
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<uint4*>(tile + place[q] + j * kRowsAt * 128) = codes_chunk(u[q]);
           }
           fence_proxy_async_smem();
         };
@@ -813,21 +875,22 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
     }
   };
   if constexpr (Q4) {
-    // 384 threads of 168 registers; 80 + 240 + 184 = 3 x 168
+    // 512 threads of 128 registers; 88 + 2 x 144 + 136 = 4 x 128
     if (warp < C::kSoftWarp) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n" ::: "memory");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n" ::: "memory");
       if (warp == 1) issuer();
     } else if (warp < C::kLoadWarp) {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 240;\n" ::: "memory");
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 144;\n" ::: "memory");
       softmax();
     } else {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 184;\n" ::: "memory");
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 136;\n" ::: "memory");
       loader();
     }
   } else {
-    if (warp == 0) producer();
+    if (warp == 0) producer(std::false_type{});
     else if (warp == 1) issuer();
-    else softmax();
+    else if (warp == 2) producer(std::true_type{});
+    else if (warp >= C::kSoftWarp) softmax();
   }
 
   if (failed && lane == 0) report_timeout();

@@ -96,6 +96,15 @@ __device__ __forceinline__ void tc_mma_ts_if(uint32_t on, uint32_t d_tmem, uint3
       : "memory");
 }
 
+__device__ __forceinline__ void tc_mma_if(uint32_t on, uint32_t d_tmem, uint64_t a, uint64_t b,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
+
 __device__ __forceinline__ void tc_commit_if(uint32_t on, uint32_t bar) {
   asm volatile(
       "{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
