@@ -697,10 +697,15 @@ int nsa_kv_read(const nsa_kv_cache* cache, const int32_t* page_table, const int3
 
 /*
  * nsa_paged_attn_workspace_bytes -- device workspace of nsa_paged_attn for a page
- * table of `tokens` = table_cols * page_size tokens: 0 where a query sees at most
- * 512 keys, or M H/G rows make more than 512 row tiles (of 8 rows, or 16 where
- * there are more than 8) in the batch; else up to 20 MB, whatever the lengths.
- * Negative nsa_status for invalid sizes. Pure host arithmetic.
+ * table of `tokens` = table_cols * page_size tokens, enough for 16 and 4 bits. 0
+ * where no row tile of a KV head is cut along its keys: a query sees few (512, or
+ * 2048 where there is a row tile for every SM), or the batch has more than 512 row
+ * tiles; else up to 20 MB, whatever the lengths. Negative nsa_status for invalid
+ * sizes. Pure host arithmetic.
+ *
+ * A row tile is 8 of the M H/G rows of a KV head where there are no more, else 16,
+ * or, with 17 rows (4 bits: 33) or more and H/G up to 128, as many whole queries as
+ * make up to 128 rows.
  */
 int64_t nsa_paged_attn_workspace_bytes(int64_t B, int64_t M, int64_t H, int64_t G, int64_t D,
                                        int64_t tokens, int64_t window_left, int64_t sinks);
@@ -726,15 +731,16 @@ int64_t nsa_paged_attn_workspace_bytes(int64_t B, int64_t M, int64_t H, int64_t 
  *                  calls that may overlap need one each
  *
  * H is a multiple of G. p is rounded to 16 bits before the product with V (to
- * dtype, or fp16 over a 4-bit cache), sums are fp32, O is rounded once. LSE is
+ * dtype, or fp16 over a 4-bit cache); in row tiles of 8 and 16 what that leaves is
+ * multiplied too (over a 4-bit cache where O is fp16). Sums are fp32, O is rounded once. LSE is
  * the natural log of sum(exp(scale q.k)) over the visible keys. A query that
  * sees no key, or is padding, gets O = 0, LSE = -inf.
  * Keys and values that no query of the sequence sees may hold anything. A V row
- * (or the scales of a 4-bit row) that some query of 8, or 16, rows sees is
- * multiplied by 0 for those that do not, and has to be finite.
+ * (or the scales of a 4-bit row) that some query of a row tile sees is multiplied
+ * by 0 for those that do not, and has to be finite.
  *
  * Every sum has an order that the sizes and positions alone decide: equal calls
- * give equal bits. Two kernels on `stream` (one without a workspace), no
+ * give equal bits. Two kernels on `stream` (one where no workspace is needed), no
  * allocation. Errors before launch: as nsa_swa_fwd, the cache's and the
  * workspace's. A timed-out device wait is reported by nsa_sync_status.
  */

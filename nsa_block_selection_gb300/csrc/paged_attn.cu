@@ -8,7 +8,7 @@
 //   LSE = ln 2 (r + log2 l),
 // r a reference that follows the largest x (by steps of 8: p <= 2^8). One pass
 // over the keys; x, p, sums and O are fp32, p is rounded to 16 bits for the
-// product with V.
+// product with V, and what the rounding leaves is multiplied too.
 //
 // Rows. A row tile is 8 or 16 of the M H/G (query, head) rows of a KV head, the
 // N of the products: S^T (16 keys x rows) = K Q^T and O^T (D x rows) += V^T P^T
@@ -34,10 +34,19 @@
 // of two into fp16's range. For V, p' = 2^(x + log2 step - r) is the product's
 // operand (r follows x + log2 step) and p = p' / step; with
 // v = (low + 8 step) + step (c - 8) it sums p' (c - 8), and p (low + 8 step) is
-// summed beside it. A slot of the
-// CTA's one ring holds 128 rows, 32 for each warp, and the warps issue the copies
-// in turn: neighbouring heads of a token lie in one 128-byte line, so a CTA takes
-// two or four of them at once.
+// summed beside it. A slot of the CTA's one ring holds 128 rows, 32 for each warp,
+// and the warps issue the copies in turn: neighbouring heads of a token lie in one
+// 128-byte line, so a CTA takes two or four of them at once.
+//
+// Many rows (drafts, pieces of a prompt) go to paged_attn_tc_kernel.
+//
+// What bounds it. 16 bits: the cache's bytes, and what surrounds them: a token of 64 +
+// 8 heads of 128 over 65,536 keys takes 44 to 48 us (5.6 to 6.1 TB/s of 268 MB), of
+// which some 6 us are the first positions, pages and copies and the join; 48 windowed
+// sequences of 32 + 4 heads (1028 keys each, 102 MB) 22 us in one kernel. 4 bits: the
+// warps' instructions, some 290 for 16 keys of a KV head: 64 ragged sequences of up to
+// 16,384 tokens of 64 + 8 heads (580 MB) 142 us, 4.1 TB/s, a warp issues in 52 % of
+// the clocks at 12 warps an SM.
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -143,6 +152,17 @@ struct PaRows {
   }
 };
 
+// What the 16-bit words of `two` leave of a and b, in the same type.
+template <bool BF16>
+__device__ __forceinline__ uint32_t pa_rest(uint32_t two, float a, float b) {
+  float2 f;
+  if constexpr (BF16)
+    f = make_float2(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u));
+  else
+    f = __half22float2(*reinterpret_cast<const __half2*>(&two));
+  return pack2_t<BF16>(a - f.x, b - f.y);
+}
+
 // ---- 16 bits -----------------------------------------------------------
 
 // One tile of the ring: S^T, the softmax step and O^T. EDGE: some query does not
@@ -189,7 +209,9 @@ __device__ __forceinline__ void pa_tile16(PaRows<D, NT>& a, const uint32_t (&qf)
       if (EDGE && see.hidden(n0 + r + 8 * (i >> 1), a.pos[nt][i & 1])) x[0][nt][i] = -INFINITY;
     }
   a.follow(x);
-  uint32_t pf[NT][2];  // P^T as B operand
+  // P^T as B operand, and what its rounding leaves: the copies bound the call, so a
+  // second product costs nothing, and O is off by its own rounding alone
+  uint32_t pf[NT][2], pl[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     float e[4];
@@ -198,8 +220,12 @@ __device__ __forceinline__ void pa_tile16(PaRows<D, NT>& a, const uint32_t (&qf)
       e[i] = ex2(x[0][nt][i] + a.neg[nt][i & 1]);
       a.l[nt][i & 1] += e[i];
     }
-    pf[nt][0] = movmatrix_t(pack2_t<BF16>(e[0], e[1]));
-    pf[nt][1] = movmatrix_t(pack2_t<BF16>(e[2], e[3]));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t two = pack2_t<BF16>(e[2 * i], e[2 * i + 1]);
+      pf[nt][i] = movmatrix_t(two);
+      pl[nt][i] = movmatrix_t(pa_rest<BF16>(two, e[2 * i], e[2 * i + 1]));
+    }
   }
   const int vrow = (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
@@ -209,8 +235,10 @@ __device__ __forceinline__ void pa_tile16(PaRows<D, NT>& a, const uint32_t (&qf)
     ldsm_x4_t(vt + (ch >> 3) * kBoxBytes + vrow * 128 + (((ch & 7) ^ (vrow & 7)) << 4), a0, a1, a2,
               a3);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
       mma_16816_t<BF16>(a.acc[nt][i], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+      mma_16816_t<BF16>(a.acc[nt][i], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+    }
   }
 }
 
@@ -310,7 +338,10 @@ __device__ __forceinline__ void pa_scores4(const PaRows<D, NT>& a, const uint8_t
 // of O instead of 0.17 with lower and upper codes in one sum.)
 constexpr uint32_t kLess8 = 0x80088008u, kLess128 = 0x80808080u;
 
-template <int D, int NT, bool EDGE>
+// REST: also the product with what the rounding of p' leaves, r (c - 8) = r c - 8 r, so
+// that an fp16 O is off by little more than its own rounding (without: 1.4 times that;
+// a bf16 one is anyway).
+template <int D, int NT, bool EDGE, bool REST>
 __device__ __forceinline__ void pa_values4(PaRows<D, NT>& a, const uint8_t* vt, const PaLanes& at,
                                            int n0, const PaSight& see, const float (&x)[NT][4],
                                            const float (&mid)[2], const float (&rstep)[2]) {
@@ -327,12 +358,22 @@ __device__ __forceinline__ void pa_values4(PaRows<D, NT>& a, const uint8_t* vt, 
     }
   }
   uint32_t pf[NT][2];
+  [[maybe_unused]] uint32_t pl[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     float e[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) e[i] = ex2(x[nt][i] + a.neg[nt][i & 1]);
     const uint32_t p0 = pack_half2(e[0], e[1]), p1 = pack_half2(e[2], e[3]);
+    if constexpr (REST) {
+      const uint32_t r0 = pa_rest<false>(p0, e[0], e[1]), r1 = pa_rest<false>(p1, e[2], e[3]);
+      const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&r0));
+      const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&r1));
+      a.base_v[nt][0] = fmaf(f0.x + f1.x, -8.f, a.base_v[nt][0]);
+      a.base_v[nt][1] = fmaf(f0.y + f1.y, -8.f, a.base_v[nt][1]);
+      pl[nt][0] = movmatrix_t(r0);
+      pl[nt][1] = movmatrix_t(r1);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float md = mid[i >> 1], pr = e[i] * rstep[i >> 1];
@@ -361,13 +402,19 @@ __device__ __forceinline__ void pa_values4(PaRows<D, NT>& a, const uint8_t* vt, 
         mma_16816(hi, kLess8, kLess128, kLess8, kLess128, pf[nt][0], pf[nt][1]);
         mma_16816(hi, u8 & 0x000f000fu, u8 & 0x00f000f0u, v8 & 0x000f000fu, v8 & 0x00f000f0u,
                   pf[nt][0], pf[nt][1]);
+        if constexpr (REST) {
+          mma_16816(lo, u & 0x000f000fu, u & 0x00f000f0u, v & 0x000f000fu, v & 0x00f000f0u,
+                    pl[nt][0], pl[nt][1]);
+          mma_16816(hi, u8 & 0x000f000fu, u8 & 0x00f000f0u, v8 & 0x000f000fu, v8 & 0x00f000f0u,
+                    pl[nt][0], pl[nt][1]);
+        }
       }
     }
   }
 }
 
 // A warp's 32 keys of a slot: two tiles, at once where the registers hold both.
-template <int D, int NT, bool EDGE>
+template <int D, int NT, bool EDGE, bool REST>
 __device__ __forceinline__ void pa_step4(PaRows<D, NT>& a, const uint8_t* slot,
                                          const uint8_t* scales, const PaLanes& at, int row_bytes,
                                          const int (&n0)[2], const uint32_t (&qf)[NT][D / 16][2],
@@ -385,7 +432,7 @@ __device__ __forceinline__ void pa_step4(PaRows<D, NT>& a, const uint8_t* slot,
     a.follow(x);
 #pragma unroll
     for (int u = 0; u < kTogether; ++u)
-      pa_values4<D, NT, EDGE>(
+      pa_values4<D, NT, EDGE, REST>(
           a, slot + kPaSlotRows * (D / 2) + (u0 + u) * kPaTile * row_bytes, at, n0[u0 + u], see,
           x[u], mid[u], rstep[u]);
   }
@@ -626,9 +673,9 @@ __global__ void __launch_bounds__(kPaThreads, PaCfg<D, Q4, NT>::kPerSm)
         const uint8_t* const slot = gbase + stage * C::kSlot;
         const uint8_t* const scales = slot + 2 * C::kKv;
         if (k0 & k1 & 1)
-          pa_step4<D, NT, false>(a, slot, scales, lanes, row_bytes, n0, qf, ka, kb, see);
+          pa_step4<D, NT, false, !BF16>(a, slot, scales, lanes, row_bytes, n0, qf, ka, kb, see);
         else if (!see.nothing(n0[0]) || !see.nothing(n0[1]))
-          pa_step4<D, NT, true>(a, slot, scales, lanes, row_bytes, n0, qf, ka, kb, see);
+          pa_step4<D, NT, true, !BF16>(a, slot, scales, lanes, row_bytes, n0, qf, ka, kb, see);
         __syncwarp();  // the slot has been read
         if (lane == 0) mbar_arrive(bars + 8 * (C::kStages + stage));
         if (++stage == C::kStages) {

@@ -767,10 +767,13 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
       // Register j of a lane is of row kRowsAt j + lane / kLanes of the warp's 32: the
       // first half of them of keys 0 to 15, in one page, the others of 16 to 31.
       const int row0 = lane / kLanes, in_page = (1 << p.c.shift) - 1;
-      uint32_t place[4];  // of a word's chunks in the operands
+      // (D = 128: lanes of the second atom take their words in another order, or they
+      // would meet the first atom's banks)
+      const bool turned = D == 128 && (lane & 2) != 0;
+      uint32_t place[4];  // of a word's chunk in the operands
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int ch = 4 * (lane % kLanes) + q;
+        const int ch = 4 * (lane % kLanes) + (turned ? q ^ 2 : q);
         place[q] = ((key_in & ~31) + row0) * 128 + (ch >> 3) * C::kAtomBytes +
                    (((ch & 7) ^ (row0 & 7)) << 4);
       }
@@ -822,7 +825,8 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
         auto store = [&](uint8_t* tile, const uint4 (&w)[W]) {
 #pragma unroll
           for (int j = 0; j < W; ++j) {
-            const uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+            const uint32_t u[4] = {turned ? w[j].z : w[j].x, turned ? w[j].w : w[j].y,
+                                   turned ? w[j].x : w[j].z, turned ? w[j].y : w[j].w};
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               *reinterpret_cast<uint4*>(tile + place[q] + j * kRowsAt * 128) = codes_chunk(u[q]);
