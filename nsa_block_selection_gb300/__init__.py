@@ -16,7 +16,12 @@ Public API (GPU only; the CUDA library must be built):
 * :func:`qk_norm_rope` and :func:`qk_norm_rope_bwd` -- RMS norm of every
   query and key head and the position rotation in one pass, before any of
   the attention calls, and its gradients (:func:`rope_tables` builds the
-  angle tables).
+  angle tables);
+* :class:`KvCache` (:func:`kv_cache` makes an empty one): a paged cache of keys
+  and values, 16-bit or 4-bit; :func:`kv_append` -- norm and rotation of new
+  tokens, with K and V stored in it; :func:`paged_attn` -- their attention over
+  the pages, with a window and first tokens; :func:`kv_read` -- rows of it as K
+  and V.
 
 The C ABI is declared in ``include/nsa_sel_attn.h``; ``inputs`` draws the
 seeded synthetic workloads.

@@ -16,7 +16,7 @@
 // by D / 16 lanes, 16 entries each (append), which hold both entries of every
 // pair, so that the turn needs no exchange; or by D / 8 lanes, 16 bytes of the
 // result each (read). 16,384 tokens of 64 + 8 heads of 128 are appended in 111 us
-// (671 MB, 6.1 TB/s), 65,536 tokens of 8 heads read from 4 bits in 57 us (340 MB,
+// (680 MB, 6.1 TB/s), 65,536 tokens of 8 heads read from 4 bits in 57 us (340 MB,
 // 6.0 TB/s); one token is 2.3 us on the device.
 
 #include <cuda_bf16.h>

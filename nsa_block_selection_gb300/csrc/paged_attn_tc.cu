@@ -24,12 +24,13 @@
 // q' = 2^e q in fp16, written by the softmax warps, ka and kb the row's factors.
 //
 // What bounds it: a step takes some 1500 clocks (16 bits; the products 800 of the
-// tensor cores' time, a group's softmax 2600 for every other step) and 3300 (4 bits:
-// the loaders, some 600 instructions a warp and step); an item's own cost is some
-// 6000. Prompts of 32 + 4 heads of 128: 16,384 tokens 1750 us (1250 TFLOP/s), 4096
-// tokens 197 us (4 bits 322); 3 x 200 tokens of 64 + 8 heads after 8800 others 178 us
-// (308). One group with two S and a P of its own, and one producer warp: 2160, 232
-// (371), 266 (384).
+// tensor cores' time, a group's softmax 2600 for every other step) and 3000 (4 bits:
+// the shared-memory pipe, by the operands' rows that the loaders write and the five
+// numbers of a key that every row reads; loaders of a warpgroup each for K and V gained
+// nothing); an item's own cost is some 6000. Prompts of 32 + 4 heads of 128: 16,384
+// tokens 1740 us (1260 TFLOP/s), 4096 tokens 197 us (4 bits 310); 3 x 200 tokens of 64
+// + 8 heads after 8800 others 176 us (296). One group with two S and a P of its own,
+// and one producer warp: 2160, 232 (371), 266 (384).
 //
 // Every mbarrier wait is bounded (1 s); a role that gives up sets the status word
 // and leaves its loop, so every role reaches the teardown, which frees the tensor
