@@ -1067,14 +1067,15 @@ def paged_attn(q, cache: KvCache, page_table, positions, window=(-1, 0), sinks: 
         raise TypeError(f"q must be of the cache's dtype {cache.k.dtype}, got {dt}")
     B, M, H, D = qs
     dev = q.get_device()
-    if dev < 0 or not (q.is_contiguous() or q.stride(3) == 1):
+    dense = q.is_contiguous()
+    if dev < 0 or not (dense or q.stride(3) == 1):
         raise ValueError("q must be a CUDA tensor with a contiguous last dimension")
     cols, pstride = _check_places(cache, page_table, positions, B, M, dev, need=True)
     left, right = window
     if right != 0:
         raise ValueError("window must be (left, 0): the cache ends at the queries")
-    if out is None:
-        out = _torch.empty(qs, dtype=dt, device=q.device)
+    if out is None:  # (empty_like takes 1.4 us less)
+        out = _torch.empty_like(q) if dense else _torch.empty(qs, dtype=dt, device=q.device)
     elif out.dtype is not dt or out.shape != qs or not out.is_contiguous() or \
             out.get_device() != dev:
         raise ValueError(f"out must be a contiguous {dt} [B, M, H, D] tensor on q's device")
@@ -1085,12 +1086,14 @@ def paged_attn(q, cache: KvCache, page_table, positions, window=(-1, 0), sinks: 
             lse.get_device() != dev:
         raise ValueError("lse must be a contiguous fp32 [B, H, M] tensor on q's device")
     strides = None
-    if not q.is_contiguous():
+    if not dense:
         b, m, h, _ = q.stride()
         strides = array("q", (b if B > 1 else 0, m if M > 1 else 0, h if H > 1 else 0))
     if workspace is None:
-        nbytes = lib.nsa_paged_attn_workspace_bytes(B, M, H, cache.kv_heads, D,
-                                                    cols * cache.page_size, left, sinks)
+        tokens, nbytes = cols * cache.page_size, 0
+        if tokens > 512:  # (0 up to there)
+            nbytes = lib.nsa_paged_attn_workspace_bytes(B, M, H, cache.kv_heads, D, tokens, left,
+                                                        sinks)
         if nbytes < 0:
             raise NsaError(nbytes, "nsa_paged_attn_workspace_bytes")
         if nbytes:

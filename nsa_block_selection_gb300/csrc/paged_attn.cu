@@ -540,6 +540,7 @@ __global__ void __launch_bounds__(kPaThreads, PaCfg<D, Q4, NT>::kPerSm)
   asm volatile("griddepcontrol.launch_dependents;\n");  // the join waits for this grid's end
   if (p.cut) {
     sh = pa_share<kPaThreads>(p, kRowsTile, count, reinterpret_cast<int*>(stat));
+    pa_zeros<D>(p, kRowsTile, count);
   } else {
     sh.item = blockIdx.x / p.groups;
     sh.group = blockIdx.x - sh.item * p.groups;
@@ -848,11 +849,13 @@ __global__ void __launch_bounds__(kPaThreads, PaCfg<D, Q4, NT>::kPerSm)
   }
 }
 
-// Items that shares have cut: their pieces joined in order; items without a
-// step: zeros. A CTA takes `rows_cta` rows of an item, D / 4 threads a row; the
-// pieces are dealt to the sets of threads that are left. A thread merges its
-// pieces as it loads them, statistics and values at once, four in flight: the
-// kernel is a chain of latencies (the counts, the pieces, the sets).
+// Items that shares have cut: their pieces joined in order. A CTA takes `rows_cta`
+// rows of an item (blockIdx.x: the item, or, where there are more items than shares,
+// the share that it begins in and does not end in: a prompt of 4096 tokens has 1024
+// items, and their CTAs took 45 us), D / 4 threads a row; the pieces are dealt to the
+// sets of threads that are left. A thread merges its pieces as it loads them,
+// statistics and values at once, four in flight: the kernel is a chain of latencies
+// (the counts, the pieces, the sets).
 constexpr int kJoinThreads = 256;
 
 struct PaPiece {
@@ -871,11 +874,27 @@ struct PaPiece {
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kJoinThreads)
-    paged_attn_join_kernel(const PagedProblem p, int rows_tile, int rows_cta) {
+    paged_attn_join_kernel(const PagedProblem p, int rows_tile, int rows_cta, bool by_share) {
   constexpr int kLanes = D / 4;  // threads of a row
   __shared__ float4 part[kJoinThreads];
   __shared__ float2 part_stat[kJoinThreads];
-  const int item = blockIdx.x / p.groups, group = blockIdx.x - item * p.groups;
+  __shared__ int holds;
+  int item = blockIdx.x / p.groups, group = blockIdx.x - item * p.groups;
+  // (launched while the kernel before is at its end; its results are there from here on)
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  const int64_t per = p.count[p.items + 1];
+  if (by_share) {  // the item that holds the first step of the next share
+    const int64_t next = (static_cast<int64_t>(blockIdx.x) + 1) * per;
+    if (threadIdx.x == 0) holds = -1;
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.items; i += kJoinThreads)
+      if (p.count[i] * p.groups <= next && next < p.count[i + 1] * p.groups) holds = i;
+    __syncthreads();
+    item = holds;
+    if (item < 0) return;  // (the shares after this one are empty)
+    const int64_t c0 = p.count[item];
+    group = static_cast<int>((next - c0 * p.groups) / (p.count[item + 1] - c0));
+  }
   const int piece_rows = p.heads_item * rows_tile;
   const int b = item / p.tiles, rt = item - b * p.tiles;
   const int sets = kJoinThreads / (kLanes * rows_cta);
@@ -886,15 +905,13 @@ __global__ void __launch_bounds__(kJoinThreads)
   const bool in = prow < piece_rows && rw < p.rows;
   const int mq = rw / p.hpg, h = (group * p.heads_item + hd) * p.hpg + rw - mq * p.hpg;
   const bool padding = in && __ldg(p.pos + b * p.pos_b + mq) < 0;
-  // (launched while the kernel before is at its end; its results are there from here on)
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  const int64_t c0 = p.count[item], c1 = p.count[item + 1], per = p.count[p.items + 1];
+  const int64_t c0 = p.count[item], c1 = p.count[item + 1];
   const int64_t n = c1 - c0 - p.item_cost;  // (below 0: no step)
   const int64_t at = c0 * p.groups + group * (c1 - c0) + p.item_cost;
   const int first = static_cast<int>(at / per);
   const int last = n > 0 ? static_cast<int>((at + n - 1) / per) : first;
-  if (n > 0 && first == last) return;  // whole in one share
-  const int pieces = n > 0 ? last - first + 1 : 0;
+  if (first == last || (by_share && first != static_cast<int>(blockIdx.x))) return;
+  const int pieces = last - first + 1;
   const float* const stats = p.piece + 2 * static_cast<int64_t>(p.ctas) * piece_rows * D;
   const int at_row = p.many ? ((d >> 1) * piece_rows + prow) * 8 + (d & 1) * 4 : prow * D + 4 * d;
   PaPiece a;
@@ -1018,11 +1035,13 @@ int launch_join(const PagedProblem& p, int rows_tile, cudaStream_t st) {
   // have their many pieces added by many threads
   const int rows = p.heads_item * rows_tile;
   int rows_cta = 1024 / D;  // a thread for every four entries
-  while (rows_cta > 1 && static_cast<int64_t>(p.items) * p.groups * (rows / rows_cta) < kPaSms)
-    rows_cta >>= 1;
+  const int64_t all = static_cast<int64_t>(p.items) * p.groups;
+  const bool by_share = all >= p.ctas;
+  while (rows_cta > 1 && all * (rows / rows_cta) < kPaSms) rows_cta >>= 1;
   if (rows_cta > 8) rows_cta = 8;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.items * p.groups), (rows + rows_cta - 1) / rows_cta);
+  cfg.gridDim = dim3(static_cast<unsigned>(by_share ? p.ctas - 1 : all),
+                     (rows + rows_cta - 1) / rows_cta);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute at{};
@@ -1031,7 +1050,7 @@ int launch_join(const PagedProblem& p, int rows_tile, cudaStream_t st) {
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<D, BF16>, PagedProblem(p), rows_tile,
-                         rows_cta) != cudaSuccess)
+                         rows_cta, by_share) != cudaSuccess)
     return NSA_ERR_LAUNCH;
   return NSA_OK;
 }

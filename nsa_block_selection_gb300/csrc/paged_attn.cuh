@@ -188,6 +188,25 @@ __device__ __forceinline__ PaShare pa_share(const PagedProblem& p, int rows_tile
   return s;
 }
 
+// Items without a step, dealt to the CTAs: zeros. `count`: as of pa_share.
+template <int D>
+__device__ __forceinline__ void pa_zeros(const PagedProblem& p, int rows_tile, const int* count) {
+  for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
+    if (count[item + 1] != count[item]) continue;
+    const int b = item / p.tiles, r0 = (item - b * p.tiles) * rows_tile;
+    const int rows = min(rows_tile, p.rows - r0);
+    const int64_t all = static_cast<int64_t>(rows) * p.G * (D / 8);
+    for (int64_t i = threadIdx.x; i < all; i += blockDim.x) {
+      const int x = static_cast<int>(i / (D / 8)), g = x / rows, rw = r0 + x - g * rows;
+      const int mq = rw / p.hpg, h = g * p.hpg + rw - mq * p.hpg;
+      reinterpret_cast<uint4*>(p.o + ((static_cast<int64_t>(b) * p.M + mq) * p.H + h) *
+                                         D)[i % (D / 8)] = make_uint4(0, 0, 0, 0);
+      if (i % (D / 8) == 0 && p.lse != nullptr)
+        p.lse[(static_cast<int64_t>(b) * p.H + h) * p.M + mq] = -INFINITY;
+    }
+  }
+}
+
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));

@@ -254,7 +254,10 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
   }
   asm volatile("griddepcontrol.launch_dependents;\n");  // the join waits for this grid's end
   PaShare share{0, 0, 0, 0, 0};
-  if (p.cut) share = pa_share<C::kThreads>(p, rows_tile, count, sums);
+  if (p.cut) {
+    share = pa_share<C::kThreads>(p, rows_tile, count, sums);
+    pa_zeros<D>(p, rows_tile, count);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
