@@ -27,8 +27,8 @@ constexpr int kPaItemCost = 320;
 // Keys of an item that is never cut, and where there is an item for every SM.
 constexpr int kPaWhole = 512, kPaWholeMany = 2048;
 // The same of paged_attn_tc_kernel, whose steps are faster. (512: a prompt of 4096
-// tokens 212 us instead of 197, 2 x 65 tokens after 8900 others 30 instead of 31; 1024:
-// 197 and 33.)
+// tokens 179 us instead of 167, 2 x 65 tokens after 8900 others 30 instead of 32; 1024:
+// 170 and 33.)
 constexpr int kTcItemCost = 768;
 constexpr int kPaLeast = 448;     // keys of a share at least, that cost among them
 constexpr float kPaSlack = 8.0f;

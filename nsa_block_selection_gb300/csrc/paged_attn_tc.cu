@@ -28,7 +28,7 @@
 // the shared-memory pipe, by the operands' rows that the loaders write and the five
 // numbers of a key that every row reads; loaders of a warpgroup each for K and V gained
 // nothing); an item's own cost is some 6000. Prompts of 32 + 4 heads of 128: 16,384
-// tokens 1740 us (1260 TFLOP/s), 4096 tokens 197 us (4 bits 310); 3 x 200 tokens of 64
+// tokens 1740 us (1260 TFLOP/s), 4096 tokens 167 us (4 bits 281); 3 x 200 tokens of 64
 // + 8 heads after 8800 others 176 us (296). One group with two S and a P of its own,
 // and one producer warp: 2160, 232 (371), 266 (384).
 //

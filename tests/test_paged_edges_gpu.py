@@ -180,3 +180,37 @@ def test_append_writes_no_other_row(bits):
             want = torch.zeros_like(diff)
             want[table[0, 3], 15] = want[table[2, 1], 1] = True
             assert torch.equal(diff, want)
+
+
+@pytest.mark.parametrize("M,H,G,D,dtype,bits,B", [
+    (20, 16, 8, 64, "f16", 16, 24), (20, 32, 8, 128, "bf16", 4, 24), (1, 16, 8, 128, "bf16", 16, 48),
+    (3, 24, 8, 64, "f16", 16, 48), (1, 16, 16, 128, "f16", 4, 70), (2, 32, 32, 64, "bf16", 4, 90)])
+def test_more_items_than_shares_and_empty_ones(M, H, G, D, dtype, bits, B):
+    """Cut items among many: padding sequences between them, sequences that share pages."""
+    import torch
+
+    from _paged import dt
+
+    g = torch.Generator(device="cuda").manual_seed(99 + B)
+    rng = np.random.default_rng(99 + B)
+    cache = make_cache(g, 48, 64, G, D, dtype, bits)
+    table = torch.from_numpy(rng.integers(0, 48, (B, 40)).astype(np.int32)).cuda()
+    lens = rng.integers(M, 2560, B)
+    pos = np.stack([np.arange(n - M, n) for n in lens]).astype(np.int32)
+    pos[::5] = -1
+    pos[3, M // 2:] = -1
+    pos[-1] = -7
+    q = torch.randn((B, M, H, D), generator=g, device="cuda").to(dt(dtype))
+    pos = torch.from_numpy(pos).cuda()
+    out, lse = _attn(q, cache, table, pos)
+    some = [0, 1, 3, 4, B // 2, B - 3, B - 2, B - 1]
+    check_attn(q[some], cache, table[some], pos[some], -1, 0, None, out[some], lse[some], dtype)
+    empty = (pos < 0)
+    assert (out[empty] == 0).all() and (lse.transpose(1, 2)[empty] == -float("inf")).all()
+    # each sequence by itself, in other shares: the roundings of p are independent, so in
+    # norm each result is off by the two roundings (p's and O's) of at most u each; twice
+    for b in range(B):
+        o, _ = _attn(q[b:b + 1], cache, table[b:b + 1], pos[b:b + 1])
+        u = torch.finfo(o.dtype).eps / 2
+        far = (o.double() - out[b:b + 1].double()).norm()
+        assert far <= 8 * u * o.double().norm() + 1e-30, (b, far)
