@@ -24,13 +24,17 @@ constexpr int kPaMostPerSm = 4;
 // keys take 0.3. (Shares by keys alone: a CTA with seven short items took 34 us
 // where the others took 13.)
 constexpr int kPaItemCost = 320;
-// Keys of an item that is never cut, and where there is an item for every SM.
+// Keys of an item that is never cut, and where there is an item for every SM. (48
+// windowed sequences of 1028 keys, 192 items: cut 26 us, whole 22.)
 constexpr int kPaWhole = 512, kPaWholeMany = 2048;
 // The same of paged_attn_tc_kernel, whose steps are faster. (512: a prompt of 4096
 // tokens 179 us instead of 167, 2 x 65 tokens after 8900 others 30 instead of 32; 1024:
 // 170 and 33.)
 constexpr int kTcItemCost = 768;
-constexpr int kPaLeast = 448;     // keys of a share at least, that cost among them
+// Keys of a share at least, that cost among them. (448: a token of 64 + 8 heads of 128
+// over 1000 keys 14.3 us instead of 11.1, two over 3000 in 4 bits 18.4 instead of 13.6;
+// 64: 10.6 and 15.8.)
+constexpr int kPaLeast = 128;
 constexpr float kPaSlack = 8.0f;
 
 // First key of a tile that is not there, past every position.
