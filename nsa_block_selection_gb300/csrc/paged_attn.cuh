@@ -24,8 +24,10 @@ constexpr int kPaMostPerSm = 4;
 // keys take 0.3. (Shares by keys alone: a CTA with seven short items took 34 us
 // where the others took 13.)
 constexpr int kPaItemCost = 320;
-// Keys of an item that is never cut, and where there is an item for every SM. (48
-// windowed sequences of 1028 keys, 192 items: cut 26 us, whole 22.)
+// Keys of an item that is never cut, and where there is an item for every SM. (A token
+// of 64 + 8 heads over 300 keys: whole 9.0 us, cut 10.8; over 500 10.9 and 10.3. 48
+// sequences of 32 + 4 heads, 192 items: 1028 keys each whole 22 us, cut 26; 1500 each 28
+// and 32, up to 1500 23 and 20, up to 3000 41 and 33.)
 constexpr int kPaWhole = 512, kPaWholeMany = 2048;
 // The same of paged_attn_tc_kernel, whose steps are faster. (512: a prompt of 4096
 // tokens 179 us instead of 167, 2 x 65 tokens after 8900 others 30 instead of 32; 1024:
