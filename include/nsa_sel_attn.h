@@ -543,8 +543,10 @@ int nsa_swa_bwd(const void* Q, const void* K, const void* V, const void* O, cons
  *                  D is contiguous. Q and K can so be slices of one projection.
  *
  * Per row x: n = x rsqrt(mean(x^2) + eps) w, then every pair (a, b) of n
- * becomes (a cos - b sin, b cos + a sin); all in fp32, rounded once (nearest
- * even) to dtype. A token whose position is negative, or >= table_rows when
+ * becomes (a cos - b sin, b cos + a sin); all in fp32, each operation rounded
+ * by itself ((x r) w; two products, then their sum), and once (nearest even) to
+ * dtype. The sum of squares adds entries 32 apart first, in rising order, then
+ * neighbours, pairs, pairs of pairs and so on. A token whose position is negative, or >= table_rows when
  * R > 0, is padding: its inputs are not read and its output rows are zero.
  * A non-finite entry reaches its own row only. With positions NULL and R > 0
  * the table must hold M rows (else NSA_ERR_SHAPE).
@@ -660,7 +662,9 @@ typedef struct nsa_kv_cache {
  * A 16-bit cache has the type of K and V. A 4-bit row is made of the row
  * rounded to that type: low = bf16(min), step = bf16((max - low) / 15), 0 where
  * that is below 2^-60, code = clamp(rint((x - low) / step), 0, 15); a row with
- * an entry that is not finite, or whose range passes fp32's, reads as NaN.
+ * an entry that is not finite, or whose range passes fp32's, reads as NaN. Codes
+ * jump where a last bit of the 16-bit row moves: they are those of that row, whose
+ * bits the order of operations above decides.
  *
  * A token of negative position, or (R > 0) of one past the angle tables, is
  * padding: its Q row is zero and nothing is stored. A token in a page that the

@@ -4,7 +4,7 @@
 //
 // Append, per token at position p: Q and K rows become
 //   y = turn_p(x rsqrt(mean(x^2) + eps) w),
-// fp32, rounded once to the 16-bit type, as in norm_rope.cu; Q is written as a
+// fp32, rounded once to the 16-bit type, in norm_rope.cu's order of operations; Q is written as a
 // tensor, K and V as rows of the token's page. A 4-bit row is made of the 16-bit
 // one: low = bf16(min), step = bf16((max - low) / 15),
 // code = clamp(rint((x - low) / step), 0, 15), all divisions IEEE, so that the
@@ -108,7 +108,7 @@ __device__ __forceinline__ void store_codes(const uint4& v0, const uint4& v1, in
 }
 
 // K's or V's rows [r0, r1) of one token, UN groups of rows in flight per warp.
-template <int D, bool BF16, bool Q4, bool V, int UN>
+template <int D, bool BF16, bool Q4, bool FULL, bool V, int UN>
 __device__ __forceinline__ void append_rows(const AppendProblem& p, const uint8_t* x, int64_t xh,
                                             int r0, int r1, int page, int off, bool rot, int c0,
                                             int c1, const float* c, const float* s) {
@@ -134,18 +134,11 @@ __device__ __forceinline__ void append_rows(const AppendProblem& p, const uint8_
     for (int u = 0; u < UN; ++u) {
       const int row = r + u * RPW + sub;
       if constexpr (!V) {
-        float f[16];
+        float f[16], sq = 0.f;
+        if (p.norm) sq = row_squares<D, BF16, FULL>(v[u][0], v[u][1], x + 2 * row * xh, row < r1);
         unpack8<BF16>(v[u][0], f);
         unpack8<BF16>(v[u][1], f + 8);
-        if (p.norm) {
-          float sq = 0.f;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) sq = fmaf(f[i], f[i], sq);
-          sq = row_sum<LPR>(sq);
-          const float rs = rsqrtf(sq * (1.f / D) + p.r.eps);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) f[i] *= rs * w[i];
-        }
+        if (p.norm) scale_row(f, rsqrtf(sq * (1.f / D) + p.r.eps), w);
         if (rot) turn(f, c, s, p.r.interleaved);
         v[u][0] = pack8<BF16>(f);
         v[u][1] = pack8<BF16>(f + 8);
@@ -165,8 +158,8 @@ __device__ __forceinline__ void append_rows(const AppendProblem& p, const uint8_
 
 // Many heads: one warp per unit of `per` rows of the H + 2 G of a token (Q's, K's,
 // V's), which share its position, page and angles, as norm_rope_kernel.
-template <int D, bool BF16, bool Q4, int UN>
-__global__ void __launch_bounds__(kKvThreads)
+template <int D, bool BF16, bool Q4, bool FULL, int UN>
+__global__ void __launch_bounds__(kKvThreads, FULL ? 5 : 4)
     kv_append_token_kernel(const AppendProblem p, int segs, int per, int64_t units) {
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kKvThreads / 32) + (threadIdx.x >> 5);
   if (unit >= units) return;
@@ -178,28 +171,31 @@ __global__ void __launch_bounds__(kKvThreads)
   const bool live = at >= 0;
   const int H = p.r.q.heads, G = p.r.k.heads;
   int c0, c1;
-  const int t = (threadIdx.x & 31) % (D / 16);
-  row_chunks(t, p.r.half, c0, c1);
-  const bool rot = t < (p.r.half >> 3);
+  const int t = (threadIdx.x & 31) % (D / 16), half = FULL ? D / 2 : p.r.half;
+  row_chunks(t, half, c0, c1);
+  const bool rot = t < (half >> 3);
   float c[8], s[8];
-  if (live && rot) load_angles(p.r, at, c0, c1, c, s);
+  if (live && rot) load_angles(p.r, at, half, c0, c1, c, s);
   const int r0 = seg * per, r1 = min(r0 + per, H + 2 * G);
   const int page = live && r1 > H ? page_of(p.c, b, at) : -1;
   const int off = static_cast<int>(at) & ((1 << p.c.shift) - 1);
   if (r0 < H)
-    norm_rope_rows<D, BF16, UN>(p.r, p.r.q, b, m, r0, min(r1, H), live, rot, c0, c1, c, s, p.norm);
+    norm_rope_rows<D, BF16, FULL, true, UN>(p.r, p.r.q, b, m, r0, min(r1, H), live, rot, c0, c1, c, s,
+                                            p.norm);
   if (page < 0) return;
   if (r1 > H && r0 < H + G)
-    append_rows<D, BF16, Q4, false, 2>(p, p.r.k.x + 2 * (b * p.r.k.xb + m * p.r.k.xm), p.r.k.xh,
-                                       max(r0 - H, 0), min(r1 - H, G), page, off, rot, c0, c1, c, s);
+    append_rows<D, BF16, Q4, FULL, false, 2>(p, p.r.k.x + 2 * (b * p.r.k.xb + m * p.r.k.xm),
+                                             p.r.k.xh, max(r0 - H, 0), min(r1 - H, G), page, off,
+                                             rot, c0, c1, c, s);
   if (r1 > H + G)
-    append_rows<D, BF16, Q4, true, 2>(p, p.v + 2 * (b * p.vb + m * p.vm), p.vh, max(r0 - H - G, 0),
-                                      r1 - H - G, page, off, false, c0, c1, c, s);
+    append_rows<D, BF16, Q4, FULL, true, 2>(p, p.v + 2 * (b * p.vb + m * p.vm), p.vh,
+                                            max(r0 - H - G, 0), r1 - H - G, page, off, false, c0, c1,
+                                            c, s);
 }
 
 // Few heads, or few tokens: a row slot of a warp keeps its head (of Q, K or V) and the
 // head's weights, and walks the tokens, as in norm_rope_few_kernel.
-template <int D, bool BF16, bool Q4>
+template <int D, bool BF16, bool Q4, bool FULL>
 __global__ void __launch_bounds__(kKvThreads, Q4 ? kAppendPerSm4 : kAppendPerSm)
     kv_append_kernel(const AppendProblem p, const RowGroups rg) {
   constexpr int LPR = D / 16, RPW = 32 / LPR;
@@ -216,8 +212,9 @@ __global__ void __launch_bounds__(kKvThreads, Q4 ? kAppendPerSm4 : kAppendPerSm)
   const bool slot = head < H + 2 * G, is_q = head < H, is_v = head >= H + G;
   const int64_t h = is_q ? head : is_v ? head - H - G : head - H;
   int c0, c1;
-  row_chunks(tl, p.r.half, c0, c1);
-  const bool rot = tl < (p.r.half >> 3) && !is_v;
+  const int half = FULL ? D / 2 : p.r.half;
+  row_chunks(tl, half, c0, c1);
+  const bool rot = tl < (half >> 3) && !is_v;
   float w[16];
   load_weights<BF16>(is_v ? nullptr : is_q ? p.r.q.w : p.r.k.w, p.r.w32, c0, c1, w);
   const uint8_t* x;
@@ -239,6 +236,7 @@ __global__ void __launch_bounds__(kKvThreads, Q4 ? kAppendPerSm4 : kAppendPerSm)
     int64_t yo = 0, so = 0;
     float f[16], c[8], s[8];
     uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
+    const uint8_t* src = x;
     if (write) {
       const int b = static_cast<int>(static_cast<uint32_t>(tok) / static_cast<uint32_t>(p.r.M));
       const int m = static_cast<int>(static_cast<uint32_t>(tok) - static_cast<uint32_t>(b) * p.r.M);
@@ -254,30 +252,18 @@ __global__ void __launch_bounds__(kKvThreads, Q4 ? kAppendPerSm4 : kAppendPerSm)
         so = ((page * static_cast<int64_t>(G) + h) << p.c.shift) + row;
       }
       if (live) {  // (padding is not read)
-        const uint4* src = reinterpret_cast<const uint4*>(x + 2 * (b * xb + m * xm));
-        v0 = src[c0];
-        v1 = src[c1];
-        if (rot) load_angles(p.r, at, c0, c1, c, s);
+        src += 2 * (b * xb + m * xm);
+        v0 = reinterpret_cast<const uint4*>(src)[c0];
+        v1 = reinterpret_cast<const uint4*>(src)[c1];
+        if (rot) load_angles(p.r, at, half, c0, c1, c, s);
       }
     }
+    float sq = 0.f;
+    if (p.norm) sq = row_squares<D, BF16, FULL>(v0, v1, src, live);
     if (!is_v) {
       unpack8<BF16>(v0, f);
       unpack8<BF16>(v1, f + 8);
-    }
-    if (p.norm) {
-      float sq = 0.f;
-      if (!is_v) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sq = fmaf(f[i], f[i], sq);
-      }
-      sq = row_sum<LPR>(sq);
-      if (live && !is_v) {
-        const float rs = rsqrtf(sq * (1.f / D) + p.r.eps);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] *= rs * w[i];
-      }
-    }
-    if (!is_v) {
+      if (live && p.norm) scale_row(f, rsqrtf(sq * (1.f / D) + p.r.eps), w);
       if (live && rot) turn(f, c, s, p.r.interleaved);
       v0 = pack8<BF16>(f);
       v1 = pack8<BF16>(f + 8);
@@ -369,8 +355,8 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const ReadProblem p, int l
   }
 }
 
-template <int D, bool BF16, bool Q4>
-int launch_append(const AppendProblem& p, cudaStream_t st) {
+template <int D, bool BF16, bool Q4, bool FULL>
+int launch_append_full(const AppendProblem& p, cudaStream_t st) {
   constexpr int RPW = 32 / (D / 16);
   constexpr int64_t kWarps = kKvThreads / 32;
   const int64_t tokens = static_cast<int64_t>(p.r.B) * p.r.M;
@@ -385,7 +371,7 @@ int launch_append(const AppendProblem& p, cudaStream_t st) {
     per = (per + RPW - 1) / RPW * RPW;
     segs = (rows + per - 1) / per;
     const int64_t units = tokens * segs;
-    kv_append_token_kernel<D, BF16, Q4, 4>
+    kv_append_token_kernel<D, BF16, Q4, FULL, 4>
         <<<static_cast<unsigned>((units + kWarps - 1) / kWarps), kKvThreads, 0, st>>>(
             p, static_cast<int>(segs), static_cast<int>(per), units);
     return cudaGetLastError() == cudaSuccess ? NSA_OK : NSA_ERR_LAUNCH;
@@ -394,9 +380,15 @@ int launch_append(const AppendProblem& p, cudaStream_t st) {
   constexpr int64_t kMost = (Q4 ? kAppendPerSm4 : kAppendPerSm) * kKvSms * kWarps;
   if (warps > kMost) warps = kMost;
   if (warps < g.per_token) warps = g.per_token;
-  kv_append_kernel<D, BF16, Q4>
+  kv_append_kernel<D, BF16, Q4, FULL>
       <<<static_cast<unsigned>((warps + kWarps - 1) / kWarps), kKvThreads, 0, st>>>(p, g);
   return cudaGetLastError() == cudaSuccess ? NSA_OK : NSA_ERR_LAUNCH;
+}
+
+template <int D, bool BF16, bool Q4>
+int launch_append(const AppendProblem& p, cudaStream_t st) {
+  return 2 * p.r.half == D ? launch_append_full<D, BF16, Q4, true>(p, st)
+                           : launch_append_full<D, BF16, Q4, false>(p, st);
 }
 
 template <int D, bool BF16>

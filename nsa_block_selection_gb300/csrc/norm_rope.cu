@@ -9,14 +9,20 @@
 // entries past R pass through. Backward, with g = the pairs of dy turned by
 // the opposite angle and xhat = x r:
 //   dw += g xhat,   dx = r (g w - xhat mean(g w xhat)).
-// All of it is fp32, rounded once when a result is stored.
+// All of it is fp32, rounded once when a result is stored. In the forward every
+// operation is rounded by itself, in this order, and a row's squares are added in a
+// fixed one (row_squares): the same row comes out of any layout and kernel, and of
+// elementary fp32 operations, so that the 4-bit codes a cache makes of it, which jump
+// by a step where a last bit moves, can be formed again anywhere. (Fused turns and
+// x (r w) moved 1 in 10,000 last bits.)
 //
 // The bytes bound both: each row is read once and written once. In the forward
 // a row is held by D / 16 lanes, 16 entries each, as two 16-byte chunks that
 // hold both entries of every pair: lane t takes chunks t and t + R/16 while
 // t < R/16, and two consecutive chunks of the tail after that, so the rotation
 // needs no exchange between lanes in either pairing and the only shuffles are
-// the row sums (3 steps at D = 128, 2 at 64). The backward does the same with
+// the row sums' (2 at D = 64; 7 at 128, or 3 and loads from the cache where R < D).
+// The backward does the same with
 // D / 8 lanes of two 8-byte chunks. A warp has 4 (D = 128) or 8 row slots in
 // the forward and 2 or 4 in the backward; with many heads they walk the heads
 // of one token, whose angles they share, with few they hold several tokens.
@@ -64,8 +70,8 @@ constexpr int64_t kFewGroups = 128 * kRopeSms;
 constexpr double kUnitCost = 0.5, kGroupCost = 0.6;
 
 // One warp per unit: `per` rows of the H + G head rows of one token.
-template <int D, bool BF16, int UN>
-__global__ void __launch_bounds__(kRopeThreads)
+template <int D, bool BF16, bool FULL, int UN>
+__global__ void __launch_bounds__(kRopeThreads, FULL ? 5 : 4)
     norm_rope_kernel(const RopeProblem p, int segs, int per, int64_t units) {
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5);
   if (unit >= units) return;
@@ -76,17 +82,18 @@ __global__ void __launch_bounds__(kRopeThreads)
   const int64_t at = token_position(p, b, m);
   const bool live = at >= 0;
   int c0, c1;
-  const int t = (threadIdx.x & 31) % (D / 16);
-  row_chunks(t, p.half, c0, c1);
-  const bool rot = t < (p.half >> 3);
+  const int t = (threadIdx.x & 31) % (D / 16), half = FULL ? D / 2 : p.half;
+  row_chunks(t, half, c0, c1);
+  const bool rot = t < (half >> 3);
   float c[8], s[8];
-  if (live && rot) load_angles(p, at, c0, c1, c, s);
+  if (live && rot) load_angles(p, at, half, c0, c1, c, s);
   const int r0 = seg * per, r1 = min(r0 + per, p.q.heads + p.k.heads);
   if (r0 < p.q.heads)
-    norm_rope_rows<D, BF16, UN>(p, p.q, b, m, r0, min(r1, p.q.heads), live, rot, c0, c1, c, s);
+    norm_rope_rows<D, BF16, FULL, !FULL, UN>(p, p.q, b, m, r0, min(r1, p.q.heads), live, rot, c0, c1,
+                                             c, s);
   if (r1 > p.q.heads)
-    norm_rope_rows<D, BF16, UN>(p, p.k, b, m, max(r0 - p.q.heads, 0), r1 - p.q.heads, live, rot, c0,
-                                c1, c, s);
+    norm_rope_rows<D, BF16, FULL, !FULL, UN>(p, p.k, b, m, max(r0 - p.q.heads, 0), r1 - p.q.heads,
+                                             live, rot, c0, c1, c, s);
 }
 
 // The forward where a token has few heads: a row slot of a warp keeps its head,
@@ -96,7 +103,7 @@ __global__ void __launch_bounds__(kRopeThreads)
 // 73 us against 13, of 8 + 2 76 against 36. Two rows in flight a lane leave 16
 // to 20 warps an SM: 40 for the latter, with 28 warps of one row it is 36;
 // loading the next position early gave nothing.)
-template <int D, bool BF16>
+template <int D, bool BF16, bool FULL>
 __global__ void __launch_bounds__(kRopeThreads, kFewPerSm)
     norm_rope_few_kernel(const RopeProblem p, const RowGroups rg) {
   constexpr int LPR = D / 16, RPW = 32 / LPR;
@@ -115,8 +122,9 @@ __global__ void __launch_bounds__(kRopeThreads, kFewPerSm)
   const RopeRows& t = is_k ? p.k : p.q;
   const int64_t h = is_k ? head - p.q.heads : head;
   int c0, c1;
-  row_chunks(tl, p.half, c0, c1);
-  const bool rot = tl < (p.half >> 3);
+  const int half = FULL ? D / 2 : p.half;
+  row_chunks(tl, half, c0, c1);
+  const bool rot = tl < (half >> 3);
   float w[16];
   load_weights<BF16>(t.w, p.w32, c0, c1, w);
   const uint8_t* const x = t.x + 2 * h * t.xh;
@@ -131,6 +139,7 @@ __global__ void __launch_bounds__(kRopeThreads, kFewPerSm)
     int64_t yo = 0;
     float f[16], c[8], s[8];
     uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
+    const uint8_t* src = x;
     if (in) {
       const int b = static_cast<int>(static_cast<uint32_t>(tok) / static_cast<uint32_t>(p.M));
       const int m = static_cast<int>(static_cast<uint32_t>(tok) - static_cast<uint32_t>(b) * p.M);
@@ -138,22 +147,17 @@ __global__ void __launch_bounds__(kRopeThreads, kFewPerSm)
       yo = 2 * (b * t.yb + m * t.ym);
       live = at >= 0;
       if (live) {  // (padding is not read)
-        const uint4* src = reinterpret_cast<const uint4*>(x + 2 * (b * t.xb + m * t.xm));
-        v0 = src[c0];
-        v1 = src[c1];
-        if (rot) load_angles(p, at, c0, c1, c, s);
+        src += 2 * (b * t.xb + m * t.xm);
+        v0 = reinterpret_cast<const uint4*>(src)[c0];
+        v1 = reinterpret_cast<const uint4*>(src)[c1];
+        if (rot) load_angles(p, at, half, c0, c1, c, s);
       }
     }
+    const float sq = row_squares<D, BF16, FULL>(v0, v1, src, live);
     unpack8<BF16>(v0, f);
     unpack8<BF16>(v1, f + 8);
-    float sq = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) sq = fmaf(f[i], f[i], sq);
-    sq = row_sum<LPR>(sq);
     if (live) {  // a padding token's rows are zero
-      const float rs = rsqrtf(sq * (1.f / D) + p.eps);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) f[i] *= rs * w[i];
+      scale_row(f, rsqrtf(sq * (1.f / D) + p.eps), w);
       if (rot) turn(f, c, s, p.interleaved);
     }
     if (in) {
@@ -544,8 +548,8 @@ void plan_rope_rows(RopeBwdRows& t, int64_t tokens, int rows_per_warp, int ctas)
   t.ctas = static_cast<int>(need < ctas ? need : ctas);
 }
 
-template <int D, bool BF16>
-int launch_norm_rope(const RopeProblem& p, cudaStream_t st) {
+template <int D, bool BF16, bool FULL>
+int launch_norm_rope_full(const RopeProblem& p, cudaStream_t st) {
   constexpr int RPW = 32 / (D / 16), UN = 4;
   const int rows = p.q.heads + p.k.heads;
   const int64_t tokens = static_cast<int64_t>(p.B) * p.M;
@@ -557,7 +561,7 @@ int launch_norm_rope(const RopeProblem& p, cudaStream_t st) {
     int64_t warps = g.groups;
     if (warps > kFewPerSm * kRopeSms * kWarps) warps = kFewPerSm * kRopeSms * kWarps;
     if (warps < g.per_token) warps = g.per_token;
-    norm_rope_few_kernel<D, BF16>
+    norm_rope_few_kernel<D, BF16, FULL>
         <<<static_cast<unsigned>((warps + kWarps - 1) / kWarps), kRopeThreads, 0, st>>>(p, g);
     return cudaGetLastError() == cudaSuccess ? NSA_OK : NSA_ERR_LAUNCH;
   }
@@ -574,9 +578,15 @@ int launch_norm_rope(const RopeProblem& p, cudaStream_t st) {
   // with more than one segment each no more than some 2 x 16 x 152 units)
   const int64_t units = tokens * segs;
   const int64_t blocks = (units + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
-  norm_rope_kernel<D, BF16, UN><<<static_cast<unsigned>(blocks), kRopeThreads, 0, st>>>(
+  norm_rope_kernel<D, BF16, FULL, UN><<<static_cast<unsigned>(blocks), kRopeThreads, 0, st>>>(
       p, static_cast<int>(segs), static_cast<int>(per), units);
   return cudaGetLastError() == cudaSuccess ? NSA_OK : NSA_ERR_LAUNCH;
+}
+
+template <int D, bool BF16>
+int launch_norm_rope(const RopeProblem& p, cudaStream_t st) {
+  return 2 * p.half == D ? launch_norm_rope_full<D, BF16, true>(p, st)
+                         : launch_norm_rope_full<D, BF16, false>(p, st);
 }
 
 template <int D, bool BF16, bool G32>

@@ -17,6 +17,7 @@
 namespace nsa {
 namespace {
 
+// Kernels with FULL are for R = D: where a lane's chunks lie is known to the compiler.
 struct RopeRows {
   const uint8_t* x;  // one of Q, K: element strides over (b, m, h)
   uint8_t* y;
@@ -100,10 +101,10 @@ __device__ __forceinline__ void load_weights(const void* w, bool w32, int c0, in
 // The 8 angles of the lane's 8 pairs. Halves: pair j is entries j of the two
 // chunks. Interleaved: pairs 0..3 are the entries (2j, 2j + 1) of the first
 // chunk, 4..7 those of the second.
-__device__ __forceinline__ void load_angles(const RopeProblem& p, int64_t at, int c0, int c1,
-                                            float* c, float* s) {
-  const float* ct = p.cos_t + at * p.half;
-  const float* st = p.sin_t + at * p.half;
+__device__ __forceinline__ void load_angles(const RopeProblem& p, int64_t at, int half, int c0,
+                                            int c1, float* c, float* s) {
+  const float* ct = p.cos_t + at * half;
+  const float* st = p.sin_t + at * half;
   if (p.interleaved) {
     const float4 a = *reinterpret_cast<const float4*>(ct + 4 * c0);
     const float4 b = *reinterpret_cast<const float4*>(ct + 4 * c1);
@@ -117,22 +118,64 @@ __device__ __forceinline__ void load_angles(const RopeProblem& p, int64_t at, in
   }
 }
 
-// (a, b) -> (a c - b s, b c + a s) on the lane's 8 pairs.
+// Two fp32 operations an instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// The turn of the lane's 8 pairs: (a, b) -> (a c - b s, b c + a s), every operation
+// rounded by itself.
 __device__ __forceinline__ void turn(float* f, const float* c, const float* s, bool interleaved) {
   if (interleaved) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float a = f[2 * j], b = f[2 * j + 1];
-      f[2 * j] = a * c[j] - b * s[j];
-      f[2 * j + 1] = b * c[j] + a * s[j];
+      f[2 * j] = __fsub_rn(__fmul_rn(a, c[j]), __fmul_rn(b, s[j]));
+      f[2 * j + 1] = __fadd_rn(__fmul_rn(b, c[j]), __fmul_rn(a, s[j]));
     }
   } else {
+    // (products two at a time, sums one: sums of pairs were fused with the products)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float a = f[j], b = f[j + 8];
-      f[j] = a * c[j] - b * s[j];
-      f[j + 8] = b * c[j] + a * s[j];
+    for (int j = 0; j < 8; j += 2) {
+      const uint64_t a = pair(f[j], f[j + 1]), b = pair(f[j + 8], f[j + 9]);
+      const uint64_t cc = pair(c[j], c[j + 1]), ss = pair(s[j], s[j + 1]);
+      const float2 ac = unpair(mul2(a, cc)), bs = unpair(mul2(b, ss));
+      const float2 bc = unpair(mul2(b, cc)), as = unpair(mul2(a, ss));
+      f[j] = __fsub_rn(ac.x, bs.x), f[j + 1] = __fsub_rn(ac.y, bs.y);
+      f[j + 8] = __fadd_rn(bc.x, as.x), f[j + 9] = __fadd_rn(bc.y, as.y);
     }
+  }
+}
+
+// (f r) w, two at a time.
+__device__ __forceinline__ void scale_row(float* f, float r, const float* w) {
+  const uint64_t rr = pair(r, r);
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {
+    const float2 x = unpair(mul2(mul2(pair(f[i], f[i + 1]), rr), pair(w[i], w[i + 1])));
+    f[i] = x.x, f[i + 1] = x.y;
   }
 }
 
@@ -143,6 +186,74 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
+// The sum of a row's squares (exact in fp32 one by one) in a fixed order that does
+// not depend on how lanes hold the row: entries 32 apart first, one after the other,
+// then neighbours, pairs, pairs of pairs and so on. Lane t of a row begins with the
+// sums of N entries from 8 t (D = 64) or 8 (t % 4) + 4 (t / 4) on: where all of a row
+// is turned (FULL) its chunks hold them, or (D = 128) its chunks and those of lane
+// t ^ 4; else it loads them from x again (cached). `have`: the slot holds a row.
+template <int D, bool BF16, bool FULL>
+__device__ __forceinline__ float row_squares(const uint4& v0, const uint4& v1, const uint8_t* x,
+                                             bool have) {
+  constexpr int N = 512 / D, K = D / 32;
+  const int t = (threadIdx.x & 31) % (D / 16);
+  uint32_t w[K][N / 2];  // entry pairs, of each of the row's 32s
+  if constexpr (D == 64) {
+    uint4 a = v0, b = v1;
+    if (!FULL && have) {
+      a = reinterpret_cast<const uint4*>(x)[t];
+      b = reinterpret_cast<const uint4*>(x)[t + 4];
+    }
+    w[0][0] = a.x, w[0][1] = a.y, w[0][2] = a.z, w[0][3] = a.w;
+    w[1][0] = b.x, w[1][1] = b.y, w[1][2] = b.z, w[1][3] = b.w;
+  } else if constexpr (FULL) {
+    // (k = 0 and 1 may change places: they are added to one another first)
+    const bool up = (t & 4) != 0;
+    const uint32_t own[4] = {up ? v0.z : v0.x, up ? v0.w : v0.y, up ? v1.z : v1.x,
+                             up ? v1.w : v1.y};
+    const uint32_t give[4] = {up ? v0.x : v0.z, up ? v0.y : v0.w, up ? v1.x : v1.z,
+                              up ? v1.y : v1.w};
+    uint32_t got[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) got[i] = __shfl_xor_sync(kFull, give[i], 4);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      w[0][i] = own[i], w[1][i] = got[i];
+      w[2][i] = up ? got[2 + i] : own[2 + i];
+      w[3][i] = up ? own[2 + i] : got[2 + i];
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const uint2 a = have ? reinterpret_cast<const uint2*>(x)[8 * k + 2 * (t & 3) + (t >> 2)]
+                           : make_uint2(0, 0);
+      w[k][0] = a.x, w[k][1] = a.y;
+    }
+  }
+  uint64_t a[N / 2];
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const float2 p = unpack2<BF16>(w[k][i]);
+      const uint64_t z = pair(p.x, p.y);
+      a[i] = k == 0 ? mul2(z, z) : fma2(z, z, a[i]);
+    }
+  float b[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    const float2 p = unpair(a[i]);
+    b[i] = __fadd_rn(p.x, p.y);
+  }
+#pragma unroll
+  for (int n = N / 4; n > 0; n >>= 1)
+#pragma unroll
+    for (int i = 0; i < n; ++i) b[i] = __fadd_rn(b[2 * i], b[2 * i + 1]);
+  if constexpr (D == 128) b[0] = __fadd_rn(b[0], __shfl_xor_sync(kFull, b[0], 4));
+  b[0] = __fadd_rn(b[0], __shfl_xor_sync(kFull, b[0], 1));
+  return __fadd_rn(b[0], __shfl_xor_sync(kFull, b[0], 2));
+}
+
 // A token's position, or -1 for padding (outside the table).
 __device__ __forceinline__ int64_t token_position(const RopeProblem& p, int b, int m) {
   int64_t at = m;
@@ -151,8 +262,11 @@ __device__ __forceinline__ int64_t token_position(const RopeProblem& p, int b, i
   return at;
 }
 
-// Rows [r0, r1) of one token's heads, UN groups of rows in flight per warp.
-template <int D, bool BF16, int UN>
+// Rows [r0, r1) of one token's heads, UN groups of rows in flight per warp. FIRST: the
+// sums of them all before the first is stored, so that no row's loads wait for
+// another's stores (65,536 tokens of 64 + 8 heads of 128: the append 404 us with and
+// 412 without; the norm alone, whose registers it takes, 366 and 360).
+template <int D, bool BF16, bool FULL, bool FIRST, int UN>
 __device__ __forceinline__ void norm_rope_rows(const RopeProblem& p, const RopeRows& t, int b, int m,
                                                int r0, int r1, bool live, bool rot, int c0, int c1,
                                                const float* c, const float* s, bool norm = true) {
@@ -174,23 +288,24 @@ __device__ __forceinline__ void norm_rope_rows(const RopeProblem& p, const RopeR
         v[u][1] = src[c1];
       }
     }
+    float sq[UN];
+    auto squares = [&](int u) {
+      const int row = r + u * RPW + sub;
+      sq[u] = row_squares<D, BF16, FULL>(v[u][0], v[u][1], x + 2 * row * t.xh, live && row < r1);
+    };
+    if (FIRST && norm) {
+#pragma unroll
+      for (int u = 0; u < UN; ++u) squares(u);
+    }
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
       const int row = r + u * RPW + sub;
+      if (!FIRST && norm) squares(u);
       float f[16];
       unpack8<BF16>(v[u][0], f);
       unpack8<BF16>(v[u][1], f + 8);
-      if (norm) {
-        float sq = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sq = fmaf(f[i], f[i], sq);
-        sq = row_sum<LPR>(sq);
-        if (live) {  // a padding token's rows are zero
-          const float rs = rsqrtf(sq * (1.f / D) + p.eps);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) f[i] *= rs * w[i];
-        }
-      }
+      // (a padding token's rows are zero)
+      if (norm && live) scale_row(f, rsqrtf(sq[u] * (1.f / D) + p.eps), w);
       if (live && rot) turn(f, c, s, p.interleaved);
       if (row < r1) {
         uint4* dst = reinterpret_cast<uint4*>(y + 2 * row * t.yh);
