@@ -743,6 +743,11 @@ int64_t nsa_paged_attn_workspace_bytes(int64_t B, int64_t M, int64_t H, int64_t 
  * (or the scales of a 4-bit row) that some query of a row tile sees is multiplied
  * by 0 for those that do not, and has to be finite.
  *
+ * Over a 4-bit cache p carries V's step (a row without one counts as the larger of
+ * 2^-60 and 2^-40 |low|): keys whose p is 2^-26 of the largest or more are all in
+ * the sums while these lie within 2^100 of one another. Entries of Q stay below
+ * 2^112.
+ *
  * Every sum has an order that the sizes and positions alone decide: equal calls
  * give equal bits. Two kernels on `stream` (one where no workspace is needed), no
  * allocation. Errors before launch: as nsa_swa_fwd, the cache's and the

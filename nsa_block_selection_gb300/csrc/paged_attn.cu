@@ -315,11 +315,12 @@ __device__ __forceinline__ void pa_scores4(const PaRows<D, NT>& a, const uint8_t
   for (int j = 0; j < 2; ++j) {
     kstep[j] = __uint_as_float(ks[j] << 16);
     klow[j] = __uint_as_float(ks[j] & 0xffff0000u);
-    const float step = __uint_as_float(vs[j] << 16);
-    const float any = step == 0.f ? 1.f : step;  // (all codes are 0 then: any step serves)
-    mid[j] = fmaf(8.f, any, __uint_as_float(vs[j] & 0xffff0000u));
-    rstep[j] = rcp_approx(any);
-    lstep[j] = lg2_approx(any);
+    const float step = __uint_as_float(vs[j] << 16), low = __uint_as_float(vs[j] & 0xffff0000u);
+    const float some = pa_step(step, low);
+    mid[j] = fmaf(8.f, step, low);
+    rstep[j] = rcp_approx(some);
+    lstep[j] = lg2_approx(some);
+    if (step == 0.f) rstep[j] = -rstep[j];
   }
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -364,9 +365,15 @@ __device__ __forceinline__ void pa_values4(PaRows<D, NT>& a, const uint8_t* vt, 
     float e[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) e[i] = ex2(x[nt][i] + a.neg[nt][i & 1]);
-    const uint32_t p0 = pack_half2(e[0], e[1]), p1 = pack_half2(e[2], e[3]);
+    uint32_t p0 = pack_half2(e[0], e[1]), p1 = pack_half2(e[2], e[3]);
+    [[maybe_unused]] uint32_t r0 = 0u, r1 = 0u;
     if constexpr (REST) {
-      const uint32_t r0 = pa_rest<false>(p0, e[0], e[1]), r1 = pa_rest<false>(p1, e[2], e[3]);
+      r0 = pa_rest<false>(p0, e[0], e[1]);
+      r1 = pa_rest<false>(p1, e[2], e[3]);
+    }
+    if (rstep[0] < 0.f) p0 = r0 = 0u;
+    if (rstep[1] < 0.f) p1 = r1 = 0u;
+    if constexpr (REST) {
       const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&r0));
       const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&r1));
       a.base_v[nt][0] = fmaf(f0.x + f1.x, -8.f, a.base_v[nt][0]);
@@ -376,7 +383,7 @@ __device__ __forceinline__ void pa_values4(PaRows<D, NT>& a, const uint8_t* vt, 
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float md = mid[i >> 1], pr = e[i] * rstep[i >> 1];
+      float md = mid[i >> 1], pr = e[i] * fabsf(rstep[i >> 1]);
       if (EDGE && see.hidden(key + 8 * (i >> 1), a.pos[nt][i & 1])) md = pr = 0.f;
       a.l[nt][i & 1] += pr;
       a.base_v[nt][i & 1] = fmaf(pr, md, a.base_v[nt][i & 1]);

@@ -213,6 +213,16 @@ __device__ __forceinline__ void pa_zeros(const PagedProblem& p, int rows_tile, c
   }
 }
 
+// What a V row enters the exponent with: its step, or, for a row without one (all
+// codes are 0, the row is its low), a number so far below low that the keys beside it
+// lose nothing that O has, and so near that p' low / step stays in fp32. Such a row's
+// p' is not multiplied with its codes (p low is its part of O). (With 1 for all of
+// them p' of small rows beside a row of zeros fell among fp16's subnormals: 500 keys
+// of std 0.002 and one of zeros with 0.96 of the weight, O 34 % off.)
+__device__ __forceinline__ float pa_step(float step, float low) {
+  return step == 0.f ? fmaxf(kLeastStep, fabsf(low) * 0x1p-40f) : step;
+}
+
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));

@@ -832,15 +832,23 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
           // the key's numbers: K's step and middle, log2 of V's step, its reciprocal
           // and the middle by that. (Their slot was last read by the softmax of
           // step g - 4, which is over: the S after its PV is.)
-          const float any = vstep == 0.f ? 1.f : vstep;  // (all codes are 0 then)
-          const float rs = rcp_approx(any);
+          const float some = pa_step(vstep, vlow);
+          const float rs = rcp_approx(some);
+          // rows without a step: codes of 8, whose c - 8 is 0
+          const uint32_t flat = __ballot_sync(kFull, vstep == 0.f);
+          if (flat != 0u) {
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+              if (flat >> (kRowsAt * j + row0) & 1u)
+                v[j] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+          }
           float* const num =
               reinterpret_cast<float*>(gbase + C::kOffInfo + (g & 3) * C::kInfoBytes) + key_in;
           num[0] = have ? kstep : 0.f;
           num[128] = have ? fmaf(8.f, kstep, klow) : 0.f;
-          num[256] = have ? lg2_approx(any) : -INFINITY;
+          num[256] = have ? lg2_approx(some) : -INFINITY;
           num[384] = have ? rs : 0.f;
-          num[512] = have ? fmaf(8.f, any, vlow) * rs : 0.f;
+          num[512] = have ? fmaf(8.f, vstep, vlow) * rs : 0.f;
           mbar_arrive(bar(kInfo + static_cast<int>(g & 3)));
           store(gbase + C::kOffK + s * C::kTile, k);
           mbar_arrive(bar(kKFull + s));
