@@ -739,9 +739,10 @@ int64_t nsa_paged_attn_workspace_bytes(int64_t B, int64_t M, int64_t H, int64_t 
  * multiplied too (over a 4-bit cache where O is fp16). Sums are fp32, O is rounded once. LSE is
  * the natural log of sum(exp(scale q.k)) over the visible keys. A query that
  * sees no key, or is padding, gets O = 0, LSE = -inf.
- * Keys and values that no query of the sequence sees may hold anything. A V row
- * (or the scales of a 4-bit row) that some query of a row tile sees is multiplied
- * by 0 for those that do not, and has to be finite.
+ * Keys and values that no query of the sequence sees may hold anything. A V row of a
+ * 16-bit cache that some query of a row tile sees is multiplied by 0 for those that
+ * do not, and has to be finite; one of a 4-bit cache that is not finite reaches only
+ * the queries that see it.
  *
  * Over a 4-bit cache p carries V's step (a row without one counts as the larger of
  * 2^-60 and 2^-40 |low|): keys whose p is 2^-26 of the largest or more are all in

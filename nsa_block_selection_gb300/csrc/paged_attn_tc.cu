@@ -833,7 +833,10 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
           // and the middle by that. (Their slot was last read by the softmax of
           // step g - 4, which is over: the S after its PV is.)
           const float some = pa_step(vstep, vlow);
-          const float rs = rcp_approx(some);
+          const float rs = rcp_approx(some), rm = fmaf(8.f, vstep, vlow) * rs;
+          // a row that is not finite reaches the queries that see it by their x alone: the
+          // others multiply its numbers by 0
+          const bool fine = rs < INFINITY && fabsf(rm) < INFINITY;
           // rows without a step: codes of 8, whose c - 8 is 0
           const uint32_t flat = __ballot_sync(kFull, vstep == 0.f);
           if (flat != 0u) {
@@ -846,9 +849,9 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
               reinterpret_cast<float*>(gbase + C::kOffInfo + (g & 3) * C::kInfoBytes) + key_in;
           num[0] = have ? kstep : 0.f;
           num[128] = have ? fmaf(8.f, kstep, klow) : 0.f;
-          num[256] = have ? lg2_approx(some) : -INFINITY;
-          num[384] = have ? rs : 0.f;
-          num[512] = have ? fmaf(8.f, vstep, vlow) * rs : 0.f;
+          num[256] = !have ? -INFINITY : fine ? lg2_approx(some) : __uint_as_float(0x7fc00000u);
+          num[384] = have && fine ? rs : 0.f;
+          num[512] = have && fine ? rm : 0.f;
           mbar_arrive(bar(kInfo + static_cast<int>(g & 3)));
           store(gbase + C::kOffK + s * C::kTile, k);
           mbar_arrive(bar(kKFull + s));
