@@ -174,10 +174,21 @@ __device__ __forceinline__ void pa_tile16(PaRows<D, NT>& a, const uint32_t (&qf)
   const int lane = threadIdx.x & 31, r = lane >> 2;
   const uint32_t vt = slot + kPaTile * 2 * D;
   if constexpr (EDGE) {
-    // V rows that no query sees may hold anything: they become zeros
+    // V rows that no query sees may hold anything: they become zeros. (Each question is
+    // asked of the columns' own positions: between windows there may be gaps. The four
+    // lanes of a key pair hold all columns.)
+    bool one = false, two = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        one = one || !see.hidden(n0 + r, a.pos[nt][j]);
+        two = two || !see.hidden(n0 + r + 8, a.pos[nt][j]);
+      }
+    const uint32_t seen[2] = {__ballot_sync(kFull, one), __ballot_sync(kFull, two)};
     for (int i = lane; i < kPaTile * (D / 8); i += 32) {
       const int row = i / (D / 8), ch = i % (D / 8);
-      if (see.nobody(n0 + row))
+      if ((seen[row >> 3] >> (4 * (row & 7)) & 15u) == 0u)
         st_shared_zero16(vt + (ch >> 3) * kBoxBytes + row * 128 + (ch & 7) * 16);
     }
     fence_proxy_async_smem();  // (before the slot's next copy)

@@ -72,9 +72,10 @@ struct PaSpan {
   __device__ __forceinline__ int key(int t) const { return (t < st ? t : t + jump) << shift; }
 };
 
-// A query's position (one at the end of int32 as kPaFar: kNoKey is past them all).
+// A query's position (padding as -1; one at the end of int32 as kPaFar: kNoKey is past
+// them all).
 __device__ __forceinline__ int pa_position(const PagedProblem& p, int b, int m) {
-  return min(__ldg(p.pos + b * p.pos_b + m), kPaFar);
+  return max(min(__ldg(p.pos + b * p.pos_b + m), kPaFar), -1);
 }
 
 // WARP: a whole warp calls it, a position a lane; else a thread by itself, several
@@ -117,7 +118,7 @@ __device__ __forceinline__ PaSpan pa_span(const PagedProblem& p, int b, int rt, 
 // What the queries of a row tile see of a key.
 struct PaSight {
   int lo_pos, hi_pos, left, sinks;
-  // no query sees it: its row may hold anything
+  // no query sees it (its row may hold anything), but for keys in a gap between windows
   __device__ __forceinline__ bool nobody(int key) const {
     return key > hi_pos || (key < lo_pos - left && key >= sinks);
   }
@@ -129,6 +130,9 @@ struct PaSight {
   __device__ __forceinline__ bool nothing(int n0) const {
     return n0 > hi_pos || (n0 + kPaTile - 1 < lo_pos - left && n0 >= sinks);
   }
+  // Some key from the first window to the last query may be in no window. (A key up to
+  // lo_pos is in lo_pos's; one after it in hi_pos's, where that reaches lo_pos.)
+  __device__ __forceinline__ bool gaps() const { return hi_pos - lo_pos > left; }
   __device__ __forceinline__ bool hidden(int key, int pos) const {
     return key > pos || (key < pos - left && key >= sinks);
   }

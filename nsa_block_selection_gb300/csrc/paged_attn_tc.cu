@@ -427,9 +427,9 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
       const bool mine = next_mine;
       const int mq = next_mq, h = next_h, pos = next_pos;
       const PaSight see{it.sp.lo_pos, it.sp.hi_pos, p.left, p.sinks};
-      // which of the 32 keys from `key` on this thread's query sees
-      auto seen = [&](int key) {
-        const int hi = pos - key;
+      // which of the 32 keys from `key` on a query at `pos` sees
+      auto seen = [&](int pos, int key) {
+        const int hi = max(pos - key, -1);
         return columns(hi - p.left, hi) | columns(0, min(hi, p.sinks - key - 1));
       };
       float ka = p.sl2, kb = 0.f;
@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
             }
           }
           if (masked) {
-            uint32_t bits = seen(n0 + 32 * c);
+            uint32_t bits = seen(pos, n0 + 32 * c);
             if constexpr (!Q4)
               bits &= (have >> (2 * c) & 1u ? 0xffffu : 0u) | (have >> (2 * c) & 2u ? ~0xffffu : 0u);
 #pragma unroll
@@ -560,7 +560,16 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
             failed = true;
             break;
           }
-          if (see.nobody(n0 + row)) {
+          bool nobody = see.nobody(n0 + row);
+          if (see.gaps()) {  // the tile's queries asked, 32 at a time, about the warp's 32 keys
+            const int m0 = it.rt * (rows_tile / p.hpg);
+            const int m1 = min(m0 + rows_tile / p.hpg, p.M);
+            uint32_t some = 0u;
+            for (int m = m0 + lane; m < m1; m += 32)
+              some |= seen(pa_position(p, it.b, m), n0 + 32 * quarter);
+            nobody = !(__reduce_or_sync(kFull, some) >> lane & 1u);
+          }
+          if (nobody) {
 #pragma unroll
             for (int c = 0; c < D / 8; ++c)
               *reinterpret_cast<uint4*>(gbase + C::kOffV + sb * C::kTile + (c >> 3) * C::kAtomBytes +
