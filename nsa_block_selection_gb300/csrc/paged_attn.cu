@@ -685,6 +685,12 @@ __global__ void __launch_bounds__(kPaThreads, PaCfg<D, Q4, NT>::kPerSm)
       for (int t = 0; t < steps && !failed; ++t) {
         if (!__all_sync(kFull, wait_phase(bars + 8 * stage, phase, kWaitLimitNs))) {
           failed = true;
+          // leave nothing in flight: of this warp's copies, step t's or the next one's (step
+          // t + 2 is issued when t has been read, and a turn is four steps)
+          const int own = t % kPaWarps == warp ? t : t + 1;
+          const uint32_t g = issued + own;
+          if (own % kPaWarps == warp && own < steps)
+            wait_phase(bars + 8 * (g % C::kStages), (g / C::kStages) & 1, kWaitLimitNs);
           break;
         }
         const int k0 = keys[stage * C::kKeys + 2 * warp_in];
@@ -772,7 +778,11 @@ __global__ void __launch_bounds__(kPaThreads, PaCfg<D, Q4, NT>::kPerSm)
           a.l[nt][j] += __shfl_xor_sync(kFull, a.l[nt][j], o);
           a.base_v[nt][j] += __shfl_xor_sync(kFull, a.base_v[nt][j], o);
         }
-    __syncthreads();  // every warp is done with the ring
+    // every warp is done with the ring; where one's wait gave up, all leave
+    if (__syncthreads_or(failed)) {
+      failed = true;
+      break;
+    }
     float* const joined = reinterpret_cast<float*>(gbase);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -856,11 +866,7 @@ __global__ void __launch_bounds__(kPaThreads, PaCfg<D, Q4, NT>::kPerSm)
     more = sh.at < sh.end;
   }
   if (failed) {
-    // leave nothing in flight
-    if constexpr (Q4) {
-      for (uint32_t g = issued > C::kStages ? issued - C::kStages : 0; g < issued; ++g)
-        wait_phase(bars + 8 * (g % C::kStages), (g / C::kStages) & 1, kWaitLimitNs);
-    } else {
+    if constexpr (!Q4) {  // leave nothing in flight
       for (; done != issued; ++done)
         wait_phase(bars + 8 * (done % C::kStages), (done / C::kStages) & 1, kWaitLimitNs);
     }
