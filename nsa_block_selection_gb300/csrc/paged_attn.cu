@@ -6,9 +6,10 @@
 // window), and the page of j is there. With x_j = scale log2(e) q.k_j:
 //   O = sum_j 2^(x_j - r) v_j / l,  l = sum_j 2^(x_j - r),
 //   LSE = ln 2 (r + log2 l),
-// r a reference that follows the largest x (by steps of 8: p <= 2^8). One pass
-// over the keys; x, p, sums and O are fp32, p is rounded to 16 bits for the
-// product with V, and what the rounding leaves is multiplied too.
+// r a reference that follows the largest x (by steps of 8, and 7 below it where p is
+// rounded to fp16: p <= 2^8, 2^15). One pass over the keys; x, p, sums and O are fp32,
+// p is rounded to 16 bits for the product with V, and what the rounding leaves is
+// multiplied too.
 //
 // Rows. A row tile is 8 or 16 of the M H/G (query, head) rows of a KV head, the
 // N of the products: S^T (16 keys x rows) = K Q^T and O^T (D x rows) += V^T P^T
@@ -112,9 +113,11 @@ struct PaRows {
     }
   }
 
-  // Moves the references that an element of x exceeds by more than the slack.
-  template <int TILES>
+  // Moves the references that an element of x exceeds by more than the slack (F16: p is
+  // rounded to fp16).
+  template <bool F16, int TILES>
   __device__ __forceinline__ void follow(const float (&x)[TILES][NT][4]) {
+    constexpr float kOver = kPaSlack + kPaBelow<F16>;
     float top[NT][2];
     bool move = false;
 #pragma unroll
@@ -125,7 +128,7 @@ struct PaRows {
 #pragma unroll
         for (int u = 1; u < TILES; ++u)
           top[nt][j] = fmaxf(top[nt][j], fmaxf(x[u][nt][j], x[u][nt][j + 2]));
-        move = move || top[nt][j] > ref[nt][j] + kPaSlack;
+        move = move || top[nt][j] > ref[nt][j] + kOver;
       }
     if (!__any_sync(kFull, move)) return;
 #pragma unroll
@@ -135,7 +138,8 @@ struct PaRows {
         float mx = top[nt][j];
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-        if (mx > ref[nt][j] + kPaSlack) {  // (alike in the lanes of a column)
+        if (mx > ref[nt][j] + kOver) {  // (alike in the lanes of a column)
+          mx -= kPaBelow<F16>;
           const float f = ex2(ref[nt][j] - mx);  // 0 while nothing was seen
           l[nt][j] *= f;
           base_v[nt][j] *= f;
@@ -219,7 +223,7 @@ __device__ __forceinline__ void pa_tile16(PaRows<D, NT>& a, const uint32_t (&qf)
       x[0][nt][i] = (sc[nt][0][i] + sc[nt][1][i]) * sl2;
       if (EDGE && see.hidden(n0 + r + 8 * (i >> 1), a.pos[nt][i & 1])) x[0][nt][i] = -INFINITY;
     }
-  a.follow(x);
+  a.template follow<!BF16>(x);
   // P^T as B operand, and what its rounding leaves: the copies bound the call, so a
   // second product costs nothing, and O is off by its own rounding alone
   uint32_t pf[NT][2], pl[NT][2];
@@ -448,7 +452,7 @@ __device__ __forceinline__ void pa_step4(PaRows<D, NT>& a, const uint8_t* slot,
       pa_scores4<D, NT, EDGE>(a, slot + (u0 + u) * kPaTile * row_bytes,
                               scales + (u0 + u) * kPaTile * 4, at, n0[u0 + u], qf, ka, kb, see, x[u],
                               mid[u], rstep[u]);
-    a.follow(x);
+    a.template follow<true>(x);
 #pragma unroll
     for (int u = 0; u < kTogether; ++u)
       pa_values4<D, NT, EDGE, REST>(

@@ -37,7 +37,13 @@ constexpr int kTcItemCost = 768;
 // over 1000 keys 14.3 us instead of 11.1, two over 3000 in 4 bits 18.4 instead of 13.6;
 // 64: 10.6 and 15.8.)
 constexpr int kPaLeast = 128;
-constexpr float kPaSlack = 8.0f;
+// A row's reference is moved where an x exceeds the largest at its last move by more
+// than kPaSlack. It lies kPaLift below that largest where p is rounded to fp16, so that
+// p reaches 2^15 and what is small beside it keeps seven bits more (without, keys of
+// 2^-26 of the largest were in the sum l and 0 in O); bf16 has the range anyway.
+constexpr float kPaSlack = 8.0f, kPaLift = 7.0f;
+template <bool F16>
+constexpr float kPaBelow = F16 ? kPaLift : 0.0f;
 
 // First key of a tile that is not there, past every position.
 constexpr int kNoKey = 0x7ffffff0, kPaFar = 0x7fffffe0;

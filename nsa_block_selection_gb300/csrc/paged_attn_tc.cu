@@ -580,7 +580,9 @@ __global__ void __launch_bounds__(TcCfg<D, Q4>::kThreads, 1)
         float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
                          fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
         if constexpr (!Q4) mx *= ka;
-        const bool move = mx > ref + kPaSlack;
+        constexpr float kBelow = kPaBelow<Q4 || !BF16>;
+        const bool move = mx > ref + (kPaSlack + kBelow);
+        mx -= kBelow;
         if (kAhead) columns_of(0);
         if (__any_sync(kFull, move)) {
           const float alpha = move ? ex2(ref - mx) : 1.f;
