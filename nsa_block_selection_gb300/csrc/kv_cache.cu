@@ -421,8 +421,9 @@ extern "C" int nsa_kv_append(const void* Q, const void* K, const void* V, void* 
                       norm ? eps : 0.f, dtype, weight_dtype);
   if (rc != NSA_OK) return rc;
   const int64_t heads[4] = {G, G, H, H};  // K, V and Q are read, the last is written
-  int64_t s[12];
-  if ((rc = take_strides(strides, 4, heads, B, M, D, s, 1)) != NSA_OK) return rc;
+  int64_t s[12] = {};
+  // (without queries neither of the last two is looked at)
+  if ((rc = take_strides(strides, H > 0 ? 4 : 2, heads, B, M, D, s, H > 0)) != NSA_OK) return rc;
   if (B == 0 || M == 0) return NSA_OK;
   if (!K || !V || (H > 0 && (!Q || !Qo))) return NSA_ERR_NULL;
   if (!norm && (wq || wk)) return NSA_ERR_SHAPE;
