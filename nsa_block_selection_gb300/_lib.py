@@ -904,6 +904,8 @@ def _check_places(cache, page_table, positions, B, M, dev, need=False):
     stride of positions over the batch)."""
     if cache._device != dev:
         raise ValueError("the cache must be on the tensors' CUDA device")
+    if page_table is None:
+        raise ValueError("page_table must be [B, cols]")
     if page_table.dtype is not _torch.int32:
         raise TypeError(f"page_table must be int32, got {page_table.dtype}")
     ts = page_table.shape
@@ -1000,8 +1002,11 @@ def kv_read(cache: KvCache, page_table, positions, dtype=None, k_out=None, v_out
     if dtype not in _F16_KINDS or (cache.bits == 16 and dtype is not cache.k.dtype):
         raise TypeError("dtype must be the cache's, or with 4 bits fp16 or bf16, got "
                         f"{dtype}")
-    B = page_table.shape[0]
-    M = positions.shape[-1] if positions.dim() else 0
+    if page_table is None or page_table.dim() != 2:
+        raise ValueError("page_table must be [B, cols]")
+    if positions is None or not positions.dim():
+        raise ValueError("positions are needed: [M] or [B, M]")
+    B, M = page_table.shape[0], positions.shape[-1]
     dev = cache._device
     cols, pstride = _check_places(cache, page_table, positions, B, M, dev, need=True)
     shape = (B, M, cache.kv_heads, cache.head_dim)

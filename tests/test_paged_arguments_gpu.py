@@ -21,3 +21,25 @@ def test_keys_of_one_sequence_for_a_whole_batch(bits):
     pos = torch.arange(40, device="cuda", dtype=torch.int32)
     for x, y in zip(*(kv_read(c, table, pos) for c in caches)):
         assert torch.equal(x, y) and not (x == 0).all()
+
+
+def test_missing_tables_and_positions_are_named():
+    import torch
+
+    from nsa_block_selection_gb300 import kv_append, kv_cache, kv_read, paged_attn
+
+    cache = kv_cache(4, 16, 2, 64)
+    table = torch.zeros((1, 4), dtype=torch.int32, device="cuda")
+    pos = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    q, k = (torch.zeros((1, 1, n, 64), device="cuda").bfloat16() for n in (4, 2))
+    for call in (lambda: kv_read(cache, table, None), lambda: paged_attn(q, cache, table, None),
+                 lambda: kv_read(cache, table, pos[0, 0]), lambda: kv_read(cache, table, pos[:, :, None])):
+        with pytest.raises(ValueError, match="positions"):
+            call()
+    for call in (lambda: kv_read(cache, None, pos), lambda: paged_attn(q, cache, None, pos),
+                 lambda: kv_append(q, k, k, cache, None, pos), lambda: kv_read(cache, table[0], pos),
+                 lambda: kv_read(cache, table[0, 0], pos), lambda: paged_attn(q, cache, table[0, 0], pos)):
+        with pytest.raises(ValueError, match="page_table"):
+            call()
+    for x in kv_read(cache, table, pos[:, :0]):
+        assert x.shape == (1, 0, 2, 64)
