@@ -1048,8 +1048,8 @@ def paged_attn(q, cache: KvCache, page_table, positions, window=(-1, 0), sinks: 
     values too (nsa_paged_attn): a decoding step (M = 1), drafted tokens, or a
     piece of a prompt.
 
-    q: fp16 or bf16 [B, M, H, D] (strided views as in :func:`kv_append`), of the
-    cache's dtype where that has 16 bits; ``page_table`` int32 [B, cols],
+    q: fp16 or bf16 [B, M, H, D] (strided views as in :func:`kv_append`, but none
+    that repeats rows by a stride of 0), of the cache's dtype where that has 16 bits; ``page_table`` int32 [B, cols],
     ``positions`` int32 [B, M] or [M], negative: padding. The query at position
     p sees the keys j <= p of its sequence with j >= p - left or j < ``sinks``
     (the first tokens, which stay visible behind the window), as far as the
@@ -1093,6 +1093,8 @@ def paged_attn(q, cache: KvCache, page_table, positions, window=(-1, 0), sinks: 
     strides = None
     if not dense:
         b, m, h, _ = q.stride()
+        if (B > 1 and b == 0) or (M > 1 and m == 0) or (H > 1 and h == 0):
+            raise ValueError("q must not repeat rows (a stride of 0)")
         strides = array("q", (b if B > 1 else 0, m if M > 1 else 0, h if H > 1 else 0))
     if workspace is None:
         tokens, nbytes = cols * cache.page_size, 0

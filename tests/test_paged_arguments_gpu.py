@@ -43,3 +43,19 @@ def test_missing_tables_and_positions_are_named():
             call()
     for x in kv_read(cache, table, pos[:, :0]):
         assert x.shape == (1, 0, 2, 64)
+
+
+def test_queries_that_repeat_rows_are_refused_by_name():
+    import torch
+
+    from nsa_block_selection_gb300 import kv_cache, paged_attn
+
+    cache = kv_cache(4, 16, 2, 64)
+    table = torch.zeros((2, 4), dtype=torch.int32, device="cuda")
+    pos = torch.zeros((2, 2), dtype=torch.int32, device="cuda")
+    for shape in ((1, 2, 4, 64), (2, 1, 4, 64), (2, 2, 1, 64)):
+        q = torch.zeros(shape, device="cuda").bfloat16().expand(2, 2, 4, 64)
+        with pytest.raises(ValueError, match="repeat"):
+            paged_attn(q, cache, table, pos)
+    q = torch.zeros((1, 1, 1, 64), device="cuda").bfloat16().expand(1, 1, 1, 64)
+    assert paged_attn(q, cache, table[:1], pos[:1, :1].contiguous())[0].shape == q.shape
