@@ -15,8 +15,8 @@
 // The bytes bound both: every row is read once and written once. A row is held
 // by D / 16 lanes, 16 entries each (append), which hold both entries of every
 // pair, so that the turn needs no exchange; or by D / 8 lanes, 16 bytes of the
-// result each (read). 16,384 tokens of 64 + 8 heads of 128 are appended in 111 us
-// (680 MB, 6.1 TB/s), 65,536 tokens of 8 heads read from 4 bits in 57 us (340 MB,
+// result each (read). 16,384 tokens of 64 + 8 heads of 128 are appended in 109 us
+// (680 MB, 6.2 TB/s), 65,536 tokens of 8 heads read from 4 bits in 57 us (340 MB,
 // 6.0 TB/s); one token is 2.3 us on the device.
 
 #include <cuda_bf16.h>
@@ -36,11 +36,12 @@ namespace nsa {
 namespace {
 
 constexpr int kKvThreads = 128;
-// CTAs of kv_append_kernel. (16 bits with 4: 4 x 2000 tokens of 16 + 2 heads of 64 13.1
-// us instead of 11.2; 4 bits with 6: 29.7 instead of 28.5.)
-constexpr int kAppendPerSm = 6, kAppendPerSm4 = 4;
+// CTAs of kv_append_kernel. (16 bits with 4: 4 x 2000 tokens of 16 + 2 heads of 64 12.0
+// us instead of 11.1; 4 bits with 5 22.0, with 4 24.4, with 6 21.0, but 48 single tokens
+// 4.3 us instead of 4.0.)
+constexpr int kAppendPerSm = 6, kAppendPerSm4 = 5;
 // Beyond so many groups of row slots a token, and in all, a warp takes a token. (16,384
-// tokens of 64 + 8 heads: 112 us, by kv_append_kernel 145.)
+// tokens of 64 + 8 heads: 109 us, by kv_append_kernel 142.)
 constexpr int kAppendFewPerToken = 8;
 constexpr int64_t kAppendFewGroups = 128 * 152;
 constexpr int kKvSms = 152;

@@ -27,11 +27,11 @@
 // the forward and 2 or 4 in the backward; with many heads they walk the heads
 // of one token, whose angles they share, with few they hold several tokens.
 //
-// Measured, bf16, 64 + 8 heads of D = 128: 65,536 tokens forward 389 us
-// (6.2 TB/s, 92 % of a copy), 32,768 tokens backward 333 us (5.5 TB/s, 81 %:
+// Measured, bf16, 64 + 8 heads of D = 128: 65,536 tokens forward 360 us
+// (6.7 TB/s, 99 % of a copy), 32,768 tokens backward 333 us (5.5 TB/s, 81 %:
 // of the instruction slots 58 % are taken, and 24 warps an SM, what 80
 // registers a thread allow, keep too few loads in flight for more). Short
-// calls are bound by their launches: a token of 64 + 8 heads takes 4 us on
+// calls are bound by their launches: a token of 64 + 8 heads takes 2.6 us on
 // the device, most of it the launch.
 
 #include <cuda_bf16.h>
@@ -56,11 +56,12 @@ constexpr int kRopeSms = 152;
 constexpr int kFewPerSm = 7;  // CTAs of norm_rope_few_kernel that an SM holds
 // The forward gives every row slot its own token up to this many groups of
 // slots a token, or this many groups in all; beyond, a warp walks a token's
-// heads with one set of angles. Both measured, 32,768 tokens of 32 + 4 heads at
-// D = 64 (5 groups): 77 us against 87, of 24 + 8 at D = 128 (8): 120 and 122, of
-// 32 + 4 at D = 128 (9): 132 against 126; 1000 tokens of 64 + 8 at D = 128
-// (18,000 groups): 16 against 18, 4096 tokens of those (73,728): 40 against 38.
-constexpr int kFewPerToken = 8;
+// heads with one set of angles. Both measured, 32,768 tokens of 48 + 8 heads at
+// D = 64 (7 groups): 93 us against 94, of 24 + 4 at D = 128 (7): 96 and 97, of 24 + 8
+// (8): 109 against 101, of 32 + 4 (9): 122 against 106; 2000 tokens of 32 + 4 at
+// D = 128 (18,000 groups): 9.2 against 10.5, 1000 of 64 + 8 (18,000) 9.0 and 8.0, 4096
+// of those (73,728) 33 against 31.
+constexpr int kFewPerToken = 7;
 constexpr int64_t kFewGroups = 128 * kRopeSms;
 // What a unit of the backward that walks a token's heads costs, beside a
 // group of slots that hold several tokens: its position and angles, and each
@@ -100,8 +101,8 @@ __global__ void __launch_bounds__(kRopeThreads, FULL ? 5 : 4)
 // and the head's weights, and walks the tokens, each with its own position and
 // angles. (A warp per token leaves row slots empty and pays the latencies of
 // position, angles and rows for each: 32,768 tokens of 1 + 1 heads at D = 64
-// 73 us against 13, of 8 + 2 76 against 36. Two rows in flight a lane leave 16
-// to 20 warps an SM: 40 for the latter, with 28 warps of one row it is 36;
+// 51 us against 5.5, of 8 + 2 55 against 27. Two rows in flight a lane, for 16
+// to 20 warps an SM, took a tenth more of the latter than 28 warps of one row;
 // loading the next position early gave nothing.)
 template <int D, bool BF16, bool FULL>
 __global__ void __launch_bounds__(kRopeThreads, kFewPerSm)
