@@ -9,7 +9,7 @@
 // r a reference that follows the largest x (by steps of 8, and 7 below it where p is
 // rounded to fp16: p <= 2^8, 2^15). One pass over the keys; x, p, sums and O are fp32,
 // p is rounded to 16 bits for the product with V, and what the rounding leaves is
-// multiplied too.
+// multiplied too (but for a bf16 O over 4 bits).
 //
 // Rows. A row tile is 8 or 16 of the M H/G (query, head) rows of a KV head, the
 // N of the products: S^T (16 keys x rows) = K Q^T and O^T (D x rows) += V^T P^T
@@ -45,8 +45,8 @@
 // 8 heads of 128 over 65,536 keys takes 44 to 48 us (5.6 to 6.1 TB/s of 268 MB), of
 // which some 6 us are the first positions, pages and copies and the join; 48 windowed
 // sequences of 32 + 4 heads (1028 keys each, 102 MB) 22 us in one kernel. 4 bits: the
-// warps' instructions, some 290 for 16 keys of a KV head: 64 ragged sequences of up to
-// 16,384 tokens of 64 + 8 heads (580 MB) 142 us, 4.1 TB/s, a warp issues in 52 % of
+// warps' instructions, some 300 for 16 keys of a KV head: 64 ragged sequences of up to
+// 16,384 tokens of 64 + 8 heads (580 MB) 146 us, 4.0 TB/s, a warp issues in 53 % of
 // the clocks at 12 warps an SM.
 
 #include <cuda.h>
@@ -436,7 +436,7 @@ __device__ __forceinline__ void pa_values4(PaRows<D, NT>& a, const uint8_t* vt, 
 }
 
 // A warp's 32 keys of a slot: two tiles, at once where the registers hold both (64
-// sequences over 4 bits 142 us, one after the other 147).
+// sequences over 4 bits 146 us, one after the other 150).
 template <int D, int NT, bool EDGE, bool REST>
 __device__ __forceinline__ void pa_step4(PaRows<D, NT>& a, const uint8_t* slot,
                                          const uint8_t* scales, const PaLanes& at, int row_bytes,

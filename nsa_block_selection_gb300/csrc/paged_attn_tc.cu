@@ -18,7 +18,7 @@
 // 4 bits: four loader warps load the codes a step ahead and write c - 8, exact in
 // fp16, as the operands' rows; five numbers of a key (steps, the middles low + 8 step,
 // log2 of V's step) go beside them, and a key that nobody sees gets -inf for x and
-// zeros. With k = mid + step (c - 8):
+// zeros. Rows of V without a step become codes of 8 (pa_step). With k = mid + step (c - 8):
 //   x = step ka (q'.(c - 8)) + mid kb + log2 step_v,  p' = 2^(x - r),
 //   l += p' / step_v,  O = sum p' (c - 8) + sum p' mid_v / step_v,
 // q' = 2^e q in fp16, written by the softmax warps, ka and kb the row's factors.
@@ -28,8 +28,8 @@
 // the shared-memory pipe, by the operands' rows that the loaders write and the five
 // numbers of a key that every row reads; loaders of a warpgroup each for K and V gained
 // nothing); an item's own cost is some 6000. Prompts of 32 + 4 heads of 128: 16,384
-// tokens 1740 us (1260 TFLOP/s), 4096 tokens 167 us (4 bits 281); 3 x 200 tokens of 64
-// + 8 heads after 8800 others 176 us (296). One group with two S and a P of its own,
+// tokens 1747 us (1260 TFLOP/s), 4096 tokens 167 us (4 bits 279); 3 x 200 tokens of 64
+// + 8 heads after 8800 others 175 us (291). One group with two S and a P of its own,
 // and one producer warp: 2160, 232 (371), 266 (384).
 //
 // Every mbarrier wait is bounded (1 s); a role that gives up sets the status word
