@@ -546,10 +546,10 @@ int nsa_swa_bwd(const void* Q, const void* K, const void* V, const void* O, cons
  * becomes (a cos - b sin, b cos + a sin); all in fp32, each operation rounded
  * by itself ((x r) w; two products, then their sum), and once (nearest even) to
  * dtype. The sum of squares adds entries 32 apart first, in rising order, then
- * neighbours, pairs, pairs of pairs and so on. A token whose position is negative, or >= table_rows when
- * R > 0, is padding: its inputs are not read and its output rows are zero.
- * A non-finite entry reaches its own row only. With positions NULL and R > 0
- * the table must hold M rows (else NSA_ERR_SHAPE).
+ * neighbours, pairs, pairs of pairs and so on. A token whose position is
+ * negative, or >= table_rows when R > 0, is padding: its inputs are not read and
+ * its output rows are zero. A non-finite entry reaches its own row only. With
+ * positions NULL and R > 0 the table must hold M rows (else NSA_ERR_SHAPE).
  *
  * One kernel on `stream`; allocates nothing and keeps no state. Errors before
  * launch: NSA_ERR_SHAPE (sizes, R, eps, B*M >= 2^31), NSA_ERR_HEAD_DIM,

@@ -1049,11 +1049,12 @@ def paged_attn(q, cache: KvCache, page_table, positions, window=(-1, 0), sinks: 
     piece of a prompt.
 
     q: fp16 or bf16 [B, M, H, D] (strided views as in :func:`kv_append`, but none
-    that repeats rows by a stride of 0), of the cache's dtype where that has 16 bits; ``page_table`` int32 [B, cols],
-    ``positions`` int32 [B, M] or [M], negative: padding. The query at position
-    p sees the keys j <= p of its sequence with j >= p - left or j < ``sinks``
-    (the first tokens, which stay visible behind the window), as far as the
-    sequence has their pages; ``window`` = (left, 0), left negative: unbounded.
+    that repeats rows by a stride of 0), of the cache's dtype where that has 16
+    bits; ``page_table`` int32 [B, cols], ``positions`` int32 [B, M] or [M],
+    negative: padding. The query at position p sees the keys j <= p of its sequence
+    with j >= p - left or j < ``sinks`` (the first tokens, which stay visible behind
+    the window), as far as the sequence has their pages; ``window`` = (left, 0), left
+    negative: unbounded.
     Returns (O [B, M, H, D] of q's dtype, LSE fp32 [B, H, M] or None); O = 0 and
     LSE = -inf where a query sees nothing. ``workspace`` (CUDA uint8,
     paged_attn_workspace_bytes) is allocated when omitted and needed; calls that may

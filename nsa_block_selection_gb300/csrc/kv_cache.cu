@@ -4,8 +4,8 @@
 //
 // Append, per token at position p: Q and K rows become
 //   y = turn_p(x rsqrt(mean(x^2) + eps) w),
-// fp32, rounded once to the 16-bit type, in norm_rope.cu's order of operations; Q is written as a
-// tensor, K and V as rows of the token's page. A 4-bit row is made of the 16-bit
+// fp32, rounded once to the 16-bit type, in norm_rope.cu's order of operations; Q is
+// written as a tensor, K and V as rows of the token's page. A 4-bit row is made of the 16-bit
 // one: low = bf16(min), step = bf16((max - low) / 15),
 // code = clamp(rint((x - low) / step), 0, 15), all divisions IEEE, so that the
 // codes are the same wherever they are formed.

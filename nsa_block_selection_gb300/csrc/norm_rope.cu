@@ -22,10 +22,10 @@
 // t < R/16, and two consecutive chunks of the tail after that, so the rotation
 // needs no exchange between lanes in either pairing and the only shuffles are
 // the row sums' (2 at D = 64; 7 at 128, or 3 and loads from the cache where R < D).
-// The backward does the same with
-// D / 8 lanes of two 8-byte chunks. A warp has 4 (D = 128) or 8 row slots in
-// the forward and 2 or 4 in the backward; with many heads they walk the heads
-// of one token, whose angles they share, with few they hold several tokens.
+// The backward does the same with D / 8 lanes of two 8-byte chunks. A warp has 4
+// (D = 128) or 8 row slots in the forward and 2 or 4 in the backward; with many heads
+// they walk the heads of one token, whose angles they share, with few they hold several
+// tokens.
 //
 // Measured, bf16, 64 + 8 heads of D = 128: 65,536 tokens forward 360 us
 // (6.7 TB/s, 99 % of a copy), 32,768 tokens backward 333 us (5.5 TB/s, 81 %:
